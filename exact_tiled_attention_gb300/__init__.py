@@ -30,5 +30,18 @@ from .binding import (  # noqa: F401
     gbattn_version,
     load_library,
 )
+from .paged import (  # noqa: F401
+    attn_cache_append,
+    attn_cache_append_fp4,
+    attn_cache_gather,
+    attn_cache_gather_fp4,
+    attn_decode_paged,
+    attn_decode_paged_fp4,
+    attn_decode_paged_workspace_bytes,
+    attn_qk_norm_rope,
+    attn_qk_norm_rope_bwd,
+    attn_qk_norm_rope_bwd_workspace_bytes,
+    rope_table,
+)
 
 __version__ = "0.1.0"

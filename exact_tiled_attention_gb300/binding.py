@@ -22,10 +22,12 @@ GBATTN_OK = 0
 GBATTN_F16 = 0
 GBATTN_BF16 = 1
 GBATTN_EDEVICE_TIMEOUT = -8
+GBATTN_EINDEX = -12
 ERRORS = {
     -1: "GBATTN_EBADSHAPE", -2: "GBATTN_EHEADS", -3: "GBATTN_EHEADDIM", -4: "GBATTN_EDTYPE",
     -5: "GBATTN_EPOINTER", -6: "GBATTN_EWORKSPACE", -7: "GBATTN_ELAUNCH",
     -8: "GBATTN_EDEVICE_TIMEOUT", -9: "GBATTN_ESPLIT", -10: "GBATTN_EUNSUPPORTED",
+    -11: "GBATTN_EPAGE", -12: "GBATTN_EINDEX",
 }
 EXPORTS = ("attn_fwd", "attn_fwd_pair", "attn_decode_workspace_bytes", "attn_decode_splitkv",
            "attn_decode_splitkv_noalloc", "attn_decode_noalloc_scratch_bytes",
@@ -33,7 +35,10 @@ EXPORTS = ("attn_fwd", "attn_fwd_pair", "attn_decode_workspace_bytes", "attn_dec
            "gbattn_exp2_paths",
            "attn_fwd_fp8_workspace_bytes", "attn_fwd_fp8", "gbattn_selftest_bounded_wait",
            "gbattn_causal_tile_counts", "gbattn_device_status", "gbattn_timeline_set",
-           "gbattn_error_string", "gbattn_version")
+           "gbattn_error_string", "gbattn_version",
+           "attn_qk_norm_rope", "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_bwd",
+           "attn_cache_append", "attn_cache_append_fp4", "attn_cache_gather", "attn_cache_gather_fp4",
+           "attn_decode_paged_workspace_bytes", "attn_decode_paged", "attn_decode_paged_fp4")
 
 _lock = threading.Lock()
 _lib = None
@@ -85,6 +90,26 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.attn_fwd_fp8_workspace_bytes.restype = sz
         lib.attn_fwd_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, cf, ci, vp, sz, vp]
         lib.attn_fwd_fp8.restype = ci
+        lib.attn_qk_norm_rope.argtypes = [vp] * 8 + [ci] * 5 + [vp] * 2 + [cf] + [ci] * 4 + [vp]
+        lib.attn_qk_norm_rope.restype = ci
+        lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [ci]
+        lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = sz
+        lib.attn_qk_norm_rope_bwd.argtypes = ([vp] * 12 + [ci] * 5 + [vp] * 4 + [cf] + [ci] * 3 + [vp, sz, ci, vp])
+        lib.attn_qk_norm_rope_bwd.restype = ci
+        lib.attn_cache_append.argtypes = [vp] * 10 + [ci] * 8 + [vp] * 3 + [ci] * 4 + [vp]
+        lib.attn_cache_append.restype = ci
+        lib.attn_cache_append_fp4.argtypes = [vp] * 14 + [ci] * 8 + [vp] * 3 + [ci] * 4 + [vp]
+        lib.attn_cache_append_fp4.restype = ci
+        lib.attn_cache_gather.argtypes = [vp] * 6 + [ci] * 8 + [vp]
+        lib.attn_cache_gather.restype = ci
+        lib.attn_cache_gather_fp4.argtypes = [vp] * 10 + [ci] * 8 + [vp]
+        lib.attn_cache_gather_fp4.restype = ci
+        lib.attn_decode_paged_workspace_bytes.argtypes = [ci] * 4
+        lib.attn_decode_paged_workspace_bytes.restype = sz
+        lib.attn_decode_paged.argtypes = [vp] * 7 + [ci] * 7 + [cf, vp, sz, ci, vp]
+        lib.attn_decode_paged.restype = ci
+        lib.attn_decode_paged_fp4.argtypes = [vp] * 11 + [ci] * 7 + [cf, vp, sz, ci, vp]
+        lib.attn_decode_paged_fp4.restype = ci
         lib.gbattn_exp2_paths.argtypes = [vp, vp, vp, ctypes.c_longlong, vp]
         lib.gbattn_exp2_paths.restype = ci
         lib.gbattn_causal_tile_counts.argtypes = [ci, ci, ci, ci, ll_p, ll_p, ll_p, ll_p, ll_p]

@@ -1,0 +1,325 @@
+// cache_pages.cu -- writing new keys and values into a paged cache, with the
+// position rotation on the way, and reading a cache's sequences back as
+// contiguous 16-bit tensors; for a cache held in 16 bits and one held in 4.
+//
+// Append: token i of sequence b stands at position p = seqlens[b] - new[b] + i
+// and goes to slot p % page of page page_table[b][p / page]; keys (and queries,
+// which go to q_out) are rotated by the table's row p in fp32 and rounded once.
+// 4 bits: for each group of 16 elements, f = E4M3(min(448, max |x| / (6 descale)))
+// and code = E2M1(x * (1 / (f descale))), both rounded to nearest even; f = 0
+// gives zero codes.  Division and reciprocal are the IEEE ones, so the codes are
+// those of the same formula evaluated anywhere in fp32.
+//
+// Both are bound by HBM (or, for one token a sequence, by the launch): each
+// element is read once and written once.
+#include <cuda_runtime.h>
+
+#include "gbattn_rows.cuh"
+
+namespace gbattn {
+namespace {
+
+constexpr int kThreads = 128;
+
+struct AppendParams {
+  const uint16_t* x[3];  // q, k, v
+  RowStrides xs[3];
+  uint16_t* q_out;
+  uint8_t* data[2];
+  uint8_t* scale[2];
+  const float* descale[2];
+  const int* page_table;
+  const int* seqlens;
+  const int* new_lens;
+  const float* table;
+  int table_rows, rot;
+  int B, S, heads[3], chunks[3], per_chunk;
+  int page_shift, n_pages, max_pages;
+  int* status;
+};
+
+__device__ __forceinline__ uint32_t e2m1x8(const float (&y)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return r;
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(code & 0xFF)));
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(h2 & 0xFFFF)));
+}
+
+// One chunk of 8 elements to 4 bits; the other half of its group of 16 is the
+// neighbouring lane's.
+__device__ __forceinline__ uint32_t quantise8(const float (&z)[8], float descale, uint8_t& factor) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(z[i]));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  const float f = fminf(__fdiv_rn(m, __fmul_rn(6.f, descale)), 448.f);
+  factor = static_cast<uint8_t>(pack4_e4m3(f, 0.f, 0.f, 0.f) & 0xFF);
+  const float fv = e4m3_value(factor);
+  const float inv = fv > 0.f ? __frcp_rn(__fmul_rn(fv, descale)) : 0.f;
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(z[i], inv);
+  return e2m1x8(y);
+}
+
+template <int D, bool BF16, int MODE, bool FP4>
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kLanes = RowCfg<D>::kLanes;
+  constexpr int kRowsCta = kThreads / kLanes;
+  const int lane_in_row = threadIdx.x % kLanes;
+  const int e0 = 8 * lane_in_row;
+  const long long tokens = static_cast<long long>(p.B) * p.S;
+  long long t = static_cast<long long>(blockIdx.x) * kRowsCta + threadIdx.x / kLanes;
+  const bool in_grid = t < tokens;
+  if (!in_grid) t = tokens - 1;  // the whole warp stays for the shuffles
+  const int b = static_cast<int>(t / p.S), i = static_cast<int>(t % p.S);
+  int which = 0, chunk = blockIdx.y;  // 0: queries, 1: keys, 2: values
+  while (which < 2 && chunk >= p.chunks[which]) chunk -= p.chunks[which++];
+  const int h0 = chunk * p.per_chunk;
+  const int h1 = min(h0 + p.per_chunk, p.heads[which]);
+
+  const int n_new = p.new_lens != nullptr ? min(p.new_lens[b], p.S) : p.S;
+  const long long pos = static_cast<long long>(p.seqlens[b]) - n_new + i;
+  const bool real = in_grid && i < n_new && pos >= 0;  // else padding
+  bool stored = real;
+  long long slot = 0;  // row of head 0 of the token's page
+  if (real && which != 0) {
+    const long long pg = pos >> p.page_shift;
+    const int page = pg < p.max_pages ? p.page_table[static_cast<long long>(b) * p.max_pages + pg] : -1;
+    if (page < 0 || page >= p.n_pages) {
+      stored = false;
+      atomicCAS(p.status, 0, kStatusIndex);
+    } else {
+      slot = ((static_cast<long long>(page) * p.heads[1]) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+    }
+  }
+  LaneRope rope;
+  int pc[2] = {e0, D / 2 + e0};
+  if constexpr (MODE != kRopeNone) {
+    if (which != 2) {
+      long long row = real ? pos : 0;
+      if (row >= p.table_rows) {
+        atomicCAS(p.status, 0, kStatusIndex);
+        row = p.table_rows - 1;
+      }
+      load_rope<D, MODE>(rope, p.table + row * p.rot, p.rot, lane_in_row);
+      if constexpr (MODE == kRopePart)
+        for (int c = 0; c < 2; ++c) pc[c] = partner_chunk(c * (D / 2) + e0, p.rot);
+    }
+  }
+  const RowStrides xs = p.xs[which];
+  const uint16_t* xrow = p.x[which] + b * xs.b + i * xs.s + h0 * xs.h;
+  for (int h = h0; h < h1; ++h, xrow += xs.h) {
+    const uint4 u0 = *reinterpret_cast<const uint4*>(xrow + e0);
+    const uint4 u1 = *reinterpret_cast<const uint4*>(xrow + D / 2 + e0);
+    float z[2][8], part[2][8];
+    unpack8<BF16>(u0, z[0]);
+    unpack8<BF16>(u1, z[1]);
+    if constexpr (MODE != kRopeNone) {
+      if (which != 2) {
+        if constexpr (MODE == kRopePart) {
+          unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + pc[0]), part[0]);
+          unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + pc[1]), part[1]);
+        }
+        rotate<MODE, false>(z, part, rope);
+      }
+    }
+    if (which == 0) {
+      if (in_grid) {
+        uint16_t* y = p.q_out + ((static_cast<long long>(b) * p.heads[0] + h) * p.S + i) * D;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(y + e0) = real ? pack8<BF16>(z[0]) : zero;
+        *reinterpret_cast<uint4*>(y + D / 2 + e0) = real ? pack8<BF16>(z[1]) : zero;
+      }
+      continue;
+    }
+    const long long row = slot + (static_cast<long long>(h) << p.page_shift);
+    if constexpr (FP4) {
+      const float ds = p.descale[which - 1] != nullptr ? p.descale[which - 1][h] : 1.f;
+      uint8_t f0, f1;
+      const uint32_t c0 = quantise8(z[0], ds, f0), c1 = quantise8(z[1], ds, f1);
+      if (stored) {
+        uint8_t* y = p.data[which - 1] + row * (D / 2);
+        *reinterpret_cast<uint32_t*>(y + e0 / 2) = c0;
+        *reinterpret_cast<uint32_t*>(y + D / 4 + e0 / 2) = c1;
+        if (lane_in_row % 2 == 0) {
+          uint8_t* f = p.scale[which - 1] + row * (D / 16);
+          f[e0 / 16] = f0;
+          f[D / 32 + e0 / 16] = f1;
+        }
+      }
+    } else if (stored) {
+      uint16_t* y = reinterpret_cast<uint16_t*>(p.data[which - 1]) + row * D;
+      *reinterpret_cast<uint4*>(y + e0) = pack8<BF16>(z[0]);
+      *reinterpret_cast<uint4*>(y + D / 2 + e0) = pack8<BF16>(z[1]);
+    }
+  }
+}
+
+struct GatherParams {
+  const uint8_t* data[2];
+  const uint8_t* scale[2];
+  const float* descale[2];
+  uint16_t* out[2];
+  const int* page_table;
+  const int* seqlens;
+  int B, Hkv, S;
+  int page_shift, n_pages, max_pages;
+  int* status;
+};
+
+// Grid (row blocks of one (batch, head), B * Hkv, 2).  A thread writes 16
+// elements (32 bytes) of one row.
+template <int D, bool BF16, bool FP4>
+__global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_constant__ GatherParams p) {
+  constexpr int kParts = D / 16;
+  const int which = blockIdx.z;
+  const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
+  const int s = blockIdx.x * (kThreads / kParts) + threadIdx.x / kParts;
+  const int part = threadIdx.x % kParts;
+  if (s >= p.S) return;
+  uint4 y0 = make_uint4(0u, 0u, 0u, 0u), y1 = y0;
+  if (s < p.seqlens[b]) {
+    const int pg = s >> p.page_shift;
+    const int page = pg < p.max_pages ? p.page_table[static_cast<long long>(b) * p.max_pages + pg] : -1;
+    if (page < 0 || page >= p.n_pages) {
+      atomicCAS(p.status, 0, kStatusIndex);
+    } else {
+      const long long row = ((static_cast<long long>(page) * p.Hkv + h) << p.page_shift) +
+                            (s & ((1 << p.page_shift) - 1));
+      if constexpr (FP4) {
+        const uint2 codes = *reinterpret_cast<const uint2*>(p.data[which] + row * (D / 2) + part * 8);
+        const float f = e4m3_value(p.scale[which][row * (D / 16) + part]);
+        const float ds = p.descale[which] != nullptr ? p.descale[which][h] : 1.f;
+        float z[2][8];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t w = c ? codes.y : codes.x;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h2;
+            asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h2) : "r"(w >> (8 * k)));
+            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+            z[c][2 * k] = __fmul_rn(__fmul_rn(t.x, f), ds);
+            z[c][2 * k + 1] = __fmul_rn(__fmul_rn(t.y, f), ds);
+          }
+        }
+        y0 = pack8<BF16>(z[0]);
+        y1 = pack8<BF16>(z[1]);
+      } else {
+        const uint4* src = reinterpret_cast<const uint4*>(p.data[which] + row * (D * 2) + part * 32);
+        y0 = src[0];
+        y1 = src[1];
+      }
+    }
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.out[which] + (static_cast<long long>(blockIdx.y) * p.S + s) * D + part * 16);
+  dst[0] = y0;
+  dst[1] = y1;
+}
+
+template <int D, bool BF16, bool FP4>
+int launch_append_t(const AppendArgs& a) {
+  AppendParams p{};
+  for (int i = 0; i < 3; ++i) {
+    p.x[i] = static_cast<const uint16_t*>(a.x[i]);
+    p.xs[i] = a.xs[i];
+    p.heads[i] = i == 0 ? (a.x[0] != nullptr ? a.H : 0) : a.cache.Hkv;
+  }
+  for (int i = 0; i < 2; ++i) {
+    p.data[i] = static_cast<uint8_t*>(a.cache.data[i]);
+    p.scale[i] = static_cast<uint8_t*>(a.cache.scale[i]);
+    p.descale[i] = a.cache.descale[i];
+  }
+  p.q_out = static_cast<uint16_t*>(a.q_out);
+  p.page_table = a.cache.page_table;
+  p.seqlens = a.cache.seqlens;
+  p.new_lens = a.new_lens;
+  p.table = a.rope.table;
+  p.table_rows = a.rope.rows;
+  p.rot = a.rope.rot_dim;
+  p.B = a.B;
+  p.S = a.S;
+  p.page_shift = a.cache.page_shift;
+  p.n_pages = a.cache.n_pages;
+  p.max_pages = a.cache.max_pages;
+  p.status = a.status;
+  const long long tokens = static_cast<long long>(a.B) * a.S;
+  const long long token_ctas = (tokens + kThreads / RowCfg<D>::kLanes - 1) / (kThreads / RowCfg<D>::kLanes);
+  // As many heads a thread as leave four CTAs for each SM, at most 8.
+  int per = 8;
+  const int heads = p.heads[0] + p.heads[1] + p.heads[2];
+  while (per > 1 && token_ctas * (heads / per) < 4LL * a.num_sms) per /= 2;
+  p.per_chunk = per;
+  int chunks = 0;
+  for (int i = 0; i < 3; ++i) chunks += p.chunks[i] = (p.heads[i] + per - 1) / per;
+  if (token_ctas > 0x7FFFFFFFLL || chunks > 65535) return -1;
+  const dim3 grid(static_cast<unsigned>(token_ctas), chunks);
+  switch (rope_mode(a.rope, D)) {
+    case kRopeNone: cache_append_kernel<D, BF16, kRopeNone, FP4><<<grid, kThreads, 0, a.stream>>>(p); break;
+    case kRopePairs: cache_append_kernel<D, BF16, kRopePairs, FP4><<<grid, kThreads, 0, a.stream>>>(p); break;
+    case kRopeHalves: cache_append_kernel<D, BF16, kRopeHalves, FP4><<<grid, kThreads, 0, a.stream>>>(p); break;
+    default: cache_append_kernel<D, BF16, kRopePart, FP4><<<grid, kThreads, 0, a.stream>>>(p); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int D, bool BF16, bool FP4>
+int launch_gather_t(const GatherArgs& a) {
+  GatherParams p{};
+  for (int i = 0; i < 2; ++i) {
+    p.data[i] = static_cast<const uint8_t*>(a.cache.data[i]);
+    p.scale[i] = static_cast<const uint8_t*>(a.cache.scale[i]);
+    p.descale[i] = a.cache.descale[i];
+    p.out[i] = static_cast<uint16_t*>(a.out[i]);
+  }
+  p.page_table = a.cache.page_table;
+  p.seqlens = a.cache.seqlens;
+  p.B = a.B;
+  p.Hkv = a.cache.Hkv;
+  p.S = a.S;
+  p.page_shift = a.cache.page_shift;
+  p.n_pages = a.cache.n_pages;
+  p.max_pages = a.cache.max_pages;
+  p.status = a.status;
+  constexpr int kRowsCta = kThreads / (D / 16);
+  const long long bh = static_cast<long long>(a.B) * a.cache.Hkv;
+  if (bh > 65535) return -1;
+  const dim3 grid((a.S + kRowsCta - 1) / kRowsCta, static_cast<unsigned>(bh), 2);
+  cache_gather_kernel<D, BF16, FP4><<<grid, kThreads, 0, a.stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+int launch_cache_append(const AppendArgs& a) {
+  if (a.cache.d == 128) {
+    if (a.cache.fp4()) return a.bf16 ? launch_append_t<128, true, true>(a) : launch_append_t<128, false, true>(a);
+    return a.bf16 ? launch_append_t<128, true, false>(a) : launch_append_t<128, false, false>(a);
+  }
+  if (a.cache.fp4()) return a.bf16 ? launch_append_t<64, true, true>(a) : launch_append_t<64, false, true>(a);
+  return a.bf16 ? launch_append_t<64, true, false>(a) : launch_append_t<64, false, false>(a);
+}
+
+int launch_cache_gather(const GatherArgs& a) {
+  if (a.cache.d == 128) {
+    if (a.cache.fp4()) return a.bf16 ? launch_gather_t<128, true, true>(a) : launch_gather_t<128, false, true>(a);
+    return launch_gather_t<128, true, false>(a);  // a copy: the type does not matter
+  }
+  if (a.cache.fp4()) return a.bf16 ? launch_gather_t<64, true, true>(a) : launch_gather_t<64, false, true>(a);
+  return launch_gather_t<64, true, false>(a);
+}
+
+}  // namespace gbattn

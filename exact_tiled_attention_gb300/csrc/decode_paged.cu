@@ -1,0 +1,675 @@
+// decode_paged.cu -- one query per sequence over a paged cache held in 16 bits
+// or in 4 (E2M1 codes with one E4M3 factor for each 16).
+//
+// Work.  The key axis of every (sequence, KV head, group of query heads) is cut
+// into units of kUnitKeys keys; a grid of resident CTAs takes equal runs of the
+// list of all units (order: sequence, head, key), whatever the sequences'
+// lengths are.  A run covers whole (sequence, head) segments, which the CTA
+// finishes itself, and at its two ends parts of segments, whose states (m, l, o)
+// it leaves in the workspace; a second kernel folds those.  The division of the
+// list follows from the lengths alone, so results repeat bitwise.
+//
+// Inside a CTA each warp takes every fourth 16 keys of a segment and keeps its
+// own online-softmax state.  It computes S^T = K Q^T and O^T = V^T P^T with
+// m16n8k16 tensor-core products: the keys (or head elements) fill the 16 rows
+// and up to 8 query heads the 8 columns.  Rows of K and V go from global memory
+// straight into operand registers: the order of the head's elements inside a
+// product is free as long as Q follows it, so a lane's 16-byte piece of a row is
+// its operand for several products, and V, whose operand pairs two keys, takes
+// one byte permute for two elements.
+//
+// The scores' reference m follows the maximum lazily (it moves when a score is
+// more than 8 above it in base-2 units), so P <= 256; P is rounded to 16 bits
+// for P V, and l sums the unrounded values.
+#include <cuda_runtime.h>
+
+#include "gbattn_internal.h"
+#include "gbattn_ptx.cuh"
+
+namespace gbattn {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCtas = 1024;        // bound of the grid, for the workspace's size
+constexpr int kMaxGroup = 16;         // query heads of one unit
+constexpr float kRescaleThreshold = 8.f;
+
+enum Format : int { kF16 = 0, kBf16 = 1, kFp4 = 2 };
+
+struct Params {
+  const uint16_t* q;
+  const uint8_t* data[2];
+  const uint8_t* factor[2];
+  const float* descale[2];
+  const int* page_table;
+  const int* seqlens;
+  uint16_t* o;
+  float* lse;
+  float* part_o;   // [ctas][2][rows][D]
+  float* part_ml;  // [ctas][2][rows][2]: m in base-2 units, l
+  int2* parts;     // [B][heads of units]: first CTA * 2 + its slot, number of parts (0: finished)
+  int B, Hq, Hkv, g, groups, rows;
+  int page_shift, n_pages, max_pages;
+  float scale_log2;
+  int out_bf16;
+  int* status;
+};
+
+__device__ __forceinline__ int seq_len(const Params& p, int b) {
+  const int cap = p.max_pages << p.page_shift;
+  return max(0, min(p.seqlens[b], cap));
+}
+
+__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld8(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld4(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (BF16) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+
+// The 8 x 8 transpose of 16-bit elements held as two to a lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// Four codes' bytes of E2M1 pairs to fp16 pairs (exact).
+__device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// What one lane holds of 16 keys: for K rows r and r + 8 (r = lane / 4), for V
+// keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9 (q = lane % 4).
+template <int D, int FMT>
+struct Tile {
+  // 16 bits: K pieces q, q + 4, .. of a row (8 elements each); V pieces r, r + 8.
+  uint4 k[2][D / 32];
+  uint4 v[4][D / 64];
+
+  __device__ __forceinline__ void load_k(const Params& p, long long row0, int lane, int n_keys) {
+    const uint8_t* base = p.data[0] + row0 * (2 * D) + (lane & 3) * 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int key = (lane >> 2) + 8 * i;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+        k[i][c] = key < n_keys ? ld16(base + key * (2 * D) + c * 64) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __device__ __forceinline__ void load_v(const Params& p, long long row0, int lane, int n_keys) {
+    const uint8_t* base = p.data[1] + row0 * (2 * D) + (lane >> 2) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = 2 * (lane & 3) + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        v[i][c] = key < n_keys ? ld16(base + key * (2 * D) + c * 128) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  // s[t] += K Q^T for the 8 query heads of each tile t.
+  template <int NT>
+  __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&qf)[NT][D / 16][2]) const {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma16816<FMT == kBf16>(s[t], k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, qf[t][2 * c][0], qf[t][2 * c][1]);
+        mma16816<FMT == kBf16>(s[t], k[0][c].z, k[1][c].z, k[0][c].w, k[1][c].w, qf[t][2 * c + 1][0],
+                               qf[t][2 * c + 1][1]);
+      }
+  }
+  // o += V^T P^T; product j = 4 c + w holds elements 64 c + 8 r + 2 w (rows r)
+  // and the next one (rows r + 8).
+  template <int NT>
+  __device__ __forceinline__ void values(float (&o)[NT][D / 16][4], const uint32_t (&pf)[NT][2]) const {
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const uint32_t w[4][4] = {{v[0][c].x, v[0][c].y, v[0][c].z, v[0][c].w},
+                                {v[1][c].x, v[1][c].y, v[1][c].z, v[1][c].w},
+                                {v[2][c].x, v[2][c].y, v[2][c].z, v[2][c].w},
+                                {v[3][c].x, v[3][c].y, v[3][c].z, v[3][c].w}};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5410), a1 = __byte_perm(w[0][j], w[1][j], 0x7632);
+        const uint32_t a2 = __byte_perm(w[2][j], w[3][j], 0x5410), a3 = __byte_perm(w[2][j], w[3][j], 0x7632);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma16816<FMT == kBf16>(o[t][4 * c + j], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+      }
+    }
+  }
+  __device__ static __forceinline__ int k_element(int step, int lane, int half) {
+    return 32 * (step / 2) + 8 * (lane & 3) + 4 * (step & 1) + 2 * half;
+  }
+  __device__ static __forceinline__ int o_element(int j, int lane, int half) {
+    return 64 * (j / 4) + 8 * (lane >> 2) + 2 * (j & 3) + half;
+  }
+};
+
+template <int D>
+struct Tile<D, kFp4> {
+  // 4 bits: K piece q of a row (D / 4 elements, D / 64 groups); V piece r (D / 8).
+  static constexpr int kW = D / 32;  // 32-bit words of a K piece
+  static constexpr int kU = D / 64;  // of a V piece
+  uint32_t k[2][kW];
+  uint32_t kf[2];      // factors of the piece's groups, one to a byte
+  uint32_t v[4][kU];
+  uint32_t vf[4];
+
+  __device__ __forceinline__ void load_k(const Params& p, long long row0, int lane, int n_keys) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int key = (lane >> 2) + 8 * i;
+      const long long row = row0 + key;
+#pragma unroll
+      for (int j = 0; j < kW; ++j) k[i][j] = 0u;
+      kf[i] = 0u;
+      if (key < n_keys) {
+        const uint8_t* src = p.data[0] + row * (D / 2) + (lane & 3) * (D / 8);
+        const uint8_t* f = p.factor[0] + row * (D / 16) + (lane & 3) * (D / 64);
+        if constexpr (D == 128) {
+          const uint4 u = ld16(src);
+          k[i][0] = u.x, k[i][1] = u.y, k[i][2] = u.z, k[i][3] = u.w;
+          kf[i] = __ldg(reinterpret_cast<const uint16_t*>(f));
+        } else {
+          const uint2 u = ld8(src);
+          k[i][0] = u.x, k[i][1] = u.y;
+          kf[i] = __ldg(f);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void load_v(const Params& p, long long row0, int lane, int n_keys) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = 2 * (lane & 3) + (i & 1) + 8 * (i >> 1);
+      const long long row = row0 + key;
+#pragma unroll
+      for (int j = 0; j < kU; ++j) v[i][j] = 0u;
+      vf[i] = 0u;
+      if (key < n_keys) {
+        const uint8_t* src = p.data[1] + row * (D / 2) + (lane >> 2) * (D / 16);
+        vf[i] = __ldg(p.factor[1] + row * (D / 16) + ((lane >> 2) * (D / 8)) / 16);
+        if constexpr (D == 128) {
+          const uint2 u = ld8(src);
+          v[i][0] = u.x, v[i][1] = u.y;
+        } else {
+          v[i][0] = ld4(src);
+        }
+      }
+    }
+  }
+  template <int NT>
+  __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&qf)[NT][D / 16][2]) const {
+    uint32_t f2[2][D / 64];  // the group's factor in both halves
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t f = e4m3x2_to_f16(kf[i]);
+      f2[i][0] = __byte_perm(f, f, 0x1010);
+      if constexpr (D == 128) f2[i][1] = __byte_perm(f, f, 0x3232);
+    }
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      uint32_t a[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        e2m1_to_f16(k[i][w], a[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[i][e] = hmul2(a[i][e], f2[i][w / 2]);  // exact: 2 by 4 significant bits
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma16816<false>(s[t], a[0][0], a[1][0], a[0][1], a[1][1], qf[t][2 * w][0], qf[t][2 * w][1]);
+        mma16816<false>(s[t], a[0][2], a[1][2], a[0][3], a[1][3], qf[t][2 * w + 1][0], qf[t][2 * w + 1][1]);
+      }
+    }
+  }
+  // Product j holds elements (D / 8) r + 2 j (rows r) and the next (rows r + 8).
+  template <int NT>
+  __device__ __forceinline__ void values(float (&o)[NT][D / 16][4], const uint32_t (&pf)[NT][2]) const {
+    const uint32_t f01 = e4m3x2_to_f16(vf[0] | (vf[1] << 8)), f23 = e4m3x2_to_f16(vf[2] | (vf[3] << 8));
+#pragma unroll
+    for (int w = 0; w < kU; ++w) {
+      // Bytes (key a, key b) for the even elements, then for the odd ones.
+      uint32_t lo0[4], lo1[4], hi0[4], hi1[4];
+      e2m1_to_f16((v[0][w] & 0x0F0F0F0Fu) | ((v[1][w] << 4) & 0xF0F0F0F0u), lo0);
+      e2m1_to_f16(((v[0][w] >> 4) & 0x0F0F0F0Fu) | (v[1][w] & 0xF0F0F0F0u), lo1);
+      e2m1_to_f16((v[2][w] & 0x0F0F0F0Fu) | ((v[3][w] << 4) & 0xF0F0F0F0u), hi0);
+      e2m1_to_f16(((v[2][w] >> 4) & 0x0F0F0F0Fu) | (v[3][w] & 0xF0F0F0F0u), hi1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a0 = hmul2(lo0[j], f01), a1 = hmul2(lo1[j], f01);
+        const uint32_t a2 = hmul2(hi0[j], f23), a3 = hmul2(hi1[j], f23);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma16816<false>(o[t][4 * w + j], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+      }
+    }
+  }
+  __device__ static __forceinline__ int k_element(int step, int lane, int half) {
+    return (D / 4) * (lane & 3) + 4 * step + 2 * half;
+  }
+  __device__ static __forceinline__ int o_element(int j, int lane, int half) {
+    return (D / 8) * (lane >> 2) + 2 * j + half;
+  }
+};
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+constexpr int kUnitKeys = 16 * kWarps;
+
+template <int D, int FMT, int NT>
+__global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
+    decode_paged_kernel(const __grid_constant__ Params p) {
+  __shared__ float sm_o[kWarps][8 * NT][D + 4];
+  __shared__ float sm_ml[kWarps][8 * NT][2];
+  __shared__ long long sm_scan[kWarps + 1];
+  __shared__ int sm_b;
+  __shared__ long long sm_before;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int r = lane >> 2, q4 = lane & 3;
+  const int HG = p.Hkv * p.groups;
+
+  // ---- this CTA's run of units: [u0, u1) of U
+  long long mine = 0;
+  for (int b = threadIdx.x; b < p.B; b += kThreads) mine += (seq_len(p, b) + kUnitKeys - 1) / kUnitKeys;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sm_scan[warp] = mine;
+  __syncthreads();
+  long long tiles = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) tiles += sm_scan[w];
+  const long long U = tiles * HG;
+  const long long N = min(static_cast<long long>(gridDim.x), U);
+  if (blockIdx.x >= N) return;
+  const long long u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
+  // ---- the sequence that holds unit u0, and the tiles before it
+  const long long t0 = u0 / HG;
+  long long before = 0;
+  for (int base = 0;; base += kThreads) {
+    const int b = base + threadIdx.x;
+    const int n = b < p.B ? (seq_len(p, b) + kUnitKeys - 1) / kUnitKeys : 0;
+    long long incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();
+    if (lane == 31) sm_scan[warp] = incl;
+    __syncthreads();
+    long long off = before;
+    for (int w = 0; w < warp; ++w) off += sm_scan[w];
+    incl += off;
+    if (t0 >= incl - n && t0 < incl) {
+      sm_b = b;
+      sm_before = incl - n;
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) before += sm_scan[w];
+    if (t0 < before) break;  // t0 < tiles, so this ends
+  }
+  __syncthreads();
+  int b = sm_b;
+  long long rem = u0 - sm_before * HG;
+  int n_tiles = (seq_len(p, b) + kUnitKeys - 1) / kUnitKeys;
+  int hg = static_cast<int>(rem / n_tiles);
+  int tile = static_cast<int>(rem % n_tiles);
+
+  for (long long u = u0; u < u1;) {
+    const int L = seq_len(p, b);
+    n_tiles = (L + kUnitKeys - 1) / kUnitKeys;
+    const int tile_end = static_cast<int>(min(static_cast<long long>(n_tiles), tile + (u1 - u)));
+    const int kvh = hg / p.groups, grp = hg % p.groups;
+    const int head0 = kvh * p.g + grp * kMaxGroup;
+    const int n_heads = min(kMaxGroup, p.g - grp * kMaxGroup);
+
+    // ---- Q as the products' B operand, in the element order of K
+    uint32_t qf[NT][D / 16][2];
+    float lam[NT][2];  // base-2 units of a score, for the lane's two query columns
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int row = 8 * t + r;
+      const uint16_t* qrow = p.q + (static_cast<long long>(b) * p.Hq + head0 + row) * D;
+#pragma unroll
+      for (int st = 0; st < D / 16; ++st)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          qf[t][st][h] = row < n_heads
+                             ? *reinterpret_cast<const uint32_t*>(qrow + Tile<D, FMT>::k_element(st, lane, h))
+                             : 0u;
+      lam[t][0] = lam[t][1] = p.scale_log2;
+      if constexpr (FMT == kFp4) {
+        // The products are in fp16: scale the row by a power of two that brings
+        // its largest element to [1, 2).  Exact for bf16 too, but for elements
+        // under 2^-14 of the largest, which keep an error of 2^-25 of it.
+        float2 f[D / 16][2];
+        float top = 0.f;
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            f[st][h] = p.out_bf16 ? unpack2<true>(qf[t][st][h]) : unpack2<false>(qf[t][st][h]);
+            top = fmaxf(top, fmaxf(fabsf(f[st][h].x), fabsf(f[st][h].y)));
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // Exponent field in [2, 252]: both the factor and its inverse are normal.
+        const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 2), 252);
+        const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) qf[t][st][h] = pack2<false>(f[st][h].x * down, f[st][h].y * down);
+        const float kd = p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f;
+        const float row_lam = p.scale_log2 * kd * up;
+        lam[t][0] = __shfl_sync(0xffffffffu, row_lam, 8 * q4);
+        lam[t][1] = __shfl_sync(0xffffffffu, row_lam, 8 * q4 + 4);
+      }
+    }
+
+    float o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];  // per query column; l is this lane's share of the sum
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+    }
+
+    // ---- the keys: 16 of every 64 for this warp
+    for (int i = tile; i < tile_end; ++i) {
+      const int key0 = i * kUnitKeys + warp * 16;
+      int n_keys = min(16, L - key0);
+      if (n_keys <= 0) break;
+      const int page = p.page_table[static_cast<long long>(b) * p.max_pages + (key0 >> p.page_shift)];
+      if (page < 0 || page >= p.n_pages) {  // keys of a page that does not exist are left out
+        if (lane == 0) atomicCAS(p.status, 0, kStatusIndex);
+        continue;
+      }
+      const long long row0 = ((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) +
+                             (key0 & ((1 << p.page_shift) - 1));
+      Tile<D, FMT> tl;
+      tl.load_k(p, row0, lane, n_keys);
+      tl.load_v(p, row0, lane, n_keys);
+      float s[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+      tl.template scores<NT>(s, qf);
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float gamma[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float x0 = r < n_keys ? s[t][c] * lam[t][c] : -INFINITY;
+          const float x1 = r + 8 < n_keys ? s[t][2 + c] * lam[t][c] : -INFINITY;
+          float mx = fmaxf(x0, x1);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          gamma[c] = 1.f;
+          if (mx - m[t][c] > kRescaleThreshold) {
+            gamma[c] = ex2_approx(m[t][c] - mx);
+            m[t][c] = mx;
+          }
+          l[t][c] *= gamma[c];
+          const float ms = m[t][c] == -INFINITY ? 0.f : m[t][c];
+          s[t][c] = ex2_approx(x0 - ms);
+          s[t][2 + c] = ex2_approx(x1 - ms);
+          l[t][c] += s[t][c] + s[t][2 + c];
+        }
+        if (gamma[0] != 1.f || gamma[1] != 1.f) {
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            o[t][j][0] *= gamma[0];
+            o[t][j][1] *= gamma[1];
+            o[t][j][2] *= gamma[0];
+            o[t][j][3] *= gamma[1];
+          }
+        }
+        pf[t][0] = transpose8x8(pack2<FMT == kBf16>(s[t][0], s[t][1]));
+        pf[t][1] = transpose8x8(pack2<FMT == kBf16>(s[t][2], s[t][3]));
+      }
+      tl.template values<NT>(o, pf);
+    }
+
+    // ---- the four warps' states into one
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float v = l[t][c];
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        const int row = 8 * t + 2 * q4 + c;
+        if (r == 0) {
+          sm_ml[warp][row][0] = m[t][c];
+          sm_ml[warp][row][1] = v;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          sm_o[warp][row][Tile<D, FMT>::o_element(j, lane, 0)] = o[t][j][c];
+          sm_o[warp][row][Tile<D, FMT>::o_element(j, lane, 1)] = o[t][j][2 + c];
+        }
+      }
+    __syncthreads();
+    const bool whole = tile == 0 && tile_end == n_tiles;
+    const int slot = u == u0 ? 0 : 1;
+    const float vd = FMT == kFp4 && p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
+    for (int idx = threadIdx.x; idx < n_heads * (D / 2); idx += kThreads) {
+      const int row = idx / (D / 2), e = 2 * (idx % (D / 2));
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_ml[w][row][0]);
+      float a0 = 0.f, a1 = 0.f, ls = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = sm_ml[w][row][0];
+        const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - M);
+        if (f != 0.f) {
+          a0 += f * sm_o[w][row][e];
+          a1 += f * sm_o[w][row][e + 1];
+          ls += f * sm_ml[w][row][1];
+        }
+      }
+      a0 *= vd;
+      a1 *= vd;
+      if (whole) {
+        const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
+        const long long row_g = static_cast<long long>(b) * p.Hq + head0 + row;
+        *reinterpret_cast<uint32_t*>(p.o + row_g * D + e) =
+            p.out_bf16 ? pack2<true>(a0 * inv, a1 * inv) : pack2<false>(a0 * inv, a1 * inv);
+        if (e == 0 && p.lse != nullptr)
+          p.lse[row_g] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+      } else {
+        const long long st = (static_cast<long long>(blockIdx.x) * 2 + slot) * p.rows + row;
+        *reinterpret_cast<float2*>(p.part_o + st * D + e) = make_float2(a0, a1);
+        if (e == 0) *reinterpret_cast<float2*>(p.part_ml + st * 2) = make_float2(M, ls);
+      }
+    }
+    if (threadIdx.x == 0 && tile == 0) {
+      const long long last = u + n_tiles - 1;  // the segment's last unit
+      const int n_parts = whole ? 0 : static_cast<int>(((last + 1) * N - 1) / U) - static_cast<int>(blockIdx.x) + 1;
+      p.parts[static_cast<long long>(b) * HG + hg] = make_int2(static_cast<int>(blockIdx.x) * 2 + slot, n_parts);
+    }
+    __syncthreads();
+
+    u += tile_end - tile;
+    tile = 0;
+    if (u < u1) {
+      if (++hg == HG) {
+        hg = 0;
+        do ++b;
+        while (seq_len(p, b) == 0);  // a unit is left, so a sequence with keys follows
+      }
+    }
+  }
+}
+
+// One warp for each (sequence, query head): folds the parts of a segment that
+// was split, and writes the zeros of an empty sequence.
+template <int D>
+__global__ void __launch_bounds__(128) decode_paged_merge_kernel(const __grid_constant__ Params p) {
+  const long long row_g = static_cast<long long>(blockIdx.x) * 4 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (row_g >= static_cast<long long>(p.B) * p.Hq) return;
+  const int b = static_cast<int>(row_g / p.Hq), hq = static_cast<int>(row_g % p.Hq);
+  constexpr int kPer = D / 32;
+  float acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  float M = -INFINITY, ls = 0.f;
+  if (seq_len(p, b) > 0) {
+    const int kvh = hq / p.g, in_g = hq % p.g;
+    const int hg = kvh * p.groups + in_g / kMaxGroup, row = in_g % kMaxGroup;
+    const int2 part = p.parts[static_cast<long long>(b) * p.Hkv * p.groups + hg];
+    if (part.y == 0) return;  // finished by one CTA
+    // Part 0 is in the first CTA's slot; the others in slot 0 of the next CTAs.
+    auto state = [&](int i) {
+      const long long s = i == 0 ? part.x : (static_cast<long long>(part.x / 2) + i) * 2;
+      return s * p.rows + row;
+    };
+    for (int i = lane; i < part.y; i += 32) M = fmaxf(M, p.part_ml[state(i) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int i = 0; i < part.y; ++i) {
+      const long long st = state(i);
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + st * 2);
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      if (f == 0.f) continue;
+      ls += f * ml.y;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] += f * p.part_o[st * D + lane * kPer + e];
+    }
+  }
+  const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2) {
+    const float x = acc[e] * inv, y = acc[e + 1] * inv;
+    *reinterpret_cast<uint32_t*>(p.o + row_g * D + lane * kPer + e) = p.out_bf16 ? pack2<true>(x, y) : pack2<false>(x, y);
+  }
+  if (lane == 0 && p.lse != nullptr) p.lse[row_g] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+}
+
+int group_rows(int Hq, int Hkv) {
+  const int g = Hq / Hkv;
+  return g < kMaxGroup ? g : kMaxGroup;
+}
+
+template <int D, int FMT, int NT>
+int launch_t(const Params& p, const PagedDecodeArgs& a) {
+  auto kern = decode_paged_kernel<D, FMT, NT>;
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, 0) != cudaSuccess || per_sm < 1) {
+    cudaGetLastError();
+    return -1;
+  }
+  int ctas = per_sm * a.num_sms;
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  kern<<<ctas, kThreads, 0, a.stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return -1;
+  const long long rows = static_cast<long long>(a.B) * a.Hq;
+  decode_paged_merge_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, a.stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int D, int FMT>
+int launch_d(const Params& p, const PagedDecodeArgs& a) {
+  return p.rows > 8 ? launch_t<D, FMT, 2>(p, a) : launch_t<D, FMT, 1>(p, a);
+}
+
+}  // namespace
+
+size_t paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d) {
+  const size_t rows = group_rows(Hq, Hkv), groups = (Hq / Hkv + kMaxGroup - 1) / kMaxGroup;
+  return static_cast<size_t>(kMaxCtas) * 2 * rows * (static_cast<size_t>(d) + 2) * sizeof(float) +
+         static_cast<size_t>(B) * Hkv * groups * sizeof(int2);
+}
+
+int launch_decode_paged(const PagedDecodeArgs& a) {
+  Params p{};
+  const CacheArgs& c = a.cache;
+  p.q = static_cast<const uint16_t*>(a.q);
+  for (int i = 0; i < 2; ++i) {
+    p.data[i] = static_cast<const uint8_t*>(c.data[i]);
+    p.factor[i] = static_cast<const uint8_t*>(c.scale[i]);
+    p.descale[i] = c.descale[i];
+  }
+  p.page_table = c.page_table;
+  p.seqlens = c.seqlens;
+  p.o = static_cast<uint16_t*>(a.o);
+  p.lse = a.lse;
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = c.Hkv;
+  p.g = a.Hq / c.Hkv;
+  p.groups = (p.g + kMaxGroup - 1) / kMaxGroup;
+  p.rows = group_rows(a.Hq, c.Hkv);
+  p.page_shift = c.page_shift;
+  p.n_pages = c.n_pages;
+  p.max_pages = c.max_pages;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.out_bf16 = a.bf16 ? 1 : 0;
+  p.status = a.status;
+  float* ws = static_cast<float*>(a.workspace);
+  const size_t states = static_cast<size_t>(kMaxCtas) * 2 * p.rows;
+  p.part_o = ws;
+  p.part_ml = ws + states * c.d;
+  p.parts = reinterpret_cast<int2*>(ws + states * (c.d + 2));
+  if (c.d == 128) {
+    if (c.fp4()) return launch_d<128, kFp4>(p, a);
+    return a.bf16 ? launch_d<128, kBf16>(p, a) : launch_d<128, kF16>(p, a);
+  }
+  if (c.fp4()) return launch_d<64, kFp4>(p, a);
+  return a.bf16 ? launch_d<64, kBf16>(p, a) : launch_d<64, kF16>(p, a);
+}
+
+}  // namespace gbattn

@@ -37,9 +37,11 @@ long long g_timeline_capacity = 0;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+}  // namespace
+
 // Returns GBATTN_OK and the status pointer (and, if asked, the SM count) of
 // the current device, or an error.
-int current_device(int** status, int* sm_count = nullptr) {
+int current_device(int** status, int* sm_count) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
     cudaGetLastError();
@@ -72,8 +74,6 @@ int current_device(int** status, int* sm_count = nullptr) {
   if (sm_count != nullptr) *sm_count = g_sm_count[dev];
   return GBATTN_OK;
 }
-
-}  // namespace
 
 unsigned long long current_context_id() {
   using GetCurrentFn = CUresult (*)(CUcontext*);
@@ -295,7 +295,7 @@ int attn_decode_splitkv(const void* q, const void* k_cache, const void* v_cache,
   if (!workspace || !aligned16(workspace)) return GBATTN_EPOINTER;
   if (workspace_bytes < attn_decode_workspace_bytes(B, Hq, n_split, d)) return GBATTN_EWORKSPACE;
   int* status = nullptr;
-  int rc = current_device(&status);
+  int rc = current_device(&status, nullptr);
   if (rc != GBATTN_OK) return rc;
   DecodeArgs a;
   a.q = q;
@@ -340,7 +340,7 @@ int attn_bwd(const void* q, const void* k, const void* v, const void* o, const f
     return GBATTN_EBADSHAPE;
   if (workspace_bytes < attn_bwd_workspace_bytes(B, H, Sq, d)) return GBATTN_EWORKSPACE;
   int* status = nullptr;
-  int rc = current_device(&status);
+  int rc = current_device(&status, nullptr);
   if (rc != GBATTN_OK) return rc;
   BackwardArgs a;
   a.q = q;
@@ -390,7 +390,7 @@ int attn_bwd_atomic(const void* q, const void* k, const void* v, const void* o, 
     return GBATTN_EBADSHAPE;
   if (workspace_bytes < attn_bwd_atomic_workspace_bytes(B, H, Sq, d)) return GBATTN_EWORKSPACE;
   int* status = nullptr;
-  int rc = current_device(&status);
+  int rc = current_device(&status, nullptr);
   if (rc != GBATTN_OK) return rc;
   BackwardArgs a;
   a.q = q;
@@ -516,7 +516,7 @@ int gbattn_exp2_paths(const float* x, float* y_poly, float* y_hw, long long n, v
       (reinterpret_cast<uintptr_t>(y_poly) & 7u) || (reinterpret_cast<uintptr_t>(y_hw) & 7u))
     return GBATTN_EPOINTER;
   int* status = nullptr;
-  int rc = current_device(&status);
+  int rc = current_device(&status, nullptr);
   if (rc != GBATTN_OK) return rc;
   const long long n2 = n / 2, blocks = (n2 + 255) / 256;
   if (blocks > 0x7FFFFFFFLL) return GBATTN_EBADSHAPE;
@@ -544,7 +544,7 @@ __global__ void selftest_wait_kernel(int arrive, int* status) {
 
 int gbattn_selftest_bounded_wait(int arrive, void* stream) {
   int* status = nullptr;
-  int rc = current_device(&status);
+  int rc = current_device(&status, nullptr);
   if (rc != GBATTN_OK) return rc;
   selftest_wait_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(arrive ? 1 : 0, status);
   return cudaGetLastError() == cudaSuccess ? GBATTN_OK : GBATTN_ELAUNCH;
@@ -563,7 +563,7 @@ int gbattn_timeline_set(unsigned long long* records, long long capacity) {
 
 int gbattn_device_status(void) {
   int* status = nullptr;
-  int rc = current_device(&status);
+  int rc = current_device(&status, nullptr);
   if (rc != GBATTN_OK) return rc;
   if (cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
@@ -577,7 +577,7 @@ int gbattn_device_status(void) {
   if (value != 0) {
     const int zero = 0;
     cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
-    return GBATTN_EDEVICE_TIMEOUT;
+    return value == kStatusIndex ? GBATTN_EINDEX : GBATTN_EDEVICE_TIMEOUT;
   }
   return GBATTN_OK;
 }
@@ -594,6 +594,8 @@ const char* gbattn_error_string(int code) {
     case GBATTN_ELAUNCH: return "CUDA launch or tensor-map encoding failed";
     case GBATTN_EDEVICE_TIMEOUT: return "a kernel gave up on the device (bounded wait timed out or shared memory misaligned)";
     case GBATTN_ESPLIT: return "n_split out of range (1..256)";
+    case GBATTN_EPAGE: return "unsupported page size or rotation width";
+    case GBATTN_EINDEX: return "a page, slot or position was outside its table (skipped or clamped on the device)";
     case GBATTN_EUNSUPPORTED: return "no sm_103 device is current";
     default: return "unknown status code";
   }

@@ -88,8 +88,114 @@ struct PrefillFp8Args {
   long long timeline_capacity;     // records the buffer holds
 };
 
+// Device status word: a page, slot or position outside its table (the host maps
+// it to GBATTN_EINDEX).  One above the codes of DeviceStatus in gbattn_ptx.cuh.
+constexpr int kStatusIndex = 9;
+
+// Element strides of a [batch, heads, seq, d] tensor whose rows of d elements
+// are contiguous.
+struct RowStrides {
+  long long b, h, s;
+};
+
+// Position rotation of a head's first rot_dim elements: `table` holds, for each
+// of `rows` positions, rot_dim / 2 cosines and then rot_dim / 2 sines.
+struct RopeArgs {
+  const float* table;  // null when rot_dim = 0
+  int rows;
+  int rot_dim;
+  int interleaved;  // 1: pairs (2 i, 2 i + 1); 0: pairs (i, i + rot_dim / 2)
+};
+
+// Norm and rotation of queries and keys (qk_norm_rope.cu); with the gradients
+// for its backward.
+struct NormRopeArgs {
+  const void* x[2];         // q, k
+  const float* w[2];        // norm weights [d], or both null: rotation alone
+  void* y[2];               // forward: outputs [B, heads, S, d], contiguous
+  const void* dy[2];        // backward: gradients of y, contiguous
+  void* dx[2];              // backward: gradients of x
+  float* dw[2];             // backward: gradients of w [d]
+  RowStrides xs[2], dxs[2];
+  int heads[2];
+  const int* positions;     // [B, S] or null: 0 .. S - 1
+  RopeArgs rope;
+  float eps;
+  int B, S, d;
+  bool bf16;
+  float* workspace;         // backward: partial weight gradients
+  cudaStream_t stream;
+  int* status;
+  int num_sms;
+};
+
+// The two halves of a paged cache.  16-bit: data [n_pages, Hkv, page, d].
+// 4-bit: data holds E2M1 codes [n_pages, Hkv, page, d / 2] (the even element in
+// the low half of a byte) and scale the E4M3 factors [n_pages, Hkv, page, d / 16]
+// of its groups of 16; a value is code * factor * descale[head].
+struct CacheArgs {
+  void* data[2];            // keys, values
+  void* scale[2];           // null for a 16-bit cache
+  const float* descale[2];  // [Hkv] or null (1)
+  const int* page_table;    // [B, max_pages]
+  const int* seqlens;       // [B]
+  int Hkv, d, page_shift, n_pages, max_pages;
+  bool fp4() const { return scale[0] != nullptr; }
+};
+
+struct AppendArgs {
+  const void* x[3];  // q (or null), k, v
+  RowStrides xs[3];
+  void* q_out;       // [B, H, S, d], contiguous
+  CacheArgs cache;
+  const int* new_lens;  // [B] or null: S
+  RopeArgs rope;
+  int B, H, S;
+  bool bf16;
+  cudaStream_t stream;
+  int* status;
+  int num_sms;
+};
+
+struct GatherArgs {
+  CacheArgs cache;
+  void* out[2];  // [B, Hkv, S, d]
+  int B, S;
+  bool bf16;     // type of `out` (4-bit cache)
+  cudaStream_t stream;
+  int* status;
+  int num_sms;
+};
+
+struct PagedDecodeArgs {
+  const void* q;
+  CacheArgs cache;
+  void* o;
+  float* lse;
+  int B, Hq;
+  float scale;
+  void* workspace;
+  bool bf16;
+  cudaStream_t stream;
+  int* status;
+  int num_sms;
+};
+
+// Looks up the current device: its status word and number of SMs.  GBATTN_OK
+// or GBATTN_EUNSUPPORTED / GBATTN_ELAUNCH.
+int current_device(int** status, int* sm_count);
+
+// Bytes of workspace of the paged decode and of the norm's backward.
+size_t paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d);
+size_t norm_rope_bwd_workspace_bytes(int d);
+
 // Each returns a cudaError_t / CUresult folded into 0 (ok) or -1 (launch or
 // tensor-map failure).
+int launch_norm_rope(const NormRopeArgs& a);
+int launch_norm_rope_bwd(const NormRopeArgs& a);
+int launch_cache_append(const AppendArgs& a);
+int launch_cache_gather(const GatherArgs& a);
+int launch_decode_paged(const PagedDecodeArgs& a);
 int launch_prefill(const PrefillArgs& a);
 // Non-causal d = 128 forward on a tcgen05 CTA pair (prefill_pair.cu); -1 if
 // the arguments are outside that case or a launch failed.

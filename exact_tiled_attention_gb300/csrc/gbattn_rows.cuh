@@ -1,0 +1,146 @@
+// gbattn_rows.cuh -- how the row operators (norm and rotation, cache append)
+// hold one head's row of d 16-bit elements: D / 16 lanes of a warp share a row,
+// and each holds two chunks of 8 consecutive elements, [8 L, 8 L + 8) and
+// [D / 2 + 8 L, ...).  A full rotation pairs element i with i + D / 2, which is
+// then the same lane's; each of the two loads of a row is a contiguous D bytes.
+#pragma once
+
+#include <stdint.h>
+
+#include "gbattn_internal.h"
+#include "gbattn_ptx.cuh"
+
+namespace gbattn {
+
+template <int D>
+struct RowCfg {
+  static constexpr int kLanes = D / 16;       // lanes of a row
+  static constexpr int kRows = 32 / kLanes;   // rows of a warp
+};
+
+// How a kernel rotates: not at all, adjacent pairs, pairs half a head apart
+// (rot_dim = d), or pairs rot_dim / 2 apart in the first rot_dim elements.
+enum RopeMode : int { kRopeNone = 0, kRopePairs = 1, kRopeHalves = 2, kRopePart = 3 };
+
+inline RopeMode rope_mode(const RopeArgs& r, int d) {
+  if (r.rot_dim == 0) return kRopeNone;
+  if (r.interleaved) return kRopePairs;
+  return r.rot_dim == d ? kRopeHalves : kRopePart;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2<BF16>(f[0], f[1]), pack2<BF16>(f[2], f[3]), pack2<BF16>(f[4], f[5]),
+                    pack2<BF16>(f[6], f[7]));
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+// The rotation of one token, held by the lane for its own elements: for element
+// e of chunk c, y = x * cos + partner * sin, with sin already negative for the
+// first element of a pair.
+struct LaneRope {
+  float cos[2][8];
+  float sin[2][8];
+};
+
+// Loads the lane's cosines and sines of a table row.  Chunks outside the
+// rotated part get (1, 0).
+template <int D, int MODE>
+__device__ __forceinline__ void load_rope(LaneRope& r, const float* row, int rot, int lane_in_row) {
+  const int half = rot / 2;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int e0 = c * (D / 2) + 8 * lane_in_row;
+    if constexpr (MODE == kRopeHalves) {
+      if (c == 0) {
+        load8(row + e0, r.cos[0]);
+        load8(row + half + e0, r.sin[0]);
+      }
+    } else if (MODE != kRopeNone && e0 < rot) {
+      if constexpr (MODE == kRopePairs) {
+        const float4 co = *reinterpret_cast<const float4*>(row + e0 / 2);
+        const float4 si = *reinterpret_cast<const float4*>(row + half + e0 / 2);
+        const float cs[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          r.cos[c][2 * i] = r.cos[c][2 * i + 1] = cs[i];
+          r.sin[c][2 * i] = -ss[i];
+          r.sin[c][2 * i + 1] = ss[i];
+        }
+      } else {
+        const int i0 = e0 < half ? e0 : e0 - half;
+        load8(row + i0, r.cos[c]);
+        load8(row + half + i0, r.sin[c]);
+        if (e0 < half) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r.sin[c][i] = -r.sin[c][i];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.cos[c][i] = 1.f, r.sin[c][i] = 0.f;
+    }
+  }
+}
+
+// Offset of the chunk that holds the partners of the chunk at e0 when pairs
+// are rot / 2 apart in a part of the head (kRopePart); e0 itself outside it.
+__device__ __forceinline__ int partner_chunk(int e0, int rot) {
+  const int half = rot / 2;
+  return e0 < half ? e0 + half : (e0 < rot ? e0 - half : e0);
+}
+
+// Rotates the lane's two chunks z; `part` holds the partners' chunks when MODE
+// is kRopePart.  Products and sum are rounded one by one (no contraction into
+// a fused multiply-add): the 4-bit codes made from the result then do not
+// depend on how an expression is compiled.  BACK turns by the negative angle.
+template <int MODE, bool BACK>
+__device__ __forceinline__ void rotate(float (&z)[2][8], const float (&part)[2][8], const LaneRope& r) {
+  if constexpr (MODE == kRopeHalves) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = z[0][i], b = z[1][i], c = r.cos[0][i], s = BACK ? -r.sin[0][i] : r.sin[0][i];
+      z[0][i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+      z[1][i] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+    }
+  } else if constexpr (MODE == kRopePairs) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float a = z[c][i], b = z[c][i + 1], co = r.cos[c][i], s = BACK ? r.sin[c][i] : r.sin[c][i + 1];
+        z[c][i] = __fsub_rn(__fmul_rn(a, co), __fmul_rn(b, s));
+        z[c][i + 1] = __fadd_rn(__fmul_rn(b, co), __fmul_rn(a, s));
+      }
+  } else if constexpr (MODE == kRopePart) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float s = BACK ? -r.sin[c][i] : r.sin[c][i];
+        z[c][i] = __fadd_rn(__fmul_rn(z[c][i], r.cos[c][i]), __fmul_rn(part[c][i], s));
+      }
+  }
+}
+
+}  // namespace gbattn

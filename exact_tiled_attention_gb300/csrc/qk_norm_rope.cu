@@ -1,0 +1,337 @@
+// qk_norm_rope.cu -- RMS norm of every query and key head with the position
+// rotation in the same pass, and its backward.
+//
+// Forward, for one row x of d elements:  r = (mean x^2 + eps)^-1/2,  n = x r,
+// z = n o w,  y = R(position) z.  Backward, from dy:  dz = R^T dy,
+// dw += dz o n,  g = dz o w,  dx = r (g - n mean(g o n));  r and n are formed
+// again from x, which the backward reads anyway, so the forward saves nothing.
+//
+// Both are bound by HBM: a forward reads and writes each row once (2 bytes an
+// element each way), a backward reads two rows and writes one.  A thread keeps
+// one token's cosines and sines in registers and walks over heads, so the
+// 4-byte table is read once for several heads.
+#include <cuda_runtime.h>
+
+#include "gbattn_rows.cuh"
+
+namespace gbattn {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kMaxBwdCtas = 1024;  // partial weight gradients kept for each of q and k
+
+struct NormRopeParams {
+  const uint16_t* x[2];
+  const float* w[2];
+  uint16_t* y[2];
+  const uint16_t* dy[2];
+  uint16_t* dx[2];
+  RowStrides xs[2], dxs[2];
+  int heads[2];
+  int chunks[2];        // head chunks of q and of k
+  const int* positions;
+  const float* table;
+  int table_rows, rot;
+  float eps;
+  int B, S, per_chunk;  // heads that a thread walks over
+  float* partial;       // backward: [2][kMaxBwdCtas][D]
+  int* status;
+};
+
+// The table row of token (b, s); a position outside the table is clamped into
+// it and reported.
+__device__ __forceinline__ const float* table_row(const NormRopeParams& p, int b, int s) {
+  int pos = p.positions != nullptr ? p.positions[static_cast<long long>(b) * p.S + s] : s;
+  if (pos < 0 || pos >= p.table_rows) {
+    atomicCAS(p.status, 0, kStatusIndex);
+    pos = min(max(pos, 0), p.table_rows - 1);
+  }
+  return p.table + static_cast<long long>(pos) * p.rot;
+}
+
+template <int D>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = RowCfg<D>::kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int D, bool BF16, int MODE, bool NORM>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+  constexpr int kRowsCta = kThreads / RowCfg<D>::kLanes;
+  const int lane_in_row = threadIdx.x % RowCfg<D>::kLanes;
+  const long long tokens = static_cast<long long>(p.B) * p.S;
+  long long t = static_cast<long long>(blockIdx.x) * kRowsCta + threadIdx.x / RowCfg<D>::kLanes;
+  const bool real = t < tokens;
+  if (!real) t = tokens - 1;  // the whole warp stays for the shuffles
+  const int b = static_cast<int>(t / p.S), s = static_cast<int>(t % p.S);
+  const int which = blockIdx.y < p.chunks[0] ? 0 : 1;
+  const int h0 = (blockIdx.y - (which ? p.chunks[0] : 0)) * p.per_chunk;
+  const int h1 = min(h0 + p.per_chunk, p.heads[which]);
+  const int e0 = 8 * lane_in_row;
+
+  LaneRope rope;
+  if constexpr (MODE != kRopeNone) load_rope<D, MODE>(rope, table_row(p, b, s), p.rot, lane_in_row);
+  float w[2][8], wp[2][8];
+  int pc[2] = {0, 0};
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    if constexpr (MODE == kRopePart) pc[c] = partner_chunk(c * (D / 2) + e0, p.rot);
+    if constexpr (NORM) {
+      load8(p.w[which] + c * (D / 2) + e0, w[c]);
+      if constexpr (MODE == kRopePart) load8(p.w[which] + pc[c], wp[c]);
+    }
+  }
+  const RowStrides xs = p.xs[which];
+  const uint16_t* xrow = p.x[which] + b * xs.b + s * xs.s + h0 * xs.h;
+  uint16_t* yrow = p.y[which] + ((static_cast<long long>(b) * p.heads[which] + h0) * p.S + s) * D;
+  for (int h = h0; h < h1; ++h, xrow += xs.h, yrow += static_cast<long long>(p.S) * D) {
+    float z[2][8], part[2][8];
+    float sq = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + c * (D / 2) + e0), z[c]);
+      if constexpr (MODE == kRopePart) unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + pc[c]), part[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sq = fmaf(z[c][i], z[c][i], sq);
+    }
+    if constexpr (MODE == kRopePart) __syncwarp();  // a lane's partners are read before they are written (y may be x)
+    const float r = rsqrtf(row_sum<D>(sq) * (1.f / D) + p.eps);
+    if constexpr (NORM) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          z[c][i] *= r * w[c][i];
+          if constexpr (MODE == kRopePart) part[c][i] *= r * wp[c][i];
+        }
+    }
+    rotate<MODE, false>(z, part, rope);
+    if (real) {
+      *reinterpret_cast<uint4*>(yrow + e0) = pack8<BF16>(z[0]);
+      *reinterpret_cast<uint4*>(yrow + D / 2 + e0) = pack8<BF16>(z[1]);
+    }
+  }
+}
+
+// Grid: (CTAs that walk over tokens, head chunks of q then k).  With NORM each
+// CTA leaves the sum of its rows' weight gradients in `partial`.
+template <int D, bool BF16, int MODE, bool NORM>
+__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
+  constexpr int kLanes = RowCfg<D>::kLanes;
+  constexpr int kRowsCta = kThreads / kLanes;
+  const int lane_in_row = threadIdx.x % kLanes;
+  const long long tokens = static_cast<long long>(p.B) * p.S;
+  const int which = blockIdx.y < p.chunks[0] ? 0 : 1;
+  const int chunk = blockIdx.y - (which ? p.chunks[0] : 0);
+  const int h0 = chunk * p.per_chunk;
+  const int h1 = min(h0 + p.per_chunk, p.heads[which]);
+  const int e0 = 8 * lane_in_row;
+  int pc[2] = {0, 0};
+  float w[2][8], dw[2][8];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    if constexpr (MODE == kRopePart) pc[c] = partner_chunk(c * (D / 2) + e0, p.rot);
+    if constexpr (NORM) load8(p.w[which] + c * (D / 2) + e0, w[c]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
+  }
+  const RowStrides xs = p.xs[which], dxs = p.dxs[which];
+  for (long long t0 = static_cast<long long>(blockIdx.x) * kRowsCta; t0 < tokens;
+       t0 += static_cast<long long>(gridDim.x) * kRowsCta) {
+    long long t = t0 + threadIdx.x / kLanes;
+    const bool real = t < tokens;
+    if (!real) t = tokens - 1;
+    const int b = static_cast<int>(t / p.S), s = static_cast<int>(t % p.S);
+    LaneRope rope;
+    if constexpr (MODE != kRopeNone) load_rope<D, MODE>(rope, table_row(p, b, s), p.rot, lane_in_row);
+    const uint16_t* xrow = p.x[which] + b * xs.b + s * xs.s + h0 * xs.h;
+    uint16_t* dxrow = p.dx[which] + b * dxs.b + s * dxs.s + h0 * dxs.h;
+    const uint16_t* dyrow = p.dy[which] + ((static_cast<long long>(b) * p.heads[which] + h0) * p.S + s) * D;
+    for (int h = h0; h < h1; ++h, xrow += xs.h, dxrow += dxs.h, dyrow += static_cast<long long>(p.S) * D) {
+      float g[2][8], part[2][8];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        unpack8<BF16>(*reinterpret_cast<const uint4*>(dyrow + c * (D / 2) + e0), g[c]);
+        if constexpr (MODE == kRopePart) unpack8<BF16>(*reinterpret_cast<const uint4*>(dyrow + pc[c]), part[c]);
+      }
+      rotate<MODE, true>(g, part, rope);
+      if constexpr (NORM) {
+        float n[2][8];
+        float sq = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + c * (D / 2) + e0), n[c]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sq = fmaf(n[c][i], n[c][i], sq);
+        }
+        const float r = rsqrtf(row_sum<D>(sq) * (1.f / D) + p.eps);
+        float dot = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            n[c][i] *= r;
+            if (real) dw[c][i] = fmaf(g[c][i], n[c][i], dw[c][i]);
+            g[c][i] *= w[c][i];
+            dot = fmaf(g[c][i], n[c][i], dot);
+          }
+        dot = row_sum<D>(dot) * (1.f / D);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[c][i] = r * (g[c][i] - n[c][i] * dot);
+      }
+      if (real) {
+        *reinterpret_cast<uint4*>(dxrow + e0) = pack8<BF16>(g[0]);
+        *reinterpret_cast<uint4*>(dxrow + D / 2 + e0) = pack8<BF16>(g[1]);
+      }
+    }
+  }
+  if constexpr (NORM) {
+    __shared__ float sum[kThreads / 32][D];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int o = kLanes; o < 32; o <<= 1) dw[c][i] += __shfl_xor_sync(0xffffffffu, dw[c][i], o);
+        if (threadIdx.x % 32 < kLanes) sum[threadIdx.x / 32][c * (D / 2) + e0 + i] = dw[c][i];
+      }
+    __syncthreads();
+    const int row = chunk * gridDim.x + blockIdx.x;  // < kMaxBwdCtas
+    for (int i = threadIdx.x; i < D; i += kThreads) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < kThreads / 32; ++k) v += sum[k][i];
+      p.partial[(static_cast<long long>(which) * kMaxBwdCtas + row) * D + i] = v;
+    }
+  }
+}
+
+// dw[which][i] = sum of the CTAs' partials, in a fixed order.  Grid (D / 32, 2).
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ partial, int rows_q, int rows_k,
+                                                       int d, float* dwq, float* dwk) {
+  __shared__ float sum[32][33];
+  const int which = blockIdx.y, rows = which ? rows_k : rows_q;
+  const int col = threadIdx.x % 32, r0 = threadIdx.x / 32;
+  const float* base = partial + static_cast<long long>(which) * kMaxBwdCtas * d + blockIdx.x * 32 + col;
+  float v = 0.f;
+  for (int r = r0; r < rows; r += 32) v += base[static_cast<long long>(r) * d];
+  sum[r0][col] = v;
+  __syncthreads();
+  v = sum[col][r0];  // transposed: warp r0 holds column r0
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (col == 0) (which ? dwk : dwq)[blockIdx.x * 32 + r0] = v;
+}
+
+NormRopeParams params(const NormRopeArgs& a) {
+  NormRopeParams p{};
+  for (int i = 0; i < 2; ++i) {
+    p.x[i] = static_cast<const uint16_t*>(a.x[i]);
+    p.w[i] = a.w[i];
+    p.y[i] = static_cast<uint16_t*>(a.y[i]);
+    p.dy[i] = static_cast<const uint16_t*>(a.dy[i]);
+    p.dx[i] = static_cast<uint16_t*>(a.dx[i]);
+    p.xs[i] = a.xs[i];
+    p.dxs[i] = a.dxs[i];
+    p.heads[i] = a.heads[i];
+  }
+  p.positions = a.positions;
+  p.table = a.rope.table;
+  p.table_rows = a.rope.rows;
+  p.rot = a.rope.rot_dim;
+  p.eps = a.eps;
+  p.B = a.B;
+  p.S = a.S;
+  p.partial = a.workspace;
+  p.status = a.status;
+  return p;
+}
+
+void set_chunks(NormRopeParams& p, int per_chunk) {
+  p.per_chunk = per_chunk;
+  for (int i = 0; i < 2; ++i) p.chunks[i] = (p.heads[i] + per_chunk - 1) / per_chunk;
+}
+
+// Calls f with the rotation mode and the presence of a norm as constants.
+template <typename F>
+int with_mode(const NormRopeArgs& a, F&& f) {
+  const bool norm = a.w[0] != nullptr;
+  switch (rope_mode(a.rope, a.d)) {
+    case kRopeNone: return f(std::integral_constant<int, kRopeNone>(), std::true_type());
+    case kRopePairs:
+      return norm ? f(std::integral_constant<int, kRopePairs>(), std::true_type())
+                  : f(std::integral_constant<int, kRopePairs>(), std::false_type());
+    case kRopeHalves:
+      return norm ? f(std::integral_constant<int, kRopeHalves>(), std::true_type())
+                  : f(std::integral_constant<int, kRopeHalves>(), std::false_type());
+    default:
+      return norm ? f(std::integral_constant<int, kRopePart>(), std::true_type())
+                  : f(std::integral_constant<int, kRopePart>(), std::false_type());
+  }
+}
+
+template <int D, bool BF16>
+int launch_fwd(const NormRopeArgs& a) {
+  NormRopeParams p = params(a);
+  const long long tokens = static_cast<long long>(a.B) * a.S;
+  const long long token_ctas = (tokens + kThreads / RowCfg<D>::kLanes - 1) / (kThreads / RowCfg<D>::kLanes);
+  const int heads = a.heads[0] + a.heads[1];
+  // As many heads a thread as leave four CTAs for each SM, at most 8.
+  int per = 8;
+  while (per > 1 && token_ctas * (heads / per) < 4LL * a.num_sms) per /= 2;
+  set_chunks(p, per);
+  if (token_ctas > 0x7FFFFFFFLL || p.chunks[0] + p.chunks[1] > 65535) return -1;
+  const dim3 grid(static_cast<unsigned>(token_ctas), p.chunks[0] + p.chunks[1]);
+  return with_mode(a, [&](auto mode, auto norm) {
+    norm_rope_kernel<D, BF16, decltype(mode)::value, decltype(norm)::value><<<grid, kThreads, 0, a.stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  });
+}
+
+template <int D, bool BF16>
+int launch_bwd(const NormRopeArgs& a) {
+  NormRopeParams p = params(a);
+  const long long tokens = static_cast<long long>(a.B) * a.S;
+  const long long token_ctas = (tokens + kThreads / RowCfg<D>::kLanes - 1) / (kThreads / RowCfg<D>::kLanes);
+  const int heads = a.heads[0] + a.heads[1];
+  int per = 4;
+  while (per > 1 && token_ctas * (heads / per) < 4LL * a.num_sms) per /= 2;
+  const int most = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
+  while ((most + per - 1) / per > kMaxBwdCtas) per *= 2;
+  set_chunks(p, per);
+  const int most_chunks = p.chunks[0] > p.chunks[1] ? p.chunks[0] : p.chunks[1];
+  // CTAs over tokens: eight for each SM in all, and no more partials than fit.
+  long long x = (8LL * a.num_sms + p.chunks[0] + p.chunks[1] - 1) / (p.chunks[0] + p.chunks[1]);
+  if (x > kMaxBwdCtas / most_chunks) x = kMaxBwdCtas / most_chunks;
+  if (x > token_ctas) x = token_ctas;
+  const dim3 grid(static_cast<unsigned>(x), p.chunks[0] + p.chunks[1]);
+  const int rc = with_mode(a, [&](auto mode, auto norm) {
+    norm_rope_bwd_kernel<D, BF16, decltype(mode)::value, decltype(norm)::value><<<grid, kThreads, 0, a.stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  });
+  if (rc != 0 || a.w[0] == nullptr) return rc;
+  norm_dw_kernel<<<dim3(D / 32, 2), 1024, 0, a.stream>>>(p.partial, static_cast<int>(x) * p.chunks[0],
+                                                         static_cast<int>(x) * p.chunks[1], D, a.dw[0], a.dw[1]);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+size_t norm_rope_bwd_workspace_bytes(int d) {
+  return 2 * static_cast<size_t>(kMaxBwdCtas) * static_cast<size_t>(d) * sizeof(float);
+}
+
+int launch_norm_rope(const NormRopeArgs& a) {
+  if (a.d == 128) return a.bf16 ? launch_fwd<128, true>(a) : launch_fwd<128, false>(a);
+  return a.bf16 ? launch_fwd<64, true>(a) : launch_fwd<64, false>(a);
+}
+
+int launch_norm_rope_bwd(const NormRopeArgs& a) {
+  if (a.d == 128) return a.bf16 ? launch_bwd<128, true>(a) : launch_bwd<128, false>(a);
+  return a.bf16 ? launch_bwd<64, true>(a) : launch_bwd<64, false>(a);
+}
+
+}  // namespace gbattn

@@ -26,7 +26,8 @@
  *    `stream` (a cudaStream_t; NULL = legacy default stream) and the call
  *    returns immediately.
  *  - Layout: every tensor is contiguous row-major [batch, heads, seq, d]
- *    ("BHSD"); LSE is contiguous fp32 [batch, heads, seq].
+ *    ("BHSD"); LSE is contiguous fp32 [batch, heads, seq].  The operators
+ *    around a paged cache (below) also take rows at other strides.
  *  - Pointers must be 16-byte aligned.  Element type of q/k/v/o is given by
  *    `dtype` (GBATTN_F16 or GBATTN_BF16); arithmetic is fp32 with fp16/bf16
  *    tensor-core operands; O is rounded to `dtype` (round-to-nearest-even).
@@ -63,6 +64,8 @@ extern "C" {
                                        shared-memory base was not 1024-byte aligned (gbattn_device_status) */
 #define GBATTN_ESPLIT (-9)          /* decode n_split < 1 or > 256 */
 #define GBATTN_EUNSUPPORTED (-10)   /* no sm_103a device, or the current device is not sm_103 */
+#define GBATTN_EPAGE (-11)          /* page size not a power of two in 16 .. 1024, or rot_dim not a multiple of 16 <= d */
+#define GBATTN_EINDEX (-12)         /* a kernel met a page, slot or position outside its table (gbattn_device_status) */
 
 /* Element types of q/k/v/o. */
 #define GBATTN_F16 0
@@ -324,6 +327,206 @@ int attn_decode_splitkv_noalloc(const void *q, const void *k_cache, const void *
 size_t attn_decode_noalloc_scratch_bytes(void);
 
 /*
+ * ---- Around a paged cache --------------------------------------------------
+ *
+ * A paged cache keeps keys and values in pages of page_size tokens (a power of
+ * two, 16 .. 1024).  Token t of sequence b lies in slot t % page_size of page
+ * page_table[b][t / page_size]:
+ *   16 bits: k_cache, v_cache [n_pages, Hkv, page_size, d] in `dtype`
+ *   4 bits:  k_codes, v_codes [n_pages, Hkv, page_size, d / 2] bytes, two E2M1
+ *            codes each (the even element in the low half);
+ *            k_factors, v_factors [n_pages, Hkv, page_size, d / 16] E4M3FN
+ *            bytes, one for each 16 elements of a row;
+ *            k_descale, v_descale [Hkv] fp32 or NULL (1).  An element is
+ *            code * factor * descale[head].
+ *   page_table [B, max_pages] int32; entries behind a sequence's last page
+ *            are not read.  seqlens [B] int32: tokens of each sequence, 0 for
+ *            an idle one; values are clamped into [0, max_pages * page_size].
+ * Both are device arrays, read when the kernels run, so a captured graph
+ * follows them.  A page that is needed but not in [0, n_pages) is neither read
+ * nor written: its tokens are not stored, read back as zeros, or left out of
+ * the attention, and gbattn_device_status() reports GBATTN_EINDEX.  So do
+ * positions outside the rotation's table, which are clamped into it.
+ *
+ * The position rotation of a head's first rot_dim elements (a multiple of 16,
+ * at most d; 0 turns it off and `rope` may be NULL) takes its angles from
+ * rope [rope_rows, rot_dim] fp32: row p holds the rot_dim / 2 cosines and then
+ * the rot_dim / 2 sines of position p.  It pairs elements (i, i + rot_dim / 2),
+ * or (2 i, 2 i + 1) where `interleaved` is not 0:
+ *   (a, b) -> (a cos - b sin, b cos + a sin), in fp32.
+ *
+ * q_strides, k_strides, ... are NULL for a contiguous [B, heads, S, d] tensor,
+ * or three host values: the distances, in elements, of consecutive sequences,
+ * heads and tokens (multiples of 8; a head's d elements are contiguous), so
+ * views of one projection output [B, S, (H + 2 Hkv) d] need no copy.
+ *
+ * One step of serving: attn_qk_norm_rope where the model has such norms (and
+ * then no rotation here), attn_cache_append, attn_decode_paged.  A chunk of a
+ * prompt: append it, attn_cache_gather the sequence, attn_fwd with causal = 1.
+ */
+
+/*
+ * attn_qk_norm_rope -- RMS norm of every query and key head and the position
+ * rotation, in one pass.  For each row x of d elements:
+ *   y = R(position) (w o x / sqrt(mean(x^2) + eps)),  in fp32, rounded once.
+ *
+ *   q [B, H, S, d], k [B, Hkv, S, d]  dtype, inputs (any strides)
+ *   q_weight, k_weight [d]  fp32, 16-byte aligned; both NULL: no norm, the
+ *            rotation alone (rot_dim > 0 then)
+ *   positions [B, S]  int32 device array, or NULL: token s has position s
+ *            (rope_rows >= S then)
+ *   q_out [B, H, S, d], k_out [B, Hkv, S, d]  dtype, outputs, contiguous;
+ *            q_out may be q and k_out k where those are contiguous
+ *
+ * Errors: GBATTN_EBADSHAPE (also H > 16384), EHEADS, EHEADDIM, EDTYPE, EPAGE
+ * (rot_dim), EPOINTER (also strides that are no multiples of 8, one weight
+ * without the other, and neither norm nor rotation), EUNSUPPORTED, ELAUNCH.
+ */
+int attn_qk_norm_rope(const void *q, const void *k, const float *q_weight, const float *k_weight,
+                      const float *rope, const int *positions, void *q_out, void *k_out,
+                      int B, int H, int Hkv, int S, int d, const long long *q_strides,
+                      const long long *k_strides, float eps, int rope_rows, int rot_dim,
+                      int interleaved, int dtype, void *stream);
+
+/*
+ * attn_qk_norm_rope_bwd_workspace_bytes -- bytes of device workspace that
+ * attn_qk_norm_rope_bwd needs with weights (partial weight gradients); 0 for an
+ * unsupported d.  Without weights no workspace is used.
+ */
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
+
+/*
+ * attn_qk_norm_rope_bwd -- gradients of attn_qk_norm_rope.  With r the row's
+ * reciprocal norm, n = r x and dz = R(position)^T dy:
+ *   dw = sum over rows of dz o n,   dx = r (g - n mean(g o n)),  g = dz o w.
+ *
+ *   dq_out [B, H, S, d], dk_out [B, Hkv, S, d]  dtype, inputs, contiguous:
+ *            the gradients of q_out and k_out (attn_bwd's dq and dk)
+ *   q, k, weights, rope, positions: as passed to attn_qk_norm_rope
+ *   dq, dk   dtype, outputs at their own strides; they overlap no input
+ *   dq_weight, dk_weight [d]  fp32, outputs (with weights): summed over all
+ *            rows in a fixed order, so they repeat bitwise
+ *   workspace: at least attn_qk_norm_rope_bwd_workspace_bytes(d) bytes,
+ *            16-byte aligned; contents on entry do not matter
+ *
+ * Errors: as attn_qk_norm_rope, and GBATTN_EWORKSPACE.
+ */
+int attn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                          const float *q_weight, const float *k_weight, const float *rope,
+                          const int *positions, void *dq, void *dk, float *dq_weight,
+                          float *dk_weight, int B, int H, int Hkv, int S, int d,
+                          const long long *q_strides, const long long *k_strides,
+                          const long long *dq_strides, const long long *dk_strides, float eps,
+                          int rope_rows, int rot_dim, int interleaved, void *workspace,
+                          size_t workspace_bytes, int dtype, void *stream);
+
+/*
+ * attn_cache_append -- writes new keys and values into a 16-bit paged cache,
+ * with the position rotation of the keys (and of the queries) on the way.
+ *
+ *   k, v     [B, Hkv, S, d]  dtype, inputs (any strides)
+ *   seqlens  counts each sequence's tokens WITH the new ones, as the following
+ *            attn_decode_paged wants it; new_lens [B] int32 (NULL: S for all)
+ *            says how many of the S rows are real.  Row i < new_lens[b] is the
+ *            token at position seqlens[b] - new_lens[b] + i.  Rows from
+ *            new_lens[b] on, and rows whose position is negative (an idle
+ *            sequence has length 0), are padding: nothing is stored for them.
+ *   q        [B, H, S, d]  dtype, input (any strides), or NULL: rotated by the
+ *            same positions into q_out [B, H, S, d] (contiguous; zeros for
+ *            padding rows; NULL where q is); q_out overlaps no input
+ * The slots that one call writes are distinct (pages that several sequences
+ * share are for reading).  All other slots stay as they are.
+ *
+ * Errors: GBATTN_EBADSHAPE (also H > 16384), EHEADS, EHEADDIM, EDTYPE, EPAGE
+ * (page_size or rot_dim), EPOINTER, EUNSUPPORTED, ELAUNCH.
+ */
+int attn_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
+                      const int *page_table, const int *seqlens, const int *new_lens,
+                      const float *rope, const void *q, void *q_out, int B, int H, int Hkv, int S,
+                      int d, int page_size, int n_pages, int max_pages,
+                      const long long *q_strides, const long long *k_strides,
+                      const long long *v_strides, int rope_rows, int rot_dim, int interleaved,
+                      int dtype, void *stream);
+
+/*
+ * attn_cache_append_fp4 -- attn_cache_append into a 4-bit paged cache.  Each
+ * group of 16 elements x (keys after the rotation, in fp32) gets
+ *   factor = E4M3(min(448, max|x| / (6 descale))),
+ *   code   = E2M1(x * (1 / (factor * descale)))
+ * both rounded to nearest even and saturating; factor 0 gives codes 0.  NaN has
+ * no code: it is stored as a number.  The codes and factors are those of the
+ * formula in IEEE fp32 arithmetic, whatever order the tokens come in.
+ *
+ * Errors: as attn_cache_append.
+ */
+int attn_cache_append_fp4(const void *k, const void *v, void *k_codes, void *k_factors,
+                          void *v_codes, void *v_factors, const float *k_descale,
+                          const float *v_descale, const int *page_table, const int *seqlens,
+                          const int *new_lens, const float *rope, const void *q, void *q_out,
+                          int B, int H, int Hkv, int S, int d, int page_size, int n_pages,
+                          int max_pages, const long long *q_strides, const long long *k_strides,
+                          const long long *v_strides, int rope_rows, int rot_dim, int interleaved,
+                          int dtype, void *stream);
+
+/*
+ * attn_cache_gather -- reads the first S tokens of every sequence of a paged
+ * cache into contiguous k_out, v_out [B, Hkv, S, d] (dtype), as attn_fwd takes
+ * them; rows from seqlens[b] on are written as zeros.
+ * attn_cache_gather_fp4 -- the same from a 4-bit cache: (code * factor) *
+ * descale in fp32, rounded once to dtype.
+ *
+ * Errors: GBATTN_EBADSHAPE (also B * Hkv > 65535), EHEADDIM, EDTYPE, EPAGE,
+ * EPOINTER, EUNSUPPORTED, ELAUNCH.
+ */
+int attn_cache_gather(const void *k_cache, const void *v_cache, const int *page_table,
+                      const int *seqlens, void *k_out, void *v_out, int B, int Hkv, int S, int d,
+                      int page_size, int n_pages, int max_pages, int dtype, void *stream);
+int attn_cache_gather_fp4(const void *k_codes, const void *k_factors, const void *v_codes,
+                          const void *v_factors, const float *k_descale, const float *v_descale,
+                          const int *page_table, const int *seqlens, void *k_out, void *v_out,
+                          int B, int Hkv, int S, int d, int page_size, int n_pages, int max_pages,
+                          int dtype, void *stream);
+
+/*
+ * attn_decode_paged_workspace_bytes -- bytes of device workspace the paged
+ * decodes need: two partial states (m, l, o[d]) of up to 16 query heads for
+ * each CTA of the grid, and two ints for each (sequence, unit of query heads).
+ * Does not depend on the lengths.  Returns 0 for invalid sizes.
+ */
+size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
+
+/*
+ * attn_decode_paged -- one-query decode over a 16-bit paged cache.
+ *
+ *   q [B, Hq, 1, d]  dtype, input;  o [B, Hq, 1, d]  dtype, output
+ *   lse [B, Hq]  fp32, output; may be NULL
+ *   seqlens: a sequence of length 0 gets o = 0 and lse = -inf
+ *   workspace: at least attn_decode_paged_workspace_bytes(B, Hq, Hkv, d) bytes,
+ *            16-byte aligned; contents on entry do not matter; calls that may
+ *            overlap on the GPU need one each
+ * The key axes of all sequences are divided evenly over the GPU, whatever the
+ * lengths are, so there is no number of splits to choose; the division follows
+ * from the lengths alone and results repeat bitwise.
+ *
+ * attn_decode_paged_fp4 -- the same over a 4-bit cache (q and o in dtype, which
+ * the cache does not depend on).
+ *
+ * Errors: GBATTN_EBADSHAPE (also B > 65535, Hq > 16384), EHEADS, EHEADDIM,
+ * EDTYPE, EPAGE, EPOINTER, EWORKSPACE, EUNSUPPORTED, ELAUNCH.
+ */
+int attn_decode_paged(const void *q, const void *k_cache, const void *v_cache,
+                      const int *page_table, const int *seqlens, void *o, float *lse, int B,
+                      int Hq, int Hkv, int d, int page_size, int n_pages, int max_pages,
+                      float scale, void *workspace, size_t workspace_bytes, int dtype,
+                      void *stream);
+int attn_decode_paged_fp4(const void *q, const void *k_codes, const void *k_factors,
+                          const void *v_codes, const void *v_factors, const float *k_descale,
+                          const float *v_descale, const int *page_table, const int *seqlens,
+                          void *o, float *lse, int B, int Hq, int Hkv, int d, int page_size,
+                          int n_pages, int max_pages, float scale, void *workspace,
+                          size_t workspace_bytes, int dtype, void *stream);
+
+/*
  * gbattn_causal_tile_counts -- host-only planning helper (no device work).
  * Classifies the (ceil(Sq/Br) x ceil(Sk/Bc)) tile grid with the half-open
  * ranges of M4.4 0x05.1A-B and delta = Sk - Sq:
@@ -368,7 +571,8 @@ int gbattn_selftest_bounded_wait(int arrive, void *stream);
 
 /*
  * gbattn_device_status -- read and clear the library's device status word.
- * Returns GBATTN_OK, or GBATTN_EDEVICE_TIMEOUT if a kernel gave up since the
+ * Returns GBATTN_OK, or GBATTN_EINDEX if a kernel met a page, slot or position
+ * outside its table, or GBATTN_EDEVICE_TIMEOUT if a kernel gave up since the
  * last call (a bounded wait timed out, or a shared-memory alignment check
  * failed), or GBATTN_ELAUNCH if the device reported an error.
  *
