@@ -23,6 +23,8 @@
 // for P V, and l sums the unrounded values.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "gbattn_internal.h"
 #include "gbattn_ptx.cuh"
 
@@ -34,6 +36,9 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 1024;        // bound of the grid, for the workspace's size
 constexpr int kMaxGroup = 16;         // query heads of one unit
 constexpr float kRescaleThreshold = 8.f;
+// The reference before any key: finite, so that a masked score minus it is -inf,
+// and below every score that does not overflow.
+constexpr float kNoReference = -3e38f;
 
 enum Format : int { kF16 = 0, kBf16 = 1, kFp4 = 2 };
 
@@ -68,14 +73,35 @@ __device__ __forceinline__ uint4 ld16(const uint8_t* p) {
                : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint2 ld8(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+// An asynchronous copy of 16 bytes into shared memory, past L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+__device__ __forceinline__ void lds(uint32_t (&v)[4], uint32_t a) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void lds(uint32_t (&v)[2], uint32_t a) {
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void lds(uint32_t (&v)[1], uint32_t a) {
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t ld4(const uint8_t* p) {
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
 
@@ -119,45 +145,84 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
+template <int NT>
+__device__ __forceinline__ void zero(float (&s)[NT][4]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+}
+template <int NT>
+__device__ __forceinline__ void add(float (&s)[NT][4], const float (&s2)[NT][4]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[t][c] += s2[t][c];
+}
+
+// Where a lane's pieces of the pool's first 16 rows lie.
+struct LanePtrs {
+  const uint8_t* data[2];
+  const uint8_t* factor;  // 4 bits: the piece of K's or V's factors that the lane copies
+};
+
 // What one lane holds of 16 keys: for K rows r and r + 8 (r = lane / 4), for V
-// keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9 (q = lane % 4).
+// keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9 (q = lane % 4).  Keys from n_keys on are
+// not read (zeros): a unit's last rows may lie behind the sequence.
 template <int D, int FMT>
 struct Tile {
   // 16 bits: K pieces q, q + 4, .. of a row (8 elements each); V pieces r, r + 8.
   uint4 k[2][D / 32];
   uint4 v[4][D / 64];
 
-  __device__ __forceinline__ void load_k(const Params& p, long long row0, int lane, int n_keys) {
-    const uint8_t* base = p.data[0] + row0 * (2 * D) + (lane & 3) * 16;
+  __device__ static __forceinline__ LanePtrs ptrs(const Params& p, int lane) {
+    LanePtrs a{};
+    a.data[0] = p.data[0] + (lane >> 2) * (2 * D) + (lane & 3) * 16;
+    a.data[1] = p.data[1] + (2 * (lane & 3)) * (2 * D) + (lane >> 2) * 16;
+    return a;
+  }
+  __device__ __forceinline__ void load_k(const LanePtrs& a, int block, int lane, int n_keys) {
+    const uint8_t* src = a.data[0] + static_cast<long long>(block) * (16 * 2 * D);
+    if (n_keys >= 16) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int key = (lane >> 2) + 8 * i;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-        k[i][c] = key < n_keys ? ld16(base + key * (2 * D) + c * 64) : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < D / 32; ++c) k[i][c] = ld16(src + 8 * i * (2 * D) + c * 64);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          k[i][c] = (lane >> 2) + 8 * i < n_keys ? ld16(src + 8 * i * (2 * D) + c * 64) : make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  __device__ __forceinline__ void load_v(const Params& p, long long row0, int lane, int n_keys) {
-    const uint8_t* base = p.data[1] + row0 * (2 * D) + (lane >> 2) * 16;
+  __device__ __forceinline__ void load_v(const LanePtrs& a, int block, int lane, int n_keys) {
+    const uint8_t* src = a.data[1] + static_cast<long long>(block) * (16 * 2 * D);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int key = 2 * (lane & 3) + (i & 1) + 8 * (i >> 1);
+      const int key = (i & 1) + 8 * (i >> 1);
+      if (n_keys >= 16 || 2 * (lane & 3) + key < n_keys) {
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        v[i][c] = key < n_keys ? ld16(base + key * (2 * D) + c * 128) : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < D / 64; ++c) v[i][c] = ld16(src + key * (2 * D) + c * 128);
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) v[i][c] = make_uint4(0u, 0u, 0u, 0u);
+      }
     }
   }
-  // s[t] += K Q^T for the 8 query heads of each tile t.
+  // s[t] = K Q^T for the 8 query heads of each tile t, in two chains of products.
   template <int NT>
   __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&qf)[NT][D / 16][2]) const {
+    float s2[NT][4];
+    zero(s);
+    zero(s2);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         mma16816<FMT == kBf16>(s[t], k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, qf[t][2 * c][0], qf[t][2 * c][1]);
-        mma16816<FMT == kBf16>(s[t], k[0][c].z, k[1][c].z, k[0][c].w, k[1][c].w, qf[t][2 * c + 1][0],
+        mma16816<FMT == kBf16>(s2[t], k[0][c].z, k[1][c].z, k[0][c].w, k[1][c].w, qf[t][2 * c + 1][0],
                                qf[t][2 * c + 1][1]);
       }
+    add(s, s2);
   }
   // o += V^T P^T; product j = 4 c + w holds elements 64 c + 8 r + 2 w (rows r)
   // and the next one (rows r + 8).
@@ -186,6 +251,37 @@ struct Tile {
   }
 };
 
+// 16 keys of a 4-bit cache in shared memory, one stage of a warp's own ring,
+// which asynchronous copies of 16 bytes fill.  Rows of V of 64 bytes are stored
+// in pairs of 128 bytes with their 16-byte pieces permuted, so that the four
+// keys that 16 lanes read at a time lie in different banks.
+template <int D>
+struct Stage {
+  static constexpr int kRow = D / 2, kFactors = D / 16;  // bytes of a row
+  static constexpr int kV = 16 * kRow, kKf = 2 * kV, kVf = kKf + 16 * kFactors;
+  static constexpr int kBytes = kVf + 16 * kFactors;
+
+  __device__ static __forceinline__ int v_offset(int key, int byte) {
+    if constexpr (D == 64) return key * kRow + byte;
+    return (key >> 1) * 128 + ((((key & 1) << 2 | byte >> 4) ^ ((key >> 1 & 3) << 1)) << 4) + (byte & 15);
+  }
+  static constexpr int kPieces = kFactors;  // 16-byte pieces of 16 rows' factors of K (and of V)
+  // All 16 rows of a block (a page holds whole blocks).
+  __device__ static __forceinline__ void fill(const LanePtrs& a, uint32_t stage, int block, int lane) {
+    const uint8_t* k = a.data[0] + static_cast<long long>(block) * kV;
+    const uint8_t* v = a.data[1] + static_cast<long long>(block) * kV;
+    const int byte = lane * 16;
+    const uint32_t to_k = stage + byte, to_v = stage + kV + v_offset(byte / kRow, byte % kRow);
+#pragma unroll
+    for (int i = 0; i < kV / 512; ++i) {  // 512 bytes on: 8 keys on, where the pieces lie alike
+      copy16(to_k + i * 512, k + i * 512);
+      copy16(to_v + i * 512, v + i * 512);
+    }
+    if (lane < 2 * kPieces)
+      copy16(stage + kKf + byte, a.factor + static_cast<long long>(block) * (16 * kFactors));
+  }
+};
+
 template <int D>
 struct Tile<D, kFp4> {
   // 4 bits: K piece q of a row (D / 4 elements, D / 64 groups); V piece r (D / 8).
@@ -196,51 +292,39 @@ struct Tile<D, kFp4> {
   uint32_t v[4][kU];
   uint32_t vf[4];
 
-  __device__ __forceinline__ void load_k(const Params& p, long long row0, int lane, int n_keys) {
+  __device__ static __forceinline__ LanePtrs ptrs(const Params& p, int lane) {
+    LanePtrs a;
+    a.data[0] = p.data[0] + lane * 16;
+    a.data[1] = p.data[1] + lane * 16;
+    a.factor = p.factor[lane / Stage<D>::kPieces & 1] + lane % Stage<D>::kPieces * 16;
+    return a;
+  }
+  __device__ __forceinline__ void load_k(uint32_t stage, int lane) {
+    const int r = lane >> 2, q = lane & 3;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int key = (lane >> 2) + 8 * i;
-      const long long row = row0 + key;
-#pragma unroll
-      for (int j = 0; j < kW; ++j) k[i][j] = 0u;
-      kf[i] = 0u;
-      if (key < n_keys) {
-        const uint8_t* src = p.data[0] + row * (D / 2) + (lane & 3) * (D / 8);
-        const uint8_t* f = p.factor[0] + row * (D / 16) + (lane & 3) * (D / 64);
-        if constexpr (D == 128) {
-          const uint4 u = ld16(src);
-          k[i][0] = u.x, k[i][1] = u.y, k[i][2] = u.z, k[i][3] = u.w;
-          kf[i] = __ldg(reinterpret_cast<const uint16_t*>(f));
-        } else {
-          const uint2 u = ld8(src);
-          k[i][0] = u.x, k[i][1] = u.y;
-          kf[i] = __ldg(f);
-        }
-      }
+      lds(k[i], stage + (r + 8 * i) * (D / 2) + q * (D / 8));
+      const uint32_t f = stage + Stage<D>::kKf + (r + 8 * i) * (D / 16) + q * (D / 64);
+      kf[i] = D == 128 ? lds_u16(f) : lds_u8(f);
     }
   }
-  __device__ __forceinline__ void load_v(const Params& p, long long row0, int lane, int n_keys) {
+  // Keys from n_keys on get factor 0: whatever their slots hold does not count.
+  template <bool WHOLE>
+  __device__ __forceinline__ void load_v(uint32_t stage, int lane, int n_keys) {
+    const int r = lane >> 2, q = lane & 3;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int key = 2 * (lane & 3) + (i & 1) + 8 * (i >> 1);
-      const long long row = row0 + key;
-#pragma unroll
-      for (int j = 0; j < kU; ++j) v[i][j] = 0u;
-      vf[i] = 0u;
-      if (key < n_keys) {
-        const uint8_t* src = p.data[1] + row * (D / 2) + (lane >> 2) * (D / 16);
-        vf[i] = __ldg(p.factor[1] + row * (D / 16) + ((lane >> 2) * (D / 8)) / 16);
-        if constexpr (D == 128) {
-          const uint2 u = ld8(src);
-          v[i][0] = u.x, v[i][1] = u.y;
-        } else {
-          v[i][0] = ld4(src);
-        }
-      }
+      const int key = 2 * q + (i & 1) + 8 * (i >> 1);
+      lds(v[i], stage + Stage<D>::kV + Stage<D>::v_offset(key, r * (D / 16)));
+      vf[i] = lds_u8(stage + Stage<D>::kVf + key * (D / 16) + r * (D / 8) / 16);
+      if (!WHOLE && key >= n_keys) vf[i] = 0u;
     }
   }
   template <int NT>
   __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&qf)[NT][D / 16][2]) const {
+    float s2[NT][4];
+    zero(s);
+    zero(s2);
     uint32_t f2[2][D / 64];  // the group's factor in both halves
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -260,21 +344,22 @@ struct Tile<D, kFp4> {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         mma16816<false>(s[t], a[0][0], a[1][0], a[0][1], a[1][1], qf[t][2 * w][0], qf[t][2 * w][1]);
-        mma16816<false>(s[t], a[0][2], a[1][2], a[0][3], a[1][3], qf[t][2 * w + 1][0], qf[t][2 * w + 1][1]);
+        mma16816<false>(s2[t], a[0][2], a[1][2], a[0][3], a[1][3], qf[t][2 * w + 1][0], qf[t][2 * w + 1][1]);
       }
     }
+    add(s, s2);
   }
   // Product j holds elements (D / 8) r + 2 j (rows r) and the next (rows r + 8).
   template <int NT>
   __device__ __forceinline__ void values(float (&o)[NT][D / 16][4], const uint32_t (&pf)[NT][2]) const {
-    const uint32_t f01 = e4m3x2_to_f16(vf[0] | (vf[1] << 8)), f23 = e4m3x2_to_f16(vf[2] | (vf[3] << 8));
+    const uint32_t f01 = e4m3x2_to_f16(vf[0] + vf[1] * 256u), f23 = e4m3x2_to_f16(vf[2] + vf[3] * 256u);
 #pragma unroll
     for (int w = 0; w < kU; ++w) {
       // Bytes (key a, key b) for the even elements, then for the odd ones.
       uint32_t lo0[4], lo1[4], hi0[4], hi1[4];
-      e2m1_to_f16((v[0][w] & 0x0F0F0F0Fu) | ((v[1][w] << 4) & 0xF0F0F0F0u), lo0);
+      e2m1_to_f16((v[0][w] & 0x0F0F0F0Fu) | ((v[1][w] * 16u) & 0xF0F0F0F0u), lo0);
       e2m1_to_f16(((v[0][w] >> 4) & 0x0F0F0F0Fu) | (v[1][w] & 0xF0F0F0F0u), lo1);
-      e2m1_to_f16((v[2][w] & 0x0F0F0F0Fu) | ((v[3][w] << 4) & 0xF0F0F0F0u), hi0);
+      e2m1_to_f16((v[2][w] & 0x0F0F0F0Fu) | ((v[3][w] * 16u) & 0xF0F0F0F0u), hi0);
       e2m1_to_f16(((v[2][w] >> 4) & 0x0F0F0F0Fu) | (v[3][w] & 0xF0F0F0F0u), hi1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -299,12 +384,91 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-constexpr int kUnitKeys = 16 * kWarps;
+constexpr int kStages = 3;  // of a warp's ring (4-bit caches)
+
+// Blocks of 16 keys that a warp works on at a time.
+template <int FMT>
+constexpr int kBlocks = FMT == kFp4 ? 2 : 1;
+template <int FMT>
+constexpr int kUnitKeys = 16 * kBlocks<FMT> * kWarps;
+
+// Scores s of KB blocks of 16 keys (in units of the products) to P as the operand
+// of P V, and the state (m, l, o) brought up to them.  A block's keys from
+// n_keys on do not count (WHOLE: there are none).
+template <int D, bool BF16, bool WHOLE, int KB, int NT>
+__device__ __forceinline__ void softmax_step(float (&s)[KB][NT][4], const float (&lam)[NT][2], int r, const int (&n_keys)[KB],
+                                             float (&m)[NT][2], float (&l)[NT][2], float (&o)[NT][D / 16][4],
+                                             uint32_t (&pf)[KB][NT][2]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    // Exponents relative to the reference; it moves (for the whole warp) only
+    // where one of them is above the threshold.
+    float x[KB][4];
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        s[k][t][c] *= lam[t][c & 1];
+        if (!WHOLE && r + 8 * (c >> 1) >= n_keys[k]) s[k][t][c] = -INFINITY;
+        x[k][c] = s[k][t][c] - m[t][c & 1];
+        top = fmaxf(top, x[k][c]);
+      }
+    if (__any_sync(0xffffffffu, top > kRescaleThreshold)) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < KB; ++k) mx = fmaxf(mx, fmaxf(s[k][t][c], s[k][t][2 + c]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        if (mx > m[t][c]) {
+          const float gamma = ex2_approx(m[t][c] - mx);  // 0 for the first keys (m = kNoReference)
+          m[t][c] = mx;
+          l[t][c] *= gamma;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            o[t][j][c] *= gamma;
+            o[t][j][2 + c] *= gamma;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+          x[k][c] = s[k][t][c] - m[t][c];
+          x[k][2 + c] = s[k][t][2 + c] - m[t][c];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        x[k][c] = ex2_approx(x[k][c]);
+        l[t][c & 1] += x[k][c];
+      }
+      pf[k][t][0] = transpose8x8(pack2<BF16>(x[k][0], x[k][1]));
+      pf[k][t][1] = transpose8x8(pack2<BF16>(x[k][2], x[k][3]));
+    }
+  }
+}
+
+// Dynamic shared memory of a CTA.
+template <int D, int FMT, int NT>
+struct Smem {
+  static constexpr int kRing = FMT == kFp4 ? kStages * kBlocks<FMT> * Stage<D>::kBytes : 0;
+  static constexpr int kStates = 8 * NT * (D + 4) * 4;  // of a warp
+  static constexpr int kBytes = kWarps * (kRing > kStates ? kRing : kStates);
+};
 
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
     decode_paged_kernel(const __grid_constant__ Params p) {
-  __shared__ float sm_o[kWarps][8 * NT][D + 4];
+  using C = Smem<D, FMT, NT>;
+  constexpr int KB = kBlocks<FMT>, UK = kUnitKeys<FMT>;
+  // The warps' rings (4 bits), and at a segment's end their states.
+  extern __shared__ __align__(128) uint8_t sm_raw[];
+  auto sm_o = reinterpret_cast<float (*)[8 * NT][D + 4]>(sm_raw);
   __shared__ float sm_ml[kWarps][8 * NT][2];
   __shared__ long long sm_scan[kWarps + 1];
   __shared__ int sm_b;
@@ -312,10 +476,12 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int r = lane >> 2, q4 = lane & 3;
   const int HG = p.Hkv * p.groups;
+  [[maybe_unused]] const uint32_t ring = smem_u32(sm_raw) + warp * C::kRing;
+  const LanePtrs src = Tile<D, FMT>::ptrs(p, lane);
 
   // ---- this CTA's run of units: [u0, u1) of U
   long long mine = 0;
-  for (int b = threadIdx.x; b < p.B; b += kThreads) mine += (seq_len(p, b) + kUnitKeys - 1) / kUnitKeys;
+  for (int b = threadIdx.x; b < p.B; b += kThreads) mine += (seq_len(p, b) + UK - 1) / UK;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) sm_scan[warp] = mine;
@@ -332,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
   long long before = 0;
   for (int base = 0;; base += kThreads) {
     const int b = base + threadIdx.x;
-    const int n = b < p.B ? (seq_len(p, b) + kUnitKeys - 1) / kUnitKeys : 0;
+    const int n = b < p.B ? (seq_len(p, b) + UK - 1) / UK : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -356,13 +522,13 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
   __syncthreads();
   int b = sm_b;
   long long rem = u0 - sm_before * HG;
-  int n_tiles = (seq_len(p, b) + kUnitKeys - 1) / kUnitKeys;
+  int n_tiles = (seq_len(p, b) + UK - 1) / UK;
   int hg = static_cast<int>(rem / n_tiles);
   int tile = static_cast<int>(rem % n_tiles);
 
   for (long long u = u0; u < u1;) {
     const int L = seq_len(p, b);
-    n_tiles = (L + kUnitKeys - 1) / kUnitKeys;
+    n_tiles = (L + UK - 1) / UK;
     const int tile_end = static_cast<int>(min(static_cast<long long>(n_tiles), tile + (u1 - u)));
     const int kvh = hg / p.groups, grp = hg % p.groups;
     const int head0 = kvh * p.g + grp * kMaxGroup;
@@ -419,68 +585,112 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
-      m[t][0] = m[t][1] = -INFINITY;
+      m[t][0] = m[t][1] = kNoReference;
       l[t][0] = l[t][1] = 0.f;
     }
 
-    // ---- the keys: 16 of every 64 for this warp
-    for (int i = tile; i < tile_end; ++i) {
-      const int key0 = i * kUnitKeys + warp * 16;
-      int n_keys = min(16, L - key0);
-      if (n_keys <= 0) break;
-      const int page = p.page_table[static_cast<long long>(b) * p.max_pages + (key0 >> p.page_shift)];
-      if (page < 0 || page >= p.n_pages) {  // keys of a page that does not exist are left out
+    // ---- the keys: piece 4 i + warp, of KB blocks of 16 keys, of every unit i
+    Tile<D, FMT> tl;
+    const int* pages = p.page_table + static_cast<long long>(b) * p.max_pages;
+    const int warp_keys = L - warp * (16 * KB);  // keys from this warp's first one on
+    const int end = min(tile_end, (warp_keys + UK - 1) / UK);
+    const int whole_end = (warp_keys + UK - 16 * KB) / UK;  // units before it have all of the warp's keys
+    const int block_shift = p.page_shift - 4;               // log2 of a page's blocks
+    const int head_block = kvh << block_shift, page_blocks = p.Hkv << block_shift;
+    // Page of a block of the sequence (behind the last: any), and the pool's
+    // block, or -1 for a page that does not exist: its keys are left out.
+    auto page_of = [&](int blk) { return 16 * blk < L ? __ldg(pages + (blk >> block_shift)) : 0; };
+    auto block_of = [&](int blk, int page) {
+      if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) {
         if (lane == 0) atomicCAS(p.status, 0, kStatusIndex);
-        continue;
+        return -1;
       }
-      const long long row0 = ((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) +
-                             (key0 & ((1 << p.page_shift) - 1));
-      Tile<D, FMT> tl;
-      tl.load_k(p, row0, lane, n_keys);
-      tl.load_v(p, row0, lane, n_keys);
-      float s[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-      tl.template scores<NT>(s, qf);
-      uint32_t pf[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float gamma[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float x0 = r < n_keys ? s[t][c] * lam[t][c] : -INFINITY;
-          const float x1 = r + 8 < n_keys ? s[t][2 + c] * lam[t][c] : -INFINITY;
-          float mx = fmaxf(x0, x1);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          gamma[c] = 1.f;
-          if (mx - m[t][c] > kRescaleThreshold) {
-            gamma[c] = ex2_approx(m[t][c] - mx);
-            m[t][c] = mx;
-          }
-          l[t][c] *= gamma[c];
-          const float ms = m[t][c] == -INFINITY ? 0.f : m[t][c];
-          s[t][c] = ex2_approx(x0 - ms);
-          s[t][2 + c] = ex2_approx(x1 - ms);
-          l[t][c] += s[t][c] + s[t][2 + c];
+      return page * page_blocks + head_block + (blk & ((1 << block_shift) - 1));
+    };
+    if constexpr (FMT == kFp4) {
+      // kStages - 1 units are on their way while one is worked on.
+      int page0 = page_of((tile * kWarps + warp) * KB), page1 = page_of((tile * kWarps + warp) * KB + 1);
+      unsigned absent = 0;  // two bits a request, the newest lowest: block k has no page
+      auto request = [&](int i, uint32_t stage) {
+        absent <<= 2;
+        if (i < end) {
+          const int blk = (i * kWarps + warp) * KB;
+          const int b0 = block_of(blk, page0), b1 = block_of(blk + 1, page1);
+          const int next = blk + kWarps * KB;
+          page0 = page_of(next);
+          page1 = page_of(next + 1);
+          if (b0 >= 0) Stage<D>::fill(src, stage, b0, lane);
+          if (b1 >= 0) Stage<D>::fill(src, stage + Stage<D>::kBytes, b1, lane);
+          absent |= (b0 < 0 ? 1u : 0u) | (b1 < 0 ? 2u : 0u);
         }
-        if (gamma[0] != 1.f || gamma[1] != 1.f) {
+        copy_commit();
+      };
+      constexpr uint32_t kUnitBytes = KB * Stage<D>::kBytes;
 #pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            o[t][j][0] *= gamma[0];
-            o[t][j][1] *= gamma[1];
-            o[t][j][2] *= gamma[0];
-            o[t][j][3] *= gamma[1];
+      for (int i = 0; i < kStages - 1; ++i) request(tile + i, ring + i * kUnitBytes);
+      uint32_t stage = ring, free_stage = ring + (kStages - 1) * kUnitBytes;
+      for (int i = tile; i < end; ++i) {
+        copy_wait<kStages - 2>();
+        __syncwarp();  // every lane's copies of unit i, and every lane done with unit i - 1
+        request(i + kStages - 1, free_stage);
+        auto step = [&](auto whole, int n0, int n1) {
+          const int n_keys[KB] = {n0, n1};
+          float s[KB][NT][4];
+          uint32_t pf[KB][NT][2];
+#pragma unroll
+          for (int k = 0; k < KB; ++k) {
+            tl.load_k(stage + k * Stage<D>::kBytes, lane);
+            tl.template scores<NT>(s[k], qf);
           }
-        }
-        pf[t][0] = transpose8x8(pack2<FMT == kBf16>(s[t][0], s[t][1]));
-        pf[t][1] = transpose8x8(pack2<FMT == kBf16>(s[t][2], s[t][3]));
+          softmax_step<D, false, decltype(whole)::value, KB, NT>(s, lam, r, n_keys, m, l, o, pf);
+#pragma unroll
+          for (int k = 0; k < KB; ++k) {
+            tl.template load_v<decltype(whole)::value>(stage + k * Stage<D>::kBytes, lane, n_keys[k]);
+            tl.template values<NT>(o, pf[k]);
+          }
+        };
+        const unsigned gone = absent >> (2 * (kStages - 1)) & 3;
+        const int left = warp_keys - i * UK;
+        if (i < whole_end && gone == 0)
+          step(std::true_type(), 16, 16);
+        else
+          step(std::false_type(), gone & 1 ? 0 : left, gone & 2 ? 0 : left - 16);
+        free_stage = stage;
+        stage = stage == ring + (kStages - 1) * kUnitBytes ? ring : stage + kUnitBytes;
       }
-      tl.template values<NT>(o, pf);
+      copy_wait<0>();
+    } else {
+      // A unit's K is requested right after the previous unit's scores and its V
+      // right after the previous P V, into the registers that those have freed.
+      int n_keys[1] = {0}, page_next = 0;
+      if (tile < end) {
+        const int blk = tile * kWarps + warp, block = block_of(blk, page_of(blk));
+        n_keys[0] = block < 0 ? 0 : L - 16 * blk;
+        page_next = page_of(blk + kWarps);
+        tl.load_k(src, block, lane, n_keys[0]);
+        tl.load_v(src, block, lane, n_keys[0]);
+      }
+      for (int i = tile; i < end; ++i) {
+        float s[1][NT][4];
+        uint32_t pf[1][NT][2];
+        tl.template scores<NT>(s[0], qf);
+        int n_next = 0, block = 0;
+        if (i + 1 < end) {
+          const int blk = (i + 1) * kWarps + warp;
+          block = block_of(blk, page_next);
+          n_next = block < 0 ? 0 : L - 16 * blk;
+          page_next = page_of(blk + kWarps);
+          tl.load_k(src, block, lane, n_next);
+        }
+        softmax_step<D, FMT == kBf16, false, 1, NT>(s, lam, r, n_keys, m, l, o, pf);
+        tl.template values<NT>(o, pf[0]);
+        if (i + 1 < end) tl.load_v(src, block, lane, n_next);
+        n_keys[0] = n_next;
+      }
     }
 
     // ---- the four warps' states into one
+    if constexpr (FMT == kFp4) __syncthreads();  // the states take the rings' place
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -506,14 +716,13 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
     const float vd = FMT == kFp4 && p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
     for (int idx = threadIdx.x; idx < n_heads * (D / 2); idx += kThreads) {
       const int row = idx / (D / 2), e = 2 * (idx % (D / 2));
-      float M = -INFINITY;
+      float M = kNoReference;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_ml[w][row][0]);
       float a0 = 0.f, a1 = 0.f, ls = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float mw = sm_ml[w][row][0];
-        const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - M);
+        const float f = ex2_approx(sm_ml[w][row][0] - M);
         if (f != 0.f) {
           a0 += f * sm_o[w][row][e];
           a1 += f * sm_o[w][row][e + 1];
@@ -566,7 +775,7 @@ __global__ void __launch_bounds__(128) decode_paged_merge_kernel(const __grid_co
   float acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  float M = -INFINITY, ls = 0.f;
+  float M = kNoReference, ls = 0.f;
   if (seq_len(p, b) > 0) {
     const int kvh = hq / p.g, in_g = hq % p.g;
     const int hg = kvh * p.groups + in_g / kMaxGroup, row = in_g % kMaxGroup;
@@ -583,7 +792,7 @@ __global__ void __launch_bounds__(128) decode_paged_merge_kernel(const __grid_co
     for (int i = 0; i < part.y; ++i) {
       const long long st = state(i);
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + st * 2);
-      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      const float f = ex2_approx(ml.x - M);
       if (f == 0.f) continue;
       ls += f * ml.y;
 #pragma unroll
@@ -607,14 +816,22 @@ int group_rows(int Hq, int Hkv) {
 template <int D, int FMT, int NT>
 int launch_t(const Params& p, const PagedDecodeArgs& a) {
   auto kern = decode_paged_kernel<D, FMT, NT>;
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, 0) != cudaSuccess || per_sm < 1) {
-    cudaGetLastError();
-    return -1;
+  constexpr int kBytes = Smem<D, FMT, NT>::kBytes;
+  static std::atomic<unsigned long long> attr_done{0};  // per instantiation
+  if (!set_smem_limit_once(kern, kBytes, attr_done)) return -1;
+  // CTAs that fit on an SM; the same on every GPU this library runs on.
+  static std::atomic<int> fit{0};
+  int per_sm = fit.load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, kBytes) != cudaSuccess || per_sm < 1) {
+      cudaGetLastError();
+      return -1;
+    }
+    fit.store(per_sm, std::memory_order_relaxed);
   }
   int ctas = per_sm * a.num_sms;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  kern<<<ctas, kThreads, 0, a.stream>>>(p);
+  kern<<<ctas, kThreads, kBytes, a.stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return -1;
   const long long rows = static_cast<long long>(a.B) * a.Hq;
   decode_paged_merge_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, a.stream>>>(p);

@@ -45,6 +45,8 @@ int check_cache(CacheArgs* out, const void* k, const void* v, const void* k_fact
   if (d != 64 && d != 128) return GBATTN_EHEADDIM;
   if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1))) return GBATTN_EPAGE;
   if (static_cast<long long>(max_pages) * page_size > 0x7FFFFFFFLL - 64) return GBATTN_EBADSHAPE;
+  // The kernels count blocks of 16 tokens of one head in 32 bits.
+  if (static_cast<long long>(n_pages) * Hkv > (0x7FFFFFFFLL << 4) / page_size) return GBATTN_EBADSHAPE;
   if (!k || !v || !page_table || !seqlens || misaligned16(k) || misaligned16(v) || misaligned4(page_table) ||
       misaligned4(seqlens) || misaligned4(k_descale) || misaligned4(v_descale))
     return GBATTN_EPOINTER;

@@ -12,6 +12,8 @@
 // 4-byte table is read once for several heads.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "gbattn_rows.cuh"
 
 namespace gbattn {
