@@ -121,12 +121,23 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   }
   const RowStrides xs = p.xs[which];
   const uint16_t* xrow = p.x[which] + b * xs.b + i * xs.s + h0 * xs.h;
+  // Rows that nothing is stored of are not read; a warp without others is done.
+  const bool read = which == 0 ? real : stored;
+  if (which != 0 && __all_sync(0xffffffffu, !read)) return;
+  // The next head's row is requested before this one is worked on.
+  uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  auto request = [&](const uint16_t* row) {
+    if (read) {
+      raw[0] = *reinterpret_cast<const uint4*>(row + e0);
+      raw[1] = *reinterpret_cast<const uint4*>(row + D / 2 + e0);
+    }
+  };
+  request(xrow);
   for (int h = h0; h < h1; ++h, xrow += xs.h) {
-    const uint4 u0 = *reinterpret_cast<const uint4*>(xrow + e0);
-    const uint4 u1 = *reinterpret_cast<const uint4*>(xrow + D / 2 + e0);
     float z[2][8], part[2][8];
-    unpack8<BF16>(u0, z[0]);
-    unpack8<BF16>(u1, z[1]);
+    unpack8<BF16>(raw[0], z[0]);
+    unpack8<BF16>(raw[1], z[1]);
+    if (h + 1 < h1) request(xrow + xs.h);
     if constexpr (MODE != kRopeNone) {
       if (which != 2) {
         if constexpr (MODE == kRopePart) {
@@ -180,54 +191,72 @@ struct GatherParams {
   int* status;
 };
 
-// Grid (row blocks of one (batch, head), B * Hkv, 2).  A thread writes 16
-// elements (32 bytes) of one row.
+constexpr int kGatherPasses = 8;  // rows of a thread, all requested before the first is written
+
+// Grid (row blocks of one (batch, head), B * Hkv, 2).  A thread writes 8
+// elements (16 bytes) of each of its rows, so that a warp's store is 512
+// consecutive bytes.
 template <int D, bool BF16, bool FP4>
 __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_constant__ GatherParams p) {
-  constexpr int kParts = D / 16;
+  constexpr int kParts = D / 8, kRowsPass = kThreads / kParts;
   const int which = blockIdx.z;
   const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
-  const int s = blockIdx.x * (kThreads / kParts) + threadIdx.x / kParts;
+  const int s0 = blockIdx.x * (kRowsPass * kGatherPasses) + threadIdx.x / kParts;
   const int part = threadIdx.x % kParts;
-  if (s >= p.S) return;
-  uint4 y0 = make_uint4(0u, 0u, 0u, 0u), y1 = y0;
-  if (s < p.seqlens[b]) {
-    const int pg = s >> p.page_shift;
-    const int page = pg < p.max_pages ? p.page_table[static_cast<long long>(b) * p.max_pages + pg] : -1;
-    if (page < 0 || page >= p.n_pages) {
-      atomicCAS(p.status, 0, kStatusIndex);
-    } else {
-      const long long row = ((static_cast<long long>(page) * p.Hkv + h) << p.page_shift) +
+  const int n = min(p.seqlens[b], p.S);
+  int page[kGatherPasses];
+#pragma unroll
+  for (int u = 0; u < kGatherPasses; ++u) {
+    const int s = s0 + u * kRowsPass, pg = s >> p.page_shift;
+    page[u] = s < n && pg < p.max_pages ? p.page_table[static_cast<long long>(b) * p.max_pages + pg] : -1;
+  }
+  uint4 y[kGatherPasses];
+  uint32_t f[kGatherPasses];
+#pragma unroll
+  for (int u = 0; u < kGatherPasses; ++u) {
+    const int s = s0 + u * kRowsPass;
+    y[u] = make_uint4(0u, 0u, 0u, 0u);
+    f[u] = 0u;  // a row behind the sequence: factor 0
+    if (static_cast<unsigned>(page[u]) < static_cast<unsigned>(p.n_pages)) {
+      const long long row = ((static_cast<long long>(page[u]) * p.Hkv + h) << p.page_shift) +
                             (s & ((1 << p.page_shift) - 1));
       if constexpr (FP4) {
-        const uint2 codes = *reinterpret_cast<const uint2*>(p.data[which] + row * (D / 2) + part * 8);
-        const float f = e4m3_value(p.scale[which][row * (D / 16) + part]);
-        const float ds = p.descale[which] != nullptr ? p.descale[which][h] : 1.f;
-        float z[2][8];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t w = c ? codes.y : codes.x;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t h2;
-            asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h2) : "r"(w >> (8 * k)));
-            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-            z[c][2 * k] = __fmul_rn(__fmul_rn(t.x, f), ds);
-            z[c][2 * k + 1] = __fmul_rn(__fmul_rn(t.y, f), ds);
-          }
-        }
-        y0 = pack8<BF16>(z[0]);
-        y1 = pack8<BF16>(z[1]);
+        y[u].x = *reinterpret_cast<const uint32_t*>(p.data[which] + row * (D / 2) + part * 4);
+        f[u] = p.scale[which][row * (D / 16) + part / 2];
       } else {
-        const uint4* src = reinterpret_cast<const uint4*>(p.data[which] + row * (D * 2) + part * 32);
-        y0 = src[0];
-        y1 = src[1];
+        y[u] = *reinterpret_cast<const uint4*>(p.data[which] + row * (D * 2) + part * 16);
       }
+    } else if (s < n) {
+      atomicCAS(p.status, 0, kStatusIndex);
     }
   }
-  uint4* dst = reinterpret_cast<uint4*>(p.out[which] + (static_cast<long long>(blockIdx.y) * p.S + s) * D + part * 16);
-  dst[0] = y0;
-  dst[1] = y1;
+  const float ds = FP4 && p.descale[which] != nullptr ? p.descale[which][h] : 1.f;
+  uint16_t* out = p.out[which] + static_cast<long long>(blockIdx.y) * p.S * D + part * 8;
+#pragma unroll
+  for (int u = 0; u < kGatherPasses; ++u) {
+    const int s = s0 + u * kRowsPass;
+    if (s >= p.S) break;
+    if constexpr (FP4) {
+      float z[8];
+      if (f[u] != 0) {
+        const float fv = e4m3_value(f[u]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h2;
+          asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+              : "=r"(h2)
+              : "r"(y[u].x >> (8 * k)));
+          const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+          z[2 * k] = __fmul_rn(__fmul_rn(t.x, fv), ds);
+          z[2 * k + 1] = __fmul_rn(__fmul_rn(t.y, fv), ds);
+        }
+        y[u] = pack8<BF16>(z);
+      } else {
+        y[u] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    *reinterpret_cast<uint4*>(out + static_cast<long long>(s) * D) = y[u];
+  }
 }
 
 template <int D, bool BF16, bool FP4>
@@ -294,10 +323,10 @@ int launch_gather_t(const GatherArgs& a) {
   p.n_pages = a.cache.n_pages;
   p.max_pages = a.cache.max_pages;
   p.status = a.status;
-  constexpr int kRowsCta = kThreads / (D / 16);
+  constexpr int kRowsCta = kThreads / (D / 8) * kGatherPasses;
   const long long bh = static_cast<long long>(a.B) * a.cache.Hkv;
   if (bh > 65535) return -1;
-  const dim3 grid((a.S + kRowsCta - 1) / kRowsCta, static_cast<unsigned>(bh), 2);
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.S) + kRowsCta - 1) / kRowsCta), static_cast<unsigned>(bh), 2);
   cache_gather_kernel<D, BF16, FP4><<<grid, kThreads, 0, a.stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

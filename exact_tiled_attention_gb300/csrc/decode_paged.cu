@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
   __shared__ long long sm_before;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int r = lane >> 2, q4 = lane & 3;
+  let_next_kernel_start();
   const int HG = p.Hkv * p.groups;
   [[maybe_unused]] const uint32_t ring = smem_u32(sm_raw) + warp * C::kRing;
   const LanePtrs src = Tile<D, FMT>::ptrs(p, lane);
@@ -763,49 +764,86 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
   }
 }
 
-// One warp for each (sequence, query head): folds the parts of a segment that
-// was split, and writes the zeros of an empty sequence.
+// One CTA for each (sequence, query head): folds the parts of a segment that was
+// split, in the order of the parts, and writes the zeros of an empty sequence.
+// Launched while the decode kernel runs; it waits for that kernel's end.
 template <int D>
-__global__ void __launch_bounds__(128) decode_paged_merge_kernel(const __grid_constant__ Params p) {
-  const long long row_g = static_cast<long long>(blockIdx.x) * 4 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (row_g >= static_cast<long long>(p.B) * p.Hq) return;
+__global__ void __launch_bounds__(kThreads) decode_paged_merge_kernel(const __grid_constant__ Params p) {
+  constexpr int kLanes = D / 4;               // threads of a part's row, four elements each
+  constexpr int kTeams = kThreads / kLanes;   // parts read at a time
+  __shared__ float weight[kMaxCtas];
+  __shared__ float red[2][kWarps];
+  __shared__ float4 sum[kTeams][kLanes];
+  const long long row_g = blockIdx.x;
   const int b = static_cast<int>(row_g / p.Hq), hq = static_cast<int>(row_g % p.Hq);
-  constexpr int kPer = D / 32;
-  float acc[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const bool empty = seq_len(p, b) == 0;
+  const int kvh = hq / p.g, in_g = hq % p.g;
+  const int hg = kvh * p.groups + in_g / kMaxGroup, row = in_g % kMaxGroup;
+  wait_for_previous_kernel();
+  const int2 part = empty ? make_int2(0, 1) : p.parts[static_cast<long long>(b) * p.Hkv * p.groups + hg];
+  if (part.y == 0) return;  // finished by one CTA
+  // Part 0 is in the first CTA's slot; the others in slot 0 of the next CTAs.
+  auto state = [&](int i) {
+    const long long s = i == 0 ? part.x : (static_cast<long long>(part.x / 2) + i) * 2;
+    return s * p.rows + row;
+  };
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = kNoReference, ls = 0.f;
-  if (seq_len(p, b) > 0) {
-    const int kvh = hq / p.g, in_g = hq % p.g;
-    const int hg = kvh * p.groups + in_g / kMaxGroup, row = in_g % kMaxGroup;
-    const int2 part = p.parts[static_cast<long long>(b) * p.Hkv * p.groups + hg];
-    if (part.y == 0) return;  // finished by one CTA
-    // Part 0 is in the first CTA's slot; the others in slot 0 of the next CTAs.
-    auto state = [&](int i) {
-      const long long s = i == 0 ? part.x : (static_cast<long long>(part.x / 2) + i) * 2;
-      return s * p.rows + row;
-    };
-    for (int i = lane; i < part.y; i += 32) M = fmaxf(M, p.part_ml[state(i) * 2]);
+  if (!empty) {
+    for (int i = threadIdx.x; i < part.y; i += kThreads) M = fmaxf(M, p.part_ml[state(i) * 2]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int i = 0; i < part.y; ++i) {
-      const long long st = state(i);
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + st * 2);
-      const float f = ex2_approx(ml.x - M);
-      if (f == 0.f) continue;
-      ls += f * ml.y;
+    if (lane == 0) red[0][warp] = M;
+    __syncthreads();
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] += f * p.part_o[st * D + lane * kPer + e];
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[0][w]);
+    for (int i = threadIdx.x; i < part.y; i += kThreads) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + state(i) * 2);
+      const float f = ex2_approx(ml.x - M);
+      weight[i] = f;
+      if (f != 0.f) ls += f * ml.y;
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+    if (lane == 0) red[1][warp] = ls;
+    __syncthreads();
+    ls = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) ls += red[1][w];
+    const int team = threadIdx.x / kLanes, piece = threadIdx.x % kLanes;
+#pragma unroll 4
+    for (int i = team; i < part.y; i += kTeams) {
+      const float f = weight[i];
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + state(i) * D + piece * 4);
+      if (f != 0.f) {
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+    }
+    sum[team][piece] = acc;
+    __syncthreads();
+    if (team != 0) return;
+#pragma unroll
+    for (int i = 1; i < kTeams; ++i) {
+      const float4 v = sum[i][piece];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+  } else if (threadIdx.x >= kLanes) {
+    return;
   }
   const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
-#pragma unroll
-  for (int e = 0; e < kPer; e += 2) {
-    const float x = acc[e] * inv, y = acc[e + 1] * inv;
-    *reinterpret_cast<uint32_t*>(p.o + row_g * D + lane * kPer + e) = p.out_bf16 ? pack2<true>(x, y) : pack2<false>(x, y);
-  }
-  if (lane == 0 && p.lse != nullptr) p.lse[row_g] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+  const float4 y = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(p.o + row_g * D + threadIdx.x * 4) =
+      p.out_bf16 ? make_uint2(pack2<true>(y.x, y.y), pack2<true>(y.z, y.w))
+                 : make_uint2(pack2<false>(y.x, y.y), pack2<false>(y.z, y.w));
+  if (threadIdx.x == 0 && p.lse != nullptr)
+    p.lse[row_g] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
 }
 
 int group_rows(int Hq, int Hkv) {
@@ -833,9 +871,7 @@ int launch_t(const Params& p, const PagedDecodeArgs& a) {
   if (ctas > kMaxCtas) ctas = kMaxCtas;
   kern<<<ctas, kThreads, kBytes, a.stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  const long long rows = static_cast<long long>(a.B) * a.Hq;
-  decode_paged_merge_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, a.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_after(decode_paged_merge_kernel<D>, dim3(static_cast<unsigned>(a.B) * a.Hq), kThreads, a.stream, p);
 }
 
 template <int D, int FMT>

@@ -264,6 +264,34 @@ inline bool set_smem_limit_once(Kernel kernel, int bytes, std::atomic<unsigned l
   return true;
 }
 
+// Launches `kernel` so that it may start while the stream's previous kernel still
+// runs (once every CTA of that one has called let_next_kernel_start or ended);
+// it must call wait_for_previous_kernel before it touches what that one writes.
+// 0, or -1 where the launch failed.
+template <typename Params>
+inline int launch_after(void (*kernel)(Params), dim3 grid, int threads, cudaStream_t stream, const Params& params) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, params) == cudaSuccess) return 0;
+  cudaGetLastError();
+  return -1;
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Returns once the previous kernel has ended and its writes are visible.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 // 3-D tensor map over a contiguous [outer, rows, d] 16-bit tensor with a
 // (64 x box_rows x 1) box and 128-byte swizzle; rows past `rows` read as 0.
 bool make_tmap_3d(CUtensorMap* map, const void* base, bool bf16, int d, int rows, long long outer,

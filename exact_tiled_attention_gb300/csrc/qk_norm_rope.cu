@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 // Grid: (CTAs that walk over tokens, head chunks of q then k).  With NORM each
 // CTA leaves the sum of its rows' weight gradients in `partial`.
 template <int D, bool BF16, int MODE, bool NORM>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int kLanes = RowCfg<D>::kLanes;
   constexpr int kRowsCta = kThreads / kLanes;
   const int lane_in_row = threadIdx.x % kLanes;
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
   const int h0 = chunk * p.per_chunk;
   const int h1 = min(h0 + p.per_chunk, p.heads[which]);
   const int e0 = 8 * lane_in_row;
+  let_next_kernel_start();
   int pc[2] = {0, 0};
   float w[2][8], dw[2][8];
 #pragma unroll
@@ -150,23 +151,34 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
     const uint16_t* xrow = p.x[which] + b * xs.b + s * xs.s + h0 * xs.h;
     uint16_t* dxrow = p.dx[which] + b * dxs.b + s * dxs.s + h0 * dxs.h;
     const uint16_t* dyrow = p.dy[which] + ((static_cast<long long>(b) * p.heads[which] + h0) * p.S + s) * D;
-    for (int h = h0; h < h1; ++h, xrow += xs.h, dxrow += dxs.h, dyrow += static_cast<long long>(p.S) * D) {
-      float g[2][8], part[2][8];
+    // The next head's rows are requested before this one is worked on.
+    uint4 dy_raw[2], x_raw[2];
+    auto request = [&] {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        unpack8<BF16>(*reinterpret_cast<const uint4*>(dyrow + c * (D / 2) + e0), g[c]);
-        if constexpr (MODE == kRopePart) unpack8<BF16>(*reinterpret_cast<const uint4*>(dyrow + pc[c]), part[c]);
+        dy_raw[c] = *reinterpret_cast<const uint4*>(dyrow + c * (D / 2) + e0);
+        if constexpr (NORM) x_raw[c] = *reinterpret_cast<const uint4*>(xrow + c * (D / 2) + e0);
       }
+    };
+    request();
+    for (int h = h0; h < h1; ++h, dxrow += dxs.h) {
+      float g[2][8], part[2][8], n[2][8];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        unpack8<BF16>(dy_raw[c], g[c]);
+        if constexpr (MODE == kRopePart) unpack8<BF16>(*reinterpret_cast<const uint4*>(dyrow + pc[c]), part[c]);
+        if constexpr (NORM) unpack8<BF16>(x_raw[c], n[c]);
+      }
+      xrow += xs.h;
+      dyrow += static_cast<long long>(p.S) * D;
+      if (h + 1 < h1) request();
       rotate<MODE, true>(g, part, rope);
       if constexpr (NORM) {
-        float n[2][8];
         float sq = 0.f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + c * (D / 2) + e0), n[c]);
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int i = 0; i < 8; ++i) sq = fmaf(n[c][i], n[c][i], sq);
-        }
         const float r = rsqrtf(row_sum<D>(sq) * (1.f / D) + p.eps);
         float dot = 0.f;
 #pragma unroll
@@ -211,21 +223,33 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
   }
 }
 
-// dw[which][i] = sum of the CTAs' partials, in a fixed order.  Grid (D / 32, 2).
-__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ partial, int rows_q, int rows_k,
-                                                       int d, float* dwq, float* dwk) {
-  __shared__ float sum[32][33];
-  const int which = blockIdx.y, rows = which ? rows_k : rows_q;
-  const int col = threadIdx.x % 32, r0 = threadIdx.x / 32;
-  const float* base = partial + static_cast<long long>(which) * kMaxBwdCtas * d + blockIdx.x * 32 + col;
+struct DwParams {
+  const float* partial;
+  int rows[2];
+  int d;
+  float* dw[2];
+};
+
+// dw[which][i] = sum of the CTAs' partials, in a fixed order.  Grid (d / 16, 2):
+// a CTA sums 16 columns, 64 rows at a time.  Launched while the backward kernel
+// runs; it waits for that kernel's end.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const __grid_constant__ DwParams p) {
+  __shared__ float sum[32][17];
+  const int which = blockIdx.y, rows = p.rows[which];
+  const int col = threadIdx.x % 16, r0 = threadIdx.x / 16;
+  const float* base = p.partial + static_cast<long long>(which) * kMaxBwdCtas * p.d + blockIdx.x * 16 + col;
+  wait_for_previous_kernel();
   float v = 0.f;
-  for (int r = r0; r < rows; r += 32) v += base[static_cast<long long>(r) * d];
-  sum[r0][col] = v;
+#pragma unroll 8
+  for (int r = r0; r < rows; r += 64) v += base[static_cast<long long>(r) * p.d];
+  v += __shfl_xor_sync(0xffffffffu, v, 16);
+  if (threadIdx.x % 32 < 16) sum[threadIdx.x / 32][col] = v;
   __syncthreads();
-  v = sum[col][r0];  // transposed: warp r0 holds column r0
+  if (threadIdx.x >= 512) return;
+  v = sum[threadIdx.x % 32][threadIdx.x / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (col == 0) (which ? dwk : dwq)[blockIdx.x * 32 + r0] = v;
+  if (threadIdx.x % 32 == 0) p.dw[which][blockIdx.x * 16 + threadIdx.x / 32] = v;
 }
 
 NormRopeParams params(const NormRopeArgs& a) {
@@ -315,9 +339,14 @@ int launch_bwd(const NormRopeArgs& a) {
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
   });
   if (rc != 0 || a.w[0] == nullptr) return rc;
-  norm_dw_kernel<<<dim3(D / 32, 2), 1024, 0, a.stream>>>(p.partial, static_cast<int>(x) * p.chunks[0],
-                                                         static_cast<int>(x) * p.chunks[1], D, a.dw[0], a.dw[1]);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  DwParams dp{};
+  dp.partial = p.partial;
+  dp.d = D;
+  for (int i = 0; i < 2; ++i) {
+    dp.rows[i] = static_cast<int>(x) * p.chunks[i];
+    dp.dw[i] = a.dw[i];
+  }
+  return launch_after(norm_dw_kernel, dim3(D / 16, 2), 1024, a.stream, dp);
 }
 
 }  // namespace
