@@ -104,7 +104,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.attn_cache_gather.restype = ci
         lib.attn_cache_gather_fp4.argtypes = [vp] * 10 + [ci] * 8 + [vp]
         lib.attn_cache_gather_fp4.restype = ci
-        lib.attn_decode_paged_workspace_bytes.argtypes = [ci] * 4
+        lib.attn_decode_paged_workspace_bytes.argtypes = [ci] * 5
         lib.attn_decode_paged_workspace_bytes.restype = sz
         lib.attn_decode_paged.argtypes = [vp] * 7 + [ci] * 7 + [cf, vp, sz, ci, vp]
         lib.attn_decode_paged.restype = ci

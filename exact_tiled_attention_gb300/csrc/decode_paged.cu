@@ -58,6 +58,7 @@ struct Params {
   int page_shift, n_pages, max_pages;
   float scale_log2;
   int out_bf16;
+  int most_ctas;   // states that the workspace has room for
   int* status;
 };
 
@@ -851,6 +852,14 @@ int group_rows(int Hq, int Hkv) {
   return g < kMaxGroup ? g : kMaxGroup;
 }
 
+int unit_groups(int Hq, int Hkv) { return (Hq / Hkv + kMaxGroup - 1) / kMaxGroup; }
+
+// CTAs that can have work: one for each unit at most (the smallest unit is 64 keys).
+int max_ctas(int B, size_t heads, int max_len) {
+  const size_t units = B * heads * ((static_cast<size_t>(max_len) + 63) / 64);
+  return units < kMaxCtas ? static_cast<int>(units) : kMaxCtas;
+}
+
 template <int D, int FMT, int NT>
 int launch_t(const Params& p, const PagedDecodeArgs& a) {
   auto kern = decode_paged_kernel<D, FMT, NT>;
@@ -868,7 +877,7 @@ int launch_t(const Params& p, const PagedDecodeArgs& a) {
     fit.store(per_sm, std::memory_order_relaxed);
   }
   int ctas = per_sm * a.num_sms;
-  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  if (ctas > p.most_ctas) ctas = p.most_ctas;
   kern<<<ctas, kThreads, kBytes, a.stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return -1;
   return launch_after(decode_paged_merge_kernel<D>, dim3(static_cast<unsigned>(a.B) * a.Hq), kThreads, a.stream, p);
@@ -881,10 +890,10 @@ int launch_d(const Params& p, const PagedDecodeArgs& a) {
 
 }  // namespace
 
-size_t paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d) {
-  const size_t rows = group_rows(Hq, Hkv), groups = (Hq / Hkv + kMaxGroup - 1) / kMaxGroup;
-  return static_cast<size_t>(kMaxCtas) * 2 * rows * (static_cast<size_t>(d) + 2) * sizeof(float) +
-         static_cast<size_t>(B) * Hkv * groups * sizeof(int2);
+size_t paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d, int max_len) {
+  const size_t rows = group_rows(Hq, Hkv), heads = static_cast<size_t>(Hkv) * unit_groups(Hq, Hkv);
+  return static_cast<size_t>(max_ctas(B, heads, max_len)) * 2 * rows * (static_cast<size_t>(d) + 2) * sizeof(float) +
+         B * heads * sizeof(int2);
 }
 
 int launch_decode_paged(const PagedDecodeArgs& a) {
@@ -904,7 +913,8 @@ int launch_decode_paged(const PagedDecodeArgs& a) {
   p.Hq = a.Hq;
   p.Hkv = c.Hkv;
   p.g = a.Hq / c.Hkv;
-  p.groups = (p.g + kMaxGroup - 1) / kMaxGroup;
+  p.groups = unit_groups(a.Hq, c.Hkv);
+  p.most_ctas = max_ctas(a.B, static_cast<size_t>(c.Hkv) * p.groups, c.max_pages << c.page_shift);
   p.rows = group_rows(a.Hq, c.Hkv);
   p.page_shift = c.page_shift;
   p.n_pages = c.n_pages;
@@ -913,7 +923,7 @@ int launch_decode_paged(const PagedDecodeArgs& a) {
   p.out_bf16 = a.bf16 ? 1 : 0;
   p.status = a.status;
   float* ws = static_cast<float*>(a.workspace);
-  const size_t states = static_cast<size_t>(kMaxCtas) * 2 * p.rows;
+  const size_t states = static_cast<size_t>(p.most_ctas) * 2 * p.rows;
   p.part_o = ws;
   p.part_ml = ws + states * c.d;
   p.parts = reinterpret_cast<int2*>(ws + states * (c.d + 2));

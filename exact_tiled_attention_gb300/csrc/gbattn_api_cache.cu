@@ -172,7 +172,7 @@ int decode(const void* q, const void* k_cache, const void* k_factors, const void
   if (dtype != GBATTN_F16 && dtype != GBATTN_BF16) return GBATTN_EDTYPE;
   if (!q || !o || !workspace || misaligned16(q) || misaligned16(o) || misaligned16(workspace) || misaligned4(lse))
     return GBATTN_EPOINTER;
-  if (workspace_bytes < paged_decode_workspace_bytes(B, Hq, Hkv, d)) return GBATTN_EWORKSPACE;
+  if (workspace_bytes < paged_decode_workspace_bytes(B, Hq, Hkv, d, max_pages * page_size)) return GBATTN_EWORKSPACE;
   rc = current_device(&a.status, &a.num_sms);
   if (rc != GBATTN_OK) return rc;
   a.q = q;
@@ -280,9 +280,9 @@ int attn_cache_gather_fp4(const void* k_codes, const void* k_factors, const void
                 B, Hkv, S, d, page_size, n_pages, max_pages, dtype, stream);
 }
 
-size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1) return 0;
-  return paged_decode_workspace_bytes(B, Hq, Hkv, d);
+size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_len) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1 || max_len < 1) return 0;
+  return paged_decode_workspace_bytes(B, Hq, Hkv, d, max_len);
 }
 
 int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, const int* page_table,

@@ -186,7 +186,7 @@ struct PagedDecodeArgs {
 int current_device(int** status, int* sm_count);
 
 // Bytes of workspace of the paged decode and of the norm's backward.
-size_t paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d);
+size_t paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d, int max_len);
 size_t norm_rope_bwd_workspace_bytes(int d);
 
 // Each returns a cudaError_t / CUresult folded into 0 (ok) or -1 (launch or

@@ -16,8 +16,17 @@ import torch
 from .binding import GBATTN_BF16, GBATTN_F16, GBATTN_OK, GbattnError, load_library
 
 _DTYPES = {torch.float16: GBATTN_F16, torch.bfloat16: GBATTN_BF16}
-_FACTOR_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+_F32, _I32, _U8, _E4M3 = torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
 _Strides = ctypes.c_longlong * 3
+_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        _lib = load_library()
+    return _lib
 
 
 def rope_table(rows: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -31,97 +40,121 @@ def rope_table(rows: int, rot_dim: int, base: float = 10000.0, device="cuda") ->
     return torch.cat([a.cos(), a.sin()], dim=1).float()
 
 
-def _on(fn, name, args, device, stream):
-    """fn(*args, stream) with `device` current; raises the library's error."""
+# A token's worth of work is a few microseconds on the device, so the checks are
+# written for few interpreter steps: one compound condition for each tensor, and
+# the reason worked out (_refuse) only where it fails.
+
+
+def _call(name, args, device, stream):
+    """The library's function `name` with `device` current; raises its error."""
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, ptr)
+        stream = _raw_stream(index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    fn = getattr(_library(), name)
+    if index == _get_device():
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, ptr)
+            rc = fn(*args, stream)
     if rc != GBATTN_OK:
         raise GbattnError(rc, name)
 
 
-def _rows(t, name, shape, dtype, device):
-    """Checks a [B, heads, S, d] tensor whose rows are contiguous; its strides
-    for the C ABI (None where it is contiguous)."""
+def _refuse(t, name, shape, dtype, device, rows=False):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 4 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must have shape {'[B, heads, S, d]' if shape is None else tuple(shape)}, "
-                         f"got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device} (there is no CPU path), got {t.device}")
-    if t.is_contiguous():
-        return None
-    sb, sh, ss, sd = t.stride()
-    if sd != 1 or (sb | sh | ss) % 8 or t.data_ptr() % 16:
-        raise ValueError(f"{name} needs contiguous rows of d elements that start on 16-byte boundaries, "
-                         f"got strides {t.stride()}")
-    return _Strides(sb, sh, ss)
-
-
-def _plain(t, name, shape, dtypes, device):
-    """Checks a contiguous tensor; its address, or None for None."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on {device}")
-    return t.data_ptr()
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device} (there is no CPU path)")
+    if rows:
+        raise ValueError(f"{name} needs contiguous rows of d elements that start on 16-byte boundaries, "
+                         f"got strides {t.stride()}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-_F32, _I32 = (torch.float32,), (torch.int32,)
+def _ptr(t, name, shape, dtype, device):
+    """The address of a contiguous tensor."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtype, device)
+
+
+def _opt(t, name, shape, dtype, device):
+    return None if t is None else _ptr(t, name, shape, dtype, device)
+
+
+def _rows(t, name, shape, dtype, device):
+    """Address and strides (None: contiguous) of a [B, heads, S, d] tensor whose
+    rows are contiguous."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device:
+            if t.is_contiguous():
+                return t.data_ptr(), None
+            sb, sh, ss, sd = t.stride()
+            if sd == 1 and not (sb | sh | ss) & 7:
+                return t.data_ptr(), _Strides(sb, sh, ss)
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtype, device, rows=True)
 
 
 def _first(t, name):
+    """Device, type, the library's code for it and shape of the tensor that the
+    others have to agree with."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.dtype not in _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype} of {name}; expected float16 or bfloat16")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must have 4 dims, got shape {tuple(t.shape)}")
-    return t.device, t.dtype
+    shape = t.shape
+    if len(shape) != 4:
+        raise ValueError(f"{name} must have 4 dims, got shape {tuple(shape)}")
+    return t.device, t.dtype, code, shape
+
+
+def _dims(t, name, n):
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{name} must be a tensor of {n} dims")
+    return t.shape
 
 
 def _rope(rope, device):
+    """Address, rows and width of the rotation's table."""
     if rope is None:
         return None, 0, 0
-    if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
-        raise ValueError("rope must be a tensor [rows, rot_dim] (see rope_table)")
-    return _plain(rope, "rope", rope.shape, _F32, device), rope.shape[0], rope.shape[1]
+    shape = _dims(rope, "rope", 2)
+    return _ptr(rope, "rope", shape, _F32, device), shape[0], shape[1]
 
 
 def _norm_rope_args(q, k, q_weight, k_weight, rope, positions):
-    device, dtype = _first(q, "q")
-    B, H, S, d = q.shape
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise ValueError("k must be a tensor [B, Hkv, S, d]")
-    Hkv = k.shape[1]
-    qs = _rows(q, "q", q.shape, dtype, device)
-    ks = _rows(k, "k", (B, Hkv, S, d), dtype, device)
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight go together: both, or neither (rotation alone)")
-    if q_weight is None and rope is None:
-        raise ValueError("nothing to do: neither norm weights nor a rotation table")
+    device, dtype, code, shape = _first(q, "q")
+    B, H, S, d = shape
+    Hkv = _dims(k, "k", 4)[1]
+    q_ptr, qs = _rows(q, "q", shape, dtype, device)
+    k_ptr, ks = _rows(k, "k", (B, Hkv, S, d), dtype, device)
     table, rows, rot = _rope(rope, device)
-    if rope is not None and positions is None and rows < S:
+    if q_weight is None or k_weight is None:
+        if q_weight is not k_weight:
+            raise ValueError("q_weight and k_weight go together: both, or neither (rotation alone)")
+        if rope is None:
+            raise ValueError("nothing to do: neither norm weights nor a rotation table")
+        weights = None, None
+    else:
+        weights = _ptr(q_weight, "q_weight", (d,), _F32, device), _ptr(k_weight, "k_weight", (d,), _F32, device)
+    if positions is None and table is not None and rows < S:
         raise ValueError(f"rope has {rows} rows for {S} tokens")
-    ptrs = (_plain(q_weight, "q_weight", (d,), _F32, device), _plain(k_weight, "k_weight", (d,), _F32, device), table,
-            _plain(positions, "positions", (B, S), _I32, device))
-    return device, dtype, (B, H, Hkv, S, d), qs, ks, ptrs, rows, rot
+    ptrs = (q_ptr, k_ptr, *weights, table, _opt(positions, "positions", (B, S), _I32, device))
+    return device, dtype, code, (B, H, Hkv, S, d), qs, ks, ptrs, rows, rot
 
 
 def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=None, eps: float = 1e-6,
@@ -134,17 +167,20 @@ def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=N
     (rotation alone); rope fp32 [rows, rot_dim] from rope_table, or None (norm
     alone); positions int32 [B,S], or None (0 .. S-1).  Returns contiguous
     (q_out, k_out), which may be given as q and k themselves."""
-    device, dtype, (B, H, Hkv, S, d), qs, ks, ptrs, rows, rot = _norm_rope_args(q, k, q_weight, k_weight, rope,
-                                                                                positions)
+    device, dtype, code, (B, H, Hkv, S, d), qs, ks, ptrs, rows, rot = _norm_rope_args(q, k, q_weight, k_weight, rope,
+                                                                                      positions)
     if q_out is None:
         q_out = torch.empty((B, H, S, d), dtype=dtype, device=device)
+        qo = q_out.data_ptr()
+    else:
+        qo = _ptr(q_out, "q_out", (B, H, S, d), dtype, device)
     if k_out is None:
         k_out = torch.empty((B, Hkv, S, d), dtype=dtype, device=device)
-    outs = (_plain(q_out, "q_out", (B, H, S, d), (dtype,), device),
-            _plain(k_out, "k_out", (B, Hkv, S, d), (dtype,), device))
-    _on(load_library().attn_qk_norm_rope, "attn_qk_norm_rope",
-        (q.data_ptr(), k.data_ptr(), *ptrs, *outs, B, H, Hkv, S, d, qs, ks, float(eps), rows, rot,
-         int(bool(interleaved)), _DTYPES[dtype]), device, stream)
+        ko = k_out.data_ptr()
+    else:
+        ko = _ptr(k_out, "k_out", (B, Hkv, S, d), dtype, device)
+    _call("attn_qk_norm_rope", (*ptrs, qo, ko, B, H, Hkv, S, d, qs, ks, eps, rows, rot, 1 if interleaved else 0, code),
+          device, stream)
     return q_out, k_out
 
 
@@ -162,97 +198,96 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, ro
     have, for instance as views of the projection output's gradient.  Returns
     (dq, dk, dq_weight, dk_weight), the last two fp32 [d], or None without
     weights."""
-    device, dtype, (B, H, Hkv, S, d), qs, ks, ptrs, rows, rot = _norm_rope_args(q, k, q_weight, k_weight, rope,
-                                                                                positions)
-    grads = (_plain(dq_out, "dq_out", (B, H, S, d), (dtype,), device),
-             _plain(dk_out, "dk_out", (B, Hkv, S, d), (dtype,), device))
-    if None in grads:
-        raise TypeError("dq_out and dk_out must be tensors")
-    lib = load_library()
+    device, dtype, code, (B, H, Hkv, S, d), qs, ks, ptrs, rows, rot = _norm_rope_args(q, k, q_weight, k_weight, rope,
+                                                                                      positions)
+    q_shape, k_shape = (B, H, S, d), (B, Hkv, S, d)
+    dqo = _ptr(dq_out, "dq_out", q_shape, dtype, device)
+    dko = _ptr(dk_out, "dk_out", k_shape, dtype, device)
     if dq is None:
-        dq = torch.empty((B, H, S, d), dtype=dtype, device=device)
+        dq = torch.empty(q_shape, dtype=dtype, device=device)
+        dq_ptr, dqs = dq.data_ptr(), None
+    else:
+        dq_ptr, dqs = _rows(dq, "dq", q_shape, dtype, device)
     if dk is None:
-        dk = torch.empty((B, Hkv, S, d), dtype=dtype, device=device)
-    dqs = _rows(dq, "dq", (B, H, S, d), dtype, device)
-    dks = _rows(dk, "dk", (B, Hkv, S, d), dtype, device)
-    ws_bytes = 0
-    if q_weight is not None:
+        dk = torch.empty(k_shape, dtype=dtype, device=device)
+        dk_ptr, dks = dk.data_ptr(), None
+    else:
+        dk_ptr, dks = _rows(dk, "dk", k_shape, dtype, device)
+    if q_weight is None:
+        dq_weight = dk_weight = None
+        wgrads, ws, ws_bytes = (None, None), None, 0
+    else:
         if dq_weight is None:
-            dq_weight = torch.empty(d, dtype=torch.float32, device=device)
+            dq_weight = torch.empty(d, dtype=_F32, device=device)
         if dk_weight is None:
-            dk_weight = torch.empty(d, dtype=torch.float32, device=device)
+            dk_weight = torch.empty(d, dtype=_F32, device=device)
+        wgrads = (_ptr(dq_weight, "dq_weight", (d,), _F32, device), _ptr(dk_weight, "dk_weight", (d,), _F32, device))
         if workspace is None:
-            workspace = torch.empty(max(lib.attn_qk_norm_rope_bwd_workspace_bytes(d), 16), dtype=torch.uint8,
+            workspace = torch.empty(max(_library().attn_qk_norm_rope_bwd_workspace_bytes(d), 16), dtype=_U8,
                                     device=device)
-        ws_bytes = _workspace(workspace, device)
-    _on(lib.attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd",
-        (*grads, q.data_ptr(), k.data_ptr(), *ptrs, dq.data_ptr(), dk.data_ptr(),
-         _plain(dq_weight, "dq_weight", (d,), _F32, device), _plain(dk_weight, "dk_weight", (d,), _F32, device),
-         B, H, Hkv, S, d, qs, ks, dqs, dks, float(eps), rows, rot, int(bool(interleaved)),
-         workspace.data_ptr() if ws_bytes else None, ws_bytes, _DTYPES[dtype]), device, stream)
-    return (dq, dk, dq_weight, dk_weight) if q_weight is not None else (dq, dk, None, None)
+        ws, ws_bytes = _workspace(workspace, device)
+    _call("attn_qk_norm_rope_bwd",
+          (dqo, dko, *ptrs, dq_ptr, dk_ptr, *wgrads, B, H, Hkv, S, d, qs, ks, dqs, dks, eps, rows, rot,
+           1 if interleaved else 0, ws, ws_bytes, code), device, stream)
+    return dq, dk, dq_weight, dk_weight
 
 
 def _workspace(t, device):
+    """Address and bytes of a workspace."""
     if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return t.numel() * t.element_size()
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _cache(k_cache, v_cache, page_table, seqlens, B, Hkv, d, dtype, device):
-    """Checks a 16-bit cache and its tables: the pointers and the sizes."""
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or k_cache.shape[1] != Hkv or k_cache.shape[3] != d:
-        raise ValueError(f"k_cache must be a tensor [n_pages, {Hkv}, page_size, {d}]")
-    n_pages, _, page, _ = k_cache.shape
-    ptrs = (_plain(k_cache, "k_cache", k_cache.shape, (dtype,), device),
-            _plain(v_cache, "v_cache", k_cache.shape, (dtype,), device))
-    return _tables(ptrs, page_table, seqlens, B, device), (page, n_pages, page_table.shape[1])
+    """Addresses of a 16-bit cache and its tables; page size, pages, pages a sequence."""
+    shape = _dims(k_cache, "k_cache", 4)
+    n_pages, heads, page, width = shape
+    if heads != Hkv or width != d:
+        raise ValueError(f"k_cache must be a tensor [n_pages, {Hkv}, page_size, {d}], got {tuple(shape)}")
+    max_pages = _dims(page_table, "page_table", 2)[1]
+    return ((_ptr(k_cache, "k_cache", shape, dtype, device), _ptr(v_cache, "v_cache", shape, dtype, device),
+             _ptr(page_table, "page_table", (B, max_pages), _I32, device), _ptr(seqlens, "seqlens", (B,), _I32, device)),
+            (page, n_pages, max_pages))
 
 
 def _cache_fp4(k_codes, k_factors, v_codes, v_factors, k_descale, v_descale, page_table, seqlens, B, Hkv, d, device):
-    if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4 or k_codes.shape[1] != Hkv or \
-            k_codes.shape[3] * 2 != d:
-        raise ValueError(f"k_codes must be a tensor [n_pages, {Hkv}, page_size, {d // 2}]")
-    n_pages, _, page, _ = k_codes.shape
+    """The same of a 4-bit cache."""
+    shape = _dims(k_codes, "k_codes", 4)
+    n_pages, heads, page, width = shape
+    if heads != Hkv or 2 * width != d:
+        raise ValueError(f"k_codes must be a tensor [n_pages, {Hkv}, page_size, {d // 2}], got {tuple(shape)}")
+    max_pages = _dims(page_table, "page_table", 2)[1]
     factors = (n_pages, Hkv, page, d // 16)
-    ptrs = (_plain(k_codes, "k_codes", k_codes.shape, (torch.uint8,), device),
-            _plain(k_factors, "k_factors", factors, _FACTOR_DTYPES, device),
-            _plain(v_codes, "v_codes", k_codes.shape, (torch.uint8,), device),
-            _plain(v_factors, "v_factors", factors, _FACTOR_DTYPES, device))
-    if None in ptrs:
-        raise TypeError("codes and factors must be tensors")
-    ptrs += (_plain(k_descale, "k_descale", (Hkv,), _F32, device), _plain(v_descale, "v_descale", (Hkv,), _F32, device))
-    return _tables(ptrs, page_table, seqlens, B, device), (page, n_pages, page_table.shape[1])
+    as_bytes = _U8 if getattr(k_factors, "dtype", None) is _U8 else _E4M3
+    return ((_ptr(k_codes, "k_codes", shape, _U8, device), _ptr(k_factors, "k_factors", factors, as_bytes, device),
+             _ptr(v_codes, "v_codes", shape, _U8, device), _ptr(v_factors, "v_factors", factors, as_bytes, device),
+             _opt(k_descale, "k_descale", (Hkv,), _F32, device), _opt(v_descale, "v_descale", (Hkv,), _F32, device),
+             _ptr(page_table, "page_table", (B, max_pages), _I32, device), _ptr(seqlens, "seqlens", (B,), _I32, device)),
+            (page, n_pages, max_pages))
 
 
-def _tables(ptrs, page_table, seqlens, B, device):
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise ValueError("page_table must be a tensor [B, max_pages]")
-    return ptrs + (_plain(page_table, "page_table", (B, page_table.shape[1]), _I32, device),
-                   _plain(seqlens, "seqlens", (B,), _I32, device))
-
-
-def _append(name, k, v, cache, new_lens, rope, interleaved, q, q_out, stream):
-    device, dtype = _first(k, "k")
-    B, Hkv, S, d = k.shape
-    ks = _rows(k, "k", k.shape, dtype, device)
-    vs = _rows(v, "v", k.shape, dtype, device)
-    H, qs, q_ptr, out_ptr = Hkv, None, None, None
-    if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 4:
-            raise ValueError("q must be a tensor [B, H, S, d]")
-        H = q.shape[1]
-        qs = _rows(q, "q", (B, H, S, d), dtype, device)
+def _append(name, first, k_ptr, ks, v, cache, new_lens, rope, interleaved, q, q_out, stream):
+    device, dtype, code, shape = first
+    B, Hkv, S, d = shape
+    v_ptr, vs = _rows(v, "v", shape, dtype, device)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        H, q_ptr, qs, out_ptr = Hkv, None, None, None
+    else:
+        H = _dims(q, "q", 4)[1]
+        q_shape = (B, H, S, d)
+        q_ptr, qs = _rows(q, "q", q_shape, dtype, device)
         if q_out is None:
-            q_out = torch.empty((B, H, S, d), dtype=dtype, device=device)
-        q_ptr, out_ptr = q.data_ptr(), _plain(q_out, "q_out", (B, H, S, d), (dtype,), device)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
+            q_out = torch.empty(q_shape, dtype=dtype, device=device)
+            out_ptr = q_out.data_ptr()
+        else:
+            out_ptr = _ptr(q_out, "q_out", q_shape, dtype, device)
     table, rows, rot = _rope(rope, device)
-    ptrs, sizes = cache(B, Hkv, d, dtype, device)
-    _on(getattr(load_library(), name), name,
-        (k.data_ptr(), v.data_ptr(), *ptrs, _plain(new_lens, "new_lens", (B,), _I32, device), table, q_ptr, out_ptr,
-         B, H, Hkv, S, d, *sizes, qs, ks, vs, rows, rot, int(bool(interleaved)), _DTYPES[dtype]), device, stream)
+    ptrs, sizes = cache
+    _call(name, (k_ptr, v_ptr, *ptrs, _opt(new_lens, "new_lens", (B,), _I32, device), table, q_ptr, out_ptr,
+                 B, H, Hkv, S, d, *sizes, qs, ks, vs, rows, rot, 1 if interleaved else 0, code), device, stream)
     return q_out
 
 
@@ -265,9 +300,10 @@ def attn_cache_append(k, v, k_cache, v_cache, page_table, seqlens, new_lens=None
     k_cache, v_cache [n_pages,Hkv,page_size,d]; page_table int32 [B,max_pages];
     seqlens int32 [B], the new tokens included; new_lens int32 [B] (None: S);
     rope from rope_table, or None.  Returns the rotated queries (None without q)."""
-    return _append("attn_cache_append", k, v,
-                   lambda B, Hkv, d, dtype, dev: _cache(k_cache, v_cache, page_table, seqlens, B, Hkv, d, dtype, dev),
-                   new_lens, rope, interleaved, q, q_out, stream)
+    first = device, dtype, _, (B, Hkv, _, d) = _first(k, "k")
+    k_ptr, ks = _rows(k, "k", first[3], dtype, device)
+    cache = _cache(k_cache, v_cache, page_table, seqlens, B, Hkv, d, dtype, device)
+    return _append("attn_cache_append", first, k_ptr, ks, v, cache, new_lens, rope, interleaved, q, q_out, stream)
 
 
 def attn_cache_append_fp4(k, v, k_codes, k_factors, v_codes, v_factors, page_table, seqlens, new_lens=None,
@@ -275,78 +311,83 @@ def attn_cache_append_fp4(k, v, k_codes, k_factors, v_codes, v_factors, page_tab
                           stream=None):
     """attn_cache_append into a 4-bit paged cache (C ABI `attn_cache_append_fp4`):
     k_codes, v_codes uint8 [n_pages,Hkv,page_size,d/2]; k_factors, v_factors
-    float8_e4m3fn (or uint8) [n_pages,Hkv,page_size,d/16]; k_descale, v_descale
-    fp32 [Hkv] or None."""
-    return _append("attn_cache_append_fp4", k, v,
-                   lambda B, Hkv, d, dtype, dev: _cache_fp4(k_codes, k_factors, v_codes, v_factors, k_descale,
-                                                            v_descale, page_table, seqlens, B, Hkv, d, dev),
-                   new_lens, rope, interleaved, q, q_out, stream)
+    float8_e4m3fn (or both uint8) [n_pages,Hkv,page_size,d/16]; k_descale,
+    v_descale fp32 [Hkv] or None."""
+    first = device, dtype, _, (B, Hkv, _, d) = _first(k, "k")
+    k_ptr, ks = _rows(k, "k", first[3], dtype, device)
+    cache = _cache_fp4(k_codes, k_factors, v_codes, v_factors, k_descale, v_descale, page_table, seqlens, B, Hkv, d,
+                       device)
+    return _append("attn_cache_append_fp4", first, k_ptr, ks, v, cache, new_lens, rope, interleaved, q, q_out, stream)
 
 
-def _gather(name, ptrs, sizes, B, Hkv, S, d, dtype, device, k_out, v_out, stream):
+def _gather(name, cache, B, Hkv, S, d, dtype, device, k_out, v_out, stream):
+    shape = (B, Hkv, S, d)
     if k_out is None:
-        k_out = torch.empty((B, Hkv, S, d), dtype=dtype, device=device)
+        k_out = torch.empty(shape, dtype=dtype, device=device)
     if v_out is None:
-        v_out = torch.empty((B, Hkv, S, d), dtype=dtype, device=device)
-    outs = (_plain(k_out, "k_out", (B, Hkv, S, d), (dtype,), device),
-            _plain(v_out, "v_out", (B, Hkv, S, d), (dtype,), device))
-    _on(getattr(load_library(), name), name, (*ptrs, *outs, B, Hkv, S, d, *sizes, _DTYPES[dtype]), device, stream)
+        v_out = torch.empty(shape, dtype=dtype, device=device)
+    ptrs, sizes = cache
+    _call(name, (*ptrs, _ptr(k_out, "k_out", shape, dtype, device), _ptr(v_out, "v_out", shape, dtype, device), B, Hkv,
+                 S, d, *sizes, _DTYPES[dtype]), device, stream)
     return k_out, v_out
 
 
 def attn_cache_gather(k_cache, v_cache, page_table, seqlens, S: int, k_out=None, v_out=None, stream=None):
     """The first S tokens of every sequence of a 16-bit paged cache as contiguous
     (k, v) [B,Hkv,S,d], zeros behind a sequence (C ABI `attn_cache_gather`)."""
-    device, dtype = _first(k_cache, "k_cache")
-    B, Hkv, d = _batch(seqlens), k_cache.shape[1], k_cache.shape[3]
-    ptrs, sizes = _cache(k_cache, v_cache, page_table, seqlens, B, Hkv, d, dtype, device)
-    return _gather("attn_cache_gather", ptrs, sizes, B, Hkv, int(S), d, dtype, device, k_out, v_out, stream)
+    device, dtype, _, (_, Hkv, _, d) = _first(k_cache, "k_cache")
+    B = _dims(seqlens, "seqlens", 1)[0]
+    cache = _cache(k_cache, v_cache, page_table, seqlens, B, Hkv, d, dtype, device)
+    return _gather("attn_cache_gather", cache, B, Hkv, int(S), d, dtype, device, k_out, v_out, stream)
 
 
 def attn_cache_gather_fp4(k_codes, k_factors, v_codes, v_factors, page_table, seqlens, S: int, k_descale=None,
                           v_descale=None, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
     """attn_cache_gather from a 4-bit paged cache, as fp16 or bf16 (C ABI
     `attn_cache_gather_fp4`)."""
-    if not isinstance(k_codes, torch.Tensor) or not k_codes.is_cuda or k_codes.dim() != 4:
-        raise ValueError("k_codes must be a CUDA tensor [n_pages, Hkv, page_size, d / 2] (there is no CPU path)")
+    _, Hkv, _, half = _dims(k_codes, "k_codes", 4)
+    if not k_codes.is_cuda:
+        raise ValueError("k_codes must be a CUDA tensor (there is no CPU path)")
     if dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {dtype}; expected float16 or bfloat16")
-    device = k_codes.device
-    B, Hkv, d = _batch(seqlens), k_codes.shape[1], k_codes.shape[3] * 2
-    ptrs, sizes = _cache_fp4(k_codes, k_factors, v_codes, v_factors, k_descale, v_descale, page_table, seqlens, B,
-                             Hkv, d, device)
-    return _gather("attn_cache_gather_fp4", ptrs, sizes, B, Hkv, int(S), d, dtype, device, k_out, v_out, stream)
+    device, B = k_codes.device, _dims(seqlens, "seqlens", 1)[0]
+    cache = _cache_fp4(k_codes, k_factors, v_codes, v_factors, k_descale, v_descale, page_table, seqlens, B, Hkv,
+                       2 * half, device)
+    return _gather("attn_cache_gather_fp4", cache, B, Hkv, int(S), 2 * half, dtype, device, k_out, v_out, stream)
 
 
-def _batch(seqlens):
-    if not isinstance(seqlens, torch.Tensor) or seqlens.dim() != 1:
-        raise ValueError("seqlens must be an int32 tensor [B]")
-    return seqlens.shape[0]
+def attn_decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, d: int, max_len: int = 2 ** 31 - 1) -> int:
+    """Bytes of the paged decodes' workspace; smaller where max_len, the tokens
+    that max_pages pages hold, is short."""
+    return int(load_library().attn_decode_paged_workspace_bytes(B, Hq, Hkv, d, max_len))
 
 
-def attn_decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, d: int) -> int:
-    return int(load_library().attn_decode_paged_workspace_bytes(B, Hq, Hkv, d))
-
-
-def _decode(name, q, Hkv, cache, scale, workspace, out, lse, return_lse, stream):
-    device, dtype = _first(q, "q")
-    B, H, one, d = q.shape
+def _decode(name, first, q, cache, Hkv, scale, workspace, out, lse, return_lse, stream):
+    device, dtype, code, shape = first
+    B, H, one, d = shape
     if one != 1:
         raise ValueError("decode takes exactly one query per sequence: q [B,Hq,1,d]")
-    q_ptr = _plain(q, "q", q.shape, (dtype,), device)
-    ptrs, sizes = cache(B, d, dtype, device)
-    lib = load_library()
+    ptrs, sizes = cache
     if workspace is None:
-        workspace = torch.empty(max(lib.attn_decode_paged_workspace_bytes(B, H, Hkv, d), 16), dtype=torch.uint8,
-                                device=device)
+        need = _library().attn_decode_paged_workspace_bytes(B, H, Hkv, d, sizes[0] * sizes[2])
+        workspace = torch.empty(max(need, 16), dtype=_U8, device=device)
+        ws, ws_bytes = workspace.data_ptr(), need
+    else:
+        ws, ws_bytes = _workspace(workspace, device)
     if out is None:
-        out = torch.empty_like(q)
-    if lse is None and return_lse:
-        lse = torch.empty((B, H), dtype=torch.float32, device=device)
-    _on(getattr(lib, name), name,
-        (q_ptr, *ptrs, _plain(out, "out", q.shape, (dtype,), device), _plain(lse, "lse", (B, H), _F32, device), B, H,
-         Hkv, d, *sizes, 1.0 / math.sqrt(d) if scale is None else float(scale), workspace.data_ptr(),
-         _workspace(workspace, device), _DTYPES[dtype]), device, stream)
+        out = torch.empty(shape, dtype=dtype, device=device)
+        o_ptr = out.data_ptr()
+    else:
+        o_ptr = _ptr(out, "out", shape, dtype, device)
+    if lse is None:
+        l_ptr = None
+        if return_lse:
+            lse = torch.empty((B, H), dtype=_F32, device=device)
+            l_ptr = lse.data_ptr()
+    else:
+        l_ptr = _ptr(lse, "lse", (B, H), _F32, device)
+    _call(name, (_ptr(q, "q", shape, dtype, device), *ptrs, o_ptr, l_ptr, B, H, Hkv, d, *sizes,
+                 1.0 / math.sqrt(d) if scale is None else scale, ws, ws_bytes, code), device, stream)
     return out, lse
 
 
@@ -359,24 +400,18 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seqlens, scale: float | N
     [B,max_pages]; seqlens int32 [B] (0: o = 0, lse = -inf).  workspace:
     optional buffer of attn_decode_paged_workspace_bytes(B, Hq, Hkv, d) bytes
     (allocated here if omitted).  Returns (o [B,Hq,1,d], lse [B,Hq] or None)."""
-    Hkv = _kv_heads(k_cache, "k_cache")
-    return _decode("attn_decode_paged", q, Hkv,
-                   lambda B, d, dtype, dev: _cache(k_cache, v_cache, page_table, seqlens, B, Hkv, d, dtype, dev),
-                   scale, workspace, out, lse, return_lse, stream)
+    first = device, dtype, _, (B, _, _, d) = _first(q, "q")
+    Hkv = _dims(k_cache, "k_cache", 4)[1]
+    cache = _cache(k_cache, v_cache, page_table, seqlens, B, Hkv, d, dtype, device)
+    return _decode("attn_decode_paged", first, q, cache, Hkv, scale, workspace, out, lse, return_lse, stream)
 
 
 def attn_decode_paged_fp4(q, k_codes, k_factors, v_codes, v_factors, page_table, seqlens, k_descale=None,
                           v_descale=None, scale: float | None = None, workspace=None, out=None, lse=None,
                           return_lse: bool = True, stream=None):
     """attn_decode_paged over a 4-bit paged cache (C ABI `attn_decode_paged_fp4`)."""
-    Hkv = _kv_heads(k_codes, "k_codes")
-    return _decode("attn_decode_paged_fp4", q, Hkv,
-                   lambda B, d, dtype, dev: _cache_fp4(k_codes, k_factors, v_codes, v_factors, k_descale, v_descale,
-                                                       page_table, seqlens, B, Hkv, d, dev),
-                   scale, workspace, out, lse, return_lse, stream)
-
-
-def _kv_heads(t, name):
-    if not isinstance(t, torch.Tensor) or t.dim() != 4:
-        raise ValueError(f"{name} must be a tensor of 4 dims [n_pages, Hkv, page_size, ..]")
-    return t.shape[1]
+    first = device, _, _, (B, _, _, d) = _first(q, "q")
+    Hkv = _dims(k_codes, "k_codes", 4)[1]
+    cache = _cache_fp4(k_codes, k_factors, v_codes, v_factors, k_descale, v_descale, page_table, seqlens, B, Hkv, d,
+                       device)
+    return _decode("attn_decode_paged_fp4", first, q, cache, Hkv, scale, workspace, out, lse, return_lse, stream)

@@ -491,9 +491,11 @@ int attn_cache_gather_fp4(const void *k_codes, const void *k_factors, const void
  * attn_decode_paged_workspace_bytes -- bytes of device workspace the paged
  * decodes need: two partial states (m, l, o[d]) of up to 16 query heads for
  * each CTA of the grid, and two ints for each (sequence, unit of query heads).
- * Does not depend on the lengths.  Returns 0 for invalid sizes.
+ * max_len is the number of tokens that a sequence's pages can hold, max_pages *
+ * page_size (any larger value is safe); the sequences' lengths do not matter.
+ * Returns 0 for invalid sizes.
  */
-size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
+size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_len);
 
 /*
  * attn_decode_paged -- one-query decode over a 16-bit paged cache.
@@ -501,8 +503,8 @@ size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
  *   q [B, Hq, 1, d]  dtype, input;  o [B, Hq, 1, d]  dtype, output
  *   lse [B, Hq]  fp32, output; may be NULL
  *   seqlens: a sequence of length 0 gets o = 0 and lse = -inf
- *   workspace: at least attn_decode_paged_workspace_bytes(B, Hq, Hkv, d) bytes,
- *            16-byte aligned; contents on entry do not matter; calls that may
+ *   workspace: at least attn_decode_paged_workspace_bytes(B, Hq, Hkv, d,
+ *            max_pages * page_size) bytes, 16-byte aligned; contents on entry do not matter; calls that may
  *            overlap on the GPU need one each
  * The key axes of all sequences are divided evenly over the GPU, whatever the
  * lengths are, so there is no number of splits to choose; the division follows

@@ -144,7 +144,7 @@ def test_cache_refusals(lib, name, fp4):
         assert call(B=1 << 15, Hkv=2) == -1
     if name == "attn_decode_paged":
         assert call(Hq=5) == -2 and call(B=65536) == -1
-        need = lib.attn_decode_paged_workspace_bytes(2, 4, 2, 128)
+        need = lib.attn_decode_paged_workspace_bytes(2, 4, 2, 128, 32)
         assert call(wsb=need - 1) == -6
         assert call(lse=FAKE + 2) == -5
     if not torch.cuda.is_available():
@@ -153,12 +153,15 @@ def test_cache_refusals(lib, name, fp4):
             assert call(q=None, qo=None, rope=None, rot=0, rows=0) == -10
 
 
-def test_decode_workspace_does_not_grow_with_lengths(lib):
-    one = lib.attn_decode_paged_workspace_bytes(1, 32, 8, 128)
+def test_decode_workspace(lib):
+    """States for the most CTAs that can have work, whatever the lengths are."""
+    size = lib.attn_decode_paged_workspace_bytes
+    one = size(1, 32, 8, 128, 1 << 20)
     assert one == 1024 * 2 * 4 * 130 * 4 + 8 * 8
-    assert lib.attn_decode_paged_workspace_bytes(64, 32, 8, 128) == one + 63 * 64
-    assert lib.attn_decode_paged_workspace_bytes(1, 32, 1, 64) == 1024 * 2 * 16 * 66 * 4 + 2 * 8
-    assert lib.attn_decode_paged_workspace_bytes(1, 5, 2, 64) == 0
+    assert size(64, 32, 8, 128, (1 << 31) - 1) == one + 63 * 64
+    assert size(1, 32, 1, 64, 1 << 20) == 1024 * 2 * 16 * 66 * 4 + 2 * 8
+    assert size(1, 32, 8, 128, 1000) == 8 * 16 * 2 * 4 * 130 * 4 + 8 * 8
+    assert size(1, 5, 2, 64, 64) == 0 and size(1, 4, 2, 64, 0) == 0
 
 
 def test_status_words(lib):
