@@ -1,5 +1,7 @@
 """Builds libgbattn.so in-tree with nvcc for sm_103a (no CMake, no torch
-extension machinery): each .cu compiles in parallel, then one link step.
+extension machinery): each .cu compiles in parallel, then one link step.  The
+compiled half of the Python binding (_paged.so, C++ against the installed
+PyTorch's headers) is built beside it.
 
     python -m exact_tiled_attention_gb300._build [--force] [--verbose]
 
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgbattn.so")
+EXT = os.path.join(PKG, "_paged.so")
+EXT_SOURCE = "paged_binding.cpp"
 
 SOURCES = ["gbattn_api.cu", "prefill_fwd.cu", "prefill_pair.cu", "prefill_fp8.cu", "decode_splitkv.cu",
            "decode_noalloc.cu", "backward.cu", "backward_atomic.cu",
@@ -56,13 +61,43 @@ def _options() -> list[str]:
     return [f"-DGBATTN_EX2_EMU_EVERY={emu}"]
 
 
+def _ext_commands() -> tuple[list[str], list[str]]:
+    """Compile and link commands of the binding's compiled half."""
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD, EXT_SOURCE.replace(".cpp", ".o"))
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+                "-I", INCLUDE, "-isystem", sysconfig.get_path("include"), "-isystem", os.path.join(base, "include"),
+                "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
+                "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
+    link = [cxx, "-shared", obj, "-o", EXT + f".tmp{os.getpid()}", "-L" + PKG, "-l:libgbattn.so",
+            "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
+    return compile_, link
+
+
+def _run(cmd: list[str], what: str, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed")
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     deps = _deps()
     stamp = os.path.join(BUILD, "options.txt")
+    import torch
+
     opts = _options()
+    built_as = " ".join(opts + [f"torch-{torch.__version__}"])
     old = open(stamp).read() if os.path.exists(stamp) else ""
-    if not force and not _stale(LIB, deps) and old == " ".join(opts):
+    if not force and not _stale(LIB, deps) and not _stale(EXT, deps) and old == built_as:
         return LIB
     cc = nvcc()
     extra = (["-Xptxas", "-v"] if ptxas_verbose else []) + opts
@@ -75,8 +110,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    ext_compile, ext_link = _ext_commands()
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext = ex.submit(_run, ext_compile, f"g++ on {EXT_SOURCE}", verbose)
         results = list(ex.map(compile_one, SOURCES))
+        ext.result()
     for src, _, r in results:
         if verbose or ptxas_verbose or r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
@@ -89,8 +127,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("nvcc link failed")
     os.replace(tmp, LIB)
+    _run(ext_link, "g++ link", verbose)
+    os.replace(EXT + f".tmp{os.getpid()}", EXT)
     with open(stamp, "w") as f:
-        f.write(" ".join(opts))
+        f.write(built_as)
     return LIB
 
 
