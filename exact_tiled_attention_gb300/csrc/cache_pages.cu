@@ -287,10 +287,11 @@ int launch_append_t(const AppendArgs& a) {
   p.status = a.status;
   const long long tokens = static_cast<long long>(a.B) * a.S;
   const long long token_ctas = (tokens + kThreads / RowCfg<D>::kLanes - 1) / (kThreads / RowCfg<D>::kLanes);
-  // As many heads a thread as leave four CTAs for each SM, at most 8.
+  // As many heads a thread as leave 32 CTAs (four rounds of them) for each SM, at
+  // most 8.
   int per = 8;
   const int heads = p.heads[0] + p.heads[1] + p.heads[2];
-  while (per > 1 && token_ctas * (heads / per) < 4LL * a.num_sms) per /= 2;
+  while (per > 1 && token_ctas * (heads / per) < 32LL * a.num_sms) per /= 2;
   p.per_chunk = per;
   int chunks = 0;
   for (int i = 0; i < 3; ++i) chunks += p.chunks[i] = (p.heads[i] + per - 1) / per;

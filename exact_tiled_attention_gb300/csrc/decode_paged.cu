@@ -120,6 +120,21 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
   }
 }
 
+// The same with accumulators of zero.
+template <bool BF16>
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  if constexpr (BF16) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  }
+}
+
 // The 8 x 8 transpose of 16-bit elements held as two to a lane.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
@@ -147,11 +162,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 }
 
 template <int NT>
-__device__ __forceinline__ void zero(float (&s)[NT][4]) {
-#pragma unroll
-  for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-}
-template <int NT>
 __device__ __forceinline__ void add(float (&s)[NT][4], const float (&s2)[NT][4]) {
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -164,6 +174,21 @@ struct LanePtrs {
   const uint8_t* data[2];
   const uint8_t* factor;  // 4 bits: the piece of K's or V's factors that the lane copies
 };
+
+// Terms that P is held in for P V.  Over a 16-bit cache the rounding's remainder
+// is a second one: a single bf16 (or fp16) P shows in O next to O's own rounding
+// (relative error 2.3e-3 against 1.7e-3 in bf16 at 64 sequences of 17 thousand
+// tokens), and the loop, bound by memory, has room for the products (673 us
+// with them, 684 without).  Over a 4-bit cache P is one fp16: the loop is bound
+// by issue there, and the cache's own error is larger.
+template <int FMT>
+constexpr int kTerms = FMT == kFp4 ? 1 : 2;
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
 
 // What one lane holds of 16 keys: for K rows r and r + 8 (r = lane / 4), for V
 // keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9 (q = lane % 4).  Keys from n_keys on are
@@ -213,22 +238,25 @@ struct Tile {
   template <int NT>
   __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&qf)[NT][D / 16][2]) const {
     float s2[NT][4];
-    zero(s);
-    zero(s2);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        mma16816<FMT == kBf16>(s[t], k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, qf[t][2 * c][0], qf[t][2 * c][1]);
-        mma16816<FMT == kBf16>(s2[t], k[0][c].z, k[1][c].z, k[0][c].w, k[1][c].w, qf[t][2 * c + 1][0],
-                               qf[t][2 * c + 1][1]);
+        const uint32_t(&q0)[2] = qf[t][2 * c], (&q1)[2] = qf[t][2 * c + 1];
+        if (c == 0) {
+          mma16816_first<FMT == kBf16>(s[t], k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, q0[0], q0[1]);
+          mma16816_first<FMT == kBf16>(s2[t], k[0][c].z, k[1][c].z, k[0][c].w, k[1][c].w, q1[0], q1[1]);
+        } else {
+          mma16816<FMT == kBf16>(s[t], k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, q0[0], q0[1]);
+          mma16816<FMT == kBf16>(s2[t], k[0][c].z, k[1][c].z, k[0][c].w, k[1][c].w, q1[0], q1[1]);
+        }
       }
     add(s, s2);
   }
   // o += V^T P^T; product j = 4 c + w holds elements 64 c + 8 r + 2 w (rows r)
   // and the next one (rows r + 8).
   template <int NT>
-  __device__ __forceinline__ void values(float (&o)[NT][D / 16][4], const uint32_t (&pf)[NT][2]) const {
+  __device__ __forceinline__ void values(float (&o)[NT][D / 16][4], const uint32_t (&pf)[NT][kTerms<FMT>][2]) const {
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       const uint32_t w[4][4] = {{v[0][c].x, v[0][c].y, v[0][c].z, v[0][c].w},
@@ -240,13 +268,15 @@ struct Tile {
         const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5410), a1 = __byte_perm(w[0][j], w[1][j], 0x7632);
         const uint32_t a2 = __byte_perm(w[2][j], w[3][j], 0x5410), a3 = __byte_perm(w[2][j], w[3][j], 0x7632);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816<FMT == kBf16>(o[t][4 * c + j], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < kTerms<FMT>; ++i)
+            mma16816<FMT == kBf16>(o[t][4 * c + j], a0, a1, a2, a3, pf[t][i][0], pf[t][i][1]);
       }
     }
   }
-  __device__ static __forceinline__ int k_element(int step, int lane, int half) {
-    return 32 * (step / 2) + 8 * (lane & 3) + 4 * (step & 1) + 2 * half;
-  }
+  // First of the 8 elements of Q that steps 2 i and 2 i + 1 take from a lane.
+  __device__ static __forceinline__ int k_element(int i, int lane) { return 32 * i + 8 * (lane & 3); }
   __device__ static __forceinline__ int o_element(int j, int lane, int half) {
     return 64 * (j / 4) + 8 * (lane >> 2) + 2 * (j & 3) + half;
   }
@@ -324,8 +354,6 @@ struct Tile<D, kFp4> {
   template <int NT>
   __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&qf)[NT][D / 16][2]) const {
     float s2[NT][4];
-    zero(s);
-    zero(s2);
     uint32_t f2[2][D / 64];  // the group's factor in both halves
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -344,15 +372,21 @@ struct Tile<D, kFp4> {
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        mma16816<false>(s[t], a[0][0], a[1][0], a[0][1], a[1][1], qf[t][2 * w][0], qf[t][2 * w][1]);
-        mma16816<false>(s2[t], a[0][2], a[1][2], a[0][3], a[1][3], qf[t][2 * w + 1][0], qf[t][2 * w + 1][1]);
+        const uint32_t(&q0)[2] = qf[t][2 * w], (&q1)[2] = qf[t][2 * w + 1];
+        if (w == 0) {
+          mma16816_first<false>(s[t], a[0][0], a[1][0], a[0][1], a[1][1], q0[0], q0[1]);
+          mma16816_first<false>(s2[t], a[0][2], a[1][2], a[0][3], a[1][3], q1[0], q1[1]);
+        } else {
+          mma16816<false>(s[t], a[0][0], a[1][0], a[0][1], a[1][1], q0[0], q0[1]);
+          mma16816<false>(s2[t], a[0][2], a[1][2], a[0][3], a[1][3], q1[0], q1[1]);
+        }
       }
     }
     add(s, s2);
   }
   // Product j holds elements (D / 8) r + 2 j (rows r) and the next (rows r + 8).
   template <int NT>
-  __device__ __forceinline__ void values(float (&o)[NT][D / 16][4], const uint32_t (&pf)[NT][2]) const {
+  __device__ __forceinline__ void values(float (&o)[NT][D / 16][4], const uint32_t (&pf)[NT][1][2]) const {
     const uint32_t f01 = e4m3x2_to_f16(vf[0] + vf[1] * 256u), f23 = e4m3x2_to_f16(vf[2] + vf[3] * 256u);
 #pragma unroll
     for (int w = 0; w < kU; ++w) {
@@ -367,23 +401,15 @@ struct Tile<D, kFp4> {
         const uint32_t a0 = hmul2(lo0[j], f01), a1 = hmul2(lo1[j], f01);
         const uint32_t a2 = hmul2(hi0[j], f23), a3 = hmul2(hi1[j], f23);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816<false>(o[t][4 * w + j], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+        for (int t = 0; t < NT; ++t) mma16816<false>(o[t][4 * w + j], a0, a1, a2, a3, pf[t][0][0], pf[t][0][1]);
       }
     }
   }
-  __device__ static __forceinline__ int k_element(int step, int lane, int half) {
-    return (D / 4) * (lane & 3) + 4 * step + 2 * half;
-  }
+  __device__ static __forceinline__ int k_element(int i, int lane) { return (D / 4) * (lane & 3) + 8 * i; }
   __device__ static __forceinline__ int o_element(int j, int lane, int half) {
     return (D / 8) * (lane >> 2) + 2 * j + half;
   }
 };
-
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
 
 constexpr int kStages = 3;  // of a warp's ring (4-bit caches)
 
@@ -396,10 +422,10 @@ constexpr int kUnitKeys = 16 * kBlocks<FMT> * kWarps;
 // Scores s of KB blocks of 16 keys (in units of the products) to P as the operand
 // of P V, and the state (m, l, o) brought up to them.  A block's keys from
 // n_keys on do not count (WHOLE: there are none).
-template <int D, bool BF16, bool WHOLE, int KB, int NT>
+template <int D, int FMT, bool WHOLE, int KB, int NT>
 __device__ __forceinline__ void softmax_step(float (&s)[KB][NT][4], const float (&lam)[NT][2], int r, const int (&n_keys)[KB],
                                              float (&m)[NT][2], float (&l)[NT][2], float (&o)[NT][D / 16][4],
-                                             uint32_t (&pf)[KB][NT][2]) {
+                                             uint32_t (&pf)[KB][NT][kTerms<FMT>][2]) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     // Exponents relative to the reference; it moves (for the whole warp) only
@@ -448,8 +474,15 @@ __device__ __forceinline__ void softmax_step(float (&s)[KB][NT][4], const float 
         x[k][c] = ex2_approx(x[k][c]);
         l[t][c & 1] += x[k][c];
       }
-      pf[k][t][0] = transpose8x8(pack2<BF16>(x[k][0], x[k][1]));
-      pf[k][t][1] = transpose8x8(pack2<BF16>(x[k][2], x[k][3]));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t w = pack2<FMT == kBf16>(x[k][2 * i], x[k][2 * i + 1]);
+        pf[k][t][0][i] = transpose8x8(w);
+        if constexpr (kTerms<FMT> == 2) {
+          const float2 v = unpack2<FMT == kBf16>(w);
+          pf[k][t][1][i] = transpose8x8(pack2<FMT == kBf16>(x[k][2 * i] - v.x, x[k][2 * i + 1] - v.y));
+        }
+      }
     }
   }
 }
@@ -481,49 +514,70 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
   [[maybe_unused]] const uint32_t ring = smem_u32(sm_raw) + warp * C::kRing;
   const LanePtrs src = Tile<D, FMT>::ptrs(p, lane);
 
-  // ---- this CTA's run of units: [u0, u1) of U
-  long long mine = 0;
-  for (int b = threadIdx.x; b < p.B; b += kThreads) mine += (seq_len(p, b) + UK - 1) / UK;
+  // ---- this CTA's run of units, [u0, u1) of U, and the sequence that holds u0
+  long long U, N, u0, u1, rem;
+  int b;
+  {
+    // Tiles of the first kThreads sequences, scanned; then of all of them.
+    auto tiles_of = [&](int i) { return i < p.B ? (seq_len(p, i) + UK - 1) / UK : 0; };
+    auto scan = [&](int n, long long before, long long& all) {
+      long long incl = n;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sm_scan[warp] = mine;
-  __syncthreads();
-  long long tiles = 0;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) sm_scan[warp] = incl;
+      __syncthreads();
+      incl += before;
+      all = before;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) tiles += sm_scan[w];
-  const long long U = tiles * HG;
-  const long long N = min(static_cast<long long>(gridDim.x), U);
-  if (blockIdx.x >= N) return;
-  const long long u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
-  // ---- the sequence that holds unit u0, and the tiles before it
-  const long long t0 = u0 / HG;
-  long long before = 0;
-  for (int base = 0;; base += kThreads) {
-    const int b = base + threadIdx.x;
-    const int n = b < p.B ? (seq_len(p, b) + UK - 1) / UK : 0;
-    long long incl = n;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) incl += sm_scan[w];
+        all += sm_scan[w];
+      }
+      return incl;
+    };
+    int i = threadIdx.x, n = tiles_of(i);
+    long long upto, tiles;  // tiles of sequences 0 .. i; of all
+    const long long first = scan(n, 0, upto);
+    tiles = upto;
+    if (p.B > kThreads) {
+      long long mine = 0, all;
+      for (int j = i + kThreads; j < p.B; j += kThreads) mine += tiles_of(j);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+      __syncthreads();
+      if (lane == 0) sm_scan[warp] = mine;
+      __syncthreads();
+      all = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) all += sm_scan[w];
+      tiles += all;
+      __syncthreads();
+    }
+    U = tiles * HG;
+    N = min(static_cast<long long>(gridDim.x), U);
+    if (blockIdx.x >= N) return;
+    u0 = U * blockIdx.x / N;
+    u1 = U * (blockIdx.x + 1) / N;
+    const long long t0 = u0 / HG;  // its tile; < tiles, so the search ends
+    long long incl = first, all = upto;
+    for (;;) {
+      if (t0 >= incl - n && t0 < incl) {
+        sm_b = i;
+        sm_before = incl - n;
+      }
+      if (t0 < all) break;
+      i += kThreads;
+      n = tiles_of(i);
+      __syncthreads();
+      incl = scan(n, all, all);
     }
     __syncthreads();
-    if (lane == 31) sm_scan[warp] = incl;
-    __syncthreads();
-    long long off = before;
-    for (int w = 0; w < warp; ++w) off += sm_scan[w];
-    incl += off;
-    if (t0 >= incl - n && t0 < incl) {
-      sm_b = b;
-      sm_before = incl - n;
-    }
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) before += sm_scan[w];
-    if (t0 < before) break;  // t0 < tiles, so this ends
+    b = sm_b;
+    rem = u0 - sm_before * HG;
   }
-  __syncthreads();
-  int b = sm_b;
-  long long rem = u0 - sm_before * HG;
   int n_tiles = (seq_len(p, b) + UK - 1) / UK;
   int hg = static_cast<int>(rem / n_tiles);
   int tile = static_cast<int>(rem % n_tiles);
@@ -536,50 +590,55 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
     const int head0 = kvh * p.g + grp * kMaxGroup;
     const int n_heads = min(kMaxGroup, p.g - grp * kMaxGroup);
 
-    // ---- Q as the products' B operand, in the element order of K
+    // ---- Q as the products' B operand, in the element order of K; read once the
+    // first keys are on their way
     uint32_t qf[NT][D / 16][2];
     float lam[NT][2];  // base-2 units of a score, for the lane's two query columns
+    auto load_q = [&] {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int row = 8 * t + r;
-      const uint16_t* qrow = p.q + (static_cast<long long>(b) * p.Hq + head0 + row) * D;
+      for (int t = 0; t < NT; ++t) {
+        const int row = 8 * t + r;
+        const uint16_t* qrow = p.q + (static_cast<long long>(b) * p.Hq + head0 + row) * D;
 #pragma unroll
-      for (int st = 0; st < D / 16; ++st)
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 w = row < n_heads ? *reinterpret_cast<const uint4*>(qrow + Tile<D, FMT>::k_element(i, lane))
+                                        : make_uint4(0u, 0u, 0u, 0u);
+          qf[t][2 * i][0] = w.x;
+          qf[t][2 * i][1] = w.y;
+          qf[t][2 * i + 1][0] = w.z;
+          qf[t][2 * i + 1][1] = w.w;
+        }
+        lam[t][0] = lam[t][1] = p.scale_log2;
+        if constexpr (FMT == kFp4) {
+          // The products are in fp16: scale the row by a power of two that brings
+          // its largest element to [1, 2).  Exact for bf16 too, but for elements
+          // under 2^-14 of the largest, which keep an error of 2^-25 of it.
+          float2 f[D / 16][2];
+          float top = 0.f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          qf[t][st][h] = row < n_heads
-                             ? *reinterpret_cast<const uint32_t*>(qrow + Tile<D, FMT>::k_element(st, lane, h))
-                             : 0u;
-      lam[t][0] = lam[t][1] = p.scale_log2;
-      if constexpr (FMT == kFp4) {
-        // The products are in fp16: scale the row by a power of two that brings
-        // its largest element to [1, 2).  Exact for bf16 too, but for elements
-        // under 2^-14 of the largest, which keep an error of 2^-25 of it.
-        float2 f[D / 16][2];
-        float top = 0.f;
+          for (int st = 0; st < D / 16; ++st)
 #pragma unroll
-        for (int st = 0; st < D / 16; ++st)
+            for (int h = 0; h < 2; ++h) {
+              f[st][h] = p.out_bf16 ? unpack2<true>(qf[t][st][h]) : unpack2<false>(qf[t][st][h]);
+              top = fmaxf(top, fmaxf(fabsf(f[st][h].x), fabsf(f[st][h].y)));
+            }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // Exponent field in [2, 252]: both the factor and its inverse are normal.
+          const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 2), 252);
+          const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+          const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            f[st][h] = p.out_bf16 ? unpack2<true>(qf[t][st][h]) : unpack2<false>(qf[t][st][h]);
-            top = fmaxf(top, fmaxf(fabsf(f[st][h].x), fabsf(f[st][h].y)));
-          }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // Exponent field in [2, 252]: both the factor and its inverse are normal.
-        const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 2), 252);
-        const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-        const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+          for (int st = 0; st < D / 16; ++st)
 #pragma unroll
-        for (int st = 0; st < D / 16; ++st)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) qf[t][st][h] = pack2<false>(f[st][h].x * down, f[st][h].y * down);
-        const float kd = p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f;
-        const float row_lam = p.scale_log2 * kd * up;
-        lam[t][0] = __shfl_sync(0xffffffffu, row_lam, 8 * q4);
-        lam[t][1] = __shfl_sync(0xffffffffu, row_lam, 8 * q4 + 4);
+            for (int h = 0; h < 2; ++h) qf[t][st][h] = pack2<false>(f[st][h].x * down, f[st][h].y * down);
+          const float kd = p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f;
+          const float row_lam = p.scale_log2 * kd * up;
+          lam[t][0] = __shfl_sync(0xffffffffu, row_lam, 8 * q4);
+          lam[t][1] = __shfl_sync(0xffffffffu, row_lam, 8 * q4 + 4);
+        }
       }
-    }
+    };
 
     float o[NT][D / 16][4];
     float m[NT][2], l[NT][2];  // per query column; l is this lane's share of the sum
@@ -620,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
           const int b0 = block_of(blk, page0), b1 = block_of(blk + 1, page1);
           const int next = blk + kWarps * KB;
           page0 = page_of(next);
-          page1 = page_of(next + 1);
+          page1 = block_shift > 0 ? page0 : page_of(next + 1);
           if (b0 >= 0) Stage<D>::fill(src, stage, b0, lane);
           if (b1 >= 0) Stage<D>::fill(src, stage + Stage<D>::kBytes, b1, lane);
           absent |= (b0 < 0 ? 1u : 0u) | (b1 < 0 ? 2u : 0u);
@@ -630,6 +689,7 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
       constexpr uint32_t kUnitBytes = KB * Stage<D>::kBytes;
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) request(tile + i, ring + i * kUnitBytes);
+      load_q();
       uint32_t stage = ring, free_stage = ring + (kStages - 1) * kUnitBytes;
       for (int i = tile; i < end; ++i) {
         copy_wait<kStages - 2>();
@@ -638,13 +698,13 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
         auto step = [&](auto whole, int n0, int n1) {
           const int n_keys[KB] = {n0, n1};
           float s[KB][NT][4];
-          uint32_t pf[KB][NT][2];
+          uint32_t pf[KB][NT][1][2];
 #pragma unroll
           for (int k = 0; k < KB; ++k) {
             tl.load_k(stage + k * Stage<D>::kBytes, lane);
             tl.template scores<NT>(s[k], qf);
           }
-          softmax_step<D, false, decltype(whole)::value, KB, NT>(s, lam, r, n_keys, m, l, o, pf);
+          softmax_step<D, FMT, decltype(whole)::value, KB, NT>(s, lam, r, n_keys, m, l, o, pf);
 #pragma unroll
           for (int k = 0; k < KB; ++k) {
             tl.template load_v<decltype(whole)::value>(stage + k * Stage<D>::kBytes, lane, n_keys[k]);
@@ -672,9 +732,10 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
         tl.load_k(src, block, lane, n_keys[0]);
         tl.load_v(src, block, lane, n_keys[0]);
       }
+      load_q();
       for (int i = tile; i < end; ++i) {
         float s[1][NT][4];
-        uint32_t pf[1][NT][2];
+        uint32_t pf[1][NT][kTerms<FMT>][2];
         tl.template scores<NT>(s[0], qf);
         int n_next = 0, block = 0;
         if (i + 1 < end) {
@@ -684,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
           page_next = page_of(blk + kWarps);
           tl.load_k(src, block, lane, n_next);
         }
-        softmax_step<D, FMT == kBf16, false, 1, NT>(s, lam, r, n_keys, m, l, o, pf);
+        softmax_step<D, FMT, false, 1, NT>(s, lam, r, n_keys, m, l, o, pf);
         tl.template values<NT>(o, pf[0]);
         if (i + 1 < end) tl.load_v(src, block, lane, n_next);
         n_keys[0] = n_next;
