@@ -80,11 +80,11 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   constexpr int kRowsCta = kThreads / kLanes;
   const int lane_in_row = threadIdx.x % kLanes;
   const int e0 = 8 * lane_in_row;
-  const long long tokens = static_cast<long long>(p.B) * p.S;
-  long long t = static_cast<long long>(blockIdx.x) * kRowsCta + threadIdx.x / kLanes;
-  const bool in_grid = t < tokens;
-  if (!in_grid) t = tokens - 1;  // the whole warp stays for the shuffles
-  const int b = static_cast<int>(t / p.S), i = static_cast<int>(t % p.S);
+  const int tokens = p.B * p.S;
+  const int at = blockIdx.x * kRowsCta + static_cast<int>(threadIdx.x) / kLanes;
+  const bool in_grid = at < tokens;
+  const int t = min(at, tokens - 1);  // the whole warp stays for the shuffles
+  const int b = t / p.S, i = t % p.S;
   int which = 0, chunk = blockIdx.y;  // 0: queries, 1: keys, 2: values
   while (which < 2 && chunk >= p.chunks[which]) chunk -= p.chunks[which++];
   const int h0 = chunk * p.per_chunk;

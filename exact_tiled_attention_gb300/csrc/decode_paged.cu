@@ -25,6 +25,7 @@
 
 #include <type_traits>
 
+#include "gbattn_copy.cuh"
 #include "gbattn_internal.h"
 #include "gbattn_ptx.cuh"
 
@@ -73,15 +74,6 @@ __device__ __forceinline__ uint4 ld16(const uint8_t* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
-}
-// An asynchronous copy of 16 bytes into shared memory, past L1.
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int PENDING>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 __device__ __forceinline__ void lds(uint32_t (&v)[4], uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"

@@ -14,6 +14,9 @@ namespace {
 bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
+// The kernels count tokens in 32 bits (with room for a grid's step behind the last).
+bool too_many_tokens(int B, int S) { return static_cast<long long>(B) * S > 0x40000000LL; }
+
 // Strides (batch, head, seq) of a [B, heads, S, d] tensor from the caller's
 // three values, or of the contiguous tensor when there are none.  Rows start on
 // 16-byte boundaries, so each stride is a multiple of 8 elements.
@@ -74,6 +77,7 @@ int check_norm_rope(NormRopeArgs* a, const void* q, const void* k, const float* 
                     const long long* q_strides, const long long* k_strides, float eps, int rope_rows, int rot_dim,
                     int interleaved, int dtype, void* stream) {
   if (B < 1 || H < 1 || Hkv < 1 || S < 1 || H > 16384 || Hkv > 16384) return GBATTN_EBADSHAPE;
+  if (too_many_tokens(B, S)) return GBATTN_EBADSHAPE;
   if (H % Hkv != 0) return GBATTN_EHEADS;
   if (d != 64 && d != 128) return GBATTN_EHEADDIM;
   if (dtype != GBATTN_F16 && dtype != GBATTN_BF16) return GBATTN_EDTYPE;
@@ -108,6 +112,7 @@ int append(const void* k, const void* v, void* k_cache, void* k_factors, void* v
            int page_size, int n_pages, int max_pages, const long long* q_strides, const long long* k_strides,
            const long long* v_strides, int rope_rows, int rot_dim, int interleaved, int dtype, void* stream) {
   if (B < 1 || H < 1 || Hkv < 1 || S < 1 || H > 16384 || Hkv > 16384) return GBATTN_EBADSHAPE;
+  if (too_many_tokens(B, S)) return GBATTN_EBADSHAPE;
   if (H % Hkv != 0) return GBATTN_EHEADS;
   AppendArgs a{};
   int rc = check_cache(&a.cache, k_cache, v_cache, k_factors, v_factors, fp4, k_descale, v_descale, page_table,

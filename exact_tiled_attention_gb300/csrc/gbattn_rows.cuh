@@ -7,6 +7,7 @@
 
 #include <stdint.h>
 
+#include "gbattn_copy.cuh"
 #include "gbattn_internal.h"
 #include "gbattn_ptx.cuh"
 
@@ -102,6 +103,61 @@ __device__ __forceinline__ void load_rope(LaneRope& r, const float* row, int rot
     }
   }
 }
+
+// The rows that a thread works on, of N tensors at once, on their way through
+// shared memory: for tokens t0, t0 + step, .. (t0 a CTA's first, a row's lanes
+// one token each) the heads [h0, h1).  Each lane copies its own pieces, STAGES - 1
+// rows ahead over heads and tokens alike, and waits for nobody else's; what it
+// has on its way would not fit in its registers.
+template <int D, int N, int THREADS, int STAGES>
+struct RowRing {
+  using Smem = uint4[STAGES][2 * N][THREADS];
+  Smem* smem;
+  const uint16_t* base[N];
+  RowStrides strides[N];
+  int S, tokens, step, h0, h1;
+  const uint16_t* row[N];  // of the next request
+  int t, h, in, out;       // its token block and head; stages to fill and to read next
+
+  __device__ __forceinline__ void at_token() {
+    const int i = min(t + static_cast<int>(threadIdx.x) / RowCfg<D>::kLanes, tokens - 1);
+    const int b = i / S, s = i % S;
+#pragma unroll
+    for (int k = 0; k < N; ++k) row[k] = base[k] + b * strides[k].b + s * strides[k].s + h0 * strides[k].h;
+  }
+  // The first requests; base and strides are set.
+  __device__ __forceinline__ void start(Smem* smem_, int S_, int tokens_, int t0, int step_, int h0_, int h1_) {
+    smem = smem_, S = S_, tokens = tokens_, t = t0, step = step_, h0 = h = h0_, h1 = h1_, in = out = 0;
+    at_token();
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) request();
+  }
+  __device__ __forceinline__ void request() {
+    if (t < tokens) {
+      const int e0 = 8 * (threadIdx.x % RowCfg<D>::kLanes);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) copy16(smem_u32(&(*smem)[in][2 * k + c][threadIdx.x]), row[k] + c * (D / 2) + e0);
+        row[k] += strides[k].h;
+      }
+      in = in + 1 == STAGES ? 0 : in + 1;
+      if (++h == h1) {
+        h = h0;
+        t += step;
+        at_token();
+      }
+    }
+    copy_commit();
+  }
+  // Waits for the next row; piece(k, c) is then its chunk c of tensor k, until pop().
+  __device__ __forceinline__ void wait() const { copy_wait<STAGES - 2>(); }
+  __device__ __forceinline__ uint4 piece(int k, int c) const { return (*smem)[out][2 * k + c][threadIdx.x]; }
+  __device__ __forceinline__ void pop() {
+    out = out + 1 == STAGES ? 0 : out + 1;
+    request();  // into the stage that the row before this one has left
+  }
+};
 
 // Offset of the chunk that holds the partners of the chunk at e0 when pairs
 // are rot / 2 apart in a part of the head (kRopePart); e0 itself outside it.

@@ -20,6 +20,8 @@ namespace gbattn {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kStages = 4;         // of the rings of rows
+constexpr int kFwdCtas = 64;       // of the forward for each SM, at most
 constexpr int kMaxBwdCtas = 1024;  // partial weight gradients kept for each of q and k
 
 struct NormRopeParams {
@@ -58,22 +60,24 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// Grid: (CTAs that walk over tokens, head chunks of q then k).
 template <int D, bool BF16, int MODE, bool NORM>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-  constexpr int kRowsCta = kThreads / RowCfg<D>::kLanes;
-  const int lane_in_row = threadIdx.x % RowCfg<D>::kLanes;
-  const long long tokens = static_cast<long long>(p.B) * p.S;
-  long long t = static_cast<long long>(blockIdx.x) * kRowsCta + threadIdx.x / RowCfg<D>::kLanes;
-  const bool real = t < tokens;
-  if (!real) t = tokens - 1;  // the whole warp stays for the shuffles
-  const int b = static_cast<int>(t / p.S), s = static_cast<int>(t % p.S);
+  constexpr int kLanes = RowCfg<D>::kLanes;
+  constexpr int kRowsCta = kThreads / kLanes;
+  using Ring = RowRing<D, 1, kThreads, kStages>;
+  __shared__ typename Ring::Smem ring_smem;
+  const int lane_in_row = threadIdx.x % kLanes;
+  const int tokens = p.B * p.S;
   const int which = blockIdx.y < p.chunks[0] ? 0 : 1;
   const int h0 = (blockIdx.y - (which ? p.chunks[0] : 0)) * p.per_chunk;
   const int h1 = min(h0 + p.per_chunk, p.heads[which]);
   const int e0 = 8 * lane_in_row;
 
-  LaneRope rope;
-  if constexpr (MODE != kRopeNone) load_rope<D, MODE>(rope, table_row(p, b, s), p.rot, lane_in_row);
+  Ring ring;
+  ring.base[0] = p.x[which];
+  ring.strides[0] = p.xs[which];
+  ring.start(&ring_smem, p.S, tokens, blockIdx.x * kRowsCta, gridDim.x * kRowsCta, h0, h1);
   float w[2][8], wp[2][8];
   int pc[2] = {0, 0};
 #pragma unroll
@@ -84,34 +88,44 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
       if constexpr (MODE == kRopePart) load8(p.w[which] + pc[c], wp[c]);
     }
   }
-  const RowStrides xs = p.xs[which];
-  const uint16_t* xrow = p.x[which] + b * xs.b + s * xs.s + h0 * xs.h;
-  uint16_t* yrow = p.y[which] + ((static_cast<long long>(b) * p.heads[which] + h0) * p.S + s) * D;
-  for (int h = h0; h < h1; ++h, xrow += xs.h, yrow += static_cast<long long>(p.S) * D) {
-    float z[2][8], part[2][8];
-    float sq = 0.f;
+  for (int t0 = blockIdx.x * kRowsCta; t0 < tokens; t0 += gridDim.x * kRowsCta) {
+    const int at = t0 + static_cast<int>(threadIdx.x) / kLanes;
+    const bool real = at < tokens;
+    const int t = min(at, tokens - 1);  // the whole warp stays for the shuffles
+    const int b = t / p.S, s = t % p.S;
+    LaneRope rope;
+    if constexpr (MODE != kRopeNone) load_rope<D, MODE>(rope, table_row(p, b, s), p.rot, lane_in_row);
+    [[maybe_unused]] const uint16_t* xrow =
+        p.x[which] + b * p.xs[which].b + s * p.xs[which].s + h0 * p.xs[which].h;
+    uint16_t* yrow = p.y[which] + ((static_cast<long long>(b) * p.heads[which] + h0) * p.S + s) * D;
+    for (int h = h0; h < h1; ++h, xrow += p.xs[which].h, yrow += static_cast<long long>(p.S) * D) {
+      ring.wait();
+      float z[2][8], part[2][8];
+      float sq = 0.f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + c * (D / 2) + e0), z[c]);
-      if constexpr (MODE == kRopePart) unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + pc[c]), part[c]);
+      for (int c = 0; c < 2; ++c) {
+        unpack8<BF16>(ring.piece(0, c), z[c]);
+        if constexpr (MODE == kRopePart) unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + pc[c]), part[c]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fmaf(z[c][i], z[c][i], sq);
-    }
-    if constexpr (MODE == kRopePart) __syncwarp();  // a lane's partners are read before they are written (y may be x)
-    const float r = rsqrtf(row_sum<D>(sq) * (1.f / D) + p.eps);
-    if constexpr (NORM) {
+        for (int i = 0; i < 8; ++i) sq = fmaf(z[c][i], z[c][i], sq);
+      }
+      ring.pop();
+      if constexpr (MODE == kRopePart) __syncwarp();  // a lane's partners are read before they are written (y may be x)
+      if constexpr (NORM) {
+        const float r = rsqrtf(row_sum<D>(sq) * (1.f / D) + p.eps);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          z[c][i] *= r * w[c][i];
-          if constexpr (MODE == kRopePart) part[c][i] *= r * wp[c][i];
-        }
-    }
-    rotate<MODE, false>(z, part, rope);
-    if (real) {
-      *reinterpret_cast<uint4*>(yrow + e0) = pack8<BF16>(z[0]);
-      *reinterpret_cast<uint4*>(yrow + D / 2 + e0) = pack8<BF16>(z[1]);
+          for (int i = 0; i < 8; ++i) {
+            z[c][i] *= r * w[c][i];
+            if constexpr (MODE == kRopePart) part[c][i] *= r * wp[c][i];
+          }
+      }
+      rotate<MODE, false>(z, part, rope);
+      if (real) {
+        *reinterpret_cast<uint4*>(yrow + e0) = pack8<BF16>(z[0]);
+        *reinterpret_cast<uint4*>(yrow + D / 2 + e0) = pack8<BF16>(z[1]);
+      }
     }
   }
 }
@@ -123,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_bwd_kernel(const __grid
   constexpr int kLanes = RowCfg<D>::kLanes;
   constexpr int kRowsCta = kThreads / kLanes;
   const int lane_in_row = threadIdx.x % kLanes;
-  const long long tokens = static_cast<long long>(p.B) * p.S;
+  const int tokens = p.B * p.S;
   const int which = blockIdx.y < p.chunks[0] ? 0 : 1;
   const int chunk = blockIdx.y - (which ? p.chunks[0] : 0);
   const int h0 = chunk * p.per_chunk;
@@ -139,39 +153,38 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_bwd_kernel(const __grid
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
   }
-  const RowStrides xs = p.xs[which], dxs = p.dxs[which];
-  for (long long t0 = static_cast<long long>(blockIdx.x) * kRowsCta; t0 < tokens;
-       t0 += static_cast<long long>(gridDim.x) * kRowsCta) {
-    long long t = t0 + threadIdx.x / kLanes;
-    const bool real = t < tokens;
-    if (!real) t = tokens - 1;
-    const int b = static_cast<int>(t / p.S), s = static_cast<int>(t % p.S);
+  const RowStrides dxs = p.dxs[which];
+  const long long dy_head = static_cast<long long>(p.S) * D;
+  using Ring = RowRing<D, NORM ? 2 : 1, kThreads, kStages>;
+  __shared__ typename Ring::Smem ring_smem;
+  const int step = gridDim.x * kRowsCta;
+  Ring ring;
+  ring.base[0] = p.dy[which];
+  ring.strides[0] = {p.heads[which] * dy_head, dy_head, D};
+  if constexpr (NORM) {
+    ring.base[1] = p.x[which];
+    ring.strides[1] = p.xs[which];
+  }
+  ring.start(&ring_smem, p.S, tokens, blockIdx.x * kRowsCta, step, h0, h1);
+  for (int t0 = blockIdx.x * kRowsCta; t0 < tokens; t0 += step) {
+    const bool real = t0 + static_cast<int>(threadIdx.x) / kLanes < tokens;
+    const int t = min(t0 + static_cast<int>(threadIdx.x) / kLanes, tokens - 1);
+    const int b = t / p.S, s = t % p.S;
     LaneRope rope;
     if constexpr (MODE != kRopeNone) load_rope<D, MODE>(rope, table_row(p, b, s), p.rot, lane_in_row);
-    const uint16_t* xrow = p.x[which] + b * xs.b + s * xs.s + h0 * xs.h;
     uint16_t* dxrow = p.dx[which] + b * dxs.b + s * dxs.s + h0 * dxs.h;
-    const uint16_t* dyrow = p.dy[which] + ((static_cast<long long>(b) * p.heads[which] + h0) * p.S + s) * D;
-    // The next head's rows are requested before this one is worked on.
-    uint4 dy_raw[2], x_raw[2];
-    auto request = [&] {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        dy_raw[c] = *reinterpret_cast<const uint4*>(dyrow + c * (D / 2) + e0);
-        if constexpr (NORM) x_raw[c] = *reinterpret_cast<const uint4*>(xrow + c * (D / 2) + e0);
-      }
-    };
-    request();
-    for (int h = h0; h < h1; ++h, dxrow += dxs.h) {
+    [[maybe_unused]] const uint16_t* dyrow =
+        p.dy[which] + ((static_cast<long long>(b) * p.heads[which] + h0) * p.S + s) * D;
+    for (int h = h0; h < h1; ++h, dxrow += dxs.h, dyrow += dy_head) {
+      ring.wait();
       float g[2][8], part[2][8], n[2][8];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        unpack8<BF16>(dy_raw[c], g[c]);
+        unpack8<BF16>(ring.piece(0, c), g[c]);
         if constexpr (MODE == kRopePart) unpack8<BF16>(*reinterpret_cast<const uint4*>(dyrow + pc[c]), part[c]);
-        if constexpr (NORM) unpack8<BF16>(x_raw[c], n[c]);
+        if constexpr (NORM) unpack8<BF16>(ring.piece(1, c), n[c]);
       }
-      xrow += xs.h;
-      dyrow += static_cast<long long>(p.S) * D;
-      if (h + 1 < h1) request();
+      ring.pop();
       rotate<MODE, true>(g, part, rope);
       if constexpr (NORM) {
         float sq = 0.f;
@@ -311,8 +324,11 @@ int launch_fwd(const NormRopeArgs& a) {
   int per = 8;
   while (per > 1 && token_ctas * (heads / per) < 32LL * a.num_sms) per /= 2;
   set_chunks(p, per);
-  if (token_ctas > 0x7FFFFFFFLL || p.chunks[0] + p.chunks[1] > 65535) return -1;
-  const dim3 grid(static_cast<unsigned>(token_ctas), p.chunks[0] + p.chunks[1]);
+  const int chunks = p.chunks[0] + p.chunks[1];
+  if (chunks > 65535) return -1;
+  long long x = (kFwdCtas * static_cast<long long>(a.num_sms) + chunks - 1) / chunks;
+  if (x > token_ctas) x = token_ctas;
+  const dim3 grid(static_cast<unsigned>(x), chunks);
   return with_mode(a, [&](auto mode, auto norm) {
     norm_rope_kernel<D, BF16, decltype(mode)::value, decltype(norm)::value><<<grid, kThreads, 0, a.stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
@@ -331,8 +347,8 @@ int launch_bwd(const NormRopeArgs& a) {
   while ((most + per - 1) / per > kMaxBwdCtas) per *= 2;
   set_chunks(p, per);
   const int most_chunks = p.chunks[0] > p.chunks[1] ? p.chunks[0] : p.chunks[1];
-  // CTAs over tokens: eight for each SM in all, and no more partials than fit.
-  long long x = (8LL * a.num_sms + p.chunks[0] + p.chunks[1] - 1) / (p.chunks[0] + p.chunks[1]);
+  // CTAs over tokens: sixteen for each SM in all, and no more partials than fit.
+  long long x = (16LL * a.num_sms + p.chunks[0] + p.chunks[1] - 1) / (p.chunks[0] + p.chunks[1]);
   if (x > kMaxBwdCtas / most_chunks) x = kMaxBwdCtas / most_chunks;
   if (x > token_ctas) x = token_ctas;
   const dim3 grid(static_cast<unsigned>(x), p.chunks[0] + p.chunks[1]);

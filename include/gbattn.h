@@ -378,8 +378,8 @@ size_t attn_decode_noalloc_scratch_bytes(void);
  *   q_out [B, H, S, d], k_out [B, Hkv, S, d]  dtype, outputs, contiguous;
  *            q_out may be q and k_out k where those are contiguous
  *
- * Errors: GBATTN_EBADSHAPE (also H > 16384), EHEADS, EHEADDIM, EDTYPE, EPAGE
- * (rot_dim), EPOINTER (also strides that are no multiples of 8, one weight
+ * Errors: GBATTN_EBADSHAPE (also H > 16384 or B * S > 2^30), EHEADS, EHEADDIM,
+ * EDTYPE, EPAGE (rot_dim), EPOINTER (also strides that are no multiples of 8, one weight
  * without the other, and neither norm nor rotation), EUNSUPPORTED, ELAUNCH.
  */
 int attn_qk_norm_rope(const void *q, const void *k, const float *q_weight, const float *k_weight,
@@ -437,8 +437,8 @@ int attn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q,
  * The slots that one call writes are distinct (pages that several sequences
  * share are for reading).  All other slots stay as they are.
  *
- * Errors: GBATTN_EBADSHAPE (also H > 16384), EHEADS, EHEADDIM, EDTYPE, EPAGE
- * (page_size or rot_dim), EPOINTER, EUNSUPPORTED, ELAUNCH.
+ * Errors: GBATTN_EBADSHAPE (also H > 16384 or B * S > 2^30), EHEADS, EHEADDIM,
+ * EDTYPE, EPAGE (page_size or rot_dim), EPOINTER, EUNSUPPORTED, ELAUNCH.
  */
 int attn_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
                       const int *page_table, const int *seqlens, const int *new_lens,
