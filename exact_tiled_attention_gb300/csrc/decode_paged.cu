@@ -288,20 +288,27 @@ struct Stage {
     if constexpr (D == 64) return key * kRow + byte;
     return (key >> 1) * 128 + ((((key & 1) << 2 | byte >> 4) ^ ((key >> 1 & 3) << 1)) << 4) + (byte & 15);
   }
-  static constexpr int kPieces = kFactors;  // 16-byte pieces of 16 rows' factors of K (and of V)
-  // All 16 rows of a block (a page holds whole blocks).
-  __device__ static __forceinline__ void fill(const LanePtrs& a, uint32_t stage, int block, int lane) {
-    const uint8_t* k = a.data[0] + static_cast<long long>(block) * kV;
-    const uint8_t* v = a.data[1] + static_cast<long long>(block) * kV;
+  static constexpr int kPieces = 2 * kFactors;  // 16-byte pieces of a block's factors, K's and then V's
+  // A unit's two blocks of 16 rows each (a page holds whole blocks).  Every lane
+  // copies in every instruction: 2 kPieces lanes have the factors of both blocks,
+  // and at D = 64 the other half copies the same pieces once more.
+  __device__ static __forceinline__ void fill(const LanePtrs& a, uint32_t stage, const int (&block)[2], int lane) {
     const int byte = lane * 16;
-    const uint32_t to_k = stage + byte, to_v = stage + kV + v_offset(byte / kRow, byte % kRow);
 #pragma unroll
-    for (int i = 0; i < kV / 512; ++i) {  // 512 bytes on: 8 keys on, where the pieces lie alike
-      copy16(to_k + i * 512, k + i * 512);
-      copy16(to_v + i * 512, v + i * 512);
+    for (int k = 0; k < 2; ++k) {
+      const uint8_t* ks = a.data[0] + static_cast<long long>(block[k]) * kV;
+      const uint8_t* vs = a.data[1] + static_cast<long long>(block[k]) * kV;
+      const uint32_t to_k = stage + k * kBytes + byte;
+      const uint32_t to_v = stage + k * kBytes + kV + v_offset(byte / kRow, byte % kRow);
+#pragma unroll
+      for (int i = 0; i < kV / 512; ++i) {  // 512 bytes on: 8 or 16 keys on, where the pieces lie alike
+        copy16(to_k + i * 512, ks + i * 512);
+        copy16(to_v + i * 512, vs + i * 512);
+      }
     }
-    if (lane < 2 * kPieces)
-      copy16(stage + kKf + byte, a.factor + static_cast<long long>(block) * (16 * kFactors));
+    const int which = lane / kPieces & 1;
+    copy16(stage + which * kBytes + kKf + lane % kPieces * 16,
+           a.factor + static_cast<long long>(which ? block[1] : block[0]) * (16 * kFactors));
   }
 };
 
@@ -319,7 +326,8 @@ struct Tile<D, kFp4> {
     LanePtrs a;
     a.data[0] = p.data[0] + lane * 16;
     a.data[1] = p.data[1] + lane * 16;
-    a.factor = p.factor[lane / Stage<D>::kPieces & 1] + lane % Stage<D>::kPieces * 16;
+    const int piece = lane % Stage<D>::kPieces;  // of a block's factors, as Stage::fill copies them
+    a.factor = p.factor[piece / Stage<D>::kFactors] + piece % Stage<D>::kFactors * 16;
     return a;
   }
   __device__ __forceinline__ void load_k(uint32_t stage, int lane) {
@@ -650,15 +658,18 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
     const int whole_end = (warp_keys + UK - 16 * KB) / UK;  // units before it have all of the warp's keys
     const int block_shift = p.page_shift - 4;               // log2 of a page's blocks
     const int head_block = kvh << block_shift, page_blocks = p.Hkv << block_shift;
-    // Page of a block of the sequence (behind the last: any), and the pool's
-    // block, or -1 for a page that does not exist: its keys are left out.
-    auto page_of = [&](int blk) { return 16 * blk < L ? __ldg(pages + (blk >> block_shift)) : 0; };
-    auto block_of = [&](int blk, int page) {
-      if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) {
-        if (lane == 0) atomicCAS(p.status, 0, kStatusIndex);
-        return -1;
-      }
+    const int last_block = (L - 1) >> 4;
+    // Page of a block of the sequence (behind the last: the last one's), and the
+    // pool's block, or -1 for a page that does not exist: its keys are left out.
+    auto page_of = [&](int blk) { return __ldg(pages + (min(blk, last_block) >> block_shift)); };
+    auto exists = [&](int page) { return static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages); };
+    auto block_at = [&](int blk, int page) {
       return page * page_blocks + head_block + (blk & ((1 << block_shift) - 1));
+    };
+    auto block_of = [&](int blk, int page) {
+      if (exists(page)) return block_at(blk, page);
+      if (lane == 0) atomicCAS(p.status, 0, kStatusIndex);
+      return -1;
     };
     if constexpr (FMT == kFp4) {
       // kStages - 1 units are on their way while one is worked on.
@@ -668,13 +679,17 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
         absent <<= 2;
         if (i < end) {
           const int blk = (i * kWarps + warp) * KB;
-          const int b0 = block_of(blk, page0), b1 = block_of(blk + 1, page1);
-          const int next = blk + kWarps * KB;
-          page0 = page_of(next);
-          page1 = block_shift > 0 ? page0 : page_of(next + 1);
-          if (b0 >= 0) Stage<D>::fill(src, stage, b0, lane);
-          if (b1 >= 0) Stage<D>::fill(src, stage + Stage<D>::kBytes, b1, lane);
-          absent |= (b0 < 0 ? 1u : 0u) | (b1 < 0 ? 2u : 0u);
+          int block[KB] = {block_at(blk, page0), block_at(blk + 1, page1)};
+          if (!exists(page0) || !exists(page1)) {
+            if (lane == 0) atomicCAS(p.status, 0, kStatusIndex);
+            absent |= (exists(page0) ? 0u : 1u) | (exists(page1) ? 0u : 2u);
+            // What is copied instead does not matter.
+            if (!exists(page0)) block[0] = 0;
+            if (!exists(page1)) block[1] = 0;
+          }
+          page0 = page_of(blk + kWarps * KB);
+          page1 = block_shift > 0 ? page0 : page_of(blk + kWarps * KB + 1);
+          Stage<D>::fill(src, stage, block, lane);
         }
         copy_commit();
       };
