@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
   __shared__ long long sm_scan[kWarps + 1];
   __shared__ int sm_b;
   __shared__ long long sm_before;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int r = lane >> 2, q4 = lane & 3;
   let_next_kernel_start();
   const int HG = p.Hkv * p.groups;
