@@ -47,7 +47,7 @@ int check_cache(CacheArgs* out, const void* k, const void* v, const void* k_fact
   if (Hkv < 1 || n_pages < 1 || max_pages < 1) return GBATTN_EBADSHAPE;
   if (d != 64 && d != 128) return GBATTN_EHEADDIM;
   if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1))) return GBATTN_EPAGE;
-  if (static_cast<long long>(max_pages) * page_size > 0x7FFFFFFFLL - 64) return GBATTN_EBADSHAPE;
+  if (static_cast<long long>(max_pages) * page_size > 0x7FFFFFFFLL - 256) return GBATTN_EBADSHAPE;
   // The kernels count blocks of 16 tokens of one head in 32 bits.
   if (static_cast<long long>(n_pages) * Hkv > (0x7FFFFFFFLL << 4) / page_size) return GBATTN_EBADSHAPE;
   if (!k || !v || !page_table || !seqlens || misaligned16(k) || misaligned16(v) || misaligned4(page_table) ||
@@ -146,7 +146,7 @@ int gather(const void* k_cache, const void* k_factors, const void* v_cache, cons
            const float* k_descale, const float* v_descale, const int* page_table, const int* seqlens, void* k_out,
            void* v_out, int B, int Hkv, int S, int d, int page_size, int n_pages, int max_pages, int dtype,
            void* stream) {
-  if (B < 1 || Hkv < 1 || S < 1 || static_cast<long long>(B) * Hkv > 65535) return GBATTN_EBADSHAPE;
+  if (B < 1 || Hkv < 1 || S < 1 || S > 0x40000000 || static_cast<long long>(B) * Hkv > 65535) return GBATTN_EBADSHAPE;
   GatherArgs a{};
   int rc = check_cache(&a.cache, k_cache, v_cache, k_factors, v_factors, fp4, k_descale, v_descale, page_table,
                        seqlens, Hkv, d, page_size, n_pages, max_pages);

@@ -14,6 +14,7 @@
 
 #include <climits>
 #include <cmath>
+#include <optional>
 #include <sstream>
 #include <string>
 
@@ -191,16 +192,30 @@ int truth(PyObject* o) {
   return v;
 }
 
-// The caller's stream (a torch stream or a raw handle), or the device's current one.
-void* stream_of(PyObject* o, const c10::Device& device) {
-  if (none(o)) return c10::cuda::getCurrentCUDAStream(device.index()).stream();
-  PyObject* handle = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : Py_NewRef(o);
-  if (handle == nullptr) throw python_error();
-  void* s = PyLong_AsVoidPtr(handle);
-  Py_DECREF(handle);
-  if (s == nullptr && PyErr_Occurred()) throw python_error();
-  return s;
-}
+// Makes the call's device current, and the caller's stream (a torch stream or a
+// raw handle) where one is given: what is allocated for the call then belongs to
+// the stream that it runs on, so a workspace that is released on return is not
+// handed out again before the kernels are through with it.
+struct Target {
+  c10::cuda::CUDAGuard device;
+  std::optional<c10::cuda::CUDAStreamGuard> guard;
+  void* stream;
+
+  Target(PyObject* o, const c10::Device& d) : device(d) {
+    if (none(o)) {
+      stream = c10::cuda::getCurrentCUDAStream(d.index()).stream();
+      return;
+    }
+    PyObject* handle = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : Py_NewRef(o);
+    if (handle == nullptr) throw python_error();
+    stream = PyLong_AsVoidPtr(handle);
+    Py_DECREF(handle);
+    if (stream == nullptr && PyErr_Occurred()) throw python_error();
+    guard.emplace(stream == nullptr
+                      ? c10::cuda::getDefaultCUDAStream(d.index())
+                      : c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), d.index()));
+  }
+};
 
 void done(int rc, const char* name) {
   if (rc == GBATTN_OK) return;
@@ -262,19 +277,20 @@ struct NormRope {
 
 PyObject* norm_rope(PyObject* const* a) {
   NormRope n(a[0], a[1], a[2], a[3], a[4], a[5]);
+  const Target target(a[10], n.f.device);
   Output q_out, k_out;
   q_out.take(a[8], "q_out", n.q_shape, n.f.type, n.f.device);
   k_out.take(a[9], "k_out", n.k_shape, n.f.type, n.f.device);
-  c10::cuda::CUDAGuard guard(n.f.device);
   done(attn_qk_norm_rope(n.q.data, n.k.data, n.q_weight, n.k_weight, n.rope.table, n.positions, q_out.data, k_out.data,
                          n.B, n.H, n.Hkv, n.S, n.d, n.q.stride(), n.k.stride(), static_cast<float>(number(a[6])),
-                         n.rope.rows, n.rope.rot, truth(a[7]), n.f.code, stream_of(a[10], n.f.device)),
+                         n.rope.rows, n.rope.rot, truth(a[7]), n.f.code, target.stream),
        "attn_qk_norm_rope");
   return tuple({&q_out, &k_out});
 }
 
 PyObject* norm_rope_bwd(PyObject* const* a) {
   NormRope n(a[2], a[3], a[4], a[5], a[6], a[7]);
+  const Target target(a[15], n.f.device);
   const void* dqo = ptr(a[0], "dq_out", n.q_shape, n.f.type, n.f.device);
   const void* dko = ptr(a[1], "dk_out", n.k_shape, n.f.type, n.f.device);
   Output dq, dk, dqw, dkw;
@@ -299,12 +315,11 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
     dkw.take(a[14], "dk_weight", {n.d}, at::kFloat, n.f.device);
     ws.take(a[10], attn_qk_norm_rope_bwd_workspace_bytes(n.d), n.f.device);
   }
-  c10::cuda::CUDAGuard guard(n.f.device);
   done(attn_qk_norm_rope_bwd(dqo, dko, n.q.data, n.k.data, n.q_weight, n.k_weight, n.rope.table, n.positions,
                              dq_rows.data, dk_rows.data, static_cast<float*>(dqw.data), static_cast<float*>(dkw.data),
                              n.B, n.H, n.Hkv, n.S, n.d, n.q.stride(), n.k.stride(), dq_rows.stride(), dk_rows.stride(),
                              static_cast<float>(number(a[8])), n.rope.rows, n.rope.rot, truth(a[9]), ws.data, ws.bytes,
-                             n.f.code, stream_of(a[15], n.f.device)),
+                             n.f.code, target.stream),
        "attn_qk_norm_rope_bwd");
   return tuple({&dq, &dk, &dqw, &dkw});
 }
@@ -358,6 +373,7 @@ PyObject* append(const First& f, const Tensor& kt, PyObject* ko, PyObject* vo, c
   const Rows k = rows(ko, "k", kt.sizes(), f), v = rows(vo, "v", kt.sizes(), f);
   const int B = size(kt.size(0), "k"), Hkv = size(kt.size(1), "k"), S = size(kt.size(2), "k");
   const int d = size(kt.size(3), "k");
+  const Target target(stream, f.device);
   int H = Hkv;
   Rows q;
   Output out;
@@ -372,8 +388,7 @@ PyObject* append(const First& f, const Tensor& kt, PyObject* ko, PyObject* vo, c
   }
   const int* n = static_cast<const int*>(opt(new_lens, "new_lens", {B}, at::kInt, f.device));
   const Rope rope(rope_o, f.device);
-  c10::cuda::CUDAGuard guard(f.device);
-  void* s = stream_of(stream, f.device);
+  void* s = target.stream;
   const int il = truth(interleaved);
   if (fp4)
     done(attn_cache_append_fp4(k.data, v.data, c.k, c.k_factors, c.v, c.v_factors, c.k_descale, c.v_descale, c.table,
@@ -416,12 +431,12 @@ PyObject* cache_gather(PyObject* const* a) {
   const Cache c(a[0], a[1], a[2], a[3], B, kt.size(1), kt.size(3), f);
   const int S = tokens(a[4]);
   const int64_t shape[4] = {B, kt.size(1), S, kt.size(3)};
+  const Target target(a[7], f.device);
   Output k, v;
   k.take(a[5], "k_out", shape, f.type, f.device);
   v.take(a[6], "v_out", shape, f.type, f.device);
-  c10::cuda::CUDAGuard guard(f.device);
   done(attn_cache_gather(c.k, c.v, c.table, c.lens, k.data, v.data, size(B, "seqlens"), size(shape[1], "k_cache"), S,
-                         size(shape[3], "k_cache"), c.page, c.n_pages, c.max_pages, f.code, stream_of(a[7], f.device)),
+                         size(shape[3], "k_cache"), c.page, c.n_pages, c.max_pages, f.code, target.stream),
        "attn_cache_gather");
   return tuple({&k, &v});
 }
@@ -436,13 +451,13 @@ PyObject* cache_gather_fp4(PyObject* const* a) {
   const Cache c(a, a[7], a[8], B, kt.size(1), kt.size(3) * 2, f.device);
   const int S = tokens(a[6]);
   const int64_t shape[4] = {B, kt.size(1), S, kt.size(3) * 2};
+  const Target target(a[12], f.device);
   Output k, v;
   k.take(a[10], "k_out", shape, f.type, f.device);
   v.take(a[11], "v_out", shape, f.type, f.device);
-  c10::cuda::CUDAGuard guard(f.device);
   done(attn_cache_gather_fp4(c.k, c.k_factors, c.v, c.v_factors, c.k_descale, c.v_descale, c.table, c.lens, k.data,
                              v.data, size(B, "seqlens"), size(shape[1], "k_codes"), S, size(shape[3], "k_codes"), c.page,
-                             c.n_pages, c.max_pages, f.code, stream_of(a[12], f.device)),
+                             c.n_pages, c.max_pages, f.code, target.stream),
        "attn_cache_gather_fp4");
   return tuple({&k, &v});
 }
@@ -454,6 +469,7 @@ PyObject* decode(const First& f, PyObject* qo, int64_t Hkv, const Cache& c, PyOb
   const void* q_ptr = ptr(qo, "q", q.sizes(), f.type, f.device);
   const int B = size(q.size(0), "q"), H = size(q.size(1), "q"), d = size(q.size(3), "q"), hkv = size(Hkv, "the cache");
   const int64_t cap = static_cast<int64_t>(c.page) * c.max_pages;
+  const Target target(stream, f.device);
   Workspace ws;
   ws.take(workspace, attn_decode_paged_workspace_bytes(B, H, hkv, d, static_cast<int>(cap < INT_MAX ? cap : INT_MAX)),
           f.device);
@@ -461,8 +477,7 @@ PyObject* decode(const First& f, PyObject* qo, int64_t Hkv, const Cache& c, PyOb
   out.take(out_o, "out", q.sizes(), f.type, f.device);
   if (!none(lse_o) || truth(return_lse)) lse.take(lse_o, "lse", {B, H}, at::kFloat, f.device);
   const float scale = static_cast<float>(none(scale_o) ? 1.0 / std::sqrt(static_cast<double>(d)) : number(scale_o));
-  c10::cuda::CUDAGuard guard(f.device);
-  void* s = stream_of(stream, f.device);
+  void* s = target.stream;
   if (fp4)
     done(attn_decode_paged_fp4(q_ptr, c.k, c.k_factors, c.v, c.v_factors, c.k_descale, c.v_descale, c.table, c.lens,
                                out.data, static_cast<float*>(lse.data), B, H, hkv, d, c.page, c.n_pages, c.max_pages,

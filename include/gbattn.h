@@ -339,7 +339,8 @@ size_t attn_decode_noalloc_scratch_bytes(void);
  *            bytes, one for each 16 elements of a row;
  *            k_descale, v_descale [Hkv] fp32 or NULL (1).  An element is
  *            code * factor * descale[head].
- *   page_table [B, max_pages] int32; entries behind a sequence's last page
+ *   page_table [B, max_pages] int32 (max_pages * page_size < 2^31 - 256 and
+ *            n_pages * Hkv * page_size / 16 < 2^31); entries behind a sequence's last page
  *            are not read.  seqlens [B] int32: tokens of each sequence, 0 for
  *            an idle one; values are clamped into [0, max_pages * page_size].
  * Both are device arrays, read when the kernels run, so a captured graph
@@ -475,8 +476,8 @@ int attn_cache_append_fp4(const void *k, const void *v, void *k_codes, void *k_f
  * attn_cache_gather_fp4 -- the same from a 4-bit cache: (code * factor) *
  * descale in fp32, rounded once to dtype.
  *
- * Errors: GBATTN_EBADSHAPE (also B * Hkv > 65535), EHEADDIM, EDTYPE, EPAGE,
- * EPOINTER, EUNSUPPORTED, ELAUNCH.
+ * Errors: GBATTN_EBADSHAPE (also B * Hkv > 65535 or S > 2^30), EHEADDIM,
+ * EDTYPE, EPAGE, EPOINTER, EUNSUPPORTED, ELAUNCH.
  */
 int attn_cache_gather(const void *k_cache, const void *v_cache, const int *page_table,
                       const int *seqlens, void *k_out, void *v_out, int B, int Hkv, int S, int d,

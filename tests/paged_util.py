@@ -10,9 +10,11 @@ that of one fp32 operation.  Every bound below counts roundings:
   steps (20 U32 of the sum, half of it in the root), rsqrt within 2 units,
   three products: below 16 U32 of each operand of the rotation, so with the
   rotation 20 U32 (|a c| + |b s|);
-* attention: P is rounded to 16 bits before P V: u sum p |v| (and, for fp16
-  P, 2^-25 |v| for each term below the smallest normal number, the largest p
-  being 1); O rounds once more: u |o|.  A score is a sum of d exact products,
+* attention: P is rounded before P V, to one fp16 over a 4-bit cache (u(fp16)),
+  to two terms of the cache's type over a 16-bit one (u^2: the second term
+  rounds the first's remainder): that times sum p |v|, and, with fp16 terms,
+  2^-25 |v| for each term below the smallest normal number, the largest p
+  being 1.  O rounds once more: u |o|.  A score is a sum of d exact products,
   each add of the tensor core within 2 U32 of the running magnitude:
   e = 2 d U32 scale sum |q k|, a relative error of p.  exp2, its argument and
   the rescalings: below 2^-20 of p together.
@@ -106,11 +108,12 @@ def sequence(pool, table_row, page, n):
     return pool[pages].transpose(0, 1).flatten(1, 2)[:, :n]
 
 
-def attention(q, k, v, scale, half_p, extra_k=0.0):
+def attention(q, k, v, scale, half_p, extra_k=0.0, fp16_p=False):
     """One sequence's decode in 64 bits.  q [Hq, d], k and v [Hkv, n, d].
     Returns o, lse and the bounds of their errors before o's last rounding,
-    where P is rounded to a type of half step half_p (2^-11: fp16).  extra_k:
-    error of an element of q relative to its row's largest."""
+    where P's rounding is off by half_p at most, relative to p (fp16_p: it has
+    fp16's smallest numbers too).  extra_k: error of an element of q relative to
+    its row's largest."""
     Hq, d = q.shape
     Hkv, n, _ = k.shape
     if n == 0:
@@ -128,6 +131,6 @@ def attention(q, k, v, scale, half_p, extra_k=0.0):
     o = torch.einsum("hn,hnd->hd", p, vv)
     a = torch.einsum("hn,hnd->hd", p, vv.abs())
     tol = (half_p + 2 * e) * a
-    if half_p == 2.0 ** -11:
+    if fp16_p:
         tol = tol + 2.0 ** -25 * vv.abs().sum(1)
     return o, lse, tol, e[:, 0] + lse.abs() * 4 * U32 + 2.0 ** -20

@@ -43,6 +43,7 @@ def test_norm_rope_refusals(lib):
     for name in ("B", "H", "Hkv", "S"):
         assert _norm(lib, **{name: 0}) == -1
     assert _norm(lib, H=16386) == -1
+    assert _norm(lib, B=1 << 15, S=(1 << 15) + 1, rows=1 << 16) == -1  # more tokens than 2^30
     assert _norm(lib, H=5) == -2
     for d in (0, 32, 96, 256):
         assert _norm(lib, d=d) == -3
@@ -121,6 +122,7 @@ def test_cache_refusals(lib, name, fp4):
     for field in ("B", "Hkv", "n", "width") + (("S",) if "S" in DEFAULTS[name] else ()):
         assert call(**{field: 0}) == -1, field
     assert call(width=1 << 27, page=16) == -1  # more slots than an int counts
+    assert call(n=1 << 30, page=64) == -1      # more blocks of 16 slots
     assert call(d=96) == -3 and call(d=256) == -3
     assert call(dtype=5) == -4
     for page in (0, 8, 24, 48, 2048):
@@ -134,14 +136,14 @@ def test_cache_refusals(lib, name, fp4):
     if fp4:
         assert call(kd=FAKE + 1) == -5
     if name == "attn_cache_append":
-        assert call(H=5) == -2 and call(H=16386) == -1
+        assert call(H=5) == -2 and call(H=16386) == -1 and call(B=1 << 15, S=1 << 16) == -1
         assert call(q=None) == -5 and call(qo=None) == -5  # one without the other
         assert call(rope=None) == -5 and call(rows=0) == -1 and call(rot=20) == -11
         assert call(new=FAKE + 1) == -5
         for s in ("qs", "ks", "vs"):
             assert call(**{s: _strides(8, 16, 4)}) == -5
     if name == "attn_cache_gather":
-        assert call(B=1 << 15, Hkv=2) == -1
+        assert call(B=1 << 15, Hkv=2) == -1 and call(S=(1 << 30) + 1) == -1
     if name == "attn_decode_paged":
         assert call(Hq=5) == -2 and call(B=65536) == -1
         need = lib.attn_decode_paged_workspace_bytes(2, 4, 2, 128, 32)

@@ -74,11 +74,13 @@ def _same_bits(a, b):
 
 def _decode_ok(pool, q, table, lens, o, lse, scale, what=""):
     o, lse = o.double().cpu(), lse.double().cpu()
-    half_p = pu.u(torch.float16) if pool.bits == 4 else pu.u(pool.dtype)
+    half_p = pu.u(torch.float16) if pool.bits == 4 else pu.u(pool.dtype) ** 2
+    fp16_p = pool.bits == 4 or pool.dtype is torch.float16
     for b, n in enumerate(lens):
         k, v = pool.values(0, table[b], n), pool.values(1, table[b], n)
         # 4 bits: q is scaled into fp16, off by up to 2^-24 of its row's largest
-        ro, rl, to, tl = pu.attention(q[b, :, 0].cpu(), k, v, scale, half_p, 2.0 ** -24 if pool.bits == 4 else 0.0)
+        ro, rl, to, tl = pu.attention(q[b, :, 0].cpu(), k, v, scale, half_p, 2.0 ** -24 if pool.bits == 4 else 0.0,
+                                      fp16_p)
         tol = to + pu.u(q.dtype) * (ro.abs() + to) + 2.0 ** -25
         assert torch.isfinite(o[b]).all(), f"{what} sequence {b}"
         bad = (o[b, :, 0] - ro).abs() - tol
@@ -223,7 +225,7 @@ def test_pages_that_do_not_exist(bits):
         assert gb.gbattn_device_status() == GBATTN_EINDEX and gb.gbattn_device_status() == 0
         keep = [i for i in range(100) if i // page != 2]
         k, v = (pool.values(i, table[0], 100)[:, keep] for i in range(2))
-        ro, rl, to, tl = pu.attention(q[0, :, 0].cpu(), k, v, 0.125, pu.u(torch.float16), 2.0 ** -24)
+        ro, rl, to, tl = pu.attention(q[0, :, 0].cpu(), k, v, 0.125, pu.u(torch.float16), 2.0 ** -24, True)
         assert ((o[0, :, 0].double().cpu() - ro).abs() <= to + pu.u(torch.float16) * (ro.abs() + to) + 2.0 ** -25).all()
         assert ((lse[0].double().cpu() - rl).abs() <= tl).all()
         kk, vv = pool.gather(t.cuda(), _i32(lens), 100)
@@ -379,7 +381,7 @@ def test_offsets_beyond_32_bits():
     assert gb.gbattn_device_status() == 0
     for b, n in enumerate(lens):
         ro, rl, to, tl = pu.attention(q[b, :, 0], ka[b, :, :n].cpu(), va[b, :, :n].cpu(), 1 / math.sqrt(d),
-                                      pu.u(torch.bfloat16))
+                                      pu.u(torch.bfloat16) ** 2)
         assert ((o[b, :, 0].double().cpu() - ro).abs() <= to + pu.u(torch.bfloat16) * (ro.abs() + to)).all()
         assert ((lse[b].double().cpu() - rl).abs() <= tl).all()
 
@@ -443,6 +445,35 @@ def test_streams_graphs_and_two_calls_at_once(bits):
         for a, b in zip(outs, refs):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     assert gb.gbattn_device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_a_given_stream_owns_what_the_call_allocates(bits):
+    """Work queued on the current stream right after a call on another one gets
+    none of that call's memory: the decode's workspace and outputs are untouched
+    by fills of the same sizes, while the other stream is still busy."""
+    g = torch.Generator().manual_seed(46)
+    page, Hq, Hkv, d, B = 64, 8, 2, 128, 3
+    pool = Pool(bits, 40, Hkv, page, d, torch.bfloat16, g)
+    lens = [700, 33, 512]
+    table = pu.page_table(lens, page, 40, 11, g).cuda()
+    q = torch.randn(B, Hq, 1, d, generator=g).bfloat16().cuda()
+    sl = _i32(lens)
+    ref = pool.decode(q, table, sl)
+    side = torch.cuda.Stream()
+    need = gb.attn_decode_paged_workspace_bytes(B, Hq, Hkv, d, 11 * page)
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                busy @ busy
+        o, lse = pool.decode(q, table, sl, stream=stream)
+        fills = [torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+                 for n in (need, need, q.numel() * 2, B * Hq * 4) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+        assert all((f == 255).all() for f in fills)
 
 
 def test_wrapper_refusals():
@@ -527,7 +558,8 @@ def test_a_prompt_in_chunks_and_then_tokens(bits):
                 kv = [pool.values(i, table_h[b], n) for i in range(2)]
                 if S > 1:  # what attn_fwd read: the values rounded to 16 bits
                     kv = [x.to(dtype).float() for x in kv]
-                ro, rl, to, tl = pu.attention(qn[b, :, t].cpu(), *kv, scale, pu.u(dtype), 2.0 ** -24)
+                half_p = pu.u(dtype) if S > 1 else pu.u(torch.float16) if bits == 4 else pu.u(dtype) ** 2
+                ro, rl, to, tl = pu.attention(qn[b, :, t].cpu(), *kv, scale, half_p, 2.0 ** -24, bits == 4)
                 err = (o[b, :, t].double().cpu() - ro).abs()
                 assert (err <= to + pu.u(dtype) * (ro.abs() + to)).all(), f"{S} tokens, query {t}: {err.max():.3e}"
                 got = lse[b].view(H, -1)[:, t].double().cpu()
