@@ -93,6 +93,20 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   const int n_new = p.new_lens != nullptr ? min(p.new_lens[b], p.S) : p.S;
   const long long pos = static_cast<long long>(p.seqlens[b]) - n_new + i;
   const bool real = in_grid && i < n_new && pos >= 0;  // else padding
+  if (which != 0 && __all_sync(0xffffffffu, !real)) return;  // nothing to store
+  const RowStrides xs = p.xs[which];
+  const uint16_t* xrow = p.x[which] + b * xs.b + i * xs.s + h0 * xs.h;
+  // Rows are requested two heads ahead, the first ones before the page and the
+  // angles are looked up; padding is not read.
+  uint4 raw[2][2] = {};
+  auto request = [&](int k, const uint16_t* row) {
+    if (real) {
+      raw[k][0] = *reinterpret_cast<const uint4*>(row + e0);
+      raw[k][1] = *reinterpret_cast<const uint4*>(row + D / 2 + e0);
+    }
+  };
+  request(0, xrow);
+  if (h0 + 1 < h1) request(1, xrow + xs.h);
   bool stored = real;
   long long slot = 0;  // row of head 0 of the token's page
   if (real && which != 0) {
@@ -119,25 +133,13 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
         for (int c = 0; c < 2; ++c) pc[c] = partner_chunk(c * (D / 2) + e0, p.rot);
     }
   }
-  const RowStrides xs = p.xs[which];
-  const uint16_t* xrow = p.x[which] + b * xs.b + i * xs.s + h0 * xs.h;
-  // Rows that nothing is stored of are not read; a warp without others is done.
-  const bool read = which == 0 ? real : stored;
-  if (which != 0 && __all_sync(0xffffffffu, !read)) return;
-  // The next head's row is requested before this one is worked on.
-  uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  auto request = [&](const uint16_t* row) {
-    if (read) {
-      raw[0] = *reinterpret_cast<const uint4*>(row + e0);
-      raw[1] = *reinterpret_cast<const uint4*>(row + D / 2 + e0);
-    }
-  };
-  request(xrow);
   for (int h = h0; h < h1; ++h, xrow += xs.h) {
     float z[2][8], part[2][8];
-    unpack8<BF16>(raw[0], z[0]);
-    unpack8<BF16>(raw[1], z[1]);
-    if (h + 1 < h1) request(xrow + xs.h);
+    unpack8<BF16>(raw[0][0], z[0]);
+    unpack8<BF16>(raw[0][1], z[1]);
+    raw[0][0] = raw[1][0];
+    raw[0][1] = raw[1][1];
+    if (h + 2 < h1) request(1, xrow + 2 * xs.h);
     if constexpr (MODE != kRopeNone) {
       if (which != 2) {
         if constexpr (MODE == kRopePart) {
