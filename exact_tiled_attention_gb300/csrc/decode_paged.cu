@@ -418,6 +418,14 @@ template <int FMT>
 constexpr int kBlocks = FMT == kFp4 ? 2 : 1;
 template <int FMT>
 constexpr int kUnitKeys = 16 * kBlocks<FMT> * kWarps;
+// Units of work that a segment's fixed part (its first pages and rows, Q, the
+// merge of the warps) counts as when the list is divided; without it the CTAs
+// whose run holds many short sequences end last.  64 sequences of 1024 to 32768
+// tokens, 0 against this: 4 bits and 8 heads a unit 247 -> 235 us (1: 240, 5:
+// 238), 16 heads 350 -> 309; 16 bits and 8 heads 683 -> 684 (3: 683), 16 heads
+// 772 -> 752 (5: 752).
+template <int FMT, int NT>
+constexpr int kSegmentCost = (FMT == kFp4 ? 3 : 1) + 2 * (NT - 1);
 
 // Scores s of KB blocks of 16 keys (in units of the products) to P as the operand
 // of P V, and the state (m, l, o) brought up to them.  A block's keys from
@@ -516,11 +524,17 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
 
   // ---- this CTA's run of units, [u0, u1) of U, and the sequence that holds u0
   long long U, N, u0, u1, rem;
-  int b;
+  int b, cost;
   {
-    // Tiles of the first kThreads sequences, scanned; then of all of them.
-    auto tiles_of = [&](int i) { return i < p.B ? (seq_len(p, i) + UK - 1) / UK : 0; };
-    auto scan = [&](int n, long long before, long long& all) {
+    // Tiles of a sequence and, in the upper bits, whether it has any: summed up,
+    // tiles and sequences with keys.
+    constexpr int kShift = 44;
+    auto tiles_of = [&](int i) {
+      const int n = i < p.B ? (seq_len(p, i) + UK - 1) / UK : 0;
+      return n > 0 ? (1ll << kShift) + n : 0ll;
+    };
+    auto units_of = [&](long long x) { return (x & ((1ll << kShift) - 1)) + cost * (x >> kShift); };
+    auto scan = [&](long long n, long long before, long long& all) {
       long long incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -538,37 +552,39 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
       }
       return incl;
     };
-    int i = threadIdx.x, n = tiles_of(i);
-    long long upto, tiles;  // tiles of sequences 0 .. i; of all
+    // The first kThreads sequences are scanned, the others summed.
+    int i = threadIdx.x;
+    long long n = tiles_of(i), upto;
     const long long first = scan(n, 0, upto);
-    tiles = upto;
+    long long total = upto;
     if (p.B > kThreads) {
-      long long mine = 0, all;
+      long long mine = 0;
       for (int j = i + kThreads; j < p.B; j += kThreads) mine += tiles_of(j);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
       __syncthreads();
       if (lane == 0) sm_scan[warp] = mine;
       __syncthreads();
-      all = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) all += sm_scan[w];
-      tiles += all;
+      for (int w = 0; w < kWarps; ++w) total += sm_scan[w];
       __syncthreads();
     }
-    U = tiles * HG;
+    cost = 0;
+    if (units_of(total) * HG > gridDim.x) cost = kSegmentCost<FMT, NT>;
+    U = units_of(total) * HG;
     N = min(static_cast<long long>(gridDim.x), U);
     if (blockIdx.x >= N) return;
     u0 = U * blockIdx.x / N;
     u1 = U * (blockIdx.x + 1) / N;
-    const long long t0 = u0 / HG;  // its tile; < tiles, so the search ends
+    const long long t0 = u0 / HG;  // < units_of(total), so the search ends
     long long incl = first, all = upto;
     for (;;) {
-      if (t0 >= incl - n && t0 < incl) {
+      const long long before = units_of(incl - n);
+      if (t0 >= before && t0 < units_of(incl)) {
         sm_b = i;
-        sm_before = incl - n;
+        sm_before = before;
       }
-      if (t0 < all) break;
+      if (t0 < units_of(all)) break;
       i += kThreads;
       n = tiles_of(i);
       __syncthreads();
@@ -578,14 +594,18 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
     b = sm_b;
     rem = u0 - sm_before * HG;
   }
-  int n_tiles = (seq_len(p, b) + UK - 1) / UK;
-  int hg = static_cast<int>(rem / n_tiles);
-  int tile = static_cast<int>(rem % n_tiles);
+  // Position in the segment: `cost` units that stand for its fixed work, then its tiles.
+  int n_units = (seq_len(p, b) + UK - 1) / UK + cost;
+  int hg = static_cast<int>(rem / n_units);
+  int at = static_cast<int>(rem % n_units);
 
   for (long long u = u0; u < u1;) {
     const int L = seq_len(p, b);
-    n_tiles = (L + UK - 1) / UK;
-    const int tile_end = static_cast<int>(min(static_cast<long long>(n_tiles), tile + (u1 - u)));
+    const int n_tiles = (L + UK - 1) / UK;
+    n_units = n_tiles + cost;
+    const int at_end = static_cast<int>(min(static_cast<long long>(n_units), at + (u1 - u)));
+    const int tile = max(0, at - cost), tile_end = at_end - cost;
+    if (tile_end <= tile) break;  // the run ends before the segment's first tile
     const int kvh = hg / p.groups, grp = hg % p.groups;
     const int head0 = kvh * p.g + grp * kMaxGroup;
     const int n_heads = min(kMaxGroup, p.g - grp * kMaxGroup);
@@ -815,14 +835,14 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
       }
     }
     if (threadIdx.x == 0 && tile == 0) {
-      const long long last = u + n_tiles - 1;  // the segment's last unit
+      const long long last = u - at + n_units - 1;  // the segment's last unit
       const int n_parts = whole ? 0 : static_cast<int>(((last + 1) * N - 1) / U) - static_cast<int>(blockIdx.x) + 1;
       p.parts[static_cast<long long>(b) * HG + hg] = make_int2(static_cast<int>(blockIdx.x) * 2 + slot, n_parts);
     }
     __syncthreads();
 
-    u += tile_end - tile;
-    tile = 0;
+    u += at_end - at;
+    at = 0;
     if (u < u1) {
       if (++hg == HG) {
         hg = 0;
