@@ -161,6 +161,20 @@ __device__ __forceinline__ void add(float (&s)[NT][4], const float (&s2)[NT][4])
     for (int c = 0; c < 4; ++c) s[t][c] += s2[t][c];
 }
 
+// Both halves of a times one half of b.
+__device__ __forceinline__ uint32_t hmul2_half(uint32_t a, uint32_t b, bool high) {
+  uint32_t r;
+  if (high)
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {h, h};\n\tmul.rn.f16x2 %0, %1, t;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {l, l};\n\tmul.rn.f16x2 %0, %1, t;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+  return r;
+}
+
 // Where a lane's pieces of the pool's first 16 rows lie.
 struct LanePtrs {
   const uint8_t* data[2];
@@ -353,14 +367,7 @@ struct Tile<D, kFp4> {
   }
   template <int NT>
   __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&qf)[NT][D / 16][2]) const {
-    float s2[NT][4];
-    uint32_t f2[2][D / 64];  // the group's factor in both halves
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t f = e4m3x2_to_f16(kf[i]);
-      f2[i][0] = __byte_perm(f, f, 0x1010);
-      if constexpr (D == 128) f2[i][1] = __byte_perm(f, f, 0x3232);
-    }
+    const uint32_t f2[2] = {e4m3x2_to_f16(kf[0]), e4m3x2_to_f16(kf[1])};  // factors of the piece's groups
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
       uint32_t a[2][4];
@@ -368,21 +375,19 @@ struct Tile<D, kFp4> {
       for (int i = 0; i < 2; ++i) {
         e2m1_to_f16(k[i][w], a[i]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a[i][e] = hmul2(a[i][e], f2[i][w / 2]);  // exact: 2 by 4 significant bits
+        for (int e = 0; e < 4; ++e) a[i][e] = hmul2_half(a[i][e], f2[i], w >= 2);  // exact: 2 by 4 significant bits
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const uint32_t(&q0)[2] = qf[t][2 * w], (&q1)[2] = qf[t][2 * w + 1];
         if (w == 0) {
           mma16816_first<false>(s[t], a[0][0], a[1][0], a[0][1], a[1][1], q0[0], q0[1]);
-          mma16816_first<false>(s2[t], a[0][2], a[1][2], a[0][3], a[1][3], q1[0], q1[1]);
         } else {
           mma16816<false>(s[t], a[0][0], a[1][0], a[0][1], a[1][1], q0[0], q0[1]);
-          mma16816<false>(s2[t], a[0][2], a[1][2], a[0][3], a[1][3], q1[0], q1[1]);
         }
+        mma16816<false>(s[t], a[0][2], a[1][2], a[0][3], a[1][3], q1[0], q1[1]);
       }
     }
-    add(s, s2);
   }
   // Product j holds elements (D / 8) r + 2 j (rows r) and the next (rows r + 8).
   template <int NT>
@@ -444,17 +449,21 @@ __device__ __forceinline__ void softmax_step(float (&s)[KB][NT][4], const float 
     for (int k = 0; k < KB; ++k)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        s[k][t][c] *= lam[t][c & 1];
-        if (!WHOLE && r + 8 * (c >> 1) >= n_keys[k]) s[k][t][c] = -INFINITY;
-        x[k][c] = s[k][t][c] - m[t][c & 1];
+        x[k][c] = fmaf(s[k][t][c], lam[t][c & 1], -m[t][c & 1]);
+        if (!WHOLE && r + 8 * (c >> 1) >= n_keys[k]) x[k][c] = -INFINITY;
         top = fmaxf(top, x[k][c]);
       }
     if (__any_sync(0xffffffffu, top > kRescaleThreshold)) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float mx = -INFINITY;
+        float mx = kNoReference;
 #pragma unroll
-        for (int k = 0; k < KB; ++k) mx = fmaxf(mx, fmaxf(s[k][t][c], s[k][t][2 + c]));
+        for (int k = 0; k < KB; ++k) {
+          // The score itself, or for a key that does not count: no reference.
+#pragma unroll
+          for (int e = c; e < 4; e += 2)
+            if (WHOLE || r + 8 * (e >> 1) < n_keys[k]) mx = fmaxf(mx, s[k][t][e] * lam[t][c]);
+        }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -469,10 +478,10 @@ __device__ __forceinline__ void softmax_step(float (&s)[KB][NT][4], const float 
           }
         }
 #pragma unroll
-        for (int k = 0; k < KB; ++k) {
-          x[k][c] = s[k][t][c] - m[t][c];
-          x[k][2 + c] = s[k][t][2 + c] - m[t][c];
-        }
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+          for (int e = c; e < 4; e += 2)
+            if (WHOLE || r + 8 * (e >> 1) < n_keys[k]) x[k][e] = fmaf(s[k][t][e], lam[t][c], -m[t][c]);
       }
     }
 #pragma unroll
