@@ -10,8 +10,13 @@
 // gives zero codes.  Division and reciprocal are the IEEE ones, so the codes are
 // those of the same formula evaluated anywhere in fp32.
 //
-// Both are bound by HBM (or, for one token a sequence, by the launch): each
-// element is read once and written once.
+// Both are bound by HBM, or, for one token a sequence, by the launch (64 tokens of
+// 32 + 16 heads: 4.1 us).  A row is read once and written once; a thread keeps one
+// token's angles and place and walks over heads.  Eight ragged prompts of up to
+// 4096 tokens into 16 bits take 80 us, 6.5 TB/s; chunks of 1500 to 2048 tokens of
+// four sequences into 4 bits 29 us, 5.4 TB/s.  Reading those back, 16384 tokens
+// each, is nearly all writes: 50 us, 6.3 TB/s, of which 5.3 are written (a fill
+// of the same memory reaches 4.0).
 #include <cuda_runtime.h>
 
 #include "gbattn_rows.cuh"
@@ -205,12 +210,12 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_con
   const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
   const int s0 = blockIdx.x * (kRowsPass * kGatherPasses) + threadIdx.x / kParts;
   const int part = threadIdx.x % kParts;
-  const int n = min(p.seqlens[b], p.S);
+  const int n = min(min(p.seqlens[b], p.max_pages << p.page_shift), p.S);
   int page[kGatherPasses];
 #pragma unroll
   for (int u = 0; u < kGatherPasses; ++u) {
     const int s = s0 + u * kRowsPass, pg = s >> p.page_shift;
-    page[u] = s < n && pg < p.max_pages ? p.page_table[static_cast<long long>(b) * p.max_pages + pg] : -1;
+    page[u] = s < n ? p.page_table[static_cast<long long>(b) * p.max_pages + pg] : -1;
   }
   uint4 y[kGatherPasses];
   uint32_t f[kGatherPasses];

@@ -9,18 +9,30 @@
 // it leaves in the workspace; a second kernel folds those.  The division of the
 // list follows from the lengths alone, so results repeat bitwise.
 //
-// Inside a CTA each warp takes every fourth 16 keys of a segment and keeps its
-// own online-softmax state.  It computes S^T = K Q^T and O^T = V^T P^T with
-// m16n8k16 tensor-core products: the keys (or head elements) fill the 16 rows
-// and up to 8 query heads the 8 columns.  Rows of K and V go from global memory
-// straight into operand registers: the order of the head's elements inside a
-// product is free as long as Q follows it, so a lane's 16-byte piece of a row is
-// its operand for several products, and V, whose operand pairs two keys, takes
-// one byte permute for two elements.
+// Inside a CTA each warp takes every fourth piece of a segment (16 keys, or 32 of
+// a 4-bit cache) and keeps its own online-softmax state.  It computes S^T = K Q^T
+// and O^T = V^T P^T with m16n8k16 tensor-core products: the keys (or head
+// elements) fill the 16 rows and up to 8 query heads the 8 columns; tcgen05's 128
+// rows would find nothing to fill them with.  The order of the head's elements
+// inside a product is free as long as Q follows it, so a lane's 16-byte piece of
+// a row of K is its operand for several products, and V, whose operand pairs two
+// keys, takes one byte permute for two elements.
+//
+// 16 bits: rows go from global memory straight into operand registers, requested
+// as the previous piece's are consumed.  Bound by HBM: 64 sequences of 1024 to
+// 32768 tokens, 32 heads on 8, d = 128, take 680 us, 7.0 TB/s.
+// 4 bits: rows go through a ring in shared memory that asynchronous copies fill.
+// A pair of codes becomes an fp16 pair in one conversion, one product applies the
+// factor (exact, 2 by 4 significant bits), and the bytes of two keys' codes are
+// interleaved for V before the conversion.  That is 275 instructions for 16 keys
+// of one KV head (72 conversions at half rate, 64 products), against 390 issue
+// slots in the time that HBM takes for their 2304 bytes: bound by issue and by
+// the conversions' pipe (62 % and 53 % busy, 16 warps an SM).  The same batch
+// takes 226 us, 5.9 TB/s.
 //
 // The scores' reference m follows the maximum lazily (it moves when a score is
-// more than 8 above it in base-2 units), so P <= 256; P is rounded to 16 bits
-// for P V, and l sums the unrounded values.
+// more than 8 above it in base-2 units), so P <= 256; l sums P before it is
+// rounded for P V (kTerms).
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -416,7 +428,11 @@ struct Tile<D, kFp4> {
   }
 };
 
-constexpr int kStages = 3;  // of a warp's ring (4-bit caches)
+// Stages of a warp's ring (4-bit caches), each of 32 keys: 4608 bytes at D = 128,
+// where two take 226 us at the 64-sequence batch and three 229; at D = 64, half
+// the bytes, three take 141 and two 144.
+template <int D>
+constexpr int kStages = D == 128 ? 2 : 3;
 
 // Blocks of 16 keys that a warp works on at a time.
 template <int FMT>
@@ -507,7 +523,7 @@ __device__ __forceinline__ void softmax_step(float (&s)[KB][NT][4], const float 
 // Dynamic shared memory of a CTA.
 template <int D, int FMT, int NT>
 struct Smem {
-  static constexpr int kRing = FMT == kFp4 ? kStages * kBlocks<FMT> * Stage<D>::kBytes : 0;
+  static constexpr int kRing = FMT == kFp4 ? kStages<D> * kBlocks<FMT> * Stage<D>::kBytes : 0;
   static constexpr int kStates = 8 * NT * (D + 4) * 4;  // of a warp
   static constexpr int kBytes = kWarps * (kRing > kStates ? kRing : kStates);
 };
@@ -701,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
       return -1;
     };
     if constexpr (FMT == kFp4) {
-      // kStages - 1 units are on their way while one is worked on.
+      // kStages<D> - 1 units are on their way while one is worked on.
       int page0 = page_of((tile * kWarps + warp) * KB), page1 = page_of((tile * kWarps + warp) * KB + 1);
       unsigned absent = 0;  // two bits a request, the newest lowest: block k has no page
       auto request = [&](int i, uint32_t stage) {
@@ -724,13 +740,13 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
       };
       constexpr uint32_t kUnitBytes = KB * Stage<D>::kBytes;
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) request(tile + i, ring + i * kUnitBytes);
+      for (int i = 0; i < kStages<D> - 1; ++i) request(tile + i, ring + i * kUnitBytes);
       load_q();
-      uint32_t stage = ring, free_stage = ring + (kStages - 1) * kUnitBytes;
+      uint32_t stage = ring, free_stage = ring + (kStages<D> - 1) * kUnitBytes;
       for (int i = tile; i < end; ++i) {
-        copy_wait<kStages - 2>();
+        copy_wait<kStages<D> - 2>();
         __syncwarp();  // every lane's copies of unit i, and every lane done with unit i - 1
-        request(i + kStages - 1, free_stage);
+        request(i + kStages<D> - 1, free_stage);
         auto step = [&](auto whole, int n0, int n1) {
           const int n_keys[KB] = {n0, n1};
           float s[KB][NT][4];
@@ -747,14 +763,14 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
             tl.template values<NT>(o, pf[k]);
           }
         };
-        const unsigned gone = absent >> (2 * (kStages - 1)) & 3;
+        const unsigned gone = absent >> (2 * (kStages<D> - 1)) & 3;
         const int left = warp_keys - i * UK;
         if (i < whole_end && gone == 0)
           step(std::true_type(), 16, 16);
         else
           step(std::false_type(), gone & 1 ? 0 : left, gone & 2 ? 0 : left - 16);
         free_stage = stage;
-        stage = stage == ring + (kStages - 1) * kUnitBytes ? ring : stage + kUnitBytes;
+        stage = stage == ring + (kStages<D> - 1) * kUnitBytes ? ring : stage + kUnitBytes;
       }
       copy_wait<0>();
     } else {

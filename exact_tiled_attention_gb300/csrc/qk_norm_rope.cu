@@ -9,7 +9,10 @@
 // Both are bound by HBM: a forward reads and writes each row once (2 bytes an
 // element each way), a backward reads two rows and writes one.  A thread keeps
 // one token's cosines and sines in registers and walks over heads, so the
-// 4-byte table is read once for several heads.
+// 4-byte table is read once for several heads, and the rows come through a ring
+// of asynchronous copies (RowRing).  At [4, 8192] tokens of 16 + 16 heads of 128
+// the forward takes 81 us (6.6 TB/s) and the backward 121 us (6.7 TB/s), against
+// 84 and 137 with the next row alone requested ahead, in registers.
 #include <cuda_runtime.h>
 
 #include <type_traits>

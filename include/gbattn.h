@@ -342,7 +342,8 @@ size_t attn_decode_noalloc_scratch_bytes(void);
  *   page_table [B, max_pages] int32 (max_pages * page_size < 2^31 - 256 and
  *            n_pages * Hkv * page_size / 16 < 2^31); entries behind a sequence's last page
  *            are not read.  seqlens [B] int32: tokens of each sequence, 0 for
- *            an idle one; values are clamped into [0, max_pages * page_size].
+ *            an idle one; values are clamped into [0, max_pages * page_size] (a
+ *            new token past it is not stored, and reported).
  * Both are device arrays, read when the kernels run, so a captured graph
  * follows them.  A page that is needed but not in [0, n_pages) is neither read
  * nor written: its tokens are not stored, read back as zeros, or left out of
@@ -509,7 +510,8 @@ size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_
  *            overlap on the GPU need one each
  * The key axes of all sequences are divided evenly over the GPU, whatever the
  * lengths are, so there is no number of splits to choose; the division follows
- * from the lengths alone and results repeat bitwise.
+ * from the lengths alone and results repeat bitwise.  A NaN or an infinity in a
+ * row that counts makes its elements of o NaN.
  *
  * attn_decode_paged_fp4 -- the same over a 4-bit cache (q and o in dtype, which
  * the cache does not depend on).

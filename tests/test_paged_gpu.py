@@ -249,6 +249,9 @@ def test_pages_that_do_not_exist(bits):
     o, lse = pool.decode(q, pu.page_table([112, 0], page, 12, 7, g).cuda(), _i32([1 << 30, -5]))
     assert gb.gbattn_device_status() == 0
     assert torch.isfinite(o).all() and (o[1] == 0).all() and torch.isneginf(lse[1]).all()
+    k, _ = pool.gather(pu.page_table([112, 0], page, 12, 7, g).cuda(), _i32([1 << 30, -5]), 130)
+    assert gb.gbattn_device_status() == 0
+    assert (k[0, :, :112] != 0).any() and (k[0, :, 112:] == 0).all() and (k[1] == 0).all()
 
 
 APPEND = [
