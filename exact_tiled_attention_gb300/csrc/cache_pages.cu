@@ -56,10 +56,17 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&y)[8]) {
   return r;
 }
 
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
+__device__ __forceinline__ __half e4m3_half(uint32_t code) {
   uint32_t h2;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(code & 0xFF)));
-  return __half2float(__ushort_as_half(static_cast<uint16_t>(h2 & 0xFFFF)));
+  return __ushort_as_half(static_cast<uint16_t>(h2 & 0xFFFF));
+}
+
+// The two E2M1 codes in the lowest byte, the low half first.
+__device__ __forceinline__ __half2 e2m1x2_half2(uint32_t codes) {
+  uint32_t h2;
+  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h2) : "r"(codes));
+  return *reinterpret_cast<const __half2*>(&h2);
 }
 
 // One chunk of 8 elements to 4 bits; the other half of its group of 16 is the
@@ -71,7 +78,7 @@ __device__ __forceinline__ uint32_t quantise8(const float (&z)[8], float descale
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
   const float f = fminf(__fdiv_rn(m, __fmul_rn(6.f, descale)), 448.f);
   factor = static_cast<uint8_t>(pack4_e4m3(f, 0.f, 0.f, 0.f) & 0xFF);
-  const float fv = e4m3_value(factor);
+  const float fv = __half2float(e4m3_half(factor));
   const float inv = fv > 0.f ? __frcp_rn(__fmul_rn(fv, descale)) : 0.f;
   float y[8];
 #pragma unroll
@@ -217,6 +224,12 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_con
     const int s = s0 + u * kRowsPass, pg = s >> p.page_shift;
     page[u] = s < n ? p.page_table[static_cast<long long>(b) * p.max_pages + pg] : -1;
   }
+  // Bytes of a row, and from one page's head to the next page's.
+  constexpr int kRow = FP4 ? D / 2 : 2 * D;
+  const long long head = static_cast<long long>(h) << p.page_shift, page_rows = static_cast<long long>(p.Hkv) << p.page_shift;
+  const int in_page = (1 << p.page_shift) - 1;
+  const uint8_t* data = p.data[which] + head * kRow + part * (kRow / kParts);
+  [[maybe_unused]] const uint8_t* factors = FP4 ? p.scale[which] + head * (D / 16) + part / 2 : nullptr;
   uint4 y[kGatherPasses];
   uint32_t f[kGatherPasses];
 #pragma unroll
@@ -225,44 +238,39 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_con
     y[u] = make_uint4(0u, 0u, 0u, 0u);
     f[u] = 0u;  // a row behind the sequence: factor 0
     if (static_cast<unsigned>(page[u]) < static_cast<unsigned>(p.n_pages)) {
-      const long long row = ((static_cast<long long>(page[u]) * p.Hkv + h) << p.page_shift) +
-                            (s & ((1 << p.page_shift) - 1));
+      const long long row = page[u] * page_rows + (s & in_page);
       if constexpr (FP4) {
-        y[u].x = *reinterpret_cast<const uint32_t*>(p.data[which] + row * (D / 2) + part * 4);
-        f[u] = p.scale[which][row * (D / 16) + part / 2];
+        y[u].x = *reinterpret_cast<const uint32_t*>(data + row * kRow);
+        f[u] = factors[row * (D / 16)];
       } else {
-        y[u] = *reinterpret_cast<const uint4*>(p.data[which] + row * (D * 2) + part * 16);
+        y[u] = *reinterpret_cast<const uint4*>(data + row * kRow);
       }
     } else if (s < n) {
       atomicCAS(p.status, 0, kStatusIndex);
     }
   }
   const float ds = FP4 && p.descale[which] != nullptr ? p.descale[which][h] : 1.f;
-  uint16_t* out = p.out[which] + static_cast<long long>(blockIdx.y) * p.S * D + part * 8;
+  uint16_t* out = p.out[which] + (static_cast<long long>(blockIdx.y) * p.S + s0) * D + part * 8;
 #pragma unroll
-  for (int u = 0; u < kGatherPasses; ++u) {
-    const int s = s0 + u * kRowsPass;
-    if (s >= p.S) break;
+  for (int u = 0; u < kGatherPasses; ++u, out += kRowsPass * D) {
+    if (s0 + u * kRowsPass >= p.S) break;
     if constexpr (FP4) {
-      float z[8];
       if (f[u] != 0) {
-        const float fv = e4m3_value(f[u]);
+        // code * factor is exact in fp16 (2 by 4 significant bits, at most 2688).
+        const __half2 f2 = __half2half2(e4m3_half(f[u]));
+        float z[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t h2;
-          asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
-              : "=r"(h2)
-              : "r"(y[u].x >> (8 * k)));
-          const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-          z[2 * k] = __fmul_rn(__fmul_rn(t.x, fv), ds);
-          z[2 * k + 1] = __fmul_rn(__fmul_rn(t.y, fv), ds);
+          const float2 t = __half22float2(__hmul2(e2m1x2_half2(y[u].x >> (8 * k)), f2));
+          z[2 * k] = __fmul_rn(t.x, ds);
+          z[2 * k + 1] = __fmul_rn(t.y, ds);
         }
         y[u] = pack8<BF16>(z);
       } else {
         y[u] = make_uint4(0u, 0u, 0u, 0u);
       }
     }
-    *reinterpret_cast<uint4*>(out + static_cast<long long>(s) * D) = y[u];
+    *reinterpret_cast<uint4*>(out) = y[u];
   }
 }
 
