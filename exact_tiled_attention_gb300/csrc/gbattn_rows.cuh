@@ -153,6 +153,13 @@ struct RowRing {
   // Waits for the next row; piece(k, c) is then its chunk c of tensor k, until pop().
   __device__ __forceinline__ void wait() const { copy_wait<STAGES - 2>(); }
   __device__ __forceinline__ uint4 piece(int k, int c) const { return (*smem)[out][2 * k + c][threadIdx.x]; }
+  // The chunk of tensor k that starts at element e of the row, copied by another
+  // of the row's lanes: between wait(), __syncwarp() and pop().  (The stage that
+  // pop() fills again is the previous row's, which every lane has left by then.)
+  __device__ __forceinline__ uint4 chunk_at(int k, int e) const {
+    const int c = e >= D / 2;
+    return (*smem)[out][2 * k + c][threadIdx.x - threadIdx.x % RowCfg<D>::kLanes + (e - c * (D / 2)) / 8];
+  }
   __device__ __forceinline__ void pop() {
     out = out + 1 == STAGES ? 0 : out + 1;
     request();  // into the stage that the row before this one has left

@@ -98,22 +98,20 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     const int b = t / p.S, s = t % p.S;
     LaneRope rope;
     if constexpr (MODE != kRopeNone) load_rope<D, MODE>(rope, table_row(p, b, s), p.rot, lane_in_row);
-    [[maybe_unused]] const uint16_t* xrow =
-        p.x[which] + b * p.xs[which].b + s * p.xs[which].s + h0 * p.xs[which].h;
     uint16_t* yrow = p.y[which] + ((static_cast<long long>(b) * p.heads[which] + h0) * p.S + s) * D;
-    for (int h = h0; h < h1; ++h, xrow += p.xs[which].h, yrow += static_cast<long long>(p.S) * D) {
+    for (int h = h0; h < h1; ++h, yrow += static_cast<long long>(p.S) * D) {
       ring.wait();
+      if constexpr (MODE == kRopePart) __syncwarp();
       float z[2][8], part[2][8];
       float sq = 0.f;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         unpack8<BF16>(ring.piece(0, c), z[c]);
-        if constexpr (MODE == kRopePart) unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + pc[c]), part[c]);
+        if constexpr (MODE == kRopePart) unpack8<BF16>(ring.chunk_at(0, pc[c]), part[c]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sq = fmaf(z[c][i], z[c][i], sq);
       }
       ring.pop();
-      if constexpr (MODE == kRopePart) __syncwarp();  // a lane's partners are read before they are written (y may be x)
       if constexpr (NORM) {
         const float r = rsqrtf(row_sum<D>(sq) * (1.f / D) + p.eps);
 #pragma unroll
@@ -176,15 +174,14 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_bwd_kernel(const __grid
     LaneRope rope;
     if constexpr (MODE != kRopeNone) load_rope<D, MODE>(rope, table_row(p, b, s), p.rot, lane_in_row);
     uint16_t* dxrow = p.dx[which] + b * dxs.b + s * dxs.s + h0 * dxs.h;
-    [[maybe_unused]] const uint16_t* dyrow =
-        p.dy[which] + ((static_cast<long long>(b) * p.heads[which] + h0) * p.S + s) * D;
-    for (int h = h0; h < h1; ++h, dxrow += dxs.h, dyrow += dy_head) {
+    for (int h = h0; h < h1; ++h, dxrow += dxs.h) {
       ring.wait();
+      if constexpr (MODE == kRopePart) __syncwarp();
       float g[2][8], part[2][8], n[2][8];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         unpack8<BF16>(ring.piece(0, c), g[c]);
-        if constexpr (MODE == kRopePart) unpack8<BF16>(*reinterpret_cast<const uint4*>(dyrow + pc[c]), part[c]);
+        if constexpr (MODE == kRopePart) unpack8<BF16>(ring.chunk_at(0, pc[c]), part[c]);
         if constexpr (NORM) unpack8<BF16>(ring.piece(1, c), n[c]);
       }
       ring.pop();
