@@ -302,11 +302,12 @@ int launch_append_t(const AppendArgs& a) {
   p.status = a.status;
   const long long tokens = static_cast<long long>(a.B) * a.S;
   const long long token_ctas = (tokens + kThreads / RowCfg<D>::kLanes - 1) / (kThreads / RowCfg<D>::kLanes);
-  // As many heads a thread as leave 32 CTAs (four rounds of them) for each SM, at
-  // most 8.
+  // As many heads a thread as leave four CTAs for each SM, at most 8.  Four CTAs
+  // against 32: 4.6 and 6.1 us at [2, 911] tokens of 24 + 6 heads, 12.5 and 16.3 at
+  // [1, 2094] of 64 + 8; the other way round 19.4 and 18.2 at [5, 1434] of 40 + 16.
   int per = 8;
   const int heads = p.heads[0] + p.heads[1] + p.heads[2];
-  while (per > 1 && token_ctas * (heads / per) < 32LL * a.num_sms) per /= 2;
+  while (per > 1 && token_ctas * (heads / per) < 4LL * a.num_sms) per /= 2;
   p.per_chunk = per;
   int chunks = 0;
   for (int i = 0; i < 3; ++i) chunks += p.chunks[i] = (p.heads[i] + per - 1) / per;

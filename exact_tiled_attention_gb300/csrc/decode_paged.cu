@@ -878,86 +878,174 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
   }
 }
 
-// One CTA for each (sequence, query head): folds the parts of a segment that was
-// split, in the order of the parts, and writes the zeros of an empty sequence.
-// Launched while the decode kernel runs; it waits for that kernel's end.
-template <int D>
-__global__ void __launch_bounds__(kThreads) decode_paged_merge_kernel(const __grid_constant__ Params p) {
-  constexpr int kLanes = D / 4;               // threads of a part's row, four elements each
-  constexpr int kTeams = kThreads / kLanes;   // parts read at a time
-  __shared__ float weight[kMaxCtas];
-  __shared__ float red[2][kWarps];
-  __shared__ float4 sum[kTeams][kLanes];
-  const long long row_g = blockIdx.x;
-  const int b = static_cast<int>(row_g / p.Hq), hq = static_cast<int>(row_g % p.Hq);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const bool empty = seq_len(p, b) == 0;
-  const int kvh = hq / p.g, in_g = hq % p.g;
-  const int hg = kvh * p.groups + in_g / kMaxGroup, row = in_g % kMaxGroup;
-  wait_for_previous_kernel();
-  const int2 part = empty ? make_int2(0, 1) : p.parts[static_cast<long long>(b) * p.Hkv * p.groups + hg];
-  if (part.y == 0) return;  // finished by one CTA
+constexpr int kMergeThreads = 256;
+
+// Where a (sequence, query head)'s parts lie.
+struct Parts {
+  int first, n, rows, row;  // first CTA * 2 + slot; number of parts (0: finished, or an empty sequence)
+  bool empty;
   // Part 0 is in the first CTA's slot; the others in slot 0 of the next CTAs.
-  auto state = [&](int i) {
-    const long long s = i == 0 ? part.x : (static_cast<long long>(part.x / 2) + i) * 2;
-    return s * p.rows + row;
-  };
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ long long state(int i) const {
+    return (i == 0 ? first : (first / 2 + i) * 2) * static_cast<long long>(rows) + row;
+  }
+};
+__device__ __forceinline__ Parts parts_of(const Params& p, int row_g) {
+  const int b = row_g / p.Hq, hq = row_g % p.Hq, kvh = hq / p.g, in_g = hq % p.g;
+  const int hg = kvh * p.groups + in_g / kMaxGroup;
+  Parts a;
+  const int2 part = p.parts[static_cast<long long>(b) * p.Hkv * p.groups + hg];  // anything for an empty sequence
+  a.empty = seq_len(p, b) == 0;
+  a.first = part.x;
+  a.n = a.empty ? 0 : part.y;
+  a.rows = p.rows;
+  a.row = in_g % kMaxGroup;
+  return a;
+}
+
+// N consecutive elements of a part's values, and of the output.
+template <int N>
+struct Piece {
+  float x[N];
+  __device__ __forceinline__ void load(const float* src) {
+    if constexpr (N == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      x[0] = v.x, x[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = 0.f;
+  }
+  __device__ __forceinline__ void add(float f, const Piece& v) {
+    if (f != 0.f) {  // a part without weight may hold anything
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = fmaf(f, v.x[i], x[i]);
+    }
+  }
+  __device__ __forceinline__ void store(const Params& p, long long row_g, int d, int e, float M, float ls) const {
+    const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      *reinterpret_cast<uint32_t*>(p.o + row_g * d + e + i) =
+          p.out_bf16 ? pack2<true>(x[i] * inv, x[i + 1] * inv) : pack2<false>(x[i] * inv, x[i + 1] * inv);
+    if (e == 0 && p.lse != nullptr)
+      p.lse[row_g] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+  }
+};
+
+// Fold the parts of segments that were split, in the order of the parts, and write
+// the zeros of empty sequences; launched while the decode kernel runs, they wait
+// for its end.  Bound by latency (place, then states and values, then their sum).
+// With few rows there may be many parts to each: a CTA a row, its teams of D / 4
+// threads taking parts in turn (57 parts of each of 32 rows: 3 us).
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_cta_kernel(const __grid_constant__ Params p) {
+  constexpr int kLanes = D / 4;                  // threads of a part's row
+  constexpr int kTeams = kMergeThreads / kLanes; // parts read at a time
+  constexpr int kMergeWarps = kMergeThreads / 32;
+  constexpr int kAhead = 8;                      // parts of a thread requested before their weights are known
+  __shared__ float weight[kMaxCtas];
+  __shared__ float red[2][kMergeWarps];
+  __shared__ Piece<4> sum[kTeams][kLanes];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int team = threadIdx.x / kLanes, e = threadIdx.x % kLanes * 4;
+  wait_for_previous_kernel();
+  const Parts a = parts_of(p, blockIdx.x);
+  if (a.n == 0 && !a.empty) return;  // finished by one CTA
+  Piece<4> v[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    v[u].clear();
+    if (team + u * kTeams < a.n) v[u].load(p.part_o + a.state(team + u * kTeams) * D + e);
+  }
   float M = kNoReference, ls = 0.f;
-  if (!empty) {
-    for (int i = threadIdx.x; i < part.y; i += kThreads) M = fmaxf(M, p.part_ml[state(i) * 2]);
+  for (int i = threadIdx.x; i < a.n; i += kMergeThreads) M = fmaxf(M, p.part_ml[a.state(i) * 2]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) red[0][warp] = M;
-    __syncthreads();
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[0][warp] = M;
+  __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[0][w]);
-    for (int i = threadIdx.x; i < part.y; i += kThreads) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + state(i) * 2);
-      const float f = ex2_approx(ml.x - M);
-      weight[i] = f;
+  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, red[0][w]);
+  for (int i = threadIdx.x; i < a.n; i += kMergeThreads) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + a.state(i) * 2);
+    const float f = ex2_approx(ml.x - M);
+    weight[i] = f;
+    if (f != 0.f) ls += f * ml.y;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+  if (lane == 0) red[1][warp] = ls;
+  __syncthreads();
+  ls = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) ls += red[1][w];
+  Piece<4> acc;
+  acc.clear();
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (team + u * kTeams < a.n) acc.add(weight[team + u * kTeams], v[u]);
+#pragma unroll 4
+  for (int i = team + kAhead * kTeams; i < a.n; i += kTeams) {
+    v[0].load(p.part_o + a.state(i) * D + e);
+    acc.add(weight[i], v[0]);
+  }
+  sum[team][threadIdx.x % kLanes] = acc;
+  __syncthreads();
+  if (team != 0) return;
+#pragma unroll
+  for (int i = 1; i < kTeams; ++i) acc.add(1.f, sum[i][threadIdx.x]);
+  acc.store(p, blockIdx.x, D, e, M, ls);
+}
+
+// With many rows most are finished, and the split ones have few parts: a warp a row.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_warp_kernel(const __grid_constant__ Params p) {
+  constexpr int kAhead = 4;
+  const int row_g = blockIdx.x * (kMergeThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (row_g >= p.B * p.Hq) return;
+  wait_for_previous_kernel();
+  const Parts a = parts_of(p, row_g);
+  if (a.n == 0 && !a.empty) return;
+  const int e = lane * (D / 32);
+  Piece<D / 32> v[kAhead], acc;
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (u < a.n) v[u].load(p.part_o + a.state(u) * D + e);
+  float M = kNoReference, ls = 0.f;
+  for (int i = lane; i < a.n; i += 32) M = fmaxf(M, p.part_ml[a.state(i) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  acc.clear();
+  for (int base = 0; base < a.n; base += 32) {
+    float f = 0.f;
+    if (base + lane < a.n) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + a.state(base + lane) * 2);
+      f = ex2_approx(ml.x - M);
       if (f != 0.f) ls += f * ml.y;
     }
+    const int m = min(32, a.n - base);
+#pragma unroll 8
+    for (int i = 0; i < m; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      if (base == 0 && i < kAhead) continue;  // below, from what was requested ahead
+      Piece<D / 32> x;
+      x.load(p.part_o + a.state(base + i) * D + e);
+      acc.add(fi, x);
+    }
+    if (base == 0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-    if (lane == 0) red[1][warp] = ls;
-    __syncthreads();
-    ls = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) ls += red[1][w];
-    const int team = threadIdx.x / kLanes, piece = threadIdx.x % kLanes;
-#pragma unroll 4
-    for (int i = team; i < part.y; i += kTeams) {
-      const float f = weight[i];
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + state(i) * D + piece * 4);
-      if (f != 0.f) {
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+      for (int u = 0; u < kAhead; ++u) {
+        const float fu = __shfl_sync(0xffffffffu, f, u);
+        if (u < a.n) acc.add(fu, v[u]);
       }
     }
-    sum[team][piece] = acc;
-    __syncthreads();
-    if (team != 0) return;
-#pragma unroll
-    for (int i = 1; i < kTeams; ++i) {
-      const float4 v = sum[i][piece];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
-    }
-  } else if (threadIdx.x >= kLanes) {
-    return;
   }
-  const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
-  const float4 y = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(p.o + row_g * D + threadIdx.x * 4) =
-      p.out_bf16 ? make_uint2(pack2<true>(y.x, y.y), pack2<true>(y.z, y.w))
-                 : make_uint2(pack2<false>(y.x, y.y), pack2<false>(y.z, y.w));
-  if (threadIdx.x == 0 && p.lse != nullptr)
-    p.lse[row_g] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+  acc.store(p, row_g, D, e, M, ls);
 }
 
 int group_rows(int Hq, int Hkv) {
@@ -993,7 +1081,13 @@ int launch_t(const Params& p, const PagedDecodeArgs& a) {
   if (ctas > p.most_ctas) ctas = p.most_ctas;
   kern<<<ctas, kThreads, kBytes, a.stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  return launch_after(decode_paged_merge_kernel<D>, dim3(static_cast<unsigned>(a.B) * a.Hq), kThreads, a.stream, p);
+  // A CTA a row while that is at most four CTAs for each SM.
+  const int rows = a.B * a.Hq;
+  if (rows <= 4 * a.num_sms)
+    return launch_after(decode_paged_merge_cta_kernel<D>, dim3(static_cast<unsigned>(rows)), kMergeThreads, a.stream, p);
+  constexpr int kRows = kMergeThreads / 32;
+  return launch_after(decode_paged_merge_warp_kernel<D>, dim3(static_cast<unsigned>((rows + kRows - 1) / kRows)),
+                      kMergeThreads, a.stream, p);
 }
 
 template <int D, int FMT>

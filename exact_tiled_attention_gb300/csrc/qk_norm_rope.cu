@@ -318,11 +318,12 @@ int launch_fwd(const NormRopeArgs& a) {
   const long long tokens = static_cast<long long>(a.B) * a.S;
   const long long token_ctas = (tokens + kThreads / RowCfg<D>::kLanes - 1) / (kThreads / RowCfg<D>::kLanes);
   const int heads = a.heads[0] + a.heads[1];
-  // As many heads a thread as leave 32 CTAs (four rounds of them) for each SM, at
-  // most 8: at [2, 4096] tokens of 40 heads 4 a thread take 30 us and 8 take 31.5,
-  // at [4, 8192] of 32 heads 8 take 84 us and 4 take 86.
+  // As many heads a thread as leave four CTAs for each SM, at most 8: a thread
+  // with few rows hardly uses its ring.  Four CTAs against 32: 10.5 and 16.1 us at
+  // [1, 2094] tokens of 68 heads, 4.9 and 6.7 at [2, 911] of 27; the other way
+  // round 28.1 and 27.5 at [2, 4096] of 40.
   int per = 8;
-  while (per > 1 && token_ctas * (heads / per) < 32LL * a.num_sms) per /= 2;
+  while (per > 1 && token_ctas * (heads / per) < 4LL * a.num_sms) per /= 2;
   set_chunks(p, per);
   const int chunks = p.chunks[0] + p.chunks[1];
   if (chunks > 65535) return -1;
@@ -341,8 +342,11 @@ int launch_bwd(const NormRopeArgs& a) {
   const long long tokens = static_cast<long long>(a.B) * a.S;
   const long long token_ctas = (tokens + kThreads / RowCfg<D>::kLanes - 1) / (kThreads / RowCfg<D>::kLanes);
   const int heads = a.heads[0] + a.heads[1];
-  int per = 8;
-  while (per > 1 && token_ctas * (heads / per) < 16LL * a.num_sms) per /= 2;
+  // Up to 16 heads a thread and two CTAs for each SM: each CTA ends with the sum of
+  // its weight gradients.  16 and 8 heads: 17.9 and 21.3 us at [1, 2094] tokens of
+  // 68 heads, 42.0 and 46.2 at [2, 4096] of 40, 61.7 and 60.5 at [1, 4777] of 96.
+  int per = 16;
+  while (per > 1 && token_ctas * (heads / per) < 2LL * a.num_sms) per /= 2;
   const int most = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
   while ((most + per - 1) / per > kMaxBwdCtas) per *= 2;
   set_chunks(p, per);

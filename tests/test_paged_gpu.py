@@ -148,6 +148,24 @@ def test_decode_many_short_sequences(bits):
     assert gb.gbattn_device_status() == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_decode_one_long_sequence_among_many(bits, d):
+    """More rows than the merge takes a CTA each for, one of them split over a
+    large part of the grid."""
+    g = torch.Generator().manual_seed(27)
+    lens = [(1, 0, 40)[i % 3] for i in range(330)]
+    lens[17] = 30011
+    page, Hq, Hkv = 64, 4, 1
+    n_pages = sum((n + page - 1) // page for n in lens)
+    pool = Pool(bits, n_pages, Hkv, page, d, torch.bfloat16, g)
+    table = pu.page_table(lens, page, n_pages, 470, g)
+    q = torch.randn(len(lens), Hq, 1, d, generator=g).bfloat16().cuda()
+    o, lse = pool.decode(q, table.cuda(), _i32(lens))
+    _decode_ok(pool, q, table, lens, o, lse, 1 / math.sqrt(d))
+    assert gb.gbattn_device_status() == 0
+
+
 @pytest.mark.parametrize("bits", [16, 4])
 def test_decode_rows_behind_the_length_are_not_used(bits):
     """Slots behind each length, unused pages and factors hold NaN."""
