@@ -837,12 +837,10 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
       float a0 = 0.f, a1 = 0.f, ls = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2_approx(sm_ml[w][row][0] - M);
-        if (f != 0.f) {
-          a0 += f * sm_o[w][row][e];
-          a1 += f * sm_o[w][row][e + 1];
-          ls += f * sm_ml[w][row][1];
-        }
+        const float f = ex2_approx(sm_ml[w][row][0] - M);  // NaN stays NaN where f is 0
+        a0 = fmaf(f, sm_o[w][row][e], a0);
+        a1 = fmaf(f, sm_o[w][row][e + 1], a1);
+        ls = fmaf(f, sm_ml[w][row][1], ls);
       }
       a0 *= vd;
       a1 *= vd;
@@ -920,10 +918,8 @@ struct Piece {
     for (int i = 0; i < N; ++i) x[i] = 0.f;
   }
   __device__ __forceinline__ void add(float f, const Piece& v) {
-    if (f != 0.f) {  // a part without weight may hold anything
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = fmaf(f, v.x[i], x[i]);
-    }
+    for (int i = 0; i < N; ++i) x[i] = fmaf(f, v.x[i], x[i]);
   }
   __device__ __forceinline__ void store(const Params& p, long long row_g, int d, int e, float M, float ls) const {
     const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
@@ -937,7 +933,8 @@ struct Piece {
 };
 
 // Fold the parts of segments that were split, in the order of the parts, and write
-// the zeros of empty sequences; launched while the decode kernel runs, they wait
+// the zeros of empty sequences (a part's NaN counts whatever its weight is, as it
+// does in the formula); launched while the decode kernel runs, they wait
 // for its end.  Bound by latency (place, then states and values, then their sum).
 // With few rows there may be many parts to each: a CTA a row, its teams of D / 4
 // threads taking parts in turn (57 parts of each of 32 rows: 3 us).
@@ -973,7 +970,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_cta_kernel(c
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + a.state(i) * 2);
     const float f = ex2_approx(ml.x - M);
     weight[i] = f;
-    if (f != 0.f) ls += f * ml.y;
+    ls = fmaf(f, ml.y, ls);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
@@ -1024,7 +1021,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_warp_kernel(
     if (base + lane < a.n) {
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + a.state(base + lane) * 2);
       f = ex2_approx(ml.x - M);
-      if (f != 0.f) ls += f * ml.y;
+      ls = fmaf(f, ml.y, ls);
     }
     const int m = min(32, a.n - base);
 #pragma unroll 8

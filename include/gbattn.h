@@ -510,8 +510,9 @@ size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_
  *            overlap on the GPU need one each
  * The key axes of all sequences are divided evenly over the GPU, whatever the
  * lengths are, so there is no number of splits to choose; the division follows
- * from the lengths alone and results repeat bitwise.  A NaN or an infinity in a
- * row that counts makes its elements of o NaN.
+ * from the lengths alone and results repeat bitwise.  A score of NaN or +inf
+ * makes its query's o and lse NaN, a score of -inf counts as a masked key, and a
+ * NaN or an infinity in a row of v that counts makes its elements of o NaN.
  *
  * attn_decode_paged_fp4 -- the same over a 4-bit cache (q and o in dtype, which
  * the cache does not depend on).

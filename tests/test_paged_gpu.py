@@ -209,6 +209,50 @@ def test_decode_large_scores_and_given_arguments(bits):
     assert none is None
 
 
+# (B, Hq, Hkv, L): a warp that holds the last key alone; a part of a split sequence
+# that does, folded by a CTA a row; many rows, folded by a warp each
+LAST_KEY = [(2, 4, 2, {16: 17, 4: 33}), (1, 4, 1, {16: 193, 4: 385}), (160, 8, 1, {16: 2048, 4: 2048})]
+
+
+@pytest.mark.parametrize("where", ["key", "value"])
+@pytest.mark.parametrize("case", LAST_KEY)
+@pytest.mark.parametrize("bits", [16, 4])
+def test_nan_in_a_row_that_counts(bits, case, where):
+    """NaN in the last key of every sequence but one: all of o and lse of its heads
+    are NaN; in the last value: its elements of o, whose weight is far below the
+    smallest fp32 number here (the keys of the second half point against q)."""
+    g = torch.Generator().manual_seed(77)
+    B, Hq, Hkv, L, d = *case[:3], case[3][bits], 64
+    n = (L + 15) // 16
+    pool = Pool(bits, B * n, Hkv, 16, d, torch.bfloat16, g)
+    table = torch.arange(B * n, dtype=torch.int32).view(B, n)
+    sign = torch.where(torch.arange(n * 16) < L // 2, 1.0, -1.0).view(n, 1, 16, 1)
+    q = torch.full((B, Hq, 1, d), 1.0, dtype=torch.bfloat16)
+    page, slot = table[1:, -1].long() if B > 1 else table[:, -1].long(), (L - 1) % 16
+    if bits == 16:
+        pool.t[0] = (sign * torch.ones(B, n, Hkv, 16, d)).flatten(0, 1).to(torch.bfloat16)
+        pool.t[0 if where == "key" else 1][page, :, slot, 5] = float("nan")
+    else:
+        code = torch.where(sign > 0, 0x22, 0xAA).to(torch.uint8)  # 1 and -1
+        pool.t[0] = code.expand(B, n, Hkv, 16, d // 2).flatten(0, 1).contiguous()
+        pool.t[1] = torch.ones_like(pool.t[1].float()).to(torch.float8_e4m3fn)
+        pool.t[1 if where == "key" else 3].view(torch.uint8)[page, :, slot, 0] = 0x7F  # elements 0 .. 15
+    pool.gpu = [t.cuda() for t in pool.t]
+    fn = gb.attn_decode_paged if bits == 16 else gb.attn_decode_paged_fp4
+    o, lse = fn(q.cuda(), *pool.gpu, table.cuda(), _i32([L] * B), scale=4.0, **pool.kw)
+    o, lse = o.cpu()[:, :, 0], lse.cpu()
+    touched = slice(1, None) if B > 1 else slice(None)
+    if B > 1:
+        assert torch.isfinite(o[0]).all() and torch.isfinite(lse[0]).all()
+    if where == "key":
+        assert torch.isnan(o[touched]).all() and torch.isnan(lse[touched]).all()
+    else:
+        bad = torch.zeros(d, dtype=torch.bool)
+        bad[slice(5, 6) if bits == 16 else slice(0, 16)] = True
+        assert torch.isnan(o[touched][..., bad]).all() and torch.isfinite(o[touched][..., ~bad]).all()
+        assert torch.isfinite(lse[touched]).all()
+
+
 def test_decode_wide_queries_over_four_bits():
     """bf16 queries far outside fp16's range, whose products the row's scale keeps exact."""
     g = torch.Generator().manual_seed(25)
