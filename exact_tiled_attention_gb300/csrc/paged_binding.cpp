@@ -113,17 +113,36 @@ struct Rows {
   const long long* stride() const { return plain ? nullptr : strides; }
 };
 
-Rows rows(PyObject* o, const char* name, Shape shape, const First& f) {
+// Whether rows of shape[3] elements at these strides (0: a dimension of one) lie
+// apart because each dimension steps over all of the next smaller one, as in any
+// view of a tensor with more heads.
+bool nested(Shape shape, const long long (&strides)[3]) {
+  bool used[3] = {};
+  long long extent = shape[3];
+  for (int dims = 0; dims < 3; ++dims) {
+    int next = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!used[i] && (next < 0 || shape[next] == 1 || (shape[i] > 1 && strides[i] < strides[next]))) next = i;
+    used[next] = true;
+    if (shape[next] == 1) continue;
+    if (strides[next] < extent) return false;
+    extent = strides[next] * shape[next];
+  }
+  return true;
+}
+
+Rows rows(PyObject* o, const char* name, Shape shape, const First& f, bool output = false) {
   const Tensor& t = tensor(o, name);
   check(t, name, shape, f.type, f.device);
   Rows r;
   r.data = t.data_ptr();
   if (t.is_contiguous()) return r;
-  const auto s = t.strides();
-  if (s[3] != 1 || ((s[0] | s[1] | s[2]) & 7))
-    refuse_value(name, " needs contiguous rows of d elements that start on 16-byte boundaries, got strides ", s);
   r.plain = false;
-  for (int i = 0; i < 3; ++i) r.strides[i] = s[i];
+  for (int i = 0; i < 3; ++i) r.strides[i] = shape[i] > 1 ? t.stride(i) : 0;  // no step, whatever the stride says
+  if (t.stride(3) != 1 || ((r.strides[0] | r.strides[1] | r.strides[2]) & 7))
+    refuse_value(name, " needs contiguous rows of d elements that start on 16-byte boundaries, got strides ", t.strides());
+  if (output && !nested(shape, r.strides))
+    refuse_value(name, " is written: its rows must not share memory, got strides ", t.strides());
   return r;
 }
 
@@ -299,14 +318,14 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
     dq.make(n.q_shape, n.f.type, n.f.device);
     dq_rows.data = dq.data;
   } else {
-    dq_rows = rows(a[11], "dq", n.q_shape, n.f);
+    dq_rows = rows(a[11], "dq", n.q_shape, n.f, true);
     dq.object = Py_NewRef(a[11]);
   }
   if (none(a[12])) {
     dk.make(n.k_shape, n.f.type, n.f.device);
     dk_rows.data = dk.data;
   } else {
-    dk_rows = rows(a[12], "dk", n.k_shape, n.f);
+    dk_rows = rows(a[12], "dk", n.k_shape, n.f, true);
     dk.object = Py_NewRef(a[12]);
   }
   Workspace ws;

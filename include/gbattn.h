@@ -405,7 +405,8 @@ size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
  *   dq_out [B, H, S, d], dk_out [B, Hkv, S, d]  dtype, inputs, contiguous:
  *            the gradients of q_out and k_out (attn_bwd's dq and dk)
  *   q, k, weights, rope, positions: as passed to attn_qk_norm_rope
- *   dq, dk   dtype, outputs at their own strides; they overlap no input
+ *   dq, dk   dtype, outputs at their own strides; they overlap no input, each other or
+ *            themselves (no stride of 0 in a dimension above one)
  *   dq_weight, dk_weight [d]  fp32, outputs (with weights): summed over all
  *            rows in a fixed order, so they repeat bitwise
  *   workspace: at least attn_qk_norm_rope_bwd_workspace_bytes(d) bytes,

@@ -126,6 +126,29 @@ def test_in_place_and_given_outputs():
     assert torch.equal(got[2], ref[2]) and torch.equal(got[3], ref[3])  # repeats bitwise
 
 
+def test_strides_of_single_rows_and_shared_ones():
+    """The stride of a dimension of one says nothing: a tensor is not refused for
+    it.  Inputs may repeat rows by a stride of 0; outputs whose rows share memory
+    are refused."""
+    q, k, _, _, _, _, wd, td, _, dyd = _case(3, 1, 4, 2, 64, torch.bfloat16, 64, 13)
+    ref = gb.attn_qk_norm_rope(q, k, *wd, rope=td)
+    ref_bwd = gb.attn_qk_norm_rope_bwd(*dyd, q, k, *wd, rope=td)
+    buf = torch.empty(3, 8, 64, dtype=torch.bfloat16, device="cuda")
+    odd = torch.as_strided(buf, (3, 4, 1, 64), (512, 64, 1, 1))
+    odd.copy_(q)
+    got = gb.attn_qk_norm_rope(odd, k, *wd, rope=td)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    got = gb.attn_qk_norm_rope_bwd(*dyd, q, k, *wd, rope=td, dq=torch.as_strided(buf, (3, 4, 1, 64), (512, 64, 1, 1)))
+    assert torch.equal(got[0], ref_bwd[0])
+    got = gb.attn_qk_norm_rope_bwd(*dyd, q, k, *wd, rope=td, dk=buf[:, ::3][:, :2].unsqueeze(2))
+    assert torch.equal(got[1], ref_bwd[1])
+    got = gb.attn_qk_norm_rope(q[:1].expand(3, -1, -1, -1), k, *wd, rope=td)
+    assert all(torch.equal(got[0][b], ref[0][0]) for b in range(3))
+    for strides in ((0, 64, 64, 1), (512, 0, 64, 1), (512, 32, 64, 1), (128, 64, 64, 1)):
+        with pytest.raises(ValueError, match="share memory"):
+            gb.attn_qk_norm_rope_bwd(*dyd, q, k, *wd, rope=td, dq=torch.as_strided(buf, (3, 4, 1, 64), strides))
+
+
 def test_zero_rows_and_extreme_values():
     """A zero row's norm is eps^-1/2 and its output 0; rows of the largest fp16
     values have a finite norm; a NaN stays in its own row."""
