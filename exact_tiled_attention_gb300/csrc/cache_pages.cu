@@ -155,8 +155,14 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
     if constexpr (MODE != kRopeNone) {
       if (which != 2) {
         if constexpr (MODE == kRopePart) {
-          unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + pc[0]), part[0]);
-          unpack8<BF16>(*reinterpret_cast<const uint4*>(xrow + pc[1]), part[1]);
+          uint4 other[2] = {};
+          if (real) {
+            other[0] = *reinterpret_cast<const uint4*>(xrow + pc[0]);
+            other[1] = *reinterpret_cast<const uint4*>(xrow + pc[1]);
+          }
+          unpack8<BF16>(other[0], part[0]);
+          unpack8<BF16>(other[1], part[1]);
+          __syncwarp();  // q_out may be q: the row's other lanes write what this one has just read
         }
         rotate<MODE, false>(z, part, rope);
       }

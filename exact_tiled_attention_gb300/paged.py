@@ -90,7 +90,8 @@ def attn_cache_append(k, v, k_cache, v_cache, page_table, seqlens, new_lens=None
     k, v [B,Hkv,S,d] and q [B,H,S,d] (contiguous rows, any strides);
     k_cache, v_cache [n_pages,Hkv,page_size,d]; page_table int32 [B,max_pages];
     seqlens int32 [B], the new tokens included; new_lens int32 [B] (None: S);
-    rope from rope_table, or None.  Returns the rotated queries (None without q)."""
+    rope from rope_table, or None.  Returns the rotated queries (None without q);
+    q_out may be q itself where that is contiguous."""
     return (_native or _load()).attn_cache_append(k, v, k_cache, v_cache, page_table, seqlens, new_lens, rope,
                                                   interleaved, q, q_out, stream)
 

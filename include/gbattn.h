@@ -337,7 +337,7 @@ size_t attn_decode_noalloc_scratch_bytes(void);
  *            codes each (the even element in the low half);
  *            k_factors, v_factors [n_pages, Hkv, page_size, d / 16] E4M3FN
  *            bytes, one for each 16 elements of a row;
- *            k_descale, v_descale [Hkv] fp32 or NULL (1).  An element is
+ *            k_descale, v_descale [Hkv] fp32, positive, or NULL (1).  An element is
  *            code * factor * descale[head].
  *   page_table [B, max_pages] int32 (max_pages * page_size < 2^31 - 256 and
  *            n_pages * Hkv * page_size / 16 < 2^31); entries behind a sequence's last page
@@ -436,7 +436,8 @@ int attn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q,
  *            sequence has length 0), are padding: nothing is stored for them.
  *   q        [B, H, S, d]  dtype, input (any strides), or NULL: rotated by the
  *            same positions into q_out [B, H, S, d] (contiguous; zeros for
- *            padding rows; NULL where q is); q_out overlaps no input
+ *            padding rows; NULL where q is); it may be q itself where that is
+ *            contiguous, and overlaps no other input
  * The slots that one call writes are distinct (pages that several sequences
  * share are for reading).  All other slots stay as they are.
  *

@@ -382,6 +382,24 @@ def test_append(cfg, ragged):
     assert all(_same_bits(a, b) for a, b in zip(before, pool.t))
 
 
+@pytest.mark.parametrize("rot,interleaved", [(128, False), (48, False), (48, True), (0, False)])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_append_rotates_queries_in_place(bits, rot, interleaved):
+    g = torch.Generator().manual_seed(32)
+    B, S, H, Hkv, d = 2, 45, 12, 4, 128
+    q, k, v = (torch.randn(B, h, S, d, generator=g).bfloat16().cuda() for h in (H, Hkv, Hkv))
+    table = pu.page_table([60, 30], 16, 8, 4, g).cuda()
+    rope = gb.rope_table(64, rot) if rot else None
+    args = dict(new_lens=_i32([45, 20]), rope=rope, interleaved=interleaved)
+    pools = [Pool(bits, 8, Hkv, 16, d, torch.bfloat16, torch.Generator().manual_seed(1)) for _ in range(2)]
+    ref = pools[0].append(k, v, table, _i32([60, 30]), q=q, **args)
+    for _ in range(20):
+        mine = q.clone()
+        out = pools[1].append(k, v, table, _i32([60, 30]), q=mine, q_out=mine, **args)
+        assert out is mine and torch.equal(mine, ref)
+    assert all(_same_bits(a, b) for a, b in zip(pools[0].gpu, pools[1].gpu))
+
+
 def test_append_four_bits_of_extreme_values():
     """Zeros, subnormals, infinities and values beyond the largest factor; NaN is
     stored as some number and does not spread beyond its group."""
