@@ -7,7 +7,9 @@
 // lengths are.  A run covers whole (sequence, head) segments, which the CTA
 // finishes itself, and at its two ends parts of segments, whose states (m, l, o)
 // it leaves in the workspace; a second kernel folds those.  The division of the
-// list follows from the lengths alone, so results repeat bitwise.
+// list follows from the lengths alone, so results repeat bitwise.  Where a page
+// table has room for few units (short_cluster), a cluster of 1 to 8 CTAs takes each
+// segment instead and folds its states through shared memory.
 //
 // Inside a CTA each warp takes every fourth piece of a segment (16 keys, or 32 of
 // a 4-bit cache) and keeps its own online-softmax state.  It computes S^T = K Q^T
@@ -520,6 +522,28 @@ __device__ __forceinline__ void softmax_step(float (&s)[KB][NT][4], const float 
   }
 }
 
+// Writes elements e, e + 1 of a row of o from their weighted sum, and its lse.
+__device__ __forceinline__ void finish(const Params& p, long long row_g, int d, int e, float a0, float a1, float M,
+                                       float ls) {
+  const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
+  *reinterpret_cast<uint32_t*>(p.o + row_g * d + e) =
+      p.out_bf16 ? pack2<true>(a0 * inv, a1 * inv) : pack2<false>(a0 * inv, a1 * inv);
+  if (e == 0 && p.lse != nullptr) p.lse[row_g] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+}
+
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t n;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ float2 ld_cluster(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
 // Dynamic shared memory of a CTA.
 template <int D, int FMT, int NT>
 struct Smem {
@@ -528,7 +552,9 @@ struct Smem {
   static constexpr int kBytes = kWarps * (kRing > kStates ? kRing : kStates);
 };
 
-template <int D, int FMT, int NT>
+// SHORT: a cluster for each segment, its CTAs take equal runs of the segment's
+// units and fold their states through shared memory.
+template <int D, int FMT, int NT, bool SHORT>
 __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
     decode_paged_kernel(const __grid_constant__ Params p) {
   using C = Smem<D, FMT, NT>;
@@ -537,20 +563,28 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
   extern __shared__ __align__(128) uint8_t sm_raw[];
   auto sm_o = reinterpret_cast<float (*)[8 * NT][D + 4]>(sm_raw);
   __shared__ float sm_ml[kWarps][8 * NT][2];
+  [[maybe_unused]] __shared__ float2 sm_fold[8 * NT];
   __shared__ long long sm_scan[kWarps + 1];
   __shared__ int sm_b;
   __shared__ long long sm_before;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int r = lane >> 2, q4 = lane & 3;
-  let_next_kernel_start();
+  if constexpr (!SHORT) let_next_kernel_start();
   const int HG = p.Hkv * p.groups;
   [[maybe_unused]] const uint32_t ring = smem_u32(sm_raw) + warp * C::kRing;
   const LanePtrs src = Tile<D, FMT>::ptrs(p, lane);
 
   // ---- this CTA's run of units, [u0, u1) of U, and the sequence that holds u0
-  long long U, N, u0, u1, rem;
-  int b, cost;
-  {
+  long long U = 0, N = 0, u0 = 0, u1 = 1, rem = 0;
+  int b, cost = 0, hg = 0, at = 0, n_units = 0;
+  [[maybe_unused]] int rank = 0, ranks = 1;
+  if constexpr (SHORT) {
+    rank = static_cast<int>(cluster_ctarank());
+    ranks = static_cast<int>(cluster_ctas());
+    const int segment = blockIdx.x / ranks;
+    b = segment / HG;
+    hg = segment % HG;
+  } else {
     // Tiles of a sequence and, in the upper bits, whether it has any: summed up,
     // tiles and sequences with keys.
     constexpr int kShift = 44;
@@ -620,20 +654,39 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
     rem = u0 - sm_before * HG;
   }
   // Position in the segment: `cost` units that stand for its fixed work, then its tiles.
-  int n_units = (seq_len(p, b) + UK - 1) / UK + cost;
-  int hg = static_cast<int>(rem / n_units);
-  int at = static_cast<int>(rem % n_units);
+  if constexpr (!SHORT) {
+    n_units = (seq_len(p, b) + UK - 1) / UK + cost;
+    hg = static_cast<int>(rem / n_units);
+    at = static_cast<int>(rem % n_units);
+  }
 
   for (long long u = u0; u < u1;) {
     const int L = seq_len(p, b);
     const int n_tiles = (L + UK - 1) / UK;
     n_units = n_tiles + cost;
-    const int at_end = static_cast<int>(min(static_cast<long long>(n_units), at + (u1 - u)));
-    const int tile = max(0, at - cost), tile_end = at_end - cost;
-    if (tile_end <= tile) break;  // the run ends before the segment's first tile
+    int at_end = 0, tile, tile_end;
+    if constexpr (SHORT) {
+      tile = static_cast<int>(static_cast<long long>(n_tiles) * rank / ranks);
+      tile_end = static_cast<int>(static_cast<long long>(n_tiles) * (rank + 1) / ranks);
+    } else {
+      at_end = static_cast<int>(min(static_cast<long long>(n_units), at + (u1 - u)));
+      tile = max(0, at - cost), tile_end = at_end - cost;
+      if (tile_end <= tile) break;  // the run ends before the segment's first tile
+    }
     const int kvh = hg / p.groups, grp = hg % p.groups;
     const int head0 = kvh * p.g + grp * kMaxGroup;
     const int n_heads = min(kMaxGroup, p.g - grp * kMaxGroup);
+    if constexpr (SHORT) {
+      if (L == 0) {  // for all CTAs of the cluster alike
+        const long long row0 = static_cast<long long>(b) * p.Hq + head0;
+        if (rank == 0) {
+          for (int i = threadIdx.x; i < n_heads * (D / 2); i += kThreads)
+            *reinterpret_cast<uint32_t*>(p.o + row0 * D + 2 * i) = 0u;
+          if (p.lse != nullptr && static_cast<int>(threadIdx.x) < n_heads) p.lse[row0 + threadIdx.x] = -INFINITY;
+        }
+        return;
+      }
+    }
 
     // ---- Q as the products' B operand, in the element order of K; read once the
     // first keys are on their way
@@ -844,18 +897,45 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
       }
       a0 *= vd;
       a1 *= vd;
-      if (whole) {
-        const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
-        const long long row_g = static_cast<long long>(b) * p.Hq + head0 + row;
-        *reinterpret_cast<uint32_t*>(p.o + row_g * D + e) =
-            p.out_bf16 ? pack2<true>(a0 * inv, a1 * inv) : pack2<false>(a0 * inv, a1 * inv);
-        if (e == 0 && p.lse != nullptr)
-          p.lse[row_g] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+      if (SHORT && ranks > 1) {  // in the place of the first warp's state
+        *reinterpret_cast<float2*>(&sm_o[0][row][e]) = make_float2(a0, a1);
+        if (e == 0) sm_fold[row] = make_float2(M, ls);
+      } else if (whole) {
+        finish(p, static_cast<long long>(b) * p.Hq + head0 + row, D, e, a0, a1, M, ls);
       } else {
         const long long st = (static_cast<long long>(blockIdx.x) * 2 + slot) * p.rows + row;
         *reinterpret_cast<float2*>(p.part_o + st * D + e) = make_float2(a0, a1);
         if (e == 0) *reinterpret_cast<float2*>(p.part_ml + st * 2) = make_float2(M, ls);
       }
+    }
+    if constexpr (SHORT) {
+      if (ranks == 1) return;
+      cluster_sync_all();
+      // Every CTA folds a share of the elements, in the order of the ranks.
+      for (int idx = rank * kThreads + threadIdx.x; idx < n_heads * (D / 2); idx += ranks * kThreads) {
+        const int row = idx / (D / 2), e = 2 * (idx % (D / 2));
+        float2 ml[kMaxCluster], v[kMaxCluster];
+        float M = kNoReference;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+          if (k < ranks) {
+            ml[k] = ld_cluster(mapa_shared(&sm_fold[row], k));
+            v[k] = ld_cluster(mapa_shared(&sm_o[0][row][e], k));
+            M = fmaxf(M, ml[k].x);
+          }
+        float a0 = 0.f, a1 = 0.f, ls = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+          if (k < ranks) {
+            const float f = ex2_approx(ml[k].x - M);
+            a0 = fmaf(f, v[k].x, a0);
+            a1 = fmaf(f, v[k].y, a1);
+            ls = fmaf(f, ml[k].y, ls);
+          }
+        finish(p, static_cast<long long>(b) * p.Hq + head0 + row, D, e, a0, a1, M, ls);
+      }
+      cluster_sync_all();  // no CTA leaves before the others have read its state
+      return;
     }
     if (threadIdx.x == 0 && tile == 0) {
       const long long last = u - at + n_units - 1;  // the segment's last unit
@@ -922,13 +1002,8 @@ struct Piece {
     for (int i = 0; i < N; ++i) x[i] = fmaf(f, v.x[i], x[i]);
   }
   __device__ __forceinline__ void store(const Params& p, long long row_g, int d, int e, float M, float ls) const {
-    const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
 #pragma unroll
-    for (int i = 0; i < N; i += 2)
-      *reinterpret_cast<uint32_t*>(p.o + row_g * d + e + i) =
-          p.out_bf16 ? pack2<true>(x[i] * inv, x[i + 1] * inv) : pack2<false>(x[i] * inv, x[i + 1] * inv);
-    if (e == 0 && p.lse != nullptr)
-      p.lse[row_g] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+    for (int i = 0; i < N; i += 2) finish(p, row_g, d, e + i, x[i], x[i + 1], M, ls);
   }
 };
 
@@ -1058,9 +1133,63 @@ int max_ctas(int B, size_t heads, int max_len) {
   return units < kMaxCtas ? static_cast<int>(units) : kMaxCtas;
 }
 
+// CTAs of a cluster that takes a whole segment, or 0 where the list of all units is
+// divided instead.  The host knows what the pages of a sequence can hold, not the
+// lengths, so a cluster is for tables of few units: it saves the division and the
+// second kernel (6.5 -> 4.8 us for one sequence of 4 units, 10.4 -> 7 us of host
+// time), and loses where one cluster has much more to do than a CTA's even share,
+// half of which is taken off for ragged batches.  Measured with 32 heads on 8,
+// d = 128, 16 bits, us (list against clusters), lengths of 0 up to what the table
+// holds:
+//   8 sequences, 4 CTAs each: 16 units 10.0 / 8.6, 24 10.6 / 10.0, 32 12.8 / 13.1
+//   24 sequences, 2 CTAs each: 8 units 12.3 / 10.4, 16 15.3 / 15.4, 24 17.7 / 19.6
+//   48 sequences, a CTA each: 8 units 16.0 / 14.4, 12 about even, 24 28 / 32
+// one sequence, 8 CTAs, equal lengths: 16 units 6.7 / 5.8, 32 7.3 / 7.2, 48 8.1 / 8.6.
+// With more segments than resident CTAs they take turns, and the last turn's
+// idle places cost what the list does not lose: from four turns on clusters of
+// one win at all 16 units tried (512 sequences 313 / 302, 4 bits 215 / 197); at
+// 1.1 turns 16 bits win up to 4 units (17.8 / 16.9) and lose at 6 (22.1 / 23.2),
+// 4 bits win up to 8 (1.7 turns: 39.1 / 32.2).
+template <int FMT>
+int short_cluster(const Params& p, int ctas) {
+  const long long segments = static_cast<long long>(p.B) * p.Hkv * p.groups;
+  const long long units = ((p.max_pages << p.page_shift) + kUnitKeys<FMT> - 1) / kUnitKeys<FMT>;
+  if (segments > ctas) return units <= (segments >= 4LL * ctas ? 16 : FMT == kFp4 ? 8 : 4) ? 1 : 0;
+  // Clusters of eight leave places of an SM group idle: 54 of them do not fit
+  // where 432 CTAs would (15.6 us against 11.9 with four).
+  int cluster = kMaxCluster;
+  while (cluster > 1 && (segments * cluster > (cluster == kMaxCluster ? ctas * 3 / 4 : ctas) || cluster / 2 >= units))
+    cluster /= 2;
+  // units / cluster - units segments / (2 ctas) <= 4 (a cluster of one: 8)
+  return units * (2 * ctas - segments * cluster) <= (cluster == 1 ? 16LL : 8LL) * ctas * cluster ? cluster : 0;
+}
+
+// A cluster for each (sequence, unit of query heads).
+template <int D, int FMT, int NT>
+int launch_short(const Params& p, const PagedDecodeArgs& a, int cluster) {
+  auto kern = decode_paged_kernel<D, FMT, NT, true>;
+  constexpr int kBytes = Smem<D, FMT, NT>::kBytes;
+  static std::atomic<unsigned long long> attr_done{0};  // per instantiation
+  if (!set_smem_limit_once(kern, kBytes, attr_done)) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.groups * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kBytes;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess) return 0;
+  cudaGetLastError();
+  return -1;
+}
+
 template <int D, int FMT, int NT>
 int launch_t(const Params& p, const PagedDecodeArgs& a) {
-  auto kern = decode_paged_kernel<D, FMT, NT>;
+  auto kern = decode_paged_kernel<D, FMT, NT, false>;
   constexpr int kBytes = Smem<D, FMT, NT>::kBytes;
   static std::atomic<unsigned long long> attr_done{0};  // per instantiation
   if (!set_smem_limit_once(kern, kBytes, attr_done)) return -1;
@@ -1075,6 +1204,7 @@ int launch_t(const Params& p, const PagedDecodeArgs& a) {
     fit.store(per_sm, std::memory_order_relaxed);
   }
   int ctas = per_sm * a.num_sms;
+  if (const int cluster = short_cluster<FMT>(p, ctas)) return launch_short<D, FMT, NT>(p, a, cluster);
   if (ctas > p.most_ctas) ctas = p.most_ctas;
   kern<<<ctas, kThreads, kBytes, a.stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return -1;

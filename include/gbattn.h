@@ -511,8 +511,11 @@ size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_
  *            max_pages * page_size) bytes, 16-byte aligned; contents on entry do not matter; calls that may
  *            overlap on the GPU need one each
  * The key axes of all sequences are divided evenly over the GPU, whatever the
- * lengths are, so there is no number of splits to choose; the division follows
- * from the lengths alone and results repeat bitwise.  A score of NaN or +inf
+ * lengths are, so there is no number of splits to choose.  Where max_pages *
+ * page_size is small for the batch (a few hundred to a few thousand tokens), each
+ * sequence and KV head gets blocks of its own instead, which is faster: a page
+ * table that is no wider than the longest sequence needs lets it.  Both divisions
+ * follow from sizes and lengths alone and results repeat bitwise.  A score of NaN or +inf
  * makes its query's o and lse NaN, a score of -inf counts as a masked key, and a
  * NaN or an infinity in a row of v that counts makes its elements of o NaN.
  *

@@ -58,7 +58,11 @@ class Pool:
             return gb.attn_cache_gather(*self.gpu, table, lens, S, **kw)
         return gb.attn_cache_gather_fp4(*self.gpu, table, lens, S, dtype=self.dtype, **self.kw, **kw)
 
+    beyond = 0  # columns that decode() adds to a page table
+
     def decode(self, q, table, lens, **kw):
+        if self.beyond:
+            table = torch.nn.functional.pad(table, (0, self.beyond), value=1 << 30)
         fn = gb.attn_decode_paged if self.bits == 16 else gb.attn_decode_paged_fp4
         return fn(q, *self.gpu, table, lens, **self.kw, **kw)
 
@@ -91,6 +95,14 @@ def _decode_ok(pool, q, table, lens, o, lse, scale, what=""):
             assert ((lse[b] - rl).abs() <= tl).all(), f"{what} sequence {b}: lse"
 
 
+@pytest.fixture(params=["narrow", "wide"])
+def table_width(request, monkeypatch):
+    """What a page table could hold decides how the work is divided: tables as the
+    test makes them, and the same ones with room for far more."""
+    if request.param == "wide":
+        monkeypatch.setattr(Pool, "beyond", 20000)
+
+
 DECODE = [
     # bits, dtype, Hq, Hkv, d, page, lens
     (16, torch.bfloat16, 1, 1, 128, 16, [1]),
@@ -116,6 +128,7 @@ DECODE = [
 ]
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("cfg", DECODE)
 def test_decode(cfg):
     bits, dtype, Hq, Hkv, d, page, lens = cfg
@@ -132,6 +145,7 @@ def test_decode(cfg):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)  # repeats bitwise
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("bits", [16, 4])
 def test_decode_many_short_sequences(bits):
     """More sequences than a block has threads, idle ones among them, lengths on
@@ -145,6 +159,24 @@ def test_decode_many_short_sequences(bits):
     q = torch.randn(len(lens), Hq, 1, d, generator=g).half().cuda()
     o, lse = pool.decode(q, table.cuda(), _i32(lens))
     _decode_ok(pool, q, table, lens, o, lse, 0.125)
+    assert gb.gbattn_device_status() == 0
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,d", [(2, 8, 4, 64), (15, 8, 4, 128), (20, 39, 3, 64), (43, 5, 5, 64), (30, 12, 12, 128)])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_decode_small_batches(bits, B, Hq, Hkv, d):
+    """From few sequences to about as many as there are places for blocks, and an
+    idle one."""
+    g = torch.Generator().manual_seed(28)
+    page = 32
+    lens = torch.randint(1, 600, (B,), generator=g).tolist()
+    lens[0], lens[-1] = 600, 0
+    n_pages = sum((n + page - 1) // page for n in lens)
+    pool = Pool(bits, n_pages, Hkv, page, d, torch.bfloat16, g)
+    table = pu.page_table(lens, page, n_pages, 19, g)
+    q = torch.randn(B, Hq, 1, d, generator=g).bfloat16().cuda()
+    o, lse = pool.decode(q, table.cuda(), _i32(lens))
+    _decode_ok(pool, q, table, lens, o, lse, 1 / math.sqrt(d))
     assert gb.gbattn_device_status() == 0
 
 
@@ -166,6 +198,7 @@ def test_decode_one_long_sequence_among_many(bits, d):
     assert gb.gbattn_device_status() == 0
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("bits", [16, 4])
 def test_decode_rows_behind_the_length_are_not_used(bits):
     """Slots behind each length, unused pages and factors hold NaN."""
@@ -188,6 +221,7 @@ def test_decode_rows_behind_the_length_are_not_used(bits):
     assert torch.isfinite(o2).all() and torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("bits", [16, 4])
 def test_decode_large_scores_and_given_arguments(bits):
     """Scores that grow along the keys by more than the lazy reference allows,
@@ -214,6 +248,7 @@ def test_decode_large_scores_and_given_arguments(bits):
 LAST_KEY = [(2, 4, 2, {16: 17, 4: 33}), (1, 4, 1, {16: 193, 4: 385}), (160, 8, 1, {16: 2048, 4: 2048})]
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("where", ["key", "value"])
 @pytest.mark.parametrize("case", LAST_KEY)
 @pytest.mark.parametrize("bits", [16, 4])
@@ -238,8 +273,7 @@ def test_nan_in_a_row_that_counts(bits, case, where):
         pool.t[1] = torch.ones_like(pool.t[1].float()).to(torch.float8_e4m3fn)
         pool.t[1 if where == "key" else 3].view(torch.uint8)[page, :, slot, 0] = 0x7F  # elements 0 .. 15
     pool.gpu = [t.cuda() for t in pool.t]
-    fn = gb.attn_decode_paged if bits == 16 else gb.attn_decode_paged_fp4
-    o, lse = fn(q.cuda(), *pool.gpu, table.cuda(), _i32([L] * B), scale=4.0, **pool.kw)
+    o, lse = pool.decode(q.cuda(), table.cuda(), _i32([L] * B), scale=4.0)
     o, lse = o.cpu()[:, :, 0], lse.cpu()
     touched = slice(1, None) if B > 1 else slice(None)
     if B > 1:
@@ -253,6 +287,7 @@ def test_nan_in_a_row_that_counts(bits, case, where):
         assert torch.isfinite(lse[touched]).all()
 
 
+@pytest.mark.usefixtures("table_width")
 def test_decode_wide_queries_over_four_bits():
     """bf16 queries far outside fp16's range, whose products the row's scale keeps exact."""
     g = torch.Generator().manual_seed(25)
@@ -487,6 +522,7 @@ def test_paged_decode_agrees_with_the_padded_one():
     assert (l1 - l2).abs().max() <= LSE_MAX_ABS
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("bits", [16, 4])
 def test_streams_graphs_and_two_calls_at_once(bits):
     """A captured step replayed with other lengths, and two calls on two streams
@@ -598,6 +634,7 @@ def test_wrapper_refusals():
     assert gb.gbattn_device_status() == 0
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("bits", [16, 4])
 def test_a_prompt_in_chunks_and_then_tokens(bits):
     """As a program runs them: a prompt in two chunks (norm and rotation, append,
