@@ -8,7 +8,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -155,7 +155,7 @@ struct Output {
   Output& operator=(const Output&) = delete;
   ~Output() { Py_XDECREF(object); }
   void make(Shape shape, at::ScalarType type, const c10::Device& device) {
-    Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(device));
+    Tensor t = at::detail::empty_cuda(shape, type, device, std::nullopt);
     data = t.data_ptr();
     object = THPVariable_Wrap(std::move(t));
     if (object == nullptr) throw python_error();
@@ -187,7 +187,7 @@ struct Workspace {
   size_t bytes = 0;
   void take(PyObject* o, size_t need, const c10::Device& device) {
     if (none(o)) {
-      own = at::empty({static_cast<int64_t>(need > 16 ? need : 16)}, at::TensorOptions().dtype(at::kByte).device(device));
+      own = at::detail::empty_cuda({static_cast<int64_t>(need > 16 ? need : 16)}, at::kByte, device, std::nullopt);
       data = own.data_ptr();
       bytes = need;
       return;
