@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   const int h0 = chunk * p.per_chunk;
   const int h1 = min(h0 + p.per_chunk, p.heads[which]);
 
+  wait_for_previous_kernel();
   const int n_new = p.new_lens != nullptr ? min(p.new_lens[b], p.S) : p.S;
   const long long pos = static_cast<long long>(p.seqlens[b]) - n_new + i;
   const bool real = in_grid && i < n_new && pos >= 0;  // else padding
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_con
   const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
   const int s0 = blockIdx.x * (kRowsPass * kGatherPasses) + threadIdx.x / kParts;
   const int part = threadIdx.x % kParts;
+  wait_for_previous_kernel();
   const int n = min(min(p.seqlens[b], p.max_pages << p.page_shift), p.S);
   int page[kGatherPasses];
 #pragma unroll
@@ -320,12 +322,11 @@ int launch_append_t(const AppendArgs& a) {
   if (token_ctas > 0x7FFFFFFFLL || chunks > 65535) return -1;
   const dim3 grid(static_cast<unsigned>(token_ctas), chunks);
   switch (rope_mode(a.rope, D)) {
-    case kRopeNone: cache_append_kernel<D, BF16, kRopeNone, FP4><<<grid, kThreads, 0, a.stream>>>(p); break;
-    case kRopePairs: cache_append_kernel<D, BF16, kRopePairs, FP4><<<grid, kThreads, 0, a.stream>>>(p); break;
-    case kRopeHalves: cache_append_kernel<D, BF16, kRopeHalves, FP4><<<grid, kThreads, 0, a.stream>>>(p); break;
-    default: cache_append_kernel<D, BF16, kRopePart, FP4><<<grid, kThreads, 0, a.stream>>>(p); break;
+    case kRopeNone: return launch_after(cache_append_kernel<D, BF16, kRopeNone, FP4>, grid, kThreads, a.stream, p);
+    case kRopePairs: return launch_after(cache_append_kernel<D, BF16, kRopePairs, FP4>, grid, kThreads, a.stream, p);
+    case kRopeHalves: return launch_after(cache_append_kernel<D, BF16, kRopeHalves, FP4>, grid, kThreads, a.stream, p);
+    default: return launch_after(cache_append_kernel<D, BF16, kRopePart, FP4>, grid, kThreads, a.stream, p);
   }
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 template <int D, bool BF16, bool FP4>
@@ -350,8 +351,7 @@ int launch_gather_t(const GatherArgs& a) {
   const long long bh = static_cast<long long>(a.B) * a.cache.Hkv;
   if (bh > 65535) return -1;
   const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.S) + kRowsCta - 1) / kRowsCta), static_cast<unsigned>(bh), 2);
-  cache_gather_kernel<D, BF16, FP4><<<grid, kThreads, 0, a.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_after(cache_gather_kernel<D, BF16, FP4>, grid, kThreads, a.stream, p);
 }
 
 }  // namespace

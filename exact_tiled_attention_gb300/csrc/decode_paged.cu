@@ -569,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
   __shared__ long long sm_before;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int r = lane >> 2, q4 = lane & 3;
+  wait_for_previous_kernel();
   if constexpr (!SHORT) let_next_kernel_start();
   const int HG = p.Hkv * p.groups;
   [[maybe_unused]] const uint32_t ring = smem_u32(sm_raw) + warp * C::kRing;
@@ -1077,8 +1078,8 @@ template <int D>
 __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_warp_kernel(const __grid_constant__ Params p) {
   constexpr int kAhead = 4;
   const int row_g = blockIdx.x * (kMergeThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (row_g >= p.B * p.Hq) return;
   wait_for_previous_kernel();
+  if (row_g >= p.B * p.Hq) return;
   const Parts a = parts_of(p, row_g);
   if (a.n == 0 && !a.empty) return;
   const int e = lane * (D / 32);
@@ -1171,20 +1172,8 @@ int launch_short(const Params& p, const PagedDecodeArgs& a, int cluster) {
   constexpr int kBytes = Smem<D, FMT, NT>::kBytes;
   static std::atomic<unsigned long long> attr_done{0};  // per instantiation
   if (!set_smem_limit_once(kern, kBytes, attr_done)) return -1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.groups * cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kBytes;
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess) return 0;
-  cudaGetLastError();
-  return -1;
+  return launch_after(kern, dim3(static_cast<unsigned>(p.B * p.Hkv * p.groups * cluster)), kThreads, a.stream, p, kBytes,
+                      cluster);
 }
 
 template <int D, int FMT, int NT>
@@ -1206,8 +1195,7 @@ int launch_t(const Params& p, const PagedDecodeArgs& a) {
   int ctas = per_sm * a.num_sms;
   if (const int cluster = short_cluster<FMT>(p, ctas)) return launch_short<D, FMT, NT>(p, a, cluster);
   if (ctas > p.most_ctas) ctas = p.most_ctas;
-  kern<<<ctas, kThreads, kBytes, a.stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return -1;
+  if (launch_after(kern, dim3(static_cast<unsigned>(ctas)), kThreads, a.stream, p, kBytes) != 0) return -1;
   // A CTA a row while that is at most four CTAs for each SM.
   const int rows = a.B * a.Hq;
   if (rows <= 4 * a.num_sms)

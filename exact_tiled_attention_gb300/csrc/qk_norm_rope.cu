@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   const int h1 = min(h0 + p.per_chunk, p.heads[which]);
   const int e0 = 8 * lane_in_row;
 
+  wait_for_previous_kernel();
   Ring ring;
   ring.base[0] = p.x[which];
   ring.strides[0] = p.xs[which];
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_bwd_kernel(const __grid
   const int h0 = chunk * p.per_chunk;
   const int h1 = min(h0 + p.per_chunk, p.heads[which]);
   const int e0 = 8 * lane_in_row;
+  wait_for_previous_kernel();
   let_next_kernel_start();
   int pc[2] = {0, 0};
   float w[2][8], dw[2][8];
@@ -331,8 +333,7 @@ int launch_fwd(const NormRopeArgs& a) {
   if (x > token_ctas) x = token_ctas;
   const dim3 grid(static_cast<unsigned>(x), chunks);
   return with_mode(a, [&](auto mode, auto norm) {
-    norm_rope_kernel<D, BF16, decltype(mode)::value, decltype(norm)::value><<<grid, kThreads, 0, a.stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    return launch_after(norm_rope_kernel<D, BF16, decltype(mode)::value, decltype(norm)::value>, grid, kThreads, a.stream, p);
   });
 }
 
@@ -357,8 +358,7 @@ int launch_bwd(const NormRopeArgs& a) {
   if (x > token_ctas) x = token_ctas;
   const dim3 grid(static_cast<unsigned>(x), p.chunks[0] + p.chunks[1]);
   const int rc = with_mode(a, [&](auto mode, auto norm) {
-    norm_rope_bwd_kernel<D, BF16, decltype(mode)::value, decltype(norm)::value><<<grid, kThreads, 0, a.stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    return launch_after(norm_rope_bwd_kernel<D, BF16, decltype(mode)::value, decltype(norm)::value>, grid, kThreads, a.stream, p);
   });
   if (rc != 0 || a.w[0] == nullptr) return rc;
   DwParams dp{};

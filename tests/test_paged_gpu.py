@@ -567,6 +567,65 @@ def test_streams_graphs_and_two_calls_at_once(bits):
 
 
 @pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.usefixtures("table_width")
+def test_calls_after_copies_fills_and_joins(bits):
+    """The operators start early behind the previous kernel of their stream; here
+    what they read and overwrite comes from copies, fills and other streams, eager
+    and captured, and their results are read at once by the next kernel."""
+    g = torch.Generator().manual_seed(45)
+    B, S, Hq, Hkv, d, page, n = 8, 160, 8, 2, 64, 16, 40
+    pool = Pool(bits, B * n, Hkv, page, d, torch.bfloat16, g)
+    table = torch.arange(B * n, dtype=torch.int32, device="cuda").view(B, n)
+    src = [torch.randn(B, h, S, d, generator=g).bfloat16().cuda() for h in (Hq, Hkv, Hkv)]
+    host = [x.cpu().pin_memory() for x in src]
+    w = [1 + 0.1 * torch.randn(d, generator=g).cuda() for _ in "qk"]
+    rope, lens = gb.rope_table(1024, d), _i32([600] * B)
+    x = [torch.empty_like(t) for t in src]
+    dw = [torch.empty(d, device="cuda") for _ in "qk"]
+    side = torch.cuda.Stream()
+
+    def run(join):
+        for t in x:
+            t.zero_()
+        if join:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                for t, h in zip(x, host):
+                    t.copy_(h, non_blocking=True)
+            torch.cuda.current_stream().wait_stream(side)
+        else:
+            for t, h in zip(x, src):
+                t.copy_(h)
+        q, k = gb.attn_qk_norm_rope(x[0], x[1], *w, rope=rope)
+        grads = gb.attn_qk_norm_rope_bwd(q, k, x[0], x[1], *w, rope=rope, dq_weight=dw[0], dk_weight=dw[1])
+        for t in x[:2]:
+            t.fill_(float("nan"))
+        q = pool.append(k, x[2], table, lens, q=q)
+        k.fill_(float("nan"))
+        x[2].zero_()
+        kk, vv = pool.gather(table, lens, 640)
+        o, lse = pool.decode(q[:, :, -1:].contiguous(), table, lens)
+        return [t.clone() for t in (*grads, q, kk, vv, o, lse)]
+
+    ref = run(False)
+    torch.cuda.synchronize()
+    assert all(torch.isfinite(t).all() for t in ref)
+    for join in (False, True):
+        for _ in range(10):
+            assert all(torch.equal(a, b) for a, b in zip(run(join), ref))
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            got = run(join)
+        for _ in range(10):
+            for t in got:
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
 def test_a_given_stream_owns_what_the_call_allocates(bits):
     """Work queued on the current stream right after a call on another one gets
     none of that call's memory: the decode's workspace and outputs are untouched
