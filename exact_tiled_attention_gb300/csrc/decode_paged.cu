@@ -552,10 +552,19 @@ struct Smem {
   static constexpr int kBytes = kWarps * (kRing > kStates ? kRing : kStates);
 };
 
+// CTAs of four warps that an SM holds at least, which bounds the registers.  At the
+// 64-sequence batch, us, with 8 and 16 query heads a unit (in brackets: CTAs):
+//   d = 64, 16 bits: 332 (3), 314 (4), 313 (5) and 442 (2), 351 (3), 331 (4)
+//   d = 64, 4 bits: 121 (4), 127 (5) and 178 (2), 159 (3), 169 (4)
+//   d = 128, 4 bits: 251 (4), 255 (5, spills), earlier, and 266 (2), 279 (3, spills)
+// At d = 128 and 16 bits a lane's rows and sums take 165 and 250 registers.
+template <int D, int FMT, int NT>
+constexpr int kResident = D == 64 ? (FMT == kFp4 ? 5 : 6) - NT : FMT == kFp4 && NT == 1 ? 4 : 4 - NT;
+
 // SHORT: a cluster for each segment, its CTAs take equal runs of the segment's
 // units and fold their states through shared memory.
 template <int D, int FMT, int NT, bool SHORT>
-__global__ void __launch_bounds__(kThreads, FMT == kFp4 && NT == 1 ? 4 : 4 - NT)
+__global__ void __launch_bounds__(kThreads, kResident<D, FMT, NT>)
     decode_paged_kernel(const __grid_constant__ Params p) {
   using C = Smem<D, FMT, NT>;
   constexpr int KB = kBlocks<FMT>, UK = kUnitKeys<FMT>;
