@@ -556,7 +556,7 @@ struct Smem {
 // 64-sequence batch, us, with 8 and 16 query heads a unit (in brackets: CTAs):
 //   d = 64, 16 bits: 332 (3), 314 (4), 313 (5) and 442 (2), 351 (3), 331 (4)
 //   d = 64, 4 bits: 121 (4), 127 (5) and 178 (2), 159 (3), 169 (4)
-//   d = 128, 4 bits: 251 (4), 255 (5, spills), earlier, and 266 (2), 279 (3, spills)
+//   d = 128, 4 bits: 251 (4), 255 (5, spills; before later steps) and 266 (2), 279 (3, spills)
 // At d = 128 and 16 bits a lane's rows and sums take 165 and 250 registers.
 template <int D, int FMT, int NT>
 constexpr int kResident = D == 64 ? (FMT == kFp4 ? 5 : 6) - NT : FMT == kFp4 && NT == 1 ? 4 : 4 - NT;
@@ -1146,7 +1146,7 @@ int max_ctas(int B, size_t heads, int max_len) {
 // CTAs of a cluster that takes a whole segment, or 0 where the list of all units is
 // divided instead.  The host knows what the pages of a sequence can hold, not the
 // lengths, so a cluster is for tables of few units: it saves the division and the
-// second kernel (6.5 -> 4.8 us for one sequence of 4 units, 10.4 -> 7 us of host
+// second kernel (6.4 -> 4.7 us for one sequence of 4 units, 10.4 -> 7 us of host
 // time), and loses where one cluster has much more to do than a CTA's even share,
 // half of which is taken off for ragged batches.  Measured with 32 heads on 8,
 // d = 128, 16 bits, us (list against clusters), lengths of 0 up to what the table
