@@ -11,12 +11,12 @@
 // those of the same formula evaluated anywhere in fp32.
 //
 // Both are bound by HBM, or, for one token a sequence, by the launch (64 tokens of
-// 32 + 16 heads: 4.1 us).  A row is read once and written once; a thread keeps one
-// token's angles and place and walks over heads.  Eight ragged prompts of up to
-// 4096 tokens into 16 bits take 80 us, 6.5 TB/s; chunks of 1500 to 2048 tokens of
-// four sequences into 4 bits 29 us, 5.4 TB/s.  Reading those back, 16384 tokens
-// each, is nearly all writes: 50 us, 6.3 TB/s, of which 5.3 are written (a fill
-// of the same memory reaches 4.0).
+// 32 + 16 heads: 1.7 us one behind another, 4.1 alone from memory).  A row is read
+// once and written once; a thread keeps one token's angles and place and walks over
+// heads.  Eight ragged prompts of up to 4096 tokens into 16 bits, 526 MB in all, take
+// 88 us, 6.0 TB/s; chunks of 2048 tokens of four sequences into 4 bits 34 us, 5.2
+// TB/s.  Reading contexts of up to 16384 tokens of four sequences back is nearly all
+// writes: 50 us, 5.4 TB/s written (a fill of the same memory reaches 4.0).
 #include <cuda_runtime.h>
 
 #include "gbattn_rows.cuh"
@@ -97,8 +97,17 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   const bool in_grid = at < tokens;
   const int t = min(at, tokens - 1);  // the whole warp stays for the shuffles
   const int b = t / p.S, i = t % p.S;
-  int which = 0, chunk = blockIdx.y;  // 0: queries, 1: keys, 2: values
-  while (which < 2 && chunk >= p.chunks[which]) chunk -= p.chunks[which++];
+  // 0: queries, 1: keys, 2: values.  The CTAs that quantise take longest and start
+  // first ([5, 1434] tokens of 40 + 16 heads, d = 64: 19.9 -> 17.4 us; four chunks of
+  // 2048 tokens 34.3 -> 34.1); in 16 bits that order costs (33.3 -> 35.9).
+  int which = 0, chunk = blockIdx.y;
+  if constexpr (FP4) {
+    const int kv = p.chunks[1] + p.chunks[2];
+    which = chunk < p.chunks[1] ? 1 : chunk < kv ? 2 : 0;
+    chunk -= which == 1 ? 0 : which == 2 ? p.chunks[1] : kv;
+  } else {
+    while (which < 2 && chunk >= p.chunks[which]) chunk -= p.chunks[which++];
+  }
   const int h0 = chunk * p.per_chunk;
   const int h1 = min(h0 + p.per_chunk, p.heads[which]);
 
