@@ -14,7 +14,7 @@
 // 32 + 16 heads: 1.7 us one behind another, 4.1 alone from memory).  A row is read
 // once and written once; a thread keeps one token's angles and place and walks over
 // heads.  Eight ragged prompts of up to 4096 tokens into 16 bits, 526 MB in all, take
-// 88 us, 6.0 TB/s; chunks of 2048 tokens of four sequences into 4 bits 34 us, 5.2
+// 88 us, 6.0 TB/s; chunks of 2048 tokens of four sequences into 4 bits 31 us, 5.7
 // TB/s.  Reading contexts of up to 16384 tokens of four sequences back is nearly all
 // writes: 50 us, 5.4 TB/s written (a fill of the same memory reaches 4.0).
 #include <cuda_runtime.h>
@@ -86,8 +86,15 @@ __device__ __forceinline__ uint32_t quantise8(const float (&z)[8], float descale
   return e2m1x8(y);
 }
 
+// CTAs that an SM holds at least, which bounds the registers (64 and 72).  Without
+// it and with one more each, us: [1, 2094] tokens of 64 + 8 heads in 16 bits 11.7, here
+// 10.5, more 13.0 (spills); [4, 2048] of 32 + 16 in 4 bits 34.0, 31.2, 31.7.  A
+// partial rotation holds its partners too and would spill.
+template <int MODE, bool FP4>
+constexpr int kResident = MODE == kRopePart ? 1 : FP4 ? 7 : 8;
+
 template <int D, bool BF16, int MODE, bool FP4>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, kResident<MODE, FP4>) cache_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = RowCfg<D>::kLanes;
   constexpr int kRowsCta = kThreads / kLanes;
   const int lane_in_row = threadIdx.x % kLanes;
@@ -98,8 +105,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   const int t = min(at, tokens - 1);  // the whole warp stays for the shuffles
   const int b = t / p.S, i = t % p.S;
   // 0: queries, 1: keys, 2: values.  The CTAs that quantise take longest and start
-  // first ([5, 1434] tokens of 40 + 16 heads, d = 64: 19.9 -> 17.4 us; four chunks of
-  // 2048 tokens 34.3 -> 34.1); in 16 bits that order costs (33.3 -> 35.9).
+  // first ([5, 1434] tokens of 40 + 16 heads, d = 64: 19.9 -> 17.4 us); in 16 bits that order costs (33.3 -> 35.9).
   int which = 0, chunk = blockIdx.y;
   if constexpr (FP4) {
     const int kv = p.chunks[1] + p.chunks[2];
