@@ -21,7 +21,7 @@
 // keys, takes one byte permute for two elements.
 //
 // 16 bits: rows go from global memory straight into operand registers, requested
-// as the previous piece's are consumed.  Bound by HBM: 64 sequences of 1024 to
+// as an earlier piece's are consumed (kDepth).  Bound by HBM: 64 sequences of 1024 to
 // 32768 tokens, 32 heads on 8, d = 128, take 680 us, 7.0 TB/s.
 // 4 bits: rows go through a ring in shared memory that asynchronous copies fill.
 // A pair of codes becomes an fp16 pair in one conversion, one product applies the
@@ -436,6 +436,15 @@ struct Tile<D, kFp4> {
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 3;
 
+// Units whose rows of a 16-bit cache a warp holds or has on their way.  At d = 128 two
+// take the registers of a third CTA on an SM (four sequences of 4000 tokens in
+// clusters: 15.4 -> 17.4 us, one of 8000 19.7 -> 16.0, where the list takes 12); at
+// d = 64 24 sequences of 2000 tokens, 64 heads on 8, take 21.2 us with one and 18.6
+// with two, and the list with 16 heads a unit 331 and 326 at the large batch, but
+// with 8 heads 313 and 324.
+template <int D, int NT, bool SHORT>
+constexpr int kDepth = D == 64 && (SHORT || NT == 2) ? 2 : 1;
+
 // Blocks of 16 keys that a warp works on at a time.
 template <int FMT>
 constexpr int kBlocks = FMT == kFp4 ? 2 : 1;
@@ -554,17 +563,18 @@ struct Smem {
 
 // CTAs of four warps that an SM holds at least, which bounds the registers.  At the
 // 64-sequence batch, us, with 8 and 16 query heads a unit (in brackets: CTAs):
-//   d = 64, 16 bits: 332 (3), 314 (4), 313 (5) and 442 (2), 351 (3), 331 (4)
+//   d = 64, 16 bits: 332 (3), 314 (4), 313 (5) and 361 (2), 326 (3)
 //   d = 64, 4 bits: 121 (4), 127 (5) and 178 (2), 159 (3), 169 (4)
 //   d = 128, 4 bits: 251 (4), 255 (5, spills; before later steps) and 266 (2), 279 (3, spills)
 // At d = 128 and 16 bits a lane's rows and sums take 165 and 250 registers.
-template <int D, int FMT, int NT>
-constexpr int kResident = D == 64 ? (FMT == kFp4 ? 5 : 6) - NT : FMT == kFp4 && NT == 1 ? 4 : 4 - NT;
+template <int D, int FMT, int NT, bool SHORT>
+constexpr int kResident = D == 64 ? (FMT != kFp4 && kDepth<D, NT, SHORT> == 1 ? 6 : 5) - NT
+                                  : FMT == kFp4 && NT == 1 ? 4 : 4 - NT;
 
 // SHORT: a cluster for each segment, its CTAs take equal runs of the segment's
 // units and fold their states through shared memory.
 template <int D, int FMT, int NT, bool SHORT>
-__global__ void __launch_bounds__(kThreads, kResident<D, FMT, NT>)
+__global__ void __launch_bounds__(kThreads, kResident<D, FMT, NT, SHORT>)
     decode_paged_kernel(const __grid_constant__ Params p) {
   using C = Smem<D, FMT, NT>;
   constexpr int KB = kBlocks<FMT>, UK = kUnitKeys<FMT>;
@@ -759,7 +769,6 @@ __global__ void __launch_bounds__(kThreads, kResident<D, FMT, NT>)
     }
 
     // ---- the keys: piece 4 i + warp, of KB blocks of 16 keys, of every unit i
-    Tile<D, FMT> tl;
     const int* pages = p.page_table + static_cast<long long>(b) * p.max_pages;
     const int warp_keys = L - warp * (16 * KB);  // keys from this warp's first one on
     const int end = min(tile_end, (warp_keys + UK - 1) / UK);
@@ -780,6 +789,7 @@ __global__ void __launch_bounds__(kThreads, kResident<D, FMT, NT>)
       return -1;
     };
     if constexpr (FMT == kFp4) {
+      Tile<D, FMT> tl;
       // kStages<D> - 1 units are on their way while one is worked on.
       int page0 = page_of((tile * kWarps + warp) * KB), page1 = page_of((tile * kWarps + warp) * KB + 1);
       unsigned absent = 0;  // two bits a request, the newest lowest: block k has no page
@@ -837,33 +847,47 @@ __global__ void __launch_bounds__(kThreads, kResident<D, FMT, NT>)
       }
       copy_wait<0>();
     } else {
-      // A unit's K is requested right after the previous unit's scores and its V
-      // right after the previous P V, into the registers that those have freed.
-      int n_keys[1] = {0}, page_next = 0;
-      if (tile < end) {
-        const int blk = tile * kWarps + warp, block = block_of(blk, page_of(blk));
-        n_keys[0] = block < 0 ? 0 : L - 16 * blk;
-        page_next = page_of(blk + kWarps);
-        tl.load_k(src, block, lane, n_keys[0]);
-        tl.load_v(src, block, lane, n_keys[0]);
+      // A unit's K is requested right after the scores of the unit whose registers it
+      // takes, and its V right after that one's P V.
+      constexpr int kAhead = kDepth<D, NT, SHORT>;
+      Tile<D, FMT> tl[kAhead];
+      int n_keys[kAhead][1], page[kAhead] = {};  // page: of the unit kAhead further
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (tile + k < end) page[k] = page_of((tile + k) * kWarps + warp);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        n_keys[k][0] = 0;
+        if (tile + k < end) {
+          const int blk = (tile + k) * kWarps + warp, block = block_of(blk, page[k]);
+          n_keys[k][0] = block < 0 ? 0 : L - 16 * blk;
+          page[k] = page_of(blk + kAhead * kWarps);
+          tl[k].load_k(src, block, lane, n_keys[k][0]);
+          tl[k].load_v(src, block, lane, n_keys[k][0]);
+        }
       }
       load_q();
-      for (int i = tile; i < end; ++i) {
-        float s[1][NT][4];
-        uint32_t pf[1][NT][kTerms<FMT>][2];
-        tl.template scores<NT>(s[0], qf);
-        int n_next = 0, block = 0;
-        if (i + 1 < end) {
-          const int blk = (i + 1) * kWarps + warp;
-          block = block_of(blk, page_next);
-          n_next = block < 0 ? 0 : L - 16 * blk;
-          page_next = page_of(blk + kWarps);
-          tl.load_k(src, block, lane, n_next);
+      for (int i0 = tile; i0 < end; i0 += kAhead) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int i = i0 + k;
+          if (k > 0 && i >= end) break;
+          float s[1][NT][4];
+          uint32_t pf[1][NT][kTerms<FMT>][2];
+          tl[k].template scores<NT>(s[0], qf);
+          int n_next = 0, block = 0;
+          if (i + kAhead < end) {
+            const int blk = (i + kAhead) * kWarps + warp;
+            block = block_of(blk, page[k]);
+            n_next = block < 0 ? 0 : L - 16 * blk;
+            page[k] = page_of(blk + kAhead * kWarps);
+            tl[k].load_k(src, block, lane, n_next);
+          }
+          softmax_step<D, FMT, false, 1, NT>(s, lam, r, n_keys[k], m, l, o, pf);
+          tl[k].template values<NT>(o, pf[0]);
+          if (i + kAhead < end) tl[k].load_v(src, block, lane, n_next);
+          n_keys[k][0] = n_next;
         }
-        softmax_step<D, FMT, false, 1, NT>(s, lam, r, n_keys, m, l, o, pf);
-        tl.template values<NT>(o, pf[0]);
-        if (i + 1 < end) tl.load_v(src, block, lane, n_next);
-        n_keys[0] = n_next;
       }
     }
 
@@ -1174,37 +1198,39 @@ int short_cluster(const Params& p, int ctas) {
   return units * (2 * ctas - segments * cluster) <= (cluster == 1 ? 16LL : 8LL) * ctas * cluster ? cluster : 0;
 }
 
-// A cluster for each (sequence, unit of query heads).
-template <int D, int FMT, int NT>
-int launch_short(const Params& p, const PagedDecodeArgs& a, int cluster) {
-  auto kern = decode_paged_kernel<D, FMT, NT, true>;
+// CTAs of a kernel that fit on an SM; the same on every GPU this library runs on.
+template <int D, int FMT, int NT, bool SHORT>
+int resident() {
   constexpr int kBytes = Smem<D, FMT, NT>::kBytes;
   static std::atomic<unsigned long long> attr_done{0};  // per instantiation
-  if (!set_smem_limit_once(kern, kBytes, attr_done)) return -1;
-  return launch_after(kern, dim3(static_cast<unsigned>(p.B * p.Hkv * p.groups * cluster)), kThreads, a.stream, p, kBytes,
-                      cluster);
+  static std::atomic<int> fit{0};
+  auto kern = decode_paged_kernel<D, FMT, NT, SHORT>;
+  if (!set_smem_limit_once(kern, kBytes, attr_done)) return 0;
+  int n = fit.load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, kBytes) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      return 0;
+    }
+    fit.store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 template <int D, int FMT, int NT>
 int launch_t(const Params& p, const PagedDecodeArgs& a) {
-  auto kern = decode_paged_kernel<D, FMT, NT, false>;
-  constexpr int kBytes = Smem<D, FMT, NT>::kBytes;
-  static std::atomic<unsigned long long> attr_done{0};  // per instantiation
-  if (!set_smem_limit_once(kern, kBytes, attr_done)) return -1;
-  // CTAs that fit on an SM; the same on every GPU this library runs on.
-  static std::atomic<int> fit{0};
-  int per_sm = fit.load(std::memory_order_relaxed);
-  if (per_sm == 0) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, kBytes) != cudaSuccess || per_sm < 1) {
-      cudaGetLastError();
-      return -1;
-    }
-    fit.store(per_sm, std::memory_order_relaxed);
-  }
-  int ctas = per_sm * a.num_sms;
-  if (const int cluster = short_cluster<FMT>(p, ctas)) return launch_short<D, FMT, NT>(p, a, cluster);
-  if (ctas > p.most_ctas) ctas = p.most_ctas;
-  if (launch_after(kern, dim3(static_cast<unsigned>(ctas)), kThreads, a.stream, p, kBytes) != 0) return -1;
+  const int short_fit = resident<D, FMT, NT, true>();
+  if (short_fit == 0) return -1;
+  if (const int cluster = short_cluster<FMT>(p, short_fit * a.num_sms))
+    return launch_after(decode_paged_kernel<D, FMT, NT, true>,
+                        dim3(static_cast<unsigned>(p.B * p.Hkv * p.groups * cluster)), kThreads, a.stream, p,
+                        Smem<D, FMT, NT>::kBytes, cluster);
+  const int fit = resident<D, FMT, NT, false>();
+  if (fit == 0) return -1;
+  const int ctas = fit * a.num_sms < p.most_ctas ? fit * a.num_sms : p.most_ctas;
+  if (launch_after(decode_paged_kernel<D, FMT, NT, false>, dim3(static_cast<unsigned>(ctas)), kThreads, a.stream, p,
+                   Smem<D, FMT, NT>::kBytes) != 0)
+    return -1;
   // A CTA a row while that is at most four CTAs for each SM.
   const int rows = a.B * a.Hq;
   if (rows <= 4 * a.num_sms)
