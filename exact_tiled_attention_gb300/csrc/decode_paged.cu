@@ -82,9 +82,11 @@ __device__ __forceinline__ int seq_len(const Params& p, int b) {
   return max(0, min(p.seqlens[b], cap));
 }
 
+// Not a read-only load: the previous kernel may write the cache while this one has
+// already started (and waits).
 __device__ __forceinline__ uint4 ld16(const uint8_t* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -778,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, kResident<D, FMT, NT, SHORT>)
     const int last_block = (L - 1) >> 4;
     // Page of a block of the sequence (behind the last: the last one's), and the
     // pool's block, or -1 for a page that does not exist: its keys are left out.
-    auto page_of = [&](int blk) { return __ldg(pages + (min(blk, last_block) >> block_shift)); };
+    auto page_of = [&](int blk) { return pages[min(blk, last_block) >> block_shift]; };
     auto exists = [&](int page) { return static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages); };
     auto block_at = [&](int blk, int page) {
       return page * page_blocks + head_block + (blk & ((1 << block_shift) - 1));
