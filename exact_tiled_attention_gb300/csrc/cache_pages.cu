@@ -172,10 +172,8 @@ __global__ void __launch_bounds__(kThreads, kResident<MODE, FP4>) cache_append_k
       if (which != 2) {
         if constexpr (MODE == kRopePart) {
           uint4 other[2] = {};
-          if (real) {
-            other[0] = *reinterpret_cast<const uint4*>(xrow + pc[0]);
-            other[1] = *reinterpret_cast<const uint4*>(xrow + pc[1]);
-          }
+          if (real && rope.turns[0]) other[0] = *reinterpret_cast<const uint4*>(xrow + pc[0]);
+          if (real && rope.turns[1]) other[1] = *reinterpret_cast<const uint4*>(xrow + pc[1]);
           unpack8<BF16>(other[0], part[0]);
           unpack8<BF16>(other[1], part[1]);
           __syncwarp();  // q_out may be q: the row's other lanes write what this one has just read

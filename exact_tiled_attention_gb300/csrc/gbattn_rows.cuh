@@ -58,20 +58,22 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
 
 // The rotation of one token, held by the lane for its own elements: for element
 // e of chunk c, y = x * cos + partner * sin, with sin already negative for the
-// first element of a pair.
+// first element of a pair.  Chunks behind the rotated part do not turn: an angle of
+// zero would make NaN of an infinity there (x + inf * 0) and of its neighbour.
 struct LaneRope {
   float cos[2][8];
   float sin[2][8];
+  bool turns[2];  // (a full rotation by halves turns both chunks and does not ask)
 };
 
-// Loads the lane's cosines and sines of a table row.  Chunks outside the
-// rotated part get (1, 0).
+// Loads the lane's cosines and sines of a table row.
 template <int D, int MODE>
 __device__ __forceinline__ void load_rope(LaneRope& r, const float* row, int rot, int lane_in_row) {
   const int half = rot / 2;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int e0 = c * (D / 2) + 8 * lane_in_row;
+    r.turns[c] = e0 < rot;
     if constexpr (MODE == kRopeHalves) {
       if (c == 0) {
         load8(row + e0, r.cos[0]);
@@ -97,9 +99,6 @@ __device__ __forceinline__ void load_rope(LaneRope& r, const float* row, int rot
           for (int i = 0; i < 8; ++i) r.sin[c][i] = -r.sin[c][i];
         }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r.cos[c][i] = 1.f, r.sin[c][i] = 0.f;
     }
   }
 }
@@ -188,21 +187,25 @@ __device__ __forceinline__ void rotate(float (&z)[2][8], const float (&part)[2][
     }
   } else if constexpr (MODE == kRopePairs) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < 2; ++c) {
+      if (!r.turns[c]) continue;
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
         const float a = z[c][i], b = z[c][i + 1], co = r.cos[c][i], s = BACK ? r.sin[c][i] : r.sin[c][i + 1];
         z[c][i] = __fsub_rn(__fmul_rn(a, co), __fmul_rn(b, s));
         z[c][i + 1] = __fadd_rn(__fmul_rn(b, co), __fmul_rn(a, s));
       }
+    }
   } else if constexpr (MODE == kRopePart) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < 2; ++c) {
+      if (!r.turns[c]) continue;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float s = BACK ? -r.sin[c][i] : r.sin[c][i];
         z[c][i] = __fadd_rn(__fmul_rn(z[c][i], r.cos[c][i]), __fmul_rn(part[c][i], s));
       }
+    }
   }
 }
 

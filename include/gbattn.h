@@ -355,7 +355,8 @@ size_t attn_decode_noalloc_scratch_bytes(void);
  * rope [rope_rows, rot_dim] fp32: row p holds the rot_dim / 2 cosines and then
  * the rot_dim / 2 sines of position p.  It pairs elements (i, i + rot_dim / 2),
  * or (2 i, 2 i + 1) where `interleaved` is not 0:
- *   (a, b) -> (a cos - b sin, b cos + a sin), in fp32.
+ *   (a, b) -> (a cos - b sin, b cos + a sin), in fp32.  The other elements pass as they
+ * are, infinities, NaN and signs of zeros included.
  *
  * q_strides, k_strides, ... are NULL for a contiguous [B, heads, S, d] tensor,
  * or three host values: the distances, in elements, of consecutive sequences,
