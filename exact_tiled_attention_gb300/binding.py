@@ -500,7 +500,8 @@ def gbattn_timeline_set(records) -> None:
 
 
 def gbattn_device_status() -> int:
-    """Synchronise and read/clear the kernels' status word (0 = ok)."""
+    """Synchronise and read/clear the kernels' status (0 = ok).  A timeout is
+    returned before an index outside its table, which the next call then returns."""
     return int(load_library().gbattn_device_status())
 
 

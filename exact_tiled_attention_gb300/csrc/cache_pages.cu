@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, kResident<MODE, FP4>) cache_append_k
     const int page = pg < p.max_pages ? p.page_table[static_cast<long long>(b) * p.max_pages + pg] : -1;
     if (page < 0 || page >= p.n_pages) {
       stored = false;
-      atomicCAS(p.status, 0, kStatusIndex);
+      report_index(p.status);
     } else {
       slot = ((static_cast<long long>(page) * p.heads[1]) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
     }
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, kResident<MODE, FP4>) cache_append_k
     if (which != 2) {
       long long row = real ? pos : 0;
       if (row >= p.table_rows) {
-        atomicCAS(p.status, 0, kStatusIndex);
+        report_index(p.status);
         row = p.table_rows - 1;
       }
       load_rope<D, MODE>(rope, p.table + row * p.rot, p.rot, lane_in_row);
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_con
         y[u] = *reinterpret_cast<const uint4*>(data + row * kRow);
       }
     } else if (s < n) {
-      atomicCAS(p.status, 0, kStatusIndex);
+      report_index(p.status);
     }
   }
   const float ds = FP4 && p.descale[which] != nullptr ? p.descale[which][h] : 1.f;

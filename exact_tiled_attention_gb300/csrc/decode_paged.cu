@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, kResident<D, FMT, NT, SHORT>)
     };
     auto block_of = [&](int blk, int page) {
       if (exists(page)) return block_at(blk, page);
-      if (lane == 0) atomicCAS(p.status, 0, kStatusIndex);
+      if (lane == 0) report_index(p.status);
       return -1;
     };
     if constexpr (FMT == kFp4) {
@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, kResident<D, FMT, NT, SHORT>)
           const int blk = (i * kWarps + warp) * KB;
           int block[KB] = {block_at(blk, page0), block_at(blk + 1, page1)};
           if (!exists(page0) || !exists(page1)) {
-            if (lane == 0) atomicCAS(p.status, 0, kStatusIndex);
+            if (lane == 0) report_index(p.status);
             absent |= (exists(page0) ? 0u : 1u) | (exists(page1) ? 0u : 2u);
             // What is copied instead does not matter.
             if (!exists(page0)) block[0] = 0;

@@ -13,8 +13,9 @@
 
 namespace gbattn {
 
-// Device status word written by the kernels' bounded waits (0 = ok).
-__device__ int g_device_status;
+// Device status (0 = ok): the word written by the kernels' bounded waits, and that
+// of pages, slots and positions outside their tables.
+__device__ int g_device_status[kStatusWords];
 
 namespace {
 
@@ -569,15 +570,17 @@ int gbattn_device_status(void) {
     cudaGetLastError();
     return GBATTN_ELAUNCH;
   }
-  int value = 0;
-  if (cudaMemcpyFromSymbol(&value, g_device_status, sizeof(int)) != cudaSuccess) {
+  int value[kStatusWords] = {};
+  if (cudaMemcpyFromSymbol(value, g_device_status, sizeof(value)) != cudaSuccess) {
     cudaGetLastError();
     return GBATTN_ELAUNCH;
   }
-  if (value != 0) {
+  // One report a call, the more serious one first; the other stays for the next.
+  for (int i = 0; i < kStatusWords; ++i) {
+    if (value[i] == 0) continue;
     const int zero = 0;
-    cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
-    return value == kStatusIndex ? GBATTN_EINDEX : GBATTN_EDEVICE_TIMEOUT;
+    cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int), i * sizeof(int));
+    return i == kStatusIndexWord ? GBATTN_EINDEX : GBATTN_EDEVICE_TIMEOUT;
   }
   return GBATTN_OK;
 }

@@ -88,9 +88,12 @@ struct PrefillFp8Args {
   long long timeline_capacity;     // records the buffer holds
 };
 
-// Device status word: a page, slot or position outside its table (the host maps
-// it to GBATTN_EINDEX).  One above the codes of DeviceStatus in gbattn_ptx.cuh.
-constexpr int kStatusIndex = 9;
+// The device status is two words, so that neither hides the other: the first code
+// of a kernel that gave up (DeviceStatus in gbattn_ptx.cuh), and whether a kernel
+// met a page, slot or position outside its table.  `status` in the arguments below
+// points to the first.
+constexpr int kStatusWords = 2;
+constexpr int kStatusIndexWord = 1;
 
 // Element strides of a [batch, heads, seq, d] tensor whose rows of d elements
 // are contiguous.
@@ -295,6 +298,9 @@ inline int launch_after(void (*kernel)(Params), dim3 grid, int threads, cudaStre
 }
 
 #ifdef __CUDACC__
+// Reports a page, slot or position outside its table (GBATTN_EINDEX).
+__device__ __forceinline__ void report_index(int* status) { atomicExch(status + kStatusIndexWord, 1); }
+
 __device__ __forceinline__ void let_next_kernel_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -50,7 +50,7 @@ struct NormRopeParams {
 __device__ __forceinline__ const float* table_row(const NormRopeParams& p, int b, int s) {
   int pos = p.positions != nullptr ? p.positions[static_cast<long long>(b) * p.S + s] : s;
   if (pos < 0 || pos >= p.table_rows) {
-    atomicCAS(p.status, 0, kStatusIndex);
+    report_index(p.status);
     pos = min(max(pos, 0), p.table_rows - 1);
   }
   return p.table + static_cast<long long>(pos) * p.rot;

@@ -582,14 +582,15 @@ int gbattn_exp2_paths(const float *x, float *y_poly, float *y_hw, long long n, v
 int gbattn_selftest_bounded_wait(int arrive, void *stream);
 
 /*
- * gbattn_device_status -- read and clear the library's device status word.
- * Returns GBATTN_OK, or GBATTN_EINDEX if a kernel met a page, slot or position
- * outside its table, or GBATTN_EDEVICE_TIMEOUT if a kernel gave up since the
- * last call (a bounded wait timed out, or a shared-memory alignment check
- * failed), or GBATTN_ELAUNCH if the device reported an error.
+ * gbattn_device_status -- read and clear the library's device status.
+ * Returns GBATTN_OK, or GBATTN_EDEVICE_TIMEOUT if a kernel gave up (a bounded
+ * wait timed out, or a shared-memory alignment check failed), or GBATTN_EINDEX if
+ * a kernel met a page, slot or position outside its table, or GBATTN_ELAUNCH if
+ * the device reported an error.  The two reports are kept apart: where both are
+ * there, one call returns and clears EDEVICE_TIMEOUT and the next one EINDEX.
  *
  * Scope: the call synchronises the whole current device
- * (cudaDeviceSynchronize, every stream), and the word is one per device,
+ * (cudaDeviceSynchronize, every stream), and the status is one per device,
  * shared by all streams and host threads that use the library there.  A
  * failure raised by a kernel on one stream is therefore reported to
  * whichever caller polls first, and that call clears it; callers that share

@@ -1,9 +1,10 @@
 """Edges of the operators around a paged cache on the GPU: what stands behind a
-partial rotation."""
+partial rotation, and reports of two kinds at once."""
 import pytest
 import torch
 
 import exact_tiled_attention_gb300 as gb
+from exact_tiled_attention_gb300.binding import GBATTN_EDEVICE_TIMEOUT, GBATTN_EINDEX
 from tests import paged_util as pu
 
 pytestmark = pytest.mark.gpu
@@ -101,4 +102,22 @@ def test_append_behind_the_rotation(bits, d, dtype, rot, interleaved):
             assert torch.equal(pool[2 * i][1, :, :S].cpu(), codes)
             assert torch.equal(pool[2 * i + 1][1, :, :S].cpu(), factors.view(torch.uint8))
     assert _same(out[..., rot:].cpu(), q[..., rot:]) and torch.isfinite(out[..., :rot]).all()
+    assert gb.gbattn_device_status() == 0
+
+
+@pytest.mark.parametrize("first", ["index", "timeout"])
+def test_an_index_report_does_not_hide_a_timeout(first):
+    """A position outside the table and a wait that gives up, in either order: both
+    are reported, the timeout first, and then the word reads clear."""
+    gb.gbattn_device_status()
+    q, k = (torch.randn(1, h, 3, 64, device="cuda").half() for h in (2, 1))
+    rope = gb.rope_table(3, 64)
+    pos = _i32([[0, 1, 7]])
+    if first == "index":
+        gb.attn_qk_norm_rope(q, k, rope=rope, positions=pos)
+    gb.gbattn_selftest_bounded_wait(False)
+    if first == "timeout":
+        gb.attn_qk_norm_rope(q, k, rope=rope, positions=pos)
+    assert gb.gbattn_device_status() == GBATTN_EDEVICE_TIMEOUT
+    assert gb.gbattn_device_status() == GBATTN_EINDEX
     assert gb.gbattn_device_status() == 0
