@@ -70,13 +70,15 @@ __device__ __forceinline__ __half2 e2m1x2_half2(uint32_t codes) {
 }
 
 // One chunk of 8 elements to 4 bits; the other half of its group of 16 is the
-// neighbouring lane's.
+// neighbouring lane's.  Magnitudes are compared as integers, where a NaN is above
+// infinity, so it goes through the maximum; the factor's bound then gives 448 and
+// the conversion 6, as for infinity.
 __device__ __forceinline__ uint32_t quantise8(const float (&z)[8], float descale, uint8_t& factor) {
-  float m = 0.f;
+  uint32_t top = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(z[i]));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  const float f = fminf(__fdiv_rn(m, __fmul_rn(6.f, descale)), 448.f);
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(z[i]) & 0x7FFFFFFFu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const float f = fminf(__fdiv_rn(__uint_as_float(top), __fmul_rn(6.f, descale)), 448.f);  // NaN: 448
   factor = static_cast<uint8_t>(pack4_e4m3(f, 0.f, 0.f, 0.f) & 0xFF);
   const float fv = __half2float(e4m3_half(factor));
   const float inv = fv > 0.f ? __frcp_rn(__fmul_rn(fv, descale)) : 0.f;

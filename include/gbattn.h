@@ -458,9 +458,11 @@ int attn_cache_append(const void *k, const void *v, void *k_cache, void *v_cache
  * group of 16 elements x (keys after the rotation, in fp32) gets
  *   factor = E4M3(min(448, max|x| / (6 descale))),
  *   code   = E2M1(x * (1 / (factor * descale)))
- * both rounded to nearest even and saturating; factor 0 gives codes 0.  NaN has
- * no code: it is stored as a number.  The codes and factors are those of the
- * formula in IEEE fp32 arithmetic, whatever order the tokens come in.
+ * both rounded to nearest even and saturating.  The codes have no NaN and no
+ * infinity: a NaN counts as +infinity, which gives its group the factor 448 and
+ * itself the code 6, so it reads back as 2688 descale (a 16-bit cache keeps both).
+ * The codes and factors are those of the formula in IEEE fp32 arithmetic, whatever
+ * order the tokens come in.
  *
  * Errors: as attn_cache_append.
  */

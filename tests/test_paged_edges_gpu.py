@@ -1,5 +1,5 @@
 """Edges of the operators around a paged cache on the GPU: what stands behind a
-partial rotation, and reports of two kinds at once."""
+partial rotation, reports of two kinds at once, and values that 4 bits cannot hold."""
 import pytest
 import torch
 
@@ -121,3 +121,34 @@ def test_an_index_report_does_not_hide_a_timeout(first):
     assert gb.gbattn_device_status() == GBATTN_EDEVICE_TIMEOUT
     assert gb.gbattn_device_status() == GBATTN_EINDEX
     assert gb.gbattn_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_four_bits_of_nan(d, dtype):
+    """NaN counts as the largest value, as infinity does: its group's factor is 448
+    and its own code 6, whatever else the group holds and whichever lane has it; it
+    reads back as 2688 descale and not as a number like its neighbours'."""
+    n = d // 16
+    k = torch.zeros(1, 1, 4 * 16, d, dtype=dtype)
+    for i in range(16):
+        for j, other in enumerate((0.0, -1.0, 60000.0, -INF)):
+            group = k[0, 0, 4 * i + j].view(n, 16)[(i + j) % n]
+            group[:] = other
+            group[i] = -NAN if j % 2 else NAN
+    descale = torch.full((1,), 0.25)
+    codes = [torch.zeros(4, 1, 16, d // 2, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    factors = [torch.full((4, 1, 16, n), 9, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    table, lens = _i32([[2, 0, 3, 1]]), _i32([64])
+    args = dict(k_descale=descale.cuda(), v_descale=descale.cuda())
+    gb.attn_cache_append_fp4(k.cuda(), k.cuda(), codes[0], factors[0], codes[1], factors[1], table, lens, **args)
+    # the formula with an infinity in each NaN's place
+    ref_codes, ref_factors = pu.quantise(torch.where(torch.isnan(k[0, 0]), INF, k[0, 0].float()), 0.25)
+    for c, f in zip(codes, factors):
+        assert torch.equal(c[table[0].long()].flatten(0, 2).cpu(), ref_codes)
+        assert torch.equal(f[table[0].long()].flatten(0, 2).cpu(), ref_factors.view(torch.uint8))
+    got, _ = gb.attn_cache_gather_fp4(codes[0], factors[0], codes[1], factors[1], table, lens, 64, dtype=dtype, **args)
+    nan = torch.isnan(k[0, 0])
+    assert (got[0, 0].cpu()[nan] == 672.0).all() and torch.isfinite(got).all()
+    groups = nan.view(64, n, 16).any(-1)
+    assert (got[0, 0].cpu().view(64, n, 16)[~groups] == 0).all()
