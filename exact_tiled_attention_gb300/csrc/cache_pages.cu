@@ -7,8 +7,9 @@
 // which go to q_out) are rotated by the table's row p in fp32 and rounded once.
 // 4 bits: for each group of 16 elements, f = E4M3(min(448, max |x| / (6 descale)))
 // and code = E2M1(x * (1 / (f descale))), both rounded to nearest even; f = 0
-// gives zero codes.  Division and reciprocal are the IEEE ones, so the codes are
-// those of the same formula evaluated anywhere in fp32.
+// gives codes of magnitude 0 with the elements' signs.  Division and reciprocal are
+// the IEEE ones, so the codes are those of the same formula evaluated anywhere in
+// fp32.
 //
 // Both are bound by HBM, or, for one token a sequence, by the launch (64 tokens of
 // 32 + 16 heads: 1.7 us one behind another, 4.1 alone from memory).  A row is read

@@ -458,11 +458,12 @@ int attn_cache_append(const void *k, const void *v, void *k_cache, void *v_cache
  * group of 16 elements x (keys after the rotation, in fp32) gets
  *   factor = E4M3(min(448, max|x| / (6 descale))),
  *   code   = E2M1(x * (1 / (factor * descale)))
- * both rounded to nearest even and saturating.  The codes have no NaN and no
- * infinity: a NaN counts as +infinity, which gives its group the factor 448 and
- * itself the code 6, so it reads back as 2688 descale (a 16-bit cache keeps both).
- * The codes and factors are those of the formula in IEEE fp32 arithmetic, whatever
- * order the tokens come in.
+ * both rounded to nearest even and saturating; factor 0 gives codes of magnitude 0
+ * with their elements' signs.  The codes have no NaN and no infinity: a NaN counts
+ * as +infinity, which gives its group the factor 448 and itself the code 6, so it
+ * reads back as 2688 descale (a 16-bit cache keeps both).  The codes and factors
+ * are those of the formula in IEEE fp32 arithmetic, whatever order the tokens come
+ * in.
  *
  * Errors: as attn_cache_append.
  */
@@ -480,7 +481,7 @@ int attn_cache_append_fp4(const void *k, const void *v, void *k_codes, void *k_f
  * cache into contiguous k_out, v_out [B, Hkv, S, d] (dtype), as attn_fwd takes
  * them; rows from seqlens[b] on are written as zeros.
  * attn_cache_gather_fp4 -- the same from a 4-bit cache: (code * factor) *
- * descale in fp32, rounded once to dtype.
+ * descale in fp32, rounded once to dtype; +0 where the factor is 0.
  *
  * Errors: GBATTN_EBADSHAPE (also B * Hkv > 65535 or S > 2^30), EHEADDIM,
  * EDTYPE, EPAGE, EPOINTER, EUNSUPPORTED, ELAUNCH.

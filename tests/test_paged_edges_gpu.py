@@ -152,3 +152,20 @@ def test_four_bits_of_nan(d, dtype):
     assert (got[0, 0].cpu()[nan] == 672.0).all() and torch.isfinite(got).all()
     groups = nan.view(64, n, 16).any(-1)
     assert (got[0, 0].cpu().view(64, n, 16)[~groups] == 0).all()
+
+
+def test_four_bits_of_groups_that_round_to_nothing():
+    """Groups below half of the smallest factor's reach get factor 0, and codes of 0
+    with their elements' signs; they read back as zeros."""
+    k = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16)
+    k[0, 0, 1], k[0, 0, 2] = -1e-30, torch.where(torch.arange(64) % 3 == 0, -1e-6, 1e-6).bfloat16()
+    k[0, 0, 3, ::2] = -0.0
+    codes = [torch.full((1, 1, 16, 32), 255, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    factors = [torch.full((1, 1, 16, 4), 9, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    gb.attn_cache_append_fp4(k.cuda(), k.cuda(), codes[0], factors[0], codes[1], factors[1], _i32([[0]]), _i32([4]))
+    sign = torch.signbit(k[0, 0]).to(torch.uint8) * 8
+    for c, f in zip(codes, factors):
+        assert (f[0, 0, :4] == 0).all()
+        assert torch.equal(c[0, 0, :4].cpu(), sign[:, ::2] | (sign[:, 1::2] << 4))
+    got = gb.attn_cache_gather_fp4(codes[0], factors[0], codes[1], factors[1], _i32([[0]]), _i32([4]), 4)
+    assert all((x == 0).all() for x in got)
