@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_bwd_kernel(const __grid
   const int h1 = min(h0 + p.per_chunk, p.heads[which]);
   const int e0 = 8 * lane_in_row;
   wait_for_previous_kernel();
-  let_next_kernel_start();
+  if constexpr (NORM) let_next_kernel_start();  // norm_dw_kernel; without weights none of this call follows
   int pc[2] = {0, 0};
   float w[2][8], dw[2][8];
 #pragma unroll
