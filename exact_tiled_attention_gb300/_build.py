@@ -1,9 +1,11 @@
 """Builds libgbattn.so in-tree with nvcc for sm_103a (no CMake, no torch
 extension machinery): each .cu compiles in parallel, then one link step.  The
-compiled half of the Python binding (_paged.so, C++ against the installed
-PyTorch's headers) is built beside it.
+compiled half of the Python binding (C++ against the installed PyTorch's headers)
+is built beside it; its file is named after the Python and the PyTorch that it is
+for, so one built for others is not loaded.
 
     python -m exact_tiled_attention_gb300._build [--force] [--verbose]
+    python exact_tiled_attention_gb300/_build.py     # the C library, without PyTorch
 
 Build option (environment): GBATTN_EX2_EMU_EVERY=E evaluates every E-th pair
 of softmax exponentials with the FMA-pipe polynomial instead of the MUFU unit
@@ -24,7 +26,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgbattn.so")
-EXT = os.path.join(PKG, "_paged.so")
 EXT_SOURCE = "paged_binding.cpp"
 
 SOURCES = ["gbattn_api.cu", "prefill_fwd.cu", "prefill_pair.cu", "prefill_fp8.cu", "decode_splitkv.cu",
@@ -45,8 +46,20 @@ def nvcc() -> str:
 def _deps() -> list[str]:
     out = [os.path.join(INCLUDE, "gbattn.h")]
     for f in os.listdir(CSRC):
-        out.append(os.path.join(CSRC, f))
+        if f != EXT_SOURCE:
+            out.append(os.path.join(CSRC, f))
     return out
+
+
+def _ext_deps() -> list[str]:
+    return [os.path.join(INCLUDE, "gbattn.h"), os.path.join(CSRC, EXT_SOURCE)]
+
+
+def ext_path() -> str:
+    """Where the binding's compiled half for this Python and this PyTorch belongs."""
+    import torch
+
+    return os.path.join(PKG, f"_paged-{sysconfig.get_config_var('SOABI')}-torch-{torch.__version__}.so")
 
 
 def _stale(target: str, deps: list[str]) -> bool:
@@ -61,8 +74,8 @@ def _options() -> list[str]:
     return [f"-DGBATTN_EX2_EMU_EVERY={emu}"]
 
 
-def _ext_commands() -> tuple[list[str], list[str]]:
-    """Compile and link commands of the binding's compiled half."""
+def _ext_commands(path: str) -> tuple[list[str], list[str]]:
+    """Compile and link commands of the binding's compiled half at `path`."""
     import torch
 
     base = os.path.dirname(torch.__file__)
@@ -73,7 +86,7 @@ def _ext_commands() -> tuple[list[str], list[str]]:
                 "-I", INCLUDE, "-isystem", sysconfig.get_path("include"), "-isystem", os.path.join(base, "include"),
                 "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
                 "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
-    link = [cxx, "-shared", obj, "-o", EXT + f".tmp{os.getpid()}", "-L" + PKG, "-l:libgbattn.so",
+    link = [cxx, "-shared", obj, "-o", path, "-L" + PKG, "-l:libgbattn.so",
             "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
     return compile_, link
 
@@ -88,18 +101,31 @@ def _run(cmd: list[str], what: str, verbose: bool) -> None:
         raise RuntimeError(f"{what} failed")
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    os.makedirs(BUILD, exist_ok=True)
-    deps = _deps()
-    stamp = os.path.join(BUILD, "options.txt")
-    import torch
+def _build_ext(path: str, verbose: bool) -> None:
+    """Links the compiled half, whose object is there, against the library."""
+    tmp = path + f".tmp{os.getpid()}"
+    _run(_ext_commands(tmp)[1], "g++ link", verbose)
+    os.replace(tmp, path)
 
+
+def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
+    """Builds what is not up to date: the library, which needs nvcc and its host
+    compiler only, and beside it the binding's compiled half where PyTorch is
+    installed.  A failure of the second leaves the first in place."""
+    os.makedirs(BUILD, exist_ok=True)
+    stamp = os.path.join(BUILD, "options.txt")
     opts = _options()
-    built_as = " ".join(opts + [f"torch-{torch.__version__}"])
     old = open(stamp).read() if os.path.exists(stamp) else ""
-    if not force and not _stale(LIB, deps) and not _stale(EXT, deps) and old == built_as:
+    lib_stale = force or _stale(LIB, _deps()) or old != " ".join(opts)
+    try:
+        ext = ext_path()
+    except ImportError:
+        ext = None
+        sys.stderr.write("PyTorch is not installed: building the C library alone, without its Python binding\n")
+    ext_stale = ext is not None and (force or _stale(ext, _ext_deps()))
+    if not lib_stale and not ext_stale:
         return LIB
-    cc = nvcc()
+    cc = nvcc() if lib_stale else ""
     extra = (["-Xptxas", "-v"] if ptxas_verbose else []) + opts
 
     def compile_one(src: str):
@@ -110,27 +136,28 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    ext_compile, ext_link = _ext_commands()
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ext = ex.submit(_run, ext_compile, f"g++ on {EXT_SOURCE}", verbose)
-        results = list(ex.map(compile_one, SOURCES))
-        ext.result()
-    for src, _, r in results:
-        if verbose or ptxas_verbose or r.returncode != 0:
-            sys.stderr.write(r.stdout + r.stderr)
+    sources = SOURCES if lib_stale else []
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        ext_object = pool.submit(_run, _ext_commands(ext)[0], f"g++ on {EXT_SOURCE}", verbose) if ext_stale else None
+        results = list(pool.map(compile_one, sources))
+    if lib_stale:
+        for src, _, r in results:
+            if verbose or ptxas_verbose or r.returncode != 0:
+                sys.stderr.write(r.stdout + r.stderr)
+            if r.returncode != 0:
+                raise RuntimeError(f"nvcc failed on {src}")
+        tmp = LIB + f".tmp{os.getpid()}"
+        link = [cc, *ARCH, "-shared", "-o", tmp, *[obj for _, obj, _ in results]]
+        r = subprocess.run(link, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}")
-    tmp = LIB + f".tmp{os.getpid()}"
-    link = [cc, *ARCH, "-shared", "-o", tmp, *[obj for _, obj, _ in results]]
-    r = subprocess.run(link, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc link failed")
-    os.replace(tmp, LIB)
-    _run(ext_link, "g++ link", verbose)
-    os.replace(EXT + f".tmp{os.getpid()}", EXT)
-    with open(stamp, "w") as f:
-        f.write(built_as)
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("nvcc link failed")
+        os.replace(tmp, LIB)
+        with open(stamp, "w") as f:
+            f.write(" ".join(opts))
+    if ext_stale:
+        ext_object.result()
+        _build_ext(ext, verbose)
     return LIB
 
 

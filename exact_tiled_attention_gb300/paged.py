@@ -14,28 +14,36 @@ All tensors of a call lie on one device.  The call is enqueued there, on
 """
 from __future__ import annotations
 
+import importlib.util
 import os
+import threading
 
 import torch
 
 from .binding import GbattnError, load_library
 
 _native = None
+_lock = threading.Lock()
 
 
 def _load():
-    """The compiled half, loaded on first use; raises if it is missing."""
+    """The compiled half, loaded on first use; raises if there is none for this
+    Python and this PyTorch."""
     global _native
-    if _native is None:
-        load_library()
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_paged.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with "
-                               "`python -m exact_tiled_attention_gb300._build` (no fallback exists)")
-        from . import _paged
+    with _lock:
+        if _native is None:
+            from ._build import ext_path
 
-        _paged.set_error(GbattnError)
-        _native = _paged
+            load_library()
+            path = ext_path()
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing: build it with "
+                                   "`python -m exact_tiled_attention_gb300._build` (no fallback exists)")
+            spec = importlib.util.spec_from_file_location(__package__ + "._paged", path)
+            native = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(native)
+            native.set_error(GbattnError)
+            _native = native
     return _native
 
 
