@@ -20,9 +20,13 @@
 // a row of K is its operand for several products, and V, whose operand pairs two
 // keys, takes one byte permute for two elements.
 //
+// "The large batch", here and below: 64 sequences whose lengths lie evenly between
+// 1024 and 32768 tokens (16896 on average), in random order, 32 query heads on 8
+// (128 for 16 heads a unit), bf16, pages of 64.
+//
 // 16 bits: rows go from global memory straight into operand registers, requested
-// as an earlier piece's are consumed (kDepth).  Bound by HBM: 64 sequences of 1024 to
-// 32768 tokens, 32 heads on 8, d = 128, take 680 us, 7.0 TB/s.
+// as an earlier piece's are consumed (kDepth).  Bound by HBM: the large batch at
+// d = 128 takes 630 us, 7.0 TB/s.
 // 4 bits: rows go through a ring in shared memory that asynchronous copies fill.
 // A pair of codes becomes an fp16 pair in one conversion, one product applies the
 // factor (exact, 2 by 4 significant bits), and the bytes of two keys' codes are
@@ -30,7 +34,7 @@
 // of one KV head (72 conversions at half rate, 64 products), against 390 issue
 // slots in the time that HBM takes for their 2304 bytes: bound by issue and by
 // the conversions' pipe (62 % and 53 % busy, 16 warps an SM).  The same batch
-// takes 226 us, 5.9 TB/s.
+// takes 205 us, 6.1 TB/s.
 //
 // The scores' reference m follows the maximum lazily (it moves when a score is
 // more than 8 above it in base-2 units), so P <= 256; l sums P before it is
@@ -200,9 +204,11 @@ struct LanePtrs {
 // Terms that P is held in for P V.  Over a 16-bit cache the rounding's remainder
 // is a second one: a single bf16 (or fp16) P shows in O next to O's own rounding
 // (relative error 2.3e-3 against 1.7e-3 in bf16 at 64 sequences of 17 thousand
-// tokens), and the loop, bound by memory, has room for the products (673 us
-// with them, 684 without).  Over a 4-bit cache P is one fp16: the loop is bound
-// by issue there, and the cache's own error is larger.
+// tokens), and the loop, bound by memory, has room for the products (the large
+// batch 630 us with and without them; with 16 heads a unit 689 and 674).  Over a
+// 4-bit cache P is one fp16, off by 2^-11 at most: the loop is bound by issue there,
+// and the cache's own error is larger (O in bf16 1.7e-3 off, as with P in fp32; in
+// fp16 2.5e-4, with P in fp32 2.1e-4).
 template <int FMT>
 constexpr int kTerms = FMT == kFp4 ? 1 : 2;
 
@@ -433,8 +439,8 @@ struct Tile<D, kFp4> {
 };
 
 // Stages of a warp's ring (4-bit caches), each of 32 keys: 4608 bytes at D = 128,
-// where two take 226 us at the 64-sequence batch and three 229; at D = 64, half
-// the bytes, three take 141 and two 144.
+// where two take 205 us at the large batch and three 209; at D = 64, half the bytes,
+// three take 127 and two 129.
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 3;
 
@@ -442,8 +448,8 @@ constexpr int kStages = D == 128 ? 2 : 3;
 // take the registers of a third CTA on an SM (four sequences of 4000 tokens in
 // clusters: 15.4 -> 17.4 us, one of 8000 19.7 -> 16.0, where the list takes 12); at
 // d = 64 24 sequences of 2000 tokens, 64 heads on 8, take 21.2 us with one and 18.6
-// with two, and the list with 16 heads a unit 331 and 326 at the large batch, but
-// with 8 heads 313 and 324.
+// with two, and the list with 16 heads a unit 341 and 336 at the large batch, but
+// with 8 heads 325 and 333.
 template <int D, int NT, bool SHORT>
 constexpr int kDepth = D == 64 && (SHORT || NT == 2) ? 2 : 1;
 
@@ -454,10 +460,12 @@ template <int FMT>
 constexpr int kUnitKeys = 16 * kBlocks<FMT> * kWarps;
 // Units of work that a segment's fixed part (its first pages and rows, Q, the
 // merge of the warps) counts as when the list is divided; without it the CTAs
-// whose run holds many short sequences end last.  64 sequences of 1024 to 32768
-// tokens, 0 against this: 4 bits and 8 heads a unit 247 -> 235 us (1: 240, 5:
-// 238), 16 heads 350 -> 309; 16 bits and 8 heads 683 -> 684 (3: 683), 16 heads
-// 772 -> 752 (5: 752).
+// whose run holds many short sequences end last.  The large batch, us, with 0, with
+// 1, with this and with 2 more (d = 128; d = 64):
+//   4 bits, 8 heads a unit   212, 206, 205, 208; 131, 127, 127, 128
+//   4 bits, 16 heads         309, 299, 277, 277; 183, 178, 165, 166
+//   16 bits, 8 heads         631, -, 630, 628; 325, -, 325, 325
+//   16 bits, 16 heads        714, 705, 689, 690; 353, 348, 336, 337
 template <int FMT, int NT>
 constexpr int kSegmentCost = (FMT == kFp4 ? 3 : 1) + 2 * (NT - 1);
 
@@ -563,12 +571,17 @@ struct Smem {
   static constexpr int kBytes = kWarps * (kRing > kStates ? kRing : kStates);
 };
 
-// CTAs of four warps that an SM holds at least, which bounds the registers.  At the
-// 64-sequence batch, us, with 8 and 16 query heads a unit (in brackets: CTAs):
-//   d = 64, 16 bits: 332 (3), 314 (4), 313 (5) and 361 (2), 326 (3)
-//   d = 64, 4 bits: 121 (4), 127 (5) and 178 (2), 159 (3), 169 (4)
-//   d = 128, 4 bits: 251 (4), 255 (5, spills; before later steps) and 266 (2), 279 (3, spills)
-// At d = 128 and 16 bits a lane's rows and sums take 165 and 250 registers.
+// CTAs of four warps that an SM holds at least, which bounds the registers.  The
+// large batch, us, with 8 and with 16 query heads a unit (in brackets: CTAs; *: some
+// registers spill, bytes stored):
+//   d = 64, 16 bits: 326 (4), 325 (5, *28), 344 (6, *136) and 375 (2), 336 (3), 505 (4, *380)
+//   d = 64, 4 bits: 128 (3), 127 (4), 132 (5) and 187 (2), 165 (3), 176 (4)
+//   d = 128, 16 bits: 655 (2), 630 (3), 731 (4, *200) and 689 (2), 915 (3, *312)
+//   d = 128, 4 bits: 201 (3), 205 (4), 217 (5, *108) and 277 (2), 288 (3, *40)
+// Kept although it spills: d = 64, 16 bits, the list with 8 heads (28 bytes, even
+// with 4 CTAs that do not) and clusters with 16 (12 bytes).
+// d = 128 over 4 bits: three CTAs gain 2 % here and up to 13 % on one sequence
+// (32000 tokens 16.5 -> 14.3), and lose 3 % on 64 short ones of 80 heads on 16.
 template <int D, int FMT, int NT, bool SHORT>
 constexpr int kResident = D == 64 ? (FMT != kFp4 && kDepth<D, NT, SHORT> == 1 ? 6 : 5) - NT
                                   : FMT == kFp4 && NT == 1 ? 4 : 4 - NT;
@@ -1181,6 +1194,13 @@ int max_ctas(int B, size_t heads, int max_len) {
 //   24 sequences, 2 CTAs each: 8 units 12.3 / 10.4, 16 15.3 / 15.4, 24 17.7 / 19.6
 //   48 sequences, a CTA each: 8 units 16.0 / 14.4, 12 about even, 24 28 / 32
 // one sequence, 8 CTAs, equal lengths: 16 units 6.7 / 5.8, 32 7.3 / 7.2, 48 8.1 / 8.6.
+// The same thresholds serve the other forms, where clusters would win further up.
+// Of 42 batches of each form (1 to 96 sequences of up to 2 to 48 units, rows in L2)
+// the choice is within 5 % of the best division in 33 (this form), 32 (16 heads a
+// unit; 4 bits with 8), 31 (4 bits with 16) and 26 to 28 (d = 64); at worst, list
+// against clusters of 8: d = 64, 8 sequences of up to 24 units in 16 bits 9.4 / 6.5,
+// of 48 in 4 bits 9.7 / 7.0; d = 128, 4 sequences of up to 48 in 4 bits 11.2 / 8.8.
+// Tables of two units get clusters of two where one CTA is faster by 0.4 to 1.5 us.
 // With more segments than resident CTAs they take turns, and the last turn's
 // idle places cost what the list does not lose: from four turns on clusters of
 // one win at all 16 units tried (512 sequences 313 / 302, 4 bits 215 / 197); at

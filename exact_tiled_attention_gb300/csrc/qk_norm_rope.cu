@@ -11,8 +11,9 @@
 // one token's cosines and sines in registers and walks over heads, so the
 // 4-byte table is read once for several heads, and the rows come through a ring
 // of asynchronous copies (RowRing).  At [4, 8192] tokens of 16 + 16 heads of 128
-// the forward takes 81 us (6.6 TB/s) and the backward 121 us (6.7 TB/s), against
-// 84 and 137 with the next row alone requested ahead, in registers.
+// the forward takes 83 us (6.5 TB/s) and the backward 127 us (6.4 TB/s); when the
+// ring came in they fell from 84 to 80 and from 137 to 121 against the next row alone
+// requested ahead, in registers.  The rotation without norms takes 83 and 82 us.
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -118,7 +118,9 @@ def attn_cache_append_fp4(k, v, k_codes, k_factors, v_codes, v_factors, page_tab
 
 def attn_cache_gather(k_cache, v_cache, page_table, seqlens, S: int, k_out=None, v_out=None, stream=None):
     """The first S tokens of every sequence of a 16-bit paged cache as contiguous
-    (k, v) [B,Hkv,S,d], zeros behind a sequence (C ABI `attn_cache_gather`)."""
+    (k, v) [B,Hkv,S,d], zeros behind a sequence (C ABI `attn_cache_gather`).
+    attn_fwd takes them where all sequences have S tokens: to it the zero rows
+    behind a shorter one are keys."""
     return (_native or _load()).attn_cache_gather(k_cache, v_cache, page_table, seqlens, S, k_out, v_out, stream)
 
 

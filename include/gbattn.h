@@ -365,7 +365,9 @@ size_t attn_decode_noalloc_scratch_bytes(void);
  *
  * One step of serving: attn_qk_norm_rope where the model has such norms (and
  * then no rotation here), attn_cache_append, attn_decode_paged.  A chunk of a
- * prompt: append it, attn_cache_gather the sequence, attn_fwd with causal = 1.
+ * prompt: append it, attn_cache_gather the sequence, attn_fwd with causal = 1;
+ * sequences of one length together, others in calls of their own (attn_fwd has one
+ * length, and would count the zero rows behind a shorter sequence as keys).
  */
 
 /*
@@ -522,9 +524,15 @@ size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_
  * follow from sizes and lengths alone and results repeat bitwise.  A score of NaN or +inf
  * makes its query's o and lse NaN, a score of -inf counts as a masked key, and a
  * NaN or an infinity in a row of v that counts makes its elements of o NaN.
+ * Scores, their maximum, the sum of exp and the sums of o are fp32.  For the product
+ * with v the weights exp(score - maximum) are rounded, to two terms of dtype
+ * (together within 2^-16 of a weight in bf16, 2^-22 in fp16).
  *
  * attn_decode_paged_fp4 -- the same over a 4-bit cache (q and o in dtype, which
- * the cache does not depend on).
+ * the cache does not depend on).  The weights are rounded to one fp16 (within 2^-11),
+ * and q, row by row, to fp16 behind a power of two that brings the row's largest
+ * element to [1, 2): exact but for elements of bf16 below 2^-14 of that one, which
+ * are off by at most 2^-25 of it.
  *
  * Errors: GBATTN_EBADSHAPE (also B > 65535, Hq > 16384), EHEADS, EHEADDIM,
  * EDTYPE, EPAGE, EPOINTER, EWORKSPACE, EUNSUPPORTED, ELAUNCH.
