@@ -149,6 +149,23 @@ bool make_tmap_3d(CUtensorMap* map, const void* base, bool bf16, int d, int rows
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_heads(CUtensorMap* map, const void* base, bool bf16, int d, int g, int Hkv, int S, int B, int box_heads,
+                     int box_tokens) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2, head = row * static_cast<cuuint64_t>(S);
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(g), static_cast<cuuint64_t>(Hkv),
+                              static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[4] = {head, head * dims[1], row, head * dims[1] * dims[2]};
+  const cuuint32_t box[5] = {64u, static_cast<cuuint32_t>(box_heads), 1u, static_cast<cuuint32_t>(box_tokens), 1u};
+  const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+  const CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_3d_f32(CUtensorMap* map, void* base, int inner, int rows, long long outer, int box_inner,
                       int box_rows) {
   EncodeTiledFn enc = encode_tiled_fn();

@@ -192,6 +192,42 @@ int decode(const void* q, const void* k_cache, const void* k_factors, const void
   return launch_decode_paged(a) == 0 ? GBATTN_OK : GBATTN_ELAUNCH;
 }
 
+int prefill(const void* q, const void* k_cache, const void* k_factors, const void* v_cache, const void* v_factors,
+            bool fp4, const float* k_descale, const float* v_descale, const int* page_table, const int* seqlens,
+            const int* new_lens, void* o, float* lse, int B, int H, int Hkv, int S, int d, int page_size, int n_pages,
+            int max_pages, float scale, int causal, void* workspace, size_t workspace_bytes, int dtype, void* stream) {
+  if (B < 1 || H < 1 || Hkv < 1 || S < 1 || H > 16384 || Hkv > 16384) return GBATTN_EBADSHAPE;
+  if (too_many_tokens(B, S)) return GBATTN_EBADSHAPE;
+  if (H % Hkv != 0) return GBATTN_EHEADS;
+  if (!(scale > 0.f) || scale > 3e38f) return GBATTN_EBADSHAPE;
+  PagedPrefillArgs a{};
+  int rc = check_cache(&a.cache, k_cache, v_cache, k_factors, v_factors, fp4, k_descale, v_descale, page_table,
+                       seqlens, Hkv, d, page_size, n_pages, max_pages);
+  if (rc != GBATTN_OK) return rc;
+  // A page and head are one coordinate of a tensor map.
+  if (static_cast<long long>(n_pages) * Hkv >= 0x7FFFFFFFLL) return GBATTN_EBADSHAPE;
+  if (dtype != GBATTN_F16 && dtype != GBATTN_BF16) return GBATTN_EDTYPE;
+  if (!q || !o || !workspace || misaligned16(q) || misaligned16(o) || misaligned16(workspace) || misaligned4(lse) ||
+      misaligned4(new_lens))
+    return GBATTN_EPOINTER;
+  if (workspace_bytes < paged_prefill_workspace_bytes(B, H, Hkv, S, d, max_pages * page_size)) return GBATTN_EWORKSPACE;
+  rc = current_device(&a.status, &a.num_sms);
+  if (rc != GBATTN_OK) return rc;
+  a.q = q;
+  a.new_lens = new_lens;
+  a.o = o;
+  a.lse = lse;
+  a.B = B;
+  a.H = H;
+  a.S = S;
+  a.scale = scale;
+  a.causal = causal ? 1 : 0;
+  a.workspace = workspace;
+  a.bf16 = dtype == GBATTN_BF16;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_prefill_paged(a) == 0 ? GBATTN_OK : GBATTN_ELAUNCH;
+}
+
 }  // namespace
 
 extern "C" {
@@ -305,6 +341,20 @@ int attn_decode_paged_fp4(const void* q, const void* k_codes, const void* k_fact
                           size_t workspace_bytes, int dtype, void* stream) {
   return decode(q, k_codes, k_factors, v_codes, v_factors, true, k_descale, v_descale, page_table, seqlens, o, lse, B,
                 Hq, Hkv, d, page_size, n_pages, max_pages, scale, workspace, workspace_bytes, dtype, stream);
+}
+
+size_t attn_fwd_paged_workspace_bytes(int B, int H, int Hkv, int S, int d, int max_len) {
+  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || S < 1 || d < 1 || max_len < 1) return 0;
+  return paged_prefill_workspace_bytes(B, H, Hkv, S, d, max_len);
+}
+
+int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const int* page_table, const int* seqlens,
+                   const int* new_lens, void* o, float* lse, int B, int H, int Hkv, int S, int d, int page_size,
+                   int n_pages, int max_pages, float scale, int causal, void* workspace, size_t workspace_bytes,
+                   int dtype, void* stream) {
+  return prefill(q, k_cache, nullptr, v_cache, nullptr, false, nullptr, nullptr, page_table, seqlens, new_lens, o, lse,
+                 B, H, Hkv, S, d, page_size, n_pages, max_pages, scale, causal, workspace, workspace_bytes, dtype,
+                 stream);
 }
 
 }  // extern "C"

@@ -184,12 +184,30 @@ struct PagedDecodeArgs {
   int num_sms;
 };
 
+// A chunk of new tokens over a paged cache (prefill_paged.cu).
+struct PagedPrefillArgs {
+  const void* q;        // [B, H, S, d]
+  CacheArgs cache;
+  const int* new_lens;  // [B] or null: S
+  void* o;
+  float* lse;           // [B, H, S] or null
+  int B, H, S;
+  float scale;
+  int causal;
+  void* workspace;
+  bool bf16;
+  cudaStream_t stream;
+  int* status;
+  int num_sms;
+};
+
 // Looks up the current device: its status word and number of SMs.  GBATTN_OK
 // or GBATTN_EUNSUPPORTED / GBATTN_ELAUNCH.
 int current_device(int** status, int* sm_count);
 
-// Bytes of workspace of the paged decode and of the norm's backward.
+// Bytes of workspace of the paged decode and prefill and of the norm's backward.
 size_t paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d, int max_len);
+size_t paged_prefill_workspace_bytes(int B, int H, int Hkv, int S, int d, int max_len);
 size_t norm_rope_bwd_workspace_bytes(int d);
 
 // Each returns a cudaError_t / CUresult folded into 0 (ok) or -1 (launch or
@@ -199,6 +217,7 @@ int launch_norm_rope_bwd(const NormRopeArgs& a);
 int launch_cache_append(const AppendArgs& a);
 int launch_cache_gather(const GatherArgs& a);
 int launch_decode_paged(const PagedDecodeArgs& a);
+int launch_prefill_paged(const PagedPrefillArgs& a);
 int launch_prefill(const PrefillArgs& a);
 // Non-causal d = 128 forward on a tcgen05 CTA pair (prefill_pair.cu); -1 if
 // the arguments are outside that case or a launch failed.
@@ -312,6 +331,12 @@ __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("gridd
 // (64 x box_rows x 1) box and 128-byte swizzle; rows past `rows` read as 0.
 bool make_tmap_3d(CUtensorMap* map, const void* base, bool bf16, int d, int rows, long long outer,
                   int box_rows);
+
+// 5-D tensor map over the queries (or outputs) [B, Hkv * g, S, d] of 16 bits, with
+// dimensions (d, g, Hkv, S, B) and a (64 x box_heads x 1 x box_tokens x 1) box: a
+// box's rows are tokens, each with its heads of one KV head, 128-byte swizzle.
+bool make_tmap_heads(CUtensorMap* map, const void* base, bool bf16, int d, int g, int Hkv, int S, int B, int box_heads,
+                     int box_tokens);
 
 // 3-D tensor map over a contiguous [outer, rows, inner] fp32 tensor with a
 // (box_inner x box_rows x 1) box, box_inner * 4 <= 128 bytes, and 128-byte

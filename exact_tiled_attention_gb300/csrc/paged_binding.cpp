@@ -525,6 +525,38 @@ PyObject* decode_paged_fp4(PyObject* const* a) {
   return decode(f, a[0], Hkv, c, a[9], a[10], a[11], a[12], a[13], a[14], true);
 }
 
+// c, the cache, is checked against q [B, H, S, d]; o = out, lse, return_lse, stream.
+PyObject* fwd_paged(const First& f, PyObject* qo, int64_t Hkv, const Cache& c, PyObject* new_lens, PyObject* scale_o,
+                    PyObject* causal_o, PyObject* workspace, PyObject* const* o, bool fp4) {
+  const Tensor& q = THPVariable_Unpack(qo);
+  const void* q_ptr = ptr(qo, "q", q.sizes(), f.type, f.device);
+  const int B = size(q.size(0), "q"), H = size(q.size(1), "q"), S = size(q.size(2), "q"), d = size(q.size(3), "q");
+  const int hkv = size(Hkv, "the cache");
+  const int* n = static_cast<const int*>(opt(new_lens, "new_lens", {B}, at::kInt, f.device));
+  const int causal = truth(causal_o);
+  const float scale = static_cast<float>(none(scale_o) ? 1.0 / std::sqrt(static_cast<double>(d)) : number(scale_o));
+  const int64_t cap = static_cast<int64_t>(c.page) * c.max_pages;
+  const Target target(o[3], f.device);
+  Workspace ws;
+  ws.take(workspace, attn_fwd_paged_workspace_bytes(B, H, hkv, S, d, static_cast<int>(cap < INT_MAX ? cap : INT_MAX)),
+          f.device);
+  Output out, lse;
+  out.take(o[0], "out", q.sizes(), f.type, f.device);
+  if (!none(o[1]) || truth(o[2])) lse.take(o[1], "lse", {B, H, S}, at::kFloat, f.device);
+  done(attn_fwd_paged(q_ptr, c.k, c.v, c.table, c.lens, n, out.data, static_cast<float*>(lse.data), B, H, hkv, S, d,
+                      c.page, c.n_pages, c.max_pages, scale, causal, ws.data, ws.bytes, f.code, target.stream),
+       "attn_fwd_paged");
+  return tuple({&out, &lse});
+}
+
+PyObject* forward_paged(PyObject* const* a) {
+  const First f = first(a[0], "q");
+  const Tensor& q = THPVariable_Unpack(a[0]);
+  const int64_t Hkv = tensor_of_dims(a[1], "k_cache", 4).size(1);
+  const Cache c(a[1], a[2], a[3], a[4], q.size(0), Hkv, q.size(3), f);
+  return fwd_paged(f, a[0], Hkv, c, a[5], a[6], a[7], a[8], a + 9, false);
+}
+
 // A function of N positional arguments; no C++ exception leaves it.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -561,6 +593,7 @@ PyMethodDef methods[] = {
     method<cache_append_fp4, 16>("attn_cache_append_fp4"),
     method<cache_gather, 8>("attn_cache_gather"),
     method<cache_gather_fp4, 13>("attn_cache_gather_fp4"),
+    method<forward_paged, 13>("attn_fwd_paged"),
     method<decode_paged, 11>("attn_decode_paged"),
     method<decode_paged_fp4, 15>("attn_decode_paged_fp4"),
     {nullptr, nullptr, 0, nullptr},

@@ -1,0 +1,1028 @@
+// prefill_paged.cu -- attention of the last `rows` tokens of every sequence over
+// a paged cache that holds them and all tokens before: a prompt's next chunk, or
+// drafted tokens to check, for sequences of different lengths in one call.
+//
+//   o_i = sum_j exp(scale q_i.k_j - lse_i) v_j,  lse_i = log sum_j exp(scale q_i.k_j)
+//
+// over the keys j <= position of i (causal), or all of the sequence's keys.
+//
+// Work.  A unit is a block of query tokens of one sequence and KV head: NT tiles
+// ("H", "L") of 128 rows, whose rows are tokens and, for each, the query heads of
+// the KV head (up to hb of them), so that a key tile serves all of them and a
+// short chunk still fills rows.  Its key axis has tiles of 128 keys.  The list of
+// all units' key tiles (order: sequence, head, block of tokens, tile) is cut into
+// equal runs, one for each CTA (one an SM), whatever the lengths are.  A run
+// covers whole units, which the CTA finishes itself, and at its two ends parts of
+// units, whose states (m, l, o) it leaves in the workspace; a second kernel folds
+// those and writes the zeros of padding rows.  The division follows from the
+// lengths alone, so results repeat bitwise.
+//
+// A CTA works through its run without a stop between units: the loader, the MMA
+// issuers, the softmax warps and the guard walk the same list of segments each at
+// its own pace.  Tensor memory: S_H, S_L, O_H, O_L and, at d = 64, P_H, P_L (at
+// d = 128 P goes through shared memory), as in the forward over contiguous tensors.
+//
+// Warp roles: warps 0-3 (4-7) softmax, correction and epilogue of tile H (L),
+// thread = row; then lanes 0 of a warp for each tile's MMAs; a warp that loads
+// (lane = one box of a page); a warp that guards V.
+//
+// The guard.  A key that a row does not see has weight 0, but 0 times a NaN or an
+// infinity in its row of V would be NaN.  Tiles with keys that some row does not
+// see (the diagonal's, and the sequence's last) therefore pass through a warp
+// which zeroes the rows of V behind the sequence, zeroes what is not finite in the
+// rows that some query token sees and others do not, and notes for each column
+// the first such key; rows that see it get NaN there at the end.  The score of a
+// key that a row does not see becomes -inf, whatever it was.
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "gbattn_internal.h"
+#include "gbattn_ptx.cuh"
+
+namespace gbattn {
+namespace {
+
+constexpr int kBM = 128;          // rows of a tile (= TMEM lanes)
+constexpr int kBN = 128;          // keys of a tile
+constexpr int kMaxCtas = 160;     // bound of the grid, for the workspace's size
+constexpr float kRescaleThreshold = 8.f;  // base-2 units
+constexpr int kSegRing = 8;       // segments whose notes of the guard are kept
+constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr bool kPInTmem = (D == 64);
+  static constexpr int kColBlocks = D / 64;
+  static constexpr int kTileBytes = kBM * D * 2;
+  static constexpr int kBlockBytes = kBM * 128;
+  static constexpr int kStageBytes = kPInTmem ? kTileBytes : kBM * kBN * 2;  // P, or (d = 64) the output alone
+  static constexpr int kStages = NT == 2 ? (D == 128 ? 3 : 8) : (D == 128 ? 5 : 12);
+  static constexpr int kQOff = 0;
+  static constexpr int kPOff = NT * kTileBytes;
+  static constexpr int kRingOff = kPOff + NT * kStageBytes;
+  static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kSmemBytes = kBarOff + 2048;
+  static constexpr int kMmaWarp = 4 * NT;  // tile x's issuer is warp kMmaWarp + x
+  static constexpr int kLoadWarp = 4 * NT + 2;
+  static constexpr int kGuardWarp = 4 * NT + 3;
+  static constexpr int kThreads = 128 * (NT + 1);
+};
+// With two tiles; the 168 registers a thread that the kernel is launched with suffice
+// for one.
+constexpr int kSoftmaxRegs = 224, kControlRegs = 56;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= 384 * 168, "register split");
+
+struct Params {
+  CUtensorMap tq, to, tk, tv;
+  const int* page_table;
+  const int* seqlens;
+  const int* new_lens;
+  void* o;
+  float* lse;
+  float* part_o;   // [ctas][2][D / 4][NT * 128][4]
+  float2* part_ml; // [ctas][2][NT * 128]: m in base-2 units, l
+  int2* parts;     // [B][heads][blocks]: first CTA, number of parts (1: finished)
+  int B, H, Hkv, S, g;
+  int hb, tq_tokens, nblk, heads, blocks;  // heads a tile; tokens a tile; head blocks; Hkv * nblk; token blocks of S
+  int page_shift, n_pages, max_pages, box_rows;
+  int causal;
+  int out_bf16;
+  float scale_log2;
+  int ctas;
+  int* status;
+};
+
+struct __align__(8) Barriers {
+  uint64_t q_full, q_empty;
+  uint64_t kv_full[12], kv_empty[12], raw[12];
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_full[2], mma_done[2];
+  uint64_t group[2];       // the four warps of a softmax warpgroup
+  uint64_t stagger;
+  long long per;           // tiles of a run
+  long long start_left;    // tiles of this run
+  int start[4];            // its first unit (sequence, head, block) and tile
+  long long scan[12];
+  uint32_t tmem_base;
+  int abort_flag;
+  uint8_t bad[kTileRing];          // 16-key blocks of a tile that have no page
+  uint8_t nan_any[kSegRing];
+  uint8_t nan_from[kSegRing][128]; // column's first non-finite key behind the first row's last key, - 1
+};
+static_assert(sizeof(Barriers) <= 2048, "barriers fit");
+
+// A sequence: cached tokens, position of query row 0 (negative: the first -p0 rows
+// are padding), query rows.
+struct Seq {
+  int n, p0, rows;
+};
+__device__ __forceinline__ Seq load_seq(const Params& p, int b) {
+  Seq s;
+  const int len = max(p.seqlens[b], 0);
+  s.rows = p.new_lens != nullptr ? min(max(p.new_lens[b], 0), p.S) : p.S;
+  s.p0 = len - s.rows;
+  s.n = min(len, p.max_pages << p.page_shift);
+  return s;
+}
+// Last key that query token t sees (t >= -p0).
+__device__ __forceinline__ int limit(const Params& p, const Seq& s, int t) {
+  return p.causal ? min(s.p0 + t, s.n - 1) : s.n - 1;
+}
+// Key tiles that the query tokens [t0, t1) visit.
+__device__ __forceinline__ int tiles_of(const Params& p, const Seq& s, int t0, int t1) {
+  const int last = min(t1, s.rows) - 1;
+  if (last < t0 || s.p0 + last < 0) return 0;
+  return limit(p, s, last) / kBN + 1;
+}
+template <int NT>
+__device__ __forceinline__ long long seq_tiles(const Params& p, const Seq& s) {
+  const int tu = NT * p.tq_tokens;
+  if (!p.causal) {  // all blocks but those of padding alone
+    const int first = max(-s.p0, 0) / tu, end = (s.rows + tu - 1) / tu;
+    return s.n > 0 && end > first ? static_cast<long long>(end - first) * ((s.n + kBN - 1) / kBN) : 0;
+  }
+  long long sum = 0;
+  for (int t = 0; t < s.rows; t += tu) sum += tiles_of(p, s, t, t + tu);
+  return sum;
+}
+
+// A run of key tiles of one unit.
+struct Seg {
+  Seq s;
+  int b, u, k;
+  int nt;      // tiles of the unit
+  int j0, j1;  // the segment's
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == nt; }
+};
+
+// Walks over the segments of a CTA's run.
+template <int NT>
+struct Cursor {
+  Seq s;
+  int b, u, k, y;
+  long long left;
+  __device__ __forceinline__ void start(const Params& p, const Barriers* bars) {
+    b = bars->start[0], u = bars->start[1], k = bars->start[2], y = bars->start[3];
+    left = bars->start_left;
+    s = load_seq(p, b);
+  }
+  __device__ __forceinline__ bool next(const Params& p, Seg& seg) {
+    if (left <= 0) return false;
+    const int tu = NT * p.tq_tokens;
+    int nt = tiles_of(p, s, k * tu, (k + 1) * tu);
+    while (nt == 0) {
+      if (!advance(p, tu)) return false;
+      nt = tiles_of(p, s, k * tu, (k + 1) * tu);
+    }
+    seg.s = s;
+    seg.b = b, seg.u = u, seg.k = k, seg.nt = nt, seg.j0 = y;
+    seg.j1 = static_cast<int>(min(static_cast<long long>(nt), y + left));
+    left -= seg.j1 - seg.j0;
+    y = 0;
+    if (left > 0) advance(p, tu);
+    return true;
+  }
+  __device__ __forceinline__ bool advance(const Params& p, int tu) {
+    if ((++k) * tu < s.rows) return true;
+    k = 0;
+    if (s.rows > 0 && ++u < p.heads) return true;
+    u = 0;
+    if (++b >= p.B) return false;
+    s = load_seq(p, b);
+    return true;
+  }
+};
+
+// What tile x of a segment's unit is.
+struct TileRows {
+  int t0;       // first token
+  int j1;       // visits the segment's tiles [seg.j0, j1)
+  int lim_min;  // last key that all of its real rows see
+  __device__ __forceinline__ TileRows(const Params& p, const Seg& seg, int x, int nt_tiles) {
+    t0 = (seg.k * nt_tiles + x) * p.tq_tokens;
+    const int nt = tiles_of(p, seg.s, t0, t0 + p.tq_tokens);
+    j1 = max(seg.j0, min(seg.j1, nt));
+    lim_min = nt > 0 ? limit(p, seg.s, max(t0, -seg.s.p0)) : 0;
+  }
+};
+
+// The first tile of the unit with keys that some real row does not see.
+template <int NT>
+__device__ __forceinline__ int first_masked(const Params& p, const Seg& seg, int& lim0) {
+  lim0 = limit(p, seg.s, max(seg.k * NT * p.tq_tokens, -seg.s.p0));
+  return (lim0 + 1) / kBN;
+}
+
+// Position of K_j / V_j among a segment's loads K_0, K_1, V_0, K_2, V_1, ..,
+// K_{n-1}, V_{n-2}, V_{n-1}.
+__device__ __forceinline__ int item_of_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int item_of_v(int j, int n) { return j <= n - 2 ? 2 * j + 2 : 2 * n - 1; }
+
+// Divides the list: every CTA sums all sequences' tiles, then the thread whose
+// share of the sequences holds the CTA's first tile finds it.
+template <int D, int NT>
+__device__ __forceinline__ void plan(const Params& p, Barriers* bars) {
+  constexpr int kWarps = Cfg<D, NT>::kThreads / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int each = (p.B + Cfg<D, NT>::kThreads - 1) / Cfg<D, NT>::kThreads;
+  const int b0 = min(p.B, static_cast<int>(threadIdx.x) * each), b1 = min(p.B, b0 + each);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += seq_tiles<NT>(p, load_seq(p, b)) * p.heads;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) bars->scan[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += bars->scan[w];
+    total += bars->scan[w];
+  }
+  const long long per = (total + p.ctas - 1) / p.ctas;
+  const long long x0 = blockIdx.x * per;
+  if (threadIdx.x == 0) {
+    bars->per = per;
+    bars->start_left = max(0LL, min(per, total - x0));
+  }
+  if (x0 >= before && x0 < before + mine) {
+    long long x = x0 - before;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = load_seq(p, b);
+      const long long head = seq_tiles<NT>(p, s);
+      if (x >= head * p.heads) {
+        x -= head * p.heads;
+        continue;
+      }
+      const int u = static_cast<int>(x / head);
+      x -= u * head;
+      const int tu = NT * p.tq_tokens;
+      int k = 0;
+      for (;; ++k) {
+        const int nt = tiles_of(p, s, k * tu, (k + 1) * tu);
+        if (x < nt) break;
+        x -= nt;
+      }
+      bars->start[0] = b, bars->start[1] = u, bars->start[2] = k, bars->start[3] = static_cast<int>(x);
+      break;
+    }
+  }
+  __syncthreads();
+}
+
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D, NT>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem + C::kQOff;
+  uint8_t* sP = smem + C::kPOff;
+  uint8_t* sRing = smem + C::kRingOff;
+  Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kBarOff);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+
+  let_next_kernel_start();
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle needs it; the same for all threads
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusSmemAlign);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, NT);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&bars->kv_full[s], 1);
+      mbar_init(&bars->kv_empty[s], NT);
+      mbar_init(&bars->raw[s], 1);
+    }
+    for (int x = 0; x < NT; ++x) {
+      mbar_init(&bars->s_full[x], 1);
+      mbar_init(&bars->s_free[x], kBM);
+      mbar_init(&bars->p_full[x], kBM);
+      mbar_init(&bars->p_free[x], 1);
+      mbar_init(&bars->o_full[x], 1);
+      mbar_init(&bars->mma_done[x], 1);
+      mbar_init(&bars->group[x], kBM);
+    }
+    mbar_init(&bars->stagger, kBM);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&p.tq);
+    prefetch_tensormap(&p.to);
+    prefetch_tensormap(&p.tk);
+    prefetch_tensormap(&p.tv);
+  }
+  wait_for_previous_kernel();
+  plan<D, NT>(p, bars);
+  if (bars->start_left == 0) return;  // fewer tiles than CTAs
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  Cursor<NT> cur;
+  cur.start(p, bars);
+  Seg seg{};
+
+  if (warp >= C::kMmaWarp) {
+    if constexpr (NT == 2) regs_dec<kControlRegs>();
+    if (warp == C::kLoadWarp) {
+      // ================================================================ loader
+      // Lane = (box, column block) of a key tile: its page's rows.
+      const int boxes = kBN / p.box_rows;
+      const int box = lane % boxes, cb = lane / boxes;
+      const bool loads = cb < C::kColBlocks;
+      const int box_shift = 31 - __clz(p.box_rows);
+      const uint64_t keep = policy_evict_last(), once = policy_evict_first();
+      const int missing = p.n_pages * p.Hkv;  // a coordinate outside: zeros
+      int items = 0, segs = 0, tiles = 0;
+      bool ok = true;
+      // The lane's page of tile j, -1 behind the sequence.
+      auto lookup = [&](int j) {
+        const int key = j * kBN + (box << box_shift);
+        return key < seg.s.n ? p.page_table[static_cast<long long>(seg.b) * p.max_pages + (key >> p.page_shift)] : -1;
+      };
+      while (ok && cur.next(p, seg)) {
+        const int kvh = seg.u / p.nblk, h0 = (seg.u % p.nblk) * p.hb;
+        int lim0;
+        const int jm = first_masked<NT>(p, seg, lim0);
+        if (lane == 0) {
+          ok = segs == 0 || bounded_wait(&bars->q_empty, (segs - 1) & 1, abort_flag, p.status, kStatusTimeoutLoad);
+          if (ok) {
+            const int t0 = seg.k * NT * p.tq_tokens;
+            int real = 0;
+            for (int x = 0; x < NT; ++x) real += t0 + x * p.tq_tokens < seg.s.rows;
+            mbar_arrive_expect_tx(&bars->q_full, real * C::kColBlocks * p.hb * p.tq_tokens * 128);
+            for (int x = 0; x < real; ++x)
+              for (int c = 0; c < C::kColBlocks; ++c)
+                tma_load_5d(sQ + x * C::kTileBytes + c * C::kBlockBytes, &p.tq, &bars->q_full, c * 64, h0, kvh,
+                            t0 + x * p.tq_tokens, seg.b, once);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        ++segs;
+        auto issue = [&](bool is_v, int j, int page) {
+          const int st = items % C::kStages;
+          if (lane == 0 && items >= C::kStages)
+            ok = bounded_wait(&bars->kv_empty[st], (items / C::kStages - 1) & 1, abort_flag, p.status,
+                              kStatusTimeoutLoad);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) return;
+          const int key = j * kBN + (box << box_shift);
+          const bool inside = key < seg.s.n;
+          const bool found = inside && page >= 0 && page < p.n_pages;
+          if (!is_v) {
+            // Missing pages, by blocks of 16 keys: the softmax leaves them out.
+            uint32_t bad = __ballot_sync(0xffffffffu, cb == 0 && inside && !found);
+            if (bad != 0) {
+              if (lane == 0) report_index(p.status);
+              uint32_t wide = 0;
+              for (int i = 0; i < 8; ++i) wide |= ((bad >> (i * 16 >> box_shift)) & 1u) << i;
+              bad = wide;
+            }
+            if (lane == 0) bars->bad[tiles % kTileRing] = static_cast<uint8_t>(bad);
+            ++tiles;
+          }
+          const bool guarded = is_v && j >= jm;
+          uint64_t* bar = guarded ? &bars->raw[st] : &bars->kv_full[st];
+          if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
+          __syncwarp();
+          if (loads) {
+            const int z = found ? page * p.Hkv + kvh : missing;
+            tma_load_3d(sRing + st * C::kTileBytes + cb * C::kBlockBytes + (box << box_shift) * 128,
+                        is_v ? &p.tv : &p.tk, bar, cb * 64, found ? key & ((1 << p.page_shift) - 1) : 0, z, keep);
+          }
+          ++items;
+        };
+        const int n = seg.j1 - seg.j0;
+        int pa = lookup(seg.j0), pb = n > 1 ? lookup(seg.j0 + 1) : -1;
+        issue(false, seg.j0, pa);
+        for (int t = 0; ok && t < n; ++t) {
+          const int pc = t + 2 < n ? lookup(seg.j0 + t + 2) : -1;
+          if (t + 1 < n) issue(false, seg.j0 + t + 1, pb);
+          if (ok) issue(true, seg.j0 + t, pa);
+          pa = pb;
+          pb = pc;
+        }
+      }
+      // Every copy must have landed before the CTA ends.
+      if (lane == 0) {
+        int dummy = 0;
+        volatile int* ignore = reinterpret_cast<volatile int*>(&dummy);
+        if (segs > 0) bounded_wait(&bars->q_full, (segs - 1) & 1, ignore, p.status, kStatusTimeoutDrain);
+        for (int it = max(0, items - C::kStages); it < items; ++it)
+          bounded_wait(&bars->kv_full[it % C::kStages], (it / C::kStages) & 1, ignore, p.status, kStatusTimeoutDrain);
+      }
+      __syncwarp();
+    } else if (warp == C::kGuardWarp) {
+      // ================================================================ guard of V
+      constexpr int kCols = D / 32;  // of a lane, in one 16-byte piece
+      const int cbyte = lane * kCols * 2;
+      const int cb = cbyte / 128, chunk = (cbyte % 128) / 16, in_chunk = cbyte % 16;
+      constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
+      int items = 0, segs = 0;
+      uint32_t raw_phase = 0;
+      bool ok = true;
+      while (ok && cur.next(p, seg)) {
+        const int n = seg.j1 - seg.j0;
+        int lim0;
+        const int jm = max(seg.j0, first_masked<NT>(p, seg, lim0));
+        uint32_t first[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) first[c] = 255u;
+        for (int j = jm; j < seg.j1; ++j) {
+          const int it = items + item_of_v(j - seg.j0, n), st = it % C::kStages;
+          ok = bounded_wait(&bars->raw[st], (raw_phase >> st) & 1, abort_flag, p.status, kStatusTimeoutMma);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          raw_phase ^= 1u << st;
+          uint8_t* base = sRing + st * C::kTileBytes + cb * C::kBlockBytes;
+          for (int r = max(0, lim0 + 1 - j * kBN); r < kBN; ++r) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(base + r * 128 + ((chunk ^ (r & 7)) << 4) + in_chunk);
+            const int key = j * kBN + r;
+            if (key >= seg.s.n) {
+#pragma unroll
+              for (int i = 0; i < kCols / 2; ++i) w[i] = 0u;
+              continue;
+            }
+#pragma unroll
+            for (int i = 0; i < kCols / 2; ++i) {
+              uint32_t v = w[i];
+              const bool lo = (v & kExp) == kExp, hi = (v >> 16 & kExp) == kExp;
+              if (lo || hi) {
+                // below 255 where a row of the unit sees the key
+                const uint32_t e = min(static_cast<uint32_t>(key - lim0 - 1), 255u);
+                if (lo) first[2 * i] = min(first[2 * i], e), v &= 0xFFFF0000u;
+                if (hi) first[2 * i + 1] = min(first[2 * i + 1], e), v &= 0xFFFFu;
+                w[i] = v;
+              }
+            }
+          }
+          // Noted after each tile: a row tile may end before the unit's last one, and
+          // keys noted later are none of its rows'.
+          bool any = false;
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            any |= first[c] != 255u;
+            bars->nan_from[segs % kSegRing][lane * kCols + c] = static_cast<uint8_t>(first[c]);
+          }
+          any = __any_sync(0xffffffffu, any);
+          if (lane == 0) bars->nan_any[segs % kSegRing] = any;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->kv_full[st]);
+        }
+        items += 2 * n;
+        ++segs;
+      }
+    } else if (warp - C::kMmaWarp < NT) {
+      // ================================================================ MMA issuers
+      // One issuing thread per tile.  Each releases every K/V slot; key tiles that
+      // its rows do not visit are released once landed.
+      if (lane == 0) {
+        const int x = warp - C::kMmaWarp;
+        constexpr uint32_t kIdescQK = idesc_f16(BF16, false, false, kBM, kBN);
+        constexpr uint32_t kIdescPV = idesc_f16(BF16, false, true, kBM, D);
+        const uint32_t ring_addr = smem_u32(sRing);
+        const uint32_t s_col = tmem + x * kBN;
+        const uint32_t o_col = tmem + 2 * kBN + x * D;
+        const uint32_t p_tcol = tmem + 2 * kBN + 2 * D + x * (kBN / 2);
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ + x * C::kTileBytes), 16, 1024);
+        const uint64_t p_desc = smem_desc_sw128(smem_u32(sP + x * C::kStageBytes), 16, 1024);
+        auto issue_qk = [&](int st) {
+          const uint64_t kd = smem_desc_sw128(ring_addr + st * C::kTileBytes, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = ((kk / 4) * C::kBlockBytes + (kk % 4) * 32) >> 4;
+            mma_f16_ss(s_col, q_desc + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
+          }
+        };
+        auto issue_pv = [&](int st, bool accumulate) {
+          const uint64_t vd = smem_desc_sw128(ring_addr + st * C::kTileBytes, C::kBlockBytes, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk) {
+            const uint32_t acc = (accumulate || kk > 0) ? 1u : 0u;
+            if constexpr (C::kPInTmem) {
+              mma_f16_ts(o_col, p_tcol + kk * 8, vd + ((kk * 2048) >> 4), kIdescPV, acc);
+            } else {
+              const uint64_t poff = ((kk / 4) * C::kBlockBytes + (kk % 4) * 32) >> 4;
+              mma_f16_ss(o_col, p_desc + poff, vd + ((kk * 2048) >> 4), kIdescPV, acc);
+            }
+          }
+        };
+        int items = 0, segs = 0;
+        int done = 0;  // key tiles of this row tile so far
+        bool ok = true;
+        auto wait_item = [&](int item) {
+          return bounded_wait(&bars->kv_full[item % C::kStages], (item / C::kStages) & 1, abort_flag, p.status,
+                              kStatusTimeoutMma);
+        };
+        auto qk = [&](int item) {
+          const int st = item % C::kStages;
+          if (!(ok = wait_item(item))) return;
+          // S_X is in registers (of the tile before this one)
+          if (done > 0 && !(ok = bounded_wait(&bars->s_free[x], (done - 1) & 1, abort_flag, p.status, kStatusTimeoutMma)))
+            return;
+          tc_fence_after();
+          issue_qk(st);
+          mma_commit(&bars->s_full[x]);
+          mma_commit(&bars->kv_empty[st]);
+        };
+        while (ok && cur.next(p, seg)) {
+          const TileRows tile(p, seg, x, NT);
+          const int n = seg.j1 - seg.j0, nx = tile.j1 - seg.j0;
+          ok = bounded_wait(&bars->q_full, segs & 1, abort_flag, p.status, kStatusTimeoutMma);
+          // Tile L starts when tile H has read its first S: the two softmax chains
+          // then run staggered.
+          if (NT == 2 && ok && x == 1 && segs == 0 && nx > 0) {
+            const TileRows other(p, seg, 0, NT);
+            if (other.j1 > seg.j0) ok = bounded_wait(&bars->stagger, 0, abort_flag, p.status, kStatusTimeoutMma);
+          }
+          if (!ok) break;
+          if (nx > 0) qk(items);
+          if (nx <= 1) {
+            if (nx == 0) mbar_arrive(&bars->q_empty);
+            else if (ok) mma_commit(&bars->q_empty);
+          }
+          for (int j = 0; ok && j < nx; ++j, ++done) {
+            if (j + 1 < nx) {
+              ++done;  // qk(j + 1) waits for S of tile j
+              qk(items + item_of_k(j + 1));
+              --done;
+              if (!ok) break;
+              if (j + 2 == nx) mma_commit(&bars->q_empty);
+            }
+            const int it = items + item_of_v(j, n), st = it % C::kStages;
+            if (!(ok = wait_item(it))) break;
+            if (!(ok = bounded_wait(&bars->p_full[x], done & 1, abort_flag, p.status, kStatusTimeoutMma))) break;
+            tc_fence_after();
+            issue_pv(st, j > 0);
+            mma_commit(&bars->p_free[x]);
+            if (j == nx - 1) mma_commit(&bars->o_full[x]);
+            mma_commit(&bars->kv_empty[st]);
+          }
+          for (int j = nx; ok && j < n; ++j)
+            for (int kv = 0; kv < 2; ++kv) {
+              const int it = items + (kv ? item_of_v(j, n) : item_of_k(j));
+              if (!(ok = wait_item(it))) break;
+              mbar_arrive(&bars->kv_empty[it % C::kStages]);
+            }
+          items += 2 * n;
+          ++segs;
+        }
+        // Every MMA this thread issued must complete before TMEM is released.
+        mma_commit(&bars->mma_done[x]);
+        int dummy = 0;
+        bounded_wait(&bars->mma_done[x], 0, reinterpret_cast<volatile int*>(&dummy), p.status, kStatusTimeoutDrain);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ================================================================ softmax
+    if constexpr (NT == 2) regs_inc<kSoftmaxRegs>();
+    const int x = warp / 4;
+    const int wq = warp % 4;
+    const int row = wq * 32 + lane;
+    const int row_token = row / p.hb, row_head = row % p.hb;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t s_tmem = tmem + lane_off + x * kBN;
+    const uint32_t o_tmem = tmem + lane_off + 2 * kBN + x * D;
+    const uint32_t p_tmem = tmem + lane_off + 2 * kBN + 2 * D + x * (kBN / 2);
+    uint8_t* p_row = sP + x * C::kStageBytes + row * 128;
+    const float lam = p.scale_log2;
+    int done = 0, segs_x = 0, segs = 0, tiles = 0;
+    bool staged = false;  // an output's store may still read the staging buffer
+    bool ok = true;
+    uint32_t group_phase = 0;
+    // Barrier of the tile's four warps; like every wait it ends when another role gave up.
+    auto group_sync = [&]() {
+      mbar_arrive(&bars->group[x]);
+      ok = bounded_wait(&bars->group[x], group_phase, abort_flag, p.status, kStatusTimeoutSoftmax);
+      ok = __all_sync(0xffffffffu, ok);
+      group_phase ^= 1u;
+    };
+    auto stage_free = [&]() {
+      if (!staged) return;
+      if (wq == 0 && lane == 0) bulk_wait_group_read0();
+      group_sync();
+      staged = false;
+    };
+    while (ok && cur.next(p, seg)) {
+      const TileRows tile(p, seg, x, NT);
+      const int t = tile.t0 + row_token;
+      const int head = (seg.u % p.nblk) * p.hb + row_head;  // of the KV head's query heads
+      const bool in_tile = row_token < p.tq_tokens && head < p.g;
+      const bool real = in_tile && t < seg.s.rows && seg.s.p0 + t >= 0;
+      const int lim = real ? limit(p, seg.s, t) : -1;
+      float r = -INFINITY;  // retained reference, raw score units
+      float l = 0.f;
+      const int nx = tile.j1 - seg.j0;
+      for (int j = 0; j < nx; ++j, ++done) {
+        ok = bounded_wait(&bars->s_full[x], done & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int k0 = (seg.j0 + j) * kBN;
+        const uint32_t bad = bars->bad[(tiles + j) % kTileRing];
+        const bool masked = k0 + kBN - 1 > tile.lim_min || bad != 0;
+        uint32_t u[kBN];
+        float mq[kBN / 32];
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < kBN / 32; ++c)
+            tmem_ld32(s_tmem + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < kBN / 32; ++c)
+            tmem_ld32_max(s_tmem + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]), mq[c]);
+        }
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < kBN / 32; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
+        tc_fence_before();
+        mbar_arrive(&bars->s_free[x]);
+        if (NT == 2 && x == 0 && segs == 0 && j == 0) mbar_arrive(&bars->stagger);
+        float* s = reinterpret_cast<float*>(u);
+        float mx;
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < kBN; ++c)
+            if (k0 + c > lim) s[c] = -INFINITY;
+          if (bad != 0) {
+#pragma unroll
+            for (int c = 0; c < kBN; ++c)
+              if (bad >> (c / 16) & 1u) s[c] = -INFINITY;
+          }
+          float mx8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx8[i] = s[i];
+#pragma unroll
+          for (int c = 8; c < kBN; c += 16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx8[i] = fmax3(mx8[i], s[c + i], s[c + 8 + i < kBN ? c + 8 + i : c + i]);
+          mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+        } else {
+          mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        }
+        float gamma = 1.f;
+        if (j == 0) {
+          r = mx;
+        } else {
+          const float cand = fmaxf(r, mx);
+          if ((cand - r) * lam > kRescaleThreshold) {  // false when both are -inf
+            gamma = ex2_approx((r - cand) * lam);
+            r = cand;
+          }
+        }
+        l *= gamma;
+        const float rs = (r == -INFINITY) ? 0.f : r * lam;
+        const float2 lam2 = make_float2(lam, lam);
+        const float2 nrs2 = make_float2(-rs, -rs);
+        float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int blk = 0; blk < kBN / 64; ++blk) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c8 = 0; c8 < 8; ++c8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = blk * 64 + c8 * 8 + 2 * i;
+              const float2 e = ex2_pair(ffma2(make_float2(s[c], s[c + 1]), lam2, nrs2), (blk * 8 + c8) * 4 + i);
+              sum4[i] = fadd2(sum4[i], e);
+              pk[c8 * 4 + i] = pack2<BF16>(e.x, e.y);
+            }
+          }
+          if (blk == 0) {
+            if (j > 0) {
+              ok = bounded_wait(&bars->p_free[x], (done - 1) & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();  // P may be overwritten, O_X is stable
+              if (__any_sync(0xffffffffu, gamma != 1.f)) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  uint32_t w32[32];
+                  tmem_ld32(o_tmem + c * 32, w32);
+                  tmem_wait_ld();
+                  reg_fence32(w32);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) w32[i] = __float_as_uint(__uint_as_float(w32[i]) * gamma);
+                  tmem_st32(o_tmem + c * 32, w32);
+                }
+                tmem_wait_st();
+              }
+            } else if constexpr (!C::kPInTmem) {
+              stage_free();
+              if (!ok) break;
+            }
+          }
+          if constexpr (C::kPInTmem) {
+            tmem_st32(p_tmem + blk * 32, pk);
+          } else {
+#pragma unroll
+            for (int c8 = 0; c8 < 8; ++c8)
+              *reinterpret_cast<uint4*>(p_row + blk * C::kBlockBytes + ((c8 ^ (row & 7)) << 4)) =
+                  make_uint4(pk[c8 * 4], pk[c8 * 4 + 1], pk[c8 * 4 + 2], pk[c8 * 4 + 3]);
+          }
+        }
+        if (!ok) break;
+        const float2 s01 = fadd2(fadd2(sum4[0], sum4[1]), fadd2(sum4[2], sum4[3]));
+        l += s01.x + s01.y;
+        if constexpr (C::kPInTmem) {
+          tmem_wait_st();
+        } else {
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[x]);
+      }
+      if (!ok) break;
+      // ---- the segment's end
+      if (nx > 0) {
+        ok = bounded_wait(&bars->o_full[x], segs_x & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        ++segs_x;
+      }
+      // Columns whose guarded rows of V are not finite for this row.
+      int lim0;
+      const bool guarded = tile.j1 > max(seg.j0, first_masked<NT>(p, seg, lim0));
+      const bool nan_any = guarded && bars->nan_any[segs % kSegRing] != 0;
+      const uint8_t* nan_from = bars->nan_from[segs % kSegRing];
+      const int seen = real ? lim - lim0 : 0;
+      if (seg.whole()) {
+        if (tile.t0 < p.S) {
+          const float inv = (!real || l == 0.f) ? 0.f : 1.f / l;
+          stage_free();
+          if (!ok) break;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t u[32];
+            if (nx > 0) {
+              tmem_ld32(o_tmem + c * 32, u);
+              tmem_wait_ld();
+              reg_fence32(u);
+            }
+            if (nx == 0 || inv == 0.f) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) u[i] = 0u;
+            }
+            if (nan_any) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (seen > nan_from[c * 32 + i]) u[i] = 0x7FFFFFFFu;
+            }
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              pk[i] = pack2<BF16>(__uint_as_float(u[2 * i]) * inv, __uint_as_float(u[2 * i + 1]) * inv);
+            uint8_t* blk = p_row + (c / 2) * C::kBlockBytes;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int ch = (c % 2) * 4 + k;
+              *reinterpret_cast<uint4*>(blk + ((ch ^ (row & 7)) << 4)) =
+                  make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+            }
+          }
+          tc_fence_before();  // O_X has been read before P's arrival lets it be overwritten
+          fence_proxy_async_smem();
+          group_sync();
+          if (!ok) break;
+          if (wq == 0 && lane == 0) {
+            for (int cb = 0; cb < C::kColBlocks; ++cb)
+              tma_store_5d(&p.to, sP + x * C::kStageBytes + cb * C::kBlockBytes, cb * 64, (seg.u % p.nblk) * p.hb,
+                           seg.u / p.nblk, tile.t0, seg.b);
+            bulk_commit_group();
+          }
+          staged = true;
+          if (p.lse != nullptr && in_tile && t < p.S) {
+            const float lse = !real || l == 0.f ? -INFINITY : (r * lam + __log2f(l)) * 0.69314718055994531f;
+            p.lse[(static_cast<long long>(seg.b) * p.H + (seg.u / p.nblk) * p.g + head) * p.S + t] = lse;
+          }
+        }
+      } else {
+        const long long part = blockIdx.x * 2LL + (seg.j0 > 0 ? 0 : 1);
+        const long long prow = part * (NT * kBM) + x * kBM + row;
+        const bool counts = real && nx > 0 && l != 0.f;
+        p.part_ml[prow] = counts ? make_float2(r * lam, l) : make_float2(-INFINITY, 0.f);
+        if (__any_sync(0xffffffffu, counts)) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o) + part * (D / 4) * (NT * kBM) + x * kBM + row;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t u[32];
+            tmem_ld32(o_tmem + c * 32, u);
+            tmem_wait_ld();
+            reg_fence32(u);
+            if (nan_any) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (seen > nan_from[c * 32 + i]) u[i] = 0x7FFFFFFFu;
+            }
+            if (counts) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[(c * 8 + i) * (NT * kBM)] =
+                    make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                                __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3]));
+            }
+          }
+          tc_fence_before();
+        }
+      }
+      // The CTA that has the unit's first tile says where its parts are.
+      if (seg.j0 == 0 && threadIdx.x == 0) {
+        const long long behind = seg.nt - (seg.j1 - seg.j0);  // the unit's tiles in the runs after this one
+        p.parts[(static_cast<long long>(seg.b) * p.heads + seg.u) * p.blocks + seg.k] =
+            make_int2(blockIdx.x, 1 + static_cast<int>((behind + bars->per - 1) / bars->per));
+      }
+      tiles += seg.j1 - seg.j0;
+      ++segs;
+    }
+    if (staged && wq == 0 && lane == 0) bulk_wait_group_read0();
+  }
+
+  // ---- teardown: all TMEM traffic done before the allocator warp frees it
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Folds the parts of units that were split, in the order of the parts, and writes
+// the zeros of units without a real row; launched while the first kernel runs, it
+// waits for its end.  A warp takes 32 rows of a unit, lane = row (the parts' layout),
+// D / kSlices elements each.
+constexpr int kMergeThreads = 128;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kMergeThreads) prefill_paged_merge_kernel(const __grid_constant__ Params p) {
+  constexpr int kSlice = 16;                 // elements of a warp's row
+  constexpr int kSlices = D / kSlice, kRowBlocks = NT * kBM / 32;
+  const int lane = threadIdx.x % 32;
+  const int rows_used = p.hb * p.tq_tokens;
+  wait_for_previous_kernel();
+  const long long units = static_cast<long long>(p.B) * p.heads * p.blocks;
+  const long long work = units * kRowBlocks * kSlices;
+  for (long long w = blockIdx.x * (kMergeThreads / 32LL) + threadIdx.x / 32; w < work;
+       w += gridDim.x * (kMergeThreads / 32LL)) {
+    const int slice = static_cast<int>(w % kSlices), rb = static_cast<int>(w / kSlices % kRowBlocks);
+    const long long unit = w / (kSlices * kRowBlocks);
+    const int k = static_cast<int>(unit % p.blocks);
+    const int u = static_cast<int>(unit / p.blocks % p.heads), b = static_cast<int>(unit / p.blocks / p.heads);
+    const int x = rb / (kBM / 32), row = rb % (kBM / 32) * 32 + lane;
+    const int tu = NT * p.tq_tokens;
+    const Seq s = load_seq(p, b);
+    int2 part = make_int2(0, 0);
+    if (tiles_of(p, s, k * tu, (k + 1) * tu) > 0) {
+      part = p.parts[unit];
+      if (part.y <= 1) continue;  // finished by one CTA
+    }
+    const int t = k * tu + x * p.tq_tokens + row / p.hb, head = (u % p.nblk) * p.hb + row % p.hb;
+    if (row >= rows_used || head >= p.g || t >= p.S) continue;
+    float M = -INFINITY;
+    auto state = [&](int i) { return (part.x + i) * 2LL + (i == 0 ? 1 : 0); };
+    for (int i = 0; i < part.y; ++i) M = fmaxf(M, p.part_ml[state(i) * (NT * kBM) + x * kBM + row].x);
+    float l = 0.f;
+    float acc[kSlice];
+#pragma unroll
+    for (int e = 0; e < kSlice; ++e) acc[e] = 0.f;
+    for (int i = 0; i < part.y; ++i) {
+      const float2 ml = p.part_ml[state(i) * (NT * kBM) + x * kBM + row];
+      if (ml.y == 0.f) continue;  // no key of this part counts
+      const float f = ml.x == M ? 1.f : ex2_approx(ml.x - M);
+      l = fmaf(f, ml.y, l);
+      const float4* src = reinterpret_cast<const float4*>(p.part_o) +
+                          (state(i) * (D / 4) + slice * (kSlice / 4)) * (NT * kBM) + x * kBM + row;
+#pragma unroll
+      for (int e = 0; e < kSlice / 4; ++e) {
+        const float4 v = src[e * (NT * kBM)];
+        acc[4 * e] = fmaf(f, v.x, acc[4 * e]);
+        acc[4 * e + 1] = fmaf(f, v.y, acc[4 * e + 1]);
+        acc[4 * e + 2] = fmaf(f, v.z, acc[4 * e + 2]);
+        acc[4 * e + 3] = fmaf(f, v.w, acc[4 * e + 3]);
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t out[kSlice / 2];
+#pragma unroll
+    for (int e = 0; e < kSlice; e += 2)
+      out[e / 2] = p.out_bf16 ? pack2<true>(acc[e] * inv, acc[e + 1] * inv) : pack2<false>(acc[e] * inv, acc[e + 1] * inv);
+    const long long hrow = (static_cast<long long>(b) * p.H + (u / p.nblk) * p.g + head) * p.S + t;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + hrow * D + slice * kSlice);
+    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+    if (slice == 0 && p.lse != nullptr)
+      p.lse[hrow] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+// How a problem is cut into units.
+struct Shape {
+  int hb, tokens, nblk, heads, nt, blocks;
+  long long units;
+};
+Shape shape_of(int B, int H, int Hkv, int S) {
+  Shape s;
+  const int g = H / Hkv;
+  s.nblk = (g + kBM - 1) / kBM;
+  s.hb = (g + s.nblk - 1) / s.nblk;
+  s.tokens = kBM / s.hb;
+  s.heads = Hkv * s.nblk;
+  s.nt = S <= s.tokens ? 1 : 2;
+  s.blocks = (S + s.nt * s.tokens - 1) / (s.nt * s.tokens);
+  s.units = static_cast<long long>(B) * s.heads * s.blocks;
+  return s;
+}
+
+// CTAs that can have work: one for each key tile at most.
+int max_ctas(const Shape& s, int max_len) {
+  const long long per_unit = (static_cast<long long>(max_len) + kBN - 1) / kBN;
+  return s.units >= kMaxCtas || s.units * per_unit >= kMaxCtas ? kMaxCtas : static_cast<int>(s.units * per_unit);
+}
+
+template <int D, bool BF16, int NT>
+int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
+  using C = Cfg<D, NT>;
+  const CacheArgs& c = a.cache;
+  const int page = 1 << c.page_shift;
+  p.box_rows = page < kBN ? page : kBN;
+  if (!make_tmap_heads(&p.tq, a.q, BF16, D, p.g, p.Hkv, a.S, a.B, s.hb, s.tokens) ||
+      !make_tmap_heads(&p.to, a.o, BF16, D, p.g, p.Hkv, a.S, a.B, s.hb, s.tokens) ||
+      !make_tmap_3d(&p.tk, c.data[0], BF16, D, page, static_cast<long long>(c.n_pages) * c.Hkv, p.box_rows) ||
+      !make_tmap_3d(&p.tv, c.data[1], BF16, D, page, static_cast<long long>(c.n_pages) * c.Hkv, p.box_rows))
+    return -1;
+  auto kern = prefill_paged_kernel<D, BF16, NT>;
+  static std::atomic<unsigned long long> attr_done{0};  // per instantiation
+  if (!set_smem_limit_once(kern, C::kSmemBytes, attr_done)) return -1;
+  if (launch_after(kern, dim3(static_cast<unsigned>(p.ctas)), C::kThreads, a.stream, p, C::kSmemBytes) != 0) return -1;
+  const long long warps = s.units * (NT * kBM / 32) * (D / 16);
+  long long ctas = (warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+  if (ctas > 8LL * a.num_sms) ctas = 8LL * a.num_sms;
+  return launch_after(prefill_paged_merge_kernel<D, NT>, dim3(static_cast<unsigned>(ctas)), kMergeThreads, a.stream, p);
+}
+
+template <int D, bool BF16>
+int launch_nt(Params& p, const PagedPrefillArgs& a, const Shape& s) {
+  return s.nt == 1 ? launch_t<D, BF16, 1>(p, a, s) : launch_t<D, BF16, 2>(p, a, s);
+}
+
+}  // namespace
+
+size_t paged_prefill_workspace_bytes(int B, int H, int Hkv, int S, int d, int max_len) {
+  const Shape s = shape_of(B, H, Hkv, S);
+  return static_cast<size_t>(max_ctas(s, max_len)) * 2 * s.nt * kBM * (static_cast<size_t>(d) + 2) * sizeof(float) +
+         static_cast<size_t>(s.units) * sizeof(int2);
+}
+
+int launch_prefill_paged(const PagedPrefillArgs& a) {
+  const CacheArgs& c = a.cache;
+  const Shape s = shape_of(a.B, a.H, c.Hkv, a.S);
+  Params p{};
+  p.page_table = c.page_table;
+  p.seqlens = c.seqlens;
+  p.new_lens = a.new_lens;
+  p.o = a.o;
+  p.lse = a.lse;
+  p.B = a.B;
+  p.H = a.H;
+  p.Hkv = c.Hkv;
+  p.S = a.S;
+  p.g = a.H / c.Hkv;
+  p.hb = s.hb;
+  p.tq_tokens = s.tokens;
+  p.nblk = s.nblk;
+  p.heads = s.heads;
+  p.blocks = s.blocks;
+  p.page_shift = c.page_shift;
+  p.n_pages = c.n_pages;
+  p.max_pages = c.max_pages;
+  p.causal = a.causal;
+  p.out_bf16 = a.bf16 ? 1 : 0;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  const int most = max_ctas(s, c.max_pages << c.page_shift);
+  p.ctas = most < a.num_sms ? most : a.num_sms;
+  p.status = a.status;
+  const size_t states = static_cast<size_t>(most) * 2 * s.nt * kBM;
+  float* ws = static_cast<float*>(a.workspace);
+  p.part_o = ws;
+  p.part_ml = reinterpret_cast<float2*>(ws + states * c.d);
+  p.parts = reinterpret_cast<int2*>(ws + states * (c.d + 2));
+  if (c.d == 128) return a.bf16 ? launch_nt<128, true>(p, a, s) : launch_nt<128, false>(p, a, s);
+  return a.bf16 ? launch_nt<64, true>(p, a, s) : launch_nt<64, false>(p, a, s);
+}
+
+}  // namespace gbattn

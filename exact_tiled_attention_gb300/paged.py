@@ -132,6 +132,29 @@ def attn_cache_gather_fp4(k_codes, k_factors, v_codes, v_factors, page_table, se
                                                       k_descale, v_descale, dtype, k_out, v_out, stream)
 
 
+def attn_fwd_paged_workspace_bytes(B: int, H: int, Hkv: int, S: int, d: int, max_len: int = 2 ** 31 - 1) -> int:
+    """Bytes of the paged forwards' workspace; smaller where max_len, the tokens
+    that max_pages pages hold, is short."""
+    return int(load_library().attn_fwd_paged_workspace_bytes(B, H, Hkv, S, d, max_len))
+
+
+def attn_fwd_paged(q, k_cache, v_cache, page_table, seqlens, new_lens=None, scale: float | None = None,
+                   causal: bool = True, workspace=None, out=None, lse=None, return_lse: bool = True, stream=None):
+    """Attention of a chunk of new tokens over a 16-bit paged cache that holds
+    them already, through the C ABI `attn_fwd_paged`.
+
+    q [B,H,S,d] contiguous; k_cache, v_cache [n_pages,Hkv,page_size,d];
+    page_table int32 [B,max_pages]; seqlens int32 [B], the new tokens included;
+    new_lens int32 [B] (None: S): row i of q is the token at position
+    seqlens - new_lens + i; the rows from new_lens on are padding (o = 0,
+    lse = -inf).  causal: a token sees the keys up to its own, or else all of its
+    sequence's.  workspace: optional buffer of attn_fwd_paged_workspace_bytes(B,
+    H, Hkv, S, d) bytes (allocated here if omitted).  Returns (o [B,H,S,d],
+    lse [B,H,S] or None)."""
+    return (_native or _load()).attn_fwd_paged(q, k_cache, v_cache, page_table, seqlens, new_lens, scale, causal,
+                                               workspace, out, lse, return_lse, stream)
+
+
 def attn_decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, d: int, max_len: int = 2 ** 31 - 1) -> int:
     """Bytes of the paged decodes' workspace; smaller where max_len, the tokens
     that max_pages pages hold, is short."""

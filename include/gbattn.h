@@ -550,6 +550,47 @@ int attn_decode_paged_fp4(const void *q, const void *k_codes, const void *k_fact
                           size_t workspace_bytes, int dtype, void *stream);
 
 /*
+ * attn_fwd_paged_workspace_bytes -- bytes of device workspace attn_fwd_paged
+ * needs: two partial states (m, l, o[d]) of up to 256 rows for each CTA of the
+ * grid, and two ints for each unit of work.  max_len as for
+ * attn_decode_paged_workspace_bytes.  Returns 0 for invalid sizes.
+ */
+size_t attn_fwd_paged_workspace_bytes(int B, int H, int Hkv, int S, int d, int max_len);
+
+/*
+ * attn_fwd_paged -- attention of a chunk of new tokens over a 16-bit paged cache
+ * that holds them already (attn_cache_append) and everything before them.  The
+ * sequences may have different lengths and numbers of new tokens.
+ *
+ *   q [B, H, S, d]  dtype, input, contiguous;  o [B, H, S, d]  dtype, output
+ *   lse [B, H, S]  fp32, output; may be NULL
+ *   seqlens, new_lens: as for attn_cache_append, seqlens with the new tokens and
+ *            new_lens NULL for S.  Row i < new_lens[b] is the token at position
+ *            seqlens[b] - new_lens[b] + i.  Rows from new_lens[b] on, and rows whose
+ *            position is negative, are padding: o = 0 and lse = -inf
+ *   causal   1: the token at position t sees the keys 0 .. t; 0: all keys of its
+ *            sequence (tokens of one image, for instance)
+ *   scale    positive and finite
+ *   workspace: at least attn_fwd_paged_workspace_bytes(B, H, Hkv, S, d,
+ *            max_pages * page_size) bytes, 16-byte aligned; contents on entry do not
+ *            matter; calls that may overlap on the GPU need one each
+ * o may not overlap an input.  The work is divided by the lengths, evenly over the
+ * GPU; results repeat bitwise.  A key that a row does not see has no influence on
+ * it, whatever its k and v hold.  Of the keys that it sees: a score of NaN or +inf
+ * makes the row's o and lse NaN, and a NaN or an infinity in v its element of o.
+ * Scores and their sums are fp32; exp(score - maximum) is rounded to dtype for the
+ * product with v, as in attn_fwd.
+ *
+ * Errors: GBATTN_EBADSHAPE (also H > 16384, B * S > 2^30, n_pages * Hkv >= 2^31 or a scale that is not
+ * positive and finite), EHEADS, EHEADDIM, EDTYPE, EPAGE, EPOINTER, EWORKSPACE,
+ * EUNSUPPORTED, ELAUNCH.
+ */
+int attn_fwd_paged(const void *q, const void *k_cache, const void *v_cache, const int *page_table,
+                   const int *seqlens, const int *new_lens, void *o, float *lse, int B, int H,
+                   int Hkv, int S, int d, int page_size, int n_pages, int max_pages, float scale,
+                   int causal, void *workspace, size_t workspace_bytes, int dtype, void *stream);
+
+/*
  * gbattn_causal_tile_counts -- host-only planning helper (no device work).
  * Classifies the (ceil(Sq/Br) x ceil(Sk/Bc)) tile grid with the half-open
  * ranges of M4.4 0x05.1A-B and delta = Sk - Sq:
