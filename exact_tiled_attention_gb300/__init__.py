@@ -39,6 +39,7 @@ from .paged import (  # noqa: F401
     attn_decode_paged_fp4,
     attn_decode_paged_workspace_bytes,
     attn_fwd_paged,
+    attn_fwd_paged_fp4,
     attn_fwd_paged_workspace_bytes,
     attn_qk_norm_rope,
     attn_qk_norm_rope_bwd,

@@ -39,7 +39,7 @@ EXPORTS = ("attn_fwd", "attn_fwd_pair", "attn_decode_workspace_bytes", "attn_dec
            "attn_qk_norm_rope", "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_bwd",
            "attn_cache_append", "attn_cache_append_fp4", "attn_cache_gather", "attn_cache_gather_fp4",
            "attn_decode_paged_workspace_bytes", "attn_decode_paged", "attn_decode_paged_fp4",
-           "attn_fwd_paged_workspace_bytes", "attn_fwd_paged")
+           "attn_fwd_paged_workspace_bytes", "attn_fwd_paged", "attn_fwd_paged_fp4")
 
 _lock = threading.Lock()
 _lib = None
@@ -115,6 +115,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.attn_fwd_paged_workspace_bytes.restype = sz
         lib.attn_fwd_paged.argtypes = [vp] * 8 + [ci] * 8 + [cf, ci, vp, sz, ci, vp]
         lib.attn_fwd_paged.restype = ci
+        lib.attn_fwd_paged_fp4.argtypes = [vp] * 12 + [ci] * 8 + [cf, ci, vp, sz, ci, vp]
+        lib.attn_fwd_paged_fp4.restype = ci
         lib.gbattn_exp2_paths.argtypes = [vp, vp, vp, ctypes.c_longlong, vp]
         lib.gbattn_exp2_paths.restype = ci
         lib.gbattn_causal_tile_counts.argtypes = [ci, ci, ci, ci, ll_p, ll_p, ll_p, ll_p, ll_p]

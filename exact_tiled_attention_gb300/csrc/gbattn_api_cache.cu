@@ -357,4 +357,14 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
                  stream);
 }
 
+int attn_fwd_paged_fp4(const void* q, const void* k_codes, const void* k_factors, const void* v_codes,
+                       const void* v_factors, const float* k_descale, const float* v_descale, const int* page_table,
+                       const int* seqlens, const int* new_lens, void* o, float* lse, int B, int H, int Hkv, int S,
+                       int d, int page_size, int n_pages, int max_pages, float scale, int causal, void* workspace,
+                       size_t workspace_bytes, int dtype, void* stream) {
+  return prefill(q, k_codes, k_factors, v_codes, v_factors, true, k_descale, v_descale, page_table, seqlens, new_lens,
+                 o, lse, B, H, Hkv, S, d, page_size, n_pages, max_pages, scale, causal, workspace, workspace_bytes,
+                 dtype, stream);
+}
+
 }  // extern "C"

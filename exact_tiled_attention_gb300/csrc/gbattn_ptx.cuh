@@ -147,6 +147,17 @@ __device__ __forceinline__ void tma_store_5d(const CUtensorMap* map, const void*
                : "memory");
 }
 
+// Untiled copy of `bytes` consecutive bytes into shared memory, completing on `bar`;
+// both addresses and the size are multiples of 16.
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar,
+                                          uint64_t cache_hint) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar)), "l"(cache_hint)
+      : "memory");
+}
+
 // Prefetch of one 3-D box into L2 (no shared memory, no completion); the
 // same coordinate rules as a tiled load.
 __device__ __forceinline__ void tma_prefetch_l2_3d(const CUtensorMap* map, int x, int y, int z) {

@@ -543,9 +543,15 @@ PyObject* fwd_paged(const First& f, PyObject* qo, int64_t Hkv, const Cache& c, P
   Output out, lse;
   out.take(o[0], "out", q.sizes(), f.type, f.device);
   if (!none(o[1]) || truth(o[2])) lse.take(o[1], "lse", {B, H, S}, at::kFloat, f.device);
-  done(attn_fwd_paged(q_ptr, c.k, c.v, c.table, c.lens, n, out.data, static_cast<float*>(lse.data), B, H, hkv, S, d,
-                      c.page, c.n_pages, c.max_pages, scale, causal, ws.data, ws.bytes, f.code, target.stream),
-       "attn_fwd_paged");
+  if (fp4)
+    done(attn_fwd_paged_fp4(q_ptr, c.k, c.k_factors, c.v, c.v_factors, c.k_descale, c.v_descale, c.table, c.lens, n,
+                            out.data, static_cast<float*>(lse.data), B, H, hkv, S, d, c.page, c.n_pages, c.max_pages,
+                            scale, causal, ws.data, ws.bytes, f.code, target.stream),
+         "attn_fwd_paged_fp4");
+  else
+    done(attn_fwd_paged(q_ptr, c.k, c.v, c.table, c.lens, n, out.data, static_cast<float*>(lse.data), B, H, hkv, S, d,
+                        c.page, c.n_pages, c.max_pages, scale, causal, ws.data, ws.bytes, f.code, target.stream),
+         "attn_fwd_paged");
   return tuple({&out, &lse});
 }
 
@@ -555,6 +561,14 @@ PyObject* forward_paged(PyObject* const* a) {
   const int64_t Hkv = tensor_of_dims(a[1], "k_cache", 4).size(1);
   const Cache c(a[1], a[2], a[3], a[4], q.size(0), Hkv, q.size(3), f);
   return fwd_paged(f, a[0], Hkv, c, a[5], a[6], a[7], a[8], a + 9, false);
+}
+
+PyObject* forward_paged_fp4(PyObject* const* a) {
+  const First f = first(a[0], "q");
+  const Tensor& q = THPVariable_Unpack(a[0]);
+  const int64_t Hkv = tensor_of_dims(a[1], "k_codes", 4).size(1);
+  const Cache c(a + 1, a[8], a[9], q.size(0), Hkv, q.size(3), f.device);
+  return fwd_paged(f, a[0], Hkv, c, a[7], a[10], a[11], a[12], a + 13, true);
 }
 
 // A function of N positional arguments; no C++ exception leaves it.
@@ -594,6 +608,7 @@ PyMethodDef methods[] = {
     method<cache_gather, 8>("attn_cache_gather"),
     method<cache_gather_fp4, 13>("attn_cache_gather_fp4"),
     method<forward_paged, 13>("attn_fwd_paged"),
+    method<forward_paged_fp4, 17>("attn_fwd_paged_fp4"),
     method<decode_paged, 11>("attn_decode_paged"),
     method<decode_paged_fp4, 15>("attn_decode_paged_fp4"),
     {nullptr, nullptr, 0, nullptr},

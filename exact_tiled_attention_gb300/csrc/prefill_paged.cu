@@ -50,31 +50,48 @@ constexpr float kRescaleThreshold = 8.f;  // base-2 units
 constexpr int kSegRing = 8;       // segments whose notes of the guard are kept
 constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
 
-template <int D, int NT>
+template <int D, int NT, bool FP4>
 struct Cfg {
   static constexpr bool kPInTmem = (D == 64);
   static constexpr int kColBlocks = D / 64;
   static constexpr int kTileBytes = kBM * D * 2;
   static constexpr int kBlockBytes = kBM * 128;
   static constexpr int kStageBytes = kPInTmem ? kTileBytes : kBM * kBN * 2;  // P, or (d = 64) the output alone
-  static constexpr int kStages = NT == 2 ? (D == 128 ? 3 : 8) : (D == 128 ? 5 : 12);
+  // 16-bit key and value tiles; of a 4-bit cache's rows, what comes from memory and
+  // what the conversion makes of it.
+  static constexpr int kStages = FP4 ? (NT == 2 ? (D == 128 ? 2 : 6) : (D == 128 ? 3 : 6))
+                                     : (NT == 2 ? (D == 128 ? 3 : 8) : (D == 128 ? 5 : 12));
+  static constexpr int kRawStages = !FP4 ? 0 : NT == 2 ? (D == 128 ? 3 : 8) : (D == 128 ? 7 : 12);
+  static constexpr int kRawBytes = kBN * (D / 2 + D / 16);  // codes, then factors
   static constexpr int kQOff = 0;
   static constexpr int kPOff = NT * kTileBytes;
   static constexpr int kRingOff = kPOff + NT * kStageBytes;
-  static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kBarOff = kRawOff + kRawStages * kRawBytes;
   static constexpr int kSmemBytes = kBarOff + 2048;
   static constexpr int kMmaWarp = 4 * NT;  // tile x's issuer is warp kMmaWarp + x
   static constexpr int kLoadWarp = 4 * NT + 2;
   static constexpr int kGuardWarp = 4 * NT + 3;
-  static constexpr int kThreads = 128 * (NT + 1);
+  static constexpr int kConvertWarp = 4 * NT + 4;  // the first of kConvertWarps
+  static constexpr int kConvertWarps = FP4 ? (NT == 2 ? 4 : 8) : 0;
+  static constexpr int kThreads = 128 * (NT + 1) + 32 * kConvertWarps;
+  // Registers a thread: at launch, and after the warpgroups have divided them (not
+  // with one tile over 16 bits, where there are enough).
+  static constexpr bool kSplit = FP4 || NT == 2;
+  static constexpr int kLaunchRegs = FP4 ? 128 : 168;
+  static constexpr int kSoftmaxRegs = FP4 ? (NT == 2 ? 200 : 240) : 216;
+  static constexpr int kControlRegs = FP4 ? (NT == 2 ? 56 : 64) : 72;
+  static constexpr int kConvertRegs = NT == 2 ? 56 : 104;
+  static_assert(!kSplit || NT * 128 * kSoftmaxRegs + 128 * kControlRegs + 32 * kConvertWarps * kConvertRegs <=
+                               kThreads * kLaunchRegs,
+                "register split");
 };
-// With two tiles; the 168 registers a thread that the kernel is launched with suffice
-// for one.
-constexpr int kSoftmaxRegs = 224, kControlRegs = 56;
-static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= 384 * 168, "register split");
 
 struct Params {
-  CUtensorMap tq, to, tk, tv;
+  CUtensorMap tq, to, tk, tv;   // (no tk, tv for a 4-bit cache)
+  const uint8_t* codes[2];
+  const uint8_t* factors[2];
+  const float* descale[2];
   const int* page_table;
   const int* seqlens;
   const int* new_lens;
@@ -95,6 +112,8 @@ struct Params {
 
 struct __align__(8) Barriers {
   uint64_t q_full, q_empty;
+  uint64_t q_ready[2];     // queries converted to fp16 (bf16 over 4 bits)
+  uint64_t raw_empty[12];  // 4 bits: codes and factors converted (raw: copied)
   uint64_t kv_full[12], kv_empty[12], raw[12];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_full[2], mma_done[2];
   uint64_t group[2];       // the four warps of a softmax warpgroup
@@ -102,7 +121,7 @@ struct __align__(8) Barriers {
   long long per;           // tiles of a run
   long long start_left;    // tiles of this run
   int start[4];            // its first unit (sequence, head, block) and tile
-  long long scan[12];
+  long long scan[16];
   uint32_t tmem_base;
   int abort_flag;
   uint8_t bad[kTileRing];          // 16-key blocks of a tile that have no page
@@ -220,11 +239,11 @@ __device__ __forceinline__ int item_of_v(int j, int n) { return j <= n - 2 ? 2 *
 
 // Divides the list: every CTA sums all sequences' tiles, then the thread whose
 // share of the sequences holds the CTA's first tile finds it.
-template <int D, int NT>
+template <int D, int NT, bool FP4>
 __device__ __forceinline__ void plan(const Params& p, Barriers* bars) {
-  constexpr int kWarps = Cfg<D, NT>::kThreads / 32;
+  constexpr int kWarps = Cfg<D, NT, FP4>::kThreads / 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int each = (p.B + Cfg<D, NT>::kThreads - 1) / Cfg<D, NT>::kThreads;
+  const int each = (p.B + Cfg<D, NT, FP4>::kThreads - 1) / Cfg<D, NT, FP4>::kThreads;
   const int b0 = min(p.B, static_cast<int>(threadIdx.x) * each), b1 = min(p.B, b0 + each);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) mine += seq_tiles<NT>(p, load_seq(p, b)) * p.heads;
@@ -273,9 +292,28 @@ __device__ __forceinline__ void plan(const Params& p, Barriers* bars) {
   __syncthreads();
 }
 
-template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<D, NT>;
+// The four pairs of E2M1 codes of a word as fp16 pairs, times a factor's fp16 pair:
+// exact, 2 by 4 significant bits of at most 2688.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t f, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 t0, t1, t2, t3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 t0, b0;\n\tcvt.rn.f16x2.e2m1x2 t1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 t2, b2;\n\tcvt.rn.f16x2.e2m1x2 t3, b3;\n\t"
+      "mul.rn.f16x2 %0, t0, %5;\n\tmul.rn.f16x2 %1, t1, %5;\n\t"
+      "mul.rn.f16x2 %2, t2, %5;\n\tmul.rn.f16x2 %3, t3, %5;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w), "r"(f));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+
+template <int D, bool BF16, int NT, bool FP4>
+__global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D, NT, FP4>;
+  constexpr bool kMmaBf16 = BF16 && !FP4;  // over 4 bits all operands are fp16
+  constexpr bool kConvertQ = BF16 && FP4;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem + C::kQOff;
   uint8_t* sP = smem + C::kPOff;
@@ -294,11 +332,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, NT);
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&bars->kv_full[s], 1);
+      mbar_init(&bars->kv_full[s], FP4 ? C::kConvertWarps : 1);
       mbar_init(&bars->kv_empty[s], NT);
+      if (!FP4) mbar_init(&bars->raw[s], 1);
+    }
+    for (int s = 0; s < C::kRawStages; ++s) {
       mbar_init(&bars->raw[s], 1);
+      mbar_init(&bars->raw_empty[s], C::kConvertWarps);
     }
     for (int x = 0; x < NT; ++x) {
+      mbar_init(&bars->q_ready[x], kBM);
       mbar_init(&bars->s_full[x], 1);
       mbar_init(&bars->s_free[x], kBM);
       mbar_init(&bars->p_full[x], kBM);
@@ -312,11 +355,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
     fence_mbar_init();
     prefetch_tensormap(&p.tq);
     prefetch_tensormap(&p.to);
-    prefetch_tensormap(&p.tk);
-    prefetch_tensormap(&p.tv);
+    if (!FP4) {
+      prefetch_tensormap(&p.tk);
+      prefetch_tensormap(&p.tv);
+    }
   }
   wait_for_previous_kernel();
-  plan<D, NT>(p, bars);
+  plan<D, NT, FP4>(p, bars);
   if (bars->start_left == 0) return;  // fewer tiles than CTAs
   if (warp == C::kMmaWarp) {
     tmem_alloc(&bars->tmem_base, 512);
@@ -330,8 +375,72 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
   cur.start(p, bars);
   Seg seg{};
 
-  if (warp >= C::kMmaWarp) {
-    if constexpr (NT == 2) regs_dec<kControlRegs>();
+  if (FP4 && warp >= C::kConvertWarp) {
+    // ================================================================ conversion of 4 bits
+    // A thread takes whole rows (two threads a row where there are 8 warps), 16 bytes
+    // of codes at a time: 32 elements, 4 pieces of 16 bytes of the tile.  At d = 128
+    // lanes of one eighth of a warp take their row's pieces in different orders, so
+    // that neither reads (rows 64 bytes apart) nor writes meet in a bank.
+    if constexpr (FP4) {
+      regs_dec<C::kConvertRegs>();
+      constexpr int kPieces = D / 32, kTeams = C::kConvertWarps / 4, kMine = kPieces / kTeams;
+      const int row = threadIdx.x % kBN, team = (warp - C::kConvertWarp) / 4;
+      int items = 0, tiles = 0;
+      bool ok = true;
+      while (ok && cur.next(p, seg)) {
+        const int n = seg.j1 - seg.j0;
+        for (int i = 0; i < 2 * n; ++i, ++items) {
+          const int rs = items % C::kRawStages, st = items % C::kStages;
+          // K_0, K_1, V_0, K_2, ..
+          const int j = i == 0 ? 0 : i == 2 * n - 1 ? n - 1 : (i & 1) ? (i + 1) / 2 : i / 2 - 1;
+          ok = bounded_wait(&bars->raw[rs], (items / C::kRawStages) & 1, abort_flag, p.status, kStatusTimeoutLoad);
+          if (ok && items >= C::kStages)
+            ok = bounded_wait(&bars->kv_empty[st], (items / C::kStages - 1) & 1, abort_flag, p.status,
+                              kStatusTimeoutLoad);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint8_t* src = smem + C::kRawOff + rs * C::kRawBytes;
+          // Rows that are not there are zeros.
+          const bool there = (seg.j0 + j) * kBN + row < seg.s.n &&
+                             !(bars->bad[(tiles + j) % kTileRing] >> (row / 16) & 1u);
+          uint32_t f[D / 64];
+          if constexpr (D == 128) {
+            const uint2 v = *reinterpret_cast<const uint2*>(src + kBN * (D / 2) + row * (D / 16));
+            f[0] = there ? v.x : 0u, f[1] = there ? v.y : 0u;
+          } else {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(src + kBN * (D / 2) + row * (D / 16));
+            f[0] = there ? v : 0u;
+          }
+          uint8_t* dst = sRing + st * C::kTileBytes + row * 128;
+#pragma unroll
+          for (int q = 0; q < kMine; ++q) {
+            const int piece = D == 128 ? ((row >> 1) + q * kTeams + team) % kPieces : q * kTeams + team;
+            const uint4 c = *reinterpret_cast<const uint4*>(src + row * (D / 2) + piece * 16);
+            const uint32_t fw = D == 128 && piece >= 2 ? f[D / 64 - 1] : f[0];
+            const uint32_t two = e4m3x2_to_f16(piece & 1 ? fw >> 16 : fw);
+            const uint32_t f0 = __byte_perm(two, two, 0x1010), f1 = __byte_perm(two, two, 0x3232);
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t h[4];
+              e2m1x8_to_f16(w[k], k < 2 ? f0 : f1, h);
+              const int chunk = (piece & 1) * 4 + k;
+              *reinterpret_cast<uint4*>(dst + (piece >> 1) * C::kBlockBytes + ((chunk ^ (row & 7)) << 4)) =
+                  make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars->raw_empty[rs]);
+            mbar_arrive(&bars->kv_full[st]);
+          }
+        }
+        tiles += n;
+      }
+    }
+  } else if (warp >= C::kMmaWarp) {
+    if constexpr (C::kSplit) regs_dec<C::kControlRegs>();
     if (warp == C::kLoadWarp) {
       // ================================================================ loader
       // Lane = (box, column block) of a key tile: its page's rows.
@@ -339,6 +448,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
       const int box = lane % boxes, cb = lane / boxes;
       const bool loads = cb < C::kColBlocks;
       const int box_shift = 31 - __clz(p.box_rows);
+      constexpr int kStages = FP4 ? C::kRawStages : C::kStages;
+      uint64_t* const empty = FP4 ? bars->raw_empty : bars->kv_empty;
       const uint64_t keep = policy_evict_last(), once = policy_evict_first();
       const int missing = p.n_pages * p.Hkv;  // a coordinate outside: zeros
       int items = 0, segs = 0, tiles = 0;
@@ -369,10 +480,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
         if (!ok) break;
         ++segs;
         auto issue = [&](bool is_v, int j, int page) {
-          const int st = items % C::kStages;
-          if (lane == 0 && items >= C::kStages)
-            ok = bounded_wait(&bars->kv_empty[st], (items / C::kStages - 1) & 1, abort_flag, p.status,
-                              kStatusTimeoutLoad);
+          const int st = items % kStages;
+          if (lane == 0 && items >= kStages)
+            ok = bounded_wait(&empty[st], (items / kStages - 1) & 1, abort_flag, p.status, kStatusTimeoutLoad);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) return;
           const int key = j * kBN + (box << box_shift);
@@ -389,6 +499,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
             }
             if (lane == 0) bars->bad[tiles % kTileRing] = static_cast<uint8_t>(bad);
             ++tiles;
+          }
+          if constexpr (FP4) {
+            // Pages that are there: lanes of the first half copy codes, the others
+            // factors (a page's rows of one head lie one behind another).
+            const uint32_t copied = __ballot_sync(0xffffffffu, cb == 0 && found);
+            if (lane == 0)
+              mbar_arrive_expect_tx(&bars->raw[st], (__popc(copied) << box_shift) * (D / 2 + D / 16));
+            __syncwarp();
+            if (found && cb < 2) {
+              const long long at = ((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) +
+                                   (key & ((1 << p.page_shift) - 1));
+              const int row_bytes = cb == 0 ? D / 2 : D / 16;
+              bulk_load(smem + C::kRawOff + st * C::kRawBytes + (cb == 0 ? 0 : kBN * (D / 2)) +
+                            (box << box_shift) * row_bytes,
+                        (cb == 0 ? p.codes[is_v] : p.factors[is_v]) + at * row_bytes,
+                        static_cast<uint32_t>(row_bytes << box_shift), &bars->raw[st], keep);
+            }
+            ++items;
+            return;
           }
           const bool guarded = is_v && j >= jm;
           uint64_t* bar = guarded ? &bars->raw[st] : &bars->kv_full[st];
@@ -417,11 +546,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
         int dummy = 0;
         volatile int* ignore = reinterpret_cast<volatile int*>(&dummy);
         if (segs > 0) bounded_wait(&bars->q_full, (segs - 1) & 1, ignore, p.status, kStatusTimeoutDrain);
-        for (int it = max(0, items - C::kStages); it < items; ++it)
-          bounded_wait(&bars->kv_full[it % C::kStages], (it / C::kStages) & 1, ignore, p.status, kStatusTimeoutDrain);
+        uint64_t* const full = FP4 ? bars->raw : bars->kv_full;
+        for (int it = max(0, items - kStages); it < items; ++it)
+          bounded_wait(&full[it % kStages], (it / kStages) & 1, ignore, p.status, kStatusTimeoutDrain);
       }
       __syncwarp();
-    } else if (warp == C::kGuardWarp) {
+    } else if (!FP4 && warp == C::kGuardWarp) {
       // ================================================================ guard of V
       constexpr int kCols = D / 32;  // of a lane, in one 16-byte piece
       const int cbyte = lane * kCols * 2;
@@ -488,8 +618,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
       // its rows do not visit are released once landed.
       if (lane == 0) {
         const int x = warp - C::kMmaWarp;
-        constexpr uint32_t kIdescQK = idesc_f16(BF16, false, false, kBM, kBN);
-        constexpr uint32_t kIdescPV = idesc_f16(BF16, false, true, kBM, D);
+        constexpr uint32_t kIdescQK = idesc_f16(kMmaBf16, false, false, kBM, kBN);
+        constexpr uint32_t kIdescPV = idesc_f16(kMmaBf16, false, true, kBM, D);
         const uint32_t ring_addr = smem_u32(sRing);
         const uint32_t s_col = tmem + x * kBN;
         const uint32_t o_col = tmem + 2 * kBN + x * D;
@@ -538,7 +668,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
         while (ok && cur.next(p, seg)) {
           const TileRows tile(p, seg, x, NT);
           const int n = seg.j1 - seg.j0, nx = tile.j1 - seg.j0;
-          ok = bounded_wait(&bars->q_full, segs & 1, abort_flag, p.status, kStatusTimeoutMma);
+          ok = bounded_wait(kConvertQ ? &bars->q_ready[x] : &bars->q_full, segs & 1, abort_flag, p.status,
+                            kStatusTimeoutMma);
           // Tile L starts when tile H has read its first S: the two softmax chains
           // then run staggered.
           if (NT == 2 && ok && x == 1 && segs == 0 && nx > 0) {
@@ -586,7 +717,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
     }
   } else {
     // ================================================================ softmax
-    if constexpr (NT == 2) regs_inc<kSoftmaxRegs>();
+    if constexpr (C::kSplit) regs_inc<C::kSoftmaxRegs>();
     const int x = warp / 4;
     const int wq = warp % 4;
     const int row = wq * 32 + lane;
@@ -596,7 +727,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
     const uint32_t o_tmem = tmem + lane_off + 2 * kBN + x * D;
     const uint32_t p_tmem = tmem + lane_off + 2 * kBN + 2 * D + x * (kBN / 2);
     uint8_t* p_row = sP + x * C::kStageBytes + row * 128;
-    const float lam = p.scale_log2;
+    float lam = p.scale_log2;  // of this row
+    float vd = 1.f;
     int done = 0, segs_x = 0, segs = 0, tiles = 0;
     bool staged = false;  // an output's store may still read the staging buffer
     bool ok = true;
@@ -621,6 +753,45 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
       const bool in_tile = row_token < p.tq_tokens && head < p.g;
       const bool real = in_tile && t < seg.s.rows && seg.s.p0 + t >= 0;
       const int lim = real ? limit(p, seg.s, t) : -1;
+      if constexpr (FP4) {
+        const int kvh = seg.u / p.nblk;
+        lam = p.scale_log2 * (p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f);
+        vd = p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
+      }
+      if constexpr (kConvertQ) {
+        // The row of Q, in place, to fp16 behind a power of two that brings its
+        // largest element to [1, 2): exact but for elements below 2^-14 of that one.
+        ok = bounded_wait(&bars->q_full, segs & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        uint8_t* q_row = sQ + x * C::kTileBytes + row * 128;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(q_row + (i / 8) * C::kBlockBytes + ((i ^ row) & 7) * 16);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7F80u, w[k] >> 16 & 0x7F80u));
+        }
+        const uint32_t e = min(max(top >> 7, 1u), 253u);
+        const float down = __uint_as_float((254u - e) << 23);
+        lam *= __uint_as_float(e << 23);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint4* at = reinterpret_cast<uint4*>(q_row + (i / 8) * C::kBlockBytes + ((i ^ row) & 7) * 16);
+          const uint4 v = *at;
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            h[k] = pack2<false>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+          *at = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->q_ready[x]);
+      }
       float r = -INFINITY;  // retained reference, raw score units
       float l = 0.f;
       const int nx = tile.j1 - seg.j0;
@@ -698,7 +869,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
               const int c = blk * 64 + c8 * 8 + 2 * i;
               const float2 e = ex2_pair(ffma2(make_float2(s[c], s[c + 1]), lam2, nrs2), (blk * 8 + c8) * 4 + i);
               sum4[i] = fadd2(sum4[i], e);
-              pk[c8 * 4 + i] = pack2<BF16>(e.x, e.y);
+              pk[c8 * 4 + i] = pack2<kMmaBf16>(e.x, e.y);
             }
           }
           if (blk == 0) {
@@ -760,13 +931,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
       }
       // Columns whose guarded rows of V are not finite for this row.
       int lim0;
-      const bool guarded = tile.j1 > max(seg.j0, first_masked<NT>(p, seg, lim0));
+      const bool guarded = !FP4 && tile.j1 > max(seg.j0, first_masked<NT>(p, seg, lim0));
       const bool nan_any = guarded && bars->nan_any[segs % kSegRing] != 0;
       const uint8_t* nan_from = bars->nan_from[segs % kSegRing];
       const int seen = real ? lim - lim0 : 0;
       if (seg.whole()) {
         if (tile.t0 < p.S) {
-          const float inv = (!real || l == 0.f) ? 0.f : 1.f / l;
+          const float inv = (!real || l == 0.f) ? 0.f : vd / l;
           stage_free();
           if (!ok) break;
 #pragma unroll 1
@@ -777,7 +948,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
               tmem_wait_ld();
               reg_fence32(u);
             }
-            if (nx == 0 || inv == 0.f) {
+            if (nx == 0 || !real || l == 0.f) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) u[i] = 0u;
             }
@@ -836,8 +1007,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) prefill_paged_kernel(
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 dst[(c * 8 + i) * (NT * kBM)] =
-                    make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
-                                __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3]));
+                    make_float4(__uint_as_float(u[4 * i]) * vd, __uint_as_float(u[4 * i + 1]) * vd,
+                                __uint_as_float(u[4 * i + 2]) * vd, __uint_as_float(u[4 * i + 3]) * vd);
             }
           }
           tc_fence_before();
@@ -954,18 +1125,26 @@ int max_ctas(const Shape& s, int max_len) {
   return s.units >= kMaxCtas || s.units * per_unit >= kMaxCtas ? kMaxCtas : static_cast<int>(s.units * per_unit);
 }
 
-template <int D, bool BF16, int NT>
+template <int D, bool BF16, int NT, bool FP4>
 int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D, NT, FP4>;
+  static_assert(C::kSmemBytes <= 232448, "shared memory of a CTA");
   const CacheArgs& c = a.cache;
   const int page = 1 << c.page_shift;
   p.box_rows = page < kBN ? page : kBN;
   if (!make_tmap_heads(&p.tq, a.q, BF16, D, p.g, p.Hkv, a.S, a.B, s.hb, s.tokens) ||
-      !make_tmap_heads(&p.to, a.o, BF16, D, p.g, p.Hkv, a.S, a.B, s.hb, s.tokens) ||
-      !make_tmap_3d(&p.tk, c.data[0], BF16, D, page, static_cast<long long>(c.n_pages) * c.Hkv, p.box_rows) ||
+      !make_tmap_heads(&p.to, a.o, BF16, D, p.g, p.Hkv, a.S, a.B, s.hb, s.tokens))
+    return -1;
+  if (FP4) {
+    for (int i = 0; i < 2; ++i) {
+      p.codes[i] = static_cast<const uint8_t*>(c.data[i]);
+      p.factors[i] = static_cast<const uint8_t*>(c.scale[i]);
+      p.descale[i] = c.descale[i];
+    }
+  } else if (!make_tmap_3d(&p.tk, c.data[0], BF16, D, page, static_cast<long long>(c.n_pages) * c.Hkv, p.box_rows) ||
       !make_tmap_3d(&p.tv, c.data[1], BF16, D, page, static_cast<long long>(c.n_pages) * c.Hkv, p.box_rows))
     return -1;
-  auto kern = prefill_paged_kernel<D, BF16, NT>;
+  auto kern = prefill_paged_kernel<D, BF16, NT, FP4>;
   static std::atomic<unsigned long long> attr_done{0};  // per instantiation
   if (!set_smem_limit_once(kern, C::kSmemBytes, attr_done)) return -1;
   if (launch_after(kern, dim3(static_cast<unsigned>(p.ctas)), C::kThreads, a.stream, p, C::kSmemBytes) != 0) return -1;
@@ -977,7 +1156,8 @@ int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
 
 template <int D, bool BF16>
 int launch_nt(Params& p, const PagedPrefillArgs& a, const Shape& s) {
-  return s.nt == 1 ? launch_t<D, BF16, 1>(p, a, s) : launch_t<D, BF16, 2>(p, a, s);
+  if (a.cache.fp4()) return s.nt == 1 ? launch_t<D, BF16, 1, true>(p, a, s) : launch_t<D, BF16, 2, true>(p, a, s);
+  return s.nt == 1 ? launch_t<D, BF16, 1, false>(p, a, s) : launch_t<D, BF16, 2, false>(p, a, s);
 }
 
 }  // namespace

@@ -155,6 +155,15 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, seqlens, new_lens=None, scal
                                                workspace, out, lse, return_lse, stream)
 
 
+def attn_fwd_paged_fp4(q, k_codes, k_factors, v_codes, v_factors, page_table, seqlens, new_lens=None, k_descale=None,
+                       v_descale=None, scale: float | None = None, causal: bool = True, workspace=None, out=None,
+                       lse=None, return_lse: bool = True, stream=None):
+    """attn_fwd_paged over a 4-bit paged cache (C ABI `attn_fwd_paged_fp4`)."""
+    return (_native or _load()).attn_fwd_paged_fp4(q, k_codes, k_factors, v_codes, v_factors, page_table, seqlens,
+                                                   new_lens, k_descale, v_descale, scale, causal, workspace, out, lse,
+                                                   return_lse, stream)
+
+
 def attn_decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, d: int, max_len: int = 2 ** 31 - 1) -> int:
     """Bytes of the paged decodes' workspace; smaller where max_len, the tokens
     that max_pages pages hold, is short."""

@@ -52,11 +52,12 @@ CHUNKS = [
 ]
 
 
+@pytest.mark.parametrize("bits", [16, 4])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("cfg", CHUNKS)
-def test_chunk(cfg, causal):
+def test_chunk(cfg, causal, bits):
     dtype, H, Hkv, d, page, S, lens, news = cfg
-    pool, table, g = _make(16, dtype, Hkv, d, page, lens, 31)
+    pool, table, g = _make(bits, dtype, Hkv, d, page, lens, 31)
     q = torch.randn(len(lens), H, S, d, generator=g).to(dtype).cuda()
     scale = 1 / math.sqrt(d)
     o, lse = _forward(pool, q, table, lens, news, causal=causal)
