@@ -44,6 +44,7 @@ from .paged import (  # noqa: F401
     attn_qk_norm_rope,
     attn_qk_norm_rope_bwd,
     attn_qk_norm_rope_bwd_workspace_bytes,
+    rope_pair_axes,
     rope_table,
 )
 

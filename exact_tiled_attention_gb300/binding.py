@@ -39,7 +39,9 @@ EXPORTS = ("attn_fwd", "attn_fwd_pair", "attn_decode_workspace_bytes", "attn_dec
            "attn_qk_norm_rope", "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_bwd",
            "attn_cache_append", "attn_cache_append_fp4", "attn_cache_gather", "attn_cache_gather_fp4",
            "attn_decode_paged_workspace_bytes", "attn_decode_paged", "attn_decode_paged_fp4",
-           "attn_fwd_paged_workspace_bytes", "attn_fwd_paged", "attn_fwd_paged_fp4")
+           "attn_fwd_paged_workspace_bytes", "attn_fwd_paged", "attn_fwd_paged_fp4",
+           "attn_qk_norm_rope_axes", "attn_qk_norm_rope_axes_bwd", "attn_cache_append_axes",
+           "attn_cache_append_axes_fp4")
 
 _lock = threading.Lock()
 _lib = None
@@ -111,6 +113,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.attn_decode_paged.restype = ci
         lib.attn_decode_paged_fp4.argtypes = [vp] * 11 + [ci] * 7 + [cf, vp, sz, ci, vp]
         lib.attn_decode_paged_fp4.restype = ci
+        lib.attn_qk_norm_rope_axes.argtypes = [vp] * 9 + [ci] * 6 + [vp, vp, cf] + [ci] * 4 + [vp]
+        lib.attn_qk_norm_rope_axes.restype = ci
+        lib.attn_qk_norm_rope_axes_bwd.argtypes = [vp] * 13 + [ci] * 6 + [vp] * 4 + [cf] + [ci] * 3 + [vp, sz, ci, vp]
+        lib.attn_qk_norm_rope_axes_bwd.restype = ci
+        lib.attn_cache_append_axes.argtypes = [vp] * 12 + [ci] * 9 + [vp] * 3 + [ci] * 4 + [vp]
+        lib.attn_cache_append_axes.restype = ci
+        lib.attn_cache_append_axes_fp4.argtypes = [vp] * 16 + [ci] * 9 + [vp] * 3 + [ci] * 4 + [vp]
+        lib.attn_cache_append_axes_fp4.restype = ci
         lib.attn_fwd_paged_workspace_bytes.argtypes = [ci] * 6
         lib.attn_fwd_paged_workspace_bytes.restype = sz
         lib.attn_fwd_paged.argtypes = [vp] * 8 + [ci] * 8 + [cf, ci, vp, sz, ci, vp]

@@ -24,6 +24,8 @@
 // rotations take 33 and 31.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "gbattn_rows.cuh"
 
 namespace gbattn {
@@ -41,8 +43,11 @@ struct AppendParams {
   const int* page_table;
   const int* seqlens;
   const int* new_lens;
+  const int* positions;  // [n_axes, B, S], or null: the slots'
   const float* table;
   int table_rows, rot;
+  int n_axes;
+  uint32_t pair_axes[4];
   int B, S, heads[3], chunks[3], per_chunk;
   int page_shift, n_pages, max_pages;
   int* status;
@@ -100,7 +105,7 @@ __device__ __forceinline__ uint32_t quantise8(const float (&z)[8], float descale
 template <int MODE, bool FP4>
 constexpr int kResident = MODE == kRopePart ? 1 : FP4 ? 7 : 8;
 
-template <int D, bool BF16, int MODE, bool FP4>
+template <int D, bool BF16, int MODE, bool FP4, bool AXES>
 __global__ void __launch_bounds__(kThreads, kResident<MODE, FP4>) cache_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = RowCfg<D>::kLanes;
   constexpr int kRowsCta = kThreads / kLanes;
@@ -158,12 +163,18 @@ __global__ void __launch_bounds__(kThreads, kResident<MODE, FP4>) cache_append_k
   int pc[2] = {e0, D / 2 + e0};
   if constexpr (MODE != kRopeNone) {
     if (which != 2) {
-      long long row = real ? pos : 0;
-      if (row >= p.table_rows) {
-        report_index(p.status);
-        row = p.table_rows - 1;
+      if constexpr (AXES) {  // (padding has no position)
+        const LaneAxes<D, MODE> axes(p.pair_axes, p.rot, lane_in_row);
+        const AxisRows rows(p.positions + t, tokens, real ? p.n_axes : 0, p.table, p.table_rows, p.rot, p.status);
+        load_rope_axes<D, MODE>(rope, axes, rows, p.rot, lane_in_row);
+      } else {
+        long long row = real ? pos : 0;
+        if (row >= p.table_rows) {
+          report_index(p.status);
+          row = p.table_rows - 1;
+        }
+        load_rope<D, MODE>(rope, p.table + row * p.rot, p.rot, lane_in_row);
       }
-      load_rope<D, MODE>(rope, p.table + row * p.rot, p.rot, lane_in_row);
       if constexpr (MODE == kRopePart)
         for (int c = 0; c < 2; ++c) pc[c] = partner_chunk(c * (D / 2) + e0, p.rot);
     }
@@ -322,6 +333,9 @@ int launch_append_t(const AppendArgs& a) {
   p.table = a.rope.table;
   p.table_rows = a.rope.rows;
   p.rot = a.rope.rot_dim;
+  p.positions = a.positions;
+  p.n_axes = a.rope.n_axes;
+  for (int i = 0; i < 4; ++i) p.pair_axes[i] = a.rope.pair_axes[i];
   p.B = a.B;
   p.S = a.S;
   p.page_shift = a.cache.page_shift;
@@ -341,11 +355,17 @@ int launch_append_t(const AppendArgs& a) {
   for (int i = 0; i < 3; ++i) chunks += p.chunks[i] = (p.heads[i] + per - 1) / per;
   if (token_ctas > 0x7FFFFFFFLL || chunks > 65535) return -1;
   const dim3 grid(static_cast<unsigned>(token_ctas), chunks);
+  const bool axes = a.rope.n_axes > 0;
+  auto launch = [&](auto mode) {
+    constexpr int kMode = decltype(mode)::value;
+    return axes ? launch_after(cache_append_kernel<D, BF16, kMode, FP4, true>, grid, kThreads, a.stream, p)
+                : launch_after(cache_append_kernel<D, BF16, kMode, FP4, false>, grid, kThreads, a.stream, p);
+  };
   switch (rope_mode(a.rope, D)) {
-    case kRopeNone: return launch_after(cache_append_kernel<D, BF16, kRopeNone, FP4>, grid, kThreads, a.stream, p);
-    case kRopePairs: return launch_after(cache_append_kernel<D, BF16, kRopePairs, FP4>, grid, kThreads, a.stream, p);
-    case kRopeHalves: return launch_after(cache_append_kernel<D, BF16, kRopeHalves, FP4>, grid, kThreads, a.stream, p);
-    default: return launch_after(cache_append_kernel<D, BF16, kRopePart, FP4>, grid, kThreads, a.stream, p);
+    case kRopeNone: return launch_after(cache_append_kernel<D, BF16, kRopeNone, FP4, false>, grid, kThreads, a.stream, p);
+    case kRopePairs: return launch(std::integral_constant<int, kRopePairs>());
+    case kRopeHalves: return launch(std::integral_constant<int, kRopeHalves>());
+    default: return launch(std::integral_constant<int, kRopePart>());
   }
 }
 

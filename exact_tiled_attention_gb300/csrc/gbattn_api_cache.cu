@@ -36,9 +36,30 @@ int check_rope(RopeArgs* out, const float* rope, int rows, int rot_dim, int inte
     if (!rope || misaligned16(rope)) return GBATTN_EPOINTER;
     if (rows < 1) return GBATTN_EBADSHAPE;
   }
-  *out = {rope, rows, rot_dim, interleaved ? 1 : 0};
+  *out = RopeArgs{rope, rows, rot_dim, interleaved ? 1 : 0, 0, {0, 0, 0, 0}};
   return GBATTN_OK;
 }
+
+// Positions of several axes (after check_rope): the pairs' axes, packed.
+int check_axes(RopeArgs* out, const int* positions, const unsigned char* pair_axes, int n_axes) {
+  if (n_axes < 1 || n_axes > 4) return GBATTN_EBADSHAPE;
+  if (out->rot_dim == 0 || !positions || !pair_axes || misaligned4(positions)) return GBATTN_EPOINTER;
+  out->n_axes = n_axes;
+  for (int i = 0; i < out->rot_dim / 2; ++i) {
+    if (pair_axes[i] >= n_axes) return GBATTN_EBADSHAPE;
+    out->pair_axes[i / 16] |= static_cast<uint32_t>(pair_axes[i]) << (2 * (i % 16));
+  }
+  return GBATTN_OK;
+}
+
+// No positions of several axes.
+struct Axes {
+  bool given;
+  const int* positions;
+  const unsigned char* pair_axes;
+  int n;
+};
+constexpr Axes kOnePosition = {false, nullptr, nullptr, 0};
 
 // Sizes and pointers of a paged cache; factors are given for a 4-bit one only.
 int check_cache(CacheArgs* out, const void* k, const void* v, const void* k_factors, const void* v_factors, bool fp4,
@@ -106,11 +127,69 @@ int check_norm_rope(NormRopeArgs* a, const void* q, const void* k, const float* 
   return GBATTN_OK;
 }
 
+int norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight, const float* rope,
+              const int* positions, void* q_out, void* k_out, int B, int H, int Hkv, int S, int d,
+              const long long* q_strides, const long long* k_strides, float eps, int rope_rows, int rot_dim,
+              int interleaved, int dtype, void* stream, const Axes& axes) {
+  NormRopeArgs a{};
+  int rc = check_norm_rope(&a, q, k, q_weight, k_weight, rope, positions, B, H, Hkv, S, d, q_strides, k_strides, eps,
+                           rope_rows, rot_dim, interleaved, dtype, stream);
+  if (rc != GBATTN_OK) return rc;
+  if (axes.given) {
+    rc = check_axes(&a.rope, positions, axes.pair_axes, axes.n);
+    if (rc != GBATTN_OK) return rc;
+  }
+  if (!q_out || !k_out || misaligned16(q_out) || misaligned16(k_out)) return GBATTN_EPOINTER;
+  rc = current_device(&a.status, &a.num_sms);
+  if (rc != GBATTN_OK) return rc;
+  a.y[0] = q_out;
+  a.y[1] = k_out;
+  return launch_norm_rope(a) == 0 ? GBATTN_OK : GBATTN_ELAUNCH;
+}
+
+int norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, const float* q_weight,
+                  const float* k_weight, const float* rope, const int* positions, void* dq, void* dk,
+                  float* dq_weight, float* dk_weight, int B, int H, int Hkv, int S, int d, const long long* q_strides,
+                  const long long* k_strides, const long long* dq_strides, const long long* dk_strides, float eps,
+                  int rope_rows, int rot_dim, int interleaved, void* workspace, size_t workspace_bytes, int dtype,
+                  void* stream, const Axes& axes) {
+  NormRopeArgs a{};
+  int rc = check_norm_rope(&a, q, k, q_weight, k_weight, rope, positions, B, H, Hkv, S, d, q_strides, k_strides, eps,
+                           rope_rows, rot_dim, interleaved, dtype, stream);
+  if (rc != GBATTN_OK) return rc;
+  if (axes.given) {
+    rc = check_axes(&a.rope, positions, axes.pair_axes, axes.n);
+    if (rc != GBATTN_OK) return rc;
+  }
+  if (!dq_out || !dk_out || !dq || !dk || misaligned16(dq_out) || misaligned16(dk_out) || misaligned16(dq) ||
+      misaligned16(dk))
+    return GBATTN_EPOINTER;
+  if (!row_strides(&a.dxs[0], dq_strides, H, S, d) || !row_strides(&a.dxs[1], dk_strides, Hkv, S, d))
+    return GBATTN_EPOINTER;
+  if (q_weight) {
+    if (!dq_weight || !dk_weight || !workspace || misaligned4(dq_weight) || misaligned4(dk_weight) ||
+        misaligned16(workspace))
+      return GBATTN_EPOINTER;
+    if (workspace_bytes < norm_rope_bwd_workspace_bytes(d)) return GBATTN_EWORKSPACE;
+  }
+  rc = current_device(&a.status, &a.num_sms);
+  if (rc != GBATTN_OK) return rc;
+  a.dy[0] = dq_out;
+  a.dy[1] = dk_out;
+  a.dx[0] = dq;
+  a.dx[1] = dk;
+  a.dw[0] = dq_weight;
+  a.dw[1] = dk_weight;
+  a.workspace = static_cast<float*>(workspace);
+  return launch_norm_rope_bwd(a) == 0 ? GBATTN_OK : GBATTN_ELAUNCH;
+}
+
 int append(const void* k, const void* v, void* k_cache, void* k_factors, void* v_cache, void* v_factors, bool fp4,
            const float* k_descale, const float* v_descale, const int* page_table, const int* seqlens,
            const int* new_lens, const float* rope, const void* q, void* q_out, int B, int H, int Hkv, int S, int d,
            int page_size, int n_pages, int max_pages, const long long* q_strides, const long long* k_strides,
-           const long long* v_strides, int rope_rows, int rot_dim, int interleaved, int dtype, void* stream) {
+           const long long* v_strides, int rope_rows, int rot_dim, int interleaved, int dtype, void* stream,
+           const Axes& axes) {
   if (B < 1 || H < 1 || Hkv < 1 || S < 1 || H > 16384 || Hkv > 16384) return GBATTN_EBADSHAPE;
   if (too_many_tokens(B, S)) return GBATTN_EBADSHAPE;
   if (H % Hkv != 0) return GBATTN_EHEADS;
@@ -121,6 +200,11 @@ int append(const void* k, const void* v, void* k_cache, void* k_factors, void* v
   if (dtype != GBATTN_F16 && dtype != GBATTN_BF16) return GBATTN_EDTYPE;
   rc = check_rope(&a.rope, rope, rope_rows, rot_dim, interleaved, d);
   if (rc != GBATTN_OK) return rc;
+  if (axes.given) {
+    rc = check_axes(&a.rope, axes.positions, axes.pair_axes, axes.n);
+    if (rc != GBATTN_OK) return rc;
+    a.positions = axes.positions;
+  }
   if (!k || !v || misaligned16(k) || misaligned16(v) || misaligned16(q) || misaligned16(q_out) || !q != !q_out ||
       misaligned4(new_lens))
     return GBATTN_EPOINTER;
@@ -236,16 +320,17 @@ int attn_qk_norm_rope(const void* q, const void* k, const float* q_weight, const
                       const int* positions, void* q_out, void* k_out, int B, int H, int Hkv, int S, int d,
                       const long long* q_strides, const long long* k_strides, float eps, int rope_rows, int rot_dim,
                       int interleaved, int dtype, void* stream) {
-  NormRopeArgs a{};
-  int rc = check_norm_rope(&a, q, k, q_weight, k_weight, rope, positions, B, H, Hkv, S, d, q_strides, k_strides, eps,
-                           rope_rows, rot_dim, interleaved, dtype, stream);
-  if (rc != GBATTN_OK) return rc;
-  if (!q_out || !k_out || misaligned16(q_out) || misaligned16(k_out)) return GBATTN_EPOINTER;
-  rc = current_device(&a.status, &a.num_sms);
-  if (rc != GBATTN_OK) return rc;
-  a.y[0] = q_out;
-  a.y[1] = k_out;
-  return launch_norm_rope(a) == 0 ? GBATTN_OK : GBATTN_ELAUNCH;
+  return norm_rope(q, k, q_weight, k_weight, rope, positions, q_out, k_out, B, H, Hkv, S, d, q_strides, k_strides, eps,
+                   rope_rows, rot_dim, interleaved, dtype, stream, kOnePosition);
+}
+
+int attn_qk_norm_rope_axes(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                           const float* rope, const int* positions, const unsigned char* pair_axes, void* q_out,
+                           void* k_out, int B, int H, int Hkv, int S, int d, int n_axes, const long long* q_strides,
+                           const long long* k_strides, float eps, int rope_rows, int rot_dim, int interleaved,
+                           int dtype, void* stream) {
+  return norm_rope(q, k, q_weight, k_weight, rope, positions, q_out, k_out, B, H, Hkv, S, d, q_strides, k_strides, eps,
+                   rope_rows, rot_dim, interleaved, dtype, stream, {true, positions, pair_axes, n_axes});
 }
 
 size_t attn_qk_norm_rope_bwd_workspace_bytes(int d) {
@@ -258,31 +343,21 @@ int attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
                           const long long* q_strides, const long long* k_strides, const long long* dq_strides,
                           const long long* dk_strides, float eps, int rope_rows, int rot_dim, int interleaved,
                           void* workspace, size_t workspace_bytes, int dtype, void* stream) {
-  NormRopeArgs a{};
-  int rc = check_norm_rope(&a, q, k, q_weight, k_weight, rope, positions, B, H, Hkv, S, d, q_strides, k_strides, eps,
-                           rope_rows, rot_dim, interleaved, dtype, stream);
-  if (rc != GBATTN_OK) return rc;
-  if (!dq_out || !dk_out || !dq || !dk || misaligned16(dq_out) || misaligned16(dk_out) || misaligned16(dq) ||
-      misaligned16(dk))
-    return GBATTN_EPOINTER;
-  if (!row_strides(&a.dxs[0], dq_strides, H, S, d) || !row_strides(&a.dxs[1], dk_strides, Hkv, S, d))
-    return GBATTN_EPOINTER;
-  if (q_weight) {
-    if (!dq_weight || !dk_weight || !workspace || misaligned4(dq_weight) || misaligned4(dk_weight) ||
-        misaligned16(workspace))
-      return GBATTN_EPOINTER;
-    if (workspace_bytes < norm_rope_bwd_workspace_bytes(d)) return GBATTN_EWORKSPACE;
-  }
-  rc = current_device(&a.status, &a.num_sms);
-  if (rc != GBATTN_OK) return rc;
-  a.dy[0] = dq_out;
-  a.dy[1] = dk_out;
-  a.dx[0] = dq;
-  a.dx[1] = dk;
-  a.dw[0] = dq_weight;
-  a.dw[1] = dk_weight;
-  a.workspace = static_cast<float*>(workspace);
-  return launch_norm_rope_bwd(a) == 0 ? GBATTN_OK : GBATTN_ELAUNCH;
+  return norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rope, positions, dq, dk, dq_weight, dk_weight, B, H,
+                       Hkv, S, d, q_strides, k_strides, dq_strides, dk_strides, eps, rope_rows, rot_dim, interleaved,
+                       workspace, workspace_bytes, dtype, stream, kOnePosition);
+}
+
+int attn_qk_norm_rope_axes_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                               const float* q_weight, const float* k_weight, const float* rope, const int* positions,
+                               const unsigned char* pair_axes, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                               int B, int H, int Hkv, int S, int d, int n_axes, const long long* q_strides,
+                               const long long* k_strides, const long long* dq_strides, const long long* dk_strides,
+                               float eps, int rope_rows, int rot_dim, int interleaved, void* workspace,
+                               size_t workspace_bytes, int dtype, void* stream) {
+  return norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rope, positions, dq, dk, dq_weight, dk_weight, B, H,
+                       Hkv, S, d, q_strides, k_strides, dq_strides, dk_strides, eps, rope_rows, rot_dim, interleaved,
+                       workspace, workspace_bytes, dtype, stream, {true, positions, pair_axes, n_axes});
 }
 
 int attn_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, const int* page_table,
@@ -292,7 +367,18 @@ int attn_cache_append(const void* k, const void* v, void* k_cache, void* v_cache
                       int rope_rows, int rot_dim, int interleaved, int dtype, void* stream) {
   return append(k, v, k_cache, nullptr, v_cache, nullptr, false, nullptr, nullptr, page_table, seqlens, new_lens, rope,
                 q, q_out, B, H, Hkv, S, d, page_size, n_pages, max_pages, q_strides, k_strides, v_strides, rope_rows,
-                rot_dim, interleaved, dtype, stream);
+                rot_dim, interleaved, dtype, stream, kOnePosition);
+}
+
+int attn_cache_append_axes(const void* k, const void* v, void* k_cache, void* v_cache, const int* page_table,
+                           const int* seqlens, const int* new_lens, const float* rope, const int* positions,
+                           const unsigned char* pair_axes, const void* q, void* q_out, int B, int H, int Hkv, int S,
+                           int d, int n_axes, int page_size, int n_pages, int max_pages, const long long* q_strides,
+                           const long long* k_strides, const long long* v_strides, int rope_rows, int rot_dim,
+                           int interleaved, int dtype, void* stream) {
+  return append(k, v, k_cache, nullptr, v_cache, nullptr, false, nullptr, nullptr, page_table, seqlens, new_lens, rope,
+                q, q_out, B, H, Hkv, S, d, page_size, n_pages, max_pages, q_strides, k_strides, v_strides, rope_rows,
+                rot_dim, interleaved, dtype, stream, {true, positions, pair_axes, n_axes});
 }
 
 int attn_cache_append_fp4(const void* k, const void* v, void* k_codes, void* k_factors, void* v_codes,
@@ -303,7 +389,19 @@ int attn_cache_append_fp4(const void* k, const void* v, void* k_codes, void* k_f
                           int rope_rows, int rot_dim, int interleaved, int dtype, void* stream) {
   return append(k, v, k_codes, k_factors, v_codes, v_factors, true, k_descale, v_descale, page_table, seqlens,
                 new_lens, rope, q, q_out, B, H, Hkv, S, d, page_size, n_pages, max_pages, q_strides, k_strides,
-                v_strides, rope_rows, rot_dim, interleaved, dtype, stream);
+                v_strides, rope_rows, rot_dim, interleaved, dtype, stream, kOnePosition);
+}
+
+int attn_cache_append_axes_fp4(const void* k, const void* v, void* k_codes, void* k_factors, void* v_codes,
+                               void* v_factors, const float* k_descale, const float* v_descale, const int* page_table,
+                               const int* seqlens, const int* new_lens, const float* rope, const int* positions,
+                               const unsigned char* pair_axes, const void* q, void* q_out, int B, int H, int Hkv,
+                               int S, int d, int n_axes, int page_size, int n_pages, int max_pages,
+                               const long long* q_strides, const long long* k_strides, const long long* v_strides,
+                               int rope_rows, int rot_dim, int interleaved, int dtype, void* stream) {
+  return append(k, v, k_codes, k_factors, v_codes, v_factors, true, k_descale, v_descale, page_table, seqlens,
+                new_lens, rope, q, q_out, B, H, Hkv, S, d, page_size, n_pages, max_pages, q_strides, k_strides,
+                v_strides, rope_rows, rot_dim, interleaved, dtype, stream, {true, positions, pair_axes, n_axes});
 }
 
 int attn_cache_gather(const void* k_cache, const void* v_cache, const int* page_table, const int* seqlens,

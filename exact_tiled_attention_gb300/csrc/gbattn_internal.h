@@ -108,6 +108,10 @@ struct RopeArgs {
   int rows;
   int rot_dim;
   int interleaved;  // 1: pairs (2 i, 2 i + 1); 0: pairs (i, i + rot_dim / 2)
+  // Positions of several axes: the axis of each pair, two bits each, pair 0 in the
+  // lowest ones.  n_axes = 0: all pairs follow one position.
+  int n_axes;
+  uint32_t pair_axes[4];
 };
 
 // Norm and rotation of queries and keys (qk_norm_rope.cu); with the gradients
@@ -121,7 +125,7 @@ struct NormRopeArgs {
   float* dw[2];             // backward: gradients of w [d]
   RowStrides xs[2], dxs[2];
   int heads[2];
-  const int* positions;     // [B, S] or null: 0 .. S - 1
+  const int* positions;     // [B, S] (n_axes = 0) or null: 0 .. S - 1; [n_axes, B, S]
   RopeArgs rope;
   float eps;
   int B, S, d;
@@ -152,6 +156,7 @@ struct AppendArgs {
   void* q_out;       // [B, H, S, d], contiguous
   CacheArgs cache;
   const int* new_lens;  // [B] or null: S
+  const int* positions; // of the rotation, [n_axes, B, S]; null: the slots' (n_axes = 0)
   RopeArgs rope;
   int B, H, S;
   bool bf16;

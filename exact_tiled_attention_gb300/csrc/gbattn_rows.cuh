@@ -66,42 +66,125 @@ struct LaneRope {
   bool turns[2];  // (a full rotation by halves turns both chunks and does not ask)
 };
 
+// First of the pairs that the chunk at e0 (< rot) takes part in.
+template <int MODE>
+__device__ __forceinline__ int first_pair(int e0, int rot) {
+  return MODE == kRopePairs ? e0 / 2 : e0 < rot / 2 ? e0 : e0 - rot / 2;
+}
+// Pairs of a chunk.
+template <int MODE>
+constexpr int kPairs = MODE == kRopePairs ? 4 : 8;
+
+// Places the cosines and sines of chunk c's pairs at its elements.
+template <int MODE>
+__device__ __forceinline__ void set_chunk(LaneRope& r, int c, const float* cs, const float* ss, bool first_half) {
+  if constexpr (MODE == kRopePairs) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.cos[c][2 * i] = r.cos[c][2 * i + 1] = cs[i];
+      r.sin[c][2 * i] = -ss[i];
+      r.sin[c][2 * i + 1] = ss[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      r.cos[c][i] = cs[i];
+      r.sin[c][i] = MODE == kRopePart && first_half ? -ss[i] : ss[i];
+    }
+  }
+}
+
+// Loads the cosines and sines of chunk c's pairs from one table row.
+template <int MODE>
+__device__ __forceinline__ void load_chunk(LaneRope& r, int c, const float* row, int e0, int rot) {
+  const int i0 = first_pair<MODE>(e0, rot);
+  float cs[8], ss[8];
+  if constexpr (MODE == kRopePairs) {
+    const float4 co = *reinterpret_cast<const float4*>(row + i0);
+    const float4 si = *reinterpret_cast<const float4*>(row + rot / 2 + i0);
+    cs[0] = co.x, cs[1] = co.y, cs[2] = co.z, cs[3] = co.w;
+    ss[0] = si.x, ss[1] = si.y, ss[2] = si.z, ss[3] = si.w;
+  } else {
+    load8(row + i0, cs);
+    load8(row + rot / 2 + i0, ss);
+  }
+  set_chunk<MODE>(r, c, cs, ss, e0 < rot / 2);
+}
+
 // Loads the lane's cosines and sines of a table row.
 template <int D, int MODE>
 __device__ __forceinline__ void load_rope(LaneRope& r, const float* row, int rot, int lane_in_row) {
-  const int half = rot / 2;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int e0 = c * (D / 2) + 8 * lane_in_row;
     r.turns[c] = e0 < rot;
-    if constexpr (MODE == kRopeHalves) {
-      if (c == 0) {
-        load8(row + e0, r.cos[0]);
-        load8(row + half + e0, r.sin[0]);
-      }
-    } else if (MODE != kRopeNone && e0 < rot) {
-      if constexpr (MODE == kRopePairs) {
-        const float4 co = *reinterpret_cast<const float4*>(row + e0 / 2);
-        const float4 si = *reinterpret_cast<const float4*>(row + half + e0 / 2);
-        const float cs[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+    if (MODE == kRopeHalves ? c == 0 : e0 < rot) load_chunk<MODE>(r, c, row, e0, rot);
+  }
+}
+
+// Positions of several axes: the axes of the pairs of a lane's chunks, two bits
+// each; they stay the same for all tokens.
+template <int D, int MODE>
+struct LaneAxes {
+  uint32_t of[2];
+  bool same[2];  // one axis for all of the chunk's pairs
+  __device__ __forceinline__ LaneAxes(const uint32_t* pair_axes, int rot, int lane_in_row) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          r.cos[c][2 * i] = r.cos[c][2 * i + 1] = cs[i];
-          r.sin[c][2 * i] = -ss[i];
-          r.sin[c][2 * i + 1] = ss[i];
-        }
-      } else {
-        const int i0 = e0 < half ? e0 : e0 - half;
-        load8(row + i0, r.cos[c]);
-        load8(row + half + i0, r.sin[c]);
-        if (e0 < half) {
+    for (int c = 0; c < 2; ++c) {
+      const int e0 = c * (D / 2) + 8 * lane_in_row;
+      const int i0 = e0 < rot ? first_pair<MODE>(e0, rot) : 0;
+      constexpr uint32_t kMask = (1u << 2 * kPairs<MODE>) - 1;
+      of[c] = pair_axes[i0 / 16] >> (2 * (i0 % 16)) & kMask;
+      same[c] = of[c] == (of[c] & 3u) * (0x5555u & kMask);
+    }
+  }
+};
+
+// load_rope from the table rows of a token's positions; row_of(a) is that of axis a.
+template <int D, int MODE, typename RowOf>
+__device__ __forceinline__ void load_rope_axes(LaneRope& r, const LaneAxes<D, MODE>& axes, RowOf&& row_of, int rot,
+                                               int lane_in_row) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) r.sin[c][i] = -r.sin[c][i];
-        }
+  for (int c = 0; c < 2; ++c) {
+    const int e0 = c * (D / 2) + 8 * lane_in_row;
+    r.turns[c] = e0 < rot;
+    if (!(MODE == kRopeHalves ? c == 0 : e0 < rot)) continue;
+    if (axes.same[c]) {
+      load_chunk<MODE>(r, c, row_of(axes.of[c] & 3u), e0, rot);
+    } else {
+      const int i0 = first_pair<MODE>(e0, rot);
+      float cs[8], ss[8];
+#pragma unroll
+      for (int i = 0; i < kPairs<MODE>; ++i) {
+        const float* row = row_of(axes.of[c] >> 2 * i & 3u);
+        cs[i] = row[i0 + i];
+        ss[i] = row[rot / 2 + i0 + i];
       }
+      set_chunk<MODE>(r, c, cs, ss, e0 < rot / 2);
     }
   }
 }
+
+// The table rows of a token's positions, [n_axes] of them `step` apart; positions
+// outside the table are clamped into it and reported.
+struct AxisRows {
+  const float* row[4];
+  __device__ __forceinline__ AxisRows(const int* positions, long long step, int n_axes, const float* table, int rows,
+                                      int rot, int* status) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      int pos = a < n_axes ? positions[a * step] : 0;
+      if (pos < 0 || pos >= rows) {
+        report_index(status);
+        pos = min(max(pos, 0), rows - 1);
+      }
+      row[a] = table + static_cast<long long>(pos) * rot;
+    }
+  }
+  __device__ __forceinline__ const float* operator()(uint32_t a) const {
+    return a & 2u ? (a & 1u ? row[3] : row[2]) : (a & 1u ? row[1] : row[0]);
+  }
+};
 
 // The rows that a thread works on, of N tensors at once, on their way through
 // shared memory: for tokens t0, t0 + step, .. (t0 a CTA's first, a row's lanes

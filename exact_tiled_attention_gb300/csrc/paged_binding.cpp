@@ -14,6 +14,7 @@
 
 #include <climits>
 #include <cmath>
+#include <cstring>
 #include <optional>
 #include <sstream>
 #include <string>
@@ -261,6 +262,35 @@ struct Rope {
   }
 };
 
+// Positions of several axes: the axis of each pair of the rotation.
+struct PairAxes {
+  unsigned char of[256];
+  int n = 0;  // axes; 0: one position
+  PairAxes(PyObject* o, PyObject* positions, const Rope& rope) {
+    if (none(o)) return;
+    if (rope.table == nullptr) refuse_value("axes without rope");
+    const int64_t axes = tensor_of_dims(positions, "positions (with axes)", 3).size(0);
+    if (axes < 1 || axes > 4) refuse_value("positions must be of 1 to 4 axes, got ", axes);
+    PyObject* seq = PySequence_Fast(o, "axes must be a sequence of whole numbers");
+    if (seq == nullptr) throw python_error();
+    const Py_ssize_t pairs = PySequence_Fast_GET_SIZE(seq);
+    bool fits = pairs == rope.rot / 2 && pairs <= static_cast<Py_ssize_t>(sizeof(of));
+    for (Py_ssize_t i = 0; fits && i < pairs; ++i) {
+      const long v = PyLong_AsLong(PySequence_Fast_GET_ITEM(seq, i));
+      if (v == -1 && PyErr_Occurred()) {
+        Py_DECREF(seq);
+        throw python_error();
+      }
+      fits = v >= 0 && v < axes;
+      of[i] = static_cast<unsigned char>(v);
+    }
+    Py_DECREF(seq);
+    if (!fits)
+      refuse_value("axes must be one of the ", axes, " axes for each of the rotation's ", rope.rot / 2, " pairs");
+    n = static_cast<int>(axes);
+  }
+};
+
 // What both directions of the norm take.
 struct NormRope {
   First f;
@@ -268,11 +298,12 @@ struct NormRope {
   Rows q, k;
   const float *q_weight = nullptr, *k_weight = nullptr;
   Rope rope;
+  PairAxes axes;
   const int* positions;
   int64_t q_shape[4], k_shape[4];
 
-  NormRope(PyObject* qo, PyObject* ko, PyObject* qw, PyObject* kw, PyObject* ro, PyObject* po)
-      : f(first(qo, "q")), rope(ro, f.device) {
+  NormRope(PyObject* qo, PyObject* ko, PyObject* qw, PyObject* kw, PyObject* ro, PyObject* po, PyObject* ao)
+      : f(first(qo, "q")), rope(ro, f.device), axes(ao, po, rope) {
     const Tensor& qt = THPVariable_Unpack(qo);
     const int64_t heads = tensor_of_dims(ko, "k", 4).size(1);
     for (int i = 0; i < 4; ++i) q_shape[i] = k_shape[i] = qt.size(i);
@@ -289,26 +320,35 @@ struct NormRope {
     if (none(qw) && none(ro)) refuse_value("nothing to do: neither norm weights nor a rotation table");
     q_weight = static_cast<const float*>(opt(qw, "q_weight", {q_shape[3]}, at::kFloat, f.device));
     k_weight = static_cast<const float*>(opt(kw, "k_weight", {q_shape[3]}, at::kFloat, f.device));
-    positions = static_cast<const int*>(opt(po, "positions", {q_shape[0], q_shape[2]}, at::kInt, f.device));
+    positions = static_cast<const int*>(
+        axes.n > 0 ? ptr(po, "positions", {axes.n, q_shape[0], q_shape[2]}, at::kInt, f.device)
+                   : opt(po, "positions", {q_shape[0], q_shape[2]}, at::kInt, f.device));
     if (none(po) && !none(ro) && rope.rows < S) refuse_value("rope has ", rope.rows, " rows for ", S, " tokens");
   }
 };
 
 PyObject* norm_rope(PyObject* const* a) {
-  NormRope n(a[0], a[1], a[2], a[3], a[4], a[5]);
+  NormRope n(a[0], a[1], a[2], a[3], a[4], a[5], a[11]);
   const Target target(a[10], n.f.device);
   Output q_out, k_out;
   q_out.take(a[8], "q_out", n.q_shape, n.f.type, n.f.device);
   k_out.take(a[9], "k_out", n.k_shape, n.f.type, n.f.device);
-  done(attn_qk_norm_rope(n.q.data, n.k.data, n.q_weight, n.k_weight, n.rope.table, n.positions, q_out.data, k_out.data,
-                         n.B, n.H, n.Hkv, n.S, n.d, n.q.stride(), n.k.stride(), static_cast<float>(number(a[6])),
-                         n.rope.rows, n.rope.rot, truth(a[7]), n.f.code, target.stream),
-       "attn_qk_norm_rope");
+  if (n.axes.n > 0)
+    done(attn_qk_norm_rope_axes(n.q.data, n.k.data, n.q_weight, n.k_weight, n.rope.table, n.positions, n.axes.of,
+                                q_out.data, k_out.data, n.B, n.H, n.Hkv, n.S, n.d, n.axes.n, n.q.stride(),
+                                n.k.stride(), static_cast<float>(number(a[6])), n.rope.rows, n.rope.rot, truth(a[7]),
+                                n.f.code, target.stream),
+         "attn_qk_norm_rope_axes");
+  else
+    done(attn_qk_norm_rope(n.q.data, n.k.data, n.q_weight, n.k_weight, n.rope.table, n.positions, q_out.data, k_out.data,
+                           n.B, n.H, n.Hkv, n.S, n.d, n.q.stride(), n.k.stride(), static_cast<float>(number(a[6])),
+                           n.rope.rows, n.rope.rot, truth(a[7]), n.f.code, target.stream),
+         "attn_qk_norm_rope");
   return tuple({&q_out, &k_out});
 }
 
 PyObject* norm_rope_bwd(PyObject* const* a) {
-  NormRope n(a[2], a[3], a[4], a[5], a[6], a[7]);
+  NormRope n(a[2], a[3], a[4], a[5], a[6], a[7], a[16]);
   const Target target(a[15], n.f.device);
   const void* dqo = ptr(a[0], "dq_out", n.q_shape, n.f.type, n.f.device);
   const void* dko = ptr(a[1], "dk_out", n.k_shape, n.f.type, n.f.device);
@@ -334,12 +374,21 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
     dkw.take(a[14], "dk_weight", {n.d}, at::kFloat, n.f.device);
     ws.take(a[10], attn_qk_norm_rope_bwd_workspace_bytes(n.d), n.f.device);
   }
-  done(attn_qk_norm_rope_bwd(dqo, dko, n.q.data, n.k.data, n.q_weight, n.k_weight, n.rope.table, n.positions,
-                             dq_rows.data, dk_rows.data, static_cast<float*>(dqw.data), static_cast<float*>(dkw.data),
-                             n.B, n.H, n.Hkv, n.S, n.d, n.q.stride(), n.k.stride(), dq_rows.stride(), dk_rows.stride(),
-                             static_cast<float>(number(a[8])), n.rope.rows, n.rope.rot, truth(a[9]), ws.data, ws.bytes,
-                             n.f.code, target.stream),
-       "attn_qk_norm_rope_bwd");
+  float *dqwp = static_cast<float*>(dqw.data), *dkwp = static_cast<float*>(dkw.data);
+  const float eps = static_cast<float>(number(a[8]));
+  const int il = truth(a[9]);
+  if (n.axes.n > 0)
+    done(attn_qk_norm_rope_axes_bwd(dqo, dko, n.q.data, n.k.data, n.q_weight, n.k_weight, n.rope.table, n.positions,
+                                    n.axes.of, dq_rows.data, dk_rows.data, dqwp, dkwp, n.B, n.H, n.Hkv, n.S, n.d,
+                                    n.axes.n, n.q.stride(), n.k.stride(), dq_rows.stride(), dk_rows.stride(), eps,
+                                    n.rope.rows, n.rope.rot, il, ws.data, ws.bytes, n.f.code, target.stream),
+         "attn_qk_norm_rope_axes_bwd");
+  else
+    done(attn_qk_norm_rope_bwd(dqo, dko, n.q.data, n.k.data, n.q_weight, n.k_weight, n.rope.table, n.positions,
+                               dq_rows.data, dk_rows.data, dqwp, dkwp, n.B, n.H, n.Hkv, n.S, n.d, n.q.stride(),
+                               n.k.stride(), dq_rows.stride(), dk_rows.stride(), eps, n.rope.rows, n.rope.rot, il,
+                               ws.data, ws.bytes, n.f.code, target.stream),
+         "attn_qk_norm_rope_bwd");
   return tuple({&dq, &dk, &dqw, &dkw});
 }
 
@@ -388,7 +437,8 @@ struct Cache {
 };
 
 PyObject* append(const First& f, const Tensor& kt, PyObject* ko, PyObject* vo, const Cache& c, PyObject* new_lens,
-                 PyObject* rope_o, PyObject* interleaved, PyObject* qo, PyObject* q_out, PyObject* stream, bool fp4) {
+                 PyObject* rope_o, PyObject* interleaved, PyObject* qo, PyObject* q_out, PyObject* stream,
+                 PyObject* positions_o, PyObject* axes_o, bool fp4) {
   const Rows k = rows(ko, "k", kt.sizes(), f), v = rows(vo, "v", kt.sizes(), f);
   const int B = size(kt.size(0), "k"), Hkv = size(kt.size(1), "k"), S = size(kt.size(2), "k");
   const int d = size(kt.size(3), "k");
@@ -407,8 +457,33 @@ PyObject* append(const First& f, const Tensor& kt, PyObject* ko, PyObject* vo, c
   }
   const int* n = static_cast<const int*>(opt(new_lens, "new_lens", {B}, at::kInt, f.device));
   const Rope rope(rope_o, f.device);
+  PairAxes axes(axes_o, positions_o, rope);
+  const int* positions = nullptr;
+  if (axes.n > 0) {
+    positions = static_cast<const int*>(ptr(positions_o, "positions", {axes.n, B, S}, at::kInt, f.device));
+  } else if (!none(positions_o)) {  // one axis for all pairs
+    if (rope.table == nullptr) refuse_value("positions without rope");
+    positions = static_cast<const int*>(ptr(positions_o, "positions", {B, S}, at::kInt, f.device));
+    axes.n = 1;
+    std::memset(axes.of, 0, sizeof(axes.of));
+  }
   void* s = target.stream;
   const int il = truth(interleaved);
+  if (axes.n > 0) {
+    // The C library reads rot_dim / 2 of them, after it has bounded rot_dim by d.
+    if (fp4)
+      done(attn_cache_append_axes_fp4(k.data, v.data, c.k, c.k_factors, c.v, c.v_factors, c.k_descale, c.v_descale,
+                                      c.table, c.lens, n, rope.table, positions, axes.of, q.data, out.data, B, H, Hkv,
+                                      S, d, axes.n, c.page, c.n_pages, c.max_pages, q.stride(), k.stride(),
+                                      v.stride(), rope.rows, rope.rot, il, f.code, s),
+           "attn_cache_append_axes_fp4");
+    else
+      done(attn_cache_append_axes(k.data, v.data, c.k, c.v, c.table, c.lens, n, rope.table, positions, axes.of, q.data,
+                                  out.data, B, H, Hkv, S, d, axes.n, c.page, c.n_pages, c.max_pages, q.stride(),
+                                  k.stride(), v.stride(), rope.rows, rope.rot, il, f.code, s),
+           "attn_cache_append_axes");
+    return out.release();
+  }
   if (fp4)
     done(attn_cache_append_fp4(k.data, v.data, c.k, c.k_factors, c.v, c.v_factors, c.k_descale, c.v_descale, c.table,
                                c.lens, n, rope.table, q.data, out.data, B, H, Hkv, S, d, c.page, c.n_pages,
@@ -426,14 +501,14 @@ PyObject* cache_append(PyObject* const* a) {
   const First f = first(a[0], "k");
   const Tensor& k = THPVariable_Unpack(a[0]);
   const Cache c(a[2], a[3], a[4], a[5], k.size(0), k.size(1), k.size(3), f);
-  return append(f, k, a[0], a[1], c, a[6], a[7], a[8], a[9], a[10], a[11], false);
+  return append(f, k, a[0], a[1], c, a[6], a[7], a[8], a[9], a[10], a[11], a[12], a[13], false);
 }
 
 PyObject* cache_append_fp4(PyObject* const* a) {
   const First f = first(a[0], "k");
   const Tensor& k = THPVariable_Unpack(a[0]);
   const Cache c(a + 2, a[9], a[10], k.size(0), k.size(1), k.size(3), f.device);
-  return append(f, k, a[0], a[1], c, a[8], a[11], a[12], a[13], a[14], a[15], true);
+  return append(f, k, a[0], a[1], c, a[8], a[11], a[12], a[13], a[14], a[15], a[16], a[17], true);
 }
 
 int tokens(PyObject* o) {
@@ -601,10 +676,10 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {
     {"set_error", set_error, METH_O, nullptr},
-    method<norm_rope, 11>("attn_qk_norm_rope"),
-    method<norm_rope_bwd, 16>("attn_qk_norm_rope_bwd"),
-    method<cache_append, 12>("attn_cache_append"),
-    method<cache_append_fp4, 16>("attn_cache_append_fp4"),
+    method<norm_rope, 12>("attn_qk_norm_rope"),
+    method<norm_rope_bwd, 17>("attn_qk_norm_rope_bwd"),
+    method<cache_append, 14>("attn_cache_append"),
+    method<cache_append_fp4, 18>("attn_cache_append_fp4"),
     method<cache_gather, 8>("attn_cache_gather"),
     method<cache_gather_fp4, 13>("attn_cache_gather_fp4"),
     method<forward_paged, 13>("attn_fwd_paged"),

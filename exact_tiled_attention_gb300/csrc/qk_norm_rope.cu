@@ -40,6 +40,8 @@ struct NormRopeParams {
   const int* positions;
   const float* table;
   int table_rows, rot;
+  int n_axes;
+  uint32_t pair_axes[4];
   float eps;
   int B, S, per_chunk;  // heads that a thread walks over
   float* partial;       // backward: [2][kMaxBwdCtas][D]
@@ -64,8 +66,29 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// The angles of token t, (b, s), for one lane; AXES: from the positions of several
+// axes.
+template <int D, int MODE, bool AXES>
+struct TokenRope {
+  const NormRopeParams& p;
+  LaneAxes<D, MODE> axes;
+  int lane;
+  __device__ __forceinline__ TokenRope(const NormRopeParams& p_, int lane_in_row)
+      : p(p_), axes(p_.pair_axes, p_.rot, lane_in_row), lane(lane_in_row) {}
+  __device__ __forceinline__ void load(LaneRope& r, int t, int b, int s) const {
+    if constexpr (MODE == kRopeNone) {
+    } else if constexpr (AXES) {
+      const AxisRows rows(p.positions + t, static_cast<long long>(p.B) * p.S, p.n_axes, p.table, p.table_rows, p.rot,
+                          p.status);
+      load_rope_axes<D, MODE>(r, axes, rows, p.rot, lane);
+    } else {
+      load_rope<D, MODE>(r, table_row(p, b, s), p.rot, lane);
+    }
+  }
+};
+
 // Grid: (CTAs that walk over tokens, head chunks of q then k).
-template <int D, bool BF16, int MODE, bool NORM>
+template <int D, bool BF16, int MODE, bool NORM, bool AXES>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int kLanes = RowCfg<D>::kLanes;
   constexpr int kRowsCta = kThreads / kLanes;
@@ -83,6 +106,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   ring.base[0] = p.x[which];
   ring.strides[0] = p.xs[which];
   ring.start(&ring_smem, p.S, tokens, blockIdx.x * kRowsCta, gridDim.x * kRowsCta, h0, h1);
+  const TokenRope<D, MODE, AXES> token_rope(p, lane_in_row);
   float w[2][8], wp[2][8];
   int pc[2] = {0, 0};
 #pragma unroll
@@ -99,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     const int t = min(at, tokens - 1);  // the whole warp stays for the shuffles
     const int b = t / p.S, s = t % p.S;
     LaneRope rope;
-    if constexpr (MODE != kRopeNone) load_rope<D, MODE>(rope, table_row(p, b, s), p.rot, lane_in_row);
+    token_rope.load(rope, t, b, s);
     uint16_t* yrow = p.y[which] + ((static_cast<long long>(b) * p.heads[which] + h0) * p.S + s) * D;
     for (int h = h0; h < h1; ++h, yrow += static_cast<long long>(p.S) * D) {
       ring.wait();
@@ -135,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 
 // Grid: (CTAs that walk over tokens, head chunks of q then k).  With NORM each
 // CTA leaves the sum of its rows' weight gradients in `partial`.
-template <int D, bool BF16, int MODE, bool NORM>
+template <int D, bool BF16, int MODE, bool NORM, bool AXES>
 __global__ void __launch_bounds__(kThreads, 4) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int kLanes = RowCfg<D>::kLanes;
   constexpr int kRowsCta = kThreads / kLanes;
@@ -148,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_bwd_kernel(const __grid
   const int e0 = 8 * lane_in_row;
   wait_for_previous_kernel();
   if constexpr (NORM) let_next_kernel_start();  // norm_dw_kernel; without weights none of this call follows
+  const TokenRope<D, MODE, AXES> token_rope(p, lane_in_row);
   int pc[2] = {0, 0};
   float w[2][8], dw[2][8];
 #pragma unroll
@@ -175,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_bwd_kernel(const __grid
     const int t = min(t0 + static_cast<int>(threadIdx.x) / kLanes, tokens - 1);
     const int b = t / p.S, s = t % p.S;
     LaneRope rope;
-    if constexpr (MODE != kRopeNone) load_rope<D, MODE>(rope, table_row(p, b, s), p.rot, lane_in_row);
+    token_rope.load(rope, t, b, s);
     uint16_t* dxrow = p.dx[which] + b * dxs.b + s * dxs.s + h0 * dxs.h;
     for (int h = h0; h < h1; ++h, dxrow += dxs.h) {
       ring.wait();
@@ -284,6 +309,8 @@ NormRopeParams params(const NormRopeArgs& a) {
   p.table = a.rope.table;
   p.table_rows = a.rope.rows;
   p.rot = a.rope.rot_dim;
+  p.n_axes = a.rope.n_axes;
+  for (int i = 0; i < 4; ++i) p.pair_axes[i] = a.rope.pair_axes[i];
   p.eps = a.eps;
   p.B = a.B;
   p.S = a.S;
@@ -297,21 +324,22 @@ void set_chunks(NormRopeParams& p, int per_chunk) {
   for (int i = 0; i < 2; ++i) p.chunks[i] = (p.heads[i] + per_chunk - 1) / per_chunk;
 }
 
-// Calls f with the rotation mode and the presence of a norm as constants.
+// Calls f with the rotation mode, the presence of a norm and of several axes as
+// constants.
+template <typename Mode, typename F>
+int with_norm(const NormRopeArgs& a, Mode mode, F&& f) {
+  const bool norm = a.w[0] != nullptr;
+  if (a.rope.n_axes > 0)
+    return norm ? f(mode, std::true_type(), std::true_type()) : f(mode, std::false_type(), std::true_type());
+  return norm ? f(mode, std::true_type(), std::false_type()) : f(mode, std::false_type(), std::false_type());
+}
 template <typename F>
 int with_mode(const NormRopeArgs& a, F&& f) {
-  const bool norm = a.w[0] != nullptr;
   switch (rope_mode(a.rope, a.d)) {
-    case kRopeNone: return f(std::integral_constant<int, kRopeNone>(), std::true_type());
-    case kRopePairs:
-      return norm ? f(std::integral_constant<int, kRopePairs>(), std::true_type())
-                  : f(std::integral_constant<int, kRopePairs>(), std::false_type());
-    case kRopeHalves:
-      return norm ? f(std::integral_constant<int, kRopeHalves>(), std::true_type())
-                  : f(std::integral_constant<int, kRopeHalves>(), std::false_type());
-    default:
-      return norm ? f(std::integral_constant<int, kRopePart>(), std::true_type())
-                  : f(std::integral_constant<int, kRopePart>(), std::false_type());
+    case kRopeNone: return f(std::integral_constant<int, kRopeNone>(), std::true_type(), std::false_type());
+    case kRopePairs: return with_norm(a, std::integral_constant<int, kRopePairs>(), f);
+    case kRopeHalves: return with_norm(a, std::integral_constant<int, kRopeHalves>(), f);
+    default: return with_norm(a, std::integral_constant<int, kRopePart>(), f);
   }
 }
 
@@ -333,8 +361,9 @@ int launch_fwd(const NormRopeArgs& a) {
   long long x = (kFwdCtas * static_cast<long long>(a.num_sms) + chunks - 1) / chunks;
   if (x > token_ctas) x = token_ctas;
   const dim3 grid(static_cast<unsigned>(x), chunks);
-  return with_mode(a, [&](auto mode, auto norm) {
-    return launch_after(norm_rope_kernel<D, BF16, decltype(mode)::value, decltype(norm)::value>, grid, kThreads, a.stream, p);
+  return with_mode(a, [&](auto mode, auto norm, auto axes) {
+    return launch_after(norm_rope_kernel<D, BF16, decltype(mode)::value, decltype(norm)::value, decltype(axes)::value>,
+                        grid, kThreads, a.stream, p);
   });
 }
 
@@ -358,8 +387,9 @@ int launch_bwd(const NormRopeArgs& a) {
   if (x > kMaxBwdCtas / most_chunks) x = kMaxBwdCtas / most_chunks;
   if (x > token_ctas) x = token_ctas;
   const dim3 grid(static_cast<unsigned>(x), p.chunks[0] + p.chunks[1]);
-  const int rc = with_mode(a, [&](auto mode, auto norm) {
-    return launch_after(norm_rope_bwd_kernel<D, BF16, decltype(mode)::value, decltype(norm)::value>, grid, kThreads, a.stream, p);
+  const int rc = with_mode(a, [&](auto mode, auto norm, auto axes) {
+    return launch_after(norm_rope_bwd_kernel<D, BF16, decltype(mode)::value, decltype(norm)::value, decltype(axes)::value>,
+                        grid, kThreads, a.stream, p);
   });
   if (rc != 0 || a.w[0] == nullptr) return rc;
   DwParams dp{};

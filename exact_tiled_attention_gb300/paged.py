@@ -58,18 +58,31 @@ def rope_table(rows: int, rot_dim: int, base: float = 10000.0, device="cuda") ->
     return torch.cat([a.cos(), a.sin()], dim=1).float()
 
 
+def rope_pair_axes(sections, cycle: bool = False) -> tuple:
+    """The axis of each pair of a rotation by positions of several axes, from the
+    number of pairs that follow each axis: the first axis's, the next one's and so
+    on, or (cycle) the axes in turn, each until its pairs are used up."""
+    if not 1 <= len(sections) <= 4 or any(n < 0 for n in sections):
+        raise ValueError("sections must be 1 to 4 numbers of pairs")
+    if not cycle:
+        return tuple(a for a, n in enumerate(sections) for _ in range(n))
+    return tuple(a for i in range(max(sections)) for a, n in enumerate(sections) if i < n)
+
+
 def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=None, eps: float = 1e-6,
-                      interleaved: bool = False, q_out=None, k_out=None, stream=None):
+                      interleaved: bool = False, q_out=None, k_out=None, stream=None, axes=None):
     """RMS norm of every query and key head with the position rotation, through
-    the C ABI `attn_qk_norm_rope`.
+    the C ABI `attn_qk_norm_rope`, or `attn_qk_norm_rope_axes` with axes.
 
     q [B,H,S,d], k [B,Hkv,S,d] fp16 or bf16 with contiguous rows (views of a
     projection output need no copy); q_weight, k_weight fp32 [d], or both None
     (rotation alone); rope fp32 [rows, rot_dim] from rope_table, or None (norm
-    alone); positions int32 [B,S], or None (0 .. S-1).  Returns contiguous
+    alone); positions int32 [B,S], or None (0 .. S-1).  With axes, the axis of
+    each of the rot_dim / 2 pairs (rope_pair_axes makes them), positions is int32
+    [n_axes,B,S] and a pair turns by its own axis's position.  Returns contiguous
     (q_out, k_out), which may be given as q and k themselves."""
     return (_native or _load()).attn_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved, q_out,
-                                                  k_out, stream)
+                                                  k_out, stream, axes)
 
 
 def attn_qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
@@ -78,8 +91,9 @@ def attn_qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
 
 def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rope=None, positions=None,
                           eps: float = 1e-6, interleaved: bool = False, workspace=None, dq=None, dk=None,
-                          dq_weight=None, dk_weight=None, stream=None):
-    """Gradients of attn_qk_norm_rope through the C ABI `attn_qk_norm_rope_bwd`.
+                          dq_weight=None, dk_weight=None, stream=None, axes=None):
+    """Gradients of attn_qk_norm_rope through the C ABI `attn_qk_norm_rope_bwd`, or
+    `attn_qk_norm_rope_axes_bwd` with axes.
 
     dq_out, dk_out: the (contiguous) gradients of its outputs; the other inputs
     as it got them.  dq and dk may be given at any strides that q and k may
@@ -87,33 +101,38 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, ro
     (dq, dk, dq_weight, dk_weight), the last two fp32 [d], or None without
     weights."""
     return (_native or _load()).attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rope, positions, eps,
-                                                      interleaved, workspace, dq, dk, dq_weight, dk_weight, stream)
+                                                      interleaved, workspace, dq, dk, dq_weight, dk_weight, stream,
+                                                      axes)
 
 
 def attn_cache_append(k, v, k_cache, v_cache, page_table, seqlens, new_lens=None, rope=None,
-                      interleaved: bool = False, q=None, q_out=None, stream=None):
+                      interleaved: bool = False, q=None, q_out=None, stream=None, positions=None, axes=None):
     """Writes new keys and values into a 16-bit paged cache through the C ABI
-    `attn_cache_append`, the keys (and q, if given) rotated on the way.
+    `attn_cache_append`, or `attn_cache_append_axes` with positions, the keys (and
+    q, if given) rotated on the way.
 
     k, v [B,Hkv,S,d] and q [B,H,S,d] (contiguous rows, any strides);
     k_cache, v_cache [n_pages,Hkv,page_size,d]; page_table int32 [B,max_pages];
     seqlens int32 [B], the new tokens included; new_lens int32 [B] (None: S);
-    rope from rope_table, or None.  Returns the rotated queries (None without q);
+    rope from rope_table, or None; positions of the rotation, where they are not
+    the tokens' places in their sequences: int32 [B,S], or [n_axes,B,S] with axes
+    (as for attn_qk_norm_rope).  Returns the rotated queries (None without q);
     q_out may be q itself where that is contiguous."""
     return (_native or _load()).attn_cache_append(k, v, k_cache, v_cache, page_table, seqlens, new_lens, rope,
-                                                  interleaved, q, q_out, stream)
+                                                  interleaved, q, q_out, stream, positions, axes)
 
 
 def attn_cache_append_fp4(k, v, k_codes, k_factors, v_codes, v_factors, page_table, seqlens, new_lens=None,
                           k_descale=None, v_descale=None, rope=None, interleaved: bool = False, q=None, q_out=None,
-                          stream=None):
-    """attn_cache_append into a 4-bit paged cache (C ABI `attn_cache_append_fp4`):
+                          stream=None, positions=None, axes=None):
+    """attn_cache_append into a 4-bit paged cache (C ABI `attn_cache_append_fp4`,
+    `attn_cache_append_axes_fp4`):
     k_codes, v_codes uint8 [n_pages,Hkv,page_size,d/2]; k_factors, v_factors
     float8_e4m3fn (or both uint8) [n_pages,Hkv,page_size,d/16]; k_descale,
     v_descale fp32 [Hkv] or None."""
     return (_native or _load()).attn_cache_append_fp4(k, v, k_codes, k_factors, v_codes, v_factors, page_table,
                                                       seqlens, new_lens, k_descale, v_descale, rope, interleaved, q,
-                                                      q_out, stream)
+                                                      q_out, stream, positions, axes)
 
 
 def attn_cache_gather(k_cache, v_cache, page_table, seqlens, S: int, k_out=None, v_out=None, stream=None):

@@ -358,6 +358,12 @@ size_t attn_decode_noalloc_scratch_bytes(void);
  *   (a, b) -> (a cos - b sin, b cos + a sin), in fp32.  The other elements pass as they
  * are, infinities, NaN and signs of zeros included.
  *
+ * The *_axes entry points turn pairs by positions of several axes (time, height and
+ * width of images and video): positions [n_axes, B, S] int32, a device array, and
+ * pair_axes [rot_dim / 2], a HOST array that is read before the call returns: pair i
+ * of token (b, s) takes cosine and sine i of row positions[pair_axes[i]][b][s].
+ * n_axes is 1 .. 4, each pair_axes[i] below it, and rot_dim above 0.
+ *
  * q_strides, k_strides, ... are NULL for a contiguous [B, heads, S, d] tensor,
  * or three host values: the distances, in elements, of consecutive sequences,
  * heads and tokens (multiples of 8; a head's d elements are contiguous), so
@@ -365,9 +371,7 @@ size_t attn_decode_noalloc_scratch_bytes(void);
  *
  * One step of serving: attn_qk_norm_rope where the model has such norms (and
  * then no rotation here), attn_cache_append, attn_decode_paged.  A chunk of a
- * prompt: append it, attn_cache_gather the sequence, attn_fwd with causal = 1;
- * sequences of one length together, others in calls of their own (attn_fwd has one
- * length, and would count the zero rows behind a shorter sequence as keys).
+ * prompt, drafted tokens to check: append them, then attn_fwd_paged.
  */
 
 /*
@@ -392,6 +396,19 @@ int attn_qk_norm_rope(const void *q, const void *k, const float *q_weight, const
                       int B, int H, int Hkv, int S, int d, const long long *q_strides,
                       const long long *k_strides, float eps, int rope_rows, int rot_dim,
                       int interleaved, int dtype, void *stream);
+
+/*
+ * attn_qk_norm_rope_axes -- attn_qk_norm_rope by positions of several axes (above).
+ *
+ * Errors: as attn_qk_norm_rope, GBATTN_EBADSHAPE also for n_axes or an entry of
+ * pair_axes out of range, EPOINTER also without positions, pair_axes or rotation.
+ */
+int attn_qk_norm_rope_axes(const void *q, const void *k, const float *q_weight,
+                           const float *k_weight, const float *rope, const int *positions,
+                           const unsigned char *pair_axes, void *q_out, void *k_out, int B, int H,
+                           int Hkv, int S, int d, int n_axes, const long long *q_strides,
+                           const long long *k_strides, float eps, int rope_rows, int rot_dim,
+                           int interleaved, int dtype, void *stream);
 
 /*
  * attn_qk_norm_rope_bwd_workspace_bytes -- bytes of device workspace that
@@ -425,6 +442,23 @@ int attn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q,
                           const long long *dq_strides, const long long *dk_strides, float eps,
                           int rope_rows, int rot_dim, int interleaved, void *workspace,
                           size_t workspace_bytes, int dtype, void *stream);
+
+/*
+ * attn_qk_norm_rope_axes_bwd -- gradients of attn_qk_norm_rope_axes; arguments and
+ * workspace as for attn_qk_norm_rope_bwd.
+ *
+ * Errors: as attn_qk_norm_rope_axes, and GBATTN_EWORKSPACE.
+ */
+int attn_qk_norm_rope_axes_bwd(const void *dq_out, const void *dk_out, const void *q,
+                               const void *k, const float *q_weight, const float *k_weight,
+                               const float *rope, const int *positions,
+                               const unsigned char *pair_axes, void *dq, void *dk,
+                               float *dq_weight, float *dk_weight, int B, int H, int Hkv, int S,
+                               int d, int n_axes, const long long *q_strides,
+                               const long long *k_strides, const long long *dq_strides,
+                               const long long *dk_strides, float eps, int rope_rows, int rot_dim,
+                               int interleaved, void *workspace, size_t workspace_bytes, int dtype,
+                               void *stream);
 
 /*
  * attn_cache_append -- writes new keys and values into a 16-bit paged cache,
@@ -477,6 +511,33 @@ int attn_cache_append_fp4(const void *k, const void *v, void *k_codes, void *k_f
                           int max_pages, const long long *q_strides, const long long *k_strides,
                           const long long *v_strides, int rope_rows, int rot_dim, int interleaved,
                           int dtype, void *stream);
+
+/*
+ * attn_cache_append_axes, attn_cache_append_axes_fp4 -- the appends with the rotation
+ * by positions of several axes (above), or of one that is not the slot's
+ * (n_axes = 1).  The slots follow from seqlens and new_lens all the same; positions
+ * of padding rows are not looked at.
+ *
+ * Errors: as attn_cache_append, and those of attn_qk_norm_rope_axes for the axes.
+ */
+int attn_cache_append_axes(const void *k, const void *v, void *k_cache, void *v_cache,
+                           const int *page_table, const int *seqlens, const int *new_lens,
+                           const float *rope, const int *positions, const unsigned char *pair_axes,
+                           const void *q, void *q_out, int B, int H, int Hkv, int S, int d,
+                           int n_axes, int page_size, int n_pages, int max_pages,
+                           const long long *q_strides, const long long *k_strides,
+                           const long long *v_strides, int rope_rows, int rot_dim, int interleaved,
+                           int dtype, void *stream);
+int attn_cache_append_axes_fp4(const void *k, const void *v, void *k_codes, void *k_factors,
+                               void *v_codes, void *v_factors, const float *k_descale,
+                               const float *v_descale, const int *page_table, const int *seqlens,
+                               const int *new_lens, const float *rope, const int *positions,
+                               const unsigned char *pair_axes, const void *q, void *q_out, int B,
+                               int H, int Hkv, int S, int d, int n_axes, int page_size,
+                               int n_pages, int max_pages, const long long *q_strides,
+                               const long long *k_strides, const long long *v_strides,
+                               int rope_rows, int rot_dim, int interleaved, int dtype,
+                               void *stream);
 
 /*
  * attn_cache_gather -- reads the first S tokens of every sequence of a paged
