@@ -52,16 +52,48 @@ constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
 
 template <int D, int NT, bool FP4>
 struct Cfg {
-  static constexpr bool kPInTmem = (D == 64);
+  // Tensor memory has room for P unless there are two tiles of d = 128, and with one
+  // tile for Q as well: over 4 bits, where shared memory's bandwidth bounds, both
+  // products then read only K or V from there.
+  static constexpr bool kPInTmem = D == 64 || NT == 1;
+  static constexpr bool kQInTmem = FP4 && NT == 1;
+  // With one tile S has two places in turn, and one thread issues the products with K,
+  // another those with V: a chain of products into one place runs at half the tensor
+  // core's rate, two at once keep it busy (two tiles have two chains each).
+  static constexpr int kSBufs = NT == 1 ? 2 : 1;
+  static constexpr int kSCol = 0, kOCol = 2 * kBN, kPCol = kOCol + NT * D;
+  struct Place {
+    int st, round;
+  };
+  // The place of K or V of a key tile: load number `item`, tile number `tile` of the CTA.
+  __device__ static __forceinline__ Place place(bool is_v, int item, int tile) {
+    if constexpr (NT == 2) {
+      return {item % kStages, item / kStages};
+    } else {
+      if (is_v) return {kKStages + tile % (kStages - kKStages), tile / (kStages - kKStages)};
+      return {tile % kKStages, tile / kKStages};
+    }
+  }
+  // Where tile x's S number d goes, and its barriers.
+  __device__ static __forceinline__ int s_bar(int x, int d) { return NT == 1 ? d & 1 : x; }
+  __device__ static constexpr int q_col() { return kPCol + kBN / 2; }
   static constexpr int kColBlocks = D / 64;
   static constexpr int kTileBytes = kBM * D * 2;
   static constexpr int kBlockBytes = kBM * 128;
-  static constexpr int kStageBytes = kPInTmem ? kTileBytes : kBM * kBN * 2;  // P, or (d = 64) the output alone
+  // Where an output waits for its store: P's place, or one of its own (one tile over 4
+  // bits: none, threads store their rows).
+  static constexpr bool kDirectO = FP4 && NT == 1;
+  static constexpr int kStageBytes = kDirectO ? 0 : kPInTmem ? kTileBytes : kBM * kBN * 2;
   // 16-bit key and value tiles; of a 4-bit cache's rows, what comes from memory and
   // what the conversion makes of it.
-  static constexpr int kStages = FP4 ? (NT == 2 ? (D == 128 ? 2 : 6) : (D == 128 ? 3 : 6))
+  static constexpr int kStages = FP4 ? (NT == 2 ? (D == 128 ? 2 : 6) : (D == 128 ? 4 : 8))
                                      : (NT == 2 ? (D == 128 ? 3 : 8) : (D == 128 ? 5 : 12));
-  static constexpr int kRawStages = !FP4 ? 0 : NT == 2 ? (D == 128 ? 3 : 8) : (D == 128 ? 7 : 12);
+  static constexpr int kRawStages = !FP4 ? 0 : NT == 2 ? (D == 128 ? 3 : 8) : (D == 128 ? 6 : 12);
+  // With two tiles every issuer takes every key and value tile, so all places form one
+  // ring.  With one, the issuers take keys and values apart, each at its own pace: a
+  // ring each (a wait tells only even from odd rounds of a place, so whoever waits has
+  // to follow all of its rounds).
+  static constexpr int kKStages = NT == 2 ? kStages : kStages / 2;
   static constexpr int kRawBytes = kBN * (D / 2 + D / 16);  // codes, then factors
   static constexpr int kQOff = 0;
   static constexpr int kPOff = NT * kTileBytes;
@@ -85,6 +117,8 @@ struct Cfg {
   static_assert(!kSplit || NT * 128 * kSoftmaxRegs + 128 * kControlRegs + 32 * kConvertWarps * kConvertRegs <=
                                kThreads * kLaunchRegs,
                 "register split");
+  static_assert(!kSplit || (kSoftmaxRegs >= kLaunchRegs && kControlRegs <= kLaunchRegs && kConvertRegs <= kLaunchRegs),
+                "the softmax's registers rise, the others' fall");
 };
 
 struct Params {
@@ -112,7 +146,7 @@ struct Params {
 
 struct __align__(8) Barriers {
   uint64_t q_full, q_empty;
-  uint64_t q_ready[2];     // queries converted to fp16 (bf16 over 4 bits)
+  uint64_t q_ready[2];     // queries converted to fp16 (bf16 over 4 bits), or in tensor memory
   uint64_t raw_empty[12];  // 4 bits: codes and factors converted (raw: copied)
   uint64_t kv_full[12], kv_empty[12], raw[12];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_full[2], mma_done[2];
@@ -124,6 +158,7 @@ struct __align__(8) Barriers {
   long long scan[16];
   uint32_t tmem_base;
   int abort_flag;
+  int last_round[12];      // of the loader's places, -1 before the first
   uint8_t bad[kTileRing];          // 16-key blocks of a tile that have no page
   uint8_t nan_any[kSegRing];
   uint8_t nan_from[kSegRing][128]; // column's first non-finite key behind the first row's last key, - 1
@@ -313,7 +348,7 @@ template <int D, bool BF16, int NT, bool FP4>
 __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D, NT, FP4>;
   constexpr bool kMmaBf16 = BF16 && !FP4;  // over 4 bits all operands are fp16
-  constexpr bool kConvertQ = BF16 && FP4;
+  constexpr bool kReadyQ = (BF16 && FP4) || C::kQInTmem;  // queries pass through the softmax warps
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem + C::kQOff;
   uint8_t* sP = smem + C::kPOff;
@@ -340,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
       mbar_init(&bars->raw[s], 1);
       mbar_init(&bars->raw_empty[s], C::kConvertWarps);
     }
-    for (int x = 0; x < NT; ++x) {
+    for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->q_ready[x], kBM);
       mbar_init(&bars->s_full[x], 1);
       mbar_init(&bars->s_free[x], kBM);
@@ -390,13 +425,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
       while (ok && cur.next(p, seg)) {
         const int n = seg.j1 - seg.j0;
         for (int i = 0; i < 2 * n; ++i, ++items) {
-          const int rs = items % C::kRawStages, st = items % C::kStages;
+          const int rs = items % C::kRawStages;
           // K_0, K_1, V_0, K_2, ..
+          const bool is_v = i == 2 * n - 1 || (i > 0 && i % 2 == 0);
           const int j = i == 0 ? 0 : i == 2 * n - 1 ? n - 1 : (i & 1) ? (i + 1) / 2 : i / 2 - 1;
+          const typename C::Place at = C::place(is_v, items, tiles + j);
+          const int st = at.st;
           ok = bounded_wait(&bars->raw[rs], (items / C::kRawStages) & 1, abort_flag, p.status, kStatusTimeoutLoad);
-          if (ok && items >= C::kStages)
-            ok = bounded_wait(&bars->kv_empty[st], (items / C::kStages - 1) & 1, abort_flag, p.status,
-                              kStatusTimeoutLoad);
+          if (ok && at.round > 0)
+            ok = bounded_wait(&bars->kv_empty[st], (at.round - 1) & 1, abort_flag, p.status, kStatusTimeoutLoad);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint8_t* src = smem + C::kRawOff + rs * C::kRawBytes;
@@ -449,14 +486,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
       const bool loads = cb < C::kColBlocks;
       const int box_shift = 31 - __clz(p.box_rows);
       constexpr int kStages = FP4 ? C::kRawStages : C::kStages;
+      int* const last_round = bars->last_round;
+      if (lane == 0)
+        for (int st = 0; st < kStages; ++st) last_round[st] = -1;
       uint64_t* const empty = FP4 ? bars->raw_empty : bars->kv_empty;
       const uint64_t keep = policy_evict_last(), once = policy_evict_first();
       const int missing = p.n_pages * p.Hkv;  // a coordinate outside: zeros
-      int items = 0, segs = 0, tiles = 0;
+      int items = 0, segs = 0, tile0 = 0;
       bool ok = true;
-      // The lane's page of tile j, -1 behind the sequence.
-      auto lookup = [&](int j) {
-        const int key = j * kBN + (box << box_shift);
+      // Pages are looked up for 32 boxes at a time, a window ahead of their use: lane l
+      // has box l % boxes of the window's tile l / boxes (-1 behind the sequence).
+      const int per_window = 32 / boxes;
+      auto lookup = [&](int w) {
+        const int key = (seg.j0 + w * per_window + lane / boxes) * kBN + (box << box_shift);
         return key < seg.s.n ? p.page_table[static_cast<long long>(seg.b) * p.max_pages + (key >> p.page_shift)] : -1;
       };
       while (ok && cur.next(p, seg)) {
@@ -480,9 +522,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
         if (!ok) break;
         ++segs;
         auto issue = [&](bool is_v, int j, int page) {
-          const int st = items % kStages;
-          if (lane == 0 && items >= kStages)
-            ok = bounded_wait(&empty[st], (items / kStages - 1) & 1, abort_flag, p.status, kStatusTimeoutLoad);
+          const typename C::Place at = FP4 ? typename C::Place{items % C::kRawStages, items / C::kRawStages}
+                                           : C::place(is_v, items, tile0 + j - seg.j0);
+          const int st = at.st;
+          if (lane == 0 && at.round > 0)
+            ok = bounded_wait(&empty[st], (at.round - 1) & 1, abort_flag, p.status, kStatusTimeoutLoad);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) return;
           const int key = j * kBN + (box << box_shift);
@@ -497,8 +541,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
               for (int i = 0; i < 8; ++i) wide |= ((bad >> (i * 16 >> box_shift)) & 1u) << i;
               bad = wide;
             }
-            if (lane == 0) bars->bad[tiles % kTileRing] = static_cast<uint8_t>(bad);
-            ++tiles;
+            if (lane == 0) bars->bad[(tile0 + j - seg.j0) % kTileRing] = static_cast<uint8_t>(bad);
           }
           if constexpr (FP4) {
             // Pages that are there: lanes of the first half copy codes, the others
@@ -508,14 +551,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
               mbar_arrive_expect_tx(&bars->raw[st], (__popc(copied) << box_shift) * (D / 2 + D / 16));
             __syncwarp();
             if (found && cb < 2) {
-              const long long at = ((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) +
+              const long long row = ((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) +
                                    (key & ((1 << p.page_shift) - 1));
               const int row_bytes = cb == 0 ? D / 2 : D / 16;
               bulk_load(smem + C::kRawOff + st * C::kRawBytes + (cb == 0 ? 0 : kBN * (D / 2)) +
                             (box << box_shift) * row_bytes,
-                        (cb == 0 ? p.codes[is_v] : p.factors[is_v]) + at * row_bytes,
+                        (cb == 0 ? p.codes[is_v] : p.factors[is_v]) + row * row_bytes,
                         static_cast<uint32_t>(row_bytes << box_shift), &bars->raw[st], keep);
             }
+            if (lane == 0) last_round[st] = at.round;
             ++items;
             return;
           }
@@ -528,18 +572,23 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
             tma_load_3d(sRing + st * C::kTileBytes + cb * C::kBlockBytes + (box << box_shift) * 128,
                         is_v ? &p.tv : &p.tk, bar, cb * 64, found ? key & ((1 << p.page_shift) - 1) : 0, z, keep);
           }
+          if (lane == 0) last_round[st] = at.round;
           ++items;
         };
         const int n = seg.j1 - seg.j0;
-        int pa = lookup(seg.j0), pb = n > 1 ? lookup(seg.j0 + 1) : -1;
-        issue(false, seg.j0, pa);
-        for (int t = 0; ok && t < n; ++t) {
-          const int pc = t + 2 < n ? lookup(seg.j0 + t + 2) : -1;
-          if (t + 1 < n) issue(false, seg.j0 + t + 1, pb);
-          if (ok) issue(true, seg.j0 + t, pa);
-          pa = pb;
-          pb = pc;
+        int now = lookup(0), next = lookup(1);  // windows of V's tile and the one behind it
+        issue(false, seg.j0, __shfl_sync(0xffffffffu, now, box));
+        for (int t = 0, in = 0; ok && t < n; ++t) {  // `in`: V's tile in its window
+          const int page_v = __shfl_sync(0xffffffffu, now, in * boxes + box);
+          if (++in == per_window) {
+            in = 0;
+            now = next;
+            next = lookup(t / per_window + 2);
+          }
+          if (t + 1 < n) issue(false, seg.j0 + t + 1, __shfl_sync(0xffffffffu, now, in * boxes + box));
+          if (ok) issue(true, seg.j0 + t, page_v);
         }
+        tile0 += n;
       }
       // Every copy must have landed before the CTA ends.
       if (lane == 0) {
@@ -547,8 +596,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
         volatile int* ignore = reinterpret_cast<volatile int*>(&dummy);
         if (segs > 0) bounded_wait(&bars->q_full, (segs - 1) & 1, ignore, p.status, kStatusTimeoutDrain);
         uint64_t* const full = FP4 ? bars->raw : bars->kv_full;
-        for (int it = max(0, items - kStages); it < items; ++it)
-          bounded_wait(&full[it % kStages], (it / kStages) & 1, ignore, p.status, kStatusTimeoutDrain);
+        for (int st = 0; st < kStages; ++st)
+          if (last_round[st] >= 0)
+            bounded_wait(&full[st], last_round[st] & 1, ignore, p.status, kStatusTimeoutDrain);
       }
       __syncwarp();
     } else if (!FP4 && warp == C::kGuardWarp) {
@@ -568,7 +618,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
 #pragma unroll
         for (int c = 0; c < kCols; ++c) first[c] = 255u;
         for (int j = jm; j < seg.j1; ++j) {
-          const int it = items + item_of_v(j - seg.j0, n), st = it % C::kStages;
+          const int st = C::place(true, items + item_of_v(j - seg.j0, n), items / 2 + j - seg.j0).st;
           ok = bounded_wait(&bars->raw[st], (raw_phase >> st) & 1, abort_flag, p.status, kStatusTimeoutMma);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -612,26 +662,30 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
         items += 2 * n;
         ++segs;
       }
-    } else if (warp - C::kMmaWarp < NT) {
+    } else if (warp - C::kMmaWarp < 2) {
       // ================================================================ MMA issuers
       // One issuing thread per tile.  Each releases every K/V slot; key tiles that
-      // its rows do not visit are released once landed.
+      // its rows do not visit are released once landed.  (One tile: one for K, one for V.)
       if (lane == 0) {
-        const int x = warp - C::kMmaWarp;
+        const int x = NT == 1 ? 0 : warp - C::kMmaWarp;
+        const bool does_qk = NT == 2 || warp == C::kMmaWarp;
         constexpr uint32_t kIdescQK = idesc_f16(kMmaBf16, false, false, kBM, kBN);
         constexpr uint32_t kIdescPV = idesc_f16(kMmaBf16, false, true, kBM, D);
         const uint32_t ring_addr = smem_u32(sRing);
-        const uint32_t s_col = tmem + x * kBN;
-        const uint32_t o_col = tmem + 2 * kBN + x * D;
-        const uint32_t p_tcol = tmem + 2 * kBN + 2 * D + x * (kBN / 2);
+        const uint32_t o_col = tmem + C::kOCol + x * D;
+        const uint32_t p_tcol = tmem + C::kPCol + x * (kBN / 2);
         const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ + x * C::kTileBytes), 16, 1024);
         const uint64_t p_desc = smem_desc_sw128(smem_u32(sP + x * C::kStageBytes), 16, 1024);
-        auto issue_qk = [&](int st) {
+        auto issue_qk = [&](int st, int d) {
+          const uint32_t s_col = tmem + C::kSCol + C::s_bar(x, d) * kBN;
           const uint64_t kd = smem_desc_sw128(ring_addr + st * C::kTileBytes, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t off = ((kk / 4) * C::kBlockBytes + (kk % 4) * 32) >> 4;
-            mma_f16_ss(s_col, q_desc + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
+            if constexpr (C::kQInTmem)
+              mma_f16_ts(s_col, tmem + C::q_col() + kk * 8, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
+            else
+              mma_f16_ss(s_col, q_desc + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
           }
         };
         auto issue_pv = [&](int st, bool accumulate) {
@@ -650,26 +704,42 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
         int items = 0, segs = 0;
         int done = 0;  // key tiles of this row tile so far
         bool ok = true;
-        auto wait_item = [&](int item) {
-          return bounded_wait(&bars->kv_full[item % C::kStages], (item / C::kStages) & 1, abort_flag, p.status,
-                              kStatusTimeoutMma);
+        int st = 0;  // place of the last item waited for
+        // K or V of the segment's key tile j.
+        auto wait_item = [&](bool is_v, int j, int n) {
+          const typename C::Place at =
+              C::place(is_v, items + (is_v ? item_of_v(j, n) : item_of_k(j)), items / 2 + j);
+          st = at.st;
+          return bounded_wait(&bars->kv_full[st], at.round & 1, abort_flag, p.status, kStatusTimeoutMma);
         };
-        auto qk = [&](int item) {
-          const int st = item % C::kStages;
-          if (!(ok = wait_item(item))) return;
-          // S_X is in registers (of the tile before this one)
-          if (done > 0 && !(ok = bounded_wait(&bars->s_free[x], (done - 1) & 1, abort_flag, p.status, kStatusTimeoutMma)))
+        // S of the tile that is number `d` of this row tile's.
+        auto qk = [&](int j, int n, int d) {
+          if (!(ok = wait_item(false, j, n))) return;
+          // The S before it in this place is in registers.
+          if (d >= C::kSBufs &&
+              !(ok = bounded_wait(&bars->s_free[C::s_bar(x, d)], (d / C::kSBufs - 1) & 1, abort_flag, p.status,
+                                  kStatusTimeoutMma)))
             return;
           tc_fence_after();
-          issue_qk(st);
-          mma_commit(&bars->s_full[x]);
+          issue_qk(st, d);
+          mma_commit(&bars->s_full[C::s_bar(x, d)]);
+          mma_commit(&bars->kv_empty[st]);
+        };
+        auto pv = [&](int j, int n, int d, bool last) {
+          if (!(ok = wait_item(true, j, n))) return;
+          if (!(ok = bounded_wait(&bars->p_full[x], d & 1, abort_flag, p.status, kStatusTimeoutMma))) return;
+          tc_fence_after();
+          issue_pv(st, j > 0);
+          mma_commit(&bars->p_free[x]);
+          if (last) mma_commit(&bars->o_full[x]);
           mma_commit(&bars->kv_empty[st]);
         };
         while (ok && cur.next(p, seg)) {
           const TileRows tile(p, seg, x, NT);
           const int n = seg.j1 - seg.j0, nx = tile.j1 - seg.j0;
-          ok = bounded_wait(kConvertQ ? &bars->q_ready[x] : &bars->q_full, segs & 1, abort_flag, p.status,
-                            kStatusTimeoutMma);
+          if (NT == 2 || does_qk)
+            ok = bounded_wait(kReadyQ ? &bars->q_ready[x] : &bars->q_full, segs & 1, abort_flag, p.status,
+                              kStatusTimeoutMma);
           // Tile L starts when tile H has read its first S: the two softmax chains
           // then run staggered.
           if (NT == 2 && ok && x == 1 && segs == 0 && nx > 0) {
@@ -677,41 +747,38 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
             if (other.j1 > seg.j0) ok = bounded_wait(&bars->stagger, 0, abort_flag, p.status, kStatusTimeoutMma);
           }
           if (!ok) break;
-          if (nx > 0) qk(items);
-          if (nx <= 1) {
+          if constexpr (NT == 1) {
+            // (one row tile: it visits all of the segment's key tiles)
+            for (int j = 0; ok && j < n; ++j, ++done) {
+              if (does_qk) qk(j, n, done);
+              else pv(j, n, done, j == n - 1);
+            }
+            if (ok && does_qk) mma_commit(&bars->q_empty);
+          } else {
+            if (nx > 0) qk(0, n, done);
             if (nx == 0) mbar_arrive(&bars->q_empty);
-            else if (ok) mma_commit(&bars->q_empty);
-          }
-          for (int j = 0; ok && j < nx; ++j, ++done) {
-            if (j + 1 < nx) {
-              ++done;  // qk(j + 1) waits for S of tile j
-              qk(items + item_of_k(j + 1));
-              --done;
-              if (!ok) break;
-              if (j + 2 == nx) mma_commit(&bars->q_empty);
+            else if (nx == 1 && ok) mma_commit(&bars->q_empty);
+            for (int j = 0; ok && j < nx; ++j, ++done) {
+              if (j + 1 < nx) {
+                qk(j + 1, n, done + 1);
+                if (!ok) break;
+                if (j + 2 == nx) mma_commit(&bars->q_empty);
+              }
+              pv(j, n, done, j == nx - 1);
             }
-            const int it = items + item_of_v(j, n), st = it % C::kStages;
-            if (!(ok = wait_item(it))) break;
-            if (!(ok = bounded_wait(&bars->p_full[x], done & 1, abort_flag, p.status, kStatusTimeoutMma))) break;
-            tc_fence_after();
-            issue_pv(st, j > 0);
-            mma_commit(&bars->p_free[x]);
-            if (j == nx - 1) mma_commit(&bars->o_full[x]);
-            mma_commit(&bars->kv_empty[st]);
+            for (int j = nx; ok && j < n; ++j)
+              for (int kv = 0; kv < 2; ++kv) {
+                if (!(ok = wait_item(kv != 0, j, n))) break;
+                mbar_arrive(&bars->kv_empty[st]);
+              }
           }
-          for (int j = nx; ok && j < n; ++j)
-            for (int kv = 0; kv < 2; ++kv) {
-              const int it = items + (kv ? item_of_v(j, n) : item_of_k(j));
-              if (!(ok = wait_item(it))) break;
-              mbar_arrive(&bars->kv_empty[it % C::kStages]);
-            }
           items += 2 * n;
           ++segs;
         }
         // Every MMA this thread issued must complete before TMEM is released.
-        mma_commit(&bars->mma_done[x]);
+        mma_commit(&bars->mma_done[warp - C::kMmaWarp]);
         int dummy = 0;
-        bounded_wait(&bars->mma_done[x], 0, reinterpret_cast<volatile int*>(&dummy), p.status, kStatusTimeoutDrain);
+        bounded_wait(&bars->mma_done[warp - C::kMmaWarp], 0, reinterpret_cast<volatile int*>(&dummy), p.status, kStatusTimeoutDrain);
       }
       __syncwarp();
     }
@@ -723,9 +790,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
     const int row = wq * 32 + lane;
     const int row_token = row / p.hb, row_head = row % p.hb;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t s_tmem = tmem + lane_off + x * kBN;
-    const uint32_t o_tmem = tmem + lane_off + 2 * kBN + x * D;
-    const uint32_t p_tmem = tmem + lane_off + 2 * kBN + 2 * D + x * (kBN / 2);
+    const uint32_t o_tmem = tmem + lane_off + C::kOCol + x * D;
+    const uint32_t p_tmem = tmem + lane_off + C::kPCol + x * (kBN / 2);
     uint8_t* p_row = sP + x * C::kStageBytes + row * 128;
     float lam = p.scale_log2;  // of this row
     float vd = 1.f;
@@ -758,45 +824,84 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
         lam = p.scale_log2 * (p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f);
         vd = p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
       }
-      if constexpr (kConvertQ) {
-        // The row of Q, in place, to fp16 behind a power of two that brings its
-        // largest element to [1, 2): exact but for elements below 2^-14 of that one.
+      if constexpr (kReadyQ) {
+        // The row of Q, in place or to tensor memory; from bf16 to fp16 behind a power
+        // of two that brings its largest element to [1, 2): exact but for elements
+        // below 2^-14 of that one.
         ok = bounded_wait(&bars->q_full, segs & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         uint8_t* q_row = sQ + x * C::kTileBytes + row * 128;
-        uint32_t top = 0;
+        auto piece = [&](int i) {
+          return reinterpret_cast<uint4*>(q_row + (i / 8) * C::kBlockBytes + ((i ^ row) & 7) * 16);
+        };
+        float down = 1.f;
+        if constexpr (BF16) {
+          uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4*>(q_row + (i / 8) * C::kBlockBytes + ((i ^ row) & 7) * 16);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = *piece(i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7F80u, w[k] >> 16 & 0x7F80u));
+            for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7F80u, w[k] >> 16 & 0x7F80u));
+          }
+          const uint32_t e = min(max(top >> 7, 1u), 253u);
+          down = __uint_as_float((254u - e) << 23);
+          lam *= __uint_as_float(e << 23);
         }
-        const uint32_t e = min(max(top >> 7, 1u), 253u);
-        const float down = __uint_as_float((254u - e) << 23);
-        lam *= __uint_as_float(e << 23);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          uint4* at = reinterpret_cast<uint4*>(q_row + (i / 8) * C::kBlockBytes + ((i ^ row) & 7) * 16);
-          const uint4 v = *at;
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t h[4];
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t h[32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            h[k] = pack2<false>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-          *at = make_uint4(h[0], h[1], h[2], h[3]);
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = *piece(c * 8 + i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[i * 4 + k] = BF16 ? pack2<false>(__uint_as_float(w[k] << 16) * down,
+                                                 __uint_as_float(w[k] & 0xFFFF0000u) * down)
+                                  : w[k];
+            if constexpr (!C::kQInTmem) *piece(c * 8 + i) = make_uint4(h[i * 4], h[i * 4 + 1], h[i * 4 + 2], h[i * 4 + 3]);
+          }
+          if constexpr (C::kQInTmem) tmem_st32(tmem + lane_off + C::q_col() + c * 32, h);
         }
-        fence_proxy_async_smem();
+        if constexpr (C::kQInTmem) {
+          tmem_wait_st();
+          tc_fence_before();
+        } else {
+          fence_proxy_async_smem();
+        }
         mbar_arrive(&bars->q_ready[x]);
       }
       float r = -INFINITY;  // retained reference, raw score units
       float l = 0.f;
       const int nx = tile.j1 - seg.j0;
+      const bool active = __any_sync(0xffffffffu, real);
       for (int j = 0; j < nx; ++j, ++done) {
-        ok = bounded_wait(&bars->s_full[x], done & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
+        if (!active) {  // no row of this warp counts: P stays as it is
+          ok = bounded_wait(&bars->s_full[C::s_bar(x, done)], (done / C::kSBufs) & 1, abort_flag, p.status,
+                            kStatusTimeoutSoftmax);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive(&bars->s_free[C::s_bar(x, done)]);
+          if (NT == 2 && x == 0 && segs == 0 && j == 0) mbar_arrive(&bars->stagger);
+          if (j > 0) {
+            ok = bounded_wait(&bars->p_free[x], (done - 1) & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
+            ok = __all_sync(0xffffffffu, ok);
+          } else if constexpr (!C::kPInTmem) {
+            stage_free();
+          }
+          if (!ok) break;
+          mbar_arrive(&bars->p_full[x]);
+          continue;
+        }
+        const uint32_t s_tmem = tmem + lane_off + C::kSCol + C::s_bar(x, done) * kBN;
+        ok = bounded_wait(&bars->s_full[C::s_bar(x, done)], (done / C::kSBufs) & 1, abort_flag, p.status,
+                          kStatusTimeoutSoftmax);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -820,7 +925,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
 #pragma unroll
         for (int c = 0; c < kBN / 32; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
         tc_fence_before();
-        mbar_arrive(&bars->s_free[x]);
+        mbar_arrive(&bars->s_free[C::s_bar(x, done)]);
         if (NT == 2 && x == 0 && segs == 0 && j == 0) mbar_arrive(&bars->stagger);
         float* s = reinterpret_cast<float*>(u);
         float mx;
@@ -936,6 +1041,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
       const uint8_t* nan_from = bars->nan_from[segs % kSegRing];
       const int seen = real ? lim - lim0 : 0;
       if (seg.whole()) {
+        [[maybe_unused]] long long store_row = -1;
+        if constexpr (C::kDirectO) {
+          if (in_tile && t < p.S) store_row = (static_cast<long long>(seg.b) * p.H + (seg.u / p.nblk) * p.g + head) * p.S + t;
+        }
         if (tile.t0 < p.S) {
           const float inv = (!real || l == 0.f) ? 0.f : vd / l;
           stage_free();
@@ -961,25 +1070,35 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               pk[i] = pack2<BF16>(__uint_as_float(u[2 * i]) * inv, __uint_as_float(u[2 * i + 1]) * inv);
-            uint8_t* blk = p_row + (c / 2) * C::kBlockBytes;
+            if constexpr (C::kDirectO) {
+              if (store_row >= 0) {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + store_row * D + c * 32);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int ch = (c % 2) * 4 + k;
-              *reinterpret_cast<uint4*>(blk + ((ch ^ (row & 7)) << 4)) =
-                  make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+                for (int k = 0; k < 4; ++k) dst[k] = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+              }
+            } else {
+              uint8_t* blk = p_row + (c / 2) * C::kBlockBytes;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int ch = (c % 2) * 4 + k;
+                *reinterpret_cast<uint4*>(blk + ((ch ^ (row & 7)) << 4)) =
+                    make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+              }
             }
           }
           tc_fence_before();  // O_X has been read before P's arrival lets it be overwritten
-          fence_proxy_async_smem();
-          group_sync();
-          if (!ok) break;
-          if (wq == 0 && lane == 0) {
-            for (int cb = 0; cb < C::kColBlocks; ++cb)
-              tma_store_5d(&p.to, sP + x * C::kStageBytes + cb * C::kBlockBytes, cb * 64, (seg.u % p.nblk) * p.hb,
-                           seg.u / p.nblk, tile.t0, seg.b);
-            bulk_commit_group();
+          if constexpr (!C::kDirectO) {
+            fence_proxy_async_smem();
+            group_sync();
+            if (!ok) break;
+            if (wq == 0 && lane == 0) {
+              for (int cb = 0; cb < C::kColBlocks; ++cb)
+                tma_store_5d(&p.to, sP + x * C::kStageBytes + cb * C::kBlockBytes, cb * 64, (seg.u % p.nblk) * p.hb,
+                             seg.u / p.nblk, tile.t0, seg.b);
+              bulk_commit_group();
+            }
+            staged = true;
           }
-          staged = true;
           if (p.lse != nullptr && in_tile && t < p.S) {
             const float lse = !real || l == 0.f ? -INFINITY : (r * lam + __log2f(l)) * 0.69314718055994531f;
             p.lse[(static_cast<long long>(seg.b) * p.H + (seg.u / p.nblk) * p.g + head) * p.S + t] = lse;

@@ -52,6 +52,17 @@ CHUNKS = [
 ]
 
 
+# More key tiles than CTAs, so that each CTA works through several units, whole
+# and split ones, in both block sizes.
+LONG = [
+    # dtype, H, Hkv, d, page, S
+    (torch.bfloat16, 8, 4, 128, 64, 3),
+    (torch.float16, 4, 2, 64, 16, 9),
+    (torch.bfloat16, 8, 4, 128, 128, 90),
+    (torch.float16, 8, 4, 64, 32, 100),
+]
+
+
 @pytest.mark.parametrize("bits", [16, 4])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("cfg", CHUNKS)
@@ -65,3 +76,21 @@ def test_chunk(cfg, causal, bits):
     _ok(pool, q, table, lens, news or [S] * len(lens), o, lse, causal, scale)
     again = _forward(pool, q, table, lens, news, causal=causal)
     assert _same_bits(again[0], o) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("cfg", LONG)
+def test_runs_of_several_units(cfg, bits):
+    dtype, H, Hkv, d, page, S = cfg
+    g = torch.Generator().manual_seed(32)
+    lens = torch.randint(100, 1500, (36,), generator=g).tolist()
+    lens[7], lens[20], lens[21] = 0, 3, 6000
+    news = [min(n, int(m)) for n, m in zip(lens, torch.randint(0, S + 1, (36,), generator=g))]
+    pool, table, g = _make(bits, dtype, Hkv, d, page, lens, 33)
+    q = torch.randn(len(lens), H, S, d, generator=g).to(dtype).cuda()
+    o, lse = _forward(pool, q, table, lens, news)
+    assert gb.gbattn_device_status() == 0
+    _ok(pool, q, table, lens, news, o, lse, True, 1 / math.sqrt(d))
+    for _ in range(5):
+        again = _forward(pool, q, table, lens, news)
+        assert _same_bits(again[0], o) and torch.equal(again[1], lse)
