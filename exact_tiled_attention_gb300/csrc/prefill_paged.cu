@@ -62,18 +62,6 @@ struct Cfg {
   // core's rate, two at once keep it busy (two tiles have two chains each).
   static constexpr int kSBufs = NT == 1 ? 2 : 1;
   static constexpr int kSCol = 0, kOCol = 2 * kBN, kPCol = kOCol + NT * D;
-  struct Place {
-    int st, round;
-  };
-  // The place of K or V of a key tile: load number `item`, tile number `tile` of the CTA.
-  __device__ static __forceinline__ Place place(bool is_v, int item, int tile) {
-    if constexpr (NT == 2) {
-      return {item % kStages, item / kStages};
-    } else {
-      if (is_v) return {kKStages + tile % (kStages - kKStages), tile / (kStages - kKStages)};
-      return {tile % kKStages, tile / kKStages};
-    }
-  }
   // Where tile x's S number d goes, and its barriers.
   __device__ static __forceinline__ int s_bar(int x, int d) { return NT == 1 ? d & 1 : x; }
   __device__ static constexpr int q_col() { return kPCol + kBN / 2; }
@@ -89,11 +77,15 @@ struct Cfg {
   static constexpr int kStages = FP4 ? (NT == 2 ? (D == 128 ? 2 : 6) : (D == 128 ? 4 : 8))
                                      : (NT == 2 ? (D == 128 ? 3 : 8) : (D == 128 ? 5 : 12));
   static constexpr int kRawStages = !FP4 ? 0 : NT == 2 ? (D == 128 ? 3 : 8) : (D == 128 ? 6 : 12);
-  // With two tiles every issuer takes every key and value tile, so all places form one
-  // ring.  With one, the issuers take keys and values apart, each at its own pace: a
-  // ring each (a wait tells only even from odd rounds of a place, so whoever waits has
-  // to follow all of its rounds).
-  static constexpr int kKStages = NT == 2 ? kStages : kStages / 2;
+  // With two tiles over 16 bits everyone takes every key and value tile in the order of
+  // their loads, so all places form one ring.  Otherwise keys and values have issuers
+  // or converting warps of their own, each at its own pace, and a ring each: a wait
+  // tells only even from odd rounds of a place, so whoever waits has to follow all of
+  // its rounds.
+  static constexpr bool kOneRing = NT == 2 && !FP4;
+  static constexpr int kKStages = kOneRing ? kStages : kStages / 2;   // K's places, [0, kKStages)
+  static constexpr int kRawKStages = FP4 ? (kRawStages + 1) / 2 : 0;  // the same of codes and factors
+  static_assert(kRawKStages <= 12 && kRawStages <= 12 && kStages <= 12, "barriers");
   static constexpr int kRawBytes = kBN * (D / 2 + D / 16);  // codes, then factors
   static constexpr int kQOff = 0;
   static constexpr int kPOff = NT * kTileBytes;
@@ -158,8 +150,7 @@ struct __align__(8) Barriers {
   long long scan[16];
   uint32_t tmem_base;
   int abort_flag;
-  int last_round[12];      // of the loader's places, -1 before the first
-  uint8_t bad[kTileRing];          // 16-key blocks of a tile that have no page
+  uint8_t bad[2][kTileRing];       // 16-key blocks of a tile (of K, of V) that have no page
   uint8_t nan_any[kSegRing];
   uint8_t nan_from[kSegRing][128]; // column's first non-finite key behind the first row's last key, - 1
 };
@@ -267,6 +258,22 @@ __device__ __forceinline__ int first_masked(const Params& p, const Seg& seg, int
   return (lim0 + 1) / kBN;
 }
 
+// The places of a ring in turn: the current one, and the parity of its round.
+struct Ring {
+  int st;
+  uint32_t phase;
+  int first, end;
+  bool fresh;  // the ring's first round: nothing to wait for before a place is filled
+  __device__ __forceinline__ Ring(int first_, int end_) : st(first_), phase(0), first(first_), end(end_), fresh(true) {}
+  __device__ __forceinline__ void next() {
+    if (++st == end) {
+      st = first;
+      phase ^= 1u;
+      fresh = false;
+    }
+  }
+};
+
 // Position of K_j / V_j among a segment's loads K_0, K_1, V_0, K_2, V_1, ..,
 // K_{n-1}, V_{n-2}, V_{n-1}.
 __device__ __forceinline__ int item_of_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
@@ -367,13 +374,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, NT);
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&bars->kv_full[s], FP4 ? C::kConvertWarps : 1);
+      mbar_init(&bars->kv_full[s], FP4 ? C::kConvertWarps / 2 : 1);
       mbar_init(&bars->kv_empty[s], NT);
       if (!FP4) mbar_init(&bars->raw[s], 1);
     }
     for (int s = 0; s < C::kRawStages; ++s) {
       mbar_init(&bars->raw[s], 1);
-      mbar_init(&bars->raw_empty[s], C::kConvertWarps);
+      mbar_init(&bars->raw_empty[s], C::kConvertWarps / 2);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->q_ready[x], kBM);
@@ -412,87 +419,95 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
 
   if (FP4 && warp >= C::kConvertWarp) {
     // ================================================================ conversion of 4 bits
-    // A thread takes whole rows (two threads a row where there are 8 warps), 16 bytes
-    // of codes at a time: 32 elements, 4 pieces of 16 bytes of the tile.  At d = 128
-    // lanes of one eighth of a warp take their row's pieces in different orders, so
-    // that neither reads (rows 64 bytes apart) nor writes meet in a bank.
+    // One half of the warps takes K, the other V, so that two conversions are under way
+    // at once.  A thread takes whole rows, 16 bytes of codes at a time: 32 elements, 4
+    // pieces of 16 bytes of the tile.  At d = 128 lanes of one eighth of a warp take
+    // their row's pieces in different orders, so that neither reads (rows 64 bytes
+    // apart) nor writes meet in a bank.
     if constexpr (FP4) {
       regs_dec<C::kConvertRegs>();
-      constexpr int kPieces = D / 32, kTeams = C::kConvertWarps / 4, kMine = kPieces / kTeams;
-      const int row = threadIdx.x % kBN, team = (warp - C::kConvertWarp) / 4;
-      int items = 0, tiles = 0;
+      constexpr int kPieces = D / 32;
+      constexpr int kTeam = C::kConvertWarps / 2 * 32, kRowsEach = kBN / kTeam;
+      const bool is_v = warp - C::kConvertWarp >= C::kConvertWarps / 2;
+      const int row0 = threadIdx.x % kTeam;
+      // Within a row: where its pieces' first and further 16 bytes go (row % 8 is the
+      // same for all rows of a thread).
+      const uint32_t r7 = row0 & 7;
+      const uint32_t half = (r7 & 4) << 4, in0 = (r7 & 3) << 4;
+      Ring raw(is_v ? C::kRawKStages : 0, is_v ? C::kRawStages : C::kRawKStages);
+      Ring at(is_v ? C::kKStages : 0, is_v ? C::kStages : C::kKStages);
+      int tile = 0;
       bool ok = true;
       while (ok && cur.next(p, seg)) {
-        const int n = seg.j1 - seg.j0;
-        for (int i = 0; i < 2 * n; ++i, ++items) {
-          const int rs = items % C::kRawStages;
-          // K_0, K_1, V_0, K_2, ..
-          const bool is_v = i == 2 * n - 1 || (i > 0 && i % 2 == 0);
-          const int j = i == 0 ? 0 : i == 2 * n - 1 ? n - 1 : (i & 1) ? (i + 1) / 2 : i / 2 - 1;
-          const typename C::Place at = C::place(is_v, items, tiles + j);
-          const int st = at.st;
-          ok = bounded_wait(&bars->raw[rs], (items / C::kRawStages) & 1, abort_flag, p.status, kStatusTimeoutLoad);
-          if (ok && at.round > 0)
-            ok = bounded_wait(&bars->kv_empty[st], (at.round - 1) & 1, abort_flag, p.status, kStatusTimeoutLoad);
+        int rows = seg.s.n - seg.j0 * kBN;  // of the tile that are there
+        for (int j = seg.j0; j < seg.j1; ++j, ++tile, rows -= kBN, raw.next(), at.next()) {
+          ok = bounded_wait(&bars->raw[raw.st], raw.phase, abort_flag, p.status, kStatusTimeoutLoad);
+          if (ok && !at.fresh)
+            ok = bounded_wait(&bars->kv_empty[at.st], at.phase ^ 1u, abort_flag, p.status, kStatusTimeoutLoad);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint8_t* src = smem + C::kRawOff + rs * C::kRawBytes;
-          // Rows that are not there are zeros.
-          const bool there = (seg.j0 + j) * kBN + row < seg.s.n &&
-                             !(bars->bad[(tiles + j) % kTileRing] >> (row / 16) & 1u);
-          uint32_t f[D / 64];
-          if constexpr (D == 128) {
-            const uint2 v = *reinterpret_cast<const uint2*>(src + kBN * (D / 2) + row * (D / 16));
-            f[0] = there ? v.x : 0u, f[1] = there ? v.y : 0u;
-          } else {
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(src + kBN * (D / 2) + row * (D / 16));
-            f[0] = there ? v : 0u;
-          }
-          uint8_t* dst = sRing + st * C::kTileBytes + row * 128;
+          const uint8_t* src = smem + C::kRawOff + raw.st * C::kRawBytes;
+          const uint32_t bad = bars->bad[is_v][tile % kTileRing];
 #pragma unroll
-          for (int q = 0; q < kMine; ++q) {
-            const int piece = D == 128 ? ((row >> 1) + q * kTeams + team) % kPieces : q * kTeams + team;
-            const uint4 c = *reinterpret_cast<const uint4*>(src + row * (D / 2) + piece * 16);
-            const uint32_t fw = D == 128 && piece >= 2 ? f[D / 64 - 1] : f[0];
-            const uint32_t two = e4m3x2_to_f16(piece & 1 ? fw >> 16 : fw);
-            const uint32_t f0 = __byte_perm(two, two, 0x1010), f1 = __byte_perm(two, two, 0x3232);
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+          for (int rr = 0; rr < kRowsEach; ++rr) {
+            const int row = row0 + rr * kTeam;
+            // Rows that are not there are zeros.
+            const bool there = row < rows && !(bad >> (row / 16) & 1u);
+            uint32_t f[D / 64];
+            if constexpr (D == 128) {
+              const uint2 v = *reinterpret_cast<const uint2*>(src + kBN * (D / 2) + row * (D / 16));
+              f[0] = there ? v.x : 0u, f[1] = there ? v.y : 0u;
+            } else {
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(src + kBN * (D / 2) + row * (D / 16));
+              f[0] = there ? v : 0u;
+            }
+            uint8_t* dst = sRing + at.st * C::kTileBytes + row * 128;
+            uint4 codes[kPieces];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t h[4];
-              e2m1x8_to_f16(w[k], k < 2 ? f0 : f1, h);
-              const int chunk = (piece & 1) * 4 + k;
-              *reinterpret_cast<uint4*>(dst + (piece >> 1) * C::kBlockBytes + ((chunk ^ (row & 7)) << 4)) =
-                  make_uint4(h[0], h[1], h[2], h[3]);
+            for (int q = 0; q < kPieces; ++q) {
+              const int piece = D == 128 ? ((row0 >> 1) + q) % kPieces : q;
+              codes[q] = *reinterpret_cast<const uint4*>(src + row * (D / 2) + piece * 16);
+            }
+#pragma unroll
+            for (int q = 0; q < kPieces; ++q) {
+              const uint32_t piece = D == 128 ? ((row0 >> 1) + q) % kPieces : q;
+              const uint32_t fw = D == 128 && piece >= 2 ? f[D / 64 - 1] : f[0];
+              const uint32_t two = e4m3x2_to_f16(piece & 1 ? fw >> 16 : fw);
+              const uint32_t f0 = __byte_perm(two, two, 0x1010), f1 = __byte_perm(two, two, 0x3232);
+              const uint32_t w[4] = {codes[q].x, codes[q].y, codes[q].z, codes[q].w};
+              uint8_t* to = dst + (piece >> 1) * C::kBlockBytes + ((piece & 1) * 64 ^ half);
+#pragma unroll
+              for (uint32_t k = 0; k < 4; ++k) {
+                uint32_t h[4];
+                e2m1x8_to_f16(w[k], k < 2 ? f0 : f1, h);
+                *reinterpret_cast<uint4*>(to + (k * 16 ^ in0)) = make_uint4(h[0], h[1], h[2], h[3]);
+              }
             }
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&bars->raw_empty[rs]);
-            mbar_arrive(&bars->kv_full[st]);
+            mbar_arrive(&bars->raw_empty[raw.st]);
+            mbar_arrive(&bars->kv_full[at.st]);
           }
         }
-        tiles += n;
       }
     }
   } else if (warp >= C::kMmaWarp) {
     if constexpr (C::kSplit) regs_dec<C::kControlRegs>();
-    if (warp == C::kLoadWarp) {
+    if (warp == C::kLoadWarp || (FP4 && warp == C::kGuardWarp)) {
       // ================================================================ loader
-      // Lane = (box, column block) of a key tile: its page's rows.
+      // Lane = (box, column block) of a key tile: its page's rows.  Over 4 bits one warp
+      // loads keys (and queries), another values; lanes of the first half copy codes,
+      // those of the second factors (a page's rows of one head lie one behind another).
+      const bool loads_v = FP4 && warp == C::kGuardWarp;
       const int boxes = kBN / p.box_rows;
       const int box = lane % boxes, cb = lane / boxes;
-      const bool loads = cb < C::kColBlocks;
       const int box_shift = 31 - __clz(p.box_rows);
-      constexpr int kStages = FP4 ? C::kRawStages : C::kStages;
-      int* const last_round = bars->last_round;
-      if (lane == 0)
-        for (int st = 0; st < kStages; ++st) last_round[st] = -1;
-      uint64_t* const empty = FP4 ? bars->raw_empty : bars->kv_empty;
       const uint64_t keep = policy_evict_last(), once = policy_evict_first();
       const int missing = p.n_pages * p.Hkv;  // a coordinate outside: zeros
-      int items = 0, segs = 0, tile0 = 0;
+      const int in_page = (1 << p.page_shift) - 1;
+      int segs = 0, tile = 0;
       bool ok = true;
       // Pages are looked up for 32 boxes at a time, a window ahead of their use: lane l
       // has box l % boxes of the window's tile l / boxes (-1 behind the sequence).
@@ -501,10 +516,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
         const int key = (seg.j0 + w * per_window + lane / boxes) * kBN + (box << box_shift);
         return key < seg.s.n ? p.page_table[static_cast<long long>(seg.b) * p.max_pages + (key >> p.page_shift)] : -1;
       };
-      while (ok && cur.next(p, seg)) {
-        const int kvh = seg.u / p.nblk, h0 = (seg.u % p.nblk) * p.hb;
-        int lim0;
-        const int jm = first_masked<NT>(p, seg, lim0);
+      // Notes the 16-key blocks without a page of tile number `at`: they are left out.
+      auto note_missing = [&](bool is_v, int at, uint32_t absent) {
+        uint32_t bad = 0;
+        if (absent != 0) {
+          if (lane == 0) report_index(p.status);
+          for (int i = 0; i < 8; ++i) bad |= ((absent >> (i * 16 >> box_shift)) & 1u) << i;
+        }
+        if (lane == 0) bars->bad[is_v][at % kTileRing] = static_cast<uint8_t>(bad);
+      };
+      auto load_q = [&]() {
         if (lane == 0) {
           ok = segs == 0 || bounded_wait(&bars->q_empty, (segs - 1) & 1, abort_flag, p.status, kStatusTimeoutLoad);
           if (ok) {
@@ -514,91 +535,114 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
             mbar_arrive_expect_tx(&bars->q_full, real * C::kColBlocks * p.hb * p.tq_tokens * 128);
             for (int x = 0; x < real; ++x)
               for (int c = 0; c < C::kColBlocks; ++c)
-                tma_load_5d(sQ + x * C::kTileBytes + c * C::kBlockBytes, &p.tq, &bars->q_full, c * 64, h0, kvh,
-                            t0 + x * p.tq_tokens, seg.b, once);
+                tma_load_5d(sQ + x * C::kTileBytes + c * C::kBlockBytes, &p.tq, &bars->q_full, c * 64,
+                            (seg.u % p.nblk) * p.hb, seg.u / p.nblk, t0 + x * p.tq_tokens, seg.b, once);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
         ++segs;
-        auto issue = [&](bool is_v, int j, int page) {
-          const typename C::Place at = FP4 ? typename C::Place{items % C::kRawStages, items / C::kRawStages}
-                                           : C::place(is_v, items, tile0 + j - seg.j0);
-          const int st = at.st;
-          if (lane == 0 && at.round > 0)
-            ok = bounded_wait(&empty[st], (at.round - 1) & 1, abort_flag, p.status, kStatusTimeoutLoad);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) return;
-          const int key = j * kBN + (box << box_shift);
-          const bool inside = key < seg.s.n;
-          const bool found = inside && page >= 0 && page < p.n_pages;
-          if (!is_v) {
-            // Missing pages, by blocks of 16 keys: the softmax leaves them out.
-            uint32_t bad = __ballot_sync(0xffffffffu, cb == 0 && inside && !found);
-            if (bad != 0) {
-              if (lane == 0) report_index(p.status);
-              uint32_t wide = 0;
-              for (int i = 0; i < 8; ++i) wide |= ((bad >> (i * 16 >> box_shift)) & 1u) << i;
-              bad = wide;
-            }
-            if (lane == 0) bars->bad[(tile0 + j - seg.j0) % kTileRing] = static_cast<uint8_t>(bad);
+      };
+      if constexpr (FP4) {
+        const int row_bytes = cb == 0 ? D / 2 : D / 16;
+        const uint32_t bytes = static_cast<uint32_t>(row_bytes << box_shift);
+        const uint8_t* const pool = cb == 0 ? p.codes[loads_v] : p.factors[loads_v];
+        uint8_t* const dst = smem + C::kRawOff + (cb == 0 ? 0 : kBN * (D / 2)) + box * bytes;
+        Ring at(loads_v ? C::kRawKStages : 0, loads_v ? C::kRawStages : C::kRawKStages);
+        int filled = 0;
+        while (ok && cur.next(p, seg)) {
+          const int kvh = seg.u / p.nblk;
+          if (!loads_v) {
+            load_q();
+            if (!ok) break;
           }
-          if constexpr (FP4) {
-            // Pages that are there: lanes of the first half copy codes, the others
-            // factors (a page's rows of one head lie one behind another).
+          int now = lookup(0), next = lookup(1), in = 0, window = 1;
+          int key = seg.j0 * kBN + (box << box_shift);
+          for (int j = seg.j0; j < seg.j1; ++j, ++tile, key += kBN, at.next()) {
+            const int page = __shfl_sync(0xffffffffu, now, in * boxes + box);
+            if (++in == per_window) {
+              in = 0;
+              now = next;
+              next = lookup(++window);
+            }
+            const bool inside = key < seg.s.n;
+            const bool found = inside && page >= 0 && page < p.n_pages;
             const uint32_t copied = __ballot_sync(0xffffffffu, cb == 0 && found);
-            if (lane == 0)
-              mbar_arrive_expect_tx(&bars->raw[st], (__popc(copied) << box_shift) * (D / 2 + D / 16));
+            note_missing(loads_v, tile, __ballot_sync(0xffffffffu, cb == 0 && inside && !found));
+            const uint8_t* src =
+                pool + (((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) + (key & in_page)) * row_bytes;
+            if (!at.fresh) ok = bounded_wait(&bars->raw_empty[at.st], at.phase ^ 1u, abort_flag, p.status, kStatusTimeoutLoad);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bars->raw[at.st], (__popc(copied) << box_shift) * (D / 2 + D / 16));
             __syncwarp();
-            if (found && cb < 2) {
-              const long long row = ((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) +
-                                   (key & ((1 << p.page_shift) - 1));
-              const int row_bytes = cb == 0 ? D / 2 : D / 16;
-              bulk_load(smem + C::kRawOff + st * C::kRawBytes + (cb == 0 ? 0 : kBN * (D / 2)) +
-                            (box << box_shift) * row_bytes,
-                        (cb == 0 ? p.codes[is_v] : p.factors[is_v]) + row * row_bytes,
-                        static_cast<uint32_t>(row_bytes << box_shift), &bars->raw[st], keep);
-            }
-            if (lane == 0) last_round[st] = at.round;
-            ++items;
-            return;
+            if (found && cb < 2) bulk_load(dst + at.st * C::kRawBytes, src, bytes, &bars->raw[at.st], keep);
+            ++filled;
           }
-          const bool guarded = is_v && j >= jm;
-          uint64_t* bar = guarded ? &bars->raw[st] : &bars->kv_full[st];
-          if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
-          __syncwarp();
-          if (loads) {
-            const int z = found ? page * p.Hkv + kvh : missing;
-            tma_load_3d(sRing + st * C::kTileBytes + cb * C::kBlockBytes + (box << box_shift) * 128,
-                        is_v ? &p.tv : &p.tk, bar, cb * 64, found ? key & ((1 << p.page_shift) - 1) : 0, z, keep);
-          }
-          if (lane == 0) last_round[st] = at.round;
-          ++items;
-        };
-        const int n = seg.j1 - seg.j0;
-        int now = lookup(0), next = lookup(1);  // windows of V's tile and the one behind it
-        issue(false, seg.j0, __shfl_sync(0xffffffffu, now, box));
-        for (int t = 0, in = 0; ok && t < n; ++t) {  // `in`: V's tile in its window
-          const int page_v = __shfl_sync(0xffffffffu, now, in * boxes + box);
-          if (++in == per_window) {
-            in = 0;
-            now = next;
-            next = lookup(t / per_window + 2);
-          }
-          if (t + 1 < n) issue(false, seg.j0 + t + 1, __shfl_sync(0xffffffffu, now, in * boxes + box));
-          if (ok) issue(true, seg.j0 + t, page_v);
         }
-        tile0 += n;
-      }
-      // Every copy must have landed before the CTA ends.
-      if (lane == 0) {
-        int dummy = 0;
-        volatile int* ignore = reinterpret_cast<volatile int*>(&dummy);
-        if (segs > 0) bounded_wait(&bars->q_full, (segs - 1) & 1, ignore, p.status, kStatusTimeoutDrain);
-        uint64_t* const full = FP4 ? bars->raw : bars->kv_full;
-        for (int st = 0; st < kStages; ++st)
-          if (last_round[st] >= 0)
-            bounded_wait(&full[st], last_round[st] & 1, ignore, p.status, kStatusTimeoutDrain);
+        // Every copy must have landed before the CTA ends.
+        if (lane == 0) {
+          int dummy = 0;
+          volatile int* ignore = reinterpret_cast<volatile int*>(&dummy);
+          if (segs > 0) bounded_wait(&bars->q_full, (segs - 1) & 1, ignore, p.status, kStatusTimeoutDrain);
+          const int places = at.end - at.first;
+          for (int i = max(0, filled - places); i < filled; ++i)
+            bounded_wait(&bars->raw[at.first + i % places], (i / places) & 1, ignore, p.status, kStatusTimeoutDrain);
+        }
+      } else {
+        const bool loads = cb < C::kColBlocks;
+        // One ring in the order of the loads, or one for K and one for V.
+        Ring ring_k(0, C::kKStages), ring_v(C::kKStages, C::kStages);
+        int filled[2] = {0, 0};
+        while (ok && cur.next(p, seg)) {
+          const int kvh = seg.u / p.nblk;
+          int lim0;
+          const int jm = first_masked<NT>(p, seg, lim0);
+          load_q();
+          if (!ok) break;
+          auto issue = [&](bool is_v, int j, int page) {
+            Ring& at = is_v && !C::kOneRing ? ring_v : ring_k;
+            const int key = j * kBN + (box << box_shift);
+            const bool inside = key < seg.s.n;
+            const bool found = inside && page >= 0 && page < p.n_pages;
+            if (!is_v) note_missing(false, tile++, __ballot_sync(0xffffffffu, cb == 0 && inside && !found));
+            if (!at.fresh) ok = bounded_wait(&bars->kv_empty[at.st], at.phase ^ 1u, abort_flag, p.status, kStatusTimeoutLoad);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            uint64_t* bar = is_v && j >= jm ? &bars->raw[at.st] : &bars->kv_full[at.st];
+            if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
+            __syncwarp();
+            if (loads)
+              tma_load_3d(sRing + at.st * C::kTileBytes + cb * C::kBlockBytes + (box << box_shift) * 128,
+                          is_v ? &p.tv : &p.tk, bar, cb * 64, found ? key & in_page : 0,
+                          found ? page * p.Hkv + kvh : missing, keep);
+            at.next();
+            ++filled[is_v && !C::kOneRing];
+          };
+          const int n = seg.j1 - seg.j0;
+          int now = lookup(0), next = lookup(1);  // windows of V's tile and the one behind it
+          issue(false, seg.j0, __shfl_sync(0xffffffffu, now, box));
+          for (int t = 0, in = 0; ok && t < n; ++t) {  // `in`: V's tile in its window
+            const int page_v = __shfl_sync(0xffffffffu, now, in * boxes + box);
+            if (++in == per_window) {
+              in = 0;
+              now = next;
+              next = lookup(t / per_window + 2);
+            }
+            if (t + 1 < n) issue(false, seg.j0 + t + 1, __shfl_sync(0xffffffffu, now, in * boxes + box));
+            if (ok) issue(true, seg.j0 + t, page_v);
+          }
+        }
+        // Every copy must have landed before the CTA ends.
+        if (lane == 0) {
+          int dummy = 0;
+          volatile int* ignore = reinterpret_cast<volatile int*>(&dummy);
+          if (segs > 0) bounded_wait(&bars->q_full, (segs - 1) & 1, ignore, p.status, kStatusTimeoutDrain);
+          for (int r = 0; r < (C::kOneRing ? 1 : 2); ++r) {
+            const int first = r ? C::kKStages : 0, places = (r ? C::kStages : C::kKStages) - first;
+            for (int i = max(0, filled[r] - places); i < filled[r]; ++i)
+              bounded_wait(&bars->kv_full[first + i % places], (i / places) & 1, ignore, p.status, kStatusTimeoutDrain);
+          }
+        }
       }
       __syncwarp();
     } else if (!FP4 && warp == C::kGuardWarp) {
@@ -618,7 +662,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
 #pragma unroll
         for (int c = 0; c < kCols; ++c) first[c] = 255u;
         for (int j = jm; j < seg.j1; ++j) {
-          const int st = C::place(true, items + item_of_v(j - seg.j0, n), items / 2 + j - seg.j0).st;
+          const int st = C::kOneRing
+                             ? (items + item_of_v(j - seg.j0, n)) % C::kStages
+                             : C::kKStages + (items / 2 + j - seg.j0) % (C::kOneRing ? 1 : C::kStages - C::kKStages);
           ok = bounded_wait(&bars->raw[st], (raw_phase >> st) & 1, abort_flag, p.status, kStatusTimeoutMma);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -705,12 +751,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
         int done = 0;  // key tiles of this row tile so far
         bool ok = true;
         int st = 0;  // place of the last item waited for
-        // K or V of the segment's key tile j.
+        Ring ring_k(0, C::kKStages), ring_v(C::kKStages, C::kStages);
+        // K or V of the segment's key tile j, all in turn.
         auto wait_item = [&](bool is_v, int j, int n) {
-          const typename C::Place at =
-              C::place(is_v, items + (is_v ? item_of_v(j, n) : item_of_k(j)), items / 2 + j);
-          st = at.st;
-          return bounded_wait(&bars->kv_full[st], at.round & 1, abort_flag, p.status, kStatusTimeoutMma);
+          uint32_t phase;
+          if constexpr (C::kOneRing) {
+            const int item = items + (is_v ? item_of_v(j, n) : item_of_k(j));
+            st = item % C::kStages, phase = (item / C::kStages) & 1;
+          } else {
+            Ring& r = is_v ? ring_v : ring_k;
+            st = r.st, phase = r.phase;
+            r.next();
+          }
+          return bounded_wait(&bars->kv_full[st], phase, abort_flag, p.status, kStatusTimeoutMma);
         };
         // S of the tile that is number `d` of this row tile's.
         auto qk = [&](int j, int n, int d) {
@@ -908,7 +961,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
         }
         tc_fence_after();
         const int k0 = (seg.j0 + j) * kBN;
-        const uint32_t bad = bars->bad[(tiles + j) % kTileRing];
+        const uint32_t bad = bars->bad[0][(tiles + j) % kTileRing];
         const bool masked = k0 + kBN - 1 > tile.lim_min || bad != 0;
         uint32_t u[kBN];
         float mq[kBN / 32];

@@ -93,4 +93,5 @@ def test_runs_of_several_units(cfg, bits):
     _ok(pool, q, table, lens, news, o, lse, True, 1 / math.sqrt(d))
     for _ in range(5):
         again = _forward(pool, q, table, lens, news)
+        assert gb.gbattn_device_status() == 0
         assert _same_bits(again[0], o) and torch.equal(again[1], lse)
