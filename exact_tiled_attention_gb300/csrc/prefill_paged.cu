@@ -374,13 +374,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, NT);
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&bars->kv_full[s], FP4 ? C::kConvertWarps / 2 : 1);
+      mbar_init(&bars->kv_full[s], FP4 ? 4 : 1);  // (the converting warps of a tile)
       mbar_init(&bars->kv_empty[s], NT);
       if (!FP4) mbar_init(&bars->raw[s], 1);
     }
     for (int s = 0; s < C::kRawStages; ++s) {
       mbar_init(&bars->raw[s], 1);
-      mbar_init(&bars->raw_empty[s], C::kConvertWarps / 2);
+      mbar_init(&bars->raw_empty[s], 4);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->q_ready[x], kBM);
@@ -419,69 +419,66 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
 
   if (FP4 && warp >= C::kConvertWarp) {
     // ================================================================ conversion of 4 bits
-    // One half of the warps takes K, the other V, so that two conversions are under way
-    // at once.  A thread takes whole rows, 16 bytes of codes at a time: 32 elements, 4
-    // pieces of 16 bytes of the tile.  At d = 128 lanes of one eighth of a warp take
-    // their row's pieces in different orders, so that neither reads (rows 64 bytes
-    // apart) nor writes meet in a bank.
+    // A thread takes whole rows, 16 bytes of codes at a time: 32 elements, 4 pieces of
+    // 16 bytes of the tile.  At d = 128 lanes of one eighth of a warp take their row's
+    // pieces in different orders, so that neither reads (rows 64 bytes apart) nor writes
+    // meet in a bank.  With one tile one half of the warps takes K, the other V, so that
+    // two conversions are under way at once; with two tiles all four warps take both, in
+    // the order of the loads: K's and V's one place each come free at different times.
     if constexpr (FP4) {
       regs_dec<C::kConvertRegs>();
       constexpr int kPieces = D / 32;
-      constexpr int kTeam = C::kConvertWarps / 2 * 32, kRowsEach = kBN / kTeam;
-      const bool is_v = warp - C::kConvertWarp >= C::kConvertWarps / 2;
-      const int row0 = threadIdx.x % kTeam;
-      // Within a row: where its pieces' first and further 16 bytes go (row % 8 is the
-      // same for all rows of a thread).
-      const uint32_t r7 = row0 & 7;
-      const uint32_t half = (r7 & 4) << 4, in0 = (r7 & 3) << 4;
-      Ring raw(is_v ? C::kRawKStages : 0, is_v ? C::kRawStages : C::kRawKStages);
-      Ring at(is_v ? C::kKStages : 0, is_v ? C::kStages : C::kKStages);
-      int tile = 0;
+      const int team = NT == 2 ? 0 : (warp - C::kConvertWarp) / 4;  // NT = 1: V's warps
+      const int row = threadIdx.x % kBN;
+      // Within a row: where its pieces' first and further 16 bytes go.
+      const uint32_t half = (row & 4) << 4, in0 = (row & 3) << 4;
+      Ring raws[2] = {Ring(0, C::kRawKStages), Ring(C::kRawKStages, C::kRawStages)};
+      Ring ats[2] = {Ring(0, C::kKStages), Ring(C::kKStages, C::kStages)};
+      int tile0 = 0;
       bool ok = true;
       while (ok && cur.next(p, seg)) {
-        int rows = seg.s.n - seg.j0 * kBN;  // of the tile that are there
-        for (int j = seg.j0; j < seg.j1; ++j, ++tile, rows -= kBN, raw.next(), at.next()) {
+        const int n = seg.j1 - seg.j0;
+        for (int i = 0; i < NT * n; ++i) {
+          const bool is_v = NT == 2 ? i == 2 * n - 1 || (i > 0 && i % 2 == 0) : team == 1;
+          const int j = NT == 1 ? i : i == 0 ? 0 : i == 2 * n - 1 ? n - 1 : (i & 1) ? (i + 1) / 2 : i / 2 - 1;
+          Ring raw = is_v ? raws[1] : raws[0], at = is_v ? ats[1] : ats[0];
           ok = bounded_wait(&bars->raw[raw.st], raw.phase, abort_flag, p.status, kStatusTimeoutLoad);
           if (ok && !at.fresh)
             ok = bounded_wait(&bars->kv_empty[at.st], at.phase ^ 1u, abort_flag, p.status, kStatusTimeoutLoad);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint8_t* src = smem + C::kRawOff + raw.st * C::kRawBytes;
-          const uint32_t bad = bars->bad[is_v][tile % kTileRing];
+          // Rows that are not there are zeros.
+          const bool there = (seg.j0 + j) * kBN + row < seg.s.n &&
+                             !(bars->bad[is_v][(tile0 + j) % kTileRing] >> (row / 16) & 1u);
+          uint32_t f[D / 64];
+          if constexpr (D == 128) {
+            const uint2 v = *reinterpret_cast<const uint2*>(src + kBN * (D / 2) + row * (D / 16));
+            f[0] = there ? v.x : 0u, f[1] = there ? v.y : 0u;
+          } else {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(src + kBN * (D / 2) + row * (D / 16));
+            f[0] = there ? v : 0u;
+          }
+          uint8_t* dst = sRing + at.st * C::kTileBytes + row * 128;
+          uint4 codes[kPieces];
 #pragma unroll
-          for (int rr = 0; rr < kRowsEach; ++rr) {
-            const int row = row0 + rr * kTeam;
-            // Rows that are not there are zeros.
-            const bool there = row < rows && !(bad >> (row / 16) & 1u);
-            uint32_t f[D / 64];
-            if constexpr (D == 128) {
-              const uint2 v = *reinterpret_cast<const uint2*>(src + kBN * (D / 2) + row * (D / 16));
-              f[0] = there ? v.x : 0u, f[1] = there ? v.y : 0u;
-            } else {
-              const uint32_t v = *reinterpret_cast<const uint32_t*>(src + kBN * (D / 2) + row * (D / 16));
-              f[0] = there ? v : 0u;
-            }
-            uint8_t* dst = sRing + at.st * C::kTileBytes + row * 128;
-            uint4 codes[kPieces];
+          for (int q = 0; q < kPieces; ++q) {
+            const int piece = D == 128 ? ((row >> 1) + q) % kPieces : q;
+            codes[q] = *reinterpret_cast<const uint4*>(src + row * (D / 2) + piece * 16);
+          }
 #pragma unroll
-            for (int q = 0; q < kPieces; ++q) {
-              const int piece = D == 128 ? ((row0 >> 1) + q) % kPieces : q;
-              codes[q] = *reinterpret_cast<const uint4*>(src + row * (D / 2) + piece * 16);
-            }
+          for (int q = 0; q < kPieces; ++q) {
+            const uint32_t piece = D == 128 ? ((row >> 1) + q) % kPieces : q;
+            const uint32_t fw = D == 128 && piece >= 2 ? f[D / 64 - 1] : f[0];
+            const uint32_t two = e4m3x2_to_f16(piece & 1 ? fw >> 16 : fw);
+            const uint32_t f0 = __byte_perm(two, two, 0x1010), f1 = __byte_perm(two, two, 0x3232);
+            const uint32_t w[4] = {codes[q].x, codes[q].y, codes[q].z, codes[q].w};
+            uint8_t* to = dst + (piece >> 1) * C::kBlockBytes + ((piece & 1) * 64 ^ half);
 #pragma unroll
-            for (int q = 0; q < kPieces; ++q) {
-              const uint32_t piece = D == 128 ? ((row0 >> 1) + q) % kPieces : q;
-              const uint32_t fw = D == 128 && piece >= 2 ? f[D / 64 - 1] : f[0];
-              const uint32_t two = e4m3x2_to_f16(piece & 1 ? fw >> 16 : fw);
-              const uint32_t f0 = __byte_perm(two, two, 0x1010), f1 = __byte_perm(two, two, 0x3232);
-              const uint32_t w[4] = {codes[q].x, codes[q].y, codes[q].z, codes[q].w};
-              uint8_t* to = dst + (piece >> 1) * C::kBlockBytes + ((piece & 1) * 64 ^ half);
-#pragma unroll
-              for (uint32_t k = 0; k < 4; ++k) {
-                uint32_t h[4];
-                e2m1x8_to_f16(w[k], k < 2 ? f0 : f1, h);
-                *reinterpret_cast<uint4*>(to + (k * 16 ^ in0)) = make_uint4(h[0], h[1], h[2], h[3]);
-              }
+            for (uint32_t k = 0; k < 4; ++k) {
+              uint32_t h[4];
+              e2m1x8_to_f16(w[k], k < 2 ? f0 : f1, h);
+              *reinterpret_cast<uint4*>(to + (k * 16 ^ in0)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
           }
           fence_proxy_async_smem();
@@ -490,7 +487,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
             mbar_arrive(&bars->raw_empty[raw.st]);
             mbar_arrive(&bars->kv_full[at.st]);
           }
+          raw.next();
+          at.next();
+          (is_v ? raws[1] : raws[0]) = raw;
+          (is_v ? ats[1] : ats[0]) = at;
         }
+        tile0 += n;
       }
     }
   } else if (warp >= C::kMmaWarp) {
@@ -747,27 +749,22 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
             }
           }
         };
-        int items = 0, segs = 0;
+        int segs = 0;
         int done = 0;  // key tiles of this row tile so far
         bool ok = true;
         int st = 0;  // place of the last item waited for
         Ring ring_k(0, C::kKStages), ring_v(C::kKStages, C::kStages);
-        // K or V of the segment's key tile j, all in turn.
-        auto wait_item = [&](bool is_v, int j, int n) {
-          uint32_t phase;
-          if constexpr (C::kOneRing) {
-            const int item = items + (is_v ? item_of_v(j, n) : item_of_k(j));
-            st = item % C::kStages, phase = (item / C::kStages) & 1;
-          } else {
-            Ring& r = is_v ? ring_v : ring_k;
-            st = r.st, phase = r.phase;
-            r.next();
-          }
+        // The next K or V, all in the order of their loads.
+        auto wait_item = [&](bool is_v) {
+          Ring& r = is_v && !C::kOneRing ? ring_v : ring_k;
+          st = r.st;
+          const uint32_t phase = r.phase;
+          r.next();
           return bounded_wait(&bars->kv_full[st], phase, abort_flag, p.status, kStatusTimeoutMma);
         };
         // S of the tile that is number `d` of this row tile's.
-        auto qk = [&](int j, int n, int d) {
-          if (!(ok = wait_item(false, j, n))) return;
+        auto qk = [&](int d) {
+          if (!(ok = wait_item(false))) return;
           // The S before it in this place is in registers.
           if (d >= C::kSBufs &&
               !(ok = bounded_wait(&bars->s_free[C::s_bar(x, d)], (d / C::kSBufs - 1) & 1, abort_flag, p.status,
@@ -778,11 +775,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
           mma_commit(&bars->s_full[C::s_bar(x, d)]);
           mma_commit(&bars->kv_empty[st]);
         };
-        auto pv = [&](int j, int n, int d, bool last) {
-          if (!(ok = wait_item(true, j, n))) return;
+        auto pv = [&](int d, bool first, bool last) {
+          if (!(ok = wait_item(true))) return;
           if (!(ok = bounded_wait(&bars->p_full[x], d & 1, abort_flag, p.status, kStatusTimeoutMma))) return;
           tc_fence_after();
-          issue_pv(st, j > 0);
+          issue_pv(st, !first);
           mma_commit(&bars->p_free[x]);
           if (last) mma_commit(&bars->o_full[x]);
           mma_commit(&bars->kv_empty[st]);
@@ -803,29 +800,30 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
           if constexpr (NT == 1) {
             // (one row tile: it visits all of the segment's key tiles)
             for (int j = 0; ok && j < n; ++j, ++done) {
-              if (does_qk) qk(j, n, done);
-              else pv(j, n, done, j == n - 1);
+              if (does_qk) qk(done);
+              else pv(done, j == 0, j == n - 1);
             }
             if (ok && does_qk) mma_commit(&bars->q_empty);
           } else {
-            if (nx > 0) qk(0, n, done);
+            // K_0, then K_{j+1} and V_j in turn; what this tile's rows do not visit is
+            // released once landed.
+            auto skip = [&](bool is_v) {
+              if ((ok = wait_item(is_v))) mbar_arrive(&bars->kv_empty[st]);
+            };
             if (nx == 0) mbar_arrive(&bars->q_empty);
-            else if (nx == 1 && ok) mma_commit(&bars->q_empty);
-            for (int j = 0; ok && j < nx; ++j, ++done) {
+            for (int j = -1; ok && j < n; ++j) {
               if (j + 1 < nx) {
-                qk(j + 1, n, done + 1);
-                if (!ok) break;
-                if (j + 2 == nx) mma_commit(&bars->q_empty);
+                qk(done + j + 1);
+                if (ok && j + 2 == nx) mma_commit(&bars->q_empty);
+              } else if (j + 1 < n) {
+                skip(false);
               }
-              pv(j, n, done, j == nx - 1);
+              if (!ok || j < 0) continue;
+              if (j < nx) pv(done + j, j == 0, j == nx - 1);
+              else skip(true);
             }
-            for (int j = nx; ok && j < n; ++j)
-              for (int kv = 0; kv < 2; ++kv) {
-                if (!(ok = wait_item(kv != 0, j, n))) break;
-                mbar_arrive(&bars->kv_empty[st]);
-              }
+            done += nx;
           }
-          items += 2 * n;
           ++segs;
         }
         // Every MMA this thread issued must complete before TMEM is released.
