@@ -50,8 +50,16 @@ constexpr float kRescaleThreshold = 8.f;  // base-2 units
 constexpr int kSegRing = 8;       // segments whose notes of the guard are kept
 constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
 
-template <int D, int NT, bool FP4>
+// COPIES: with one tile and few rows, the tile holds the rows two or four times, and
+// each copy's warps take another part of the keys (the other weights of their rows
+// stay 0): the softmax of a tile, which otherwise waits for one or two of the four
+// warps, takes a half or a quarter of the time.  The copies are folded at a segment's
+// end.
+template <int D, int NT, bool FP4, int COPIES>
 struct Cfg {
+  static_assert(NT == 1 || COPIES == 1, "copies are of one tile");
+  static constexpr int kRows = kBM / COPIES;  // of a copy
+  static constexpr int kCols = kBN / COPIES;  // keys of a copy
   // Tensor memory has room for P unless there are two tiles of d = 128, and with one
   // tile for Q as well: over 4 bits, where shared memory's bandwidth bounds, both
   // products then read only K or V from there.
@@ -70,8 +78,13 @@ struct Cfg {
   static constexpr int kBlockBytes = kBM * 128;
   // Where an output waits for its store: P's place, or one of its own (one tile over 4
   // bits: none, threads store their rows).
-  static constexpr bool kDirectO = FP4 && NT == 1;
-  static constexpr int kStageBytes = kDirectO ? 0 : kPInTmem ? kTileBytes : kBM * kBN * 2;
+  // Copies are folded there, 32 columns at a time, by threads that store the sums.
+  static constexpr bool kDirectO = NT == 1 && (FP4 || COPIES > 1);
+  static constexpr int kStageBytes = COPIES > 1 ? kBM * 32 * 4 : kDirectO ? 0 : kPInTmem ? kTileBytes : kBM * kBN * 2;
+  // Rows of Q in shared memory: those of the tile, or of one copy on its way to
+  // tensor memory.
+  static constexpr int kQRows = kQInTmem ? kRows : kBM;
+  static constexpr int kQBytes = kQRows * D * 2;
   // 16-bit key and value tiles; of a 4-bit cache's rows, what comes from memory and
   // what the conversion makes of it.
   static constexpr int kStages = FP4 ? (NT == 2 ? (D == 128 ? 2 : 6) : (D == 128 ? 4 : 8))
@@ -88,7 +101,7 @@ struct Cfg {
   static_assert(kRawKStages <= 12 && kRawStages <= 12 && kStages <= 12, "barriers");
   static constexpr int kRawBytes = kBN * (D / 2 + D / 16);  // codes, then factors
   static constexpr int kQOff = 0;
-  static constexpr int kPOff = NT * kTileBytes;
+  static constexpr int kPOff = NT * kQBytes;
   static constexpr int kRingOff = kPOff + NT * kStageBytes;
   static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
   static constexpr int kBarOff = kRawOff + kRawStages * kRawBytes;
@@ -274,18 +287,17 @@ struct Ring {
   }
 };
 
-// Position of K_j / V_j among a segment's loads K_0, K_1, V_0, K_2, V_1, ..,
-// K_{n-1}, V_{n-2}, V_{n-1}.
-__device__ __forceinline__ int item_of_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+// Position of V_j among a segment's loads K_0, K_1, V_0, K_2, V_1, .., K_{n-1},
+// V_{n-2}, V_{n-1}.
 __device__ __forceinline__ int item_of_v(int j, int n) { return j <= n - 2 ? 2 * j + 2 : 2 * n - 1; }
 
 // Divides the list: every CTA sums all sequences' tiles, then the thread whose
 // share of the sequences holds the CTA's first tile finds it.
-template <int D, int NT, bool FP4>
+template <typename C, int NT>
 __device__ __forceinline__ void plan(const Params& p, Barriers* bars) {
-  constexpr int kWarps = Cfg<D, NT, FP4>::kThreads / 32;
+  constexpr int kWarps = C::kThreads / 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int each = (p.B + Cfg<D, NT, FP4>::kThreads - 1) / Cfg<D, NT, FP4>::kThreads;
+  const int each = (p.B + C::kThreads - 1) / C::kThreads;
   const int b0 = min(p.B, static_cast<int>(threadIdx.x) * each), b1 = min(p.B, b0 + each);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) mine += seq_tiles<NT>(p, load_seq(p, b)) * p.heads;
@@ -351,9 +363,10 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
   return r;
 }
 
-template <int D, bool BF16, int NT, bool FP4>
-__global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<D, NT, FP4>;
+template <int D, bool BF16, int NT, bool FP4, int COPIES>
+__global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
+    prefill_paged_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D, NT, FP4, COPIES>;
   constexpr bool kMmaBf16 = BF16 && !FP4;  // over 4 bits all operands are fp16
   constexpr bool kReadyQ = (BF16 && FP4) || C::kQInTmem;  // queries pass through the softmax warps
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -403,7 +416,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
     }
   }
   wait_for_previous_kernel();
-  plan<D, NT, FP4>(p, bars);
+  plan<C, NT>(p, bars);
   if (bars->start_left == 0) return;  // fewer tiles than CTAs
   if (warp == C::kMmaWarp) {
     tmem_alloc(&bars->tmem_base, 512);
@@ -534,11 +547,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
             const int t0 = seg.k * NT * p.tq_tokens;
             int real = 0;
             for (int x = 0; x < NT; ++x) real += t0 + x * p.tq_tokens < seg.s.rows;
-            mbar_arrive_expect_tx(&bars->q_full, real * C::kColBlocks * p.hb * p.tq_tokens * 128);
+            constexpr int kLoads = C::kQInTmem ? 1 : COPIES;
+            mbar_arrive_expect_tx(&bars->q_full, real * kLoads * C::kColBlocks * p.hb * p.tq_tokens * 128);
             for (int x = 0; x < real; ++x)
               for (int c = 0; c < C::kColBlocks; ++c)
-                tma_load_5d(sQ + x * C::kTileBytes + c * C::kBlockBytes, &p.tq, &bars->q_full, c * 64,
-                            (seg.u % p.nblk) * p.hb, seg.u / p.nblk, t0 + x * p.tq_tokens, seg.b, once);
+                for (int i = 0; i < kLoads; ++i)
+                  tma_load_5d(sQ + x * C::kQBytes + c * C::kQRows * 128 + i * C::kRows * 128, &p.tq, &bars->q_full,
+                              c * 64, (seg.u % p.nblk) * p.hb, seg.u / p.nblk, t0 + x * p.tq_tokens, seg.b, once);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -722,7 +737,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
         const uint32_t ring_addr = smem_u32(sRing);
         const uint32_t o_col = tmem + C::kOCol + x * D;
         const uint32_t p_tcol = tmem + C::kPCol + x * (kBN / 2);
-        const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ + x * C::kTileBytes), 16, 1024);
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ + x * C::kQBytes), 16, 1024);
         const uint64_t p_desc = smem_desc_sw128(smem_u32(sP + x * C::kStageBytes), 16, 1024);
         auto issue_qk = [&](int st, int d) {
           const uint32_t s_col = tmem + C::kSCol + C::s_bar(x, d) * kBN;
@@ -839,7 +854,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
     const int x = warp / 4;
     const int wq = warp % 4;
     const int row = wq * 32 + lane;
-    const int row_token = row / p.hb, row_head = row % p.hb;
+    const int copy = row / C::kRows, crow = row % C::kRows;  // (a warp's lanes are of one copy)
+    const int col0 = copy * C::kCols;                        // its first key of a tile
+    const int row_token = crow / p.hb, row_head = crow % p.hb;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t o_tmem = tmem + lane_off + C::kOCol + x * D;
     const uint32_t p_tmem = tmem + lane_off + C::kPCol + x * (kBN / 2);
@@ -863,6 +880,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
       group_sync();
       staged = false;
     };
+    if constexpr (COPIES > 1) {  // the weights of the other copies' keys
+      uint32_t zero[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) zero[i] = 0u;
+      tmem_st32(p_tmem, zero);
+      tmem_st32(p_tmem + 32, zero);
+      tmem_wait_st();
+    }
     while (ok && cur.next(p, seg)) {
       const TileRows tile(p, seg, x, NT);
       const int t = tile.t0 + row_token;
@@ -884,9 +909,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
           ok = false;
           break;
         }
-        uint8_t* q_row = sQ + x * C::kTileBytes + row * 128;
+        uint8_t* q_row = sQ + x * C::kQBytes + (C::kQInTmem ? crow : row) * 128;
         auto piece = [&](int i) {
-          return reinterpret_cast<uint4*>(q_row + (i / 8) * C::kBlockBytes + ((i ^ row) & 7) * 16);
+          return reinterpret_cast<uint4*>(q_row + (i / 8) * C::kQRows * 128 + ((i ^ row) & 7) * 16);
         };
         float down = 1.f;
         if constexpr (BF16) {
@@ -950,7 +975,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
           mbar_arrive(&bars->p_full[x]);
           continue;
         }
-        const uint32_t s_tmem = tmem + lane_off + C::kSCol + C::s_bar(x, done) * kBN;
+        const uint32_t s_tmem = tmem + lane_off + C::kSCol + C::s_bar(x, done) * kBN + col0;
         ok = bounded_wait(&bars->s_full[C::s_bar(x, done)], (done / C::kSBufs) & 1, abort_flag, p.status,
                           kStatusTimeoutSoftmax);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -958,23 +983,24 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
           break;
         }
         tc_fence_after();
-        const int k0 = (seg.j0 + j) * kBN;
-        const uint32_t bad = bars->bad[0][(tiles + j) % kTileRing];
-        const bool masked = k0 + kBN - 1 > tile.lim_min || bad != 0;
-        uint32_t u[kBN];
-        float mq[kBN / 32];
+        constexpr int kCols = C::kCols;
+        const int k0 = (seg.j0 + j) * kBN + col0;
+        const uint32_t bad = bars->bad[0][(tiles + j) % kTileRing] >> (col0 / 16);
+        const bool masked = k0 + kCols - 1 > tile.lim_min || bad != 0;
+        uint32_t u[kCols];
+        float mq[kCols / 32];
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < kBN / 32; ++c)
+          for (int c = 0; c < kCols / 32; ++c)
             tmem_ld32(s_tmem + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
         } else {
 #pragma unroll
-          for (int c = 0; c < kBN / 32; ++c)
+          for (int c = 0; c < kCols / 32; ++c)
             tmem_ld32_max(s_tmem + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]), mq[c]);
         }
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < kBN / 32; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
+        for (int c = 0; c < kCols / 32; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
         tc_fence_before();
         mbar_arrive(&bars->s_free[C::s_bar(x, done)]);
         if (NT == 2 && x == 0 && segs == 0 && j == 0) mbar_arrive(&bars->stagger);
@@ -982,23 +1008,25 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
         float mx;
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < kBN; ++c)
+          for (int c = 0; c < kCols; ++c)
             if (k0 + c > lim) s[c] = -INFINITY;
           if (bad != 0) {
 #pragma unroll
-            for (int c = 0; c < kBN; ++c)
+            for (int c = 0; c < kCols; ++c)
               if (bad >> (c / 16) & 1u) s[c] = -INFINITY;
           }
           float mx8[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) mx8[i] = s[i];
 #pragma unroll
-          for (int c = 8; c < kBN; c += 16)
+          for (int c = 8; c < kCols; c += 16)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) mx8[i] = fmax3(mx8[i], s[c + i], s[c + 8 + i < kBN ? c + 8 + i : c + i]);
+            for (int i = 0; i < 8; ++i) mx8[i] = fmax3(mx8[i], s[c + i], s[c + 8 + i < kCols ? c + 8 + i : c + i]);
           mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
         } else {
-          mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+          mx = mq[0];
+#pragma unroll
+          for (int c = 1; c < kCols / 32; ++c) mx = fmaxf(mx, mq[c]);
         }
         float gamma = 1.f;
         if (j == 0) {
@@ -1016,10 +1044,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
         const float2 nrs2 = make_float2(-rs, -rs);
         float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int blk = 0; blk < kBN / 64; ++blk) {
-          uint32_t pk[32];
+        for (int blk = 0; blk < (kCols + 63) / 64; ++blk) {
+          constexpr int kBlk = kCols < 64 ? kCols : 64;
+          uint32_t pk[kBlk / 2];
 #pragma unroll
-          for (int c8 = 0; c8 < 8; ++c8) {
+          for (int c8 = 0; c8 < kBlk / 8; ++c8) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int c = blk * 64 + c8 * 8 + 2 * i;
@@ -1054,8 +1083,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
               if (!ok) break;
             }
           }
-          if constexpr (C::kPInTmem) {
-            tmem_st32(p_tmem + blk * 32, pk);
+          if constexpr (kBlk == 32) {
+            tmem_st16(p_tmem + col0 / 2, pk);
+          } else if constexpr (C::kPInTmem) {
+            tmem_st32(p_tmem + col0 / 2 + blk * 32, pk);
           } else {
 #pragma unroll
             for (int c8 = 0; c8 < 8; ++c8)
@@ -1091,7 +1122,88 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4>::kThreads, 1) prefill_paged_ke
       const bool nan_any = guarded && bars->nan_any[segs % kSegRing] != 0;
       const uint8_t* nan_from = bars->nan_from[segs % kSegRing];
       const int seen = real ? lim - lim0 : 0;
-      if (seg.whole()) {
+      if constexpr (COPIES > 1) {
+        // Fold the copies: their references and sums, then O, 32 columns at a time; a
+        // thread sums its row's part of the columns.
+        constexpr int kPer = 32 / COPIES;
+        const bool whole = seg.whole();
+        const bool counts = real && l != 0.f;
+        const float m = r * lam;
+        float2* ml = reinterpret_cast<float2*>(sP);
+        ml[row] = counts ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+        group_sync();
+        if (!ok) break;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int c = 0; c < COPIES; ++c) M = fmaxf(M, ml[crow + c * C::kRows].x);
+#pragma unroll
+        for (int c = 0; c < COPIES; ++c) {
+          const float2 v = ml[crow + c * C::kRows];
+          if (v.y != 0.f) L = fmaf(v.x == M ? 1.f : ex2_approx(v.x - M), v.y, L);
+        }
+        const float weight = !counts ? 0.f : m == M ? vd : vd * ex2_approx(m - M);
+        const bool writes = in_tile && t < p.S;
+        const long long hrow = (static_cast<long long>(seg.b) * p.H + (seg.u / p.nblk) * p.g + head) * p.S + t;
+        const long long part = blockIdx.x * 2LL + (seg.j0 > 0 ? 0 : 1);
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        float4* fold = reinterpret_cast<float4*>(sP);  // [8][kBM]
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t u[32];
+          tmem_ld32(o_tmem + c * 32, u);
+          tmem_wait_ld();
+          reg_fence32(u);
+          if (nan_any) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (seen > nan_from[c * 32 + i]) u[i] = 0x7FFFFFFFu;
+          }
+          group_sync();  // what was there has been read
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = counts ? __uint_as_float(u[4 * i + k]) * weight : 0.f;
+            fold[i * kBM + row] = make_float4(v[0], v[1], v[2], v[3]);
+          }
+          group_sync();
+          if (!ok) break;
+          float acc[kPer];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll
+          for (int k = 0; k < COPIES; ++k)
+#pragma unroll
+            for (int i = 0; i < kPer / 4; ++i) {
+              const float4 v = fold[(copy * (kPer / 4) + i) * kBM + crow + k * C::kRows];
+              acc[4 * i] += v.x, acc[4 * i + 1] += v.y, acc[4 * i + 2] += v.z, acc[4 * i + 3] += v.w;
+            }
+          if (!writes) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + hrow * D + c * 32 + copy * kPer);
+#pragma unroll
+            for (int i = 0; i < kPer / 8; ++i)
+              dst[i] = make_uint4(pack2<BF16>(acc[8 * i] * inv, acc[8 * i + 1] * inv),
+                                  pack2<BF16>(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv),
+                                  pack2<BF16>(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv),
+                                  pack2<BF16>(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.part_o) + (part * (D / 4) + c * 8 + copy * (kPer / 4)) * kBM + crow;
+#pragma unroll
+            for (int i = 0; i < kPer / 4; ++i)
+              dst[i * kBM] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+          }
+        }
+        if (!ok) break;
+        tc_fence_before();  // O has been read before P's arrival lets it be overwritten
+        group_sync();       // the last columns too
+        if (!ok) break;
+        if (writes && copy == 0) {
+          if (!whole) p.part_ml[part * kBM + crow] = make_float2(M, L);
+          else if (p.lse != nullptr) p.lse[hrow] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+        }
+      } else if (seg.whole()) {
         [[maybe_unused]] long long store_row = -1;
         if constexpr (C::kDirectO) {
           if (in_tile && t < p.S) store_row = (static_cast<long long>(seg.b) * p.H + (seg.u / p.nblk) * p.g + head) * p.S + t;
@@ -1284,6 +1396,7 @@ Shape shape_of(int B, int H, int Hkv, int S) {
   s.tokens = kBM / s.hb;
   s.heads = Hkv * s.nblk;
   s.nt = S <= s.tokens ? 1 : 2;
+  if (s.nt == 1) s.tokens = S;
   s.blocks = (S + s.nt * s.tokens - 1) / (s.nt * s.tokens);
   s.units = static_cast<long long>(B) * s.heads * s.blocks;
   return s;
@@ -1295,9 +1408,9 @@ int max_ctas(const Shape& s, int max_len) {
   return s.units >= kMaxCtas || s.units * per_unit >= kMaxCtas ? kMaxCtas : static_cast<int>(s.units * per_unit);
 }
 
-template <int D, bool BF16, int NT, bool FP4>
+template <int D, bool BF16, int NT, bool FP4, int COPIES>
 int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
-  using C = Cfg<D, NT, FP4>;
+  using C = Cfg<D, NT, FP4, COPIES>;
   static_assert(C::kSmemBytes <= 232448, "shared memory of a CTA");
   const CacheArgs& c = a.cache;
   const int page = 1 << c.page_shift;
@@ -1314,7 +1427,7 @@ int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   } else if (!make_tmap_3d(&p.tk, c.data[0], BF16, D, page, static_cast<long long>(c.n_pages) * c.Hkv, p.box_rows) ||
       !make_tmap_3d(&p.tv, c.data[1], BF16, D, page, static_cast<long long>(c.n_pages) * c.Hkv, p.box_rows))
     return -1;
-  auto kern = prefill_paged_kernel<D, BF16, NT, FP4>;
+  auto kern = prefill_paged_kernel<D, BF16, NT, FP4, COPIES>;
   static std::atomic<unsigned long long> attr_done{0};  // per instantiation
   if (!set_smem_limit_once(kern, C::kSmemBytes, attr_done)) return -1;
   if (launch_after(kern, dim3(static_cast<unsigned>(p.ctas)), C::kThreads, a.stream, p, C::kSmemBytes) != 0) return -1;
@@ -1324,10 +1437,17 @@ int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   return launch_after(prefill_paged_merge_kernel<D, NT>, dim3(static_cast<unsigned>(ctas)), kMergeThreads, a.stream, p);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool FP4>
 int launch_nt(Params& p, const PagedPrefillArgs& a, const Shape& s) {
-  if (a.cache.fp4()) return s.nt == 1 ? launch_t<D, BF16, 1, true>(p, a, s) : launch_t<D, BF16, 2, true>(p, a, s);
-  return s.nt == 1 ? launch_t<D, BF16, 1, false>(p, a, s) : launch_t<D, BF16, 2, false>(p, a, s);
+  if (s.nt == 2) return launch_t<D, BF16, 2, FP4, 1>(p, a, s);
+  const int rows = s.hb * s.tokens;
+  if (rows <= kBM / 4) return launch_t<D, BF16, 1, FP4, 4>(p, a, s);
+  if (rows <= kBM / 2) return launch_t<D, BF16, 1, FP4, 2>(p, a, s);
+  return launch_t<D, BF16, 1, FP4, 1>(p, a, s);
+}
+template <int D, bool BF16>
+int launch_d(Params& p, const PagedPrefillArgs& a, const Shape& s) {
+  return a.cache.fp4() ? launch_nt<D, BF16, true>(p, a, s) : launch_nt<D, BF16, false>(p, a, s);
 }
 
 }  // namespace
@@ -1371,8 +1491,8 @@ int launch_prefill_paged(const PagedPrefillArgs& a) {
   p.part_o = ws;
   p.part_ml = reinterpret_cast<float2*>(ws + states * c.d);
   p.parts = reinterpret_cast<int2*>(ws + states * (c.d + 2));
-  if (c.d == 128) return a.bf16 ? launch_nt<128, true>(p, a, s) : launch_nt<128, false>(p, a, s);
-  return a.bf16 ? launch_nt<64, true>(p, a, s) : launch_nt<64, false>(p, a, s);
+  if (c.d == 128) return a.bf16 ? launch_d<128, true>(p, a, s) : launch_d<128, false>(p, a, s);
+  return a.bf16 ? launch_d<64, true>(p, a, s) : launch_d<64, false>(p, a, s);
 }
 
 }  // namespace gbattn
