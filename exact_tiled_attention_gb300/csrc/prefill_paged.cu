@@ -47,6 +47,9 @@ constexpr int kBM = 128;          // rows of a tile (= TMEM lanes)
 constexpr int kBN = 128;          // keys of a tile
 constexpr int kMaxCtas = 160;     // bound of the grid, for the workspace's size
 constexpr float kRescaleThreshold = 8.f;  // base-2 units
+// A scale of scores is at least this, so that -inf times it stays -inf; finite products
+// of Q and K are then as good as 0.
+constexpr float kLeastScale = 1.1754944e-38f;
 constexpr int kSegRing = 8;       // segments whose notes of the guard are kept
 constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
 
@@ -144,7 +147,8 @@ struct Params {
   int page_shift, n_pages, max_pages, box_rows;
   int causal;
   int out_bf16;
-  float scale_log2;
+  float scale_log2;  // |scale| log2 e (of a scale of 0: log2 e)
+  float sign;        // -1 or 0 where scale is negative or 0, and scores are taken times it
   int ctas;
   int* status;
 };
@@ -897,7 +901,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       const int lim = real ? limit(p, seg.s, t) : -1;
       if constexpr (FP4) {
         const int kvh = seg.u / p.nblk;
-        lam = p.scale_log2 * (p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f);
+        lam = fmaxf(p.scale_log2 * (p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f), kLeastScale);
         vd = p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
       }
       if constexpr (kReadyQ) {
@@ -927,6 +931,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           down = __uint_as_float((254u - e) << 23);
           lam *= __uint_as_float(e << 23);
         }
+        if constexpr (BF16) lam = fmaxf(lam, kLeastScale);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           uint32_t h[32];
@@ -986,7 +991,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         constexpr int kCols = C::kCols;
         const int k0 = (seg.j0 + j) * kBN + col0;
         const uint32_t bad = bars->bad[0][(tiles + j) % kTileRing] >> (col0 / 16);
-        const bool masked = k0 + kCols - 1 > tile.lim_min || bad != 0;
+        const bool masked = k0 + kCols - 1 > tile.lim_min || bad != 0 || p.sign != 1.f;
         uint32_t u[kCols];
         float mq[kCols / 32];
         if (masked) {
@@ -1007,6 +1012,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         float* s = reinterpret_cast<float*>(u);
         float mx;
         if (masked) {
+          if (p.sign != 1.f) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) s[c] *= p.sign;
+          }
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
             if (k0 + c > lim) s[c] = -INFINITY;
@@ -1482,7 +1491,9 @@ int launch_prefill_paged(const PagedPrefillArgs& a) {
   p.max_pages = c.max_pages;
   p.causal = a.causal;
   p.out_bf16 = a.bf16 ? 1 : 0;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.scale_log2 = (a.scale == 0.f ? 1.f : a.scale < 0.f ? -a.scale : a.scale) * 1.4426950408889634f;
+  if (p.scale_log2 < kLeastScale) p.scale_log2 = kLeastScale;
+  p.sign = a.scale == 0.f ? 0.f : a.scale < 0.f ? -1.f : 1.f;
   const int most = max_ctas(s, c.max_pages << c.page_shift);
   p.ctas = most < a.num_sms ? most : a.num_sms;
   p.status = a.status;

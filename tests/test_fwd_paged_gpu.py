@@ -95,3 +95,316 @@ def test_runs_of_several_units(cfg, bits):
         again = _forward(pool, q, table, lens, news)
         assert gb.gbattn_device_status() == 0
         assert _same_bits(again[0], o) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("S", [1, 30, 90])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_slots_behind_the_length_and_unused_pages_hold_nan(bits, S):
+    lens, page, H, Hkv, d = [1, 333, 130, 700], 64, 8, 2, 128
+    news = [1, min(S, 333), S, S]
+    pool, table, g = _make(bits, torch.bfloat16, Hkv, d, page, lens, 34, spare=9)
+    q = torch.randn(4, H, S, d, generator=g).bfloat16().cuda()
+    o, lse = _forward(pool, q, table, lens, news)
+    dirty, _, _ = _make(bits, torch.bfloat16, Hkv, d, page, lens, 34, spare=9, nan=True)
+    for t, src in zip(dirty.gpu, pool.gpu):
+        t, src = (x.view(torch.uint8) if x.element_size() == 1 else x for x in (t, src))
+        for b, n in enumerate(lens):
+            for i in range((n + page - 1) // page):
+                rows = min(page, n - i * page)
+                t[table[b, i], :, :rows] = src[table[b, i], :, :rows]
+    dirty.kw = pool.kw
+    for causal in (True, False):
+        o, lse = _forward(pool, q, table, lens, news, causal=causal)
+        o2, lse2 = _forward(dirty, q, table, lens, news, causal=causal)
+        assert torch.isfinite(o2).all() and _same_bits(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,d,S,L", [
+    (torch.bfloat16, 4, 2, 128, 9, 150), (torch.float16, 8, 1, 64, 20, 500), (torch.bfloat16, 2, 2, 128, 200, 350),
+    (torch.float16, 4, 1, 64, 100, 130), (torch.bfloat16, 2, 1, 128, 300, 300), (torch.bfloat16, 1, 1, 64, 256, 1000)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite(dtype, H, Hkv, d, S, L, value):
+    """A NaN or an infinity in a token's v reaches the tokens that see it, in its
+    element, and nothing else; in its k, the tokens that see it alone."""
+    page = 16
+    pool, table, g = _make(16, dtype, Hkv, d, page, [L, L], 35)
+    q = torch.randn(2, H, S, d, generator=g).to(dtype).cuda()
+    clean = _forward(pool, q, table, [L, L], None)
+    at = [L - S + t for t in sorted({0, 1, S // 2, S - 1})] + [L - S - 1] * (L > S)
+    # a token and an element each, the same element twice
+    el = [(7 * i) % d for i in range(len(at))]
+    el[-1] = el[0]
+    for p, e in zip(at, el):
+        pool.gpu[1][table[0, p // page], :, p % page, e] = value
+    o, lse = _forward(pool, q, table, [L, L], None)
+    assert gb.gbattn_device_status() == 0
+    bad = torch.zeros(S, d, dtype=torch.bool, device="cuda")
+    for p, e in zip(at, el):
+        bad[max(0, p - (L - S)):, e] = True
+    assert torch.equal(torch.isnan(o[0]) | torch.isinf(o[0]), bad.expand(H, S, d))
+    assert _same_bits(torch.where(bad, 0.0, o[0].float()).to(dtype), torch.where(bad, 0.0, clean[0][0].float()).to(dtype))
+    assert _same_bits(o[1], clean[0][1]) and torch.equal(lse, clean[1])
+    if math.isnan(value):
+        t0 = S // 2
+        pool.gpu[0][table[1, (L - S + t0) // page], :, (L - S + t0) % page, 3] = value
+        o, lse = _forward(pool, q, table, [L, L], None)
+        assert torch.isnan(o[1, :, t0:]).all() and torch.isnan(lse[1, :, t0:]).all()
+        assert _same_bits(o[1, :, :t0].contiguous(), clean[0][1, :, :t0].contiguous())
+        assert torch.equal(lse[1, :, :t0], clean[1][1, :, :t0])
+
+
+@pytest.mark.parametrize("S", [1, 20, 70])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_pages_that_do_not_exist(bits, S):
+    """A page outside the pool is left out, and reported; a sequence without any
+    counts no key."""
+    lens, page, H, Hkv, d = [300, 80], 16, 4, 2, 64
+    pool, table, g = _make(bits, torch.float16, Hkv, d, page, lens, 36)
+    n_pages = pool.gpu[0].shape[0]
+    q = torch.randn(2, H, S, d, generator=g).half().cuda()
+    gb.gbattn_device_status()
+    for bad in (-1, n_pages, 2 ** 31 - 1):
+        t = table.clone()
+        t[0, 2], t[0, 18] = bad, bad  # slots 32 .. 47 and 288 .. 299, the last ones
+        o, lse = _forward(pool, q, t, lens, None, causal=False)
+        assert gb.gbattn_device_status() == GBATTN_EINDEX and gb.gbattn_device_status() == 0
+        keep = [i for i in range(300) if i // page not in (2, 18)]
+        k, v = (pool.values(i, table[0], 300)[:, keep] for i in range(2))
+        half_p = pu.u(torch.float16)
+        ro, rl, to, tl = cu.attention(q[0].cpu(), k, v, torch.full((S,), len(keep) - 1), 0.125, half_p, 2.0 ** -24, True)
+        assert ((o[0].double().cpu() - ro).abs() <= to + half_p * (ro.abs() + to) + 2.0 ** -25).all()
+        assert ((lse[0].double().cpu() - rl).abs() <= tl).all()
+        t[1] = bad
+        o, lse = _forward(pool, q, t, lens, None)
+        assert gb.gbattn_device_status() == GBATTN_EINDEX
+        assert (o[1] == 0).all() and torch.isneginf(lse[1]).all() and torch.isfinite(o[0]).all()
+    gb.gbattn_device_status()
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_lengths_outside_their_ranges(bits):
+    """Lengths are clamped into the page table, numbers of new tokens into 0 .. S."""
+    page, H, Hkv, d, S = 16, 4, 2, 128, 5
+    pool, table, g = _make(bits, torch.bfloat16, Hkv, d, page, [64, 64, 64, 64], 37)
+    table = table[:, :4].contiguous()
+    q = torch.randn(4, H, S, d, generator=g).bfloat16().cuda()
+    o, lse = _forward(pool, q, table, [1 << 30, -5, 64, -(2 ** 31)], [5, 5, 100, 5], causal=False)
+    ref, rl = _forward(pool, q, table, [64, 0, 64, 0], [5, 0, 5, 0], causal=False)
+    assert gb.gbattn_device_status() == 0 and _same_bits(o, ref) and torch.equal(lse, rl)
+    o, _ = _forward(pool, q, table, [64, 64, 2, 2 ** 31 - 1], [-1, -(2 ** 31), 2 ** 31 - 1, 2 ** 31 - 1])
+    ref, _ = _forward(pool, q, table, [64, 64, 2, 64], [0, 0, 5, 0])
+    assert gb.gbattn_device_status() == 0 and _same_bits(o[:3], ref[:3])
+    assert torch.isfinite(o).all() and (o[2, :, :3] == 0).all()
+
+
+@pytest.mark.parametrize("S", [2, 40, 130])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_scales_scores_and_given_arguments(bits, S):
+    """Scores that grow along the keys by more than the lazy reference allows, up to a
+    softmax that is one key's; scales of every sign; out, lse and workspace given."""
+    lens, page, H, Hkv, d = [400, 329], 32, 4, 1, 128
+    pool, table, g = _make(bits, torch.float16, Hkv, d, page, lens, 38)
+    q = (torch.randn(2, H, S, d, generator=g) * torch.tensor([0.01, 1.0, 30.0, 300.0])[:, None, None]).half().cuda()
+    ws = torch.empty(gb.attn_fwd_paged_workspace_bytes(2, H, Hkv, S, d), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(2, H, S, device="cuda")
+    for scale in (0.7, -0.3, 0.0):
+        ws.fill_(255)
+        o, l2 = _forward(pool, q, table, lens, None, scale=scale, out=out, lse=lse, workspace=ws)
+        assert o is out and l2 is lse and gb.gbattn_device_status() == 0
+        _ok(pool, q if scale >= 0 else -q, table, lens, [S, S], o, lse, True, abs(scale))
+    o, none = _forward(pool, q, table, lens, None, return_lse=False)
+    assert none is None
+
+
+@pytest.mark.parametrize("S", [2, 100])
+def test_wide_queries_over_four_bits(S):
+    """bf16 queries far outside fp16's range, whose products the row's scale keeps exact."""
+    pool, table, g = _make(4, torch.bfloat16, 1, 64, 64, [200], 39)
+    q = torch.randn(1, 3, S, 64, generator=g)
+    q[0, 0] *= 1e30
+    q[0, 1] *= 1e-30
+    q[0, 2] = 0
+    q = q.bfloat16().cuda()
+    for scale in (1e-30, 1e30):
+        qs = q[:, [0, 2] if scale < 1 else [1, 2]].contiguous()
+        o, lse = _forward(pool, qs, table, [200], None, scale=scale)
+        _ok(pool, qs, table, [200], [S], o, lse, True, scale)
+
+
+def test_offsets_beyond_32_bits():
+    """A pool of more than 2^32 bytes and 2^31 elements, in both units of work."""
+    page, Hkv, d = 1024, 2, 128
+    n_pages = 8400  # 2.2e9 elements, 4.4e9 bytes
+    kc, vc = (torch.empty(n_pages, Hkv, page, d, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    g = torch.Generator().manual_seed(42)
+    table = torch.tensor([[n_pages - 1, -1], [n_pages - 2, n_pages - 3]], dtype=torch.int32)
+    lens = [140, 1140]
+    new = torch.randn(2, 3, 2, Hkv, page, d, generator=g).bfloat16()[0].cuda()
+    kc[n_pages - 3:], vc[n_pages - 3:] = new[:, 0], new[:, 1]
+    for S in (40, 140):
+        q = torch.randn(2, Hkv, S, d, generator=g).bfloat16().cuda()
+        o, lse = gb.attn_fwd_paged(q, kc, vc, table.cuda(), _i32(lens))
+        assert gb.gbattn_device_status() == 0
+        kv = gb.attn_cache_gather(kc, vc, table.cuda(), _i32(lens), 1140)
+        cu.check(o, lse, q, lambda b, n: tuple(t[b, :, :n].cpu() for t in kv), lens, [S, S], True, 1 / math.sqrt(d),
+                 pu.u(torch.bfloat16), half_o=pu.u(torch.bfloat16))
+    codes = [torch.zeros(2 * n_pages, Hkv, page, n, dtype=torch.uint8, device="cuda") for _ in "kv" for n in (64, 8)]
+    table = 2 * table.clamp(min=0) + 1
+    gb.attn_cache_append_fp4(kv[0], kv[1], *codes, table.cuda(), _i32([1140, 1140]), new_lens=_i32([0, 1140]))
+    q = torch.randn(2, Hkv, 40, d, generator=g).bfloat16().cuda()
+    o, lse = gb.attn_fwd_paged_fp4(q, *codes, table.cuda(), _i32([0, 1140]))
+    assert gb.gbattn_device_status() == 0
+    back = gb.attn_cache_gather_fp4(*codes, table.cuda(), _i32([0, 1140]), 1140, dtype=torch.float16)  # exact
+    cu.check(o, lse, q, lambda b, n: tuple(t[b, :, :n].cpu() for t in back), [0, 1140], [40, 40], True,
+             1 / math.sqrt(d), pu.u(torch.float16), 2.0 ** -24, True, pu.u(torch.bfloat16))
+
+
+@pytest.mark.parametrize("S", [3, 90])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_streams_graphs_and_two_calls_at_once(bits, S):
+    """A captured step (append, attention) replayed with other lengths, behind fills
+    and copies, and two calls on two streams with a workspace each."""
+    page, H, Hkv, d, B = 16, 8, 2, 128, 4
+    pool, table, g = _make(bits, torch.bfloat16, Hkv, d, page, [300] * B, 40)
+    q, other = (torch.randn(B, H, S, d, generator=g).bfloat16().cuda() for _ in range(2))
+    k, v = (torch.randn(B, Hkv, S, d, generator=g).bfloat16().cuda() for _ in "kv")
+    rope, td = gb.rope_table(400, d), table.cuda()
+    lens, new = _i32([S] * B), _i32([S] * B)
+    fn = gb.attn_fwd_paged if bits == 16 else gb.attn_fwd_paged_fp4
+
+    def step():
+        qr = pool.append(k, v, td, lens, rope=rope, q=q, new_lens=new)
+        out = fn(qr, *pool.gpu, td, lens, new_lens=new, **pool.kw)
+        qr.fill_(float("nan"))
+        return [t.clone() for t in out]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for a, b in (([S] * B, [S] * B), ([300, 117, 0, 290], [S, 1, 0, S - 1]), ([100, 128, 129, 300], [S, S, 2, 0])):
+        lens.copy_(_i32(a))
+        new.copy_(_i32(b))
+        graph.replay()
+        torch.cuda.synchronize()
+        first = [t.clone() for t in got]
+        assert all(torch.equal(x, y) for x, y in zip(first, step()))
+    refs = [fn(x, *pool.gpu, td, lens, **pool.kw) for x in (q, other)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ws = [torch.empty(gb.attn_fwd_paged_workspace_bytes(B, H, Hkv, S, d), dtype=torch.uint8, device="cuda")
+          for _ in streams]
+    for _ in range(5):
+        outs = [fn(x, *pool.gpu, td, lens, **pool.kw, workspace=w, stream=s) for x, w, s in zip((q, other), ws, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(outs, refs):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # what a call on another stream allocates is that stream's
+    need = gb.attn_fwd_paged_workspace_bytes(B, H, Hkv, S, d, table.shape[1] * page)
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(streams[0]):
+        for _ in range(8):
+            busy @ busy
+    o, lse = fn(q, *pool.gpu, td, lens, **pool.kw, stream=streams[0])
+    fills = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (need, need, q.numel() * 2, B * H * S * 4)]
+    torch.cuda.synchronize()
+    assert torch.equal(o, refs[0][0]) and torch.equal(lse, refs[0][1]) and all((f == 255).all() for f in fills)
+    assert gb.gbattn_device_status() == 0
+
+
+def test_agrees_with_the_contiguous_forward_and_the_decode():
+    """The same attention through attn_fwd over the gathered cache, and through the
+    decode for its last token: all within their bounds of one definition, so within
+    the parity tests' bounds of each other."""
+    from tests.parity_util import LSE_MAX_ABS, O_MAX_ABS
+
+    lens, page, H, Hkv, d, S = [500] * 3, 32, 8, 2, 128, 200
+    pool, table, g = _make(16, torch.bfloat16, Hkv, d, page, lens, 41)
+    q = torch.randn(3, H, S, d, generator=g).bfloat16().cuda()
+    kv = pool.gather(table.cuda(), _i32(lens), 500)
+    for causal in (True, False):
+        o, lse = _forward(pool, q, table, lens, None, causal=causal)
+        o1, l1 = gb.attn_fwd(q, *kv, causal=causal)
+        assert (o.float() - o1.float()).abs().max() <= O_MAX_ABS and (lse - l1).abs().max() <= LSE_MAX_ABS
+    last = q[:, :, -1:].contiguous()
+    o2, l2 = pool.decode(last, table.cuda(), _i32(lens))
+    assert (o[:, :, -1:].float() - o2.float()).abs().max() <= O_MAX_ABS
+    assert (lse[:, :, -1] - l2).abs().max() <= LSE_MAX_ABS
+
+
+def test_wrapper_refusals():
+    g = torch.Generator().manual_seed(45)
+    pool, pool4 = Pool(16, 3, 2, 16, 64, torch.float16, g), Pool(4, 3, 2, 16, 64, torch.float16, g)
+    table, lens = _i32([[0, 1]]), _i32([20])
+    q = torch.zeros(1, 4, 5, 64, dtype=torch.float16, device="cuda")
+    bad = [
+        lambda: gb.attn_fwd_paged(q.bfloat16(), *pool.gpu, table, lens),
+        lambda: gb.attn_fwd_paged(q.transpose(1, 2), *pool.gpu, table, lens),
+        lambda: gb.attn_fwd_paged(q[:, :3].contiguous(), *pool.gpu, table, lens),
+        lambda: gb.attn_fwd_paged(q, *pool.gpu, table.long(), lens),
+        lambda: gb.attn_fwd_paged(q, *pool.gpu, table, lens, new_lens=_i32([5, 5])),
+        lambda: gb.attn_fwd_paged(q, *pool.gpu, table, lens, new_lens=lens.long()),
+        lambda: gb.attn_fwd_paged(q, *pool.gpu, table.cpu(), lens),
+        lambda: gb.attn_fwd_paged(q, pool.gpu[0], pool.gpu[1][:2], table, lens),
+        lambda: gb.attn_fwd_paged(q, *pool.gpu, table, lens, scale=float("nan")),
+        lambda: gb.attn_fwd_paged(q, *pool.gpu, table, lens, scale=float("inf")),
+        lambda: gb.attn_fwd_paged(q, *pool.gpu, table, lens, lse=torch.zeros(1, 4, device="cuda")),
+        lambda: gb.attn_fwd_paged(q, *pool.gpu, table, lens, out=q.float()),
+        lambda: gb.attn_fwd_paged(q, *pool.gpu, table, lens, workspace=torch.empty(16, device="cuda")),
+        lambda: gb.attn_fwd_paged(q[:, :, :0], *pool.gpu, table, lens),
+        lambda: gb.attn_fwd_paged_fp4(q, *pool4.gpu[:3], None, table, lens),
+        lambda: gb.attn_fwd_paged_fp4(q, pool4.gpu[0], pool4.gpu[1][..., :2], *pool4.gpu[2:], table, lens),
+        lambda: gb.attn_fwd_paged_fp4(q, *pool4.gpu, table, lens, v_descale=torch.ones(3, device="cuda")),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises((TypeError, ValueError, gb.GbattnError)):
+            f()
+            pytest.fail(f"call {i} was not refused")
+    assert gb.gbattn_device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_text_and_images_served_in_chunks(bits):
+    """As a program runs them: two sequences of different lengths take chunks of text
+    and images (norms and rotation by three axes, append, attention of the chunk), then
+    one token each by append and decode; each step against the definition applied to
+    what the step before it gave."""
+    g = torch.Generator().manual_seed(51)
+    B, H, Hkv, d, page, dtype = 2, 4, 2, 64, 16, torch.bfloat16
+    pool = Pool(bits, 30, Hkv, page, d, dtype, g)
+    table = pu.page_table([200, 200], page, 30, 13, g)
+    rope, axes = gb.rope_table(256, d), gb.rope_pair_axes((8, 12, 12))
+    w = [1 + 0.1 * torch.randn(d, generator=g) for _ in "qk"]
+    wd = [x.cuda() for x in w]
+    done, scale = [0, 0], 1 / math.sqrt(d)
+    for S, news in ((50, [50, 31]), (70, [12, 70]), (3, [3, 3]), (1, [1, 1])):
+        x = torch.randn(B, S, H + 2 * Hkv, d, generator=g).to(dtype).cuda().transpose(1, 2)
+        q, k, v = x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:]
+        pos = torch.randint(0, 256, (3, B, S), generator=g, dtype=torch.int32)
+        qn, kn = gb.attn_qk_norm_rope(q, k, *wd, rope=rope, positions=pos.cuda(), axes=axes)
+        done = [a + b for a, b in zip(done, news)]
+        pool.append(kn, v, table.cuda(), _i32(done), new_lens=_i32(news))
+        pool.pull()
+        if S > 1:
+            o, lse = _forward(pool, qn, table, done, news)
+        else:
+            o, lse = pool.decode(qn, table.cuda(), _i32(done))
+            lse = lse[..., None]
+        assert gb.gbattn_device_status() == 0
+        for b, (n, m) in enumerate(zip(done, news)):
+            half = rope.shape[1] // 2
+            at = torch.stack([pos[a, b] for a in axes], -1).long()
+            own = torch.cat([rope.cpu()[at, torch.arange(half)], rope.cpu()[at, half + torch.arange(half)]], -1)
+            for i, (raw, got) in enumerate(((q, qn), (k, kn))):
+                ref, mag = pu.norm_rope(raw[b].double().cpu(), w[i].double(), own, torch.arange(S), 1e-6, False)
+                assert ((got[b].double().cpu() - ref).abs() <= pu.u(dtype) * ref.abs() + 20 * pu.U32 * mag).all()
+            if bits == 16:
+                assert torch.equal(pool.values(0, table[b], n)[:, n - m:], kn[b, :, :m].float().cpu())
+        if S > 1:
+            _ok(pool, qn, table, done, news, o, lse, True, scale)
+        else:
+            half_p = pu.u(torch.float16) if bits == 4 else pu.u(dtype) ** 2
+            cu.check(o, lse, qn, lambda b, n: (pool.values(0, table[b], n), pool.values(1, table[b], n)), done, news,
+                     True, scale, half_p, 2.0 ** -24 if bits == 4 else 0.0, bits == 4, pu.u(dtype))
