@@ -14,8 +14,9 @@
 // equal runs, one for each CTA (one an SM), whatever the lengths are.  A run
 // covers whole units, which the CTA finishes itself, and at its two ends parts of
 // units, whose states (m, l, o) it leaves in the workspace; a second kernel folds
-// those and writes the zeros of padding rows.  The division follows from the
-// lengths alone, so results repeat bitwise.
+// those and writes the zeros of padding rows.  Where equal numbers of whole units
+// take hardly longer than equal runs (kSplitCost), CTAs get those.  The division
+// follows from the lengths alone, so results repeat bitwise.
 //
 // A CTA works through its run without a stop between units: the loader, the MMA
 // issuers, the softmax warps and the guard walk the same list of segments each at
@@ -51,6 +52,10 @@ constexpr float kRescaleThreshold = 8.f;  // base-2 units
 // of Q and K are then as good as 0.
 constexpr float kLeastScale = 1.1754944e-38f;
 constexpr int kSegRing = 8;       // segments whose notes of the guard are kept
+// Key tiles that the states of split units cost (writing, and a second kernel that has
+// to fold them) for units of one and two row tiles.
+template <int NT>
+constexpr int kSplitCost = NT == 2 ? 6 : 4;
 constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
 
 // COPIES: with one tile and few rows, the tile holds the rows two or four times, and
@@ -162,9 +167,11 @@ struct __align__(8) Barriers {
   uint64_t group[2];       // the four warps of a softmax warpgroup
   uint64_t stagger;
   long long per;           // tiles of a run
-  long long start_left;    // tiles of this run
+  long long start_left;    // tiles of this run, or (per = 0) its units
   int start[4];            // its first unit (sequence, head, block) and tile
-  long long scan[16];
+  long long scan[16];      // of the warps: tiles,
+  long long scan_units[16];  // units that have any,
+  int scan_most[16];         // and the most tiles of a unit
   uint32_t tmem_base;
   int abort_flag;
   uint8_t bad[2][kTileRing];       // 16-key blocks of a tile (of K, of V) that have no page
@@ -196,6 +203,15 @@ __device__ __forceinline__ int tiles_of(const Params& p, const Seq& s, int t0, i
   if (last < t0 || s.p0 + last < 0) return 0;
   return limit(p, s, last) / kBN + 1;
 }
+// Units of a head with any tile, and the most tiles of one: the last one's.
+template <int NT>
+__device__ __forceinline__ int seq_units(const Params& p, const Seq& s) {
+  const int tu = NT * p.tq_tokens;
+  return s.rows > 0 && s.p0 + s.rows > 0 ? (s.rows + tu - 1) / tu - max(-s.p0, 0) / tu : 0;
+}
+__device__ __forceinline__ int most_tiles(const Params& p, const Seq& s) {
+  return s.rows > 0 && s.p0 + s.rows > 0 ? limit(p, s, s.rows - 1) / kBN + 1 : 0;
+}
 template <int NT>
 __device__ __forceinline__ long long seq_tiles(const Params& p, const Seq& s) {
   const int tu = NT * p.tq_tokens;
@@ -222,10 +238,12 @@ template <int NT>
 struct Cursor {
   Seq s;
   int b, u, k, y;
+  bool units;      // `left` counts units, which are whole
   long long left;
   __device__ __forceinline__ void start(const Params& p, const Barriers* bars) {
     b = bars->start[0], u = bars->start[1], k = bars->start[2], y = bars->start[3];
     left = bars->start_left;
+    units = bars->per == 0;
     s = load_seq(p, b);
   }
   __device__ __forceinline__ bool next(const Params& p, Seg& seg) {
@@ -238,8 +256,8 @@ struct Cursor {
     }
     seg.s = s;
     seg.b = b, seg.u = u, seg.k = k, seg.nt = nt, seg.j0 = y;
-    seg.j1 = static_cast<int>(min(static_cast<long long>(nt), y + left));
-    left -= seg.j1 - seg.j0;
+    seg.j1 = units ? nt : static_cast<int>(min(static_cast<long long>(nt), y + left));
+    left -= units ? 1 : seg.j1 - seg.j0;
     y = 0;
     if (left > 0) advance(p, tu);
     return true;
@@ -295,59 +313,99 @@ struct Ring {
 // V_{n-2}, V_{n-1}.
 __device__ __forceinline__ int item_of_v(int j, int n) { return j <= n - 2 ? 2 * j + 2 : 2 * n - 1; }
 
-// Divides the list: every CTA sums all sequences' tiles, then the thread whose
-// share of the sequences holds the CTA's first tile finds it.
+// Divides the list: every CTA sums all sequences' tiles (plan_sum, then a barrier),
+// then the thread whose share of the sequences holds the CTA's first tile finds it
+// (plan_find, and another barrier).
+struct Plan {
+  Seq s;            // the thread's first sequence
+  int b0, b1;       // its share
+  long long tiles, tiles_to;  // of the share; of all up to its end within the warp
+  long long units, units_to;
+};
 template <typename C, int NT>
-__device__ __forceinline__ void plan(const Params& p, Barriers* bars) {
-  constexpr int kWarps = C::kThreads / 32;
+__device__ __forceinline__ void plan_sum(const Params& p, Barriers* bars, Plan& plan) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int each = (p.B + C::kThreads - 1) / C::kThreads;
-  const int b0 = min(p.B, static_cast<int>(threadIdx.x) * each), b1 = min(p.B, b0 + each);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_tiles<NT>(p, load_seq(p, b)) * p.heads;
-  long long incl = mine;
+  plan.b0 = min(p.B, static_cast<int>(threadIdx.x) * each), plan.b1 = min(p.B, plan.b0 + each);
+  plan.tiles = plan.units = 0;
+  int most = 0;
+  for (int b = plan.b0; b < plan.b1; ++b) {
+    const Seq s = load_seq(p, b);
+    if (b == plan.b0) plan.s = s;
+    plan.tiles += seq_tiles<NT>(p, s);
+    plan.units += seq_units<NT>(p, s);
+    most = max(most, most_tiles(p, s));
+  }
+  plan.tiles *= p.heads;
+  plan.units *= p.heads;
+  plan.tiles_to = plan.tiles;
+  plan.units_to = plan.units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const long long v = __shfl_up_sync(0xffffffffu, plan.tiles_to, o);
+    const long long u = __shfl_up_sync(0xffffffffu, plan.units_to, o);
+    if (lane >= o) plan.tiles_to += v, plan.units_to += u;
   }
-  if (lane == 31) bars->scan[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    bars->scan[warp] = plan.tiles_to;
+    bars->scan_units[warp] = plan.units_to;
+    bars->scan_most[warp] = most;
+  }
+}
+// (a division of 64 bits is a long one)
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+template <typename C, int NT>
+__device__ __forceinline__ long long plan_find(const Params& p, Barriers* bars, const Plan& plan) {
+  const int warp = threadIdx.x / 32;
+  long long tiles_before = plan.tiles_to - plan.tiles, units_before = plan.units_to - plan.units;
+  long long tiles = 0, units = 0;
+  int most = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += bars->scan[w];
-    total += bars->scan[w];
+  for (int w = 0; w < C::kThreads / 32; ++w) {
+    if (w < warp) tiles_before += bars->scan[w], units_before += bars->scan_units[w];
+    tiles += bars->scan[w];
+    units += bars->scan_units[w];
+    most = max(most, bars->scan_most[w]);
   }
-  const long long per = (total + p.ctas - 1) / p.ctas;
-  const long long x0 = blockIdx.x * per;
+  const long long run = divide(tiles + p.ctas - 1, p.ctas), run_units = divide(units + p.ctas - 1, p.ctas);
+  const bool whole = run_units * most <= run + kSplitCost<NT>;
+  const long long step = whole ? run_units : run, all = whole ? units : tiles;
+  const long long x0 = blockIdx.x * step, left = max(0LL, min(step, all - x0));
   if (threadIdx.x == 0) {
-    bars->per = per;
-    bars->start_left = max(0LL, min(per, total - x0));
+    bars->per = whole ? 0 : run;
+    bars->start_left = left;
   }
-  if (x0 >= before && x0 < before + mine) {
+  const long long before = whole ? units_before : tiles_before;
+  if (left > 0 && x0 >= before && x0 < before + (whole ? plan.units : plan.tiles)) {
     long long x = x0 - before;
-    for (int b = b0; b < b1; ++b) {
-      const Seq s = load_seq(p, b);
-      const long long head = seq_tiles<NT>(p, s);
-      if (x >= head * p.heads) {
-        x -= head * p.heads;
-        continue;
-      }
-      const int u = static_cast<int>(x / head);
-      x -= u * head;
-      const int tu = NT * p.tq_tokens;
-      int k = 0;
+    Seq s = plan.s;
+    int b = plan.b0;
+    long long head = whole ? seq_units<NT>(p, s) : seq_tiles<NT>(p, s);
+    while (x >= head * p.heads) {
+      x -= head * p.heads;
+      s = load_seq(p, ++b);
+      head = whole ? seq_units<NT>(p, s) : seq_tiles<NT>(p, s);
+    }
+    const int u = static_cast<int>(divide(x, head));
+    x -= u * head;
+    const int tu = NT * p.tq_tokens;
+    int k = max(-s.p0, 0) / tu;  // the first block with a real row
+    if (whole) {
+      k += static_cast<int>(x);
+      x = 0;
+    } else {
       for (;; ++k) {
         const int nt = tiles_of(p, s, k * tu, (k + 1) * tu);
         if (x < nt) break;
         x -= nt;
       }
-      bars->start[0] = b, bars->start[1] = u, bars->start[2] = k, bars->start[3] = static_cast<int>(x);
-      break;
     }
+    bars->start[0] = b, bars->start[1] = u, bars->start[2] = k, bars->start[3] = static_cast<int>(x);
   }
-  __syncthreads();
+  return left;
 }
 
 // The four pairs of E2M1 codes of a word as fp16 pairs, times a factor's fp16 pair:
@@ -365,6 +423,28 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
   return r;
+}
+
+// Whether rows [r0, 128) of a V tile hold a NaN or an infinity, which 0 times it tells:
+// one instruction for two elements.
+template <bool BF16, int COL_BLOCKS>
+__device__ __forceinline__ bool any_not_finite(const uint8_t* tile, int r0, int lane) {
+  uint32_t acc = 0u;
+  auto add = [&](uint32_t w) {
+    if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w), "r"(0u));
+    else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w), "r"(0u));
+  };
+#pragma unroll
+  for (int cb = 0; cb < COL_BLOCKS; ++cb) {
+    const uint8_t* block = tile + cb * (kBM * 128);
+#pragma unroll 8
+    for (int at = r0 * 128 + lane * 16; at < kBM * 128; at += 512) {
+      const uint4 v = *reinterpret_cast<const uint4*>(block + at);
+      add(v.x), add(v.y), add(v.z), add(v.w);
+    }
+  }
+  constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
+  return __any_sync(0xffffffffu, (acc & 0x7FFFu) > kInf || (acc >> 16 & 0x7FFFu) > kInf);
 }
 
 template <int D, bool BF16, int NT, bool FP4, int COPIES>
@@ -420,8 +500,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     }
   }
   wait_for_previous_kernel();
-  plan<C, NT>(p, bars);
-  if (bars->start_left == 0) return;  // fewer tiles than CTAs
+  {
+    Plan plan;
+    plan_sum<C, NT>(p, bars, plan);
+    __syncthreads();
+    if (plan_find<C, NT>(p, bars, plan) == 0) return;  // fewer tiles than CTAs
+  }
   if (warp == C::kMmaWarp) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
@@ -691,7 +775,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           if (!ok) break;
           raw_phase ^= 1u << st;
           uint8_t* base = sRing + st * C::kTileBytes + cb * C::kBlockBytes;
-          for (int r = max(0, lim0 + 1 - j * kBN); r < kBN; ++r) {
+          const int r0 = max(0, lim0 + 1 - j * kBN);
+          if (!any_not_finite<BF16, C::kColBlocks>(sRing + st * C::kTileBytes, r0, lane)) {
+            if (j == jm) {  // (later tiles add to what has been noted)
+              if (lane == 0) bars->nan_any[segs % kSegRing] = 0;
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(&bars->kv_full[st]);
+            continue;
+          }
+          for (int r = r0; r < kBN; ++r) {
             uint32_t* w = reinterpret_cast<uint32_t*>(base + r * 128 + ((chunk ^ (r & 7)) << 4) + in_chunk);
             const int key = j * kBN + r;
             if (key >= seg.s.n) {
@@ -1309,7 +1402,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       if (seg.j0 == 0 && threadIdx.x == 0) {
         const long long behind = seg.nt - (seg.j1 - seg.j0);  // the unit's tiles in the runs after this one
         p.parts[(static_cast<long long>(seg.b) * p.heads + seg.u) * p.blocks + seg.k] =
-            make_int2(blockIdx.x, 1 + static_cast<int>((behind + bars->per - 1) / bars->per));
+            make_int2(blockIdx.x, behind == 0 ? 1 : 1 + static_cast<int>(divide(behind + bars->per - 1, bars->per)));
       }
       tiles += seg.j1 - seg.j0;
       ++segs;
@@ -1347,36 +1440,63 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_paged_merge_kernel(cons
     const int u = static_cast<int>(unit / p.blocks % p.heads), b = static_cast<int>(unit / p.blocks / p.heads);
     const int x = rb / (kBM / 32), row = rb % (kBM / 32) * 32 + lane;
     const int tu = NT * p.tq_tokens;
+    // Everything is requested before it is known to be needed: the unit's parts with its
+    // lengths, the first parts' states and values before their weights.
+    const int2 said = p.parts[unit];
     const Seq s = load_seq(p, b);
     int2 part = make_int2(0, 0);
     if (tiles_of(p, s, k * tu, (k + 1) * tu) > 0) {
-      part = p.parts[unit];
+      part = said;
       if (part.y <= 1) continue;  // finished by one CTA
     }
     const int t = k * tu + x * p.tq_tokens + row / p.hb, head = (u % p.nblk) * p.hb + row % p.hb;
     if (row >= rows_used || head >= p.g || t >= p.S) continue;
-    float M = -INFINITY;
     auto state = [&](int i) { return (part.x + i) * 2LL + (i == 0 ? 1 : 0); };
-    for (int i = 0; i < part.y; ++i) M = fmaxf(M, p.part_ml[state(i) * (NT * kBM) + x * kBM + row].x);
+    auto load_ml = [&](int i) { return p.part_ml[state(i) * (NT * kBM) + x * kBM + row]; };
+    auto load_o = [&](int i, float4 (&v)[kSlice / 4]) {
+      const float4* src = reinterpret_cast<const float4*>(p.part_o) +
+                          (state(i) * (D / 4) + slice * (kSlice / 4)) * (NT * kBM) + x * kBM + row;
+#pragma unroll
+      for (int e = 0; e < kSlice / 4; ++e) v[e] = src[e * (NT * kBM)];
+    };
+    constexpr int kAhead = 4;
+    float2 ml[kAhead];
+    float4 v[kAhead][kSlice / 4];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (i < part.y) {
+        ml[i] = load_ml(i);
+        load_o(i, v[i]);
+      }
+    }
+    float M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+#pragma unroll 8
+    for (int i = kAhead; i < part.y; ++i) M = fmaxf(M, load_ml(i).x);
     float l = 0.f;
     float acc[kSlice];
 #pragma unroll
     for (int e = 0; e < kSlice; ++e) acc[e] = 0.f;
-    for (int i = 0; i < part.y; ++i) {
-      const float2 ml = p.part_ml[state(i) * (NT * kBM) + x * kBM + row];
-      if (ml.y == 0.f) continue;  // no key of this part counts
-      const float f = ml.x == M ? 1.f : ex2_approx(ml.x - M);
-      l = fmaf(f, ml.y, l);
-      const float4* src = reinterpret_cast<const float4*>(p.part_o) +
-                          (state(i) * (D / 4) + slice * (kSlice / 4)) * (NT * kBM) + x * kBM + row;
+    // (a part without a key that counts has no values)
+    auto add = [&](float2 m, const float4 (&o)[kSlice / 4]) {
+      if (m.y == 0.f) return;
+      const float f = m.x == M ? 1.f : ex2_approx(m.x - M);
+      l = fmaf(f, m.y, l);
 #pragma unroll
       for (int e = 0; e < kSlice / 4; ++e) {
-        const float4 v = src[e * (NT * kBM)];
-        acc[4 * e] = fmaf(f, v.x, acc[4 * e]);
-        acc[4 * e + 1] = fmaf(f, v.y, acc[4 * e + 1]);
-        acc[4 * e + 2] = fmaf(f, v.z, acc[4 * e + 2]);
-        acc[4 * e + 3] = fmaf(f, v.w, acc[4 * e + 3]);
+        acc[4 * e] = fmaf(f, o[e].x, acc[4 * e]);
+        acc[4 * e + 1] = fmaf(f, o[e].y, acc[4 * e + 1]);
+        acc[4 * e + 2] = fmaf(f, o[e].z, acc[4 * e + 2]);
+        acc[4 * e + 3] = fmaf(f, o[e].w, acc[4 * e + 3]);
       }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < part.y) add(ml[i], v[i]);
+#pragma unroll 4
+    for (int i = kAhead; i < part.y; ++i) {
+      load_o(i, v[0]);
+      add(load_ml(i), v[0]);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint32_t out[kSlice / 2];
@@ -1446,12 +1566,19 @@ int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   return launch_after(prefill_paged_merge_kernel<D, NT>, dim3(static_cast<unsigned>(ctas)), kMergeThreads, a.stream, p);
 }
 
+constexpr long long kCopyRun = 16;  // tiles of a CTA that make copies worth their folding
+
 template <int D, bool BF16, bool FP4>
 int launch_nt(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   if (s.nt == 2) return launch_t<D, BF16, 2, FP4, 1>(p, a, s);
-  const int rows = s.hb * s.tokens;
-  if (rows <= kBM / 4) return launch_t<D, BF16, 1, FP4, 4>(p, a, s);
-  if (rows <= kBM / 2) return launch_t<D, BF16, 1, FP4, 2>(p, a, s);
+  if constexpr (FP4 || D == 64) {
+    const int rows = s.hb * s.tokens;
+    const long long tiles = s.units * (((p.max_pages << p.page_shift) + kBN - 1) / kBN);  // at most
+    if (tiles >= kCopyRun * p.ctas) {
+      if (rows <= kBM / 4) return launch_t<D, BF16, 1, FP4, 4>(p, a, s);
+      if (rows <= kBM / 2) return launch_t<D, BF16, 1, FP4, 2>(p, a, s);
+    }
+  }
   return launch_t<D, BF16, 1, FP4, 1>(p, a, s);
 }
 template <int D, bool BF16>
