@@ -51,7 +51,7 @@ constexpr float kRescaleThreshold = 8.f;  // base-2 units
 // A scale of scores is at least this, so that -inf times it stays -inf; finite products
 // of Q and K are then as good as 0.
 constexpr float kLeastScale = 1.1754944e-38f;
-constexpr int kSegRing = 8;       // segments whose notes of the guard are kept
+constexpr int kSegRing = 4;       // segments whose notes of the guard are kept: it is at most 3 ahead
 // Key tiles that the states of split units cost (writing, and a second kernel that has
 // to fold them) for units of one and two row tiles.
 template <int NT>
@@ -66,6 +66,7 @@ constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
 template <int D, int NT, bool FP4, int COPIES>
 struct Cfg {
   static_assert(NT == 1 || COPIES == 1, "copies are of one tile");
+  static constexpr int kDim = D;
   static constexpr int kRows = kBM / COPIES;  // of a copy
   static constexpr int kCols = kBN / COPIES;  // keys of a copy
   // Tensor memory has room for P unless there are two tiles of d = 128, and with one
@@ -113,7 +114,7 @@ struct Cfg {
   static constexpr int kRingOff = kPOff + NT * kStageBytes;
   static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
   static constexpr int kBarOff = kRawOff + kRawStages * kRawBytes;
-  static constexpr int kSmemBytes = kBarOff + 2048;
+  static constexpr int kSmemBytes = kBarOff + 3072;
   static constexpr int kMmaWarp = 4 * NT;  // tile x's issuer is warp kMmaWarp + x
   static constexpr int kLoadWarp = 4 * NT + 2;
   static constexpr int kGuardWarp = 4 * NT + 3;
@@ -155,6 +156,7 @@ struct Params {
   float scale_log2;  // |scale| log2 e (of a scale of 0: log2 e)
   float sign;        // -1 or 0 where scale is negative or 0, and scores are taken times it
   int ctas;
+  int cluster;       // CTAs of each unit, which fold their states themselves; 0: runs of the list
   int* status;
 };
 
@@ -172,13 +174,14 @@ struct __align__(8) Barriers {
   long long scan[16];      // of the warps: tiles,
   long long scan_units[16];  // units that have any,
   int scan_most[16];         // and the most tiles of a unit
+  float state[2 * kBM];    // of the rows, with clusters: log2 of the sum of weights
   uint32_t tmem_base;
   int abort_flag;
   uint8_t bad[2][kTileRing];       // 16-key blocks of a tile (of K, of V) that have no page
   uint8_t nan_any[kSegRing];
   uint8_t nan_from[kSegRing][128]; // column's first non-finite key behind the first row's last key, - 1
 };
-static_assert(sizeof(Barriers) <= 2048, "barriers fit");
+static_assert(sizeof(Barriers) <= 3072, "barriers fit");
 
 // A sequence: cached tokens, position of query row 0 (negative: the first -p0 rows
 // are padding), query rows.
@@ -245,6 +248,12 @@ struct Cursor {
     left = bars->start_left;
     units = bars->per == 0;
     s = load_seq(p, b);
+  }
+  // The tiles [j0, j1) of one unit.
+  __device__ __forceinline__ void start(const Seg& seg) {
+    s = seg.s, b = seg.b, u = seg.u, k = seg.k, y = seg.j0;
+    units = false;
+    left = seg.j1 - seg.j0;
   }
   __device__ __forceinline__ bool next(const Params& p, Seg& seg) {
     if (left <= 0) return false;
@@ -447,6 +456,72 @@ __device__ __forceinline__ bool any_not_finite(const uint8_t* tile, int r0, int 
   return __any_sync(0xffffffffu, (acc & 0x7FFFu) > kInf || (acc >> 16 & 0x7FFFu) > kInf);
 }
 
+// Where the first 16-byte piece of a row's state's half with columns 4 c4, .. is.
+template <typename C>
+__device__ __forceinline__ uint8_t* state_row(uint8_t* smem, int x, int row, int c4) {
+  constexpr int kHalf = C::kDim / 8;  // pieces of half a row
+  return (c4 < kHalf ? smem + C::kQOff + x * C::kQBytes : smem + C::kPOff + x * C::kStageBytes) + row * (kHalf * 16);
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// The cluster's CTAs fold their states, a share of the unit's rows each, and write
+// them; rows that count no key become zeros.  By the softmax threads, lanes along
+// a row.
+template <typename C, int D, bool BF16, int NT>
+__device__ __forceinline__ void fold_cluster(const Params& p, const Seg& seg, uint8_t* smem, Barriers* bars) {
+  const int rows = NT * kBM / p.cluster, rank = blockIdx.x % p.cluster;
+  for (int i = threadIdx.x; i < rows * (D / 4); i += NT * kBM) {
+    const int at = rank * rows + i / (D / 4), c4 = i % (D / 4);
+    const int x = at / kBM, row = at % kBM;
+    const int row_token = row / p.hb, head = (seg.u % p.nblk) * p.hb + row % p.hb;
+    const int t = (seg.k * NT + x) * p.tq_tokens + row_token;
+    if (row_token >= p.tq_tokens || head >= p.g || t >= p.S) continue;
+    float m[8];
+    float4 o[8];
+    const uint8_t* piece = state_row<C>(smem, x, row, c4) + ((c4 % (D / 8) ^ (row & 7)) << 4);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      m[r] = -INFINITY;
+      o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < p.cluster) {
+        m[r] = ld_cluster(mapa_shared(&bars->state[at], r));
+        o[r] = ld_cluster4(mapa_shared(piece, r));
+      }
+    }
+    float M = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) M = fmaxf(M, m[r]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      if (m[r] == -INFINITY) continue;  // no key counts (and its O is not set)
+      const float f = m[r] == M ? 1.f : ex2_approx(m[r] - M);
+      sum += f;
+      acc.x = fmaf(f, o[r].x, acc.x), acc.y = fmaf(f, o[r].y, acc.y);
+      acc.z = fmaf(f, o[r].z, acc.z), acc.w = fmaf(f, o[r].w, acc.w);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long long hrow = (static_cast<long long>(seg.b) * p.H + (seg.u / p.nblk) * p.g + head) * p.S + t;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + hrow * D + c4 * 4) =
+        make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+    if (c4 == 0 && p.lse != nullptr)
+      p.lse[hrow] = sum == 0.f ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994531f;
+  }
+}
+
 template <int D, bool BF16, int NT, bool FP4, int COPIES>
 __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     prefill_paged_kernel(const __grid_constant__ Params p) {
@@ -500,7 +575,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     }
   }
   wait_for_previous_kernel();
-  {
+  Seg seg{};
+  if (COPIES == 1 && p.cluster > 0) {
+    const int unit = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+    seg.k = unit % p.blocks;
+    seg.u = unit / p.blocks % p.heads;
+    seg.b = unit / p.blocks / p.heads;
+    seg.s = load_seq(p, seg.b);
+    seg.nt = tiles_of(p, seg.s, seg.k * NT * p.tq_tokens, (seg.k + 1) * NT * p.tq_tokens);
+    seg.j0 = seg.nt * rank / p.cluster;
+    seg.j1 = seg.nt * (rank + 1) / p.cluster;
+  } else {
     Plan plan;
     plan_sum<C, NT>(p, bars, plan);
     __syncthreads();
@@ -515,8 +600,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   Cursor<NT> cur;
-  cur.start(p, bars);
-  Seg seg{};
+  if (COPIES == 1 && p.cluster > 0) cur.start(seg);
+  else cur.start(p, bars);
 
   if (FP4 && warp >= C::kConvertWarp) {
     // ================================================================ conversion of 4 bits
@@ -1305,6 +1390,33 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           if (!whole) p.part_ml[part * kBM + crow] = make_float2(M, L);
           else if (p.lse != nullptr) p.lse[hrow] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
         }
+      } else if (p.cluster > 0) {
+        // The row's state: O normalised, and log2 of the sum of its weights.  O lies in
+        // this tile's places of Q and P, which are through, half a row each; 16-byte
+        // pieces are permuted against bank conflicts.
+        const bool counts = real && nx > 0 && l != 0.f;
+        bars->state[x * kBM + row] = counts ? r * lam + __log2f(l) : -INFINITY;
+        if (__any_sync(0xffffffffu, counts)) {
+          const float inv = vd / l;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t u[32];
+            tmem_ld32(o_tmem + c * 32, u);
+            tmem_wait_ld();
+            reg_fence32(u);
+            if (nan_any) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (seen > nan_from[c * 32 + i]) u[i] = 0x7FFFFFFFu;
+            }
+            uint8_t* dst = state_row<C>(smem, x, row, c * 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(dst + (((c * 8 + i) % (D / 8) ^ (row & 7)) << 4)) =
+                  make_float4(__uint_as_float(u[4 * i]) * inv, __uint_as_float(u[4 * i + 1]) * inv,
+                              __uint_as_float(u[4 * i + 2]) * inv, __uint_as_float(u[4 * i + 3]) * inv);
+          }
+        }
       } else if (seg.whole()) {
         [[maybe_unused]] long long store_row = -1;
         if constexpr (C::kDirectO) {
@@ -1399,7 +1511,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         }
       }
       // The CTA that has the unit's first tile says where its parts are.
-      if (seg.j0 == 0 && threadIdx.x == 0) {
+      if (seg.j0 == 0 && threadIdx.x == 0 && p.cluster == 0) {
         const long long behind = seg.nt - (seg.j1 - seg.j0);  // the unit's tiles in the runs after this one
         p.parts[(static_cast<long long>(seg.b) * p.heads + seg.u) * p.blocks + seg.k] =
             make_int2(blockIdx.x, behind == 0 ? 1 : 1 + static_cast<int>(divide(behind + bars->per - 1, bars->per)));
@@ -1408,6 +1520,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       ++segs;
     }
     if (staged && wq == 0 && lane == 0) bulk_wait_group_read0();
+    if (COPIES == 1 && p.cluster > 0) {
+      if (segs == 0) bars->state[x * kBM + row] = -INFINITY;  // no tile for this CTA
+      cluster_sync_all();
+      if (ok) fold_cluster<C, D, BF16, NT>(p, seg, smem, bars);
+    }
+  }
+  // The others' arrivals at the first barrier, and the second: no CTA ends while its
+  // states are read.
+  if (COPIES == 1 && p.cluster > 0) {
+    if (warp >= C::kMmaWarp) cluster_sync_all();
+    cluster_sync_all();
   }
 
   // ---- teardown: all TMEM traffic done before the allocator warp frees it
@@ -1493,10 +1616,16 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_paged_merge_kernel(cons
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (i < part.y) add(ml[i], v[i]);
-#pragma unroll 4
-    for (int i = kAhead; i < part.y; ++i) {
-      load_o(i, v[0]);
-      add(load_ml(i), v[0]);
+    for (int base = kAhead; base < part.y; base += kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (base + i < part.y) {
+          ml[i] = load_ml(base + i);
+          load_o(base + i, v[i]);
+        }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (base + i < part.y) add(ml[i], v[i]);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint32_t out[kSlice / 2];
@@ -1537,6 +1666,18 @@ int max_ctas(const Shape& s, int max_len) {
   return s.units >= kMaxCtas || s.units * per_unit >= kMaxCtas ? kMaxCtas : static_cast<int>(s.units * per_unit);
 }
 
+// CTAs of a cluster that takes a unit, or 0 where runs of the list are taken.  The host
+// knows what the pages of a sequence can hold, not the lengths; clusters need neither
+// the division of the list nor the second kernel, and are for units of few tiles.
+// (With one CTA an SM, 16 clusters of eight, 32 of four and 72 of two run at once.)
+constexpr int kClusterRun = 6;  // tiles of a CTA
+int cluster_of(const Shape& s, int max_len, int num_sms) {
+  const int tiles = (max_len + kBN - 1) / kBN;
+  int c = s.units <= 16 ? 8 : s.units <= 32 ? 4 : s.units <= 72 ? 2 : 1;
+  while (c > 1 && c > tiles) c /= 2;
+  return s.units <= num_sms && tiles <= kClusterRun * c ? c : 0;
+}
+
 template <int D, bool BF16, int NT, bool FP4, int COPIES>
 int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   using C = Cfg<D, NT, FP4, COPIES>;
@@ -1559,6 +1700,10 @@ int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   auto kern = prefill_paged_kernel<D, BF16, NT, FP4, COPIES>;
   static std::atomic<unsigned long long> attr_done{0};  // per instantiation
   if (!set_smem_limit_once(kern, C::kSmemBytes, attr_done)) return -1;
+  if (COPIES == 1) p.cluster = cluster_of(s, p.max_pages << p.page_shift, a.num_sms);
+  if (p.cluster > 0)
+    return launch_after(kern, dim3(static_cast<unsigned>(s.units * p.cluster)), C::kThreads, a.stream, p, C::kSmemBytes,
+                        p.cluster);
   if (launch_after(kern, dim3(static_cast<unsigned>(p.ctas)), C::kThreads, a.stream, p, C::kSmemBytes) != 0) return -1;
   const long long warps = s.units * (NT * kBM / 32) * (D / 16);
   long long ctas = (warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
