@@ -160,6 +160,12 @@ struct Params {
   int* status;
 };
 
+// A sequence: cached tokens, position of query row 0 (negative: the first -p0 rows
+// are padding), query rows.
+struct Seq {
+  int n, p0, rows;
+};
+
 struct __align__(8) Barriers {
   uint64_t q_full, q_empty;
   uint64_t q_ready[2];     // queries converted to fp16 (bf16 over 4 bits), or in tensor memory
@@ -171,6 +177,7 @@ struct __align__(8) Barriers {
   long long per;           // tiles of a run
   long long start_left;    // tiles of this run, or (per = 0) its units
   int start[4];            // its first unit (sequence, head, block) and tile
+  Seq start_seq;
   long long scan[16];      // of the warps: tiles,
   long long scan_units[16];  // units that have any,
   int scan_most[16];         // and the most tiles of a unit
@@ -183,11 +190,6 @@ struct __align__(8) Barriers {
 };
 static_assert(sizeof(Barriers) <= 3072, "barriers fit");
 
-// A sequence: cached tokens, position of query row 0 (negative: the first -p0 rows
-// are padding), query rows.
-struct Seq {
-  int n, p0, rows;
-};
 __device__ __forceinline__ Seq load_seq(const Params& p, int b) {
   Seq s;
   const int len = max(p.seqlens[b], 0);
@@ -247,7 +249,7 @@ struct Cursor {
     b = bars->start[0], u = bars->start[1], k = bars->start[2], y = bars->start[3];
     left = bars->start_left;
     units = bars->per == 0;
-    s = load_seq(p, b);
+    s = bars->start_seq;
   }
   // The tiles [j0, j1) of one unit.
   __device__ __forceinline__ void start(const Seg& seg) {
@@ -281,6 +283,10 @@ struct Cursor {
     return true;
   }
 };
+
+// KV head and first query head (of the KV head's) of a unit.
+__device__ __forceinline__ int kv_head(const Params& p, int u) { return p.nblk == 1 ? u : u / p.nblk; }
+__device__ __forceinline__ int first_head(const Params& p, int u) { return p.nblk == 1 ? 0 : u % p.nblk * p.hb; }
 
 // What tile x of a segment's unit is.
 struct TileRows {
@@ -413,6 +419,7 @@ __device__ __forceinline__ long long plan_find(const Params& p, Barriers* bars, 
       }
     }
     bars->start[0] = b, bars->start[1] = u, bars->start[2] = k, bars->start[3] = static_cast<int>(x);
+    bars->start_seq = s;
   }
   return left;
 }
@@ -482,11 +489,12 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
 // a row.
 template <typename C, int D, bool BF16, int NT>
 __device__ __forceinline__ void fold_cluster(const Params& p, const Seg& seg, uint8_t* smem, Barriers* bars) {
-  const int rows = NT * kBM / p.cluster, rank = blockIdx.x % p.cluster;
-  for (int i = threadIdx.x; i < rows * (D / 4); i += NT * kBM) {
-    const int at = rank * rows + i / (D / 4), c4 = i % (D / 4);
+  const int shift = 31 - __clz(p.cluster), rank = blockIdx.x & (p.cluster - 1);
+#pragma unroll 2
+  for (int i = threadIdx.x; i < (NT * kBM >> shift) * (D / 4); i += NT * kBM) {
+    const int at = (i / (D / 4) << shift) + rank, c4 = i % (D / 4);  // every p.cluster-th row
     const int x = at / kBM, row = at % kBM;
-    const int row_token = row / p.hb, head = (seg.u % p.nblk) * p.hb + row % p.hb;
+    const int row_token = row / p.hb, head = first_head(p, seg.u) + row % p.hb;
     const int t = (seg.k * NT + x) * p.tq_tokens + row_token;
     if (row_token >= p.tq_tokens || head >= p.g || t >= p.S) continue;
     float m[8];
@@ -514,7 +522,7 @@ __device__ __forceinline__ void fold_cluster(const Params& p, const Seg& seg, ui
       acc.z = fmaf(f, o[r].z, acc.z), acc.w = fmaf(f, o[r].w, acc.w);
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const long long hrow = (static_cast<long long>(seg.b) * p.H + (seg.u / p.nblk) * p.g + head) * p.S + t;
+    const long long hrow = (static_cast<long long>(seg.b) * p.H + kv_head(p, seg.u) * p.g + head) * p.S + t;
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + hrow * D + c4 * 4) =
         make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
     if (c4 == 0 && p.lse != nullptr)
@@ -577,14 +585,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
   wait_for_previous_kernel();
   Seg seg{};
   if (COPIES == 1 && p.cluster > 0) {
-    const int unit = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
-    seg.k = unit % p.blocks;
-    seg.u = unit / p.blocks % p.heads;
-    seg.b = unit / p.blocks / p.heads;
+    // Grid (clusters of the token blocks, heads, sequences); sizes are powers of two.
+    const int shift = 31 - __clz(p.cluster), rank = blockIdx.x & (p.cluster - 1);
+    seg.k = blockIdx.x >> shift;
+    seg.u = blockIdx.y;
+    seg.b = blockIdx.z;
     seg.s = load_seq(p, seg.b);
     seg.nt = tiles_of(p, seg.s, seg.k * NT * p.tq_tokens, (seg.k + 1) * NT * p.tq_tokens);
-    seg.j0 = seg.nt * rank / p.cluster;
-    seg.j1 = seg.nt * (rank + 1) / p.cluster;
+    seg.j0 = seg.nt * rank >> shift;
+    seg.j1 = seg.nt * (rank + 1) >> shift;
   } else {
     Plan plan;
     plan_sum<C, NT>(p, bars, plan);
@@ -689,9 +698,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       // loads keys (and queries), another values; lanes of the first half copy codes,
       // those of the second factors (a page's rows of one head lie one behind another).
       const bool loads_v = FP4 && warp == C::kGuardWarp;
-      const int boxes = kBN / p.box_rows;
-      const int box = lane % boxes, cb = lane / boxes;
-      const int box_shift = 31 - __clz(p.box_rows);
+      const int box_shift = min(p.page_shift, 7), boxes_shift = 7 - box_shift;
+      const int boxes = 1 << boxes_shift;
+      const int box = lane & (boxes - 1), cb = lane >> boxes_shift;
       const uint64_t keep = policy_evict_last(), once = policy_evict_first();
       const int missing = p.n_pages * p.Hkv;  // a coordinate outside: zeros
       const int in_page = (1 << p.page_shift) - 1;
@@ -699,9 +708,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       bool ok = true;
       // Pages are looked up for 32 boxes at a time, a window ahead of their use: lane l
       // has box l % boxes of the window's tile l / boxes (-1 behind the sequence).
-      const int per_window = 32 / boxes;
+      const int per_window = 32 >> boxes_shift;
       auto lookup = [&](int w) {
-        const int key = (seg.j0 + w * per_window + lane / boxes) * kBN + (box << box_shift);
+        const int key = (seg.j0 + w * per_window + cb) * kBN + (box << box_shift);
         return key < seg.s.n ? p.page_table[static_cast<long long>(seg.b) * p.max_pages + (key >> p.page_shift)] : -1;
       };
       // Notes the 16-key blocks without a page of tile number `at`: they are left out.
@@ -726,7 +735,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
               for (int c = 0; c < C::kColBlocks; ++c)
                 for (int i = 0; i < kLoads; ++i)
                   tma_load_5d(sQ + x * C::kQBytes + c * C::kQRows * 128 + i * C::kRows * 128, &p.tq, &bars->q_full,
-                              c * 64, (seg.u % p.nblk) * p.hb, seg.u / p.nblk, t0 + x * p.tq_tokens, seg.b, once);
+                              c * 64, first_head(p, seg.u), kv_head(p, seg.u), t0 + x * p.tq_tokens, seg.b, once);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -740,12 +749,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         Ring at(loads_v ? C::kRawKStages : 0, loads_v ? C::kRawStages : C::kRawKStages);
         int filled = 0;
         while (ok && cur.next(p, seg)) {
-          const int kvh = seg.u / p.nblk;
+          const int kvh = kv_head(p, seg.u);
+          int now = lookup(0), next = lookup(1), in = 0, window = 1;
           if (!loads_v) {
             load_q();
             if (!ok) break;
           }
-          int now = lookup(0), next = lookup(1), in = 0, window = 1;
           int key = seg.j0 * kBN + (box << box_shift);
           for (int j = seg.j0; j < seg.j1; ++j, ++tile, key += kBN, at.next()) {
             const int page = __shfl_sync(0xffffffffu, now, in * boxes + box);
@@ -784,7 +793,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         Ring ring_k(0, C::kKStages), ring_v(C::kKStages, C::kStages);
         int filled[2] = {0, 0};
         while (ok && cur.next(p, seg)) {
-          const int kvh = seg.u / p.nblk;
+          int now = lookup(0), next = lookup(1), window = 1;  // windows of V's tile and the one behind it
+          const int kvh = kv_head(p, seg.u);
           int lim0;
           const int jm = first_masked<NT>(p, seg, lim0);
           load_q();
@@ -809,14 +819,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             ++filled[is_v && !C::kOneRing];
           };
           const int n = seg.j1 - seg.j0;
-          int now = lookup(0), next = lookup(1);  // windows of V's tile and the one behind it
           issue(false, seg.j0, __shfl_sync(0xffffffffu, now, box));
           for (int t = 0, in = 0; ok && t < n; ++t) {  // `in`: V's tile in its window
             const int page_v = __shfl_sync(0xffffffffu, now, in * boxes + box);
             if (++in == per_window) {
               in = 0;
               now = next;
-              next = lookup(t / per_window + 2);
+              next = lookup(++window);
             }
             if (t + 1 < n) issue(false, seg.j0 + t + 1, __shfl_sync(0xffffffffu, now, in * boxes + box));
             if (ok) issue(true, seg.j0 + t, page_v);
@@ -1073,12 +1082,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     while (ok && cur.next(p, seg)) {
       const TileRows tile(p, seg, x, NT);
       const int t = tile.t0 + row_token;
-      const int head = (seg.u % p.nblk) * p.hb + row_head;  // of the KV head's query heads
+      const int head = first_head(p, seg.u) + row_head;  // of the KV head's query heads
       const bool in_tile = row_token < p.tq_tokens && head < p.g;
       const bool real = in_tile && t < seg.s.rows && seg.s.p0 + t >= 0;
       const int lim = real ? limit(p, seg.s, t) : -1;
       if constexpr (FP4) {
-        const int kvh = seg.u / p.nblk;
+        const int kvh = kv_head(p, seg.u);
         lam = fmaxf(p.scale_log2 * (p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f), kLeastScale);
         vd = p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
       }
@@ -1330,7 +1339,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         }
         const float weight = !counts ? 0.f : m == M ? vd : vd * ex2_approx(m - M);
         const bool writes = in_tile && t < p.S;
-        const long long hrow = (static_cast<long long>(seg.b) * p.H + (seg.u / p.nblk) * p.g + head) * p.S + t;
+        const long long hrow = (static_cast<long long>(seg.b) * p.H + kv_head(p, seg.u) * p.g + head) * p.S + t;
         const long long part = blockIdx.x * 2LL + (seg.j0 > 0 ? 0 : 1);
         const float inv = L == 0.f ? 0.f : 1.f / L;
         float4* fold = reinterpret_cast<float4*>(sP);  // [8][kBM]
@@ -1420,7 +1429,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       } else if (seg.whole()) {
         [[maybe_unused]] long long store_row = -1;
         if constexpr (C::kDirectO) {
-          if (in_tile && t < p.S) store_row = (static_cast<long long>(seg.b) * p.H + (seg.u / p.nblk) * p.g + head) * p.S + t;
+          if (in_tile && t < p.S) store_row = (static_cast<long long>(seg.b) * p.H + kv_head(p, seg.u) * p.g + head) * p.S + t;
         }
         if (tile.t0 < p.S) {
           const float inv = (!real || l == 0.f) ? 0.f : vd / l;
@@ -1470,15 +1479,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             if (!ok) break;
             if (wq == 0 && lane == 0) {
               for (int cb = 0; cb < C::kColBlocks; ++cb)
-                tma_store_5d(&p.to, sP + x * C::kStageBytes + cb * C::kBlockBytes, cb * 64, (seg.u % p.nblk) * p.hb,
-                             seg.u / p.nblk, tile.t0, seg.b);
+                tma_store_5d(&p.to, sP + x * C::kStageBytes + cb * C::kBlockBytes, cb * 64, first_head(p, seg.u),
+                             kv_head(p, seg.u), tile.t0, seg.b);
               bulk_commit_group();
             }
             staged = true;
           }
           if (p.lse != nullptr && in_tile && t < p.S) {
             const float lse = !real || l == 0.f ? -INFINITY : (r * lam + __log2f(l)) * 0.69314718055994531f;
-            p.lse[(static_cast<long long>(seg.b) * p.H + (seg.u / p.nblk) * p.g + head) * p.S + t] = lse;
+            p.lse[(static_cast<long long>(seg.b) * p.H + kv_head(p, seg.u) * p.g + head) * p.S + t] = lse;
           }
         }
       } else {
@@ -1702,7 +1711,7 @@ int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   if (!set_smem_limit_once(kern, C::kSmemBytes, attr_done)) return -1;
   if (COPIES == 1) p.cluster = cluster_of(s, p.max_pages << p.page_shift, a.num_sms);
   if (p.cluster > 0)
-    return launch_after(kern, dim3(static_cast<unsigned>(s.units * p.cluster)), C::kThreads, a.stream, p, C::kSmemBytes,
+    return launch_after(kern, dim3(p.blocks * p.cluster, p.heads, p.B), C::kThreads, a.stream, p, C::kSmemBytes,
                         p.cluster);
   if (launch_after(kern, dim3(static_cast<unsigned>(p.ctas)), C::kThreads, a.stream, p, C::kSmemBytes) != 0) return -1;
   const long long warps = s.units * (NT * kBM / 32) * (D / 16);
