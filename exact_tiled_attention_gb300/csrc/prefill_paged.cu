@@ -487,34 +487,30 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
 // The cluster's CTAs fold their states, a share of the unit's rows each, and write
 // them; rows that count no key become zeros.  By the softmax threads, lanes along
 // a row.
-template <typename C, int D, bool BF16, int NT>
+template <typename C, int D, bool BF16, int NT, int CTAS>
 __device__ __forceinline__ void fold_cluster(const Params& p, const Seg& seg, uint8_t* smem, Barriers* bars) {
-  const int shift = 31 - __clz(p.cluster), rank = blockIdx.x & (p.cluster - 1);
-#pragma unroll 2
-  for (int i = threadIdx.x; i < (NT * kBM >> shift) * (D / 4); i += NT * kBM) {
-    const int at = (i / (D / 4) << shift) + rank, c4 = i % (D / 4);  // every p.cluster-th row
+  const int rank = blockIdx.x % CTAS;
+#pragma unroll CTAS == 8 ? 2 : 8 / CTAS  // several rows' loads at a time
+  for (int i = threadIdx.x; i < NT * kBM / CTAS * (D / 4); i += NT * kBM) {
+    const int at = i / (D / 4) * CTAS + rank, c4 = i % (D / 4);  // every CTAS-th row
     const int x = at / kBM, row = at % kBM;
     const int row_token = row / p.hb, head = first_head(p, seg.u) + row % p.hb;
     const int t = (seg.k * NT + x) * p.tq_tokens + row_token;
     if (row_token >= p.tq_tokens || head >= p.g || t >= p.S) continue;
-    float m[8];
-    float4 o[8];
+    float m[CTAS];
+    float4 o[CTAS];
     const uint8_t* piece = state_row<C>(smem, x, row, c4) + ((c4 % (D / 8) ^ (row & 7)) << 4);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      m[r] = -INFINITY;
-      o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < p.cluster) {
-        m[r] = ld_cluster(mapa_shared(&bars->state[at], r));
-        o[r] = ld_cluster4(mapa_shared(piece, r));
-      }
+    for (int r = 0; r < CTAS; ++r) {
+      m[r] = ld_cluster(mapa_shared(&bars->state[at], r));
+      o[r] = ld_cluster4(mapa_shared(piece, r));
     }
     float M = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) M = fmaxf(M, m[r]);
+    for (int r = 0; r < CTAS; ++r) M = fmaxf(M, m[r]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
+    for (int r = 0; r < CTAS; ++r) {
       if (m[r] == -INFINITY) continue;  // no key counts (and its O is not set)
       const float f = m[r] == M ? 1.f : ex2_approx(m[r] - M);
       sum += f;
@@ -1532,7 +1528,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     if (COPIES == 1 && p.cluster > 0) {
       if (segs == 0) bars->state[x * kBM + row] = -INFINITY;  // no tile for this CTA
       cluster_sync_all();
-      if (ok) fold_cluster<C, D, BF16, NT>(p, seg, smem, bars);
+      if (ok) {
+        if (p.cluster == 8) fold_cluster<C, D, BF16, NT, 8>(p, seg, smem, bars);
+        else if (p.cluster == 4) fold_cluster<C, D, BF16, NT, 4>(p, seg, smem, bars);
+        else if (p.cluster == 2) fold_cluster<C, D, BF16, NT, 2>(p, seg, smem, bars);
+        else fold_cluster<C, D, BF16, NT, 1>(p, seg, smem, bars);
+      }
     }
   }
   // The others' arrivals at the first barrier, and the second: no CTA ends while its
