@@ -149,6 +149,7 @@ struct Params {
   float2* part_ml; // [ctas][2][NT * 128]: m in base-2 units, l
   int2* parts;     // [B][heads][blocks]: first CTA, number of parts (1: finished)
   int B, H, Hkv, S, g;
+  int hb_inverse;  // 65536 / hb rounded up: row / hb = row * hb_inverse >> 16 for the 128 rows of a tile
   int hb, tq_tokens, nblk, heads, blocks;  // heads a tile; tokens a tile; head blocks; Hkv * nblk; token blocks of S
   int page_shift, n_pages, max_pages, box_rows;
   int causal;
@@ -283,6 +284,9 @@ struct Cursor {
     return true;
   }
 };
+
+// The query token and head of a tile's row.
+__device__ __forceinline__ int token_of(const Params& p, int row) { return row * p.hb_inverse >> 16; }
 
 // KV head and first query head (of the KV head's) of a unit.
 __device__ __forceinline__ int kv_head(const Params& p, int u) { return p.nblk == 1 ? u : u / p.nblk; }
@@ -489,40 +493,54 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
 // a row.
 template <typename C, int D, bool BF16, int NT, int CTAS>
 __device__ __forceinline__ void fold_cluster(const Params& p, const Seg& seg, uint8_t* smem, Barriers* bars) {
+  constexpr int kItems = NT * kBM / CTAS * (D / 4);          // pieces of four columns
+  constexpr int kAtOnce = CTAS == 8 ? 2 : CTAS == 4 ? 4 : 8;  // of a thread, requested together
   const int rank = blockIdx.x % CTAS;
-#pragma unroll CTAS == 8 ? 2 : 8 / CTAS  // several rows' loads at a time
-  for (int i = threadIdx.x; i < NT * kBM / CTAS * (D / 4); i += NT * kBM) {
-    const int at = i / (D / 4) * CTAS + rank, c4 = i % (D / 4);  // every CTAS-th row
-    const int x = at / kBM, row = at % kBM;
-    const int row_token = row / p.hb, head = first_head(p, seg.u) + row % p.hb;
-    const int t = (seg.k * NT + x) * p.tq_tokens + row_token;
-    if (row_token >= p.tq_tokens || head >= p.g || t >= p.S) continue;
-    float m[CTAS];
-    float4 o[CTAS];
-    const uint8_t* piece = state_row<C>(smem, x, row, c4) + ((c4 % (D / 8) ^ (row & 7)) << 4);
+  const int kvh = kv_head(p, seg.u), head0 = first_head(p, seg.u);
+  for (int i0 = threadIdx.x; i0 < kItems; i0 += kAtOnce * NT * kBM) {
+    float m[kAtOnce][CTAS];
+    float4 o[kAtOnce][CTAS];
+    long long hrow[kAtOnce];
 #pragma unroll
-    for (int r = 0; r < CTAS; ++r) {
-      m[r] = ld_cluster(mapa_shared(&bars->state[at], r));
-      o[r] = ld_cluster4(mapa_shared(piece, r));
+    for (int v = 0; v < kAtOnce; ++v) {
+      // (threads without a piece of their own read some)
+      const int i = i0 + v * NT * kBM;
+      const int at = (i < kItems ? i / (D / 4) : 0) * CTAS + rank, c4 = i % (D / 4);  // every CTAS-th row
+      const int x = at / kBM, row = at % kBM;
+      const int row_token = token_of(p, row), head = head0 + row - row_token * p.hb;
+      const int t = (seg.k * NT + x) * p.tq_tokens + row_token;
+      hrow[v] = i < kItems && row_token < p.tq_tokens && head < p.g && t < p.S
+                    ? (static_cast<long long>(seg.b) * p.H + kvh * p.g + head) * p.S + t
+                    : -1;
+      const uint8_t* piece = state_row<C>(smem, x, row, c4) + ((c4 % (D / 8) ^ (row & 7)) << 4);
+#pragma unroll
+      for (int r = 0; r < CTAS; ++r) {
+        m[v][r] = ld_cluster(mapa_shared(&bars->state[at], r));
+        o[v][r] = ld_cluster4(mapa_shared(piece, r));
+      }
     }
-    float M = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < CTAS; ++r) M = fmaxf(M, m[r]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int v = 0; v < kAtOnce; ++v) {
+      if (hrow[v] < 0) continue;
+      const int c4 = (i0 + v * NT * kBM) % (D / 4);
+      float M = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < CTAS; ++r) {
-      if (m[r] == -INFINITY) continue;  // no key counts (and its O is not set)
-      const float f = m[r] == M ? 1.f : ex2_approx(m[r] - M);
-      sum += f;
-      acc.x = fmaf(f, o[r].x, acc.x), acc.y = fmaf(f, o[r].y, acc.y);
-      acc.z = fmaf(f, o[r].z, acc.z), acc.w = fmaf(f, o[r].w, acc.w);
+      for (int r = 0; r < CTAS; ++r) M = fmaxf(M, m[v][r]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < CTAS; ++r) {
+        if (m[v][r] == -INFINITY) continue;  // no key counts (and its O is not set)
+        const float f = m[v][r] == M ? 1.f : ex2_approx(m[v][r] - M);
+        sum += f;
+        acc.x = fmaf(f, o[v][r].x, acc.x), acc.y = fmaf(f, o[v][r].y, acc.y);
+        acc.z = fmaf(f, o[v][r].z, acc.z), acc.w = fmaf(f, o[v][r].w, acc.w);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + hrow[v] * D + c4 * 4) =
+          make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+      if (c4 == 0 && p.lse != nullptr)
+        p.lse[hrow[v]] = sum == 0.f ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994531f;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const long long hrow = (static_cast<long long>(seg.b) * p.H + kv_head(p, seg.u) * p.g + head) * p.S + t;
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + hrow * D + c4 * 4) =
-        make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-    if (c4 == 0 && p.lse != nullptr)
-      p.lse[hrow] = sum == 0.f ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994531f;
   }
 }
 
@@ -1043,7 +1061,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     const int row = wq * 32 + lane;
     const int copy = row / C::kRows, crow = row % C::kRows;  // (a warp's lanes are of one copy)
     const int col0 = copy * C::kCols;                        // its first key of a tile
-    const int row_token = crow / p.hb, row_head = crow % p.hb;
+    const int row_token = token_of(p, crow), row_head = crow - row_token * p.hb;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t o_tmem = tmem + lane_off + C::kOCol + x * D;
     const uint32_t p_tmem = tmem + lane_off + C::kPCol + x * (kBN / 2);
@@ -1395,7 +1413,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           if (!whole) p.part_ml[part * kBM + crow] = make_float2(M, L);
           else if (p.lse != nullptr) p.lse[hrow] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
         }
-      } else if (p.cluster > 0) {
+      } else if (p.cluster > 1) {
         // The row's state: O normalised, and log2 of the sum of its weights.  O lies in
         // this tile's places of Q and P, which are through, half a row each; 16-byte
         // pieces are permuted against bank conflicts.
@@ -1528,7 +1546,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     if (COPIES == 1 && p.cluster > 0) {
       if (segs == 0) bars->state[x * kBM + row] = -INFINITY;  // no tile for this CTA
       cluster_sync_all();
-      if (ok) {
+      if (ok && (p.cluster > 1 || segs == 0)) {  // (a CTA of its own has written its unit, or writes zeros)
         if (p.cluster == 8) fold_cluster<C, D, BF16, NT, 8>(p, seg, smem, bars);
         else if (p.cluster == 4) fold_cluster<C, D, BF16, NT, 4>(p, seg, smem, bars);
         else if (p.cluster == 2) fold_cluster<C, D, BF16, NT, 2>(p, seg, smem, bars);
@@ -1582,7 +1600,8 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_paged_merge_kernel(cons
       part = said;
       if (part.y <= 1) continue;  // finished by one CTA
     }
-    const int t = k * tu + x * p.tq_tokens + row / p.hb, head = (u % p.nblk) * p.hb + row % p.hb;
+    const int row_token = token_of(p, row);
+    const int t = k * tu + x * p.tq_tokens + row_token, head = first_head(p, u) + row - row_token * p.hb;
     if (row >= rows_used || head >= p.g || t >= p.S) continue;
     auto state = [&](int i) { return (part.x + i) * 2LL + (i == 0 ? 1 : 0); };
     auto load_ml = [&](int i) { return p.part_ml[state(i) * (NT * kBM) + x * kBM + row]; };
@@ -1642,7 +1661,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_paged_merge_kernel(cons
 #pragma unroll
     for (int e = 0; e < kSlice; e += 2)
       out[e / 2] = p.out_bf16 ? pack2<true>(acc[e] * inv, acc[e + 1] * inv) : pack2<false>(acc[e] * inv, acc[e + 1] * inv);
-    const long long hrow = (static_cast<long long>(b) * p.H + (u / p.nblk) * p.g + head) * p.S + t;
+    const long long hrow = (static_cast<long long>(b) * p.H + kv_head(p, u) * p.g + head) * p.S + t;
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + hrow * D + slice * kSlice);
     dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
     dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
@@ -1676,16 +1695,27 @@ int max_ctas(const Shape& s, int max_len) {
   return s.units >= kMaxCtas || s.units * per_unit >= kMaxCtas ? kMaxCtas : static_cast<int>(s.units * per_unit);
 }
 
-// CTAs of a cluster that takes a unit, or 0 where runs of the list are taken.  The host
-// knows what the pages of a sequence can hold, not the lengths; clusters need neither
-// the division of the list nor the second kernel, and are for units of few tiles.
-// (With one CTA an SM, 16 clusters of eight, 32 of four and 72 of two run at once.)
-constexpr int kClusterRun = 6;  // tiles of a CTA
-int cluster_of(const Shape& s, int max_len, int num_sms) {
-  const int tiles = (max_len + kBN - 1) / kBN;
-  int c = s.units <= 16 ? 8 : s.units <= 32 ? 4 : s.units <= 72 ? 2 : 1;
-  while (c > 1 && c > tiles) c /= 2;
-  return s.units <= num_sms && tiles <= kClusterRun * c ? c : 0;
+// Clusters of n CTAs that run at once; the same on every GPU this library runs on.
+template <typename Kernel>
+int clusters_at_once(Kernel kern, int threads, int smem, int n, std::atomic<int>& known) {
+  int most = known.load(std::memory_order_relaxed);
+  if (most > 0) return most;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(n));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(n);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&most, kern, &cfg) != cudaSuccess || most < 1) {
+    cudaGetLastError();
+    return 0;
+  }
+  known.store(most, std::memory_order_relaxed);
+  return most;
 }
 
 template <int D, bool BF16, int NT, bool FP4, int COPIES>
@@ -1710,7 +1740,24 @@ int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   auto kern = prefill_paged_kernel<D, BF16, NT, FP4, COPIES>;
   static std::atomic<unsigned long long> attr_done{0};  // per instantiation
   if (!set_smem_limit_once(kern, C::kSmemBytes, attr_done)) return -1;
-  if (COPIES == 1) p.cluster = cluster_of(s, p.max_pages << p.page_shift, a.num_sms);
+  if constexpr (COPIES == 1) {
+    // CTAs of a cluster that takes a unit, or 0: runs of the list.  The host knows what
+    // the pages of a sequence can hold, not the lengths.  Clusters need neither the
+    // division of the list nor the second kernel; one of several CTAs folds its states,
+    // the longer the fewer it has.  In tiles of a unit, measured: kScan and kFold.
+    constexpr float kScan = NT == 2 ? 5.f : 9.f;
+    const float fold = (NT == 2 ? 10.f : 12.f) * static_cast<float>(s.hb * s.tokens) / kBM;  // of one CTA alone
+    static std::atomic<int> at_once[4];  // per instantiation, for clusters of 1, 2, 4 and 8
+    const int tiles = ((p.max_pages << p.page_shift) + kBN - 1) / kBN;
+    float best = static_cast<float>(s.units) * tiles / p.ctas + kScan;
+    for (int i = 0, n = 1; i < 4; ++i, n *= 2) {
+      const float cost = static_cast<float>((tiles + n - 1) / n) + (n > 1 ? fold / n : 0.f);
+      if (s.units * n > a.num_sms || n > tiles || cost >= best) continue;
+      if (n > 1 && s.units > clusters_at_once(kern, C::kThreads, C::kSmemBytes, n, at_once[i])) continue;
+      p.cluster = n;
+      best = cost;
+    }
+  }
   if (p.cluster > 0)
     return launch_after(kern, dim3(p.blocks * p.cluster, p.heads, p.B), C::kThreads, a.stream, p, C::kSmemBytes,
                         p.cluster);
@@ -1764,6 +1811,7 @@ int launch_prefill_paged(const PagedPrefillArgs& a) {
   p.S = a.S;
   p.g = a.H / c.Hkv;
   p.hb = s.hb;
+  p.hb_inverse = (65536 + s.hb - 1) / s.hb;
   p.tq_tokens = s.tokens;
   p.nblk = s.nblk;
   p.heads = s.heads;
