@@ -157,6 +157,7 @@ struct Params {
   float scale_log2;  // |scale| log2 e (of a scale of 0: log2 e)
   float sign;        // -1 or 0 where scale is negative or 0, and scores are taken times it
   int ctas;
+  int wide;          // whether tiles may count past 2^31
   int cluster;       // CTAs of each unit, which fold their states themselves; 0: runs of the list
   int* status;
 };
@@ -335,14 +336,15 @@ __device__ __forceinline__ int item_of_v(int j, int n) { return j <= n - 2 ? 2 *
 // Divides the list: every CTA sums all sequences' tiles (plan_sum, then a barrier),
 // then the thread whose share of the sequences holds the CTA's first tile finds it
 // (plan_find, and another barrier).
+template <typename T>  // int, or long long where tiles may count past 2^31
 struct Plan {
   Seq s;            // the thread's first sequence
   int b0, b1;       // its share
-  long long tiles, tiles_to;  // of the share; of all up to its end within the warp
-  long long units, units_to;
+  T tiles, tiles_to;  // of the share; of all up to its end within the warp
+  T units, units_to;
 };
-template <typename C, int NT>
-__device__ __forceinline__ void plan_sum(const Params& p, Barriers* bars, Plan& plan) {
+template <typename C, int NT, typename T>
+__device__ __forceinline__ void plan_sum(const Params& p, Barriers* bars, Plan<T>& plan) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int each = (p.B + C::kThreads - 1) / C::kThreads;
   plan.b0 = min(p.B, static_cast<int>(threadIdx.x) * each), plan.b1 = min(p.B, plan.b0 + each);
@@ -351,7 +353,7 @@ __device__ __forceinline__ void plan_sum(const Params& p, Barriers* bars, Plan& 
   for (int b = plan.b0; b < plan.b1; ++b) {
     const Seq s = load_seq(p, b);
     if (b == plan.b0) plan.s = s;
-    plan.tiles += seq_tiles<NT>(p, s);
+    plan.tiles += static_cast<T>(seq_tiles<NT>(p, s));
     plan.units += seq_units<NT>(p, s);
     most = max(most, most_tiles(p, s));
   }
@@ -361,8 +363,8 @@ __device__ __forceinline__ void plan_sum(const Params& p, Barriers* bars, Plan& 
   plan.units_to = plan.units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, plan.tiles_to, o);
-    const long long u = __shfl_up_sync(0xffffffffu, plan.units_to, o);
+    const T v = __shfl_up_sync(0xffffffffu, plan.tiles_to, o);
+    const T u = __shfl_up_sync(0xffffffffu, plan.units_to, o);
     if (lane >= o) plan.tiles_to += v, plan.units_to += u;
   }
   most = __reduce_max_sync(0xffffffffu, most);
@@ -372,43 +374,40 @@ __device__ __forceinline__ void plan_sum(const Params& p, Barriers* bars, Plan& 
     bars->scan_most[warp] = most;
   }
 }
-// (a division of 64 bits is a long one)
-__device__ __forceinline__ long long divide(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
-}
-template <typename C, int NT>
-__device__ __forceinline__ long long plan_find(const Params& p, Barriers* bars, const Plan& plan) {
+template <typename C, int NT, typename T>
+__device__ __forceinline__ bool plan_find(const Params& p, Barriers* bars, const Plan<T>& plan) {
   const int warp = threadIdx.x / 32;
-  long long tiles_before = plan.tiles_to - plan.tiles, units_before = plan.units_to - plan.units;
-  long long tiles = 0, units = 0;
+  T tiles_before = plan.tiles_to - plan.tiles, units_before = plan.units_to - plan.units;
+  T tiles = 0, units = 0;
   int most = 0;
 #pragma unroll
   for (int w = 0; w < C::kThreads / 32; ++w) {
-    if (w < warp) tiles_before += bars->scan[w], units_before += bars->scan_units[w];
-    tiles += bars->scan[w];
-    units += bars->scan_units[w];
+    if (w < warp) tiles_before += static_cast<T>(bars->scan[w]), units_before += static_cast<T>(bars->scan_units[w]);
+    tiles += static_cast<T>(bars->scan[w]);
+    units += static_cast<T>(bars->scan_units[w]);
     most = max(most, bars->scan_most[w]);
   }
-  const long long run = divide(tiles + p.ctas - 1, p.ctas), run_units = divide(units + p.ctas - 1, p.ctas);
+  const T run = (tiles + p.ctas - 1) / p.ctas, run_units = (units + p.ctas - 1) / p.ctas;
   const bool whole = run_units * most <= run + kSplitCost<NT>;
-  const long long step = whole ? run_units : run, all = whole ? units : tiles;
-  const long long x0 = blockIdx.x * step, left = max(0LL, min(step, all - x0));
+  const T step = whole ? run_units : run, all = whole ? units : tiles;
+  const T x0 = blockIdx.x * step;
+  const T left = all > x0 ? min(step, all - x0) : 0;
   if (threadIdx.x == 0) {
     bars->per = whole ? 0 : run;
     bars->start_left = left;
   }
-  const long long before = whole ? units_before : tiles_before;
+  const T before = whole ? units_before : tiles_before;
   if (left > 0 && x0 >= before && x0 < before + (whole ? plan.units : plan.tiles)) {
-    long long x = x0 - before;
+    T x = x0 - before;
     Seq s = plan.s;
     int b = plan.b0;
-    long long head = whole ? seq_units<NT>(p, s) : seq_tiles<NT>(p, s);
+    T head = static_cast<T>(whole ? seq_units<NT>(p, s) : seq_tiles<NT>(p, s));
     while (x >= head * p.heads) {
       x -= head * p.heads;
       s = load_seq(p, ++b);
-      head = whole ? seq_units<NT>(p, s) : seq_tiles<NT>(p, s);
+      head = static_cast<T>(whole ? seq_units<NT>(p, s) : seq_tiles<NT>(p, s));
     }
-    const int u = static_cast<int>(divide(x, head));
+    const int u = static_cast<int>(x / head);
     x -= u * head;
     const int tu = NT * p.tq_tokens;
     int k = max(-s.p0, 0) / tu;  // the first block with a real row
@@ -425,7 +424,7 @@ __device__ __forceinline__ long long plan_find(const Params& p, Barriers* bars, 
     bars->start[0] = b, bars->start[1] = u, bars->start[2] = k, bars->start[3] = static_cast<int>(x);
     bars->start_seq = s;
   }
-  return left;
+  return left > 0;
 }
 
 // The four pairs of E2M1 codes of a word as fp16 pairs, times a factor's fp16 pair:
@@ -609,10 +608,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     seg.j0 = seg.nt * rank >> shift;
     seg.j1 = seg.nt * (rank + 1) >> shift;
   } else {
-    Plan plan;
-    plan_sum<C, NT>(p, bars, plan);
-    __syncthreads();
-    if (plan_find<C, NT>(p, bars, plan) == 0) return;  // fewer tiles than CTAs
+    bool any;
+    if (!p.wide) {
+      Plan<int> plan;
+      plan_sum<C, NT>(p, bars, plan);
+      __syncthreads();
+      any = plan_find<C, NT>(p, bars, plan);
+    } else {
+      Plan<long long> plan;
+      plan_sum<C, NT>(p, bars, plan);
+      __syncthreads();
+      any = plan_find<C, NT>(p, bars, plan);
+    }
+    if (!any) return;  // fewer tiles than CTAs
   }
   if (warp == C::kMmaWarp) {
     tmem_alloc(&bars->tmem_base, 512);
@@ -1193,17 +1201,30 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         const int k0 = (seg.j0 + j) * kBN + col0;
         const uint32_t bad = bars->bad[0][(tiles + j) % kTileRing] >> (col0 / 16);
         const bool masked = k0 + kCols - 1 > tile.lim_min || bad != 0 || p.sign != 1.f;
+        if (masked) {
+          // A pass of its own, in a loop: as a second form of what follows, unrolled for
+          // all keys, it took 7000 cycles of each CTA's first such tile, most of them on
+          // instructions' way into their cache, and the other warps with it.
+#pragma unroll 1
+          for (int c = 0; c < kCols / 32; ++c) {
+            uint32_t w[32];
+            tmem_ld32(s_tmem + c * 32, w);
+            tmem_wait_ld();
+            reg_fence32(w);
+            const int last = lim - (k0 + c * 32);
+            const uint32_t gone = bad >> (2 * c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              w[i] = i <= last && !(gone >> (i / 16) & 1u) ? __float_as_uint(__uint_as_float(w[i]) * p.sign) : 0xFF800000u;
+            tmem_st32(s_tmem + c * 32, w);
+          }
+          tmem_wait_st();
+        }
         uint32_t u[kCols];
         float mq[kCols / 32];
-        if (masked) {
 #pragma unroll
-          for (int c = 0; c < kCols / 32; ++c)
-            tmem_ld32(s_tmem + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
-        } else {
-#pragma unroll
-          for (int c = 0; c < kCols / 32; ++c)
-            tmem_ld32_max(s_tmem + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]), mq[c]);
-        }
+        for (int c = 0; c < kCols / 32; ++c)
+          tmem_ld32_max(s_tmem + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]), mq[c]);
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < kCols / 32; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
@@ -1211,33 +1232,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         mbar_arrive(&bars->s_free[C::s_bar(x, done)]);
         if (NT == 2 && x == 0 && segs == 0 && j == 0) mbar_arrive(&bars->stagger);
         float* s = reinterpret_cast<float*>(u);
-        float mx;
-        if (masked) {
-          if (p.sign != 1.f) {
+        float mx = mq[0];
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) s[c] *= p.sign;
-          }
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (k0 + c > lim) s[c] = -INFINITY;
-          if (bad != 0) {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c)
-              if (bad >> (c / 16) & 1u) s[c] = -INFINITY;
-          }
-          float mx8[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mx8[i] = s[i];
-#pragma unroll
-          for (int c = 8; c < kCols; c += 16)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mx8[i] = fmax3(mx8[i], s[c + i], s[c + 8 + i < kCols ? c + 8 + i : c + i]);
-          mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-        } else {
-          mx = mq[0];
-#pragma unroll
-          for (int c = 1; c < kCols / 32; ++c) mx = fmaxf(mx, mq[c]);
-        }
+        for (int c = 1; c < kCols / 32; ++c) mx = fmaxf(mx, mq[c]);
         float gamma = 1.f;
         if (j == 0) {
           r = mx;
@@ -1330,8 +1327,22 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       int lim0;
       const bool guarded = !FP4 && tile.j1 > max(seg.j0, first_masked<NT>(p, seg, lim0));
       const bool nan_any = guarded && bars->nan_any[segs % kSegRing] != 0;
-      const uint8_t* nan_from = bars->nan_from[segs % kSegRing];
-      const int seen = real ? lim - lim0 : 0;
+      if (nan_any) {
+        const uint8_t* nan_from = bars->nan_from[segs % kSegRing];
+        const int seen = real ? lim - lim0 : 0;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t w[32];
+          tmem_ld32(o_tmem + c * 32, w);
+          tmem_wait_ld();
+          reg_fence32(w);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (seen > nan_from[c * 32 + i]) w[i] = 0x7FFFFFFFu;
+          tmem_st32(o_tmem + c * 32, w);
+        }
+        tmem_wait_st();
+      }
       if constexpr (COPIES > 1) {
         // Fold the copies: their references and sums, then O, 32 columns at a time; a
         // thread sums its row's part of the columns.
@@ -1363,11 +1374,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           tmem_ld32(o_tmem + c * 32, u);
           tmem_wait_ld();
           reg_fence32(u);
-          if (nan_any) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (seen > nan_from[c * 32 + i]) u[i] = 0x7FFFFFFFu;
-          }
           group_sync();  // what was there has been read
           if (!ok) break;
 #pragma unroll
@@ -1427,11 +1433,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             tmem_ld32(o_tmem + c * 32, u);
             tmem_wait_ld();
             reg_fence32(u);
-            if (nan_any) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (seen > nan_from[c * 32 + i]) u[i] = 0x7FFFFFFFu;
-            }
             uint8_t* dst = state_row<C>(smem, x, row, c * 8);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -1460,11 +1461,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             if (nx == 0 || !real || l == 0.f) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) u[i] = 0u;
-            }
-            if (nan_any) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (seen > nan_from[c * 32 + i]) u[i] = 0x7FFFFFFFu;
             }
             uint32_t pk[16];
 #pragma unroll
@@ -1517,11 +1513,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             tmem_ld32(o_tmem + c * 32, u);
             tmem_wait_ld();
             reg_fence32(u);
-            if (nan_any) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (seen > nan_from[c * 32 + i]) u[i] = 0x7FFFFFFFu;
-            }
             if (counts) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
@@ -1535,9 +1526,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       }
       // The CTA that has the unit's first tile says where its parts are.
       if (seg.j0 == 0 && threadIdx.x == 0 && p.cluster == 0) {
-        const long long behind = seg.nt - (seg.j1 - seg.j0);  // the unit's tiles in the runs after this one
+        const int behind = seg.nt - (seg.j1 - seg.j0);  // the unit's tiles in the runs after this one
+        const int per = static_cast<int>(min(bars->per, 0x7FFFFFFFLL));
         p.parts[(static_cast<long long>(seg.b) * p.heads + seg.u) * p.blocks + seg.k] =
-            make_int2(blockIdx.x, behind == 0 ? 1 : 1 + static_cast<int>(divide(behind + bars->per - 1, bars->per)));
+            make_int2(blockIdx.x, behind == 0 ? 1 : 2 + (behind - 1) / per);
       }
       tiles += seg.j1 - seg.j0;
       ++segs;
@@ -1826,6 +1818,7 @@ int launch_prefill_paged(const PagedPrefillArgs& a) {
   p.sign = a.scale == 0.f ? 0.f : a.scale < 0.f ? -1.f : 1.f;
   const int most = max_ctas(s, c.max_pages << c.page_shift);
   p.ctas = most < a.num_sms ? most : a.num_sms;
+  p.wide = s.units * ((static_cast<long long>(c.max_pages << c.page_shift) + kBN - 1) / kBN) >= (1LL << 31) - kMaxCtas;
   p.status = a.status;
   const size_t states = static_cast<size_t>(most) * 2 * s.nt * kBM;
   float* ws = static_cast<float*>(a.workspace);
