@@ -48,6 +48,7 @@ constexpr int kBM = 128;          // rows of a tile (= TMEM lanes)
 constexpr int kBN = 128;          // keys of a tile
 constexpr int kMaxCtas = 160;     // bound of the grid, for the workspace's size
 constexpr float kRescaleThreshold = 8.f;  // base-2 units
+constexpr int kPBlock = 64;
 // A scale of scores is at least this, so that -inf times it stays -inf; finite products
 // of Q and K are then as good as 0.
 constexpr float kLeastScale = 1.1754944e-38f;
@@ -125,9 +126,9 @@ struct Cfg {
   // with one tile over 16 bits, where there are enough).
   static constexpr bool kSplit = FP4 || NT == 2;
   static constexpr int kLaunchRegs = FP4 ? 128 : 168;
-  static constexpr int kSoftmaxRegs = FP4 ? (NT == 2 ? 200 : 240) : 216;
-  static constexpr int kControlRegs = FP4 ? (NT == 2 ? 56 : 64) : 72;
-  static constexpr int kConvertRegs = NT == 2 ? 56 : 104;
+  static constexpr int kSoftmaxRegs = FP4 ? (NT == 2 ? 192 : 240) : 216;
+  static constexpr int kControlRegs = FP4 ? 64 : 72;
+  static constexpr int kConvertRegs = NT == 2 ? 64 : 104;
   static_assert(!kSplit || NT * 128 * kSoftmaxRegs + 128 * kControlRegs + 32 * kConvertWarps * kConvertRegs <=
                                kThreads * kLaunchRegs,
                 "register split");
@@ -313,18 +314,17 @@ __device__ __forceinline__ int first_masked(const Params& p, const Seg& seg, int
   return (lim0 + 1) / kBN;
 }
 
-// The places of a ring in turn: the current one, and the parity of its round.
+// The places [FIRST, END) of a ring in turn: the current one and its round.  A place is
+// filled in its round for the (round)th time; in round 0 there is nothing to wait for.
+template <int FIRST, int END>
 struct Ring {
-  int st;
-  uint32_t phase;
-  int first, end;
-  bool fresh;  // the ring's first round: nothing to wait for before a place is filled
-  __device__ __forceinline__ Ring(int first_, int end_) : st(first_), phase(0), first(first_), end(end_), fresh(true) {}
+  int st = FIRST;
+  uint32_t round = 0;
+  __device__ __forceinline__ uint32_t phase() const { return round & 1u; }
   __device__ __forceinline__ void next() {
-    if (++st == end) {
-      st = first;
-      phase ^= 1u;
-      fresh = false;
+    if (END - FIRST == 1 || ++st == END) {
+      st = FIRST;
+      ++round;
     }
   }
 };
@@ -649,8 +649,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       const int row = threadIdx.x % kBN;
       // Within a row: where its pieces' first and further 16 bytes go.
       const uint32_t half = (row & 4) << 4, in0 = (row & 3) << 4;
-      Ring raws[2] = {Ring(0, C::kRawKStages), Ring(C::kRawKStages, C::kRawStages)};
-      Ring ats[2] = {Ring(0, C::kKStages), Ring(C::kKStages, C::kStages)};
+      // (of the two pairs of rings, with one tile each half of the warps moves one)
+      Ring<0, C::kRawKStages> raw_k;
+      Ring<C::kRawKStages, C::kRawStages> raw_v;
+      Ring<0, C::kKStages> at_k;
+      Ring<C::kKStages, C::kStages> at_v;
       int tile0 = 0;
       bool ok = true;
       while (ok && cur.next(p, seg)) {
@@ -658,13 +661,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         for (int i = 0; i < NT * n; ++i) {
           const bool is_v = NT == 2 ? i == 2 * n - 1 || (i > 0 && i % 2 == 0) : team == 1;
           const int j = NT == 1 ? i : i == 0 ? 0 : i == 2 * n - 1 ? n - 1 : (i & 1) ? (i + 1) / 2 : i / 2 - 1;
-          Ring raw = is_v ? raws[1] : raws[0], at = is_v ? ats[1] : ats[0];
-          ok = bounded_wait(&bars->raw[raw.st], raw.phase, abort_flag, p.status, kStatusTimeoutLoad);
-          if (ok && !at.fresh)
-            ok = bounded_wait(&bars->kv_empty[at.st], at.phase ^ 1u, abort_flag, p.status, kStatusTimeoutLoad);
+          const int raw = is_v ? raw_v.st : raw_k.st, at = is_v ? at_v.st : at_k.st;
+          ok = bounded_wait(&bars->raw[raw], is_v ? raw_v.phase() : raw_k.phase(), abort_flag, p.status,
+                            kStatusTimeoutLoad);
+          const uint32_t round = is_v ? at_v.round : at_k.round;
+          if (ok && round > 0)
+            ok = bounded_wait(&bars->kv_empty[at], (round & 1u) ^ 1u, abort_flag, p.status, kStatusTimeoutLoad);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint8_t* src = smem + C::kRawOff + raw.st * C::kRawBytes;
+          const uint8_t* src = smem + C::kRawOff + raw * C::kRawBytes;
           // Rows that are not there are zeros.
           const bool there = (seg.j0 + j) * kBN + row < seg.s.n &&
                              !(bars->bad[is_v][(tile0 + j) % kTileRing] >> (row / 16) & 1u);
@@ -676,20 +681,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             const uint32_t v = *reinterpret_cast<const uint32_t*>(src + kBN * (D / 2) + row * (D / 16));
             f[0] = there ? v : 0u;
           }
-          uint8_t* dst = sRing + at.st * C::kTileBytes + row * 128;
-          uint4 codes[kPieces];
-#pragma unroll
-          for (int q = 0; q < kPieces; ++q) {
-            const int piece = D == 128 ? ((row >> 1) + q) % kPieces : q;
-            codes[q] = *reinterpret_cast<const uint4*>(src + row * (D / 2) + piece * 16);
-          }
+          uint8_t* dst = sRing + at * C::kTileBytes + row * 128;
 #pragma unroll
           for (int q = 0; q < kPieces; ++q) {
             const uint32_t piece = D == 128 ? ((row >> 1) + q) % kPieces : q;
             const uint32_t fw = D == 128 && piece >= 2 ? f[D / 64 - 1] : f[0];
             const uint32_t two = e4m3x2_to_f16(piece & 1 ? fw >> 16 : fw);
             const uint32_t f0 = __byte_perm(two, two, 0x1010), f1 = __byte_perm(two, two, 0x3232);
-            const uint32_t w[4] = {codes[q].x, codes[q].y, codes[q].z, codes[q].w};
+            const uint4 codes = *reinterpret_cast<const uint4*>(src + row * (D / 2) + piece * 16);
+            const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
             uint8_t* to = dst + (piece >> 1) * C::kBlockBytes + ((piece & 1) * 64 ^ half);
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k) {
@@ -701,13 +701,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&bars->raw_empty[raw.st]);
-            mbar_arrive(&bars->kv_full[at.st]);
+            mbar_arrive(&bars->raw_empty[raw]);
+            mbar_arrive(&bars->kv_full[at]);
           }
-          raw.next();
-          at.next();
-          (is_v ? raws[1] : raws[0]) = raw;
-          (is_v ? ats[1] : ats[0]) = at;
+          if (is_v) raw_v.next(), at_v.next();
+          else raw_k.next(), at_k.next();
         }
         tile0 += n;
       }
@@ -768,8 +766,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         const uint32_t bytes = static_cast<uint32_t>(row_bytes << box_shift);
         const uint8_t* const pool = cb == 0 ? p.codes[loads_v] : p.factors[loads_v];
         uint8_t* const dst = smem + C::kRawOff + (cb == 0 ? 0 : kBN * (D / 2)) + box * bytes;
-        Ring at(loads_v ? C::kRawKStages : 0, loads_v ? C::kRawStages : C::kRawKStages);
-        int filled = 0;
+        const int first = loads_v ? C::kRawKStages : 0, places = loads_v ? C::kRawStages - C::kRawKStages : C::kRawKStages;
+        int st = first, round = 0, filled = 0;
         while (ok && cur.next(p, seg)) {
           const int kvh = kv_head(p, seg.u);
           int now = lookup(0), next = lookup(1), in = 0, window = 1;
@@ -778,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             if (!ok) break;
           }
           int key = seg.j0 * kBN + (box << box_shift);
-          for (int j = seg.j0; j < seg.j1; ++j, ++tile, key += kBN, at.next()) {
+          for (int j = seg.j0; j < seg.j1; ++j, ++tile, key += kBN) {
             const int page = __shfl_sync(0xffffffffu, now, in * boxes + box);
             if (++in == per_window) {
               in = 0;
@@ -791,13 +789,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             note_missing(loads_v, tile, __ballot_sync(0xffffffffu, cb == 0 && inside && !found));
             const uint8_t* src =
                 pool + (((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) + (key & in_page)) * row_bytes;
-            if (!at.fresh) ok = bounded_wait(&bars->raw_empty[at.st], at.phase ^ 1u, abort_flag, p.status, kStatusTimeoutLoad);
+            if (round > 0) ok = bounded_wait(&bars->raw_empty[st], (round & 1) ^ 1, abort_flag, p.status, kStatusTimeoutLoad);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&bars->raw[at.st], (__popc(copied) << box_shift) * (D / 2 + D / 16));
+            if (lane == 0) mbar_arrive_expect_tx(&bars->raw[st], (__popc(copied) << box_shift) * (D / 2 + D / 16));
             __syncwarp();
-            if (found && cb < 2) bulk_load(dst + at.st * C::kRawBytes, src, bytes, &bars->raw[at.st], keep);
+            if (found && cb < 2) bulk_load(dst + st * C::kRawBytes, src, bytes, &bars->raw[st], keep);
             ++filled;
+            if (++st == first + places) st = first, ++round;
           }
         }
         // Every copy must have landed before the CTA ends.
@@ -805,14 +804,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           int dummy = 0;
           volatile int* ignore = reinterpret_cast<volatile int*>(&dummy);
           if (segs > 0) bounded_wait(&bars->q_full, (segs - 1) & 1, ignore, p.status, kStatusTimeoutDrain);
-          const int places = at.end - at.first;
           for (int i = max(0, filled - places); i < filled; ++i)
-            bounded_wait(&bars->raw[at.first + i % places], (i / places) & 1, ignore, p.status, kStatusTimeoutDrain);
+            bounded_wait(&bars->raw[first + i % places], (i / places) & 1, ignore, p.status, kStatusTimeoutDrain);
         }
       } else {
         const bool loads = cb < C::kColBlocks;
         // One ring in the order of the loads, or one for K and one for V.
-        Ring ring_k(0, C::kKStages), ring_v(C::kKStages, C::kStages);
+        Ring<0, C::kKStages> ring_k;
+        Ring<C::kOneRing ? 0 : C::kKStages, C::kStages> ring_v;
         int filled[2] = {0, 0};
         while (ok && cur.next(p, seg)) {
           int now = lookup(0), next = lookup(1), window = 1;  // windows of V's tile and the one behind it
@@ -822,23 +821,26 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           load_q();
           if (!ok) break;
           auto issue = [&](bool is_v, int j, int page) {
-            Ring& at = is_v && !C::kOneRing ? ring_v : ring_k;
+            const bool by_v = is_v && !C::kOneRing;
+            const int st = by_v ? ring_v.st : ring_k.st;
+            const uint32_t round = by_v ? ring_v.round : ring_k.round;
             const int key = j * kBN + (box << box_shift);
             const bool inside = key < seg.s.n;
             const bool found = inside && page >= 0 && page < p.n_pages;
             if (!is_v) note_missing(false, tile++, __ballot_sync(0xffffffffu, cb == 0 && inside && !found));
-            if (!at.fresh) ok = bounded_wait(&bars->kv_empty[at.st], at.phase ^ 1u, abort_flag, p.status, kStatusTimeoutLoad);
+            if (round > 0) ok = bounded_wait(&bars->kv_empty[st], (round & 1u) ^ 1u, abort_flag, p.status, kStatusTimeoutLoad);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
-            uint64_t* bar = is_v && j >= jm ? &bars->raw[at.st] : &bars->kv_full[at.st];
+            uint64_t* bar = is_v && j >= jm ? &bars->raw[st] : &bars->kv_full[st];
             if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
             __syncwarp();
             if (loads)
-              tma_load_3d(sRing + at.st * C::kTileBytes + cb * C::kBlockBytes + (box << box_shift) * 128,
+              tma_load_3d(sRing + st * C::kTileBytes + cb * C::kBlockBytes + (box << box_shift) * 128,
                           is_v ? &p.tv : &p.tk, bar, cb * 64, found ? key & in_page : 0,
                           found ? page * p.Hkv + kvh : missing, keep);
-            at.next();
-            ++filled[is_v && !C::kOneRing];
+            if (by_v) ring_v.next();
+            else ring_k.next();
+            ++filled[by_v];
           };
           const int n = seg.j1 - seg.j0;
           issue(false, seg.j0, __shfl_sync(0xffffffffu, now, box));
@@ -981,15 +983,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         int done = 0;  // key tiles of this row tile so far
         bool ok = true;
         int st = 0;  // place of the last item waited for
-        Ring ring_k(0, C::kKStages), ring_v(C::kKStages, C::kStages);
+        Ring<0, C::kKStages> ring_k;
+        Ring<C::kOneRing ? 0 : C::kKStages, C::kStages> ring_v;
         // The next K or V, all in the order of their loads.
-        auto wait_item = [&](bool is_v) {
-          Ring& r = is_v && !C::kOneRing ? ring_v : ring_k;
-          st = r.st;
-          const uint32_t phase = r.phase;
-          r.next();
+        auto wait_next = [&](auto& ring) {
+          st = ring.st;
+          const uint32_t phase = ring.phase();
+          ring.next();
           return bounded_wait(&bars->kv_full[st], phase, abort_flag, p.status, kStatusTimeoutMma);
         };
+        auto wait_item = [&](bool is_v) { return is_v && !C::kOneRing ? wait_next(ring_v) : wait_next(ring_k); };
         // S of the tile that is number `d` of this row tile's.
         auto qk = [&](int d) {
           if (!(ok = wait_item(false))) return;
@@ -1198,6 +1201,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         }
         tc_fence_after();
         constexpr int kCols = C::kCols;
+        constexpr int kBlk = kCols < kPBlock ? kCols : kPBlock;  // keys whose weights are stored together
         const int k0 = (seg.j0 + j) * kBN + col0;
         const uint32_t bad = bars->bad[0][(tiles + j) % kTileRing] >> (col0 / 16);
         const bool masked = k0 + kCols - 1 > tile.lim_min || bad != 0 || p.sign != 1.f;
@@ -1251,15 +1255,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         const float2 nrs2 = make_float2(-rs, -rs);
         float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int blk = 0; blk < (kCols + 63) / 64; ++blk) {
-          constexpr int kBlk = kCols < 64 ? kCols : 64;
+        for (int blk = 0; blk < kCols / kBlk; ++blk) {
           uint32_t pk[kBlk / 2];
 #pragma unroll
           for (int c8 = 0; c8 < kBlk / 8; ++c8) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int c = blk * 64 + c8 * 8 + 2 * i;
-              const float2 e = ex2_pair(ffma2(make_float2(s[c], s[c + 1]), lam2, nrs2), (blk * 8 + c8) * 4 + i);
+              const int c = blk * kBlk + c8 * 8 + 2 * i;
+              const float2 e = ex2_pair(ffma2(make_float2(s[c], s[c + 1]), lam2, nrs2), c / 2);
               sum4[i] = fadd2(sum4[i], e);
               pk[c8 * 4 + i] = pack2<kMmaBf16>(e.x, e.y);
             }
@@ -1290,15 +1293,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
               if (!ok) break;
             }
           }
-          if constexpr (kBlk == 32) {
-            tmem_st16(p_tmem + col0 / 2, pk);
-          } else if constexpr (C::kPInTmem) {
-            tmem_st32(p_tmem + col0 / 2 + blk * 32, pk);
-          } else {
+          if constexpr (!C::kPInTmem) {
 #pragma unroll
-            for (int c8 = 0; c8 < 8; ++c8)
-              *reinterpret_cast<uint4*>(p_row + blk * C::kBlockBytes + ((c8 ^ (row & 7)) << 4)) =
+            for (int c8 = 0; c8 < kBlk / 8; ++c8) {
+              const int chunk = (blk * kBlk / 8 + c8) % 8;
+              *reinterpret_cast<uint4*>(p_row + blk * kBlk / 64 * C::kBlockBytes + ((chunk ^ (row & 7)) << 4)) =
                   make_uint4(pk[c8 * 4], pk[c8 * 4 + 1], pk[c8 * 4 + 2], pk[c8 * 4 + 3]);
+            }
+          } else if constexpr (kBlk == 32) {
+            tmem_st16(p_tmem + col0 / 2 + blk * 16, pk);
+          } else {
+            tmem_st32(p_tmem + col0 / 2 + blk * 32, pk);
           }
         }
         if (!ok) break;
