@@ -14,7 +14,20 @@ from tests.test_paged_gpu import Pool, _i32, _same_bits
 pytestmark = pytest.mark.gpu
 
 
+beyond = 0  # columns that _forward adds to a page table
+
+
+@pytest.fixture(params=["narrow", "wide"])
+def table_width(request, monkeypatch):
+    """What a page table could hold decides how the work is divided and which kernels
+    take it: tables as the test makes them, and the same ones with room for far more."""
+    if request.param == "wide":
+        monkeypatch.setitem(globals(), "beyond", 20000)
+
+
 def _forward(pool, q, table, lens, news, **kw):
+    if beyond:
+        table = torch.nn.functional.pad(table, (0, beyond), value=1 << 30)
     fn = gb.attn_fwd_paged if pool.bits == 16 else gb.attn_fwd_paged_fp4
     return fn(q, *pool.gpu, table.cuda(), _i32(lens), new_lens=None if news is None else _i32(news), **pool.kw, **kw)
 
@@ -63,6 +76,7 @@ LONG = [
 ]
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("bits", [16, 4])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("cfg", CHUNKS)
@@ -97,6 +111,7 @@ def test_runs_of_several_units(cfg, bits):
         assert _same_bits(again[0], o) and torch.equal(again[1], lse)
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("S", [1, 30, 90])
 @pytest.mark.parametrize("bits", [16, 4])
 def test_slots_behind_the_length_and_unused_pages_hold_nan(bits, S):
@@ -119,6 +134,7 @@ def test_slots_behind_the_length_and_unused_pages_hold_nan(bits, S):
         assert torch.isfinite(o2).all() and _same_bits(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("dtype,H,Hkv,d,S,L", [
     (torch.bfloat16, 4, 2, 128, 9, 150), (torch.float16, 8, 1, 64, 20, 500), (torch.bfloat16, 2, 2, 128, 200, 350),
     (torch.float16, 4, 1, 64, 100, 130), (torch.bfloat16, 2, 1, 128, 300, 300), (torch.bfloat16, 1, 1, 64, 256, 1000)])
@@ -153,6 +169,7 @@ def test_values_that_are_not_finite(dtype, H, Hkv, d, S, L, value):
         assert torch.equal(lse[1, :, :t0], clean[1][1, :, :t0])
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("S", [1, 20, 70])
 @pytest.mark.parametrize("bits", [16, 4])
 def test_pages_that_do_not_exist(bits, S):
@@ -197,6 +214,7 @@ def test_lengths_outside_their_ranges(bits):
     assert torch.isfinite(o).all() and (o[2, :, :3] == 0).all()
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("S", [2, 40, 130])
 @pytest.mark.parametrize("bits", [16, 4])
 def test_scales_scores_and_given_arguments(bits, S):
@@ -216,6 +234,7 @@ def test_scales_scores_and_given_arguments(bits, S):
     assert none is None
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("S", [2, 100])
 def test_wide_queries_over_four_bits(S):
     """bf16 queries far outside fp16's range, whose products the row's scale keeps exact."""
@@ -365,6 +384,7 @@ def test_wrapper_refusals():
     assert gb.gbattn_device_status() == 0
 
 
+@pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("bits", [16, 4])
 def test_text_and_images_served_in_chunks(bits):
     """As a program runs them: two sequences of different lengths take chunks of text
