@@ -63,31 +63,24 @@ constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
 // each copy's warps take another part of the keys (the other weights of their rows
 // stay 0): the softmax of a tile, which otherwise waits for one or two of the four
 // warps, takes a half or a quarter of the time.  The copies are folded at a segment's
-// end.  COPIES = kTurned: up to 32 rows are the columns of the products instead, whose
-// 128 rows are then the keys (S^T = K Q^T) and the elements of the output
-// (O^T = V^T P^T): a quarter of the tensor core's time, which bounds the other form.
-constexpr int kTurned = 0, kTurnedRows = 32;
+// end.
 template <int D, int NT, bool FP4, int COPIES>
 struct Cfg {
   static_assert(NT == 1 || COPIES == 1, "copies are of one tile");
-  static constexpr bool kTurn = COPIES == kTurned;
-  static_assert(!kTurn || (D == 128 && FP4), "rows as columns: over 4 bits, where products bound");
-  static constexpr int kRows = kTurn ? kTurnedRows : kBM / (kTurn ? 1 : COPIES);  // of a copy
-  static constexpr int kCols = kBN / (kTurn ? 1 : COPIES);                        // keys of a copy
-  static_assert(kRows * kBN >= kCols, "a copy has rows");
-  // Tensor memory has room for P unless there are two tiles of d = 128, and with one
-  // tile for Q as well: over 4 bits, where shared memory's bandwidth bounds, both
-  // products then read only K or V from there.
+  static constexpr int kDim = D;
+  static constexpr int kRows = kBM / COPIES;  // of a copy
+  static constexpr int kCols = kBN / COPIES;  // keys of a copy
+  // Tensor memory has room for P unless there are two tiles of d = 128.
   static constexpr bool kPInTmem = D == 64 || NT == 1;
-  static constexpr bool kQInTmem = FP4 && NT == 1 && !kTurn;
-  // With one tile S has two places in turn, and one thread issues the products with K,
-  // another those with V: a chain of products into one place runs at half the tensor
-  // core's rate, two at once keep it busy (two tiles have two chains each).
+  // With one tile S and P have two places each in turn, and one thread issues the
+  // products with K, another those with V.  A chain of products into one place takes
+  // about 100 cycles each whatever their size is, and a softmax that had to wait for
+  // the end of one before it could hand over the next P would wait most of its time
+  // (two tiles do each other's waiting).
   static constexpr int kSBufs = NT == 1 ? 2 : 1;
   static constexpr int kSCol = 0, kOCol = 2 * kBN, kPCol = kOCol + NT * D;
   // Where tile x's S number d goes, and its barriers.
   __device__ static __forceinline__ int s_bar(int x, int d) { return NT == 1 ? d & 1 : x; }
-  __device__ static constexpr int q_col() { return kPCol + kBN / 2; }
   static constexpr int kColBlocks = D / 64;
   static constexpr int kTileBytes = kBM * D * 2;
   static constexpr int kBlockBytes = kBM * 128;
@@ -95,16 +88,13 @@ struct Cfg {
   // bits: none, threads store their rows).
   // Copies are folded there, 32 columns at a time, by threads that store the sums.
   static constexpr bool kDirectO = NT == 1 && (FP4 || COPIES > 1);
-  static constexpr int kStageBytes = kTurn ? kTurnedRows * kBN * 2 : COPIES > 1 ? kBM * 32 * 4 : kDirectO ? 0 : kPInTmem ? kTileBytes : kBM * kBN * 2;
-  // Rows of Q in shared memory: those of the tile, or of one copy on its way to
-  // tensor memory.
-  static constexpr int kQRows = kQInTmem || kTurn ? kRows : kBM;
-  static constexpr int kQBytes = kQRows * D * 2;
+  static constexpr int kStageBytes = COPIES > 1 ? kBM * 32 * 4 : kDirectO ? 0 : kPInTmem ? kTileBytes : kBM * kBN * 2;
+  static constexpr int kQBytes = kTileBytes;
   // 16-bit key and value tiles; of a 4-bit cache's rows, what comes from memory and
   // what the conversion makes of it.
   static constexpr int kStages = FP4 ? (NT == 2 ? (D == 128 ? 2 : 6) : (D == 128 ? 4 : 8))
                                      : (NT == 2 ? (D == 128 ? 3 : 8) : (D == 128 ? 5 : 12));
-  static constexpr int kRawStages = !FP4 ? 0 : NT == 2 ? (D == 128 ? 3 : 8) : kTurn ? 8 : (D == 128 ? 6 : 12);
+  static constexpr int kRawStages = !FP4 ? 0 : NT == 2 ? (D == 128 ? 3 : 8) : (D == 128 ? 5 : 12);
   // With two tiles over 16 bits everyone takes every key and value tile in the order of
   // their loads, so all places form one ring.  Otherwise keys and values have issuers
   // or converting warps of their own, each at its own pace, and a ring each: a wait
@@ -182,7 +172,6 @@ struct __align__(8) Barriers {
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_full[2], mma_done[2];
   uint64_t group[2];       // the four warps of a softmax warpgroup
   uint64_t stagger;
-  uint64_t vote;           // rows as columns: one arrival of each softmax warp
   long long per;           // tiles of a run
   long long start_left;    // tiles of this run, or (per = 0) its units
   int start[4];            // its first unit (sequence, head, block) and tile
@@ -475,7 +464,7 @@ __device__ __forceinline__ bool any_not_finite(const uint8_t* tile, int r0, int 
 // Where the first 16-byte piece of a row's state's half with columns 4 c4, .. is.
 template <typename C>
 __device__ __forceinline__ uint8_t* state_row(uint8_t* smem, int x, int row, int c4) {
-  constexpr int kHalf = C::kTileBytes / (2 * kBM) / 8;  // pieces of half a row
+  constexpr int kHalf = C::kDim / 8;  // pieces of half a row
   return (c4 < kHalf ? smem + C::kQOff + x * C::kQBytes : smem + C::kPOff + x * C::kStageBytes) + row * (kHalf * 16);
 }
 
@@ -491,18 +480,6 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
                : "r"(a)
                : "memory");
   return v;
-}
-
-// Where the parts of a unit are, said by the CTA that has its first tile.
-__device__ __forceinline__ void say_parts(const Params& p, const Barriers* bars, const Seg& seg) {
-  const int behind = seg.nt - (seg.j1 - seg.j0);  // the unit's tiles in the runs after this one
-  const int per = static_cast<int>(min(bars->per, 0x7FFFFFFFLL));
-  p.parts[(static_cast<long long>(seg.b) * p.heads + seg.u) * p.blocks + seg.k] =
-      make_int2(blockIdx.x, behind == 0 ? 1 : 2 + (behind - 1) / per);
-}
-
-__device__ __forceinline__ void st_shared_u16(uint32_t a, uint32_t v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(v)) : "memory");
 }
 
 // The cluster's CTAs fold their states, a share of the unit's rows each, and write
@@ -561,262 +538,12 @@ __device__ __forceinline__ void fold_cluster(const Params& p, const Seg& seg, ui
   }
 }
 
-// The row of Q at piece(0), piece(1), .. (16 bytes each) from bf16 to fp16 behind a
-// power of two that brings its largest element to [1, 2): exact but for elements below
-// 2^-14 of that one.  Returns what the scores have to be multiplied with again.
-template <int D, typename Piece>
-__device__ __forceinline__ float q_row_scale(Piece&& piece, float& down) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    const uint4 v = *piece(i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7F80u, w[k] >> 16 & 0x7F80u));
-  }
-  const uint32_t e = min(max(top >> 7, 1u), 253u);
-  down = __uint_as_float((254u - e) << 23);
-  return __uint_as_float(e << 23);
-}
-
-// The softmax warps' work with rows as columns (kTurned): a thread has one key of each
-// tile and all 32 rows' scores of it, and at a segment's end one element of all rows'
-// outputs.  A row's reference is common to all threads, so a score too far above it
-// (in base-2 units, as ever) is a matter for all four warps: they vote on each tile,
-// and where one has such a score all take the tile's maxima.  Sums of weights stay
-// with the threads until the end.
-template <typename C, int D, bool BF16, typename Walk>
-__device__ __forceinline__ void softmax_turned(const Params& p, Barriers* bars, uint8_t* smem, uint32_t tmem, Walk cur) {
-  constexpr int kN = kTurnedRows;
-  constexpr float kNoReference = -1e30f;  // finite, so that a masked score minus it is -inf
-  const int tid = threadIdx.x, wq = tid / 32, lane = tid % 32;
-  volatile int* abort_flag = &bars->abort_flag;
-  uint8_t* sQ = smem + C::kQOff;
-  uint8_t* sP = smem + C::kPOff;
-  const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-  const uint32_t o_tmem = tmem + lane_off + C::kOCol;
-  float* row_lam = bars->state;                                // [32]
-  int* row_lim = reinterpret_cast<int*>(bars->state + 32);     // [32]
-  float(*warp_row)[kN] = reinterpret_cast<float(*)[kN]>(bars->state + 64);  // [4][32]
-  int* flags = reinterpret_cast<int*>(bars->state + 192);      // [3], of tiles in turn
-  float* row_sum = bars->state + 196;                          // [32]
-  // This key's place in a row of P: 16-byte pieces are permuted by the row.
-  const uint32_t p_key = smem_u32(sP) + (tid / 64) * (kN * 128) + (tid % 8) * 2, p_chunk = tid % 64 / 8;
-  int done = 0, segs = 0, tiles = 0;
-  bool ok = true;
-  uint32_t vote_phase = 0;
-  auto vote = [&]() {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->vote);
-    ok = bounded_wait(&bars->vote, vote_phase, abort_flag, p.status, kStatusTimeoutSoftmax);
-    ok = __all_sync(0xffffffffu, ok);
-    vote_phase ^= 1u;
-  };
-  if (tid < 3) flags[tid] = 0;
-  Seg seg{};
-  while (ok && cur.next(p, seg)) {
-    const TileRows tile(p, seg, 0, 1);
-    const int kvh = kv_head(p, seg.u), n = seg.j1 - seg.j0;
-    const float vd = p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
-    // Row `lane` of the tile (all warps alike).
-    const int row_token = token_of(p, lane), head = first_head(p, seg.u) + lane - row_token * p.hb;
-    const int t = tile.t0 + row_token;
-    const bool in_tile = row_token < p.tq_tokens && head < p.g && t < p.S;
-    const bool real = in_tile && t < seg.s.rows && seg.s.p0 + t >= 0;
-    ok = bounded_wait(&bars->q_full, segs & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    if (wq == 0) {
-      float lam = p.scale_log2 * (p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f);
-      // The row to fp16; rows that do not count become zeros, or what they hold would
-      // have a say in the others' references.
-      uint8_t* q_row = sQ + lane * 128;
-      auto piece = [&](int i) {
-        return reinterpret_cast<uint4*>(q_row + (i / 8) * C::kQRows * 128 + ((i ^ lane) & 7) * 16);
-      };
-      float down = 1.f;
-      if constexpr (BF16) {
-        if (real) lam *= q_row_scale<D>(piece, down);
-      }
-      if (BF16 || !real) {
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 v = *piece(i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t h[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            h[k] = !real ? 0u
-                         : pack2<false>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-          *piece(i) = make_uint4(h[0], h[1], h[2], h[3]);
-        }
-        fence_proxy_async_smem();
-      }
-      row_lam[lane] = fmaxf(lam, kLeastScale);
-      row_lim[lane] = real ? limit(p, seg.s, t) : -1;
-    }
-    vote();
-    if (!ok) break;
-    mbar_arrive(&bars->q_ready[0]);
-    float lam[kN], ref[kN], l[kN];
-#pragma unroll
-    for (int r = 0; r < kN; ++r) lam[r] = row_lam[r], ref[r] = kNoReference, l[r] = 0.f;
-    for (int j = 0; j < n; ++j, ++done) {
-      ok = bounded_wait(&bars->s_full[done & 1], (done >> 1) & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t u[kN];
-      tmem_ld32(tmem + lane_off + C::kSCol + (done & 1) * kBN, u);
-      tmem_wait_ld();
-      reg_fence32(u);
-      tc_fence_before();
-      mbar_arrive(&bars->s_free[done & 1]);
-      const int k0 = (seg.j0 + j) * kBN;
-      const uint32_t bad = bars->bad[0][(tiles + j) % kTileRing];
-      if (k0 + kBN - 1 > tile.lim_min || bad != 0 || p.sign != 1.f) {
-        const bool gone = bad >> (tid / 16) & 1u;
-#pragma unroll
-        for (int r = 0; r < kN; ++r)
-          u[r] = gone || k0 + tid > row_lim[r] ? 0xFF800000u : __float_as_uint(__uint_as_float(u[r]) * p.sign);
-      }
-      float e[kN];
-      float most = -INFINITY;
-#pragma unroll
-      for (int r = 0; r < kN; ++r) {
-        e[r] = fmaf(__uint_as_float(u[r]), lam[r], -ref[r]);
-        most = fmaxf(most, e[r]);
-      }
-      const int slot = done % 3;
-      if (__any_sync(0xffffffffu, most > kRescaleThreshold) && lane == 0) flags[slot] = 1;
-      vote();
-      if (!ok) break;
-      const bool raise = *reinterpret_cast<volatile int*>(&flags[slot]) != 0;
-      if (tid == 0) flags[(done + 2) % 3] = 0;  // read by all before this vote, used after the next one
-      bool waited = j == 0;
-      if (raise) {
-        float mine = 0.f;
-#pragma unroll
-        for (int r = 0; r < kN; ++r) {
-          // floats in the order of integers
-          const int b = __float_as_int(__uint_as_float(u[r]) * lam[r]);
-          const int m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7FFFFFFF));
-          if (lane == r) mine = __int_as_float(m ^ (m >> 31 & 0x7FFFFFFF));
-        }
-        warp_row[wq][lane] = mine;
-        vote();
-        if (!ok) break;
-        if (!waited) {
-          ok = bounded_wait(&bars->p_free[0], (done - 1) & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          waited = true;
-        }
-        uint32_t o[32];
-        if (j > 0) {
-          tmem_ld32(o_tmem, o);
-          tmem_wait_ld();
-          reg_fence32(o);
-        }
-#pragma unroll
-        for (int r = 0; r < kN; ++r) {
-          const float top = fmaxf(fmaxf(warp_row[0][r], warp_row[1][r]), fmaxf(warp_row[2][r], warp_row[3][r]));
-          const float now = fmaxf(ref[r], top);
-          const float gamma = ex2_approx(ref[r] - now);
-          ref[r] = now;
-          l[r] *= gamma;
-          e[r] = fmaf(__uint_as_float(u[r]), lam[r], -now);
-          if (j > 0) o[r] = __float_as_uint(__uint_as_float(o[r]) * gamma);
-        }
-        if (j > 0) {
-          tmem_st32(o_tmem, o);
-          tmem_wait_st();
-        }
-      }
-      if (!waited) {
-        ok = bounded_wait(&bars->p_free[0], (done - 1) & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-      }
-#pragma unroll
-      for (int r = 0; r < kN; r += 2) {
-        const float a = ex2_approx(e[r]), b = ex2_approx(e[r + 1]);
-        l[r] += a, l[r + 1] += b;
-        const uint32_t h = pack2<false>(a, b);
-        st_shared_u16(p_key + r * 128 + ((p_chunk ^ (r & 7)) << 4), h);
-        st_shared_u16(p_key + (r + 1) * 128 + ((p_chunk ^ ((r + 1) & 7)) << 4), h >> 16);
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(&bars->p_full[0]);
-    }
-    if (!ok) break;
-    // ---- the segment's end: the rows' sums, then each thread's element of every row
-    ok = bounded_wait(&bars->o_full[0], segs & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    tc_fence_after();
-    // Halves change places until lane r has row r's sum over the warp.
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < o; ++i) {
-        const bool up = (lane & o) != 0;
-        const float send = up ? l[i] : l[i + o], keep = up ? l[i + o] : l[i];
-        l[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-      }
-    warp_row[wq][lane] = l[0];
-    vote();
-    if (!ok) break;
-    const bool whole = seg.whole();
-    const long long part = blockIdx.x * 2LL + (seg.j0 > 0 ? 0 : 1);
-    const long long hrow = (static_cast<long long>(seg.b) * p.H + kvh * p.g + head) * p.S + t;
-    const float sum = warp_row[0][lane] + warp_row[1][lane] + warp_row[2][lane] + warp_row[3][lane];
-    if (wq == 0) {
-      // What a thread multiplies its element of the row with; 0 where no key counts.
-      row_sum[lane] = !real || sum == 0.f ? 0.f : whole ? vd / sum : vd;
-      float m = 0.f;  // ref[lane]
-#pragma unroll
-      for (int r = 0; r < kN; ++r) m = lane == r ? ref[r] : m;
-      if (in_tile) {
-        const bool counts = real && sum != 0.f;
-        if (!whole) p.part_ml[part * kBM + lane] = counts ? make_float2(m, sum) : make_float2(-INFINITY, 0.f);
-        else if (p.lse != nullptr) p.lse[hrow] = counts ? (m + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
-      }
-    }
-    vote();
-    if (!ok) break;
-    uint32_t o[32];
-    tmem_ld32(o_tmem, o);
-    tmem_wait_ld();
-    reg_fence32(o);
-    tc_fence_before();  // O has been read before P's arrival lets it be overwritten
-    float* part_o = p.part_o + (part * (D / 4) + tid / 4) * (kBM * 4) + tid % 4;
-#pragma unroll
-    for (int r = 0; r < kN; ++r) {
-      // (lane r has the row's place)
-      const long long at = __shfl_sync(0xffffffffu, in_tile ? hrow : -1LL, r);
-      const float f = row_sum[r];
-      const float v = f == 0.f ? 0.f : __uint_as_float(o[r]) * f;
-      if (at < 0) continue;
-      if (whole) reinterpret_cast<uint16_t*>(p.o)[at * D + tid] = static_cast<uint16_t>(pack2<BF16>(v, 0.f));
-      else part_o[r * 4] = v;
-    }
-    // The CTA that has the unit's first tile says where its parts are.
-    if (seg.j0 == 0 && tid == 0) say_parts(p, bars, seg);
-    tiles += n;
-    ++segs;
-  }
-}
-
 template <int D, bool BF16, int NT, bool FP4, int COPIES>
 __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     prefill_paged_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D, NT, FP4, COPIES>;
   constexpr bool kMmaBf16 = BF16 && !FP4;  // over 4 bits all operands are fp16
-  constexpr bool kReadyQ = (BF16 && FP4) || C::kQInTmem || C::kTurn;  // queries pass through the softmax warps
+  constexpr bool kReadyQ = BF16 && FP4;  // queries pass through the softmax warps
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem + C::kQOff;
   uint8_t* sP = smem + C::kPOff;
@@ -854,7 +581,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       mbar_init(&bars->group[x], kBM);
     }
     mbar_init(&bars->stagger, kBM);
-    mbar_init(&bars->vote, 4);
     bars->abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&p.tq);
@@ -1018,12 +744,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             const int t0 = seg.k * NT * p.tq_tokens;
             int real = 0;
             for (int x = 0; x < NT; ++x) real += t0 + x * p.tq_tokens < seg.s.rows;
-            constexpr int kLoads = C::kQInTmem || C::kTurn ? 1 : COPIES;
+            constexpr int kLoads = COPIES;
             mbar_arrive_expect_tx(&bars->q_full, real * kLoads * C::kColBlocks * p.hb * p.tq_tokens * 128);
             for (int x = 0; x < real; ++x)
               for (int c = 0; c < C::kColBlocks; ++c)
                 for (int i = 0; i < kLoads; ++i)
-                  tma_load_5d(sQ + x * C::kQBytes + c * C::kQRows * 128 + i * C::kRows * 128, &p.tq, &bars->q_full,
+                  tma_load_5d(sQ + x * C::kQBytes + c * kBM * 128 + i * C::kRows * 128, &p.tq, &bars->q_full,
                               c * 64, first_head(p, seg.u), kv_head(p, seg.u), t0 + x * p.tq_tokens, seg.b, once);
           }
         }
@@ -1216,12 +942,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       if (lane == 0) {
         const int x = NT == 1 ? 0 : warp - C::kMmaWarp;
         const bool does_qk = NT == 2 || warp == C::kMmaWarp;
-        constexpr uint32_t kIdescQK = idesc_f16(kMmaBf16, false, false, kBM, C::kTurn ? kTurnedRows : kBN);
-        constexpr uint32_t kIdescPV = C::kTurn ? idesc_f16(kMmaBf16, true, false, kBM, kTurnedRows)
-                                               : idesc_f16(kMmaBf16, false, true, kBM, D);
+        constexpr uint32_t kIdescQK = idesc_f16(kMmaBf16, false, false, kBM, kBN);
+        constexpr uint32_t kIdescPV = idesc_f16(kMmaBf16, false, true, kBM, D);
         const uint32_t ring_addr = smem_u32(sRing);
         const uint32_t o_col = tmem + C::kOCol + x * D;
-        const uint32_t p_tcol = tmem + C::kPCol + x * (kBN / 2);
         const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ + x * C::kQBytes), 16, 1024);
         const uint64_t p_desc = smem_desc_sw128(smem_u32(sP + x * C::kStageBytes), 16, 1024);
         auto issue_qk = [&](int st, int d) {
@@ -1230,24 +954,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t off = ((kk / 4) * C::kBlockBytes + (kk % 4) * 32) >> 4;
-            if constexpr (C::kTurn)
-              mma_f16_ss(s_col, kd + off, q_desc + (((kk / 4) * C::kQRows * 128 + (kk % 4) * 32) >> 4), kIdescQK,
-                         kk > 0 ? 1u : 0u);
-            else if constexpr (C::kQInTmem)
-              mma_f16_ts(s_col, tmem + C::q_col() + kk * 8, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
-            else
-              mma_f16_ss(s_col, q_desc + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
+            mma_f16_ss(s_col, q_desc + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
           }
         };
-        auto issue_pv = [&](int st, bool accumulate) {
+        auto issue_pv = [&](int st, int d, bool accumulate) {
+          const uint32_t p_tcol = tmem + C::kPCol + C::s_bar(x, d) * (kBN / 2);
           const uint64_t vd = smem_desc_sw128(ring_addr + st * C::kTileBytes, C::kBlockBytes, 1024);
 #pragma unroll
           for (int kk = 0; kk < kBN / 16; ++kk) {
             const uint32_t acc = (accumulate || kk > 0) ? 1u : 0u;
-            if constexpr (C::kTurn) {
-              const uint64_t poff = ((kk / 4) * kTurnedRows * 128 + (kk % 4) * 32) >> 4;
-              mma_f16_ss(o_col, vd + ((kk * 2048) >> 4), p_desc + poff, kIdescPV, acc);
-            } else if constexpr (C::kPInTmem) {
+            if constexpr (C::kPInTmem) {
               mma_f16_ts(o_col, p_tcol + kk * 8, vd + ((kk * 2048) >> 4), kIdescPV, acc);
             } else {
               const uint64_t poff = ((kk / 4) * C::kBlockBytes + (kk % 4) * 32) >> 4;
@@ -1284,10 +1000,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         };
         auto pv = [&](int d, bool first, bool last) {
           if (!(ok = wait_item(true))) return;
-          if (!(ok = bounded_wait(&bars->p_full[x], d & 1, abort_flag, p.status, kStatusTimeoutMma))) return;
+          if (!(ok = bounded_wait(&bars->p_full[C::s_bar(x, d)], (d / C::kSBufs) & 1, abort_flag, p.status,
+                                  kStatusTimeoutMma)))
+            return;
           tc_fence_after();
-          issue_pv(st, !first);
-          mma_commit(&bars->p_free[x]);
+          issue_pv(st, d, !first);
+          mma_commit(&bars->p_free[C::s_bar(x, d)]);
           if (last) mma_commit(&bars->o_full[x]);
           mma_commit(&bars->kv_empty[st]);
         };
@@ -1343,9 +1061,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
   } else {
     // ================================================================ softmax
     if constexpr (C::kSplit) regs_inc<C::kSoftmaxRegs>();
-    if constexpr (C::kTurn) {
-      softmax_turned<C, D, BF16>(p, bars, smem, tmem, cur);
-    } else {
     const int x = warp / 4;
     const int wq = warp % 4;
     const int row = wq * 32 + lane;
@@ -1354,13 +1069,18 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     const int row_token = token_of(p, crow), row_head = crow - row_token * p.hb;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t o_tmem = tmem + lane_off + C::kOCol + x * D;
-    const uint32_t p_tmem = tmem + lane_off + C::kPCol + x * (kBN / 2);
+    bool ok = true;
+    const uint32_t p_place = tmem + lane_off + C::kPCol;
+    // P.V of the tile that is number d of this row tile's is through.
+    auto wait_pv = [&](int d) {
+      ok = bounded_wait(&bars->p_free[C::s_bar(x, d)], (d / C::kSBufs) & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
+      ok = __all_sync(0xffffffffu, ok);
+    };
     uint8_t* p_row = sP + x * C::kStageBytes + row * 128;
     float lam = p.scale_log2;  // of this row
     float vd = 1.f;
     int done = 0, segs_x = 0, segs = 0, tiles = 0;
     bool staged = false;  // an output's store may still read the staging buffer
-    bool ok = true;
     uint32_t group_phase = 0;
     // Barrier of the tile's four warps; like every wait it ends when another role gave up.
     auto group_sync = [&]() {
@@ -1379,8 +1099,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       uint32_t zero[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) zero[i] = 0u;
-      tmem_st32(p_tmem, zero);
-      tmem_st32(p_tmem + 32, zero);
+#pragma unroll
+      for (int i = 0; i < C::kSBufs * kBN / 64; ++i) tmem_st32(p_place + i * 32, zero);
       tmem_wait_st();
     }
     while (ok && cur.next(p, seg)) {
@@ -1396,41 +1116,39 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         vd = p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
       }
       if constexpr (kReadyQ) {
-        // The row of Q, in place or to tensor memory, from bf16 as fp16.
+        // The row of Q, in place, to fp16 behind a power of two that brings its largest
+        // element to [1, 2): exact but for elements below 2^-14 of that one.
         ok = bounded_wait(&bars->q_full, segs & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
-        uint8_t* q_row = sQ + x * C::kQBytes + (C::kQInTmem ? crow : row) * 128;
+        uint8_t* q_row = sQ + x * C::kQBytes + row * 128;
         auto piece = [&](int i) {
-          return reinterpret_cast<uint4*>(q_row + (i / 8) * C::kQRows * 128 + ((i ^ row) & 7) * 16);
+          return reinterpret_cast<uint4*>(q_row + (i / 8) * C::kBlockBytes + ((i ^ row) & 7) * 16);
         };
-        float down = 1.f;
-        if constexpr (BF16) lam *= q_row_scale<D>(piece, down);
-        if constexpr (BF16) lam = fmaxf(lam, kLeastScale);
+        uint32_t top = 0;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t h[32];
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 v = *piece(i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 v = *piece(c * 8 + i);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              h[i * 4 + k] = BF16 ? pack2<false>(__uint_as_float(w[k] << 16) * down,
-                                                 __uint_as_float(w[k] & 0xFFFF0000u) * down)
-                                  : w[k];
-            if constexpr (!C::kQInTmem) *piece(c * 8 + i) = make_uint4(h[i * 4], h[i * 4 + 1], h[i * 4 + 2], h[i * 4 + 3]);
-          }
-          if constexpr (C::kQInTmem) tmem_st32(tmem + lane_off + C::q_col() + c * 32, h);
+          for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7F80u, w[k] >> 16 & 0x7F80u));
         }
-        if constexpr (C::kQInTmem) {
-          tmem_wait_st();
-          tc_fence_before();
-        } else {
-          fence_proxy_async_smem();
+        const uint32_t e = min(max(top >> 7, 1u), 253u);
+        const float down = __uint_as_float((254u - e) << 23);
+        lam = fmaxf(lam * __uint_as_float(e << 23), kLeastScale);
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 v = *piece(i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            h[k] = pack2<false>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+          *piece(i) = make_uint4(h[0], h[1], h[2], h[3]);
         }
+        fence_proxy_async_smem();
         mbar_arrive(&bars->q_ready[x]);
       }
       float r = -INFINITY;  // retained reference, raw score units
@@ -1447,14 +1165,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           }
           mbar_arrive(&bars->s_free[C::s_bar(x, done)]);
           if (NT == 2 && x == 0 && segs == 0 && j == 0) mbar_arrive(&bars->stagger);
-          if (j > 0) {
-            ok = bounded_wait(&bars->p_free[x], (done - 1) & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
-            ok = __all_sync(0xffffffffu, ok);
+          if (j >= C::kSBufs) {
+            wait_pv(done - C::kSBufs);
           } else if constexpr (!C::kPInTmem) {
             stage_free();
           }
           if (!ok) break;
-          mbar_arrive(&bars->p_full[x]);
+          mbar_arrive(&bars->p_full[C::s_bar(x, done)]);
           continue;
         }
         const uint32_t s_tmem = tmem + lane_off + C::kSCol + C::s_bar(x, done) * kBN + col0;
@@ -1533,14 +1250,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             }
           }
           if (blk == 0) {
-            if (j > 0) {
-              ok = bounded_wait(&bars->p_free[x], (done - 1) & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
-              if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();  // P may be overwritten, O_X is stable
-              if (__any_sync(0xffffffffu, gamma != 1.f)) {
+            // The last tile that had P in this place, or, before O can be corrected, the
+            // tile before this one is through.
+            const bool correct = j > 0 && __any_sync(0xffffffffu, gamma != 1.f);
+            if (j >= C::kSBufs || correct) {
+              if (j >= C::kSBufs) wait_pv(done - C::kSBufs);
+              if (C::kSBufs > 1 && ok && correct) wait_pv(done - 1);
+              if (!ok) break;
+              tc_fence_after();
+              if (correct) {
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                   uint32_t w32[32];
@@ -1553,8 +1271,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
                 }
                 tmem_wait_st();
               }
-            } else if constexpr (!C::kPInTmem) {
-              stage_free();
+            }
+            if constexpr (!C::kPInTmem) {
+              if (j == 0) stage_free();
               if (!ok) break;
             }
           }
@@ -1566,9 +1285,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
                   make_uint4(pk[c8 * 4], pk[c8 * 4 + 1], pk[c8 * 4 + 2], pk[c8 * 4 + 3]);
             }
           } else if constexpr (kBlk == 32) {
-            tmem_st16(p_tmem + col0 / 2 + blk * 16, pk);
+            tmem_st16(p_place + C::s_bar(x, done) * (kBN / 2) + col0 / 2 + blk * 16, pk);
           } else {
-            tmem_st32(p_tmem + col0 / 2 + blk * 32, pk);
+            tmem_st32(p_place + C::s_bar(x, done) * (kBN / 2) + col0 / 2 + blk * 32, pk);
           }
         }
         if (!ok) break;
@@ -1580,7 +1299,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        mbar_arrive(&bars->p_full[x]);
+        mbar_arrive(&bars->p_full[C::s_bar(x, done)]);
       }
       if (!ok) break;
       // ---- the segment's end
@@ -1796,7 +1515,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       }
       // The CTA that has the unit's first tile says where its parts are.
       if (seg.j0 == 0 && threadIdx.x == 0 && p.cluster == 0) {
-        say_parts(p, bars, seg);
+        const int behind = seg.nt - (seg.j1 - seg.j0);  // the unit's tiles in the runs after this one
+        const int per = static_cast<int>(min(bars->per, 0x7FFFFFFFLL));
+        p.parts[(static_cast<long long>(seg.b) * p.heads + seg.u) * p.blocks + seg.k] =
+            make_int2(blockIdx.x, behind == 0 ? 1 : 2 + (behind - 1) / per);
       }
       tiles += seg.j1 - seg.j0;
       ++segs;
@@ -1811,7 +1533,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         else if (p.cluster == 2) fold_cluster<C, D, BF16, NT, 2>(p, seg, smem, bars);
         else fold_cluster<C, D, BF16, NT, 1>(p, seg, smem, bars);
       }
-    }
     }
   }
   // The others' arrivals at the first barrier, and the second: no CTA ends while its
@@ -2037,7 +1758,7 @@ int launch_nt(Params& p, const PagedPrefillArgs& a, const Shape& s) {
     const int rows = s.hb * s.tokens;
     const long long tiles = s.units * (((p.max_pages << p.page_shift) + kBN - 1) / kBN);  // at most
     if (tiles >= kCopyRun * p.ctas) {
-      if (rows <= kBM / 4) return launch_t<D, BF16, 1, FP4, FP4 && D == 128 ? kTurned : 4>(p, a, s);
+      if (rows <= kBM / 4) return launch_t<D, BF16, 1, FP4, 4>(p, a, s);
       if (rows <= kBM / 2) return launch_t<D, BF16, 1, FP4, 2>(p, a, s);
     }
   }
