@@ -278,6 +278,34 @@ def test_offsets_beyond_32_bits():
              1 / math.sqrt(d), pu.u(torch.float16), 2.0 ** -24, True, pu.u(torch.bfloat16))
 
 
+@pytest.mark.parametrize("S", [1, 200])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_longest_cache(bits, S):
+    """As many tokens as a page table may hold, where the pages that are looked up ahead
+    would be past what 32 bits count.  All but the last two pages are one page; the
+    queries follow a key of the last but one, beside which the other pages' weights are
+    as good as 0."""
+    dtype, d, page = torch.bfloat16, 64, 1024
+    g = torch.Generator().manual_seed(41)
+    pool = Pool(bits, 3, 1, page, d, dtype, g)
+    n_pages, rest = (2 ** 31 - 257) // page, 700
+    table = torch.zeros(1, n_pages, dtype=torch.int32)
+    table[0, -2:] = torch.tensor([1, 2])
+    tail = torch.tensor([1, 2], dtype=torch.int32)
+    n = page + rest
+    k, v = pool.values(0, tail, n), pool.values(1, tail, n)
+    q = (8 * k[:, 5].float()).to(dtype)[None, :, None].expand(1, 1, S, d).contiguous()
+    scale = 1 / math.sqrt(d)
+    first = pool.values(0, torch.zeros(1, dtype=torch.int32), page)[0].double() @ q[0, 0, 0].double() * scale
+    own = float(k[0, 5].double() @ q[0, 0, 0].double()) * scale
+    assert torch.logsumexp(first, 0) + math.log(n_pages) < own - 20
+    o, lse = _forward(pool, q.cuda(), table, [(n_pages - 1) * page + rest], None, scale=scale)
+    assert gb.gbattn_device_status() == 0
+    half_p = pu.u(torch.float16) if bits == 4 else pu.u(dtype)
+    cu.check(o, lse, q, lambda b, _: (k, v), [n], [S], True, scale, half_p, 2.0 ** -24 if bits == 4 else 0.0, bits == 4,
+             pu.u(dtype))
+
+
 @pytest.mark.parametrize("S", [3, 90])
 @pytest.mark.parametrize("bits", [16, 4])
 def test_streams_graphs_and_two_calls_at_once(bits, S):
