@@ -179,7 +179,7 @@ struct __align__(8) Barriers {
   long long scan[16];      // of the warps: tiles,
   long long scan_units[16];  // units that have any,
   int scan_most[16];         // and the most tiles of a unit
-  float state[2 * kBM];    // of the rows, with clusters: log2 of the sum of weights
+  float state[kBM];        // of the rows, with clusters: log2 of the sum of weights
   uint32_t tmem_base;
   int abort_flag;
   uint8_t bad[2][kTileRing];       // 16-key blocks of a tile (of K, of V) that have no page
@@ -461,11 +461,13 @@ __device__ __forceinline__ bool any_not_finite(const uint8_t* tile, int r0, int 
   return __any_sync(0xffffffffu, (acc & 0x7FFFu) > kInf || (acc >> 16 & 0x7FFFu) > kInf);
 }
 
-// Where the first 16-byte piece of a row's state's half with columns 4 c4, .. is.
+// Where the first 16-byte piece of a row's state's half with columns 4 c4, .. is: in the
+// place of Q or in the one for outputs (4 bits: behind Q all the same, where the first
+// keys were).
 template <typename C>
-__device__ __forceinline__ uint8_t* state_row(uint8_t* smem, int x, int row, int c4) {
+__device__ __forceinline__ uint8_t* state_row(uint8_t* smem, int row, int c4) {
   constexpr int kHalf = C::kDim / 8;  // pieces of half a row
-  return (c4 < kHalf ? smem + C::kQOff + x * C::kQBytes : smem + C::kPOff + x * C::kStageBytes) + row * (kHalf * 16);
+  return smem + (c4 < kHalf ? C::kQOff : C::kPOff) + row * (kHalf * 16);
 }
 
 __device__ __forceinline__ float ld_cluster(uint32_t a) {
@@ -485,38 +487,38 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
 // The cluster's CTAs fold their states, a share of the unit's rows each, and write
 // them; rows that count no key become zeros.  By the softmax threads, lanes along
 // a row.
-template <typename C, int D, bool BF16, int NT, int CTAS>
+template <typename C, int D, bool BF16, int CTAS>
 __device__ __forceinline__ void fold_cluster(const Params& p, const Seg& seg, uint8_t* smem, Barriers* bars) {
-  constexpr int kItems = NT * kBM / CTAS * (D / 4);          // pieces of four columns
-  constexpr int kAtOnce = CTAS == 8 ? 2 : CTAS == 4 ? 4 : 8;  // of a thread, requested together
+  constexpr int kItems = kBM / CTAS * (D / 4);  // pieces of four columns
+  // Of a thread, requested together: one at a time waited for each trip to another SM.
+  constexpr int kAtOnce = CTAS == 8 ? 2 : CTAS == 4 ? 4 : 8;
   const int rank = blockIdx.x % CTAS;
   const int kvh = kv_head(p, seg.u), head0 = first_head(p, seg.u);
-  for (int i0 = threadIdx.x; i0 < kItems; i0 += kAtOnce * NT * kBM) {
+  for (int i0 = threadIdx.x; i0 < kItems; i0 += kAtOnce * kBM) {
     float m[kAtOnce][CTAS];
     float4 o[kAtOnce][CTAS];
     long long hrow[kAtOnce];
 #pragma unroll
     for (int v = 0; v < kAtOnce; ++v) {
       // (threads without a piece of their own read some)
-      const int i = i0 + v * NT * kBM;
-      const int at = (i < kItems ? i / (D / 4) : 0) * CTAS + rank, c4 = i % (D / 4);  // every CTAS-th row
-      const int x = at / kBM, row = at % kBM;
+      const int i = i0 + v * kBM;
+      const int row = (i < kItems ? i / (D / 4) : 0) * CTAS + rank, c4 = i % (D / 4);  // every CTAS-th row
       const int row_token = token_of(p, row), head = head0 + row - row_token * p.hb;
-      const int t = (seg.k * NT + x) * p.tq_tokens + row_token;
+      const int t = seg.k * p.tq_tokens + row_token;
       hrow[v] = i < kItems && row_token < p.tq_tokens && head < p.g && t < p.S
                     ? (static_cast<long long>(seg.b) * p.H + kvh * p.g + head) * p.S + t
                     : -1;
-      const uint8_t* piece = state_row<C>(smem, x, row, c4) + ((c4 % (D / 8) ^ (row & 7)) << 4);
+      const uint8_t* piece = state_row<C>(smem, row, c4) + ((c4 % (D / 8) ^ (row & 7)) << 4);
 #pragma unroll
       for (int r = 0; r < CTAS; ++r) {
-        m[v][r] = ld_cluster(mapa_shared(&bars->state[at], r));
+        m[v][r] = ld_cluster(mapa_shared(&bars->state[row], r));
         o[v][r] = ld_cluster4(mapa_shared(piece, r));
       }
     }
 #pragma unroll
     for (int v = 0; v < kAtOnce; ++v) {
       if (hrow[v] < 0) continue;
-      const int c4 = (i0 + v * NT * kBM) % (D / 4);
+      const int c4 = (i0 + v * kBM) % (D / 4);
       float M = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int r = 0; r < CTAS; ++r) M = fmaxf(M, m[v][r]);
@@ -1411,12 +1413,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           if (!whole) p.part_ml[part * kBM + crow] = make_float2(M, L);
           else if (p.lse != nullptr) p.lse[hrow] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
         }
-      } else if (p.cluster > 1) {
+      } else if (NT == 1 && p.cluster > 1) {
         // The row's state: O normalised, and log2 of the sum of its weights.  O lies in
-        // this tile's places of Q and P, which are through, half a row each; 16-byte
-        // pieces are permuted against bank conflicts.
+        // two places that are through, half a row each; 16-byte pieces are permuted
+        // against bank conflicts.
         const bool counts = real && nx > 0 && l != 0.f;
-        bars->state[x * kBM + row] = counts ? r * lam + __log2f(l) : -INFINITY;
+        bars->state[row] = counts ? r * lam + __log2f(l) : -INFINITY;
         if (__any_sync(0xffffffffu, counts)) {
           const float inv = vd / l;
 #pragma unroll 1
@@ -1425,7 +1427,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             tmem_ld32(o_tmem + c * 32, u);
             tmem_wait_ld();
             reg_fence32(u);
-            uint8_t* dst = state_row<C>(smem, x, row, c * 8);
+            uint8_t* dst = state_row<C>(smem, row, c * 8);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               *reinterpret_cast<float4*>(dst + (((c * 8 + i) % (D / 8) ^ (row & 7)) << 4)) =
@@ -1528,13 +1530,22 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     }
     if (staged && wq == 0 && lane == 0) bulk_wait_group_read0();
     if (COPIES == 1 && p.cluster > 0) {
-      if (segs == 0) bars->state[x * kBM + row] = -INFINITY;  // no tile for this CTA
+      if (segs == 0) {  // no tile for this CTA
+        if (NT == 1) bars->state[row] = -INFINITY;
+        const int head = first_head(p, seg.u) + row_head, t = (seg.k * NT + x) * p.tq_tokens + row_token;
+        if (p.cluster == 1 && row_token < p.tq_tokens && head < p.g && t < p.S) {  // the unit has no key: zeros
+          const long long hrow = (static_cast<long long>(seg.b) * p.H + kv_head(p, seg.u) * p.g + head) * p.S + t;
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + hrow * D);
+#pragma unroll 1
+          for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (p.lse != nullptr) p.lse[hrow] = -INFINITY;
+        }
+      }
       cluster_sync_all();
-      if (ok && (p.cluster > 1 || segs == 0)) {  // (a CTA of its own has written its unit, or writes zeros)
-        if (p.cluster == 8) fold_cluster<C, D, BF16, NT, 8>(p, seg, smem, bars);
-        else if (p.cluster == 4) fold_cluster<C, D, BF16, NT, 4>(p, seg, smem, bars);
-        else if (p.cluster == 2) fold_cluster<C, D, BF16, NT, 2>(p, seg, smem, bars);
-        else fold_cluster<C, D, BF16, NT, 1>(p, seg, smem, bars);
+      if (NT == 1 && ok) {
+        if (p.cluster == 8) fold_cluster<C, D, BF16, 8>(p, seg, smem, bars);
+        else if (p.cluster == 4) fold_cluster<C, D, BF16, 4>(p, seg, smem, bars);
+        else if (p.cluster == 2) fold_cluster<C, D, BF16, 2>(p, seg, smem, bars);
       }
     }
   }
@@ -1659,18 +1670,31 @@ struct Shape {
   int hb, tokens, nblk, heads, nt, blocks;
   long long units;
 };
-Shape shape_of(int B, int H, int Hkv, int S) {
+Shape shape_of(int B, int H, int Hkv, int S, int nt) {
   Shape s;
   const int g = H / Hkv;
   s.nblk = (g + kBM - 1) / kBM;
   s.hb = (g + s.nblk - 1) / s.nblk;
   s.tokens = kBM / s.hb;
   s.heads = Hkv * s.nblk;
-  s.nt = S <= s.tokens ? 1 : 2;
-  if (s.nt == 1) s.tokens = S;
+  if (S < s.tokens) s.tokens = S;
+  s.nt = S == s.tokens ? 1 : nt;
   s.blocks = (S + s.nt * s.tokens - 1) / (s.nt * s.tokens);
   s.units = static_cast<long long>(B) * s.heads * s.blocks;
   return s;
+}
+
+// One tile where units of one find an SM each and two tiles would have at most
+// kOneTileRun key tiles a CTA: more CTAs then share the work, and a tile alone starts and
+// ends sooner.  Elsewhere two tiles share each key tile.  Measured with 8 KV heads of 4
+// query heads, d = 128 (us by one tile, by two): one sequence, 500 tokens of 1000 18.6,
+// 22.7 (4 bits 22.6, 31.4), 100 of 4000 22.6, 31.0 (26.8, 43.0); 4 sequences, 100 of 4000
+// 41.1, 45.2 (52.4, 61.3).  Beyond the bounds: 4 sequences, 500 of 1000 70.7, 52.4; 100 of
+// 16000 168, 113.
+constexpr long long kOneTileRun = 16;
+Shape shape_of(int B, int H, int Hkv, int S, long long max_len, int num_sms) {
+  const Shape one = shape_of(B, H, Hkv, S, 1), two = shape_of(B, H, Hkv, S, 2);
+  return one.units <= num_sms && two.units * ((max_len + kBN - 1) / kBN) <= kOneTileRun * num_sms ? one : two;
 }
 
 // CTAs that can have work: one for each key tile at most.
@@ -1727,14 +1751,18 @@ int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   if constexpr (COPIES == 1) {
     // CTAs of a cluster that takes a unit, or 0: runs of the list.  The host knows what
     // the pages of a sequence can hold, not the lengths.  Clusters need neither the
-    // division of the list nor the second kernel; one of several CTAs folds its states,
-    // the longer the fewer it has.  In tiles of a unit, measured: kScan and kFold.
+    // division of the list nor the second kernel (kScan); one of several CTAs folds its
+    // states, the longer the fewer it has (fold); both in key tiles of a unit, fitted to
+    // measured times.  Clusters and runs, us in a captured graph, 8 KV heads of 4 query
+    // heads, d = 128: 16 tokens of 1000 12.3, 14.3, of 4000 14.3, 22.3; of 16000 the runs
+    // are taken.  (With two row tiles the units are too many for several CTAs each, or
+    // have so many key tiles that runs win.)
     constexpr float kScan = NT == 2 ? 5.f : 9.f;
-    const float fold = (NT == 2 ? 10.f : 12.f) * static_cast<float>(s.hb * s.tokens) / kBM;  // of one CTA alone
+    const float fold = 12.f * static_cast<float>(s.hb * s.tokens) / kBM;  // of one CTA alone
     static std::atomic<int> at_once[4];  // per instantiation, for clusters of 1, 2, 4 and 8
     const int tiles = ((p.max_pages << p.page_shift) + kBN - 1) / kBN;
     float best = static_cast<float>(s.units) * tiles / p.ctas + kScan;
-    for (int i = 0, n = 1; i < 4; ++i, n *= 2) {
+    for (int i = 0, n = 1; i < (NT == 1 ? 4 : 1); ++i, n *= 2) {
       const float cost = static_cast<float>((tiles + n - 1) / n) + (n > 1 ? fold / n : 0.f);
       if (s.units * n > a.num_sms || n > tiles || cost >= best) continue;
       if (n > 1 && s.units > clusters_at_once(kern, C::kThreads, C::kSmemBytes, n, at_once[i])) continue;
@@ -1775,14 +1803,20 @@ int launch_d(Params& p, const PagedPrefillArgs& a, const Shape& s) {
 }  // namespace
 
 size_t paged_prefill_workspace_bytes(int B, int H, int Hkv, int S, int d, int max_len) {
-  const Shape s = shape_of(B, H, Hkv, S);
-  return static_cast<size_t>(max_ctas(s, max_len)) * 2 * s.nt * kBM * (static_cast<size_t>(d) + 2) * sizeof(float) +
-         static_cast<size_t>(s.units) * sizeof(int2);
+  size_t most = 0;  // of either shape: the choice depends on the GPU
+  for (int nt = 1; nt <= 2; ++nt) {
+    const Shape s = shape_of(B, H, Hkv, S, nt);
+    const size_t bytes =
+        static_cast<size_t>(max_ctas(s, max_len)) * 2 * s.nt * kBM * (static_cast<size_t>(d) + 2) * sizeof(float) +
+        static_cast<size_t>(s.units) * sizeof(int2);
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 
 int launch_prefill_paged(const PagedPrefillArgs& a) {
   const CacheArgs& c = a.cache;
-  const Shape s = shape_of(a.B, a.H, c.Hkv, a.S);
+  const Shape s = shape_of(a.B, a.H, c.Hkv, a.S, static_cast<long long>(c.max_pages) << c.page_shift, a.num_sms);
   Params p{};
   p.page_table = c.page_table;
   p.seqlens = c.seqlens;

@@ -56,14 +56,15 @@ def test_forward_refusals(lib, fp4):
 
 
 def test_forward_workspace(lib):
-    """States of one or two tiles of 128 rows for the most CTAs that can have work."""
+    """States of one or two tiles of 128 rows, whichever takes more, for the most CTAs that can have work."""
     size = lib.attn_fwd_paged_workspace_bytes
     one, two = 2 * 128 * 130 * 4, 2 * 256 * 130 * 4
     assert size(1, 32, 8, 16, 128, 1000) == 64 * one + 8 * 8      # 8 units of 8 tiles
     assert size(1, 32, 8, 32, 128, 1 << 20) == 160 * one + 8 * 8  # 128 rows: one tile
     assert size(1, 32, 8, 33, 128, 1 << 20) == 160 * two + 8 * 8
     assert size(4, 32, 8, 2048, 128, 16384) == 160 * two + 4 * 8 * 32 * 8
-    assert size(1, 130, 1, 2, 64, 64) == 2 * (2 * 256 * 66 * 4) + 2 * 8  # two blocks of 65 heads
+    # two blocks of 65 heads, a token a tile: 4 units of one tile (more than 2 of two), whichever are taken
+    assert size(1, 130, 1, 2, 64, 64) == 4 * (2 * 128 * 66 * 4) + 4 * 8
     assert size(1, 5, 2, 4, 64, 64) == 0 and size(1, 4, 2, 0, 64, 64) == 0 and size(1, 4, 2, 4, 64, 0) == 0
 
 

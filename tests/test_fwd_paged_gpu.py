@@ -62,6 +62,12 @@ CHUNKS = [
     (torch.float16, 2, 1, 128, 16, 20, [5, 12, 20], None),  # rows before the sequence's start are padding
     (torch.bfloat16, 2, 2, 64, 16, 4, [0, 0], None),
     (torch.bfloat16, 4, 2, 128, 64, 3, [20000], None),
+    # more units of one row tile than SMs, of two not: a CTA for each
+    (torch.bfloat16, 8, 8, 128, 64, 200, [200, 300, 129, 0, 500, 257, 256, 131, 420, 100], [200, 200, 1, 0, 130, 200, 128, 131, 199, 100]),
+    (torch.float16, 16, 8, 64, 16, 100, [100, 300, 65, 0, 500, 257, 256, 131, 420, 64], [100, 100, 1, 0, 65, 100, 64, 99, 100, 64]),
+    # few units of one row tile, of one or several CTAs each; rows before the sequence's start
+    (torch.bfloat16, 7, 1, 128, 32, 130, [100, 700, 130], None),
+    (torch.float16, 12, 4, 64, 128, 300, [300, 1200], None),
 ]
 
 
