@@ -21,7 +21,10 @@
 // bits [4, 8192] tokens of 16 heads take 79.5 us, 6.8 TB/s.  A partial rotation by
 // halves reads each turning piece's partner again, when it is needed: [2, 4096]
 // tokens of 32 + 16 heads 45 us into 16 bits and 48 into 4, where the other
-// rotations take 33 and 31.
+// rotations take 33 and 31.  Positions of several axes (AXES) add two dependent loads
+// and, where axes take turns, loads of single angles: four chunks of 2048 tokens of 32 +
+// 16 heads 35 us into 16 bits and 33 into 4 by the slots, 37 and 34 by sections of 16,
+// 24 and 24 pairs, 39 and 36 by axes in turn.
 #include <cuda_runtime.h>
 
 #include <type_traits>

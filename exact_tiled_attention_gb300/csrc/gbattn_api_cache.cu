@@ -1,6 +1,7 @@
 // gbattn_api_cache.cu -- the C ABI of the operators around a paged cache:
-// argument validation and dispatch (attn_qk_norm_rope, attn_cache_append,
-// attn_cache_gather, attn_decode_paged, their 4-bit forms and the backward).
+// argument validation and dispatch (attn_qk_norm_rope, attn_cache_append, their forms
+// with positions of several axes, attn_cache_gather, attn_decode_paged, attn_fwd_paged,
+// the 4-bit forms and the backward).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -1,39 +1,65 @@
 // prefill_paged.cu -- attention of the last `rows` tokens of every sequence over
-// a paged cache that holds them and all tokens before: a prompt's next chunk, or
-// drafted tokens to check, for sequences of different lengths in one call.
+// a paged cache of 16 or 4 bits that holds them and all tokens before: a prompt's next
+// chunk, or drafted tokens to check, for sequences of different lengths in one call.
 //
 //   o_i = sum_j exp(scale q_i.k_j - lse_i) v_j,  lse_i = log sum_j exp(scale q_i.k_j)
 //
-// over the keys j <= position of i (causal), or all of the sequence's keys.
+// over the keys j <= position of i (causal), or all of the sequence's keys.  One pass
+// over the keys with the running maximum (moved only when it rises by more than 2^8, as
+// in the forward over contiguous tensors) and sum in fp32.
 //
 // Work.  A unit is a block of query tokens of one sequence and KV head: NT tiles
 // ("H", "L") of 128 rows, whose rows are tokens and, for each, the query heads of
 // the KV head (up to hb of them), so that a key tile serves all of them and a
-// short chunk still fills rows.  Its key axis has tiles of 128 keys.  The list of
-// all units' key tiles (order: sequence, head, block of tokens, tile) is cut into
-// equal runs, one for each CTA (one an SM), whatever the lengths are.  A run
-// covers whole units, which the CTA finishes itself, and at its two ends parts of
-// units, whose states (m, l, o) it leaves in the workspace; a second kernel folds
-// those and writes the zeros of padding rows.  Where equal numbers of whole units
-// take hardly longer than equal runs (kSplitCost), CTAs get those.  The division
-// follows from the lengths alone, so results repeat bitwise.
+// short chunk still fills rows.  Its key axis has tiles of 128 keys.
 //
-// A CTA works through its run without a stop between units: the loader, the MMA
+// Division.  (a) The list of all units' key tiles (order: sequence, head, block of
+// tokens, tile) is cut into equal runs, one for each CTA (one an SM), whatever the
+// lengths are.  A run covers whole units, which the CTA finishes itself, and at its two
+// ends parts of units, whose states (m, l, o) it leaves in the workspace; a second
+// kernel folds those and writes the zeros of padding rows.  Every CTA finds its run from
+// the lengths, so the host knows none, and results repeat bitwise.  (b) Where equal
+// numbers of whole units take hardly longer than equal runs (kSplitCost), CTAs get
+// those.  (c) Where the page table has room for few key tiles (launch_t), a cluster of 1
+// to 8 CTAs takes each unit and folds its states through shared memory: no division, no
+// workspace, no second kernel.
+//
+// A CTA works through its run without a stop between units: the loaders, the MMA
 // issuers, the softmax warps and the guard walk the same list of segments each at
-// its own pace.  Tensor memory: S_H, S_L, O_H, O_L and, at d = 64, P_H, P_L (at
-// d = 128 P goes through shared memory), as in the forward over contiguous tensors.
+// its own pace.
 //
 // Warp roles: warps 0-3 (4-7) softmax, correction and epilogue of tile H (L),
-// thread = row; then lanes 0 of a warp for each tile's MMAs; a warp that loads
-// (lane = one box of a page); a warp that guards V.
+// thread = row; lane 0 of two warps issues MMAs (two tiles: one each; one tile: one the
+// products with K, the other those with V); over 16 bits a warp that loads (lane = one
+// box of a page) and one that guards V; over 4 bits two warps that load (K, V) and four
+// or eight that convert codes and factors into fp16 tiles, exactly.
 //
-// The guard.  A key that a row does not see has weight 0, but 0 times a NaN or an
-// infinity in its row of V would be NaN.  Tiles with keys that some row does not
-// see (the diagonal's, and the sequence's last) therefore pass through a warp
-// which zeroes the rows of V behind the sequence, zeroes what is not finite in the
-// rows that some query token sees and others do not, and notes for each column
-// the first such key; rows that see it get NaN there at the end.  The score of a
-// key that a row does not see becomes -inf, whatever it was.
+// Tensor memory (512 columns): two tiles: S_H, S_L, O_H, O_L and, at d = 64, P_H, P_L
+// (at d = 128 P goes through shared memory).  One tile: two places each of S and P,
+// and O.
+//
+// The guard (16 bits; codes of 4 bits and their factors are finite).  A key that a row
+// does not see has weight 0, but 0 times a NaN or an infinity in its row of V would be
+// NaN.  Tiles with keys that some row does not see (the diagonal's, and the sequence's
+// last) therefore pass through a warp which zeroes the rows of V behind the sequence,
+// zeroes what is not finite in the rows that some query token sees and others do not,
+// and notes for each column the first such key; rows that see it get NaN there at the
+// end.  The score of a key that a row does not see becomes -inf, whatever it was.
+//
+// Fewer bits than fp32: the weights are rounded to the cache's 16-bit type for P.V (as in
+// the forward over contiguous tensors; tensor cores take both operands in 16 bits), over
+// 4 bits to fp16, which 2^-11 keeps below the codes' own spacing; bf16 queries over 4
+// bits become fp16 behind a power of two a row.  The sum of weights, the maximum, O and
+// what is folded stay fp32.
+//
+// Measured (us among other calls; 32 query heads on 8, d = 128, pages of 64; floor in
+// brackets from the copy rate and the dense bf16 rate):
+//   bound by the tensor pipe and the softmax's chain: 4096 tokens of 32768 1400 (1065,
+//   1475 TFLOP/s), 2048 tokens of 4 sequences of up to 16384 732 (562), over 4 bits 855;
+//   by HBM: 5 tokens of 64 sequences of 1024 to 32768 600 (653 at the rate of a copy;
+//   reads alone go faster, 7.4 TB/s); over 4 bits 422 (184) by the chains of products
+//   into one accumulator, about 100 cycles each whatever their size, 16 a key tile;
+//   by latency: 16 tokens of one sequence of 1000 10.8 (0.6).
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -49,12 +75,15 @@ constexpr int kBN = 128;          // keys of a tile
 constexpr int kMaxCtas = 160;     // bound of the grid, for the workspace's size
 constexpr float kRescaleThreshold = 8.f;  // base-2 units
 constexpr int kPBlock = 64;
-// A scale of scores is at least this, so that -inf times it stays -inf; finite products
-// of Q and K are then as good as 0.
+// A scale of scores is at least this, so that -inf times it stays -inf: FLT_MIN.  (Scores
+// that a smaller scale makes would differ from 0 only if q.k passed 1e36.)
 constexpr float kLeastScale = 1.1754944e-38f;
 constexpr int kSegRing = 4;       // segments whose notes of the guard are kept: it is at most 3 ahead
 // Key tiles that the states of split units cost (writing, and a second kernel that has
-// to fold them) for units of one and two row tiles.
+// to fold them) for units of one and two row tiles.  Whole units and runs, us in a
+// captured graph: 2000 tokens of one prompt from its start 67, 77; 3 of 40 sequences of
+// 400 to 1000, 4 bits, 49, 57; 3 of 40 of 2000 68, 63; 40 of 8 of 4000 63, 48; 5 of 64 of
+// 1024 to 32768 994, 608.
 template <int NT>
 constexpr int kSplitCost = NT == 2 ? 6 : 4;
 constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
@@ -63,7 +92,8 @@ constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
 // each copy's warps take another part of the keys (the other weights of their rows
 // stay 0): the softmax of a tile, which otherwise waits for one or two of the four
 // warps, takes a half or a quarter of the time.  The copies are folded at a segment's
-// end.
+// end.  5 tokens of 64 sequences (20 rows), with and without: 4 bits 422, 695 us, 16 bits
+// at d = 64 340, 444; at d = 128 in 16 bits HBM bounds both.
 template <int D, int NT, bool FP4, int COPIES>
 struct Cfg {
   static_assert(NT == 1 || COPIES == 1, "copies are of one tile");
@@ -84,8 +114,8 @@ struct Cfg {
   static constexpr int kColBlocks = D / 64;
   static constexpr int kTileBytes = kBM * D * 2;
   static constexpr int kBlockBytes = kBM * 128;
-  // Where an output waits for its store: P's place, or one of its own (one tile over 4
-  // bits: none, threads store their rows).
+  // Where an output waits for its store: P's place, or one of its own.  One tile over 4
+  // bits has none, threads store their rows: shared memory holds more key tiles instead.
   // Copies are folded there, 32 columns at a time, by threads that store the sums.
   static constexpr bool kDirectO = NT == 1 && (FP4 || COPIES > 1);
   static constexpr int kStageBytes = COPIES > 1 ? kBM * 32 * 4 : kDirectO ? 0 : kPInTmem ? kTileBytes : kBM * kBN * 2;
@@ -118,7 +148,9 @@ struct Cfg {
   static constexpr int kConvertWarps = FP4 ? (NT == 2 ? 4 : 8) : 0;
   static constexpr int kThreads = 128 * (NT + 1) + 32 * kConvertWarps;
   // Registers a thread: at launch, and after the warpgroups have divided them (not
-  // with one tile over 16 bits, where there are enough).
+  // with one tile over 16 bits, where there are enough).  One tile over 4 bits, softmax /
+  // control / conversion: 240/64/104 423 us (5 tokens of 64 sequences), 208/64/120 431,
+  // 160/96/128 and 224/64/112 more.
   static constexpr bool kSplit = FP4 || NT == 2;
   static constexpr int kLaunchRegs = FP4 ? 128 : 168;
   static constexpr int kSoftmaxRegs = FP4 ? (NT == 2 ? 192 : 240) : 216;
@@ -166,7 +198,7 @@ struct Seq {
 
 struct __align__(8) Barriers {
   uint64_t q_full, q_empty;
-  uint64_t q_ready[2];     // queries converted to fp16 (bf16 over 4 bits), or in tensor memory
+  uint64_t q_ready[2];     // queries converted to fp16 (bf16 over 4 bits)
   uint64_t raw_empty[12];  // 4 bits: codes and factors converted (raw: copied)
   uint64_t kv_full[12], kv_empty[12], raw[12];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_full[2], mma_done[2];
@@ -1730,6 +1762,42 @@ template <int D, bool BF16, int NT, bool FP4, int COPIES>
 int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   using C = Cfg<D, NT, FP4, COPIES>;
   static_assert(C::kSmemBytes <= 232448, "shared memory of a CTA");
+  auto kern = prefill_paged_kernel<D, BF16, NT, FP4, COPIES>;
+  static std::atomic<unsigned long long> attr_done{0};  // per instantiation
+  if (!set_smem_limit_once(kern, C::kSmemBytes, attr_done)) return -1;
+  if constexpr (COPIES == 1) {
+    // CTAs of a cluster that takes a unit, or 0: runs of the list.  The host knows what
+    // the pages of a sequence can hold, not the lengths.  Clusters need neither the
+    // division of the list nor the second kernel (kScan); one of several CTAs folds its
+    // states, the longer the fewer it has (fold); both in key tiles of a unit, fitted to
+    // measured times.  Clusters and runs, us in a captured graph, 8 KV heads of 4 query
+    // heads, d = 128: 16 tokens of 1000 12.3, 14.3, of 4000 14.3, 22.3; of 16000 the runs
+    // are taken.  (With two row tiles the units are too many for several CTAs each, or
+    // have so many key tiles that runs win.)
+    constexpr float kScan = NT == 2 ? 5.f : 9.f;
+    // Few rows have copies in runs: a key tile takes a CTA of a cluster `tile` times as
+    // long.  3 tokens of 40 sequences over 4 bits, with and without copies: of 800 50, 63
+    // us, of 200 35, 37.  5 tokens of 8 sequences over 4 bits, copies and clusters: of 4000
+    // 35.0, 38.9, of 1000 21.2, 20.5; over 16 bits with d = 64, of 2000 22.5, 18.4.
+    const int rows = s.hb * s.tokens;
+    const bool copies = NT == 1 && (FP4 || D == 64) && rows <= kBM / 2;
+    const float tile = !copies ? 1.f : FP4 ? 1.6f : 1.3f;
+    const float fold = 12.f * static_cast<float>(rows) / kBM;  // of one CTA alone
+    static std::atomic<int> at_once[4];  // per instantiation, for clusters of 1, 2, 4 and 8
+    const int tiles = ((p.max_pages << p.page_shift) + kBN - 1) / kBN;
+    float best = static_cast<float>(s.units) * tiles / p.ctas + kScan;
+    for (int i = 0, n = 1; i < (NT == 1 ? 4 : 1); ++i, n *= 2) {
+      const float cost = tile * static_cast<float>((tiles + n - 1) / n) + (n > 1 ? fold / n : 0.f);
+      if (s.units * n > a.num_sms || n > tiles || cost >= best) continue;
+      if (n > 1 && s.units > clusters_at_once(kern, C::kThreads, C::kSmemBytes, n, at_once[i])) continue;
+      p.cluster = n;
+      best = cost;
+    }
+    if constexpr (NT == 1 && (FP4 || D == 64)) {
+      if (copies && p.cluster == 0)
+        return rows <= kBM / 4 ? launch_t<D, BF16, 1, FP4, 4>(p, a, s) : launch_t<D, BF16, 1, FP4, 2>(p, a, s);
+    }
+  }
   const CacheArgs& c = a.cache;
   const int page = 1 << c.page_shift;
   p.box_rows = page < kBN ? page : kBN;
@@ -1745,31 +1813,6 @@ int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   } else if (!make_tmap_3d(&p.tk, c.data[0], BF16, D, page, static_cast<long long>(c.n_pages) * c.Hkv, p.box_rows) ||
       !make_tmap_3d(&p.tv, c.data[1], BF16, D, page, static_cast<long long>(c.n_pages) * c.Hkv, p.box_rows))
     return -1;
-  auto kern = prefill_paged_kernel<D, BF16, NT, FP4, COPIES>;
-  static std::atomic<unsigned long long> attr_done{0};  // per instantiation
-  if (!set_smem_limit_once(kern, C::kSmemBytes, attr_done)) return -1;
-  if constexpr (COPIES == 1) {
-    // CTAs of a cluster that takes a unit, or 0: runs of the list.  The host knows what
-    // the pages of a sequence can hold, not the lengths.  Clusters need neither the
-    // division of the list nor the second kernel (kScan); one of several CTAs folds its
-    // states, the longer the fewer it has (fold); both in key tiles of a unit, fitted to
-    // measured times.  Clusters and runs, us in a captured graph, 8 KV heads of 4 query
-    // heads, d = 128: 16 tokens of 1000 12.3, 14.3, of 4000 14.3, 22.3; of 16000 the runs
-    // are taken.  (With two row tiles the units are too many for several CTAs each, or
-    // have so many key tiles that runs win.)
-    constexpr float kScan = NT == 2 ? 5.f : 9.f;
-    const float fold = 12.f * static_cast<float>(s.hb * s.tokens) / kBM;  // of one CTA alone
-    static std::atomic<int> at_once[4];  // per instantiation, for clusters of 1, 2, 4 and 8
-    const int tiles = ((p.max_pages << p.page_shift) + kBN - 1) / kBN;
-    float best = static_cast<float>(s.units) * tiles / p.ctas + kScan;
-    for (int i = 0, n = 1; i < (NT == 1 ? 4 : 1); ++i, n *= 2) {
-      const float cost = static_cast<float>((tiles + n - 1) / n) + (n > 1 ? fold / n : 0.f);
-      if (s.units * n > a.num_sms || n > tiles || cost >= best) continue;
-      if (n > 1 && s.units > clusters_at_once(kern, C::kThreads, C::kSmemBytes, n, at_once[i])) continue;
-      p.cluster = n;
-      best = cost;
-    }
-  }
   if (p.cluster > 0)
     return launch_after(kern, dim3(p.blocks * p.cluster, p.heads, p.B), C::kThreads, a.stream, p, C::kSmemBytes,
                         p.cluster);
@@ -1780,24 +1823,10 @@ int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
   return launch_after(prefill_paged_merge_kernel<D, NT>, dim3(static_cast<unsigned>(ctas)), kMergeThreads, a.stream, p);
 }
 
-constexpr long long kCopyRun = 16;  // tiles of a CTA that make copies worth their folding
-
-template <int D, bool BF16, bool FP4>
-int launch_nt(Params& p, const PagedPrefillArgs& a, const Shape& s) {
-  if (s.nt == 2) return launch_t<D, BF16, 2, FP4, 1>(p, a, s);
-  if constexpr (FP4 || D == 64) {
-    const int rows = s.hb * s.tokens;
-    const long long tiles = s.units * (((p.max_pages << p.page_shift) + kBN - 1) / kBN);  // at most
-    if (tiles >= kCopyRun * p.ctas) {
-      if (rows <= kBM / 4) return launch_t<D, BF16, 1, FP4, 4>(p, a, s);
-      if (rows <= kBM / 2) return launch_t<D, BF16, 1, FP4, 2>(p, a, s);
-    }
-  }
-  return launch_t<D, BF16, 1, FP4, 1>(p, a, s);
-}
 template <int D, bool BF16>
 int launch_d(Params& p, const PagedPrefillArgs& a, const Shape& s) {
-  return a.cache.fp4() ? launch_nt<D, BF16, true>(p, a, s) : launch_nt<D, BF16, false>(p, a, s);
+  if (a.cache.fp4()) return s.nt == 2 ? launch_t<D, BF16, 2, true, 1>(p, a, s) : launch_t<D, BF16, 1, true, 1>(p, a, s);
+  return s.nt == 2 ? launch_t<D, BF16, 2, false, 1>(p, a, s) : launch_t<D, BF16, 1, false, 1>(p, a, s);
 }
 
 }  // namespace

@@ -1,7 +1,7 @@
 """Python binding of the operators around a paged cache: norms and rotation of
-queries and keys with their backward, append, read-back and one-query decode,
-for caches held in 16 bits and in 4.  The definitions are those of
-include/gbattn.h.
+queries and keys with their backward, append, read-back, one-query decode and
+the attention of chunks of new tokens, for caches held in 16 bits and in 4.  The
+definitions are those of include/gbattn.h.
 
 As in binding.py, only arguments are marshalled here: checks of tensor metadata
 (TypeError, ValueError), outputs from PyTorch's allocator, the C ABI call

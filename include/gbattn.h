@@ -642,14 +642,13 @@ size_t attn_fwd_paged_workspace_bytes(int B, int H, int Hkv, int S, int d, int m
  * Scores and their sums are fp32; exp(score - maximum) is rounded to dtype for the
  * product with v, as in attn_fwd.
  *
- *
  * attn_fwd_paged_fp4 -- the same over a 4-bit cache (q and o in dtype, which the
  * cache does not depend on).  The factors of the sequences' tokens are finite, as
  * attn_cache_append_fp4 writes them.  exp(score - maximum) is rounded to fp16
  * (within 2^-11), and q, row by row, as by attn_decode_paged_fp4.
  *
- * Errors: GBATTN_EBADSHAPE (also H > 16384, B * S > 2^30, n_pages * Hkv > 2^31 - 2 or a scale that is not
- * finite), EHEADS, EHEADDIM, EDTYPE, EPAGE, EPOINTER, EWORKSPACE,
+ * Errors: GBATTN_EBADSHAPE (also H > 16384, B * S > 2^30, n_pages * Hkv > 2^31 - 2 or a
+ * scale that is not finite), EHEADS, EHEADDIM, EDTYPE, EPAGE, EPOINTER, EWORKSPACE,
  * EUNSUPPORTED, ELAUNCH.
  */
 int attn_fwd_paged(const void *q, const void *k_cache, const void *v_cache, const int *page_table,
