@@ -1128,7 +1128,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     };
     auto stage_free = [&]() {
       if (!staged) return;
-      if (wq == 0 && lane == 0) bulk_wait_group_read0();
+      if (wq < C::kColBlocks && lane == 0) bulk_wait_group_read0();
       group_sync();
       staged = false;
     };
@@ -1228,8 +1228,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           // A pass of its own, in a loop: as a second form of what follows, unrolled for
           // all keys, it took 7000 cycles of each CTA's first such tile, most of them on
           // instructions' way into their cache, and the other warps with it.
+          // 32 keys that all rows of the warp see stay as they are (2500 cycles of the two
+          // tiles' 2900 a key tile for all four blocks).
+          const int all_see = __reduce_min_sync(0xffffffffu, real ? lim : 0x7FFFFFFF);
 #pragma unroll 1
           for (int c = 0; c < kCols / 32; ++c) {
+            if (all_see >= k0 + c * 32 + 31 && (bad >> (2 * c) & 3u) == 0 && p.sign == 1.f) continue;
             uint32_t w[32];
             tmem_ld32(s_tmem + c * 32, w);
             tmem_wait_ld();
@@ -1513,10 +1517,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             fence_proxy_async_smem();
             group_sync();
             if (!ok) break;
-            if (wq == 0 && lane == 0) {
-              for (int cb = 0; cb < C::kColBlocks; ++cb)
-                tma_store_5d(&p.to, sP + x * C::kStageBytes + cb * C::kBlockBytes, cb * 64, first_head(p, seg.u),
-                             kv_head(p, seg.u), tile.t0, seg.b);
+            // (issuing one takes some 700 cycles: a warp each)
+            if (wq < C::kColBlocks && lane == 0) {
+              tma_store_5d(&p.to, sP + x * C::kStageBytes + wq * C::kBlockBytes, wq * 64, first_head(p, seg.u),
+                           kv_head(p, seg.u), tile.t0, seg.b);
               bulk_commit_group();
             }
             staged = true;
@@ -1560,7 +1564,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       tiles += seg.j1 - seg.j0;
       ++segs;
     }
-    if (staged && wq == 0 && lane == 0) bulk_wait_group_read0();
+    if (staged && wq < C::kColBlocks && lane == 0) bulk_wait_group_read0();
     if (COPIES == 1 && p.cluster > 0) {
       if (segs == 0) {  // no tile for this CTA
         if (NT == 1) bars->state[row] = -INFINITY;
