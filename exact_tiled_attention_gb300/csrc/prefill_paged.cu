@@ -54,14 +54,15 @@
 //
 // Measured (us among other calls; 32 query heads on 8, d = 128, pages of 64; floor in
 // brackets from the copy rate and the dense bf16 rate):
-//   bound by the tensor pipe and the softmax's chain: 4096 tokens of 32768 1400 (1065,
-//   1475 TFLOP/s), 2048 tokens of 4 sequences of up to 16384 732 (562), over 4 bits 855;
+//   bound by the tensor pipe and the softmax's chain: 4096 tokens of 32768 1390 (1065,
+//   1480 TFLOP/s), 2048 tokens of 4 sequences of up to 16384 724 (562), over 4 bits 835;
 //   by HBM: 5 tokens of 64 sequences of 1024 to 32768 600 (653 at the rate of a copy;
 //   reads alone go faster, 7.4 TB/s); over 4 bits 422 (184) by the chains of products
 //   into one accumulator, about 100 cycles each whatever their size, 16 a key tile;
 //   by latency: 16 tokens of one sequence of 1000 10.8 (0.6).
 #include <cuda_runtime.h>
 
+#include <cstring>
 #include <type_traits>
 
 #include "gbattn_internal.h"
@@ -214,6 +215,7 @@ struct __align__(8) Barriers {
   float state[kBM];        // of the rows, with clusters: log2 of the sum of weights
   uint32_t tmem_base;
   int abort_flag;
+  uint32_t walk[8][24];    // each softmax warp's cursor and segment while it goes over the keys
   uint8_t bad[2][kTileRing];       // 16-key blocks of a tile (of K, of V) that have no page
   uint8_t nan_any[kSegRing];
   uint8_t nan_from[kSegRing][128]; // column's first non-finite key behind the first row's last key, - 1
@@ -1140,209 +1142,250 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       for (int i = 0; i < C::kSBufs * kBN / 64; ++i) tmem_st32(p_place + i * 32, zero);
       tmem_wait_st();
     }
-    while (ok && cur.next(p, seg)) {
-      const TileRows tile(p, seg, x, NT);
-      const int t = tile.t0 + row_token;
-      const int head = first_head(p, seg.u) + row_head;  // of the KV head's query heads
-      const bool in_tile = row_token < p.tq_tokens && head < p.g;
-      const bool real = in_tile && t < seg.s.rows && seg.s.p0 + t >= 0;
-      const int lim = real ? limit(p, seg.s, t) : -1;
-      if constexpr (FP4) {
-        const int kvh = kv_head(p, seg.u);
-        lam = fmaxf(p.scale_log2 * (p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f), kLeastScale);
-        vd = p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
-      }
-      if constexpr (kReadyQ) {
-        // The row of Q, in place, to fp16 behind a power of two that brings its largest
-        // element to [1, 2): exact but for elements below 2^-14 of that one.
-        ok = bounded_wait(&bars->q_full, segs & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        uint8_t* q_row = sQ + x * C::kQBytes + row * 128;
-        auto piece = [&](int i) {
-          return reinterpret_cast<uint4*>(q_row + (i / 8) * C::kBlockBytes + ((i ^ row) & 7) * 16);
-        };
-        uint32_t top = 0;
+    // The walk's state waits in shared memory: the softmax of 128 keys wants its registers
+    // (chunks of 4 sequences over 4 bits 858 -> 835 us, 16 bits 727 -> 724; with copies, of
+    // fewer keys a thread, it stays in registers: 5 tokens of 64 sequences 423, not 432).
+    constexpr bool kParked = COPIES == 1;
+    static_assert(sizeof(Cursor<NT>) <= 48 && sizeof(Seg) <= 48, "walk");
+    volatile uint32_t* const walk = bars->walk[warp];
+    auto put = [&](int at, const auto& v) {
+      uint32_t w[sizeof(v) / 4];
+      memcpy(w, &v, sizeof(v));
+      __syncwarp();
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 v = *piece(i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int i = 0; i < static_cast<int>(sizeof(v) / 4); ++i) walk[at + i] = w[i];
+      __syncwarp();
+    };
+    auto get = [&](int at, auto& v) {
+      uint32_t w[sizeof(v) / 4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7F80u, w[k] >> 16 & 0x7F80u));
-        }
-        const uint32_t e = min(max(top >> 7, 1u), 253u);
-        const float down = __uint_as_float((254u - e) << 23);
-        lam = fmaxf(lam * __uint_as_float(e << 23), kLeastScale);
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 v = *piece(i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t h[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            h[k] = pack2<false>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-          *piece(i) = make_uint4(h[0], h[1], h[2], h[3]);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&bars->q_ready[x]);
+      for (int i = 0; i < static_cast<int>(sizeof(v) / 4); ++i) w[i] = walk[at + i];
+      memcpy(&v, w, sizeof(v));
+    };
+    if constexpr (kParked) put(0, cur);
+    while (ok) {
+      if constexpr (!kParked) {
+        if (!cur.next(p, seg)) break;
+      } else {
+        Cursor<NT> at;
+        get(0, at);
+        if (!at.next(p, seg)) break;
+        put(0, at);
+        put(12, seg);
       }
       float r = -INFINITY;  // retained reference, raw score units
       float l = 0.f;
-      const int nx = tile.j1 - seg.j0;
-      const bool active = __any_sync(0xffffffffu, real);
-      for (int j = 0; j < nx; ++j, ++done) {
-        if (!active) {  // no row of this warp counts: P stays as it is
+      bool real;
+      int lim;
+      {
+        const TileRows tile(p, seg, x, NT);
+        const int t = tile.t0 + row_token;
+        const int head = first_head(p, seg.u) + row_head;  // of the KV head's query heads
+        const bool in_tile = row_token < p.tq_tokens && head < p.g;
+        real = in_tile && t < seg.s.rows && seg.s.p0 + t >= 0;
+        lim = real ? limit(p, seg.s, t) : -1;
+        if constexpr (FP4) {
+          const int kvh = kv_head(p, seg.u);
+          lam = fmaxf(p.scale_log2 * (p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f), kLeastScale);
+          vd = p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
+        }
+        if constexpr (kReadyQ) {
+          // The row of Q, in place, to fp16 behind a power of two that brings its largest
+          // element to [1, 2): exact but for elements below 2^-14 of that one.
+          ok = bounded_wait(&bars->q_full, segs & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          uint8_t* q_row = sQ + x * C::kQBytes + row * 128;
+          auto piece = [&](int i) {
+            return reinterpret_cast<uint4*>(q_row + (i / 8) * C::kBlockBytes + ((i ^ row) & 7) * 16);
+          };
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = *piece(i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7F80u, w[k] >> 16 & 0x7F80u));
+          }
+          const uint32_t e = min(max(top >> 7, 1u), 253u);
+          const float down = __uint_as_float((254u - e) << 23);
+          lam = fmaxf(lam * __uint_as_float(e << 23), kLeastScale);
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = *piece(i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[k] = pack2<false>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+            *piece(i) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&bars->q_ready[x]);
+        }
+        const int nx = tile.j1 - seg.j0;
+        const bool active = __any_sync(0xffffffffu, real);
+        for (int j = 0; j < nx; ++j, ++done) {
+          if (!active) {  // no row of this warp counts: P stays as it is
+            ok = bounded_wait(&bars->s_full[C::s_bar(x, done)], (done / C::kSBufs) & 1, abort_flag, p.status,
+                              kStatusTimeoutSoftmax);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive(&bars->s_free[C::s_bar(x, done)]);
+            if (NT == 2 && x == 0 && segs == 0 && j == 0) mbar_arrive(&bars->stagger);
+            if (j >= C::kSBufs) {
+              wait_pv(done - C::kSBufs);
+            } else if constexpr (!C::kPInTmem) {
+              stage_free();
+            }
+            if (!ok) break;
+            mbar_arrive(&bars->p_full[C::s_bar(x, done)]);
+            continue;
+          }
+          const uint32_t s_tmem = tmem + lane_off + C::kSCol + C::s_bar(x, done) * kBN + col0;
           ok = bounded_wait(&bars->s_full[C::s_bar(x, done)], (done / C::kSBufs) & 1, abort_flag, p.status,
                             kStatusTimeoutSoftmax);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
+          tc_fence_after();
+          constexpr int kCols = C::kCols;
+          constexpr int kBlk = kCols < kPBlock ? kCols : kPBlock;  // keys whose weights are stored together
+          const int k0 = (seg.j0 + j) * kBN + col0;
+          const uint32_t bad = bars->bad[0][(tiles + j) % kTileRing] >> (col0 / 16);
+          const bool masked = k0 + kCols - 1 > tile.lim_min || bad != 0 || p.sign != 1.f;
+          if (masked) {
+            // A pass of its own, in a loop: as a second form of what follows, unrolled for
+            // all keys, it took 7000 cycles of each CTA's first such tile, most of them on
+            // instructions' way into their cache, and the other warps with it.
+            // 32 keys that all rows of the warp see stay as they are (2500 cycles of the two
+            // tiles' 2900 a key tile for all four blocks).
+            const int all_see = __reduce_min_sync(0xffffffffu, real ? lim : 0x7FFFFFFF);
+#pragma unroll 1
+            for (int c = 0; c < kCols / 32; ++c) {
+              if (all_see >= k0 + c * 32 + 31 && (bad >> (2 * c) & 3u) == 0 && p.sign == 1.f) continue;
+              uint32_t w[32];
+              tmem_ld32(s_tmem + c * 32, w);
+              tmem_wait_ld();
+              reg_fence32(w);
+              const int last = lim - (k0 + c * 32);
+              const uint32_t gone = bad >> (2 * c);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                w[i] = i <= last && !(gone >> (i / 16) & 1u) ? __float_as_uint(__uint_as_float(w[i]) * p.sign) : 0xFF800000u;
+              tmem_st32(s_tmem + c * 32, w);
+            }
+            tmem_wait_st();
+          }
+          uint32_t u[kCols];
+          float mq[kCols / 32];
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c)
+            tmem_ld32_max(s_tmem + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]), mq[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
+          tc_fence_before();
           mbar_arrive(&bars->s_free[C::s_bar(x, done)]);
           if (NT == 2 && x == 0 && segs == 0 && j == 0) mbar_arrive(&bars->stagger);
-          if (j >= C::kSBufs) {
-            wait_pv(done - C::kSBufs);
-          } else if constexpr (!C::kPInTmem) {
-            stage_free();
-          }
-          if (!ok) break;
-          mbar_arrive(&bars->p_full[C::s_bar(x, done)]);
-          continue;
-        }
-        const uint32_t s_tmem = tmem + lane_off + C::kSCol + C::s_bar(x, done) * kBN + col0;
-        ok = bounded_wait(&bars->s_full[C::s_bar(x, done)], (done / C::kSBufs) & 1, abort_flag, p.status,
-                          kStatusTimeoutSoftmax);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        constexpr int kCols = C::kCols;
-        constexpr int kBlk = kCols < kPBlock ? kCols : kPBlock;  // keys whose weights are stored together
-        const int k0 = (seg.j0 + j) * kBN + col0;
-        const uint32_t bad = bars->bad[0][(tiles + j) % kTileRing] >> (col0 / 16);
-        const bool masked = k0 + kCols - 1 > tile.lim_min || bad != 0 || p.sign != 1.f;
-        if (masked) {
-          // A pass of its own, in a loop: as a second form of what follows, unrolled for
-          // all keys, it took 7000 cycles of each CTA's first such tile, most of them on
-          // instructions' way into their cache, and the other warps with it.
-          // 32 keys that all rows of the warp see stay as they are (2500 cycles of the two
-          // tiles' 2900 a key tile for all four blocks).
-          const int all_see = __reduce_min_sync(0xffffffffu, real ? lim : 0x7FFFFFFF);
-#pragma unroll 1
-          for (int c = 0; c < kCols / 32; ++c) {
-            if (all_see >= k0 + c * 32 + 31 && (bad >> (2 * c) & 3u) == 0 && p.sign == 1.f) continue;
-            uint32_t w[32];
-            tmem_ld32(s_tmem + c * 32, w);
-            tmem_wait_ld();
-            reg_fence32(w);
-            const int last = lim - (k0 + c * 32);
-            const uint32_t gone = bad >> (2 * c);
+          float* s = reinterpret_cast<float*>(u);
+          float mx = mq[0];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              w[i] = i <= last && !(gone >> (i / 16) & 1u) ? __float_as_uint(__uint_as_float(w[i]) * p.sign) : 0xFF800000u;
-            tmem_st32(s_tmem + c * 32, w);
-          }
-          tmem_wait_st();
-        }
-        uint32_t u[kCols];
-        float mq[kCols / 32];
-#pragma unroll
-        for (int c = 0; c < kCols / 32; ++c)
-          tmem_ld32_max(s_tmem + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]), mq[c]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
-        tc_fence_before();
-        mbar_arrive(&bars->s_free[C::s_bar(x, done)]);
-        if (NT == 2 && x == 0 && segs == 0 && j == 0) mbar_arrive(&bars->stagger);
-        float* s = reinterpret_cast<float*>(u);
-        float mx = mq[0];
-#pragma unroll
-        for (int c = 1; c < kCols / 32; ++c) mx = fmaxf(mx, mq[c]);
-        float gamma = 1.f;
-        if (j == 0) {
-          r = mx;
-        } else {
-          const float cand = fmaxf(r, mx);
-          if ((cand - r) * lam > kRescaleThreshold) {  // false when both are -inf
-            gamma = ex2_approx((r - cand) * lam);
-            r = cand;
-          }
-        }
-        l *= gamma;
-        const float rs = (r == -INFINITY) ? 0.f : r * lam;
-        const float2 lam2 = make_float2(lam, lam);
-        const float2 nrs2 = make_float2(-rs, -rs);
-        float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int blk = 0; blk < kCols / kBlk; ++blk) {
-          uint32_t pk[kBlk / 2];
-#pragma unroll
-          for (int c8 = 0; c8 < kBlk / 8; ++c8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = blk * kBlk + c8 * 8 + 2 * i;
-              const float2 e = ex2_pair(ffma2(make_float2(s[c], s[c + 1]), lam2, nrs2), c / 2);
-              sum4[i] = fadd2(sum4[i], e);
-              pk[c8 * 4 + i] = pack2<kMmaBf16>(e.x, e.y);
+          for (int c = 1; c < kCols / 32; ++c) mx = fmaxf(mx, mq[c]);
+          float gamma = 1.f;
+          if (j == 0) {
+            r = mx;
+          } else {
+            const float cand = fmaxf(r, mx);
+            if ((cand - r) * lam > kRescaleThreshold) {  // false when both are -inf
+              gamma = ex2_approx((r - cand) * lam);
+              r = cand;
             }
           }
-          if (blk == 0) {
-            // The last tile that had P in this place, or, before O can be corrected, the
-            // tile before this one is through.
-            const bool correct = j > 0 && __any_sync(0xffffffffu, gamma != 1.f);
-            if (j >= C::kSBufs || correct) {
-              if (j >= C::kSBufs) wait_pv(done - C::kSBufs);
-              if (C::kSBufs > 1 && ok && correct) wait_pv(done - 1);
-              if (!ok) break;
-              tc_fence_after();
-              if (correct) {
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                  uint32_t w32[32];
-                  tmem_ld32(o_tmem + c * 32, w32);
-                  tmem_wait_ld();
-                  reg_fence32(w32);
+          l *= gamma;
+          const float rs = (r == -INFINITY) ? 0.f : r * lam;
+          const float2 lam2 = make_float2(lam, lam);
+          const float2 nrs2 = make_float2(-rs, -rs);
+          float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) w32[i] = __float_as_uint(__uint_as_float(w32[i]) * gamma);
-                  tmem_st32(o_tmem + c * 32, w32);
+          for (int blk = 0; blk < kCols / kBlk; ++blk) {
+            uint32_t pk[kBlk / 2];
+#pragma unroll
+            for (int c8 = 0; c8 < kBlk / 8; ++c8) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int c = blk * kBlk + c8 * 8 + 2 * i;
+                const float2 e = ex2_pair(ffma2(make_float2(s[c], s[c + 1]), lam2, nrs2), c / 2);
+                sum4[i] = fadd2(sum4[i], e);
+                pk[c8 * 4 + i] = pack2<kMmaBf16>(e.x, e.y);
+              }
+            }
+            if (blk == 0) {
+              // The last tile that had P in this place, or, before O can be corrected, the
+              // tile before this one is through.
+              const bool correct = j > 0 && __any_sync(0xffffffffu, gamma != 1.f);
+              if (j >= C::kSBufs || correct) {
+                if (j >= C::kSBufs) wait_pv(done - C::kSBufs);
+                if (C::kSBufs > 1 && ok && correct) wait_pv(done - 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (correct) {
+#pragma unroll 1
+                  for (int c = 0; c < D / 32; ++c) {
+                    uint32_t w32[32];
+                    tmem_ld32(o_tmem + c * 32, w32);
+                    tmem_wait_ld();
+                    reg_fence32(w32);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) w32[i] = __float_as_uint(__uint_as_float(w32[i]) * gamma);
+                    tmem_st32(o_tmem + c * 32, w32);
+                  }
+                  tmem_wait_st();
                 }
-                tmem_wait_st();
+              }
+              if constexpr (!C::kPInTmem) {
+                if (j == 0) stage_free();
+                if (!ok) break;
               }
             }
             if constexpr (!C::kPInTmem) {
-              if (j == 0) stage_free();
-              if (!ok) break;
-            }
-          }
-          if constexpr (!C::kPInTmem) {
 #pragma unroll
-            for (int c8 = 0; c8 < kBlk / 8; ++c8) {
-              const int chunk = (blk * kBlk / 8 + c8) % 8;
-              *reinterpret_cast<uint4*>(p_row + blk * kBlk / 64 * C::kBlockBytes + ((chunk ^ (row & 7)) << 4)) =
-                  make_uint4(pk[c8 * 4], pk[c8 * 4 + 1], pk[c8 * 4 + 2], pk[c8 * 4 + 3]);
+              for (int c8 = 0; c8 < kBlk / 8; ++c8) {
+                const int chunk = (blk * kBlk / 8 + c8) % 8;
+                *reinterpret_cast<uint4*>(p_row + blk * kBlk / 64 * C::kBlockBytes + ((chunk ^ (row & 7)) << 4)) =
+                    make_uint4(pk[c8 * 4], pk[c8 * 4 + 1], pk[c8 * 4 + 2], pk[c8 * 4 + 3]);
+              }
+            } else if constexpr (kBlk == 32) {
+              tmem_st16(p_place + C::s_bar(x, done) * (kBN / 2) + col0 / 2 + blk * 16, pk);
+            } else {
+              tmem_st32(p_place + C::s_bar(x, done) * (kBN / 2) + col0 / 2 + blk * 32, pk);
             }
-          } else if constexpr (kBlk == 32) {
-            tmem_st16(p_place + C::s_bar(x, done) * (kBN / 2) + col0 / 2 + blk * 16, pk);
-          } else {
-            tmem_st32(p_place + C::s_bar(x, done) * (kBN / 2) + col0 / 2 + blk * 32, pk);
           }
+          if (!ok) break;
+          const float2 s01 = fadd2(fadd2(sum4[0], sum4[1]), fadd2(sum4[2], sum4[3]));
+          l += s01.x + s01.y;
+          if constexpr (C::kPInTmem) {
+            tmem_wait_st();
+          } else {
+            fence_proxy_async_smem();
+          }
+          tc_fence_before();
+          mbar_arrive(&bars->p_full[C::s_bar(x, done)]);
         }
         if (!ok) break;
-        const float2 s01 = fadd2(fadd2(sum4[0], sum4[1]), fadd2(sum4[2], sum4[3]));
-        l += s01.x + s01.y;
-        if constexpr (C::kPInTmem) {
-          tmem_wait_st();
-        } else {
-          fence_proxy_async_smem();
-        }
-        tc_fence_before();
-        mbar_arrive(&bars->p_full[C::s_bar(x, done)]);
       }
       if (!ok) break;
+      if constexpr (kParked) get(12, seg);
+      const TileRows tile(p, seg, x, NT);
+      const int t = tile.t0 + row_token;
+      const int head = first_head(p, seg.u) + row_head;
+      const bool in_tile = row_token < p.tq_tokens && head < p.g;
+      const int nx = tile.j1 - seg.j0;
       // ---- the segment's end
       if (nx > 0) {
         ok = bounded_wait(&bars->o_full[x], segs_x & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
