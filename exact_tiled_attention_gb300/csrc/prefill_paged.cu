@@ -75,7 +75,8 @@ constexpr int kBM = 128;          // rows of a tile (= TMEM lanes)
 constexpr int kBN = 128;          // keys of a tile
 constexpr int kMaxCtas = 160;     // bound of the grid, for the workspace's size
 constexpr float kRescaleThreshold = 8.f;  // base-2 units
-constexpr int kPBlock = 64;
+constexpr int kPBlock = 64;        // keys whose weights are stored together
+constexpr int kBarBytes = 3 << 10;  // of Barriers
 // A scale of scores is at least this, so that -inf times it stays -inf: FLT_MIN.  (Scores
 // that a smaller scale makes would differ from 0 only if q.k passed 1e36.)
 constexpr float kLeastScale = 1.1754944e-38f;
@@ -141,7 +142,7 @@ struct Cfg {
   static constexpr int kRingOff = kPOff + NT * kStageBytes;
   static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
   static constexpr int kBarOff = kRawOff + kRawStages * kRawBytes;
-  static constexpr int kSmemBytes = kBarOff + 3072;
+  static constexpr int kSmemBytes = kBarOff + kBarBytes;
   static constexpr int kMmaWarp = 4 * NT;  // tile x's issuer is warp kMmaWarp + x
   static constexpr int kLoadWarp = 4 * NT + 2;
   static constexpr int kGuardWarp = 4 * NT + 3;
@@ -220,7 +221,7 @@ struct __align__(8) Barriers {
   uint8_t nan_any[kSegRing];
   uint8_t nan_from[kSegRing][128]; // column's first non-finite key behind the first row's last key, - 1
 };
-static_assert(sizeof(Barriers) <= 3072, "barriers fit");
+static_assert(sizeof(Barriers) <= kBarBytes, "barriers fit");
 
 __device__ __forceinline__ Seq load_seq(const Params& p, int b) {
   Seq s;
@@ -800,7 +801,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         const uint32_t bytes = static_cast<uint32_t>(row_bytes << box_shift);
         const uint8_t* const pool = cb == 0 ? p.codes[loads_v] : p.factors[loads_v];
         uint8_t* const dst = smem + C::kRawOff + (cb == 0 ? 0 : kBN * (D / 2)) + box * bytes;
-        const int first = loads_v ? C::kRawKStages : 0, places = loads_v ? C::kRawStages - C::kRawKStages : C::kRawKStages;
+        const int first = loads_v ? C::kRawKStages : 0;
+        const int places = loads_v ? C::kRawStages - C::kRawKStages : C::kRawKStages;
         int st = first, round = 0, filled = 0;
         while (ok && cur.next(p, seg)) {
           const int kvh = kv_head(p, seg.u);
@@ -823,7 +825,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             note_missing(loads_v, tile, __ballot_sync(0xffffffffu, cb == 0 && inside && !found));
             const uint8_t* src =
                 pool + (((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) + (key & in_page)) * row_bytes;
-            if (round > 0) ok = bounded_wait(&bars->raw_empty[st], (round & 1) ^ 1, abort_flag, p.status, kStatusTimeoutLoad);
+            if (round > 0)
+              ok = bounded_wait(&bars->raw_empty[st], (round & 1) ^ 1, abort_flag, p.status, kStatusTimeoutLoad);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&bars->raw[st], (__popc(copied) << box_shift) * (D / 2 + D / 16));
@@ -862,7 +865,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             const bool inside = key < seg.s.n;
             const bool found = inside && page >= 0 && page < p.n_pages;
             if (!is_v) note_missing(false, tile++, __ballot_sync(0xffffffffu, cb == 0 && inside && !found));
-            if (round > 0) ok = bounded_wait(&bars->kv_empty[st], (round & 1u) ^ 1u, abort_flag, p.status, kStatusTimeoutLoad);
+            if (round > 0)
+              ok = bounded_wait(&bars->kv_empty[st], (round & 1u) ^ 1u, abort_flag, p.status, kStatusTimeoutLoad);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             uint64_t* bar = is_v && j >= jm ? &bars->raw[st] : &bars->kv_full[st];
@@ -1093,7 +1097,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         // Every MMA this thread issued must complete before TMEM is released.
         mma_commit(&bars->mma_done[warp - C::kMmaWarp]);
         int dummy = 0;
-        bounded_wait(&bars->mma_done[warp - C::kMmaWarp], 0, reinterpret_cast<volatile int*>(&dummy), p.status, kStatusTimeoutDrain);
+        bounded_wait(&bars->mma_done[warp - C::kMmaWarp], 0, reinterpret_cast<volatile int*>(&dummy), p.status,
+                     kStatusTimeoutDrain);
       }
       __syncwarp();
     }
@@ -1112,7 +1117,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
     const uint32_t p_place = tmem + lane_off + C::kPCol;
     // P.V of the tile that is number d of this row tile's is through.
     auto wait_pv = [&](int d) {
-      ok = bounded_wait(&bars->p_free[C::s_bar(x, d)], (d / C::kSBufs) & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
+      ok = bounded_wait(&bars->p_free[C::s_bar(x, d)], (d / C::kSBufs) & 1, abort_flag, p.status,
+                        kStatusTimeoutSoftmax);
       ok = __all_sync(0xffffffffu, ok);
     };
     uint8_t* p_row = sP + x * C::kStageBytes + row * 128;
@@ -1263,8 +1269,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             // A pass of its own, in a loop: as a second form of what follows, unrolled for
             // all keys, it took 7000 cycles of each CTA's first such tile, most of them on
             // instructions' way into their cache, and the other warps with it.
-            // 32 keys that all rows of the warp see stay as they are (2500 cycles of the two
-            // tiles' 2900 a key tile for all four blocks).
+            // 32 keys that all rows of the warp see stay as they are: all four blocks take
+            // 2500 cycles, where a key tile takes 2900.
             const int all_see = __reduce_min_sync(0xffffffffu, real ? lim : 0x7FFFFFFF);
 #pragma unroll 1
             for (int c = 0; c < kCols / 32; ++c) {
@@ -1277,7 +1283,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
               const uint32_t gone = bad >> (2 * c);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                w[i] = i <= last && !(gone >> (i / 16) & 1u) ? __float_as_uint(__uint_as_float(w[i]) * p.sign) : 0xFF800000u;
+                w[i] = i <= last && !(gone >> (i / 16) & 1u) ? __float_as_uint(__uint_as_float(w[i]) * p.sign)
+                                                             : 0xFF800000u;
               tmem_st32(s_tmem + c * 32, w);
             }
             tmem_wait_st();
@@ -1478,7 +1485,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
                                   pack2<BF16>(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv),
                                   pack2<BF16>(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
           } else {
-            float4* dst = reinterpret_cast<float4*>(p.part_o) + (part * (D / 4) + c * 8 + copy * (kPer / 4)) * kBM + crow;
+            float4* dst =
+                reinterpret_cast<float4*>(p.part_o) + (part * (D / 4) + c * 8 + copy * (kPer / 4)) * kBM + crow;
 #pragma unroll
             for (int i = 0; i < kPer / 4; ++i)
               dst[i * kBM] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
@@ -1517,7 +1525,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       } else if (seg.whole()) {
         [[maybe_unused]] long long store_row = -1;
         if constexpr (C::kDirectO) {
-          if (in_tile && t < p.S) store_row = (static_cast<long long>(seg.b) * p.H + kv_head(p, seg.u) * p.g + head) * p.S + t;
+          if (in_tile && t < p.S)
+            store_row = (static_cast<long long>(seg.b) * p.H + kv_head(p, seg.u) * p.g + head) * p.S + t;
         }
         if (tile.t0 < p.S) {
           const float inv = (!real || l == 0.f) ? 0.f : vd / l;
@@ -1734,7 +1743,8 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_paged_merge_kernel(cons
     uint32_t out[kSlice / 2];
 #pragma unroll
     for (int e = 0; e < kSlice; e += 2)
-      out[e / 2] = p.out_bf16 ? pack2<true>(acc[e] * inv, acc[e + 1] * inv) : pack2<false>(acc[e] * inv, acc[e + 1] * inv);
+      out[e / 2] =
+          p.out_bf16 ? pack2<true>(acc[e] * inv, acc[e + 1] * inv) : pack2<false>(acc[e] * inv, acc[e + 1] * inv);
     const long long hrow = (static_cast<long long>(b) * p.H + kv_head(p, u) * p.g + head) * p.S + t;
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + hrow * D + slice * kSlice);
     dst[0] = make_uint4(out[0], out[1], out[2], out[3]);

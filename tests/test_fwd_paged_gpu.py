@@ -117,6 +117,20 @@ def test_runs_of_several_units(cfg, bits):
         assert _same_bits(again[0], o) and torch.equal(again[1], lse)
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+def test_units_of_one_row_tile_in_runs(bits):
+    """More units of one row tile than clusters take, and so many key tiles that they are
+    cut into runs: 104 units of 33 to 36 tiles."""
+    lens, S, d = [4500], 400, 64
+    pool, table, g = _make(bits, torch.bfloat16, 8, d, 64, lens, 42)
+    q = torch.randn(1, 32, S, d, generator=g).bfloat16().cuda()
+    o, lse = _forward(pool, q, table, lens, None)
+    assert gb.gbattn_device_status() == 0
+    _ok(pool, q, table, lens, [S], o, lse, True, 1 / math.sqrt(d))
+    again = _forward(pool, q, table, lens, None)
+    assert _same_bits(again[0], o) and torch.equal(again[1], lse)
+
+
 @pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("S", [1, 30, 90])
 @pytest.mark.parametrize("bits", [16, 4])
