@@ -66,6 +66,7 @@
 #include <type_traits>
 
 #include "gbattn_internal.h"
+#include "gbattn_parts.h"
 #include "gbattn_ptx.cuh"
 
 namespace gbattn {
@@ -1681,7 +1682,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_paged_merge_kernel(cons
     int2 part = make_int2(0, 0);
     if (tiles_of(p, s, k * tu, (k + 1) * tu) > 0) {
       part = said;
-      if (part.y <= 1) continue;  // finished by one CTA
+      if (!split_parts(part.x, part.y, p.ctas)) continue;  // finished by one CTA, or by none
     }
     const int row_token = token_of(p, row);
     const int t = k * tu + x * p.tq_tokens + row_token, head = first_head(p, u) + row - row_token * p.hb;
