@@ -81,7 +81,7 @@ constexpr int kBarBytes = 3 << 10;  // of Barriers
 // A scale of scores is at least this, so that -inf times it stays -inf: FLT_MIN.  (Scores
 // that a smaller scale makes would differ from 0 only if q.k passed 1e36.)
 constexpr float kLeastScale = 1.1754944e-38f;
-constexpr int kSegRing = 4;       // segments whose notes of the guard are kept: it is at most 3 ahead
+constexpr int kSegRing = 4;       // segments whose notes of the guard are kept
 // Key tiles that the states of split units cost (writing, and a second kernel that has
 // to fold them) for units of one and two row tiles.  Whole units and runs, us in a
 // captured graph: 2000 tokens of one prompt from its start 67, 77; 3 of 40 sequences of
@@ -218,6 +218,7 @@ struct __align__(8) Barriers {
   uint32_t tmem_base;
   int abort_flag;
   uint32_t walk[8][24];    // each softmax warp's cursor and segment while it goes over the keys
+  uint32_t notes_read[8];  // segments whose notes each softmax warp is through with
   uint8_t bad[2][kTileRing];       // 16-key blocks of a tile (of K, of V) that have no page
   uint8_t nan_any[kSegRing];
   uint8_t nan_from[kSegRing][128]; // column's first non-finite key behind the first row's last key, - 1
@@ -506,6 +507,42 @@ __device__ __forceinline__ uint8_t* state_row(uint8_t* smem, int row, int c4) {
   return smem + (c4 < kHalf ? C::kQOff : C::kPOff) + row * (kHalf * 16);
 }
 
+// The guard's notes: each softmax warp counts the segments whose notes it is through
+// with, and before the guard writes those of segment number `seg` it waits, like
+// bounded_wait, until all WARPS of them have read what its place held.  (What visits a
+// segment's keys does not bound the guard for every warp: a row tile without any in
+// several segments gives their keys and Q back at once, whatever its warps still do.)
+__device__ __forceinline__ void notes_done(Barriers* bars, int warp, int lane, uint32_t segs) {
+  __syncwarp();
+  if (lane == 0)
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(&bars->notes_read[warp])), "r"(segs) : "memory");
+}
+template <int WARPS>
+__device__ __forceinline__ bool notes_free(Barriers* bars, int lane, int seg, int* status) {
+  if (seg < kSegRing) return true;
+  const uint32_t least = seg - kSegRing + 1;
+  volatile int* abort_flag = &bars->abort_flag;
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t read = least;
+    if (lane < WARPS)
+      asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(read) : "r"(smem_u32(&bars->notes_read[lane])) : "memory");
+    if (__all_sync(0xffffffffu, read >= least)) break;
+    if ((it & 15u) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (it == 0) t0 = now;
+      const bool late = now - t0 > kWaitTimeoutNs;
+      if (late) {
+        *abort_flag = 1;
+        atomicCAS(status, 0, kStatusTimeoutMma);
+      }
+      if (__any_sync(0xffffffffu, late || *abort_flag != 0)) return false;
+    }
+  }
+  __syncwarp();
+  return true;
+}
+
 __device__ __forceinline__ float ld_cluster(uint32_t a) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
@@ -619,6 +656,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       mbar_init(&bars->group[x], kBM);
     }
     mbar_init(&bars->stagger, kBM);
+    for (int w = 0; w < 4 * NT; ++w) bars->notes_read[w] = 0;
     bars->abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&p.tq);
@@ -923,6 +961,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         uint32_t first[kCols];
 #pragma unroll
         for (int c = 0; c < kCols; ++c) first[c] = 255u;
+        if (jm < seg.j1 && !notes_free<4 * NT>(bars, lane, segs, p.status)) break;
         for (int j = jm; j < seg.j1; ++j) {
           const int st = C::kOneRing
                              ? (items + item_of_v(j - seg.j0, n)) % C::kStages
@@ -1424,6 +1463,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         }
         tmem_wait_st();
       }
+      if constexpr (!FP4) notes_done(bars, warp, lane, segs + 1);
       if constexpr (COPIES > 1) {
         // Fold the copies: their references and sums, then O, 32 columns at a time; a
         // thread sums its row's part of the columns.

@@ -189,6 +189,37 @@ def test_values_that_are_not_finite(dtype, H, Hkv, d, S, L, value):
         assert torch.equal(lse[1, :, :t0], clean[1][1, :, :t0])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_notes_of_many_short_segments(d):
+    """Units of two row tiles of which the second is empty in all but a few: many
+    segments for each CTA, where only one of the row tiles' warps meets the keys.  A NaN
+    in v of one token of each sequence, another element each, and in every slot behind
+    it."""
+    page, Hkv, S, B = 64, 4, 200, 300
+    g = torch.Generator().manual_seed(43)
+    news = [int(m) for m in torch.randint(1, 129, (B,), generator=g)]
+    for b in range(0, B, 7):
+        news[b] = 129 + b % 72  # the second row tile has rows
+    lens = [m + int(n) for m, n in zip(news, torch.randint(0, 120, (B,), generator=g))]
+    pool, table, g = _make(16, torch.bfloat16, Hkv, d, page, lens, 44)
+    q = torch.randn(B, Hkv, S, d, generator=g).bfloat16().cuda()
+    clean = _forward(pool, q, table, lens, news)
+    assert gb.gbattn_device_status() == 0
+    bad = torch.zeros(B, 1, S, d, dtype=torch.bool)
+    for b, (n, m) in enumerate(zip(lens, news)):
+        last = int(table[b, (n - 1) // page])
+        pool.gpu[1][last, :, (n - 1) % page + 1:] = float("nan")
+        t, e = (5 * b) % m, (11 * b) % d
+        pool.gpu[1][int(table[b, (n - m + t) // page]), :, (n - m + t) % page, e] = float("nan")
+        bad[b, 0, t:m, e] = True
+    bad = bad.cuda()
+    for _ in range(20):
+        o, lse = _forward(pool, q, table, lens, news)
+        assert gb.gbattn_device_status() == 0 and torch.equal(lse, clean[1])
+        assert torch.equal(torch.isnan(o), bad.expand_as(o))
+        assert _same_bits(o.masked_fill(bad, 0.0), clean[0].masked_fill(bad, 0.0))
+
+
 @pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("S", [1, 20, 70])
 @pytest.mark.parametrize("bits", [16, 4])
