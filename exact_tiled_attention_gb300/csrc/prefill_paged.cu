@@ -507,6 +507,12 @@ __device__ __forceinline__ uint8_t* state_row(uint8_t* smem, int row, int c4) {
   return smem + (c4 < kHalf ? C::kQOff : C::kPOff) + row * (kHalf * 16);
 }
 
+// An output from a row's sum and 1 / l: the product, but NaN where the sum is infinite.
+// A value of V that is not finite makes its elements NaN, as in the decode, not an
+// infinity or NaN by what its weight rounds to, whether the guard has noted it, or which
+// copy or part of the row met it.
+__device__ __forceinline__ float normalised(float o, float inv) { return fmaf(o, inv, o * 0.f); }
+
 // The guard's notes: each softmax warp counts the segments whose notes it is through
 // with, and before the guard writes those of segment number `seg` it waits, like
 // bounded_wait, until all WARPS of them have read what its place held.  (What visits a
@@ -606,7 +612,8 @@ __device__ __forceinline__ void fold_cluster(const Params& p, const Seg& seg, ui
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + hrow[v] * D + c4 * 4) =
-          make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+          make_uint2(pack2<BF16>(normalised(acc.x, inv), normalised(acc.y, inv)),
+                     pack2<BF16>(normalised(acc.z, inv), normalised(acc.w, inv)));
       if (c4 == 0 && p.lse != nullptr)
         p.lse[hrow[v]] = sum == 0.f ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994531f;
     }
@@ -1520,11 +1527,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + hrow * D + c * 32 + copy * kPer);
 #pragma unroll
+            for (int i = 0; i < kPer; ++i) acc[i] = normalised(acc[i], inv);
+#pragma unroll
             for (int i = 0; i < kPer / 8; ++i)
-              dst[i] = make_uint4(pack2<BF16>(acc[8 * i] * inv, acc[8 * i + 1] * inv),
-                                  pack2<BF16>(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv),
-                                  pack2<BF16>(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv),
-                                  pack2<BF16>(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
+              dst[i] = make_uint4(pack2<BF16>(acc[8 * i], acc[8 * i + 1]), pack2<BF16>(acc[8 * i + 2], acc[8 * i + 3]),
+                                  pack2<BF16>(acc[8 * i + 4], acc[8 * i + 5]),
+                                  pack2<BF16>(acc[8 * i + 6], acc[8 * i + 7]));
           } else {
             float4* dst =
                 reinterpret_cast<float4*>(p.part_o) + (part * (D / 4) + c * 8 + copy * (kPer / 4)) * kBM + crow;
@@ -1588,7 +1596,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              pk[i] = pack2<BF16>(__uint_as_float(u[2 * i]) * inv, __uint_as_float(u[2 * i + 1]) * inv);
+              pk[i] = pack2<BF16>(normalised(__uint_as_float(u[2 * i]), inv),
+                                  normalised(__uint_as_float(u[2 * i + 1]), inv));
             if constexpr (C::kDirectO) {
               if (store_row >= 0) {
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + store_row * D + c * 32);
@@ -1783,9 +1792,10 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_paged_merge_kernel(cons
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint32_t out[kSlice / 2];
 #pragma unroll
+    for (int e = 0; e < kSlice; ++e) acc[e] = normalised(acc[e], inv);
+#pragma unroll
     for (int e = 0; e < kSlice; e += 2)
-      out[e / 2] =
-          p.out_bf16 ? pack2<true>(acc[e] * inv, acc[e + 1] * inv) : pack2<false>(acc[e] * inv, acc[e + 1] * inv);
+      out[e / 2] = p.out_bf16 ? pack2<true>(acc[e], acc[e + 1]) : pack2<false>(acc[e], acc[e + 1]);
     const long long hrow = (static_cast<long long>(b) * p.H + kv_head(p, u) * p.g + head) * p.S + t;
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + hrow * D + slice * kSlice);
     dst[0] = make_uint4(out[0], out[1], out[2], out[3]);

@@ -638,7 +638,9 @@ size_t attn_fwd_paged_workspace_bytes(int B, int H, int Hkv, int S, int d, int m
  * o may not overlap an input.  The work is divided by the lengths, evenly over the
  * GPU; results repeat bitwise.  A key that a row does not see has no influence on
  * it, whatever its k and v hold.  Of the keys that it sees: a score of NaN or +inf
- * makes the row's o and lse NaN, and a NaN or an infinity in v its element of o.
+ * makes the row's o and lse NaN, and a NaN or an infinity in v, whatever its weight,
+ * makes its element of o NaN, as in attn_decode_paged (a key with a score of -inf may
+ * count as one that is not seen).
  * Scores and their sums are fp32; exp(score - maximum) is rounded to dtype for the
  * product with v, as in attn_fwd.
  *

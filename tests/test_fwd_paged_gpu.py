@@ -189,6 +189,32 @@ def test_values_that_are_not_finite(dtype, H, Hkv, d, S, L, value):
         assert torch.equal(lse[1, :, :t0], clean[1][1, :, :t0])
 
 
+@pytest.mark.usefixtures("table_width")
+@pytest.mark.parametrize("dtype,H,Hkv,d,S,L", [
+    (torch.bfloat16, 8, 2, 64, 3, 700), (torch.float16, 4, 2, 64, 12, 900), (torch.bfloat16, 4, 2, 128, 9, 900),
+    (torch.float16, 2, 2, 128, 200, 700), (torch.bfloat16, 1, 1, 64, 256, 1000), (torch.float16, 40, 8, 128, 300, 9000)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite_give_nan(dtype, H, Hkv, d, S, L, value):
+    """However the work is divided: a value in the first, a middle and the last tile
+    before the chunk and in the chunk, with a weight that counts or (a key against the
+    queries, at a scale that makes it so) one that is 0 in fp32."""
+    page = 64
+    pool, table, g = _make(16, dtype, Hkv, d, page, [L, L], 46)
+    pool.gpu[0][table[1, 1], :, 3] = -4.0
+    q = (0.5 + torch.rand(2, H, S, d, generator=g)).to(dtype).cuda()
+    clean = _forward(pool, q, table, [L, L], None, scale=1.0)
+    at = [(0, 2), (0, L // 2), (0, L - S - 1), (0, L - S), (0, L - S // 2 - 1), (1, page + 3)]
+    bad = torch.zeros(2, 1, S, d, dtype=torch.bool)
+    for i, (b, p) in enumerate(at):
+        pool.gpu[1][table[b, p // page], :, p % page, 9 * i + 1] = value
+        bad[b, :, max(0, p - (L - S)):, 9 * i + 1] = True
+    bad = bad.cuda()
+    o, lse = _forward(pool, q, table, [L, L], None, scale=1.0)
+    assert gb.gbattn_device_status() == 0
+    assert torch.equal(torch.isnan(o), bad.expand_as(o)) and torch.isfinite(lse).all()
+    assert _same_bits(o.masked_fill(bad, 0.0), clean[0].masked_fill(bad, 0.0)) and torch.equal(lse, clean[1])
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_notes_of_many_short_segments(d):
     """Units of two row tiles of which the second is empty in all but a few: many
