@@ -284,7 +284,7 @@ int prefill(const void* q, const void* k_cache, const void* k_factors, const voi
   if (B < 1 || H < 1 || Hkv < 1 || S < 1 || H > 16384 || Hkv > 16384) return GBATTN_EBADSHAPE;
   if (too_many_tokens(B, S)) return GBATTN_EBADSHAPE;
   if (H % Hkv != 0) return GBATTN_EHEADS;
-  if (!(scale >= -3e38f && scale <= 3e38f)) return GBATTN_EBADSHAPE;
+  if (!(scale >= -2.3e38f && scale <= 2.3e38f)) return GBATTN_EBADSHAPE;  // scale log2 e is an fp32 number
   PagedPrefillArgs a{};
   int rc = check_cache(&a.cache, k_cache, v_cache, k_factors, v_factors, fp4, k_descale, v_descale, page_table,
                        seqlens, Hkv, d, page_size, n_pages, max_pages);

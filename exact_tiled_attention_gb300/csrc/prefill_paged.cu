@@ -62,6 +62,7 @@
 //   by latency: 16 tokens of one sequence of 1000 10.8 (0.6).
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstring>
 #include <type_traits>
 
@@ -78,9 +79,10 @@ constexpr int kMaxCtas = 160;     // bound of the grid, for the workspace's size
 constexpr float kRescaleThreshold = 8.f;  // base-2 units
 constexpr int kPBlock = 64;        // keys whose weights are stored together
 constexpr int kBarBytes = 3 << 10;  // of Barriers
-// A scale of scores is at least this, so that -inf times it stays -inf: FLT_MIN.  (Scores
-// that a smaller scale makes would differ from 0 only if q.k passed 1e36.)
-constexpr float kLeastScale = 1.1754944e-38f;
+// A scale of scores is at least this, so that -inf times it stays -inf: fp32's smallest
+// number, 2^-149.  (Rounding a scale to a multiple of it moves no score by more than 2^-150
+// times fp32's largest, 2.4e-7.)
+constexpr float kLeastScale = 1.4012985e-45f;
 constexpr int kSegRing = 4;       // segments whose notes of the guard are kept
 // Key tiles that the states of split units cost (writing, and a second kernel that has
 // to fold them) for units of one and two row tiles.  Whole units and runs, us in a
@@ -185,7 +187,8 @@ struct Params {
   int page_shift, n_pages, max_pages, box_rows;
   int causal;
   int out_bf16;
-  float scale_log2;  // |scale| log2 e (of a scale of 0: log2 e)
+  float scale_log2;  // |scale| log2 e (of a scale of 0: log2 e), at least kLeastScale
+  double scale64;    // the same, where fp32's normal numbers do not have it in 64 bits
   float sign;        // -1 or 0 where scale is negative or 0, and scores are taken times it
   int ctas;
   int wide;          // whether tiles may count past 2^31
@@ -1237,9 +1240,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         const bool in_tile = row_token < p.tq_tokens && head < p.g;
         real = in_tile && t < seg.s.rows && seg.s.p0 + t >= 0;
         lim = real ? limit(p, seg.s, t) : -1;
+        // The scale of the scores: of three factors over 4 bits, whose product may be an
+        // fp32 number where that of two is none; in 64 bits it is rounded once.
+        [[maybe_unused]] double scale = p.scale64;
         if constexpr (FP4) {
           const int kvh = kv_head(p, seg.u);
-          lam = fmaxf(p.scale_log2 * (p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f), kLeastScale);
+          scale *= p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f;
           vd = p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
         }
         if constexpr (kReadyQ) {
@@ -1264,7 +1270,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           }
           const uint32_t e = min(max(top >> 7, 1u), 253u);
           const float down = __uint_as_float((254u - e) << 23);
-          lam = fmaxf(lam * __uint_as_float(e << 23), kLeastScale);
+          scale *= __uint_as_float(e << 23);
 #pragma unroll 4
           for (int i = 0; i < D / 8; ++i) {
             const uint4 v = *piece(i);
@@ -1277,6 +1283,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           }
           fence_proxy_async_smem();
           mbar_arrive(&bars->q_ready[x]);
+        }
+        if constexpr (FP4) {
+          lam = static_cast<float>(scale);
+          if (lam < kLeastScale) lam = kLeastScale;
         }
         const int nx = tile.j1 - seg.j0;
         const bool active = __any_sync(0xffffffffu, real);
@@ -1976,7 +1986,9 @@ int launch_prefill_paged(const PagedPrefillArgs& a) {
   p.max_pages = c.max_pages;
   p.causal = a.causal;
   p.out_bf16 = a.bf16 ? 1 : 0;
-  p.scale_log2 = (a.scale == 0.f ? 1.f : a.scale < 0.f ? -a.scale : a.scale) * 1.4426950408889634f;
+  const float scale = a.scale == 0.f ? 1.f : a.scale < 0.f ? -a.scale : a.scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale64 = p.scale_log2 < FLT_MIN ? scale * 1.4426950408889634 : p.scale_log2;
   if (p.scale_log2 < kLeastScale) p.scale_log2 = kLeastScale;
   p.sign = a.scale == 0.f ? 0.f : a.scale < 0.f ? -1.f : 1.f;
   const int most = max_ctas(s, c.max_pages << c.page_shift);

@@ -631,7 +631,7 @@ size_t attn_fwd_paged_workspace_bytes(int B, int H, int Hkv, int S, int d, int m
  *            position is negative, are padding: o = 0 and lse = -inf
  *   causal   1: the token at position t sees the keys 0 .. t; 0: all keys of its
  *            sequence (tokens of one image, for instance)
- *   scale    finite
+ *   scale    -2.3e38 .. 2.3e38
  *   workspace: at least attn_fwd_paged_workspace_bytes(B, H, Hkv, S, d,
  *            max_pages * page_size) bytes, 16-byte aligned; contents on entry do not
  *            matter; calls that may overlap on the GPU need one each
@@ -650,7 +650,7 @@ size_t attn_fwd_paged_workspace_bytes(int B, int H, int Hkv, int S, int d, int m
  * (within 2^-11), and q, row by row, as by attn_decode_paged_fp4.
  *
  * Errors: GBATTN_EBADSHAPE (also H > 16384, B * S > 2^30, n_pages * Hkv > 2^31 - 2 or a
- * scale that is not finite), EHEADS, EHEADDIM, EDTYPE, EPAGE, EPOINTER, EWORKSPACE,
+ * scale out of its range), EHEADS, EHEADDIM, EDTYPE, EPAGE, EPOINTER, EWORKSPACE,
  * EUNSUPPORTED, ELAUNCH.
  */
 int attn_fwd_paged(const void *q, const void *k_cache, const void *v_cache, const int *page_table,

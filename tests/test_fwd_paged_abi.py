@@ -127,3 +127,15 @@ def test_plain_form_against_single_queries():
             ro, rl, _, _ = pu.attention(q[:, i], k[:, :seen], v[:, :seen], 0.25, 0.0)
             assert torch.allclose(o[:, i], ro, atol=1e-12) and torch.allclose(lse[:, i], rl, atol=1e-12)
     assert cu.limits(3, 5, True).tolist() == [-1, -1, 0, 1, 2] and cu.limits(3, 5, False).tolist() == [-1, -1, 2, 2, 2]
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_forward_refuses_scales_that_log2_e_takes_out_of_fp32(lib, fp4):
+    pool = "kc kf vc vf kd vd table lens " if fp4 else "kc vc table lens "
+    order = "q " + pool + "new o lse B H Hkv S d page n width scale causal ws wsb dtype stream"
+    fn = lib.attn_fwd_paged_fp4 if fp4 else lib.attn_fwd_paged
+    for scale in (2.4e38, -2.4e38, 3e38):
+        assert _call(fn, FORWARD, order, dict(scale=scale)) == -1, scale
+    if not torch.cuda.is_available():
+        for scale in (2.29e38, -2.29e38, 1e-45, 0.0):
+            assert _call(fn, FORWARD, order, dict(scale=scale)) == -10, scale

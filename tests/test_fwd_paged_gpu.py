@@ -327,6 +327,37 @@ def test_wide_queries_over_four_bits(S):
         _ok(pool, qs, table, [200], [S], o, lse, True, scale)
 
 
+@pytest.mark.usefixtures("table_width")
+@pytest.mark.parametrize("S", [2, 100])
+@pytest.mark.parametrize("scale", [2.0 ** -127, 2.0 ** -140])
+def test_scales_below_the_normal_numbers(scale, S):
+    """Scores of up to 2^127 before their scale."""
+    pool, table, g = _make(16, torch.bfloat16, 2, 64, 64, [300], 47)
+    pool.t[0] = pool.t[0] * 2.0 ** 60
+    pool.gpu[0] = pool.t[0].cuda()
+    q = (torch.randn(1, 4, S, 64, generator=g) * 2.0 ** 61).bfloat16().cuda()
+    o, lse = _forward(pool, q, table, [300], None, scale=scale)
+    assert gb.gbattn_device_status() == 0
+    _ok(pool, q, table, [300], [S], o, lse, True, scale)
+
+
+@pytest.mark.usefixtures("table_width")
+@pytest.mark.parametrize("S", [2, 100])
+@pytest.mark.parametrize("scale,descale,size", [(-100, -30, 124), (118, 10, -126), (-146, 20, 126), (2, 100, -105)])
+def test_scale_times_descale_outside_fp32(scale, descale, size, S):
+    """Powers of two whose product with the size of the queries is an ordinary scale,
+    while the scale times the descale (or the scale itself) is no normal number."""
+    pool, table, g = _make(4, torch.bfloat16, 2, 64, 64, [300], 48)
+    pool.descale[0] = pool.descale[0] * 2.0 ** descale
+    pool.kw["k_descale"] = pool.descale[0].cuda()
+    q = (torch.rand(1, 4, S, 64, generator=g) - 0.5).bfloat16() * 2.0 ** size
+    assert (q.float().abs().amax(-1) > 2.0 ** (size - 2)).all()
+    q = q.cuda()
+    o, lse = _forward(pool, q, table, [300], None, scale=2.0 ** scale)
+    assert gb.gbattn_device_status() == 0
+    _ok(pool, q, table, [300], [S], o, lse, True, 2.0 ** scale)
+
+
 def test_offsets_beyond_32_bits():
     """A pool of more than 2^32 bytes and 2^31 elements, in both units of work."""
     page, Hkv, d = 1024, 2, 128
