@@ -1689,6 +1689,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           if (p.lse != nullptr) p.lse[hrow] = -INFINITY;
         }
       }
+      __syncwarp();  // (the cluster's barrier takes whole warps)
       cluster_sync_all();
       if (NT == 1 && ok) {
         if (p.cluster == 8) fold_cluster<C, D, BF16, 8>(p, seg, smem, bars);
@@ -1700,6 +1701,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
   // The others' arrivals at the first barrier, and the second: no CTA ends while its
   // states are read.
   if (COPIES == 1 && p.cluster > 0) {
+    __syncwarp();
     if (warp >= C::kMmaWarp) cluster_sync_all();
     cluster_sync_all();
   }
