@@ -600,6 +600,24 @@ PyObject* decode_paged_fp4(PyObject* const* a) {
   return decode(f, a[0], Hkv, c, a[9], a[10], a[11], a[12], a[13], a[14], true);
 }
 
+// Device memory that a call reads or writes.
+struct Range {
+  const char* name;
+  const void* data;
+  int64_t bytes;
+};
+
+// Refuses an output that the caller gave and that shares memory with one of `others`
+// (contiguous tensors; those of no bytes or that are not given do not count).
+void check_apart(const Range& out, std::initializer_list<Range> others) {
+  const char* const begin = static_cast<const char*>(out.data);
+  for (const Range& r : others) {
+    const char* const b = static_cast<const char*>(r.data);
+    if (b != nullptr && begin < b + r.bytes && b < begin + out.bytes)
+      refuse_value(out.name, " is written: it must not share memory with ", r.name);
+  }
+}
+
 // c, the cache, is checked against q [B, H, S, d]; o = out, lse, return_lse, stream.
 PyObject* fwd_paged(const First& f, PyObject* qo, int64_t Hkv, const Cache& c, PyObject* new_lens, PyObject* scale_o,
                     PyObject* causal_o, PyObject* workspace, PyObject* const* o, bool fp4) {
@@ -618,6 +636,25 @@ PyObject* fwd_paged(const First& f, PyObject* qo, int64_t Hkv, const Cache& c, P
   Output out, lse;
   out.take(o[0], "out", q.sizes(), f.type, f.device);
   if (!none(o[1]) || truth(o[2])) lse.take(o[1], "lse", {B, H, S}, at::kFloat, f.device);
+  const int64_t slots = static_cast<int64_t>(c.n_pages) * hkv * c.page;
+  const int64_t queries = static_cast<int64_t>(B) * H * S, row = fp4 ? d / 2 : 2 * d;
+  const Range out_range{"out", out.data, queries * d * 2}, lse_range{"lse", lse.data, queries * 4};
+  auto apart = [&](const Range& own, const Range& other) {
+    check_apart(own, {{"q", q_ptr, queries * d * 2},
+                      {"the keys' pool", c.k, slots * row},
+                      {"the values' pool", c.v, slots * row},
+                      {"k_factors", c.k_factors, slots * (d / 16)},
+                      {"v_factors", c.v_factors, slots * (d / 16)},
+                      {"k_descale", c.k_descale, 4LL * hkv},
+                      {"v_descale", c.v_descale, 4LL * hkv},
+                      {"page_table", c.table, 4LL * B * c.max_pages},
+                      {"seqlens", c.lens, 4LL * B},
+                      {"new_lens", n, 4LL * B},
+                      {"workspace", ws.data, static_cast<int64_t>(ws.bytes)},
+                      other});
+  };
+  if (!none(o[0])) apart(out_range, lse_range);
+  if (!none(o[1])) apart(lse_range, out_range);
   if (fp4)
     done(attn_fwd_paged_fp4(q_ptr, c.k, c.k_factors, c.v, c.v_factors, c.k_descale, c.v_descale, c.table, c.lens, n,
                             out.data, static_cast<float*>(lse.data), B, H, hkv, S, d, c.page, c.n_pages, c.max_pages,

@@ -168,8 +168,9 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, seqlens, new_lens=None, scal
     seqlens - new_lens + i; the rows from new_lens on are padding (o = 0,
     lse = -inf).  causal: a token sees the keys up to its own, or else all of its
     sequence's.  workspace: optional buffer of attn_fwd_paged_workspace_bytes(B,
-    H, Hkv, S, d) bytes (allocated here if omitted).  Returns (o [B,H,S,d],
-    lse [B,H,S] or None)."""
+    H, Hkv, S, d) bytes (allocated here if omitted).  out and lse share memory with
+    no input, the workspace or each other.  Returns (o [B,H,S,d], lse [B,H,S] or
+    None)."""
     return (_native or _load()).attn_fwd_paged(q, k_cache, v_cache, page_table, seqlens, new_lens, scale, causal,
                                                workspace, out, lse, return_lse, stream)
 

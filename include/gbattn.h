@@ -635,7 +635,8 @@ size_t attn_fwd_paged_workspace_bytes(int B, int H, int Hkv, int S, int d, int m
  *   workspace: at least attn_fwd_paged_workspace_bytes(B, H, Hkv, S, d,
  *            max_pages * page_size) bytes, 16-byte aligned; contents on entry do not
  *            matter; calls that may overlap on the GPU need one each
- * o may not overlap an input.  The work is divided by the lengths, evenly over the
+ * o and lse may not overlap an input, the workspace or each other (the Python binding
+ * refuses it).  The work is divided by the lengths, evenly over the
  * GPU; results repeat bitwise.  A key that a row does not see has no influence on
  * it, whatever its k and v hold.  Of the keys that it sees: a score of NaN or +inf
  * makes the row's o and lse NaN, and a NaN or an infinity in v, whatever its weight,

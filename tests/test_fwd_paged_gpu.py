@@ -520,6 +520,55 @@ def test_wrapper_refusals():
     assert gb.gbattn_device_status() == 0
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+def test_outputs_that_share_memory_are_refused(bits):
+    g = torch.Generator().manual_seed(49)
+    B, H, Hkv, S, d, page = 2, 4, 2, 5, 64, 16
+    # everything from one block of memory, so that neighbours can be had
+    block = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    used = 0
+
+    def place(t):
+        nonlocal used
+        at, used = used, used + (t.numel() * t.element_size() + 255) // 256 * 256
+        view = block[at:at + t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+        view.copy_(t)
+        return view
+
+    pool = Pool(bits, 3, Hkv, page, d, torch.float16, g)
+    pool.gpu = [place(t.view(torch.uint8)).view(t.dtype) if t.element_size() == 1 else place(t) for t in pool.gpu]
+    pool.kw = {n: place(t) for n, t in pool.kw.items()}
+    table, lens, news = place(_i32([[0, 1], [2, 0]])), place(_i32([20, 10])), place(_i32([5, 3]))
+    q = place(torch.randn(B, H, S, d, generator=g).half().cuda())
+    ws = place(torch.zeros(gb.attn_fwd_paged_workspace_bytes(B, H, Hkv, S, d, 32), dtype=torch.uint8, device="cuda"))
+    out, lse = place(torch.zeros_like(q)), place(torch.zeros(B, H, S, device="cuda"))
+    fn = gb.attn_fwd_paged if bits == 16 else gb.attn_fwd_paged_fp4
+
+    def call(**kw):
+        kw = dict(dict(new_lens=news, workspace=ws, out=out, lse=lse), **pool.kw, **kw)
+        return fn(q, *pool.gpu, table, lens, **kw)
+
+    ref = fn(q, *pool.gpu, table, lens, new_lens=news, **pool.kw)
+    o, l2 = call()
+    assert o is out and l2 is lse and torch.equal(o, ref[0]) and torch.equal(l2, ref[1])
+    inputs = [q, *pool.gpu, *pool.kw.values(), table, lens, news, ws]
+    for like, name in ((out, "out"), (lse, "lse")):
+        size = like.numel() * like.element_size()
+        for other in [*inputs, lse if name == "out" else out]:
+            first = other.data_ptr() - block.data_ptr()
+            last = first + other.numel() * other.element_size()
+            for at in {first, max(0, first - size + 16), (last - 1) // 16 * 16}:
+                bad = block[at:at + size].view(like.dtype).view(like.shape)
+                with pytest.raises(ValueError, match="is written"):  # (its end may lie in a third tensor)
+                    call(**{name: bad})
+    # side by side is no overlap
+    both = place(torch.zeros(2, *q.shape, dtype=q.dtype, device="cuda"))
+    both[0].copy_(q)
+    o, _ = fn(both[0], *pool.gpu, table, lens, new_lens=news, out=both[1], **pool.kw)
+    assert torch.equal(o, ref[0]) and torch.equal(both[0], q)
+    assert gb.gbattn_device_status() == 0
+
+
 @pytest.mark.usefixtures("table_width")
 @pytest.mark.parametrize("bits", [16, 4])
 def test_text_and_images_served_in_chunks(bits):
