@@ -271,12 +271,14 @@ struct PairAxes {
     if (rope.table == nullptr) refuse_value("axes without rope");
     const int64_t axes = tensor_of_dims(positions, "positions (with axes)", 3).size(0);
     if (axes < 1 || axes > 4) refuse_value("positions must be of 1 to 4 axes, got ", axes);
-    PyObject* seq = PySequence_Fast(o, "axes must be a sequence of whole numbers");
+    // A tuple of this call's own: what turns an entry into a number may be Python code,
+    // which could change a list meanwhile.
+    PyObject* seq = PySequence_Tuple(o);
     if (seq == nullptr) throw python_error();
-    const Py_ssize_t pairs = PySequence_Fast_GET_SIZE(seq);
+    const Py_ssize_t pairs = PyTuple_GET_SIZE(seq);
     bool fits = pairs == rope.rot / 2 && pairs <= static_cast<Py_ssize_t>(sizeof(of));
     for (Py_ssize_t i = 0; fits && i < pairs; ++i) {
-      const long v = PyLong_AsLong(PySequence_Fast_GET_ITEM(seq, i));
+      const long v = PyLong_AsLong(PyTuple_GET_ITEM(seq, i));
       if (v == -1 && PyErr_Occurred()) {
         Py_DECREF(seq);
         throw python_error();

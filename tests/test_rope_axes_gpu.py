@@ -211,6 +211,38 @@ def test_wrapper_refusals():
     assert gb.gbattn_device_status() == 0
 
 
+def test_axes_whose_entries_run_code():
+    """Entries are whatever has an index; a list that one of them empties counts as it
+    was, and one that raises ends the call."""
+    q = torch.randn(2, 4, 3, 64, device="cuda", dtype=torch.float16)
+    kw = dict(rope=gb.rope_table(8, 64), positions=torch.randint(0, 8, (3, 2, 3), dtype=torch.int32, device="cuda"))
+    axes = gb.rope_pair_axes((16, 8, 8))
+    ref = gb.attn_qk_norm_rope(q, q, axes=axes, **kw)
+
+    class Entry:
+        def __init__(self, value, act):
+            self.value, self.act = value, act
+
+        def __index__(self):
+            self.act()
+            return self.value
+
+    entries = []
+    entries += [Entry(a, entries.clear) for a in axes]
+    out = gb.attn_qk_norm_rope(q, q, axes=entries, **kw)
+    assert not entries and all(torch.equal(a, b) for a, b in zip(out, ref))
+
+    def fail():
+        raise KeyError("entry")
+
+    with pytest.raises(KeyError):
+        gb.attn_qk_norm_rope(q, q, axes=[*axes[:-1], Entry(0, fail)], **kw)
+    pool = Pool(16, 4, 4, 16, 64, torch.float16, torch.Generator().manual_seed(1))
+    entries += [Entry(a, entries.clear) for a in axes]
+    back = pool.append(q, q, torch.zeros(2, 1, dtype=torch.int32, device="cuda"), _i32([3, 0]), q=q, axes=entries, **kw)
+    assert not entries and torch.equal(back[0], ref[0][0]) and gb.gbattn_device_status() == 0
+
+
 def test_streams_and_graph():
     cfg = (2, 33, 8, 2, 128, torch.bfloat16, 128, False, 3, "sections", True)
     q, k, w, wd, table, pos, axes, dy = _tensors(cfg)
