@@ -414,6 +414,25 @@ def test_longest_cache(bits, S):
              pu.u(dtype))
 
 
+@pytest.mark.parametrize("S,lens,causal", [(3, [700], True), (3, [2500, 100], True), (300, [2500, 301], True),
+                                           (3, [2500, 0], False)])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_units_by_the_longest_tables_key_tiles_pass_32_bits(bits, S, lens, causal):
+    """Units times the key tiles that the table has room for pass 2^31, so the list of
+    tiles is divided in 64 bits: whole units and runs, one and two row tiles, against the
+    same call with a table that is divided in 32."""
+    dtype, heads, d, page = torch.bfloat16, 130, 64, 1024
+    pool, table, g = _make(bits, dtype, heads, d, page, lens, 50)
+    q = torch.randn(len(lens), heads, S, d, generator=g).to(dtype).cuda()
+    widths = [128, (2 ** 31 - 257) // page]
+    assert len(lens) * heads * (widths[1] * page // 128) > 2 ** 31
+    outs = [_forward(pool, q, torch.nn.functional.pad(table, (0, w - table.shape[1]), value=1 << 30), lens, None,
+                     causal=causal) for w in widths]
+    assert gb.gbattn_device_status() == 0
+    assert _same_bits(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    _ok(pool, q, table, lens, [S] * len(lens), *outs[1], causal, 1 / math.sqrt(d))
+
+
 @pytest.mark.parametrize("S", [3, 90])
 @pytest.mark.parametrize("bits", [16, 4])
 def test_streams_graphs_and_two_calls_at_once(bits, S):
