@@ -83,7 +83,11 @@ constexpr int kBarBytes = 3 << 10;  // of Barriers
 // number, 2^-149.  (Rounding a scale to a multiple of it moves no score by more than 2^-150
 // times fp32's largest, 2.4e-7.)
 constexpr float kLeastScale = 1.4012985e-45f;
-constexpr int kSegRing = 4;       // segments whose notes of the guard are kept
+// Segments whose notes of the guard are kept: it is at most 3 ahead of every softmax
+// warp.  It follows V, which is loaded behind Q; Q's places are loaded when every row tile
+// has released the Q before: with its last product with K, at most two key tiles ahead of
+// its softmax, or, a tile that visits no key, when each of its softmax warps gets there.
+constexpr int kSegRing = 4;
 // Key tiles that the states of split units cost (writing, and a second kernel that has
 // to fold them) for units of one and two row tiles.  Whole units and runs, us in a
 // captured graph: 2000 tokens of one prompt from its start 67, 77; 3 of 40 sequences of
@@ -221,7 +225,6 @@ struct __align__(8) Barriers {
   uint32_t tmem_base;
   int abort_flag;
   uint32_t walk[8][24];    // each softmax warp's cursor and segment while it goes over the keys
-  uint32_t notes_read[8];  // segments whose notes each softmax warp is through with
   uint8_t bad[2][kTileRing];       // 16-key blocks of a tile (of K, of V) that have no page
   uint8_t nan_any[kSegRing];
   uint8_t nan_from[kSegRing][128]; // column's first non-finite key behind the first row's last key, - 1
@@ -516,42 +519,6 @@ __device__ __forceinline__ uint8_t* state_row(uint8_t* smem, int row, int c4) {
 // copy or part of the row met it.
 __device__ __forceinline__ float normalised(float o, float inv) { return fmaf(o, inv, o * 0.f); }
 
-// The guard's notes: each softmax warp counts the segments whose notes it is through
-// with, and before the guard writes those of segment number `seg` it waits, like
-// bounded_wait, until all WARPS of them have read what its place held.  (What visits a
-// segment's keys does not bound the guard for every warp: a row tile without any in
-// several segments gives their keys and Q back at once, whatever its warps still do.)
-__device__ __forceinline__ void notes_done(Barriers* bars, int warp, int lane, uint32_t segs) {
-  __syncwarp();
-  if (lane == 0)
-    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(&bars->notes_read[warp])), "r"(segs) : "memory");
-}
-template <int WARPS>
-__device__ __forceinline__ bool notes_free(Barriers* bars, int lane, int seg, int* status) {
-  if (seg < kSegRing) return true;
-  const uint32_t least = seg - kSegRing + 1;
-  volatile int* abort_flag = &bars->abort_flag;
-  uint64_t t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    uint32_t read = least;
-    if (lane < WARPS)
-      asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(read) : "r"(smem_u32(&bars->notes_read[lane])) : "memory");
-    if (__all_sync(0xffffffffu, read >= least)) break;
-    if ((it & 15u) == 0) {
-      const uint64_t now = global_timer_ns();
-      if (it == 0) t0 = now;
-      const bool late = now - t0 > kWaitTimeoutNs;
-      if (late) {
-        *abort_flag = 1;
-        atomicCAS(status, 0, kStatusTimeoutMma);
-      }
-      if (__any_sync(0xffffffffu, late || *abort_flag != 0)) return false;
-    }
-  }
-  __syncwarp();
-  return true;
-}
-
 __device__ __forceinline__ float ld_cluster(uint32_t a) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
@@ -645,7 +612,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
   }
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, NT);
+    mbar_init(&bars->q_empty, NT == 1 ? 1 : 5 * NT);  // (of two tiles each: the issuer, and four for what has read Q)
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&bars->kv_full[s], FP4 ? 4 : 1);  // (the converting warps of a tile)
       mbar_init(&bars->kv_empty[s], NT);
@@ -666,7 +633,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       mbar_init(&bars->group[x], kBM);
     }
     mbar_init(&bars->stagger, kBM);
-    for (int w = 0; w < 4 * NT; ++w) bars->notes_read[w] = 0;
     bars->abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&p.tq);
@@ -971,7 +937,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         uint32_t first[kCols];
 #pragma unroll
         for (int c = 0; c < kCols; ++c) first[c] = 255u;
-        if (jm < seg.j1 && !notes_free<4 * NT>(bars, lane, segs, p.status)) break;
         for (int j = jm; j < seg.j1; ++j) {
           const int st = C::kOneRing
                              ? (items + item_of_v(j - seg.j0, n)) % C::kStages
@@ -1128,7 +1093,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             auto skip = [&](bool is_v) {
               if ((ok = wait_item(is_v))) mbar_arrive(&bars->kv_empty[st]);
             };
-            if (nx == 0) mbar_arrive(&bars->q_empty);
+            mbar_arrive(&bars->q_empty, nx > 0 ? 4 : 1);  // (the rest: below, or the softmax warps)
             for (int j = -1; ok && j < n; ++j) {
               if (j + 1 < nx) {
                 qk(done + j + 1);
@@ -1459,6 +1424,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         }
         tc_fence_after();
         ++segs_x;
+      } else if constexpr (NT == 2) {  // this warp has read all notes so far
+        ok = bounded_wait(&bars->q_full, segs & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive(&bars->q_empty);
       }
       // Columns whose guarded rows of V are not finite for this row.
       int lim0;
@@ -1480,7 +1452,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         }
         tmem_wait_st();
       }
-      if constexpr (!FP4) notes_done(bars, warp, lane, segs + 1);
       if constexpr (COPIES > 1) {
         // Fold the copies: their references and sums, then O, 32 columns at a time; a
         // thread sums its row's part of the columns.
