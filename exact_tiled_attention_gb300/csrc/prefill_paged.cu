@@ -513,11 +513,15 @@ __device__ __forceinline__ uint8_t* state_row(uint8_t* smem, int row, int c4) {
   return smem + (c4 < kHalf ? C::kQOff : C::kPOff) + row * (kHalf * 16);
 }
 
-// An output from a row's sum and 1 / l: the product, but NaN where the sum is infinite.
+// Two outputs from a row's sums and 1 / l: the products, but NaN where a sum is infinite.
 // A value of V that is not finite makes its elements NaN, as in the decode, not an
 // infinity or NaN by what its weight rounds to, whether the guard has noted it, or which
 // copy or part of the row met it.
-__device__ __forceinline__ float normalised(float o, float inv) { return fmaf(o, inv, o * 0.f); }
+template <bool BF16>
+__device__ __forceinline__ uint32_t normalised(float x, float y, float inv) {
+  const float2 o = make_float2(x, y), r = ffma2(o, make_float2(inv, inv), fmul2(o, make_float2(0.f, 0.f)));
+  return pack2<BF16>(r.x, r.y);
+}
 
 __device__ __forceinline__ float ld_cluster(uint32_t a) {
   float v;
@@ -582,8 +586,7 @@ __device__ __forceinline__ void fold_cluster(const Params& p, const Seg& seg, ui
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + hrow[v] * D + c4 * 4) =
-          make_uint2(pack2<BF16>(normalised(acc.x, inv), normalised(acc.y, inv)),
-                     pack2<BF16>(normalised(acc.z, inv), normalised(acc.w, inv)));
+          make_uint2(normalised<BF16>(acc.x, acc.y, inv), normalised<BF16>(acc.z, acc.w, inv));
       if (c4 == 0 && p.lse != nullptr)
         p.lse[hrow[v]] = sum == 0.f ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994531f;
     }
@@ -1508,12 +1511,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + hrow * D + c * 32 + copy * kPer);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] = normalised(acc[i], inv);
-#pragma unroll
             for (int i = 0; i < kPer / 8; ++i)
-              dst[i] = make_uint4(pack2<BF16>(acc[8 * i], acc[8 * i + 1]), pack2<BF16>(acc[8 * i + 2], acc[8 * i + 3]),
-                                  pack2<BF16>(acc[8 * i + 4], acc[8 * i + 5]),
-                                  pack2<BF16>(acc[8 * i + 6], acc[8 * i + 7]));
+              dst[i] = make_uint4(normalised<BF16>(acc[8 * i], acc[8 * i + 1], inv),
+                                  normalised<BF16>(acc[8 * i + 2], acc[8 * i + 3], inv),
+                                  normalised<BF16>(acc[8 * i + 4], acc[8 * i + 5], inv),
+                                  normalised<BF16>(acc[8 * i + 6], acc[8 * i + 7], inv));
           } else {
             float4* dst =
                 reinterpret_cast<float4*>(p.part_o) + (part * (D / 4) + c * 8 + copy * (kPer / 4)) * kBM + crow;
@@ -1577,8 +1579,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              pk[i] = pack2<BF16>(normalised(__uint_as_float(u[2 * i]), inv),
-                                  normalised(__uint_as_float(u[2 * i + 1]), inv));
+              pk[i] = normalised<BF16>(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]), inv);
             if constexpr (C::kDirectO) {
               if (store_row >= 0) {
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + store_row * D + c * 32);
@@ -1775,10 +1776,8 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_paged_merge_kernel(cons
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint32_t out[kSlice / 2];
 #pragma unroll
-    for (int e = 0; e < kSlice; ++e) acc[e] = normalised(acc[e], inv);
-#pragma unroll
     for (int e = 0; e < kSlice; e += 2)
-      out[e / 2] = p.out_bf16 ? pack2<true>(acc[e], acc[e + 1]) : pack2<false>(acc[e], acc[e + 1]);
+      out[e / 2] = p.out_bf16 ? normalised<true>(acc[e], acc[e + 1], inv) : normalised<false>(acc[e], acc[e + 1], inv);
     const long long hrow = (static_cast<long long>(b) * p.H + kv_head(p, u) * p.g + head) * p.S + t;
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + hrow * D + slice * kSlice);
     dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
