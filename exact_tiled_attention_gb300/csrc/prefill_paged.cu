@@ -782,9 +782,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
       const int per_window = 32 >> boxes_shift;
       auto lookup = [&](int w) {
         const int j = seg.j0 + w * per_window + cb;
-        if (j >= seg.j1) return -1;
-        const int key = j * kBN + (box << box_shift);
-        return key < seg.s.n ? p.page_table[static_cast<long long>(seg.b) * p.max_pages + (key >> p.page_shift)] : -1;
+        const uint32_t key = static_cast<uint32_t>(j) * kBN + (box << box_shift);
+        return j < seg.j1 && key < static_cast<uint32_t>(seg.s.n)
+                   ? p.page_table[static_cast<long long>(seg.b) * p.max_pages + (key >> p.page_shift)]
+                   : -1;
       };
       // Notes the 16-key blocks without a page of tile number `at`: they are left out.
       auto note_missing = [&](bool is_v, int at, uint32_t absent) {
