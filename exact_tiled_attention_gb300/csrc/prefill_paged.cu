@@ -1662,18 +1662,20 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           if (p.lse != nullptr) p.lse[hrow] = -INFINITY;
         }
       }
-      __syncwarp();  // (the cluster's barrier takes whole warps)
-      cluster_sync_all();
-      if (NT == 1 && ok) {
-        if (p.cluster == 8) fold_cluster<C, D, BF16, 8>(p, seg, smem, bars);
-        else if (p.cluster == 4) fold_cluster<C, D, BF16, 4>(p, seg, smem, bars);
-        else if (p.cluster == 2) fold_cluster<C, D, BF16, 2>(p, seg, smem, bars);
+      if (NT == 1 && p.cluster > 1) {
+        __syncwarp();  // (the cluster's barrier takes whole warps)
+        cluster_sync_all();
+        if (ok) {
+          if (p.cluster == 8) fold_cluster<C, D, BF16, 8>(p, seg, smem, bars);
+          else if (p.cluster == 4) fold_cluster<C, D, BF16, 4>(p, seg, smem, bars);
+          else fold_cluster<C, D, BF16, 2>(p, seg, smem, bars);
+        }
       }
     }
   }
   // The others' arrivals at the first barrier, and the second: no CTA ends while its
   // states are read.
-  if (COPIES == 1 && p.cluster > 0) {
+  if (NT == 1 && COPIES == 1 && p.cluster > 1) {
     __syncwarp();
     if (warp >= C::kMmaWarp) cluster_sync_all();
     cluster_sync_all();
