@@ -1209,12 +1209,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
         const bool in_tile = row_token < p.tq_tokens && head < p.g;
         real = in_tile && t < seg.s.rows && seg.s.p0 + t >= 0;
         lim = real ? limit(p, seg.s, t) : -1;
-        // The scale of the scores: of three factors over 4 bits, whose product may be an
-        // fp32 number where that of two is none; in 64 bits it is rounded once.
-        [[maybe_unused]] double scale = p.scale64;
+        [[maybe_unused]] float kd = 1.f, up = 1.f;
         if constexpr (FP4) {
           const int kvh = kv_head(p, seg.u);
-          scale *= p.descale[0] != nullptr ? p.descale[0][kvh] : 1.f;
+          if (p.descale[0] != nullptr) kd = p.descale[0][kvh];
           vd = p.descale[1] != nullptr ? p.descale[1][kvh] : 1.f;
         }
         if constexpr (kReadyQ) {
@@ -1239,7 +1237,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           }
           const uint32_t e = min(max(top >> 7, 1u), 253u);
           const float down = __uint_as_float((254u - e) << 23);
-          scale *= __uint_as_float(e << 23);
+          up = __uint_as_float(e << 23);
 #pragma unroll 4
           for (int i = 0; i < D / 8; ++i) {
             const uint4 v = *piece(i);
@@ -1254,7 +1252,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, FP4, COPIES>::kThreads, 1)
           mbar_arrive(&bars->q_ready[x]);
         }
         if constexpr (FP4) {
-          lam = static_cast<float>(scale);
+          // The three factors' product may be an fp32 number where that of two is none: in
+          // 64 bits then (always, 3 tokens of 40 sequences of 200 took 32.6 us, not 32.3).
+          lam = p.scale_log2 * kd;
+          if (p.scale_log2 >= FLT_MIN && lam >= FLT_MIN && lam <= FLT_MAX) lam *= up;
+          else lam = static_cast<float>(p.scale64 * kd * up);
           if (lam < kLeastScale) lam = kLeastScale;
         }
         const int nx = tile.j1 - seg.j0;
