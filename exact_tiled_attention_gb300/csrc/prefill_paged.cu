@@ -47,19 +47,23 @@
 // end.  The score of a key that a row does not see becomes -inf, whatever it was.
 //
 // Fewer bits than fp32: the weights are rounded to the cache's 16-bit type for P.V (as in
-// the forward over contiguous tensors; tensor cores take both operands in 16 bits), over
-// 4 bits to fp16, which 2^-11 keeps below the codes' own spacing; bf16 queries over 4
-// bits become fp16 behind a power of two a row.  The sum of weights, the maximum, O and
-// what is folded stay fp32.
+// the forward over contiguous tensors; tensor cores take both operands in 16 bits, and a
+// second term, which the decode keeps, would be a second product with V), over 4 bits to
+// fp16, which 2^-11 keeps below the codes' own spacing (in fp16 a weight below 2^-14 is off
+// by up to 2^-25); bf16 queries over 4 bits become fp16 behind a power of two a row.  The sum
+// of weights, the maximum, O and what is folded stay fp32.
 //
-// Measured (us among other calls; 32 query heads on 8, d = 128, pages of 64; floor in
-// brackets from the copy rate and the dense bf16 rate):
-//   bound by the tensor pipe and the softmax's chain: 4096 tokens of 32768 1390 (1065,
-//   1480 TFLOP/s), 2048 tokens of 4 sequences of up to 16384 724 (562), over 4 bits 835;
-//   by HBM: 5 tokens of 64 sequences of 1024 to 32768 600 (653 at the rate of a copy;
-//   reads alone go faster, 7.4 TB/s); over 4 bits 422 (184) by the chains of products
+// Measured (us among other calls, and in brackets the floor at the same lengths, from the
+// copy rate and the dense bf16 rate; 32 query heads on 8, d = 128, pages of 64):
+//   bound by the tensor pipe and the softmax's chain: 4096 tokens of 32768 1346 to 1394
+//   (1065; 1479 to 1531 TFLOP/s), 1500 to 2048 tokens of 4 sequences of 4096 to 16384 672
+//   (478), over 4 bits 794; d = 64, 2048 of 4 sequences of 12000 728 (380), over 4 bits 859;
+//   by the ends and starts of units: 4 x 4096 tokens from their start 491 (284), 500 of each
+//   of 16 sequences of 1000 159 (51);
+//   by HBM: 5 tokens of 64 sequences of 1024 to 32768 598 (604: reads alone go a little
+//   faster than a copy, 6.85 TB/s); over 4 bits 443 (170) by the chains of products
 //   into one accumulator, about 100 cycles each whatever their size, 16 a key tile;
-//   by latency: 16 tokens of one sequence of 1000 10.8 (0.6).
+//   by latency: 16 tokens of one sequence of 1000 10.5 (0.6), 9.5 of them on the device.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -90,9 +94,10 @@ constexpr float kLeastScale = 1.4012985e-45f;
 constexpr int kSegRing = 4;
 // Key tiles that the states of split units cost (writing, and a second kernel that has
 // to fold them) for units of one and two row tiles.  Whole units and runs, us in a
-// captured graph: 2000 tokens of one prompt from its start 67, 77; 3 of 40 sequences of
-// 400 to 1000, 4 bits, 49, 57; 3 of 40 of 2000 68, 63; 40 of 8 of 4000 63, 48; 5 of 64 of
-// 1024 to 32768 994, 608.
+// captured graph: 3 tokens of 40 sequences of 2000 80, 70, over 4 bits 70, 64; 5 of 64 of
+// 1024 to 32768 1042, 722, over 4 bits 830, 482.  The estimate takes every unit for as long
+// as the longest, so prompts from their start and short ragged batches get runs where whole
+// units would win: 2000 tokens of one prompt 67, 75; 3 of 40 of 400 to 1000, 4 bits, 53, 57.
 template <int NT>
 constexpr int kSplitCost = NT == 2 ? 6 : 4;
 constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
@@ -101,8 +106,8 @@ constexpr int kTileRing = 16;     // key tiles whose missing pages are kept
 // each copy's warps take another part of the keys (the other weights of their rows
 // stay 0): the softmax of a tile, which otherwise waits for one or two of the four
 // warps, takes a half or a quarter of the time.  The copies are folded at a segment's
-// end.  5 tokens of 64 sequences (20 rows), with and without: 4 bits 422, 695 us, 16 bits
-// at d = 64 340, 444; at d = 128 in 16 bits HBM bounds both.
+// end.  5 tokens of 64 sequences (20 rows), with and without: 4 bits 481, 757 us, 16 bits
+// at d = 64 378, 494; at d = 128 in 16 bits HBM bounds both.
 template <int D, int NT, bool FP4, int COPIES>
 struct Cfg {
   static_assert(NT == 1 || COPIES == 1, "copies are of one tile");
@@ -1814,10 +1819,12 @@ Shape shape_of(int B, int H, int Hkv, int S, int nt) {
 // One tile where units of one find an SM each and two tiles would have at most
 // kOneTileRun key tiles a CTA: more CTAs then share the work, and a tile alone starts and
 // ends sooner.  Elsewhere two tiles share each key tile.  Measured with 8 KV heads of 4
-// query heads, d = 128 (us by one tile, by two): one sequence, 500 tokens of 1000 18.6,
-// 22.7 (4 bits 22.6, 31.4), 100 of 4000 22.6, 31.0 (26.8, 43.0); 4 sequences, 100 of 4000
-// 41.1, 45.2 (52.4, 61.3).  Beyond the bounds: 4 sequences, 500 of 1000 70.7, 52.4; 100 of
-// 16000 168, 113.
+// query heads (us in a captured graph by one tile, by two, and in brackets over 4 bits).
+// d = 128: one sequence, 500 tokens of 1000 18.5, 20.6 (22.6, 28.2), 100 of 4000 22.6, 30.6
+// (26.7, 41.0), 200 of 4000 30.8, 32.8 (41.0, 45.1); 4 sequences, 100 of 4000 41.0, 43.2 (51.3,
+// 58.7).  Beyond the bounds: 4 sequences, 500 of 1000 71, 52; 100 of 16000 168, 113.  The rule
+// does not ask for d: at 64 one tile wins for 500 of 1000 16.5, 18.5 and 100 of 4000 18.5,
+// 24.7, and loses for 500 of 4000 39.0, 34.9 (43.1, 41.7) and 100 of 16000 41.0, 36.9 (45.1, 44.8).
 constexpr long long kOneTileRun = 16;
 Shape shape_of(int B, int H, int Hkv, int S, long long max_len, int num_sms) {
   const Shape one = shape_of(B, H, Hkv, S, 1), two = shape_of(B, H, Hkv, S, 2);
@@ -1866,14 +1873,14 @@ int launch_t(Params& p, const PagedPrefillArgs& a, const Shape& s) {
     // division of the list nor the second kernel (kScan); one of several CTAs folds its
     // states, the longer the fewer it has (fold); both in key tiles of a unit, fitted to
     // measured times.  Clusters and runs, us in a captured graph, 8 KV heads of 4 query
-    // heads, d = 128: 16 tokens of 1000 12.3, 14.3, of 4000 14.3, 22.3; of 16000 the runs
-    // are taken.  (With two row tiles the units are too many for several CTAs each, or
+    // heads, d = 128: 16 tokens of 1000 12.4, 14.4 (4 bits 14.4, 18.5), of 4000 14.4, 21.9; of
+    // 16000 the runs are taken.  (With two row tiles the units are too many for several CTAs each, or
     // have so many key tiles that runs win.)
     constexpr float kScan = NT == 2 ? 5.f : 9.f;
     // Few rows have copies in runs: a key tile takes a CTA of a cluster `tile` times as
-    // long.  3 tokens of 40 sequences over 4 bits, with and without copies: of 800 50, 63
-    // us, of 200 35, 37.  5 tokens of 8 sequences over 4 bits, copies and clusters: of 4000
-    // 35.0, 38.9, of 1000 21.2, 20.5; over 16 bits with d = 64, of 2000 22.5, 18.4.
+    // long.  3 tokens of 40 sequences over 4 bits, with and without copies: of 800 51, 64
+    // us, of 200 37 both.  5 tokens of 8 sequences over 4 bits, copies and clusters: of 4000
+    // 36.2, 38.8, of 1000 21.9, 20.5; over 16 bits with d = 64, of 2000 22.6, 18.5.
     const int rows = s.hb * s.tokens;
     const bool copies = NT == 1 && (FP4 || D == 64) && rows <= kBM / 2;
     const float tile = !copies ? 1.f : FP4 ? 1.6f : 1.3f;

@@ -636,19 +636,22 @@ size_t attn_fwd_paged_workspace_bytes(int B, int H, int Hkv, int S, int d, int m
  *            max_pages * page_size) bytes, 16-byte aligned; contents on entry do not
  *            matter; calls that may overlap on the GPU need one each
  * o and lse may not overlap an input, the workspace or each other (the Python binding
- * refuses it).  The work is divided by the lengths, evenly over the
- * GPU; results repeat bitwise.  A key that a row does not see has no influence on
- * it, whatever its k and v hold.  Of the keys that it sees: a score of NaN or +inf
- * makes the row's o and lse NaN, and a NaN or an infinity in v, whatever its weight,
- * makes its element of o NaN, as in attn_decode_paged (a key with a score of -inf may
- * count as one that is not seen).
+ * refuses it).  The work is divided by the lengths, evenly over the GPU; for few or
+ * short sequences a page table no wider than the longest one needs is faster, since
+ * what it could hold is all that the host knows.  Results repeat bitwise.  A key that a
+ * row does not see has no influence on it, whatever its k and v hold.  Of the keys that
+ * it sees: a score of NaN or +inf makes the row's o and lse NaN, and a NaN or an
+ * infinity in v, whatever its weight, makes its element of o NaN, as in
+ * attn_decode_paged (a key with a score of -inf may count as one that is not seen).
  * Scores and their sums are fp32; exp(score - maximum) is rounded to dtype for the
- * product with v, as in attn_fwd.
+ * product with v, as in attn_fwd: within 2^-8 in bf16, in fp16 within 2^-11, and below
+ * 2^-14 within 2^-25.  (attn_decode_paged keeps two terms, so a token's o there is closer.)
  *
  * attn_fwd_paged_fp4 -- the same over a 4-bit cache (q and o in dtype, which the
  * cache does not depend on).  The factors of the sequences' tokens are finite, as
  * attn_cache_append_fp4 writes them.  exp(score - maximum) is rounded to fp16
- * (within 2^-11), and q, row by row, as by attn_decode_paged_fp4.
+ * (within 2^-11, below 2^-14 within 2^-25), and q, row by row, as by
+ * attn_decode_paged_fp4.
  *
  * Errors: GBATTN_EBADSHAPE (also H > 16384, B * S > 2^30, n_pages * Hkv > 2^31 - 2 or a
  * scale out of its range), EHEADS, EHEADDIM, EDTYPE, EPAGE, EPOINTER, EWORKSPACE,

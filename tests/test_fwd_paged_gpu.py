@@ -433,6 +433,40 @@ def test_units_by_the_longest_tables_key_tiles_pass_32_bits(bits, S, lens, causa
     _ok(pool, q, table, lens, [S] * len(lens), *outs[1], causal, 1 / math.sqrt(d))
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+def test_more_sequences_than_a_grid_dimension_holds(bits):
+    """70000 sequences of 0 to 16 tokens, a page each (some share one), against the
+    definition for all of them at once."""
+    B, H, S, d, page, dtype = 70000, 2, 2, 64, 16, torch.float16
+    g = torch.Generator().manual_seed(52)
+    pool = Pool(bits, 300, 1, page, d, dtype, g)
+    lens = torch.randint(0, page + 1, (B,), generator=g)
+    table = torch.randint(0, 300, (B, 1), generator=g, dtype=torch.int32)
+    q = torch.randn(B, H, S, d, generator=g).to(dtype).cuda()
+    o, lse = _forward(pool, q, table, lens.tolist(), None)
+    assert gb.gbattn_device_status() == 0
+    every = torch.arange(300, dtype=torch.int32)
+    k, v = (pool.values(i, every, 300 * page).double().view(300, page, d).cuda()[table[:, 0].cuda().long()] for i in range(2))
+    lens, scale = lens.cuda(), 1 / math.sqrt(d)
+    seen = torch.arange(page, device="cuda") <= (lens[:, None] - S + torch.arange(S, device="cuda"))[..., None]  # [B, S, page]
+    raw = torch.einsum("bhsd,bpd->bhsp", q.double(), k)
+    mag = torch.einsum("bhsd,bpd->bhsp", q.double().abs(), k.abs()).amax(-1, keepdim=True) * scale
+    s = (raw * scale).masked_fill(~seen[:, None], -math.inf)
+    real = seen.any(-1)[:, None].expand(B, H, S)
+    rl = torch.logsumexp(s, -1)
+    p = torch.exp(s - rl.masked_fill(~real, 0.0)[..., None])
+    ro = torch.einsum("bhsp,bpd->bhsd", p, v)
+    # chunk_util's bound, with fp16 weights (over 4 bits too)
+    half = pu.u(torch.float16)
+    e = 2 * d * pu.U32 * mag + mag * 4 * pu.U32 + 2.0 ** -20
+    tol = (half + 2 * e) * torch.einsum("bhsp,bpd->bhsd", p, v.abs()) + 2.0 ** -25 * torch.einsum(
+        "bsp,bpd->bsd", seen.double(), v.abs())[:, None]
+    tol = tol + half * (ro.abs() + tol) + 2.0 ** -25
+    assert ((o.double() - ro).abs() <= tol).all()
+    assert ((lse.double() - rl).abs() <= e[..., 0] + rl.abs() * 4 * pu.U32 + 2.0 ** -20)[real].all()
+    assert (o[~real] == 0).all() and torch.isneginf(lse[~real]).all() and not real.all()
+
+
 @pytest.mark.parametrize("S", [3, 90])
 @pytest.mark.parametrize("bits", [16, 4])
 def test_streams_graphs_and_two_calls_at_once(bits, S):
