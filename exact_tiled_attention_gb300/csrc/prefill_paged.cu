@@ -196,7 +196,7 @@ struct Params {
   int page_shift, n_pages, max_pages, box_rows;
   int causal;
   int out_bf16;
-  float scale_log2;  // |scale| log2 e (of a scale of 0: log2 e), at least kLeastScale
+  float scale_log2;  // |scale| log2 e, at least kLeastScale
   double scale64;    // the same, where fp32's normal numbers do not have it in 64 bits
   float sign;        // -1 or 0 where scale is negative or 0, and scores are taken times it
   int ctas;
@@ -1970,7 +1970,7 @@ int launch_prefill_paged(const PagedPrefillArgs& a) {
   p.max_pages = c.max_pages;
   p.causal = a.causal;
   p.out_bf16 = a.bf16 ? 1 : 0;
-  const float scale = a.scale == 0.f ? 1.f : a.scale < 0.f ? -a.scale : a.scale;
+  const float scale = a.scale < 0.f ? -a.scale : a.scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.scale64 = p.scale_log2 < FLT_MIN ? scale * 1.4426950408889634 : p.scale_log2;
   if (p.scale_log2 < kLeastScale) p.scale_log2 = kLeastScale;

@@ -358,6 +358,21 @@ def test_scale_times_descale_outside_fp32(scale, descale, size, S):
     _ok(pool, q, table, [300], [S], o, lse, True, 2.0 ** scale)
 
 
+@pytest.mark.usefixtures("table_width")
+@pytest.mark.parametrize("S", [2, 100])
+def test_a_scale_of_zero_with_wide_factors(S):
+    """Every score is 0, whatever the descale and the queries are."""
+    pool, table, g = _make(4, torch.bfloat16, 2, 64, 64, [300], 53)
+    pool.descale[0] = pool.descale[0] * 2.0 ** 100
+    pool.kw["k_descale"] = pool.descale[0].cuda()
+    q = torch.randn(1, 4, S, 64, generator=g).bfloat16() * 2.0 ** 100
+    for scale in (0.0, -0.0):
+        o, lse = _forward(pool, q.cuda(), table, [300], None, scale=scale)
+        assert gb.gbattn_device_status() == 0
+        # the keys' magnitude does not matter to the bound: at a scale of 0 it is 0
+        _ok(pool, q, table, [300], [S], o, lse, True, 0.0)
+
+
 def test_offsets_beyond_32_bits():
     """A pool of more than 2^32 bytes and 2^31 elements, in both units of work."""
     page, Hkv, d = 1024, 2, 128
